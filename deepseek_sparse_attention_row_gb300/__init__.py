@@ -1,7 +1,8 @@
 """GB300 (sm_103a) DSA candidate-block selection.
 
-A thin binding over ``libdsa_cb.so`` (C ABI declared in ``include/dsa_cb.h``
-and ``include/dsa_dcp_attn.h``):
+A thin binding over ``libdsa_cb.so`` (C ABI declared in ``include/dsa_cb.h``,
+``include/dsa_dcp_attn.h``, ``include/dsa_attention.h`` and
+``include/dsa_cache.h``):
 argument marshalling only. Every step of the computation runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback, and every call
 raises if the library is missing or a call fails.
@@ -19,12 +20,19 @@ Functions carry the C ABI's names:
 * ``dsa_correct_attn_out`` / ``dsa_merge_attn_out`` -- the DCP partial-
   attention LSE correction (sglang ``dcp/kernels.py``, ``correct_attn_out``;
   C ABI in ``include/dsa_dcp_attn.h``) and the sum over shards after it.
+* ``dsa_prompt_attention`` / ``dsa_shared_prefix_attention`` -- attention over
+  packed prompts, and of single tokens on a paged cache whose first pages a
+  batch shares; both give the base-2 LSE that the merge takes
+  (``include/dsa_attention.h``).
+* ``dsa_cache_fork`` / ``dsa_cache_free`` / ``dsa_cache_compact`` -- the pages
+  of such a cache (``include/dsa_cache.h``).
 
 Tensors are PyTorch CUDA tensors (PyTorch supplies device memory and the
 current stream) or pinned host tensors, which the kernels read and write in
 place through ``dsa_mapped_host_pointer`` (across NVLink-C2C on Grace
 systems). Logits may be float32 or bfloat16 (the ``*_bf16`` C entry points);
-scores follow the logits' dtype. ``select_candidate_blocks[_sharded]_host``
+scores follow the logits' dtype. The attention and cache operators take CUDA
+tensors only. ``select_candidate_blocks[_sharded]_host``
 take host tensors and wait for the ids: pinned inputs are read in place
 (only the in-window logits cross the link), other host tensors are copied to
 the device first.
@@ -47,8 +55,18 @@ __all__ = [
     "dsa_mask_candidate_logits_sharded",
     "dsa_correct_attn_out",
     "dsa_merge_attn_out",
+    "dsa_prompt_attention",
+    "dsa_shared_prefix_attention",
+    "dsa_cache_fork",
+    "dsa_cache_free",
+    "dsa_cache_compact",
+    "FORK_OK",
+    "FORK_NO_PAGE",
+    "FORK_REFUSED",
     "select_candidate_blocks_host",
     "select_candidate_blocks_sharded_host",
+    "shared_prefix_workspace_bytes",
+    "cache_workspace_bytes",
     "max_select_blocks",
     "mapped_host_pointer",
     "set_launch_override",
@@ -85,6 +103,13 @@ EXPORTED_SYMBOLS = (
     "dsa_mask_candidate_logits_sharded_starts_bf16",
     "dsa_select_set_launch_override",
     "dsa_pipeline_error",
+    "dsa_prompt_attention",
+    "dsa_shared_prefix_workspace_bytes",
+    "dsa_shared_prefix_attention",
+    "dsa_cache_workspace_bytes",
+    "dsa_cache_fork",
+    "dsa_cache_free",
+    "dsa_cache_compact",
 )
 
 # Knobs of dsa_select_set_launch_override (include/dsa_cb.h).
@@ -147,6 +172,25 @@ def library():
         p, i32, i64, i64, i64, i64, p, p, i32, i32, i32, i32, p, i64, p, i64, p, sz, p]
     lib.dsa_mask_candidate_logits_sharded_starts.argtypes = [p, i32, i64, i64, i64, i64, p, p,
                                                              i32, i32, p, i32, i64, p]
+    f32 = ctypes.c_float
+    lib.dsa_prompt_attention.argtypes = [p, p, p, i32, i64, i64, i32, i32, i32, i64, i64, i64,
+                                         i64, i64, i64, p, p, i32, i32, f32, p, i64, i64, p, i64,
+                                         i64, p]
+    lib.dsa_shared_prefix_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i64, i32]
+    lib.dsa_shared_prefix_workspace_bytes.restype = sz
+    lib.dsa_shared_prefix_attention.argtypes = [p, p, p, i32, i64, i32, i32, i32, i64, i32, i64,
+                                                i64, i64, i64, i64, i64, i64, i64, p, i64, p, i64,
+                                                i64, p, f32, p, i64, i64, p, i64, i64, p, sz, p]
+    lib.dsa_cache_workspace_bytes.argtypes = [i64, i64]
+    lib.dsa_cache_workspace_bytes.restype = sz
+    lib.dsa_cache_fork.argtypes = [p, i64, i64, i64, i64, i32, i64, p, p, i64, i64, i64, p, p, p,
+                                   i64, p, p, sz, p]
+    lib.dsa_cache_free.argtypes = [p, i64, p, i64, i64, i64, p, p, i64, p]
+    lib.dsa_cache_compact.argtypes = [p, i64, i64, i64, i64, i32, i64, p, p, i64, i64, i64, p, p,
+                                      p, sz, p]
+    for f in (lib.dsa_prompt_attention, lib.dsa_shared_prefix_attention, lib.dsa_cache_fork,
+              lib.dsa_cache_free, lib.dsa_cache_compact):
+        f.restype = ctypes.c_int
     for name in ("dsa_block_scores", "dsa_select_candidate_blocks",
                  "dsa_select_candidate_blocks_sharded", "dsa_mask_candidate_logits",
                  "dsa_mask_candidate_logits_sharded", "dsa_select_candidate_blocks_sharded_starts",
@@ -495,6 +539,325 @@ def dsa_merge_attn_out(outs, lses, merged=None, lse_out=None, stream=None):
         _dev_ptr(lse_out, torch.float32, "lse_out"), *lse_out.stride(), _stream_handle(stream))
     _check("dsa_merge_attn_out", st)
     return merged, lse_out
+
+
+DTYPE_F16 = 2
+
+
+class _Launch:
+    """One call's device and stream: the tensors' device made current, and
+    (for a given ``stream``) that stream, so that what the call allocates
+    belongs to the stream that it runs on."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self._guards = []
+        if device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self._guards.append(torch.cuda.stream(stream))
+        self._stream = stream
+        self._device = device
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        s = self._stream
+        if s is None:
+            s = _torch().cuda.current_stream(self._device)
+        return s.cuda_stream or None
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _on_gpu(t, dtype, name, dim, device=None):
+    """Device address of a CUDA tensor of the given type, rank and device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr() or None
+
+
+def _rows_of(t, name):
+    """Strides of all dimensions but the last, which has unit stride. A
+    dimension of one element is never stepped over: any stride will do."""
+    last = t.shape[-1]
+    if last > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return [st if n > 1 else last for n, st in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def _vector(t, name, device):
+    """Address and length of a contiguous int32 vector."""
+    torch = _torch()
+    ptr = _on_gpu(t, torch.int32, name, 1, device)
+    if t.shape[0] > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return ptr, t.shape[0]
+
+
+def _attention_dtype(t, name):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float16:
+        return DTYPE_F16
+    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _attention_outputs(q, out, lse_out):
+    """Output tensors (allocated when None) and their addresses and strides."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    if lse_out is None:
+        lse_out = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse_out.shape != q.shape[:2]:
+        raise ValueError(f"lse_out must be {tuple(q.shape[:2])}, got {tuple(lse_out.shape)}")
+    args = (_on_gpu(out, q.dtype, "out", 3, q.device), *_rows_of(out, "out"),
+            _on_gpu(lse_out, torch.float32, "lse_out", 2, q.device), *lse_out.stride())
+    return out, lse_out, args
+
+
+def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None, out=None,
+                         lse_out=None, stream=None):
+    """Attention over packed prompts with grouped heads.
+
+    ``q`` [Tq, H, D], ``k`` and ``v`` [Tk, Hkv, D] bfloat16 or float16, D a
+    multiple of 8 up to 128; sequence i's queries are rows cu_q[i]:cu_q[i+1]
+    and its keys rows cu_k[i]:cu_k[i+1] (int32 CUDA tensors of equal length).
+    ``causal``: the last query of a sequence sees all of its keys, each
+    earlier one a key less. ``scale`` defaults to 1/sqrt(D). Writes ``out``
+    [Tq, H, D] and the base-2 log-sum-exp ``lse_out`` [Tq, H] fp32 (allocated
+    when None) and returns both; rows that see no key get 0 and -inf, rows of
+    no sequence are left as they were. Forward only: the outputs carry no
+    autograd graph."""
+    code = _attention_dtype(q, "q")
+    dev = q.device
+    qp = _on_gpu(q, q.dtype, "q", 3)
+    kp, vp = _on_gpu(k, q.dtype, "k", 3, dev), _on_gpu(v, q.dtype, "v", 3, dev)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} "
+                         "do not match")
+    (cq, nq), (ck, nk) = _vector(cu_q, "cu_q", dev), _vector(cu_k, "cu_k", dev)
+    if nq != nk or nq < 1:
+        raise ValueError(f"cu_q and cu_k must have one length of at least 1, got {nq} and {nk}")
+    D = q.shape[2]
+    scale = D ** -0.5 if scale is None and D else scale or 0.0
+    with _Launch(dev, stream) as handle:
+        out, lse_out, outs = _attention_outputs(q, out, lse_out)
+        st = library().dsa_prompt_attention(
+            qp, kp, vp, code, q.shape[0], k.shape[0], q.shape[1], k.shape[1], D,
+            *_rows_of(q, "q"), *_rows_of(k, "k"), *_rows_of(v, "v"), cq, ck, nq - 1,
+            int(bool(causal)), scale, *outs, handle)
+    _check("dsa_prompt_attention", st)
+    return out, lse_out
+
+
+def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: int = 0, *,
+                                prefix_pages=None, scale=None, out=None, lse_out=None,
+                                workspace=None, stream=None):
+    """Attention of one query token per sequence on a paged cache, the first
+    ``prefix_len`` tokens of which (whole pages) are the same for the batch.
+
+    ``q`` [B, H, D] bfloat16 or float16; ``k_pages`` and ``v_pages`` [N, page,
+    Hkv, D]; token t of sequence b lies on page ``tables``[b, t // page]
+    (int32 [B, P]); the sequence sees its first ``lens``[b] tokens (int32
+    [B]). The prefix is read once, through ``prefix_pages`` (int32, by default
+    the first row of ``tables``); 0 gives plain paged decode attention. Pages
+    numbered outside [0, N) are not seen. Writes ``out`` [B, H, D] and the
+    base-2 log-sum-exp ``lse_out`` [B, H] fp32 (allocated when None) and
+    returns both; a sequence that sees no token gets 0 and -inf.
+    ``workspace``: a CUDA uint8 tensor of
+    ``shared_prefix_workspace_bytes(...)`` bytes that no overlapping call
+    uses (allocated when None)."""
+    torch = _torch()
+    code = _attention_dtype(q, "q")
+    dev = q.device
+    qp = _on_gpu(q, q.dtype, "q", 3)
+    kp = _on_gpu(k_pages, q.dtype, "k_pages", 4, dev)
+    vp = _on_gpu(v_pages, q.dtype, "v_pages", 4, dev)
+    tp = _on_gpu(tables, torch.int32, "tables", 2, dev)
+    lp, n = _vector(lens, "lens", dev)
+    B, H, D = q.shape
+    N, page, Hkv, _ = k_pages.shape
+    if k_pages.shape != v_pages.shape or k_pages.shape[3] != D:
+        raise ValueError(f"q {tuple(q.shape)}, k_pages {tuple(k_pages.shape)} and v_pages "
+                         f"{tuple(v_pages.shape)} do not match")
+    if n != B or tables.shape[0] != B:
+        raise ValueError(f"tables {tuple(tables.shape)} and lens {tuple(lens.shape)} do not "
+                         f"match q {tuple(q.shape)}")
+    P = tables.shape[1]
+    if P > 1 and tables.stride(1) != 1:
+        raise ValueError("tables must have unit stride in its last dimension")
+    prefix_len = int(prefix_len)
+    pp = None
+    if prefix_len > 0:
+        if prefix_pages is None:
+            pp = tp
+        else:
+            pp, n = _vector(prefix_pages, "prefix_pages", dev)
+            if page > 0 and n < prefix_len // page:
+                raise ValueError(f"prefix_pages holds {n} pages, prefix_len {prefix_len} needs "
+                                 f"{prefix_len // page}")
+    scale = D ** -0.5 if scale is None and D else scale or 0.0
+    with _Launch(dev, stream) as handle:
+        out, lse_out, outs = _attention_outputs(q, out, lse_out)
+        need = shared_prefix_workspace_bytes(B, H, Hkv, D, prefix_len, P, page)
+        ws, ws_bytes = _scratch(workspace, need, dev)
+        st = library().dsa_shared_prefix_attention(
+            qp, kp, vp, code, B, H, Hkv, D, N, page, *_rows_of(q, "q"),
+            *_rows_of(k_pages, "k_pages"), *_rows_of(v_pages, "v_pages"), pp, prefix_len, tp, P,
+            tables.stride(0) if B > 1 else P, lp, scale, *outs,
+            ws.data_ptr() if ws_bytes else None, ws_bytes, handle)
+    _check("dsa_shared_prefix_attention", st)
+    return out, lse_out
+
+
+def shared_prefix_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int,
+                                  prefix_len: int, max_pages: int, page_size: int) -> int:
+    """Bytes of workspace of a ``dsa_shared_prefix_attention`` call."""
+    return int(library().dsa_shared_prefix_workspace_bytes(batch, heads, kv_heads, head_dim,
+                                                           prefix_len, max_pages, page_size))
+
+
+def _scratch(workspace, need: int, device):
+    """A call's workspace and its bytes: the caller's tensor, or a new one.
+    A new one comes from the allocator of the current stream (of the graph,
+    in a capture), which hands its memory on only behind this call."""
+    torch = _torch()
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+FORK_OK, FORK_NO_PAGE, FORK_REFUSED = 0, 1, 2
+
+
+def _cache_state(refs, tables, lens, device=None):
+    """Arguments that describe refs, tables and lens, and their device."""
+    torch = _torch()
+    tp = _on_gpu(tables, torch.int32, "tables", 2, device)
+    dev = tables.device
+    rp, pages = _vector(refs, "refs", dev)
+    S, P = tables.shape
+    if P > 1 and tables.stride(1) != 1:
+        raise ValueError("tables must have unit stride in its last dimension")
+    if S > 1 and tables.stride(0) < P:
+        raise ValueError("rows of tables must not overlap")
+    lp = None
+    if lens is not None:
+        lp, n = _vector(lens, "lens", dev)
+        if n != S:
+            raise ValueError(f"lens holds {n} lengths, tables {S} rows")
+    return rp, pages, tp, S, P, tables.stride(0) if S > 1 else P, lp, dev
+
+
+def _cache_planes(cache, pages):
+    """Arguments that describe the page contents [planes, N, page, ...]."""
+    if not cache.is_cuda:
+        raise ValueError("cache must be a CUDA tensor")
+    if cache.dim() < 3 or cache.shape[1] != pages:
+        raise ValueError(f"cache must be [planes, {pages}, page, ...], got {tuple(cache.shape)}")
+    e = cache.element_size()
+    token = e
+    for n, st in zip(reversed(cache.shape[3:]), reversed(cache.stride()[3:])):
+        if n > 1 and st * e != token:
+            raise ValueError("the pages of cache must be contiguous")
+        token *= n
+    if cache.shape[2] > 1 and cache.stride(2) * e != token:
+        raise ValueError("the pages of cache must be contiguous")
+    page = cache.shape[2] * token
+    strides = [st * e if n > 1 else page for n, st in zip(cache.shape[:2], cache.stride()[:2])]
+    if any(n > 1 and st < page for n, st in zip(cache.shape[:2], strides)):
+        raise ValueError("the pages of cache must not overlap")
+    return (cache.data_ptr() or None, cache.shape[0], strides[0], pages, strides[1],
+            cache.shape[2], token)
+
+
+def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None, workspace=None,
+                   stream=None):
+    """Make slot children[i] a copy of slot parents[i] (int32 CUDA vectors).
+
+    ``cache`` [planes, N, page, ...] of any type (pages contiguous, tokens of
+    a multiple of 16 bytes), ``refs`` int32 [N], ``tables`` int32 [S, P],
+    ``lens`` int32 [S]. Whole pages are shared; the used tokens of a partly
+    filled last page are copied to the lowest free page. Returns ``status``
+    int32 (FORK_OK, FORK_NO_PAGE or FORK_REFUSED for each pair), allocated
+    when None; the host waits for nothing."""
+    torch = _torch()
+    rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
+    planes = _cache_planes(cache, pages)
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    (pp, n), (cp, nc) = _vector(parents, "parents", dev), _vector(children, "children", dev)
+    if n != nc:
+        raise ValueError(f"{n} parents, {nc} children")
+    with _Launch(dev, stream) as handle:
+        if status is None:
+            status = torch.empty(n, dtype=torch.int32, device=dev)
+        sp, ns = _vector(status, "status", dev)
+        if ns != n:
+            raise ValueError(f"status holds {ns} entries, expected {n}")
+        ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(n, pages) if n else 0, dev)
+        st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp,
+                                      ws.data_ptr() if ws_bytes else None, ws_bytes, handle)
+    _check("dsa_cache_fork", st)
+    return status
+
+
+def dsa_cache_free(refs, tables, lens, seqs, *, stream=None):
+    """Empty the slots named in ``seqs`` (int32 CUDA vector): their pages'
+    refs go down by one, their rows become -1 and their lengths 0."""
+    rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
+    sp, n = _vector(seqs, "seqs", dev)
+    with _Launch(dev, stream) as handle:
+        st = library().dsa_cache_free(rp, pages, tp, S, P, ld, lp, sp, n, handle)
+    _check("dsa_cache_free", st)
+
+
+def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=None, stream=None):
+    """Move the pages in use to the lowest numbers (contents in all planes,
+    refs and table entries). Returns ``remap`` int32 [N], the new number of
+    each used page (-1 for free ones), and ``live`` int32 [1], how many are in
+    use; allocated when None."""
+    torch = _torch()
+    rp, pages, tp, S, P, ld, _, dev = _cache_state(refs, tables, None)
+    planes = _cache_planes(cache, pages)
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    with _Launch(dev, stream) as handle:
+        if remap is None:
+            remap = torch.empty(pages, dtype=torch.int32, device=dev)
+        if live is None:
+            live = torch.empty(1, dtype=torch.int32, device=dev)
+        (mp, n), (vp, one) = _vector(remap, "remap", dev), _vector(live, "live", dev)
+        if n != pages or one != 1:
+            raise ValueError(f"remap must have {pages} entries and live one")
+        ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(0, pages), dev)
+        st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp,
+                                         ws.data_ptr() if ws_bytes else None, ws_bytes, handle)
+    _check("dsa_cache_compact", st)
+    return remap, live
+
+
+def cache_workspace_bytes(pairs: int, num_pages: int) -> int:
+    """Bytes of workspace of ``dsa_cache_fork`` (of ``pairs`` pairs) or, with
+    0 pairs, of ``dsa_cache_compact``."""
+    return int(library().dsa_cache_workspace_bytes(pairs, num_pages))
 
 
 def _to_device(host, dev_buf, stream):

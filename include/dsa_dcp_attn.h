@@ -43,10 +43,13 @@
 extern "C" {
 #endif
 
-/* Element type of the attention outputs (the LSEs are always fp32). */
+/* Element type of the attention outputs (the LSEs are always fp32). The two
+ * entry points below take F32 and BF16, those of dsa_attention.h BF16 and
+ * F16. */
 typedef enum {
     DSA_DTYPE_F32 = 0,
-    DSA_DTYPE_BF16 = 1
+    DSA_DTYPE_BF16 = 1,
+    DSA_DTYPE_F16 = 2
 } dsa_dtype;
 
 /* Largest shard count N the two entry points accept (one lane of a warp per
