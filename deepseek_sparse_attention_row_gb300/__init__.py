@@ -71,6 +71,7 @@ __all__ = [
     "mapped_host_pointer",
     "set_launch_override",
     "pipeline_error",
+    "attention_error",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -106,6 +107,7 @@ EXPORTED_SYMBOLS = (
     "dsa_prompt_attention",
     "dsa_shared_prefix_workspace_bytes",
     "dsa_shared_prefix_attention",
+    "dsa_attention_error",
     "dsa_cache_workspace_bytes",
     "dsa_cache_fork",
     "dsa_cache_free",
@@ -181,6 +183,8 @@ def library():
     lib.dsa_shared_prefix_attention.argtypes = [p, p, p, i32, i64, i32, i32, i32, i64, i32, i64,
                                                 i64, i64, i64, i64, i64, i64, i64, p, i64, p, i64,
                                                 i64, p, f32, p, i64, i64, p, i64, i64, p, sz, p]
+    lib.dsa_attention_error.argtypes = [ctypes.c_int]
+    lib.dsa_attention_error.restype = ctypes.c_int
     lib.dsa_cache_workspace_bytes.argtypes = [i64, i64]
     lib.dsa_cache_workspace_bytes.restype = sz
     lib.dsa_cache_fork.argtypes = [p, i64, i64, i64, i64, i32, i64, p, p, i64, i64, i64, p, p, p,
@@ -222,6 +226,12 @@ def pipeline_error(clear: bool = False) -> int:
     """The pipelined kernels' give-up flag (0: none of their waits ever gave
     up); see dsa_pipeline_error."""
     return int(library().dsa_pipeline_error(1 if clear else 0))
+
+
+def attention_error(clear: bool = False) -> int:
+    """The attention kernels' give-up flag (0: none of their waits ever gave
+    up); see dsa_attention_error."""
+    return int(library().dsa_attention_error(1 if clear else 0))
 
 
 def _check(fn: str, status: int):

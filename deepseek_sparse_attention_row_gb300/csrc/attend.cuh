@@ -1,0 +1,1059 @@
+// attend.cuh -- the attention kernel on the tensor cores, shared by prompt
+// attention and by decode attention on pages.
+//
+// Mathematics. For a row q over the keys that it sees (c = scale * log2 e):
+// x_j = c <q, k_j>, m = max x_j, l = sum 2^(x_j - m), O = sum 2^(x_j - m) v_j.
+// Keys go by in tiles of 128. Per tile the row keeps a base b <= m + 8 / c
+// (in units of <q, k>) and adds 2^(c (s_j - b)) to l and to O; only when a new
+// maximum passes the base by more than 2^8 in weight are l and O multiplied
+// down and the base moved. Weights then stay below 2^8, and the largest is at
+// least 1, so that neither fp32 sums nor 16-bit weights lose anything by it.
+//
+// Rows. The G query heads of one key/value head share every key, so a matrix
+// tile of 128 rows holds 128 / G tokens of G heads each.
+//
+// One CTA per SM with 12 warps: four warps for each of two streams (one row
+// per thread: maxima, exponentials, sums, and at the end the output), one
+// warp that issues matrix products, one that loads, one that schedules. A
+// stream has its own 128 columns of tensor memory for the scores S = Q K^T
+// (the weights P overwrite them, as 16-bit pairs) and up to 128 for O += P V.
+// While one stream's warps are busy with exponentials, the tensor cores run
+// the other's products. The streams either take two row tiles over the same
+// keys (shared: each K and V tile is loaded once for 256 rows) or one row
+// tile over alternate key tiles (split: few rows, both streams busy; the
+// results are two partial outputs).
+//
+// A persistent CTA walks a list of segments (row tiles x a range of key
+// tiles) that the scheduling warp writes to a two-entry ring, so that loads
+// of the next segment run under the current one's end.
+//
+// Every wait is bounded (kAttendLimitNs); one that gives up records its site
+// in g_pipe_error, and all roles leave.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "umma.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
+constexpr int kAttendThreads = 384;  // no calls in the kernel: ptxas could not split registers
+constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's base
+// A row's recomputation (fix_row) may hold up its CTA's other roles for
+// seconds when a huge context holds infinities in masked places.
+constexpr unsigned long long kAttendLimitNs = 10000000000ull;
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+// {lo, hi} rounded to nearest even, lo in the low half
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
+
+// What a stream of segments is made of. Sizes are below 2^31.
+struct Seg {
+  int32_t n[2];     // key tiles of each stream; n[0] < 0: the list's end
+  int32_t split;    // streams: 0 two row tiles, 1 alternate key tiles
+  int32_t t0;       // first key tile
+  int32_t kh;       // key/value head
+  int32_t tok[2];   // first token of each row tile
+  int32_t ntok[2];  // its tokens
+  // prompt: keys [k0, k0 + kv_len); the token before q_end sees all of them
+  int32_t k0, kv_len, q_end;
+  // pages: the sequence whose own tokens these are, or -1 for the prefix
+  int32_t seq;
+  int64_t slot;     // of the partial outputs
+};
+
+struct AttendArgs {
+  const void *q, *k, *v;
+  int64_t q_st, q_sh;
+  int32_t heads, kv_heads, group, dim, tile_tokens;
+  float c;  // scale * log2 e
+  int64_t tokens;
+  // prompt
+  int64_t total_k, k_st, k_sh, v_st, v_sh;
+  const int32_t *cu_q, *cu_k;
+  int32_t seqs, causal;
+  void* out;
+  int64_t o_st, o_sh;
+  float* lse;
+  int64_t l_st, l_sh;
+  // pages
+  int64_t k_sn, v_sn;
+  int64_t num_pages, max_pages, ld_tables;
+  int32_t page_size, page_log2;
+  const int32_t *prefix_pages, *tables, *lens;
+  int64_t prefix_len;
+  int32_t prefix_tiles, prefix_blocks, prefix_split;
+  int64_t* starts;                 // [tokens + 1]: own units before each sequence
+  float *prefix_o, *prefix_lse;    // [slot][256][DP], [slot][256]
+  float *own_o, *own_lse;          // [slot][2 G][DP], [slot][2 G]
+};
+
+template <int DP>
+struct Layout {
+  static constexpr int kHalves = DP / 64;
+  static constexpr uint32_t kHalf = kTile * 128;  // [128 rows][64 elements], swizzled
+  static constexpr uint32_t kBytes = kHalf * kHalves;
+  static constexpr int kStages = DP == 128 ? 5 : 10;
+  static constexpr uint32_t kRing = 2 * kBytes;
+  static constexpr uint32_t kCtrl = kRing + kStages * kBytes;
+};
+
+constexpr int kMaxStages = 10;
+struct Ctrl {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t seg_full[2], seg_empty[2];
+  Seg seg[2];
+  uint32_t tmem;
+  int dead;
+};
+constexpr size_t attend_smem(uint32_t ctrl) { return 1024 + ctrl + sizeof(Ctrl); }
+
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctrl* c, unsigned site) {
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&c->dead)) return false;
+    if (global_ns() - t0 > kAttendLimitNs) {
+      atomicCAS(&g_pipe_error, 0u, site);
+      *reinterpret_cast<volatile int*>(&c->dead) = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctrl* c, unsigned site) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, c, site);
+}
+
+// The same for a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* c,
+                                          unsigned site) {
+  return __all_sync(~0u, wait(bar, parity, c, site));
+}
+
+__device__ __forceinline__ int32_t clamp_to(int32_t x, int64_t top) {
+  return x < 0 ? 0 : (x > top ? static_cast<int32_t>(top) : x);
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t n) { return n <= 0 ? 0 : (n + kTile - 1) / kTile; }
+
+// ---- schedules ------------------------------------------------------------
+
+// Prompts: blocks of 2 * tile_tokens tokens for every key/value head, those
+// of the same tokens next to each other, a sequence's last (causal: longest)
+// ones first; CTA x takes blocks x, x + grid, ...
+struct PromptSchedule {
+  int64_t id;
+  int32_t chunk = 0;     // first of the 32 sequences that the lanes hold
+  int64_t before = 0;    // blocks before them
+  bool loaded = false;
+  int32_t q0, q1, k0, k1;
+  int64_t upto;          // blocks up to the lane's sequence, it included
+
+  __device__ explicit PromptSchedule(const AttendArgs&) : id(blockIdx.x) {}
+
+  __device__ bool next(const AttendArgs& a, Seg& g) {
+    const int lane = threadIdx.x & 31;
+    const int32_t block = 2 * a.tile_tokens;
+    const int64_t at = id / a.kv_heads;
+    g.kh = static_cast<int32_t>(id % a.kv_heads);
+    id += gridDim.x;
+    for (; chunk < a.seqs; chunk += 32, loaded = false) {
+      if (!loaded) {
+        const int32_t i = chunk + lane;
+        q0 = q1 = k0 = k1 = 0;
+        if (i < a.seqs) {
+          q0 = clamp_to(a.cu_q[i], a.tokens);
+          q1 = clamp_to(a.cu_q[i + 1], a.tokens);
+          k0 = clamp_to(a.cu_k[i], a.total_k);
+          k1 = clamp_to(a.cu_k[i + 1], a.total_k);
+          if (q1 < q0) q1 = q0;
+          if (k1 < k0) k1 = k0;
+        }
+        upto = (static_cast<int64_t>(q1 - q0) + block - 1) / block;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(~0u, upto, o);
+          if (lane >= o) upto += y;
+        }
+        loaded = true;
+      }
+      const int64_t all = __shfl_sync(~0u, upto, 31);
+      if (at - before < all) {
+        const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
+        const int32_t s0 = __shfl_sync(~0u, q0, src), s1 = __shfl_sync(~0u, q1, src);
+        g.k0 = __shfl_sync(~0u, k0, src);
+        g.kv_len = __shfl_sync(~0u, k1, src) - g.k0;
+        g.q_end = s1;
+        const int64_t last = __shfl_sync(~0u, upto, src) - 1 - (at - before);
+        g.tok[0] = s0 + static_cast<int32_t>(last) * block;
+        g.ntok[0] = min(a.tile_tokens, s1 - g.tok[0]);
+        g.tok[1] = g.tok[0] + g.ntok[0];
+        g.ntok[1] = min(a.tile_tokens, s1 - g.tok[1]);
+        g.split = 0;
+        g.t0 = 0;
+        g.seq = 0;
+        g.slot = 0;
+        for (int s = 0; s < 2; ++s) {
+          // keys that the tile's last token sees
+          const int32_t lim =
+              a.causal ? g.kv_len - (s1 - g.tok[s] - g.ntok[s]) : g.kv_len;
+          g.n[s] = g.ntok[s] > 0 ? tiles_of(lim) : 0;
+        }
+        return true;
+      }
+      before += all;
+    }
+    return false;
+  }
+};
+
+// Keys of sequence b that lie in the prefix, and behind it.
+__device__ __forceinline__ int32_t seen_tokens(const AttendArgs& a, int64_t b) {
+  return clamp_to(a.lens[b], a.max_pages * a.page_size);
+}
+__device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
+  const int64_t n = seen_tokens(a, b) - a.prefix_len;
+  return n > 0 ? static_cast<int32_t>(n) : 0;
+}
+
+// Pages: the work is a line of units, one per (row block, key tile): first
+// the prefix (key/value head, block of the batch, tile), then every
+// sequence's own tokens (sequence, key/value head, tile). A unit is about as
+// dear in either part: 256 rows of products against a tile read from HBM. CTA
+// x takes the x-th equal share of the line, cut into segments where the row
+// block changes. Segment (group g, CTA x) has slot g + x, which grows along
+// the line: no two segments share one.
+struct PagedSchedule {
+  int64_t pos, end, prefix_units, own_units;
+  int32_t chunk = 0;
+  int64_t before = 0;   // own units before the chunk
+  bool loaded = false;
+  int32_t mine;         // own tiles of the lane's sequence
+  int64_t upto;
+
+  __device__ static int64_t units(const AttendArgs& a) {
+    return static_cast<int64_t>(a.kv_heads) * a.prefix_blocks * a.prefix_tiles;
+  }
+  __device__ static int64_t share_of(int64_t all, int64_t grid) { return (all + grid - 1) / grid; }
+
+  __device__ explicit PagedSchedule(const AttendArgs& a) {
+    const int lane = threadIdx.x & 31;
+    prefix_units = units(a);
+    own_units = 0;
+    // CTA 0 also writes down where each sequence's units start.
+    const bool first = blockIdx.x == 0;
+    for (int64_t b0 = 0; b0 < a.tokens; b0 += 32) {
+      const int64_t b = b0 + lane;
+      int64_t n = 0;
+      if (b < a.tokens) n = static_cast<int64_t>(tiles_of(own_tokens(a, b))) * a.kv_heads;
+      int64_t inc = n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (first && b < a.tokens) a.starts[b] = own_units + inc - n;
+      own_units += __shfl_sync(~0u, inc, 31);
+    }
+    if (first && lane == 0) a.starts[a.tokens] = own_units;
+    const int64_t all = prefix_units + own_units, share = share_of(all, gridDim.x);
+    pos = min(share * blockIdx.x, all);
+    end = min(pos + share, all);
+  }
+
+  __device__ bool next(const AttendArgs& a, Seg& g) {
+    if (pos >= end) return false;
+    g.k0 = g.q_end = g.kv_len = 0;
+    if (pos < prefix_units) {
+      const int64_t pg = pos / a.prefix_tiles;
+      const int32_t t = static_cast<int32_t>(pos % a.prefix_tiles);
+      const int32_t rb = static_cast<int32_t>(pg % a.prefix_blocks);
+      const int32_t n = static_cast<int32_t>(
+          min(static_cast<int64_t>(a.prefix_tiles - t), end - pos));
+      pos += n;
+      g.kh = static_cast<int32_t>(pg / a.prefix_blocks);
+      g.split = a.prefix_split;
+      g.t0 = t;
+      g.seq = -1;
+      g.slot = pg + blockIdx.x;
+      const int32_t rows = static_cast<int32_t>(a.tokens);
+      g.tok[0] = rb * (a.prefix_split ? 1 : 2) * a.tile_tokens;
+      g.ntok[0] = min(a.tile_tokens, rows - g.tok[0]);
+      g.tok[1] = g.tok[0] + g.ntok[0];
+      g.ntok[1] = g.split ? 0 : min(a.tile_tokens, rows - g.tok[1]);
+      g.n[0] = g.split ? (n + 1) / 2 : n;
+      g.n[1] = g.split ? n / 2 : (g.ntok[1] > 0 ? n : 0);
+      return true;
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t at = pos - prefix_units;
+    for (;; chunk += 32, loaded = false) {
+      if (chunk >= a.tokens) return false;  // the lengths changed under the call
+      if (!loaded) {
+        const int64_t b = static_cast<int64_t>(chunk) + lane;
+        mine = b < a.tokens ? tiles_of(own_tokens(a, b)) : 0;
+        upto = static_cast<int64_t>(mine) * a.kv_heads;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(~0u, upto, o);
+          if (lane >= o) upto += y;
+        }
+        loaded = true;
+      }
+      const int64_t all = __shfl_sync(~0u, upto, 31);
+      if (at - before < all) break;
+      before += all;
+    }
+    const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
+    const int32_t tiles = __shfl_sync(~0u, mine, src);
+    const int64_t rel = at - before - (__shfl_sync(~0u, upto, src) -
+                                       static_cast<int64_t>(tiles) * a.kv_heads);
+    g.kh = static_cast<int32_t>(rel / tiles);
+    g.t0 = static_cast<int32_t>(rel % tiles);
+    const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(tiles - g.t0), end - pos));
+    pos += n;
+    g.seq = chunk + src;
+    g.split = 1;
+    g.n[0] = (n + 1) / 2;
+    g.n[1] = n / 2;
+    g.tok[0] = g.tok[1] = g.seq;
+    g.ntok[0] = 1;
+    g.ntok[1] = 0;
+    g.slot = static_cast<int64_t>(g.seq) * a.kv_heads + g.kh + blockIdx.x;
+    return true;
+  }
+};
+
+template <bool PAGED>
+struct ScheduleOf { using type = PromptSchedule; };
+template <>
+struct ScheduleOf<true> { using type = PagedSchedule; };
+
+// ---- keys on pages ----------------------------------------------------------
+
+// The page of the segment's token t (counted from the prefix's start, or from
+// the sequence's first own token), or num_pages when there is none.
+__device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int64_t t) {
+  int64_t p = t >> a.page_log2;
+  const int32_t none = static_cast<int32_t>(a.num_pages);
+  const int64_t pre = a.prefix_len >> a.page_log2;
+  int32_t id;
+  if (seq < 0) {
+    if (p >= pre) return none;
+    id = __ldg(a.prefix_pages + p);
+  } else {
+    p += pre;
+    if (p >= a.max_pages) return none;
+    id = __ldg(a.tables + seq * a.ld_tables + p);
+  }
+  return id < 0 || id > none ? none : id;
+}
+
+// Address of key (or value) j of a segment; nullptr where none is.
+template <typename T, bool PAGED>
+__device__ __forceinline__ const T* row_at(const AttendArgs& a, const Seg& g, const void* base,
+                                           int64_t sn, int64_t st, int64_t sh, int64_t j) {
+  if constexpr (PAGED) {
+    const int32_t id = page_of(a, g.seq, j);
+    if (id >= a.num_pages) return nullptr;
+    return static_cast<const T*>(base) + id * sn + (j & (a.page_size - 1)) * st + g.kh * sh;
+  } else {
+    if (g.k0 + j >= a.total_k) return nullptr;
+    return static_cast<const T*>(base) + (g.k0 + j) * st + g.kh * sh;
+  }
+}
+
+// ---- rows with infinities or NaN in places that they do not see ------------
+
+// A masked weight is 0, but 0 times an infinite or NaN value is NaN: where a
+// row's output is not finite and a key tile that it visited holds a value
+// that is not finite behind the row's last key, the warp computes the row
+// again from its own keys alone. Returns false where no such value exists.
+// On return acc[i] is the normalised output of dimension lane + 32 i.
+template <typename T, bool PAGED>
+__device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s, int32_t lim,
+                                     int32_t tok, int32_t head, float (&acc)[4], float& lse) {
+  const int lane = threadIdx.x & 31;
+  const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s : 0);
+  bool hidden = false;
+  for (int32_t i = 0; i < g.n[s]; ++i) {
+    const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
+    for (int64_t j = max(k0, static_cast<int64_t>(lim)); j < k0 + kTile; ++j) {
+      const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
+      if (!v) continue;
+      for (int d = lane; d < a.dim; d += 32) hidden |= !finite(to_f(v[d]));
+    }
+    if (__any_sync(~0u, hidden)) break;
+  }
+  if (!__any_sync(~0u, hidden)) return false;
+  const T* q = static_cast<const T*>(a.q) + tok * a.q_st + head * a.q_sh;
+  float m = neg_inf(), l = 0.f;
+  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+  for (int32_t i = 0; i < g.n[s]; ++i) {
+    const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
+    const int64_t k1 = min(k0 + kTile, static_cast<int64_t>(lim));
+    for (int64_t j0 = k0; j0 < k1; j0 += 32) {
+      float x = neg_inf();
+      const T* k = j0 + lane < k1
+                       ? row_at<T, PAGED>(a, g, a.k, a.k_sn, a.k_st, a.k_sh, j0 + lane)
+                       : nullptr;
+      if (k) {
+        x = 0.f;
+        for (int d = 0; d < a.dim; ++d) x = fmaf(to_f(q[d]), to_f(k[d]), x);
+        x *= a.c;
+      }
+      float mx = x;
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+      const float m_new = fmaxf(m, mx), base = m_new == neg_inf() ? 0.f : m_new;
+      const float keep = ex2(m - base), p = ex2(x - base);
+      float sum = p;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      l = l * keep + sum;
+      m = m_new;
+      for (int e = 0; e < 4; ++e) acc[e] *= keep;
+      for (int64_t j = j0; j < j0 + 32 && j < k1; ++j) {
+        const float pj = __shfl_sync(~0u, p, static_cast<int>(j - j0));
+        const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
+        if (!v) continue;
+        for (int e = 0; e < 4; ++e)
+          if (lane + 32 * e < a.dim) acc[e] = fmaf(pj, to_f(v[lane + 32 * e]), acc[e]);
+      }
+      // nothing brings a NaN back: stop once all of the row is one
+      bool gone = true;
+      for (int e = 0; e < 4; ++e) gone &= lane + 32 * e >= a.dim || acc[e] != acc[e];
+      if (l != l || __all_sync(~0u, gone)) {
+        i = g.n[s];
+        break;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int e = 0; e < 4; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
+  lse = l == 0.f ? neg_inf() : m + log2f(l);
+  return true;
+}
+
+// ---- roles ------------------------------------------------------------------
+
+template <int DP>
+struct Cta {
+  unsigned char* base;
+  __device__ unsigned char* q(int s) const { return base + s * Layout<DP>::kBytes; }
+  __device__ unsigned char* stage(int i) const {
+    return base + Layout<DP>::kRing + i * Layout<DP>::kBytes;
+  }
+  __device__ Ctrl* ctrl() const { return reinterpret_cast<Ctrl*>(base + Layout<DP>::kCtrl); }
+};
+
+// Where a role stands in the ring of K and V stages.
+template <int DP>
+struct Ring {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ void next() {
+    if (++stage == Layout<DP>::kStages) stage = 0, ++round;
+  }
+};
+
+// Segment `k` of the list, for one warp (or for one thread alone).
+template <bool WARP>
+__device__ __forceinline__ bool take_seg(Ctrl* c, uint32_t k, Seg& g, unsigned site) {
+  uint64_t* bar = &c->seg_full[k & 1];
+  if (!(WARP ? wait_warp(bar, (k >> 1) & 1, c, site) : wait(bar, (k >> 1) & 1, c, site)))
+    return false;
+  g = c->seg[k & 1];
+  if (WARP) __syncwarp();
+  if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&c->seg_empty[k & 1]);
+  return true;
+}
+
+template <int DP, bool PAGED>
+__device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
+  Ctrl* c = cta.ctrl();
+  typename ScheduleOf<PAGED>::type list(a);
+  for (uint32_t k = 0;; ++k) {
+    Seg g;
+    const bool more = list.next(a, g);
+    if (!more) g.n[0] = -1;
+    if (k >= 2 && !wait_warp(&c->seg_empty[k & 1], ((k >> 1) - 1) & 1, c, 16)) return;
+    if ((threadIdx.x & 31) == 0) {
+      c->seg[k & 1] = g;
+      mbar_arrive(&c->seg_full[k & 1]);
+    }
+    __syncwarp();
+    if (!more) return;
+  }
+}
+
+// The loading warp: per segment the row tiles, then K and V in the order in
+// which the products take them: K leads V by one tile (shared) or two (split).
+template <int DP, bool PAGED>
+__device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorMap* km,
+                     const CUtensorMap* vm, Cta<DP> cta) {
+  using L = Layout<DP>;
+  Ctrl* c = cta.ctrl();
+  const int lane = threadIdx.x & 31;
+  Ring<DP> ring;
+  uint32_t active = 0;
+  // boxes of a K or V tile, one lane each: page within the tile, half
+  const int boxes = PAGED && a.page_size < kTile ? kTile / a.page_size : 1;
+  const int pi = lane / L::kHalves, h = lane % L::kHalves;
+  const uint32_t to = h * L::kHalf + (PAGED ? pi * a.page_size * 128 : 0);
+  for (uint32_t k = 0;; ++k) {
+    Seg g;
+    if (!take_seg<true>(c, k, g, 17)) return;
+    if (g.n[0] < 0) break;
+    const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
+    if (n == 0) continue;
+    if (active > 0 && !wait_warp(&c->q_empty, (active - 1) & 1, c, 18)) return;
+    ++active;
+    const int tiles = g.ntok[1] > 0 ? 2 : 1;
+    if (lane == 0)
+      mbar_arrive_expect_tx(&c->q_full, tiles * L::kHalves * a.tile_tokens * a.group * 128);
+    __syncwarp();
+    if (lane < tiles * L::kHalves)
+      tma_load3(cta.q(lane / L::kHalves) + h * L::kHalf, qm, h * 64, g.kh * a.group,
+                g.tok[lane / L::kHalves], &c->q_full);
+    const auto page = [&](int32_t t) -> int32_t {
+      if constexpr (PAGED) {
+        if (lane < boxes * L::kHalves && t < g.t0 + n)
+          return page_of(a, g.seq, static_cast<int64_t>(t) * kTile + pi * a.page_size);
+      }
+      return 0;
+    };
+    const auto put = [&](const CUtensorMap* map, int32_t t, int32_t id) -> bool {
+      const int st = ring.stage;
+      if (ring.round > 0 && !wait_warp(&c->kv_empty[st], (ring.round - 1) & 1, c, 19)) return false;
+      ring.next();
+      if (lane == 0) mbar_arrive_expect_tx(&c->kv_full[st], L::kBytes);
+      __syncwarp();
+      if (lane < boxes * L::kHalves) {
+        unsigned char* dst = cta.stage(st) + to;
+        if constexpr (PAGED)
+          tma_load4(dst, map, h * 64, g.kh, (t * kTile) & (a.page_size - 1), id, &c->kv_full[st]);
+        else
+          tma_load3(dst, map, h * 64, g.kh, g.k0 + t * kTile, &c->kv_full[st]);
+      }
+      return true;
+    };
+    int32_t id0 = page(g.t0), id1 = page(g.t0 + 1);
+    const int lead = g.split ? 2 : 1;
+    if (!put(km, g.t0, id0)) return;
+    if (lead == 2 && n > 1 && !put(km, g.t0 + 1, id1)) return;
+    for (int32_t j = 0; j < n; ++j) {
+      const int32_t t = g.t0 + j;
+      const int32_t id2 = page(t + 2);
+      if (!put(vm, t, id0)) return;
+      if (j + lead < n && !put(km, t + lead, lead == 2 ? id2 : id1)) return;
+      id0 = id1;
+      id1 = id2;
+    }
+  }
+  // The last arrivals of the products on these barriers come before the
+  // shared memory is given back.
+  for (int i = 0; i < L::kStages; ++i) {
+    const uint32_t uses = ring.round + (i < ring.stage ? 1 : 0);
+    if (uses > 0 && !wait_warp(&c->kv_empty[i], (uses - 1) & 1, c, 19)) return;
+  }
+  if (active > 0) wait_warp(&c->q_empty, (active - 1) & 1, c, 18);
+}
+
+// The thread that issues the products. In program order: for each key tile
+// the products P V of a stream, then the next Q K^T into the same columns.
+template <typename T, int DP>
+__device__ void multiply(Cta<DP> cta, uint32_t tmem) {
+  using L = Layout<DP>;
+  Ctrl* c = cta.ctrl();
+  constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
+  constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
+  const uint32_t q0 = smem_addr(cta.q(0)), st0 = smem_addr(cta.stage(0));
+  Ring<DP> ring;
+  uint32_t segs = 0;             // segments with products so far
+  uint32_t done[2] = {0, 0};     // tiles of each stream
+  uint32_t outs[2] = {0, 0};     // segments of each stream with products
+
+  const auto full = [&]() { return wait(&c->kv_full[ring.stage], ring.round & 1, c, 20); };
+  const auto drop = [&]() {
+    mma_commit(&c->kv_empty[ring.stage]);
+    ring.next();
+  };
+  const auto scores = [&](int s, int qs) {
+    const uint64_t qa = operand(q0 + qs * L::kBytes, 16, 1024);
+    const uint64_t kb = operand(st0 + ring.stage * L::kBytes, 16, 1024);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const uint64_t off = ((i / 4) * L::kHalf + (i % 4) * 32) >> 4;
+      mma_ss(tmem + s * kTile, qa + off, kb + off, kShapeS, i > 0);
+    }
+    mma_commit(&c->s_full[s]);
+  };
+  // P V of stream s with the V tile in the ring's current stage
+  const auto values = [&](int s, bool first) -> bool {
+    if (!wait(&c->p_full[s], done[s] & 1, c, 21)) return false;
+    if (first) {
+      if (outs[s] > 0 && !wait(&c->o_free[s], (outs[s] - 1) & 1, c, 22)) return false;
+      ++outs[s];
+    }
+    ++done[s];
+    tc_fence_after();
+    const uint64_t vb = operand(st0 + ring.stage * L::kBytes, L::kHalf, 1024);
+#pragma unroll
+    for (int i = 0; i < kTile / 16; ++i)
+      mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + i * 8, vb + ((i * 2048) >> 4),
+             kShapeO, !first || i > 0);
+    mma_commit(&c->o_done[s]);
+    return true;
+  };
+
+  for (uint32_t k = 0;; ++k) {
+    Seg g;
+    if (!take_seg<false>(c, k, g, 23) || g.n[0] < 0) return;
+    const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
+    if (n == 0) continue;
+    if (!wait(&c->q_full, segs & 1, c, 24)) return;
+    ++segs;
+    if (g.split) {
+      for (int32_t j = 0; j < min(n, 2); ++j) {
+        if (!full()) return;
+        tc_fence_after();
+        scores(j, 0);
+        drop();
+      }
+      if (n <= 2) mma_commit(&c->q_empty);
+      for (int32_t j = 0; j < n; ++j) {
+        const int s = j & 1;
+        if (!full()) return;
+        if (!values(s, j < 2)) return;
+        drop();
+        if (j + 2 < n) {
+          if (!full()) return;
+          tc_fence_after();
+          scores(s, 0);
+          drop();
+          if (j + 3 == n) mma_commit(&c->q_empty);
+        }
+      }
+    } else {
+      if (!full()) return;
+      tc_fence_after();
+      for (int s = 0; s < 2; ++s)
+        if (g.n[s] > 0) scores(s, s);
+      drop();
+      if (n == 1) mma_commit(&c->q_empty);
+      for (int32_t j = 0; j < n; ++j) {
+        // V_j in the current stage, K_{j+1} in the next one
+        if (!full()) return;
+        const Ring<DP> v = ring;
+        Ring<DP> kn = ring;
+        kn.next();
+        bool have = false;
+        for (int s = 0; s < 2; ++s) {
+          if (j < g.n[s]) {
+            if (!values(s, j == 0)) return;
+          }
+          if (s == 1) mma_commit(&c->kv_empty[v.stage]);
+          if (j + 1 < g.n[s]) {
+            ring = kn;
+            if (!have && !full()) return;
+            have = true;
+            tc_fence_after();
+            scores(s, s);
+            ring = v;
+          }
+        }
+        ring = kn;
+        if (j + 1 < n) {
+          drop();
+          if (j + 2 == n) mma_commit(&c->q_empty);
+        }
+      }
+    }
+  }
+}
+
+// Four warps of stream s, one row per thread.
+template <typename T, int DP, bool PAGED>
+__device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
+  Ctrl* c = cta.ctrl();
+  const int lane = threadIdx.x & 31;
+  const int32_t row = threadIdx.x & 127;
+  const int32_t rt = row / a.group, head0 = row % a.group;  // token of the tile, head of the group
+  const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
+  const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kTile;
+  const float grow = kGrow / a.c;
+  uint32_t done = 0;
+  for (uint32_t k = 0;; ++k) {
+    Seg g;
+    if (!take_seg<true>(c, k, g, 25) || g.n[0] < 0) return;
+    const int qs = g.split ? 0 : s;
+    const int32_t n = g.n[s];
+    const bool valid = rt < g.ntok[qs];  // ntok <= tile_tokens
+    const int32_t tok = g.tok[qs] + rt;
+    // keys that the row sees, of the segment's list; rows of no token are
+    // not masked at all (nothing is written for them)
+    int32_t lim = 0x7fffffff;
+    if (valid) {
+      if constexpr (PAGED) {
+        lim = g.seq < 0 ? min(seen_tokens(a, tok), static_cast<int32_t>(a.prefix_len))
+                        : own_tokens(a, tok);
+      } else {
+        lim = a.causal ? g.kv_len - (g.q_end - 1 - tok) : g.kv_len;
+      }
+    }
+    float base = neg_inf(), l = 0.f;  // the row's base, in units of <q, k>
+    for (int32_t i = 0; i < n; ++i) {
+      const int32_t t = g.split ? g.t0 + s + 2 * i : g.t0 + i;
+      uint32_t bad = 0;  // pages of the tile that are not there
+      if constexpr (PAGED) {
+        const int pages = a.page_size < kTile ? kTile >> a.page_log2 : 1;
+        bool none = false;
+        if (lane < pages)
+          none = page_of(a, g.seq, static_cast<int64_t>(t) * kTile + lane * a.page_size) >=
+                 a.num_pages;
+        bad = __ballot_sync(~0u, none);
+      }
+      if (!wait_warp(&c->s_full[s], done & 1, c, 26)) return;
+      ++done;
+      tc_fence_after();
+      float x[kTile];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        tmem_load32(ts + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
+      tmem_wait_load();
+      const int64_t rel = static_cast<int64_t>(lim) - static_cast<int64_t>(t) * kTile;
+      if (rel < kTile || bad != 0) {
+        const int r = rel < 0 ? 0 : (rel > kTile ? kTile : static_cast<int>(rel));
+        if (bad == 0) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) x[j] = j < r ? x[j] : neg_inf();
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            x[j] = j < r && !((bad >> (j >> a.page_log2)) & 1) ? x[j] : neg_inf();
+        }
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int j = 4; j < kTile - 4; j += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (__any_sync(~0u, top > base + grow)) {
+        const float was = base;
+        base = fmaxf(base, top);
+        if (i > 0) {
+          const float f = was == base ? 1.f : ex2((was - base) * a.c);
+          l *= f;
+          if (!wait_warp(&c->o_done[s], (done - 2) & 1, c, 27)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int b = 0; b < DP; b += 32) {
+            uint32_t o[32];
+            tmem_load32(to + b, o);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_store32(to + b, o);
+          }
+        }
+      }
+      // base is -inf while the row has seen no key: every x is -inf then
+      const float shift = base == neg_inf() ? 0.f : -base * a.c;
+      const float2 cc = make_float2(a.c, a.c), sh = make_float2(shift, shift);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int e = b * 32 + 2 * j;
+          float2 y = fma2(make_float2(x[e], x[e + 1]), cc, sh);
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum[j & 1] = add2(sum[j & 1], y);
+          p[j] = pack2(y.x, y.y, T());
+        }
+        tmem_store16(ts + 16 * b, p);
+      }
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
+      tmem_wait_store();
+      tc_fence_before();
+      mbar_arrive(&c->p_full[s]);
+    }
+
+    // The output. l is 0 only where no key was seen.
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float lse = l == 0.f ? neg_inf() : base * a.c + log2f(l);
+    const int32_t head = g.kh * a.group + head0;
+    T* out = nullptr;
+    float *part = nullptr, *lse_at = nullptr;
+    if (valid) {
+      if constexpr (PAGED) {
+        if (g.seq < 0) {
+          const int64_t r = g.slot * 256 + s * kTile + row;
+          part = a.prefix_o + r * DP;
+          lse_at = a.prefix_lse + r;
+        } else {
+          const int64_t r = (g.slot * 2 + s) * a.group + row;
+          part = a.own_o + r * DP;
+          lse_at = a.own_lse + r;
+        }
+      } else {
+        out = static_cast<T*>(a.out) + tok * a.o_st + head * a.o_sh;
+        if (a.lse) lse_at = a.lse + tok * a.l_st + head * a.l_sh;
+      }
+    }
+    bool odd = false;  // a value that is not finite
+    if (n > 0) {
+      if (!wait_warp(&c->o_done[s], (done - 1) & 1, c, 28)) return;
+      tc_fence_after();
+    }
+#pragma unroll 1
+    for (int b = 0; b < DP; b += 32) {
+      float o[32];
+      if (n > 0) {
+        tmem_load32(to + b, *reinterpret_cast<uint32_t(*)[32]>(o));
+        tmem_wait_load();
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        o[j] = l == 0.f ? 0.f : o[j] * inv;
+        odd |= b + j < a.dim && !finite(o[j]);
+      }
+      if constexpr (PAGED) {
+        if (part) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(part + b + j) =
+                make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+      } else {
+        if (out) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            if (b + j < a.dim)
+              *reinterpret_cast<uint4*>(out + b + j) =
+                  make_uint4(pack2(o[j], o[j + 1], T()), pack2(o[j + 2], o[j + 3], T()),
+                             pack2(o[j + 4], o[j + 5], T()), pack2(o[j + 6], o[j + 7], T()));
+        }
+      }
+    }
+    if (n > 0) {
+      tc_fence_before();
+      mbar_arrive(&c->o_free[s]);
+    }
+    if (lse_at) *lse_at = lse;
+
+    const int32_t seen_tiles = n > 0 ? (g.split ? g.t0 + s + 2 * (n - 1) : g.t0 + n - 1) + 1 : 0;
+    uint32_t todo = __ballot_sync(
+        ~0u, valid && odd && lim < static_cast<int64_t>(seen_tiles) * kTile);
+    while (todo != 0) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int32_t flim = __shfl_sync(~0u, lim, src), ftok = __shfl_sync(~0u, tok, src),
+                    fhead = __shfl_sync(~0u, head, src);
+      T* fout = reinterpret_cast<T*>(
+          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), src));
+      float* fpart = reinterpret_cast<float*>(
+          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(part), src));
+      float* flse_at = reinterpret_cast<float*>(
+          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(lse_at), src));
+      float acc[4], flse;
+      if (!fix_row<T, PAGED>(a, g, s, flim, ftok, fhead, acc, flse)) continue;
+      __syncwarp();  // behind the row's first stores, which another lane made
+      for (int e = 0; e < 4; ++e) {
+        const int d = lane + 32 * e;
+        if (d < a.dim) {
+          if constexpr (PAGED) fpart[d] = acc[e];
+          else fout[d] = from_f<T>(acc[e]);
+        }
+      }
+      if (flse_at && lane == 0) *flse_at = flse;
+      __syncwarp();
+    }
+  }
+}
+
+template <typename T, int DP, bool PAGED>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                  const __grid_constant__ CUtensorMap vm, const __grid_constant__ AttendArgs a) {
+  using L = Layout<DP>;
+  extern __shared__ unsigned char raw[];
+  Cta<DP> cta;
+  cta.base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);  // swizzle atoms are 1 KiB
+  Ctrl* c = cta.ctrl();
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&c->kv_full[i], 1);
+      mbar_init(&c->kv_empty[i], 1);
+    }
+    mbar_init(&c->q_full, 1);
+    mbar_init(&c->q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&c->s_full[s], 1);
+      mbar_init(&c->p_full[s], kTile);
+      mbar_init(&c->o_done[s], 1);
+      mbar_init(&c->o_free[s], kTile);
+      mbar_init(&c->seg_full[s], 1);
+      mbar_init(&c->seg_empty[s], 10);  // the loading and multiplying roles, eight warps
+    }
+    c->dead = 0;
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    tmem_alloc(&c->tmem);
+  } else if (warp == 9 && (threadIdx.x & 31) == 0) {
+    tma_prefetch(&qm);
+    tma_prefetch(&km);
+    tma_prefetch(&vm);
+  }
+  // Rows that no token of a tile fills are products of zeros.
+  const int used = a.tile_tokens * a.group;
+  for (int i = threadIdx.x; i < 2 * L::kHalves * (kTile - used) * 8; i += kAttendThreads) {
+    const int tile = i / ((kTile - used) * 8), rest = i % ((kTile - used) * 8);
+    *reinterpret_cast<uint4*>(cta.base + tile * L::kHalf + used * 128 + rest * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+  async_proxy_fence();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  // 168 registers a thread at the launch: 256 x 216 + 128 x 72 = 384 x 168.
+  if (warp < 8) {
+    reg_grow<216>();
+    soften<T, DP, PAGED>(a, cta, tmem, warp >> 2);
+  } else {
+    reg_shrink<72>();
+    if (warp == 8) {
+      if ((threadIdx.x & 31) == 0) multiply<T, DP>(cta, tmem);
+    } else if (warp == 9) {
+      load<DP, PAGED>(a, &qm, &km, &vm, cta);
+    } else if (warp == 10) {
+      schedule<DP, PAGED>(a, cta);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (c->dead) {
+    // A wait gave up: loads and products may still be under way. Give them
+    // time to land before the memory is handed on.
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 10000000ull) __nanosleep(100000);
+    __syncthreads();
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem);
+  }
+}
+
+// ---- partial outputs of the paged form joined -------------------------------
+
+// One warp per (sequence, head): the partial outputs of its prefix segments
+// and of its own ones, weighted by 2^(lse_i - F) with F the log-sum-exp of
+// their log-sum-exps.
+struct JoinArgs {
+  void* out;
+  int64_t o_sb, o_sh;
+  float* lse;
+  int64_t l_sb, l_sh;
+  int64_t grid;  // CTAs that shared the work
+};
+constexpr int kJoinWarps = 4;
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    join_kernel(const __grid_constant__ AttendArgs a, const JoinArgs j) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  if (r >= a.tokens * a.heads) return;
+  const int64_t b = r / a.heads;
+  const int32_t h = static_cast<int32_t>(r % a.heads), kh = h / a.group, e = h % a.group;
+  const int64_t pre = PagedSchedule::units(a), own = a.starts[a.tokens];
+  const int64_t share = PagedSchedule::share_of(pre + own, j.grid);
+  // Partial i < np: prefix; np <= i < np + no: own. In both the segments of
+  // one group have consecutive slots, each with one or two partials.
+  int64_t p0 = 0, o0 = 0;
+  int32_t np = 0, no = 0;
+  const int32_t per = a.prefix_split ? 2 : 1;
+  if (a.prefix_tiles > 0) {
+    const int32_t block = (a.prefix_split ? 1 : 2) * a.tile_tokens;
+    const int64_t rb = b / block, in = b % block, pg = kh * a.prefix_blocks + rb;
+    const int64_t u = pg * a.prefix_tiles, c0 = u / share,
+                  c1 = (u + a.prefix_tiles - 1) / share;
+    np = static_cast<int32_t>(c1 - c0 + 1) * per;
+    p0 = (pg + c0) * 256 + (in / a.tile_tokens) * kTile + (in % a.tile_tokens) * a.group + e;
+  }
+  const int64_t mine = a.starts[b + 1] - a.starts[b];
+  if (mine > 0) {
+    const int64_t tiles = mine / a.kv_heads, u = pre + a.starts[b] + kh * tiles;
+    const int64_t c0 = u / share, c1 = (u + tiles - 1) / share;
+    no = static_cast<int32_t>(c1 - c0 + 1) * 2;
+    o0 = (b * a.kv_heads + kh + c0) * 2 * a.group + e;
+  }
+  const auto at = [&](int32_t i) -> int64_t {  // row of partial i in its buffer
+    if (i < np) return p0 + (a.prefix_split ? static_cast<int64_t>(i) * kTile : i * 256ll);
+    return o0 + static_cast<int64_t>(i - np) * a.group;
+  };
+  const auto lse_of = [&](int32_t i) {
+    return i < np ? a.prefix_lse[at(i)] : a.own_lse[at(i)];
+  };
+  float m = neg_inf();
+  for (int32_t i = lane; i < np + no; i += 32) m = fmaxf(m, lse_of(i));
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  const float base = m == neg_inf() ? 0.f : m;
+  float sum = 0.f;
+  for (int32_t i = lane; i < np + no; i += 32) sum += ex2(lse_of(i) - base);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  const bool any = sum != 0.f;  // NaN counts
+  const float lse = any ? base + log2f(sum) : neg_inf();
+  constexpr int kPer = DP / 32;  // values of a lane
+  float acc[kPer];
+  for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
+#pragma unroll 4
+  for (int32_t i = 0; i < np + no; ++i) {
+    const float x = lse_of(i);
+    if (x == neg_inf()) continue;  // nothing seen: its output was not written
+    const float w = ex2(x - lse);
+    const float* o = (i < np ? a.prefix_o : a.own_o) + at(i) * DP + lane * kPer;
+    for (int d = 0; d < kPer; ++d) acc[d] = fmaf(w, o[d], acc[d]);
+  }
+  if (lane * kPer < a.dim) {
+    T* out = static_cast<T*>(j.out) + b * j.o_sb + h * j.o_sh + lane * kPer;
+    for (int d = 0; d < kPer; ++d) out[d] = from_f<T>(acc[d]);
+  }
+  if (j.lse && lane == 0) j.lse[b * j.l_sb + h * j.l_sh] = lse;
+}
+
+}  // namespace
+}  // namespace dsa

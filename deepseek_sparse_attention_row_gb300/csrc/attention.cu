@@ -1,21 +1,15 @@
 // attention.cu -- prompt attention and shared-prefix decode attention: the C
-// ABI of include/dsa_attention.h.
-//
-// Per query row, over the keys that it sees (c = scale * log2 e):
-//   x_j = c <q, k_j>,  m = max x_j,  l = sum 2^(x_j - m),
-//   out = (sum 2^(x_j - m) v_j) / l,  lse = m + log2 l.
-// One warp takes one row and walks its keys 32 at a time with a running
-// maximum and sum: a lane forms the product of one key with the row (kept in
-// shared memory as fp32), then every lane adds its dimensions of the 32
-// values.
+// ABI of include/dsa_attention.h. The kernel is in attend.cuh; here are the
+// checks of arguments, the tensor maps, the workspace and the launches.
 #include "../../include/dsa_attention.h"
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+
+#include "attend.cuh"
 
 namespace dsa {
 namespace {
@@ -24,186 +18,155 @@ constexpr int kMaxHeadDim = 128;
 constexpr int kMaxGroup = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
-
-// Where key (or value) j of one row's sequence lies: nullptr when no page
-// holds it.
-template <typename T>
-struct Packed {
-  const T* base;
-  int64_t st;
-  __device__ const T* at(int64_t j) const { return base + j * st; }
-};
-template <typename T>
-struct Paged {
-  const T* base;  // head's offset included
-  int64_t sn, st;
-  const int32_t* prefix;
-  int64_t prefix_len;
-  const int32_t* table;
-  int64_t num_pages;
-  int32_t page_size;
-  __device__ const T* at(int64_t j) const {
-    const int64_t p = j / page_size;
-    const int32_t id = j < prefix_len ? prefix[p] : table[p];
-    if (id < 0 || id >= num_pages) return nullptr;
-    return base + id * sn + (j % page_size) * st;
-  }
-};
-
-// One warp, one row: q in qs (fp32, shared memory), keys [0, n).
-template <typename T, typename KAt, typename VAt>
-__device__ void attend_row(const float* qs, int dim, const KAt& ks, const VAt& vs, int64_t n,
-                           float c, T* out, float* lse) {
-  const int lane = threadIdx.x & 31;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};  // dimensions lane + 32 i
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j0 = 0; j0 < n; j0 += 32) {
-    float x = -INFINITY;
-    const T* k = j0 + lane < n ? ks.at(j0 + lane) : nullptr;
-    if (k) {
-      x = 0.f;
-      for (int d = 0; d < dim; ++d) x = fmaf(qs[d], to_f(k[d]), x);
-      x *= c;
-    }
-    float mx = x;
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    const float m_new = fmaxf(m, mx);
-    const float base = m_new == -INFINITY ? 0.f : m_new;
-    const float keep = exp2f(m - base);
-    const float p = exp2f(x - base);  // 0 for keys that are not seen
-    float sum = p;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    l = l * keep + sum;
-    m = m_new;
-    for (int i = 0; i < 4; ++i) acc[i] *= keep;
-    const int32_t cnt = static_cast<int32_t>(n - j0 < 32 ? n - j0 : 32);
-    for (int32_t jj = 0; jj < cnt; ++jj) {
-      const float pj = __shfl_sync(~0u, p, jj);
-      const T* v = vs.at(j0 + jj);
-      if (!v) continue;
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < dim) acc[i] = fmaf(pj, to_f(v[lane + 32 * i]), acc[i]);
-    }
-  }
-  // l is 0 only where no key was seen (or every weight is 0 by x = -inf)
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < dim) out[lane + 32 * i] = from_f<T>(l == 0.f ? 0.f : acc[i] * inv);
-  if (lse && lane == 0) *lse = l == 0.f ? -INFINITY : m + log2f(l);
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? dev : -1;
 }
 
-struct PromptArgs {
-  const void *q, *k, *v;
-  int64_t total_q, total_k;
-  int32_t heads, kv_heads, dim;
-  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
-  const int32_t *cu_q, *cu_k;
-  int32_t seqs, causal;
-  float c;
-  void* out;
-  int64_t o_st, o_sh;
-  float* lse;
-  int64_t l_st, l_sh;
+// Streaming multiprocessors of the current device, cached per device.
+int sm_count() {
+  static std::atomic<int> cached[64];
+  const int dev = current_device();
+  if (dev < 0) return 152;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      return 152;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// The driver's encoder of tensor maps (a host function; looked up once).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static std::atomic<EncodeFn> cached{nullptr};
+  EncodeFn fn = cached.load(std::memory_order_relaxed);
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn = reinterpret_cast<EncodeFn>(p);
+    cached.store(fn, std::memory_order_relaxed);
+  }
+  return fn;
+}
+
+// A map of rank `n` over 16-bit elements; strides (of dimensions 1...) in
+// elements; boxes are [64 elements] x box[1...], swizzled by 128 bytes, and
+// read zeros outside the tensor.
+template <int N>
+bool encode(CUtensorMap* map, int32_t dtype, const void* base, const int64_t (&dims)[N],
+            const int64_t (&strides)[N - 1], const int (&box)[N]) {
+  EncodeFn fn = encoder();
+  if (!fn) return false;
+  cuuint64_t d[N], st[N - 1];
+  cuuint32_t b[N], one[N];
+  for (int i = 0; i < N; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    one[i] = 1;
+    if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
+  }
+  return fn(map,
+            dtype == DSA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            N, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap q, k, v;
 };
 
-__device__ __forceinline__ int64_t clamped(int32_t x, int64_t top) {
-  return x < 0 ? 0 : (x > top ? top : x);
+template <typename T, int DP, bool PAGED>
+dsa_status launch(const Maps& m, const AttendArgs& a, int grid, cudaStream_t stream) {
+  constexpr size_t kSmem = attend_smem(Layout<DP>::kCtrl);
+  static_assert(kSmem <= 232448, "shared memory of one SM");
+  static std::atomic<bool> ready[64];  // per device
+  const int dev = current_device();
+  if (dev < 0) return DSA_ECUDA;
+  auto* kernel = attend_kernel<T, DP, PAGED>;
+  if (!ready[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem)) != cudaSuccess)
+      return DSA_ECUDA;
+    ready[dev].store(true, std::memory_order_relaxed);
+  }
+  kernel<<<grid, kAttendThreads, kSmem, stream>>>(m.q, m.k, m.v, a);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
-constexpr int kWarps = 8;
+template <bool PAGED>
+dsa_status launch(const Maps& m, const AttendArgs& a, int32_t dtype, int grid,
+                  cudaStream_t stream) {
+  if (dtype == DSA_DTYPE_BF16)
+    return a.dim > 64 ? launch<__nv_bfloat16, 128, PAGED>(m, a, grid, stream)
+                      : launch<__nv_bfloat16, 64, PAGED>(m, a, grid, stream);
+  return a.dim > 64 ? launch<__half, 128, PAGED>(m, a, grid, stream)
+                    : launch<__half, 64, PAGED>(m, a, grid, stream);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) prompt_kernel(const PromptArgs a) {
-  __shared__ float qs[kWarps][kMaxHeadDim];
-  float* mine = qs[threadIdx.x >> 5];
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = a.total_q * a.heads;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < rows;
-       r += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t t = r / a.heads;
-    const int32_t h = static_cast<int32_t>(r % a.heads);
-    // the sequence of token t: the last one that starts at or before it
-    int32_t lo = 0, hi = a.seqs;  // cu_q[lo] <= t < cu_q[hi]
-    if (t < clamped(a.cu_q[0], a.total_q) || t >= clamped(a.cu_q[a.seqs], a.total_q)) continue;
-    while (hi - lo > 1) {
-      const int32_t mid = (lo + hi) >> 1;
-      if (clamped(a.cu_q[mid], a.total_q) <= t) lo = mid; else hi = mid;
-    }
-    const int64_t q0 = clamped(a.cu_q[lo], a.total_q), q1 = clamped(a.cu_q[lo + 1], a.total_q);
-    const int64_t k0 = clamped(a.cu_k[lo], a.total_k);
-    int64_t n = clamped(a.cu_k[lo + 1], a.total_k) - k0;
-    if (n < 0) n = 0;
-    if (a.causal) {
-      const int64_t lim = t - q0 + 1 + n - (q1 - q0);
-      n = lim < n ? (lim < 0 ? 0 : lim) : n;
-    }
-    const int64_t kh = h / (a.heads / a.kv_heads);
-    const T* q = static_cast<const T*>(a.q) + t * a.q_st + h * a.q_sh;
-    __syncwarp();
-    for (int d = lane; d < a.dim; d += 32) mine[d] = to_f(q[d]);
-    __syncwarp();
-    const Packed<T> ks{static_cast<const T*>(a.k) + k0 * a.k_st + kh * a.k_sh, a.k_st};
-    const Packed<T> vs{static_cast<const T*>(a.v) + k0 * a.v_st + kh * a.v_sh, a.v_st};
-    attend_row<T>(mine, a.dim, ks, vs, n, a.c, static_cast<T*>(a.out) + t * a.o_st + h * a.o_sh,
-                  a.lse ? a.lse + t * a.l_st + h * a.l_sh : nullptr);
-  }
+dsa_status launch_join(const AttendArgs& a, const JoinArgs& j, cudaStream_t stream) {
+  const int64_t rows = a.tokens * a.heads;
+  const int64_t ctas = (rows + kJoinWarps - 1) / kJoinWarps;
+  if (ctas > INT32_MAX) return DSA_EUNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(ctas);
+  if (a.dim > 64) join_kernel<T, 128><<<grid, kJoinWarps * 32, 0, stream>>>(a, j);
+  else join_kernel<T, 64><<<grid, kJoinWarps * 32, 0, stream>>>(a, j);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
-struct SharedArgs {
-  const void *q, *k, *v;
-  int64_t batch;
-  int32_t heads, kv_heads, dim;
-  int64_t num_pages;
-  int32_t page_size;
-  int64_t q_sb, q_sh, k_sn, k_st, k_sh, v_sn, v_st, v_sh;
-  const int32_t* prefix_pages;
-  int64_t prefix_len;
-  const int32_t* tables;
-  int64_t max_pages, ld_tables;
-  const int32_t* lens;
-  float c;
-  void* out;
-  int64_t o_sb, o_sh;
-  float* lse;
-  int64_t l_sb, l_sh;
+// How a paged call's work is cut, and where its partial outputs lie in the
+// workspace (each part 256-byte aligned).
+struct PagedPlan {
+  int32_t tile_tokens, prefix_tiles, prefix_blocks, prefix_split;
+  int grid;
+  size_t starts, prefix_o, prefix_lse, own_o, own_lse, bytes;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) shared_kernel(const SharedArgs a) {
-  __shared__ float qs[kWarps][kMaxHeadDim];
-  float* mine = qs[threadIdx.x >> 5];
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = a.batch * a.heads;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < rows;
-       r += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t b = r / a.heads, h = r % a.heads;
-    const int64_t kh = h / (a.heads / a.kv_heads);
-    const int64_t n = clamped(a.lens[b], a.max_pages * a.page_size);
-    const T* q = static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh;
-    __syncwarp();
-    for (int d = lane; d < a.dim; d += 32) mine[d] = to_f(q[d]);
-    __syncwarp();
-    const int32_t* table = a.tables + b * a.ld_tables;
-    const Paged<T> ks{static_cast<const T*>(a.k) + kh * a.k_sh, a.k_sn, a.k_st, a.prefix_pages,
-                      a.prefix_len, table, a.num_pages, a.page_size};
-    const Paged<T> vs{static_cast<const T*>(a.v) + kh * a.v_sh, a.v_sn, a.v_st, a.prefix_pages,
-                      a.prefix_len, table, a.num_pages, a.page_size};
-    attend_row<T>(mine, a.dim, ks, vs, n, a.c, static_cast<T*>(a.out) + b * a.o_sb + h * a.o_sh,
-                  a.lse ? a.lse + b * a.l_sb + h * a.l_sh : nullptr);
-  }
-}
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-unsigned grid_for(int64_t rows) {
-  const int64_t want = (rows + kWarps - 1) / kWarps;
-  return static_cast<unsigned>(want < 4096 ? want : 4096);
+PagedPlan plan_paged(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                     int64_t prefix_len, int64_t max_pages, int32_t page_size) {
+  PagedPlan p{};
+  const int32_t group = heads / kv_heads;
+  const size_t dp = head_dim > 64 ? 128 : 64;
+  p.tile_tokens = kTile / group;
+  // One row tile holds the batch: its stream would be alone with the prefix,
+  // so two streams take alternate key tiles instead.
+  p.prefix_split = batch <= p.tile_tokens;
+  const int64_t block = (p.prefix_split ? 1 : 2) * static_cast<int64_t>(p.tile_tokens);
+  p.prefix_tiles = static_cast<int32_t>((prefix_len + kTile - 1) / kTile);
+  p.prefix_blocks = static_cast<int32_t>((batch + block - 1) / block);
+  const int64_t groups = static_cast<int64_t>(kv_heads) * p.prefix_blocks;
+  const int64_t own_tiles = (max_pages * page_size - prefix_len + kTile - 1) / kTile;
+  const int64_t most = groups * p.prefix_tiles + batch * kv_heads * own_tiles;
+  const int64_t sms = sm_count();
+  p.grid = static_cast<int>(most < 1 ? 1 : (most < sms ? most : sms));
+  const size_t pslots = p.prefix_tiles > 0 ? groups + p.grid : 0;
+  const size_t oslots = own_tiles > 0 ? batch * kv_heads + p.grid : 0;
+  size_t at = 0;
+  const auto take = [&](size_t n) {
+    const size_t was = at;
+    at += up256(n);
+    return was;
+  };
+  p.starts = take((batch + 1) * 8);
+  p.prefix_o = take(pslots * 256 * dp * 4);
+  p.prefix_lse = take(pslots * 256 * 4);
+  p.own_o = take(oslots * 2 * group * dp * 4);
+  p.own_lse = take(oslots * 2 * group * 4);
+  p.bytes = at;
+  return p;
 }
 
 // Sizes and scale that both operators share.
@@ -218,6 +181,15 @@ dsa_status check_common(int32_t dtype, int64_t tokens, int32_t heads, int32_t kv
       heads / kv_heads > kMaxGroup || tokens > INT32_MAX)
     return DSA_EUNSUPPORTED;
   return DSA_OK;
+}
+
+dsa_status check_pages(int64_t num_pages, int32_t page_size, int64_t max_pages,
+                       int64_t prefix_len) {
+  if (num_pages < 0 || page_size < 1 || max_pages < 0 || prefix_len < 0) return DSA_EINVAL;
+  if (num_pages > INT32_MAX || max_pages > INT32_MAX || page_size < 16 ||
+      (page_size & (page_size - 1)) != 0 || max_pages * page_size > INT32_MAX)
+    return DSA_EUNSUPPORTED;
+  return prefix_len % page_size != 0 || prefix_len > max_pages * page_size ? DSA_EINVAL : DSA_OK;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -244,25 +216,60 @@ extern "C" dsa_status dsa_prompt_attention(
       !dsa::by8(q_st, q_sh) || !dsa::by8(k_st, k_sh) || !dsa::by8(v_st, v_sh) ||
       !dsa::by8(o_st, o_sh))
     return DSA_EUNSUPPORTED;
-  const dsa::PromptArgs a{q,    k,    v,    total_q, total_k, heads, kv_heads, head_dim,
-                          q_st, q_sh, k_st, k_sh,    v_st,    v_sh,  cu_q,     cu_k,
-                          seqs, causal, scale * dsa::kLog2e, out, o_st, o_sh, lse, l_st, l_sh};
-  const unsigned grid = dsa::grid_for(total_q * heads);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == DSA_DTYPE_BF16)
-    dsa::prompt_kernel<__nv_bfloat16><<<grid, dsa::kWarps * 32, 0, s>>>(a);
-  else
-    dsa::prompt_kernel<__half><<<grid, dsa::kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
+  dsa::AttendArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_st = q_st;
+  a.q_sh = q_sh;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.dim = head_dim;
+  a.tile_tokens = dsa::kTile / a.group;
+  a.c = scale * dsa::kLog2e;
+  a.tokens = total_q;
+  a.total_k = total_k;
+  a.k_st = k_st;
+  a.k_sh = k_sh;
+  a.v_st = v_st;
+  a.v_sh = v_sh;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.seqs = seqs;
+  a.causal = causal != 0;
+  a.out = out;
+  a.o_st = o_st;
+  a.o_sh = o_sh;
+  a.lse = lse;
+  a.l_st = l_st;
+  a.l_sh = l_sh;
+  dsa::Maps m;
+  if (!dsa::encode<3>(&m.q, dtype, q, {head_dim, heads, total_q}, {q_sh, q_st},
+                      {64, a.group, a.tile_tokens}))
+    return DSA_EUNSUPPORTED;
+  m.k = m.v = m.q;  // without keys nothing is loaded through these
+  if (total_k > 0 &&
+      (!dsa::encode<3>(&m.k, dtype, k, {head_dim, kv_heads, total_k}, {k_sh, k_st},
+                       {64, 1, dsa::kTile}) ||
+       !dsa::encode<3>(&m.v, dtype, v, {head_dim, kv_heads, total_k}, {v_sh, v_st},
+                       {64, 1, dsa::kTile})))
+    return DSA_EUNSUPPORTED;
+  // No more blocks than this, whatever the offsets hold.
+  const int64_t blocks = (total_q / (2 * a.tile_tokens) + seqs) * kv_heads;
+  const int64_t sms = dsa::sm_count();
+  return dsa::launch<false>(m, a, dtype, static_cast<int>(blocks < sms ? blocks : sms),
+                            static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t dsa_shared_prefix_workspace_bytes(int64_t batch, int32_t heads,
                                                     int32_t kv_heads, int32_t head_dim,
                                                     int64_t prefix_len, int64_t max_pages,
                                                     int32_t page_size) {
-  (void)batch, (void)heads, (void)kv_heads, (void)head_dim;
-  (void)prefix_len, (void)max_pages, (void)page_size;
-  return 0;
+  if (dsa::check_common(DSA_DTYPE_BF16, batch, heads, kv_heads, head_dim, 1.f) != DSA_OK ||
+      dsa::check_pages(0, page_size, max_pages, prefix_len) != DSA_OK || batch == 0 || heads == 0)
+    return 0;
+  return dsa::plan_paged(batch, heads, kv_heads, head_dim, prefix_len, max_pages, page_size).bytes;
 }
 
 extern "C" dsa_status dsa_shared_prefix_attention(
@@ -273,15 +280,11 @@ extern "C" dsa_status dsa_shared_prefix_attention(
     const int32_t* tables, int64_t max_pages, int64_t ld_tables, const int32_t* lens, float scale,
     void* out, int64_t o_sb, int64_t o_sh, float* lse, int64_t l_sb, int64_t l_sh,
     void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace, (void)workspace_bytes;
-  if (num_pages < 0 || page_size < 1 || max_pages < 0 || ld_tables < max_pages || prefix_len < 0)
-    return DSA_EINVAL;
-  const dsa_status st = dsa::check_common(dtype, batch, heads, kv_heads, head_dim, scale);
+  if (ld_tables < max_pages) return DSA_EINVAL;
+  dsa_status st = dsa::check_common(dtype, batch, heads, kv_heads, head_dim, scale);
   if (st != DSA_OK) return st;
-  if (num_pages > INT32_MAX || max_pages > INT32_MAX || page_size < 16 ||
-      (page_size & (page_size - 1)) != 0 || max_pages * page_size > INT32_MAX)
-    return DSA_EUNSUPPORTED;
-  if (prefix_len % page_size != 0 || prefix_len > max_pages * page_size) return DSA_EINVAL;
+  st = dsa::check_pages(num_pages, page_size, max_pages, prefix_len);
+  if (st != DSA_OK) return st;
   if (batch == 0 || heads == 0) return DSA_OK;
   if (!q || !out || !lens || (max_pages > 0 && !tables) || (prefix_len > 0 && !prefix_pages) ||
       (num_pages > 0 && (!k_pages || !v_pages)))
@@ -290,16 +293,74 @@ extern "C" dsa_status dsa_shared_prefix_attention(
       !dsa::aligned16(out) || !dsa::by8(q_sb, q_sh) || !dsa::by8(k_sn, k_st, k_sh) ||
       !dsa::by8(v_sn, v_st, v_sh) || !dsa::by8(o_sb, o_sh))
     return DSA_EUNSUPPORTED;
-  const dsa::SharedArgs a{q,         k_pages, v_pages, batch, heads,  kv_heads, head_dim,
-                          num_pages, page_size, q_sb,  q_sh,  k_sn,   k_st,     k_sh,
-                          v_sn,      v_st,    v_sh,    prefix_pages, prefix_len, tables,
-                          max_pages, ld_tables, lens,  scale * dsa::kLog2e, out, o_sb, o_sh,
-                          lse,       l_sb,    l_sh};
-  const unsigned grid = dsa::grid_for(batch * heads);
+  const dsa::PagedPlan p =
+      dsa::plan_paged(batch, heads, kv_heads, head_dim, prefix_len, max_pages, page_size);
+  if (!workspace || workspace_bytes < p.bytes ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return DSA_EINVAL;
+  char* ws = static_cast<char*>(workspace);
+  dsa::AttendArgs a{};
+  a.q = q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.q_st = q_sb;
+  a.q_sh = q_sh;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.dim = head_dim;
+  a.tile_tokens = p.tile_tokens;
+  a.c = scale * dsa::kLog2e;
+  a.tokens = batch;
+  a.k_st = k_st;
+  a.k_sh = k_sh;
+  a.v_st = v_st;
+  a.v_sh = v_sh;
+  a.k_sn = k_sn;
+  a.v_sn = v_sn;
+  a.num_pages = num_pages;
+  a.max_pages = num_pages > 0 ? max_pages : 0;  // without pages nothing is seen
+  a.ld_tables = ld_tables;
+  a.page_size = page_size;
+  while ((1 << a.page_log2) < page_size) ++a.page_log2;
+  a.prefix_pages = prefix_pages;
+  a.tables = tables;
+  a.lens = lens;
+  a.prefix_len = prefix_len;
+  a.prefix_tiles = num_pages > 0 ? p.prefix_tiles : 0;
+  a.prefix_blocks = p.prefix_blocks;
+  a.prefix_split = p.prefix_split;
+  a.starts = reinterpret_cast<int64_t*>(ws + p.starts);
+  a.prefix_o = reinterpret_cast<float*>(ws + p.prefix_o);
+  a.prefix_lse = reinterpret_cast<float*>(ws + p.prefix_lse);
+  a.own_o = reinterpret_cast<float*>(ws + p.own_o);
+  a.own_lse = reinterpret_cast<float*>(ws + p.own_lse);
+  dsa::Maps m;
+  if (!dsa::encode<3>(&m.q, dtype, q, {head_dim, heads, batch}, {q_sh, q_sb},
+                      {64, a.group, a.tile_tokens}))
+    return DSA_EUNSUPPORTED;
+  m.k = m.v = m.q;
+  const int rows = page_size < dsa::kTile ? page_size : dsa::kTile;
+  if (num_pages > 0 &&
+      (!dsa::encode<4>(&m.k, dtype, k_pages, {head_dim, kv_heads, page_size, num_pages},
+                       {k_sh, k_st, k_sn}, {64, 1, rows, 1}) ||
+       !dsa::encode<4>(&m.v, dtype, v_pages, {head_dim, kv_heads, page_size, num_pages},
+                       {v_sh, v_st, v_sn}, {64, 1, rows, 1})))
+    return DSA_EUNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == DSA_DTYPE_BF16)
-    dsa::shared_kernel<__nv_bfloat16><<<grid, dsa::kWarps * 32, 0, s>>>(a);
-  else
-    dsa::shared_kernel<__half><<<grid, dsa::kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
+  st = dsa::launch<true>(m, a, dtype, p.grid, s);
+  if (st != DSA_OK) return st;
+  const dsa::JoinArgs j{out, o_sb, o_sh, lse, l_sb, l_sh, p.grid};
+  return dtype == DSA_DTYPE_BF16 ? dsa::launch_join<__nv_bfloat16>(a, j, s)
+                                 : dsa::launch_join<__half>(a, j, s);
+}
+
+extern "C" int dsa_attention_error(int clear) {
+  unsigned int code = 0;
+  if (cudaMemcpyFromSymbol(&code, dsa::g_pipe_error, sizeof(code)) != cudaSuccess) return -1;
+  if (clear && code != 0) {
+    const unsigned int zero = 0;
+    if (cudaMemcpyToSymbol(dsa::g_pipe_error, &zero, sizeof(zero)) != cudaSuccess) return -1;
+  }
+  return static_cast<int>(code);
 }

@@ -15,9 +15,10 @@
 
 namespace dsa {
 
-// Set (to the failing wait's site code) by a wait that timed out; read and
-// cleared by the host through dsa_pipeline_error(). One copy per translation
-// unit that includes this header (select_pipe.cu alone does).
+// Set (to the failing wait's site code) by a wait that timed out. One copy per
+// translation unit that includes this header: the host reads and clears that
+// of select_pipe.cu through dsa_pipeline_error() and that of attention.cu
+// through dsa_attention_error().
 static __device__ unsigned int g_pipe_error = 0u;
 
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s

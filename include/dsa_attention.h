@@ -11,8 +11,9 @@
  *   l   = sum_j 2^(x_j - m);
  *   out = (sum_j 2^(x_j - m) v_j) / l;  lse = m + log2(l)   (base 2).
  * A row that sees no key has out = 0 and lse = -inf. Keys that a row does not
- * see have no influence on it, whatever they hold (infinities and NaN
- * included); a NaN in a key that it sees makes the row NaN.
+ * see have no influence on it, whatever they hold (rows beside infinities or
+ * NaN that they do not see are summed in another order, within the same
+ * rounding); a NaN in a key that it sees makes the row NaN.
  *
  * (out, lse) is a partial output as dsa_merge_attn_out and
  * dsa_correct_attn_out of dsa_dcp_attn.h take it: runs over disjoint sets of
@@ -134,6 +135,15 @@ dsa_status dsa_shared_prefix_attention(
     const int32_t *lens, float scale, void *out, int64_t o_sb, int64_t o_sh,
     float *lse, int64_t l_sb, int64_t l_sh, void *workspace,
     size_t workspace_bytes, void *stream);
+
+/*
+ * dsa_attention_error -- whether a wait inside an attention kernel has given
+ * up (after ten seconds) since the process started or the last clear; such a
+ * call's outputs are not valid. Returns the wait's nonzero site code, 0 for
+ * none, or -1 if the flag could not be read. clear != 0 resets it after
+ * reading. Synchronises with the current device.
+ */
+int dsa_attention_error(int clear);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,9 @@ def env():
     import deepseek_sparse_attention_row_gb300 as dsa
 
     assert torch.cuda.is_available(), "these tests need a CUDA device"
-    return torch, dsa
+    yield torch, dsa
+    torch.cuda.synchronize()
+    assert dsa.attention_error() == 0, "a kernel's wait gave up"
 
 
 def ints(torch, values):
@@ -173,10 +175,16 @@ def test_prompt_masked_places_hold_anything(env, what, dtype):
     k[260 + 288, 1] = x
     out, _ = check_prompt(env, q, k, v, ql, kl, True)
     base, _ = check_prompt(env, *clean, ql, kl, True)
+    _, _, tol, _ = ref.prompt(*clean, offsets(ql), offsets(kl), True)
     seen = torch.zeros(400, dtype=torch.bool, device="cuda")
     seen[199] = True
     seen[200 + 194:] = True
-    assert torch.equal(out[~seen], base[~seen])
+    # The other rows' definition is the same in both runs and each run is
+    # within tol of it (checked above), so they differ by 2 tol at most: equal
+    # bits are not promised, rows next to such values are summed in another
+    # order.
+    off = (out[~seen].double() - base[~seen].double()).abs().cpu()
+    assert (off <= 2 * tol[~seen.cpu()]).all()
 
 
 def test_prompt_merges_over_key_shards(env):
