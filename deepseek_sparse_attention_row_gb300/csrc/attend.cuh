@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   } else {
     reg_shrink<72>();
     if (warp == 8) {
-      if ((threadIdx.x & 31) == 0) multiply<T, DP>(cta, tmem);
+      if (elect_one()) multiply<T, DP>(cta, tmem);
     } else if (warp == 9) {
       load<DP, PAGED>(a, &qm, &km, &vm, cta);
     } else if (warp == 10) {

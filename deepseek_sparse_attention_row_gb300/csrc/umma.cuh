@@ -12,6 +12,17 @@
 
 namespace dsa {
 
+// True in one lane of a converged warp. The compiler then knows that a single
+// thread goes on, and keeps the operands of its tensor-core instructions in
+// uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
 // ---- tensor memory -------------------------------------------------------
 
 // All 512 columns of the SM's tensor memory; one warp, converged.
