@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
 constexpr int kAttendThreads = 384;  // no calls in the kernel: ptxas could not split registers
+constexpr int kParts = 2;            // parts of a weight tile handed to the products one by one
 constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's base
 // A row's recomputation (fix_row) may hold up its CTA's other roles for
 // seconds when a huge context holds infinities in masked places.
@@ -125,7 +126,7 @@ constexpr int kMaxStages = 10;
 struct Ctrl {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t s_full[2], p_full[2][kParts], o_done[2], o_free[2];
   uint64_t seg_full[2], seg_empty[2];
   Seg seg[2];
   uint32_t tmem;
@@ -164,23 +165,26 @@ __device__ __forceinline__ int32_t tiles_of(int32_t n) { return n <= 0 ? 0 : (n 
 
 // Prompts: blocks of 2 * tile_tokens tokens for every key/value head, those
 // of the same tokens next to each other, a sequence's last (causal: longest)
-// ones first; CTA x takes blocks x, x + grid, ...
+// ones first. They are dealt in rounds of one block per CTA, every other
+// round in reverse, so that the CTAs' sums of falling costs come out alike.
 struct PromptSchedule {
-  int64_t id;
+  int64_t round = 0;
   int32_t chunk = 0;     // first of the 32 sequences that the lanes hold
   int64_t before = 0;    // blocks before them
   bool loaded = false;
   int32_t q0, q1, k0, k1;
   int64_t upto;          // blocks up to the lane's sequence, it included
 
-  __device__ explicit PromptSchedule(const AttendArgs&) : id(blockIdx.x) {}
+  __device__ explicit PromptSchedule(const AttendArgs&) {}
 
   __device__ bool next(const AttendArgs& a, Seg& g) {
     const int lane = threadIdx.x & 31;
     const int32_t block = 2 * a.tile_tokens;
+    const int64_t id =
+        round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    ++round;
     const int64_t at = id / a.kv_heads;
     g.kh = static_cast<int32_t>(id % a.kv_heads);
-    id += gridDim.x;
     for (; chunk < a.seqs; chunk += 32, loaded = false) {
       if (!loaded) {
         const int32_t i = chunk + lane;
@@ -611,18 +615,24 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
   };
   // P V of stream s with the V tile in the ring's current stage
   const auto values = [&](int s, bool first) -> bool {
-    if (!wait(&c->p_full[s], done[s] & 1, c, 21)) return false;
     if (first) {
       if (outs[s] > 0 && !wait(&c->o_free[s], (outs[s] - 1) & 1, c, 22)) return false;
       ++outs[s];
     }
-    ++done[s];
-    tc_fence_after();
     const uint64_t vb = operand(st0 + ring.stage * L::kBytes, L::kHalf, 1024);
 #pragma unroll
-    for (int i = 0; i < kTile / 16; ++i)
-      mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + i * 8, vb + ((i * 2048) >> 4),
-             kShapeO, !first || i > 0);
+    for (int p = 0; p < kParts; ++p) {
+      if (!wait(&c->p_full[s][p], done[s] & 1, c, 21)) return false;
+      tc_fence_after();
+      constexpr int kSteps = kTile / 16 / kParts;
+#pragma unroll
+      for (int e = 0; e < kSteps; ++e) {
+        const int i = p * kSteps + e;
+        mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + i * 8, vb + ((i * 2048) >> 4),
+               kShapeO, !first || i > 0);
+      }
+    }
+    ++done[s];
     mma_commit(&c->o_done[s]);
     return true;
   };
@@ -799,12 +809,14 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
           p[j] = pack2(y.x, y.y, T());
         }
         tmem_store16(ts + 16 * b, p);
+        if ((b + 1) % (4 / kParts) == 0) {
+          tmem_wait_store();
+          tc_fence_before();
+          mbar_arrive(&c->p_full[s][b / (4 / kParts)]);
+        }
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
-      tmem_wait_store();
-      tc_fence_before();
-      mbar_arrive(&c->p_full[s]);
     }
 
     // The output. l is 0 only where no key was seen.
@@ -919,7 +931,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     mbar_init(&c->q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c->s_full[s], 1);
-      mbar_init(&c->p_full[s], kTile);
+      for (int p = 0; p < kParts; ++p) mbar_init(&c->p_full[s][p], kTile);
       mbar_init(&c->o_done[s], 1);
       mbar_init(&c->o_free[s], kTile);
       mbar_init(&c->seg_full[s], 1);
