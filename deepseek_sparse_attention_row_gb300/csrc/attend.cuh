@@ -75,6 +75,7 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_flo
 struct Seg {
   int32_t n[2];     // key tiles of each stream; n[0] < 0: the list's end
   int32_t split;    // streams: 0 two row tiles, 1 alternate key tiles
+  int32_t first;    // split: the stream of the first key tile
   int32_t t0;       // first key tile
   int32_t kh;       // key/value head
   int32_t tok[2];   // first token of each row tile
@@ -125,7 +126,7 @@ struct Layout {
 constexpr int kMaxStages = 10;
 struct Ctrl {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2][kParts], o_done[2], o_free[2];
   uint64_t seg_full[2], seg_empty[2];
   Seg seg[2];
@@ -216,7 +217,7 @@ struct PromptSchedule {
         g.ntok[0] = min(a.tile_tokens, s1 - g.tok[0]);
         g.tok[1] = g.tok[0] + g.ntok[0];
         g.ntok[1] = min(a.tile_tokens, s1 - g.tok[1]);
-        g.split = 0;
+        g.split = g.first = 0;
         g.t0 = 0;
         g.seq = 0;
         g.slot = 0;
@@ -252,6 +253,7 @@ __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
 // the line: no two segments share one.
 struct PagedSchedule {
   int64_t pos, end, prefix_units, own_units;
+  int32_t turn = 0;     // split segments so far: they begin on the streams in turn
   int32_t chunk = 0;
   int64_t before = 0;   // own units before the chunk
   bool loaded = false;
@@ -287,6 +289,12 @@ struct PagedSchedule {
     end = min(pos + share, all);
   }
 
+  __device__ void split(Seg& g, int32_t n) {
+    g.first = turn++ & 1;
+    g.n[g.first] = (n + 1) / 2;
+    g.n[1 - g.first] = n / 2;
+  }
+
   __device__ bool next(const AttendArgs& a, Seg& g) {
     if (pos >= end) return false;
     g.k0 = g.q_end = g.kv_len = 0;
@@ -307,8 +315,13 @@ struct PagedSchedule {
       g.ntok[0] = min(a.tile_tokens, rows - g.tok[0]);
       g.tok[1] = g.tok[0] + g.ntok[0];
       g.ntok[1] = g.split ? 0 : min(a.tile_tokens, rows - g.tok[1]);
-      g.n[0] = g.split ? (n + 1) / 2 : n;
-      g.n[1] = g.split ? n / 2 : (g.ntok[1] > 0 ? n : 0);
+      if (g.split) {
+        split(g, n);
+      } else {
+        g.first = 0;
+        g.n[0] = n;
+        g.n[1] = g.ntok[1] > 0 ? n : 0;
+      }
       return true;
     }
     const int lane = threadIdx.x & 31;
@@ -339,8 +352,7 @@ struct PagedSchedule {
     pos += n;
     g.seq = chunk + src;
     g.split = 1;
-    g.n[0] = (n + 1) / 2;
-    g.n[1] = n / 2;
+    split(g, n);
     g.tok[0] = g.tok[1] = g.seq;
     g.ntok[0] = 1;
     g.ntok[1] = 0;
@@ -399,7 +411,7 @@ template <typename T, bool PAGED>
 __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s, int32_t lim,
                                      int32_t tok, int32_t head, float (&acc)[4], float& lse) {
   const int lane = threadIdx.x & 31;
-  const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s : 0);
+  const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s ^ g.first : 0);
   bool hidden = false;
   for (int32_t i = 0; i < g.n[s]; ++i) {
     const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
@@ -513,13 +525,14 @@ __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
 // The loading warp: per segment the row tiles, then K and V in the order in
 // which the products take them: K leads V by one tile (shared) or two (split).
 template <int DP, bool PAGED>
-__device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorMap* km,
-                     const CUtensorMap* vm, Cta<DP> cta) {
+__device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorMap* qm1,
+                     const CUtensorMap* km, const CUtensorMap* vm, Cta<DP> cta) {
   using L = Layout<DP>;
   Ctrl* c = cta.ctrl();
   const int lane = threadIdx.x & 31;
   Ring<DP> ring;
-  uint32_t active = 0;
+  uint32_t qs[2] = {0, 0};  // uses of the two row-tile buffers
+  uint32_t turn = 0;
   // boxes of a K or V tile, one lane each: page within the tile, half
   const int boxes = PAGED && a.page_size < kTile ? kTile / a.page_size : 1;
   const int pi = lane / L::kHalves, h = lane % L::kHalves;
@@ -530,15 +543,22 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     if (g.n[0] < 0) break;
     const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
     if (n == 0) continue;
-    if (active > 0 && !wait_warp(&c->q_empty, (active - 1) & 1, c, 18)) return;
-    ++active;
-    const int tiles = g.ntok[1] > 0 ? 2 : 1;
-    if (lane == 0)
-      mbar_arrive_expect_tx(&c->q_full, tiles * L::kHalves * a.tile_tokens * a.group * 128);
-    __syncwarp();
-    if (lane < tiles * L::kHalves)
-      tma_load3(cta.q(lane / L::kHalves) + h * L::kHalf, qm, h * 64, g.kh * a.group,
-                g.tok[lane / L::kHalves], &c->q_full);
+    // Split segments take the two row-tile buffers in turn, so that the next
+    // segment's rows load while this one's are in use; shared ones take both.
+    const int q_first = g.split ? turn++ & 1 : 0, q_count = !g.split && g.ntok[1] > 0 ? 2 : 1;
+    for (int i = q_first; i < q_first + q_count; ++i) {
+      if (qs[i] > 0 && !wait_warp(&c->q_empty[i], (qs[i] - 1) & 1, c, 18)) return;
+      ++qs[i];
+      // a segment of one sequence needs that token's rows alone
+      const bool one = PAGED && g.seq >= 0;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&c->q_full[i],
+                              L::kHalves * (one ? 1 : a.tile_tokens) * a.group * 128);
+      __syncwarp();
+      if (lane < L::kHalves)
+        tma_load3(cta.q(i) + lane * L::kHalf, one ? qm1 : qm, lane * 64, g.kh * a.group,
+                  g.tok[g.split ? 0 : i], &c->q_full[i]);
+    }
     const auto page = [&](int32_t t) -> int32_t {
       if constexpr (PAGED) {
         if (lane < boxes * L::kHalves && t < g.t0 + n)
@@ -580,7 +600,8 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     const uint32_t uses = ring.round + (i < ring.stage ? 1 : 0);
     if (uses > 0 && !wait_warp(&c->kv_empty[i], (uses - 1) & 1, c, 19)) return;
   }
-  if (active > 0) wait_warp(&c->q_empty, (active - 1) & 1, c, 18);
+  for (int i = 0; i < 2; ++i)
+    if (qs[i] > 0 && !wait_warp(&c->q_empty[i], (qs[i] - 1) & 1, c, 18)) return;
 }
 
 // The thread that issues the products. In program order: for each key tile
@@ -594,7 +615,8 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
   constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
   const uint32_t q0 = smem_addr(cta.q(0)), st0 = smem_addr(cta.stage(0));
   Ring<DP> ring;
-  uint32_t segs = 0;             // segments with products so far
+  uint32_t qn[2] = {0, 0};       // uses of the two row-tile buffers
+  uint32_t turn = 0;
   uint32_t done[2] = {0, 0};     // tiles of each stream
   uint32_t outs[2] = {0, 0};     // segments of each stream with products
 
@@ -642,36 +664,45 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
     if (!take_seg<false>(c, k, g, 23) || g.n[0] < 0) return;
     const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
     if (n == 0) continue;
-    if (!wait(&c->q_full, segs & 1, c, 24)) return;
-    ++segs;
     if (g.split) {
+      const int b = turn++ & 1;
+      if (!wait(&c->q_full[b], qn[b] & 1, c, 24)) return;
+      ++qn[b];
       for (int32_t j = 0; j < min(n, 2); ++j) {
         if (!full()) return;
         tc_fence_after();
-        scores(j, 0);
+        scores((j & 1) ^ g.first, b);
         drop();
       }
-      if (n <= 2) mma_commit(&c->q_empty);
+      if (n <= 2) mma_commit(&c->q_empty[b]);
       for (int32_t j = 0; j < n; ++j) {
-        const int s = j & 1;
+        const int s = (j & 1) ^ g.first;
         if (!full()) return;
         if (!values(s, j < 2)) return;
         drop();
         if (j + 2 < n) {
           if (!full()) return;
           tc_fence_after();
-          scores(s, 0);
+          scores(s, b);
           drop();
-          if (j + 3 == n) mma_commit(&c->q_empty);
+          if (j + 3 == n) mma_commit(&c->q_empty[b]);
         }
       }
     } else {
+      const int tiles = g.ntok[1] > 0 ? 2 : 1;
+      for (int i = 0; i < tiles; ++i) {
+        if (!wait(&c->q_full[i], qn[i] & 1, c, 24)) return;
+        ++qn[i];
+      }
+      const auto drop_rows = [&]() {
+        for (int i = 0; i < tiles; ++i) mma_commit(&c->q_empty[i]);
+      };
       if (!full()) return;
       tc_fence_after();
       for (int s = 0; s < 2; ++s)
         if (g.n[s] > 0) scores(s, s);
       drop();
-      if (n == 1) mma_commit(&c->q_empty);
+      if (n == 1) drop_rows();
       for (int32_t j = 0; j < n; ++j) {
         // V_j in the current stage, K_{j+1} in the next one
         if (!full()) return;
@@ -696,7 +727,7 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
         ring = kn;
         if (j + 1 < n) {
           drop();
-          if (j + 2 == n) mma_commit(&c->q_empty);
+          if (j + 2 == n) drop_rows();
         }
       }
     }
@@ -732,9 +763,10 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
         lim = a.causal ? g.kv_len - (g.q_end - 1 - tok) : g.kv_len;
       }
     }
+    const bool busy = __any_sync(~0u, valid);  // else the warp only keeps step
     float base = neg_inf(), l = 0.f;  // the row's base, in units of <q, k>
     for (int32_t i = 0; i < n; ++i) {
-      const int32_t t = g.split ? g.t0 + s + 2 * i : g.t0 + i;
+      const int32_t t = g.split ? g.t0 + (s ^ g.first) + 2 * i : g.t0 + i;
       uint32_t bad = 0;  // pages of the tile that are not there
       if constexpr (PAGED) {
         const int pages = a.page_size < kTile ? kTile >> a.page_log2 : 1;
@@ -747,6 +779,10 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       if (!wait_warp(&c->s_full[s], done & 1, c, 26)) return;
       ++done;
       tc_fence_after();
+      if (!busy) {
+        for (int p = 0; p < kParts; ++p) mbar_arrive(&c->p_full[s][p]);
+        continue;
+      }
       float x[kTile];
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -773,7 +809,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (__any_sync(~0u, top > base + grow)) {
+      if (__any_sync(~0u, valid && top > base + grow)) {
         const float was = base;
         base = fmaxf(base, top);
         if (i > 0) {
@@ -828,11 +864,11 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     if (valid) {
       if constexpr (PAGED) {
         if (g.seq < 0) {
-          const int64_t r = g.slot * 256 + s * kTile + row;
+          const int64_t r = g.slot * 256 + (s ^ g.first) * kTile + row;
           part = a.prefix_o + r * DP;
           lse_at = a.prefix_lse + r;
         } else {
-          const int64_t r = (g.slot * 2 + s) * a.group + row;
+          const int64_t r = (g.slot * 2 + (s ^ g.first)) * a.group + row;
           part = a.own_o + r * DP;
           lse_at = a.own_lse + r;
         }
@@ -849,7 +885,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
 #pragma unroll 1
     for (int b = 0; b < DP; b += 32) {
       float o[32];
-      if (n > 0) {
+      if (n > 0 && busy) {
         tmem_load32(to + b, *reinterpret_cast<uint32_t(*)[32]>(o));
         tmem_wait_load();
       }
@@ -882,7 +918,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     }
     if (lse_at) *lse_at = lse;
 
-    const int32_t seen_tiles = n > 0 ? (g.split ? g.t0 + s + 2 * (n - 1) : g.t0 + n - 1) + 1 : 0;
+    const int32_t seen_tiles = n > 0 ? (g.split ? g.t0 + (s ^ g.first) + 2 * (n - 1) : g.t0 + n - 1) + 1 : 0;
     uint32_t todo = __ballot_sync(
         ~0u, valid && odd && lim < static_cast<int64_t>(seen_tiles) * kTile);
     while (todo != 0) {
@@ -914,8 +950,9 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
 
 template <typename T, int DP, bool PAGED>
 __global__ void __launch_bounds__(kAttendThreads, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
-                  const __grid_constant__ CUtensorMap vm, const __grid_constant__ AttendArgs a) {
+    attend_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap q1,
+                  const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                  const __grid_constant__ AttendArgs a) {
   using L = Layout<DP>;
   extern __shared__ unsigned char raw[];
   Cta<DP> cta;
@@ -927,9 +964,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(&c->kv_full[i], 1);
       mbar_init(&c->kv_empty[i], 1);
     }
-    mbar_init(&c->q_full, 1);
-    mbar_init(&c->q_empty, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&c->q_full[s], 1);
+      mbar_init(&c->q_empty[s], 1);
       mbar_init(&c->s_full[s], 1);
       for (int p = 0; p < kParts; ++p) mbar_init(&c->p_full[s][p], kTile);
       mbar_init(&c->o_done[s], 1);
@@ -943,7 +980,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   if (warp == 8) {
     tmem_alloc(&c->tmem);
   } else if (warp == 9 && (threadIdx.x & 31) == 0) {
-    tma_prefetch(&qm);
+    tma_prefetch(PAGED ? &q1 : &qm);
     tma_prefetch(&km);
     tma_prefetch(&vm);
   }
@@ -968,7 +1005,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     if (warp == 8) {
       if (elect_one()) multiply<T, DP>(cta, tmem);
     } else if (warp == 9) {
-      load<DP, PAGED>(a, &qm, &km, &vm, cta);
+      load<DP, PAGED>(a, &qm, &q1, &km, &vm, cta);
     } else if (warp == 10) {
       schedule<DP, PAGED>(a, cta);
     }

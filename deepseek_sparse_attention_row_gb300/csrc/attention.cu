@@ -82,8 +82,9 @@ bool encode(CUtensorMap* map, int32_t dtype, const void* base, const int64_t (&d
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q1: boxes of one token (paged calls only).
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, q1, k, v;
 };
 
 template <typename T, int DP, bool PAGED>
@@ -100,7 +101,7 @@ dsa_status launch(const Maps& m, const AttendArgs& a, int grid, cudaStream_t str
       return DSA_ECUDA;
     ready[dev].store(true, std::memory_order_relaxed);
   }
-  kernel<<<grid, kAttendThreads, kSmem, stream>>>(m.q, m.k, m.v, a);
+  kernel<<<grid, kAttendThreads, kSmem, stream>>>(m.q, m.q1, m.k, m.v, a);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
@@ -248,7 +249,7 @@ extern "C" dsa_status dsa_prompt_attention(
   if (!dsa::encode<3>(&m.q, dtype, q, {head_dim, heads, total_q}, {q_sh, q_st},
                       {64, a.group, a.tile_tokens}))
     return DSA_EUNSUPPORTED;
-  m.k = m.v = m.q;  // without keys nothing is loaded through these
+  m.q1 = m.k = m.v = m.q;  // without keys nothing is loaded through these
   if (total_k > 0 &&
       (!dsa::encode<3>(&m.k, dtype, k, {head_dim, kv_heads, total_k}, {k_sh, k_st},
                        {64, 1, dsa::kTile}) ||
@@ -337,7 +338,8 @@ extern "C" dsa_status dsa_shared_prefix_attention(
   a.own_lse = reinterpret_cast<float*>(ws + p.own_lse);
   dsa::Maps m;
   if (!dsa::encode<3>(&m.q, dtype, q, {head_dim, heads, batch}, {q_sh, q_sb},
-                      {64, a.group, a.tile_tokens}))
+                      {64, a.group, a.tile_tokens}) ||
+      !dsa::encode<3>(&m.q1, dtype, q, {head_dim, heads, batch}, {q_sh, q_sb}, {64, a.group, 1}))
     return DSA_EUNSUPPORTED;
   m.k = m.v = m.q;
   const int rows = page_size < dsa::kTile ? page_size : dsa::kTile;
