@@ -82,8 +82,9 @@ struct Seg {
   int32_t ntok[2];  // its tokens
   // prompt: keys [k0, k0 + kv_len); the token before q_end sees all of them
   int32_t k0, kv_len, q_end;
-  // pages: the sequence whose own tokens these are, or -1 for the prefix
-  int32_t seq;
+  // pages: the sequence whose own tokens these are (kv_len of them), or -1
+  // for the prefix; whether a page of the segment is missing
+  int32_t seq, gaps;
   int64_t slot;     // of the partial outputs
 };
 
@@ -162,6 +163,26 @@ __device__ __forceinline__ int32_t clamp_to(int32_t x, int64_t top) {
 }
 __device__ __forceinline__ int32_t tiles_of(int32_t n) { return n <= 0 ? 0 : (n + kTile - 1) / kTile; }
 
+// ---- keys on pages ----------------------------------------------------------
+
+// The page of the segment's token t (counted from the prefix's start, or from
+// the sequence's first own token), or num_pages when there is none.
+__device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int64_t t) {
+  int64_t p = t >> a.page_log2;
+  const int32_t none = static_cast<int32_t>(a.num_pages);
+  const int64_t pre = a.prefix_len >> a.page_log2;
+  int32_t id;
+  if (seq < 0) {
+    if (p >= pre) return none;
+    id = __ldg(a.prefix_pages + p);
+  } else {
+    p += pre;
+    if (p >= a.max_pages) return none;
+    id = __ldg(a.tables + seq * a.ld_tables + p);
+  }
+  return id < 0 || id > none ? none : id;
+}
+
 // ---- schedules ------------------------------------------------------------
 
 // Prompts: blocks of 2 * tile_tokens tokens for every key/value head, those
@@ -219,7 +240,7 @@ struct PromptSchedule {
         g.ntok[1] = min(a.tile_tokens, s1 - g.tok[1]);
         g.split = g.first = 0;
         g.t0 = 0;
-        g.seq = 0;
+        g.seq = g.gaps = 0;
         g.slot = 0;
         for (int s = 0; s < 2; ++s) {
           // keys that the tile's last token sees
@@ -257,7 +278,7 @@ struct PagedSchedule {
   int32_t chunk = 0;
   int64_t before = 0;   // own units before the chunk
   bool loaded = false;
-  int32_t mine;         // own tiles of the lane's sequence
+  int32_t mine;         // own tokens of the lane's sequence
   int64_t upto;
 
   __device__ static int64_t units(const AttendArgs& a) {
@@ -295,6 +316,20 @@ struct PagedSchedule {
     g.n[1 - g.first] = n / 2;
   }
 
+  // Whether a page of the segment's tiles is missing: looked up here, ahead
+  // of the streams, which then need no table.
+  __device__ static void find_gaps(const AttendArgs& a, Seg& g) {
+    const int64_t k0 = static_cast<int64_t>(g.t0) * kTile;
+    int64_t k1 = k0 + static_cast<int64_t>(max(g.split ? g.n[0] + g.n[1] : g.n[0], g.n[1])) * kTile;
+    k1 = min(k1, g.seq < 0 ? a.prefix_len : static_cast<int64_t>(g.kv_len));
+    const int64_t p1 = (k1 + a.page_size - 1) >> a.page_log2;
+    bool none = false;
+#pragma unroll 4
+    for (int64_t p = (k0 >> a.page_log2) + (threadIdx.x & 31); p < p1; p += 32)
+      none |= page_of(a, g.seq, p << a.page_log2) >= a.num_pages;
+    g.gaps = __any_sync(~0u, none);
+  }
+
   __device__ bool next(const AttendArgs& a, Seg& g) {
     if (pos >= end) return false;
     g.k0 = g.q_end = g.kv_len = 0;
@@ -322,6 +357,7 @@ struct PagedSchedule {
         g.n[0] = n;
         g.n[1] = g.ntok[1] > 0 ? n : 0;
       }
+      find_gaps(a, g);
       return true;
     }
     const int lane = threadIdx.x & 31;
@@ -330,8 +366,8 @@ struct PagedSchedule {
       if (chunk >= a.tokens) return false;  // the lengths changed under the call
       if (!loaded) {
         const int64_t b = static_cast<int64_t>(chunk) + lane;
-        mine = b < a.tokens ? tiles_of(own_tokens(a, b)) : 0;
-        upto = static_cast<int64_t>(mine) * a.kv_heads;
+        mine = b < a.tokens ? own_tokens(a, b) : 0;
+        upto = static_cast<int64_t>(tiles_of(mine)) * a.kv_heads;
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t y = __shfl_up_sync(~0u, upto, o);
           if (lane >= o) upto += y;
@@ -343,7 +379,8 @@ struct PagedSchedule {
       before += all;
     }
     const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
-    const int32_t tiles = __shfl_sync(~0u, mine, src);
+    g.kv_len = __shfl_sync(~0u, mine, src);
+    const int32_t tiles = tiles_of(g.kv_len);
     const int64_t rel = at - before - (__shfl_sync(~0u, upto, src) -
                                        static_cast<int64_t>(tiles) * a.kv_heads);
     g.kh = static_cast<int32_t>(rel / tiles);
@@ -357,6 +394,7 @@ struct PagedSchedule {
     g.ntok[0] = 1;
     g.ntok[1] = 0;
     g.slot = static_cast<int64_t>(g.seq) * a.kv_heads + g.kh + blockIdx.x;
+    find_gaps(a, g);
     return true;
   }
 };
@@ -365,26 +403,6 @@ template <bool PAGED>
 struct ScheduleOf { using type = PromptSchedule; };
 template <>
 struct ScheduleOf<true> { using type = PagedSchedule; };
-
-// ---- keys on pages ----------------------------------------------------------
-
-// The page of the segment's token t (counted from the prefix's start, or from
-// the sequence's first own token), or num_pages when there is none.
-__device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int64_t t) {
-  int64_t p = t >> a.page_log2;
-  const int32_t none = static_cast<int32_t>(a.num_pages);
-  const int64_t pre = a.prefix_len >> a.page_log2;
-  int32_t id;
-  if (seq < 0) {
-    if (p >= pre) return none;
-    id = __ldg(a.prefix_pages + p);
-  } else {
-    p += pre;
-    if (p >= a.max_pages) return none;
-    id = __ldg(a.tables + seq * a.ld_tables + p);
-  }
-  return id < 0 || id > none ? none : id;
-}
 
 // Address of key (or value) j of a segment; nullptr where none is.
 template <typename T, bool PAGED>
@@ -758,7 +776,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     if (valid) {
       if constexpr (PAGED) {
         lim = g.seq < 0 ? min(seen_tokens(a, tok), static_cast<int32_t>(a.prefix_len))
-                        : own_tokens(a, tok);
+                        : g.kv_len;
       } else {
         lim = a.causal ? g.kv_len - (g.q_end - 1 - tok) : g.kv_len;
       }
@@ -768,7 +786,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     for (int32_t i = 0; i < n; ++i) {
       const int32_t t = g.split ? g.t0 + (s ^ g.first) + 2 * i : g.t0 + i;
       uint32_t bad = 0;  // pages of the tile that are not there
-      if constexpr (PAGED) {
+      if (PAGED && g.gaps) {
         const int pages = a.page_size < kTile ? kTile >> a.page_log2 : 1;
         bool none = false;
         if (lane < pages)
@@ -1074,28 +1092,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (i < np) return p0 + (a.prefix_split ? static_cast<int64_t>(i) * kTile : i * 256ll);
     return o0 + static_cast<int64_t>(i - np) * a.group;
   };
+  const int32_t all = np + no;
   const auto lse_of = [&](int32_t i) {
-    return i < np ? a.prefix_lse[at(i)] : a.own_lse[at(i)];
+    return i >= all ? neg_inf() : i < np ? a.prefix_lse[at(i)] : a.own_lse[at(i)];
   };
-  float m = neg_inf();
-  for (int32_t i = lane; i < np + no; i += 32) m = fmaxf(m, lse_of(i));
+  // Lane i keeps the log-sum-exp of partial i; more than 32 are read again.
+  const float held = lse_of(lane);
+  float m = held;
+  for (int32_t i = lane + 32; i < all; i += 32) m = fmaxf(m, lse_of(i));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
   const float base = m == neg_inf() ? 0.f : m;
-  float sum = 0.f;
-  for (int32_t i = lane; i < np + no; i += 32) sum += ex2(lse_of(i) - base);
+  float sum = ex2(held - base);
+  for (int32_t i = lane + 32; i < all; i += 32) sum += ex2(lse_of(i) - base);
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const bool any = sum != 0.f;  // NaN counts
   const float lse = any ? base + log2f(sum) : neg_inf();
   constexpr int kPer = DP / 32;  // values of a lane
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   float acc[kPer];
   for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
-#pragma unroll 4
-  for (int32_t i = 0; i < np + no; ++i) {
-    const float x = lse_of(i);
-    if (x == neg_inf()) continue;  // nothing seen: its output was not written
-    const float w = ex2(x - lse);
-    const float* o = (i < np ? a.prefix_o : a.own_o) + at(i) * DP + lane * kPer;
-    for (int d = 0; d < kPer; ++d) acc[d] = fmaf(w, o[d], acc[d]);
+  // Every partial holds an output (zeros where it saw nothing), so that the
+  // loads wait for no log-sum-exp.
+  for (int32_t i0 = 0; i0 < all; i0 += 32) {
+    const float w = any ? ex2((i0 == 0 ? held : lse_of(i0 + lane)) - lse) : 0.f;
+    const int32_t n = min(all - i0, 32);
+#pragma unroll 8
+    for (int32_t i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(~0u, w, i);
+      const float* o = (i0 + i < np ? a.prefix_o : a.own_o) + at(i0 + i) * DP + lane * kPer;
+      const Vec v = *reinterpret_cast<const Vec*>(o);
+      acc[0] = fmaf(wi, v.x, acc[0]);
+      acc[1] = fmaf(wi, v.y, acc[1]);
+      if constexpr (kPer == 4) {
+        acc[2] = fmaf(wi, v.z, acc[2]);
+        acc[3] = fmaf(wi, v.w, acc[3]);
+      }
+    }
   }
   if (lane * kPer < a.dim) {
     T* out = static_cast<T*>(j.out) + b * j.o_sb + h * j.o_sh + lane * kPer;
