@@ -27,8 +27,13 @@
 // tiles) that the scheduling warp writes to a two-entry ring, so that loads
 // of the next segment run under the current one's end.
 //
-// Every wait is bounded (kAttendLimitNs); one that gives up records its site
-// in g_pipe_error, and all roles leave.
+// Every wait is bounded (kWaitTurns); one that gives up records its site in
+// g_pipe_error, and all roles leave.
+//
+// Code size matters: the roles of an SM run different code at the same time,
+// and a call with short segments runs each piece only a few times. Loops that
+// need no registers as arrays are therefore not unrolled, and each wait and
+// product sequence stands in as few places as possible.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -45,9 +50,12 @@ constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
 constexpr int kAttendThreads = 384;  // no calls in the kernel: ptxas could not split registers
 constexpr int kParts = 2;            // parts of a weight tile handed to the products one by one
 constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's base
-// A row's recomputation (fix_row) may hold up its CTA's other roles for
-// seconds when a huge context holds infinities in masked places.
-constexpr unsigned long long kAttendLimitNs = 10000000000ull;
+constexpr int kSegs = 8;             // segments that the scheduling warp may be ahead
+// A wait gives up between its second and third turn of the global timer's high
+// word, after 8.6 to 12.9 seconds: a row's recomputation (fix_row) may hold up
+// its CTA's other roles for seconds when a huge context holds infinities in
+// masked places.
+constexpr uint32_t kWaitTurns = 3;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -85,7 +93,7 @@ struct Seg {
   // pages: the sequence whose own tokens these are (kv_len of them), or -1
   // for the prefix; whether a page of the segment is missing
   int32_t seq, gaps;
-  int64_t slot;     // of the partial outputs
+  int32_t slot;     // of the partial outputs
 };
 
 struct AttendArgs {
@@ -109,7 +117,7 @@ struct AttendArgs {
   const int32_t *prefix_pages, *tables, *lens;
   int64_t prefix_len;
   int32_t prefix_tiles, prefix_blocks, prefix_split;
-  int64_t* starts;                 // [tokens + 1]: own units before each sequence
+  int32_t* starts;                 // [tokens + 1]: own units before each sequence
   float *prefix_o, *prefix_lse;    // [slot][256][DP], [slot][256]
   float *own_o, *own_lse;          // [slot][2 G][DP], [slot][2 G]
 };
@@ -129,27 +137,31 @@ struct Ctrl {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2][kParts], o_done[2], o_free[2];
-  uint64_t seg_full[2], seg_empty[2];
-  Seg seg[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Seg seg[kSegs];
   uint32_t tmem;
   int dead;
 };
 constexpr size_t attend_smem(uint32_t ctrl) { return 1024 + ctrl + sizeof(Ctrl); }
 
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctrl* c, unsigned site) {
-  const unsigned long long t0 = global_ns();
+__device__ __forceinline__ uint32_t global_turns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctrl* c, unsigned site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = global_turns();
+#pragma unroll 1
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&c->dead)) return false;
-    if (global_ns() - t0 > kAttendLimitNs) {
+    if (global_turns() - t0 >= kWaitTurns) {
       atomicCAS(&g_pipe_error, 0u, site);
       *reinterpret_cast<volatile int*>(&c->dead) = 1;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctrl* c, unsigned site) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, c, site);
 }
 
 // The same for a whole warp: all lanes go on, or none.
@@ -160,6 +172,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* 
 
 __device__ __forceinline__ int32_t clamp_to(int32_t x, int64_t top) {
   return x < 0 ? 0 : (x > top ? static_cast<int32_t>(top) : x);
+}
+// Sum of x over the lanes up to this one.
+__device__ __forceinline__ uint32_t warp_sum_upto(uint32_t x) {
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(~0u, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
 }
 __device__ __forceinline__ int32_t tiles_of(int32_t n) { return n <= 0 ? 0 : (n + kTile - 1) / kTile; }
 
@@ -190,58 +211,50 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int
 // ones first. They are dealt in rounds of one block per CTA, every other
 // round in reverse, so that the CTAs' sums of falling costs come out alike.
 struct PromptSchedule {
-  int64_t round = 0;
+  uint32_t round = 0;
   int32_t chunk = 0;     // first of the 32 sequences that the lanes hold
-  int64_t before = 0;    // blocks before them
+  uint32_t before = 0;   // blocks before them
   bool loaded = false;
   int32_t q0, q1, k0, k1;
-  int64_t upto;          // blocks up to the lane's sequence, it included
+  uint32_t upto;         // blocks up to the lane's sequence, it included
 
   __device__ explicit PromptSchedule(const AttendArgs&) {}
 
   __device__ bool next(const AttendArgs& a, Seg& g) {
     const int lane = threadIdx.x & 31;
     const int32_t block = 2 * a.tile_tokens;
-    const int64_t id =
+    const uint32_t id =
         round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     ++round;
-    const int64_t at = id / a.kv_heads;
-    g.kh = static_cast<int32_t>(id % a.kv_heads);
+    const uint32_t at = id / a.kv_heads;
+    g.kh = static_cast<int32_t>(id - at * a.kv_heads);
+#pragma unroll 1
     for (; chunk < a.seqs; chunk += 32, loaded = false) {
       if (!loaded) {
         const int32_t i = chunk + lane;
         q0 = q1 = k0 = k1 = 0;
         if (i < a.seqs) {
           q0 = clamp_to(a.cu_q[i], a.tokens);
-          q1 = clamp_to(a.cu_q[i + 1], a.tokens);
+          q1 = max(q0, clamp_to(a.cu_q[i + 1], a.tokens));
           k0 = clamp_to(a.cu_k[i], a.total_k);
-          k1 = clamp_to(a.cu_k[i + 1], a.total_k);
-          if (q1 < q0) q1 = q0;
-          if (k1 < k0) k1 = k0;
+          k1 = max(k0, clamp_to(a.cu_k[i + 1], a.total_k));
         }
-        upto = (static_cast<int64_t>(q1 - q0) + block - 1) / block;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(~0u, upto, o);
-          if (lane >= o) upto += y;
-        }
+        upto = warp_sum_upto((static_cast<uint32_t>(q1 - q0) + block - 1) / block);
         loaded = true;
       }
-      const int64_t all = __shfl_sync(~0u, upto, 31);
+      const uint32_t all = __shfl_sync(~0u, upto, 31);
       if (at - before < all) {
         const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
         const int32_t s0 = __shfl_sync(~0u, q0, src), s1 = __shfl_sync(~0u, q1, src);
         g.k0 = __shfl_sync(~0u, k0, src);
         g.kv_len = __shfl_sync(~0u, k1, src) - g.k0;
         g.q_end = s1;
-        const int64_t last = __shfl_sync(~0u, upto, src) - 1 - (at - before);
-        g.tok[0] = s0 + static_cast<int32_t>(last) * block;
+        g.tok[0] = s0 + static_cast<int32_t>(__shfl_sync(~0u, upto, src) - 1 - (at - before)) *
+                            block;
         g.ntok[0] = min(a.tile_tokens, s1 - g.tok[0]);
         g.tok[1] = g.tok[0] + g.ntok[0];
         g.ntok[1] = min(a.tile_tokens, s1 - g.tok[1]);
-        g.split = g.first = 0;
-        g.t0 = 0;
-        g.seq = g.gaps = 0;
-        g.slot = 0;
+        g.split = g.first = g.t0 = g.seq = g.gaps = g.slot = 0;
         for (int s = 0; s < 2; ++s) {
           // keys that the tile's last token sees
           const int32_t lim =
@@ -256,60 +269,72 @@ struct PromptSchedule {
   }
 };
 
-// Keys of sequence b that lie in the prefix, and behind it.
+// Keys of sequence b, and those of them that lie behind the prefix.
 __device__ __forceinline__ int32_t seen_tokens(const AttendArgs& a, int64_t b) {
-  return clamp_to(a.lens[b], a.max_pages * a.page_size);
+  return clamp_to(a.lens[b], a.max_pages << a.page_log2);
 }
 __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
-  const int64_t n = seen_tokens(a, b) - a.prefix_len;
-  return n > 0 ? static_cast<int32_t>(n) : 0;
+  return max(seen_tokens(a, b) - static_cast<int32_t>(a.prefix_len), 0);
 }
 
-// Pages: the work is a line of units, one per (row block, key tile): first
-// the prefix (key/value head, block of the batch, tile), then every
-// sequence's own tokens (sequence, key/value head, tile). A unit is about as
-// dear in either part: 256 rows of products against a tile read from HBM. CTA
-// x takes the x-th equal share of the line, cut into segments where the row
-// block changes. Segment (group g, CTA x) has slot g + x, which grows along
-// the line: no two segments share one.
+// Pages: the work is a line of units (fewer than 2^31), cut into equal shares,
+// one per CTA: first the prefix (key/value head, block of the batch), then
+// every sequence's own tokens (sequence, key/value head). Each such group is
+// as long as its key tiles, of which one costs about the same in either part
+// (256 rows of products against a tile read from HBM), and kSegCost for
+// itself. A share is a list of segments, a group's tiles each; segment
+// (group g, CTA x) has slot g + x, which grows along the line: no two
+// segments share one.
+constexpr int32_t kSegCost = 2;
+
 struct PagedSchedule {
-  int64_t pos, end, prefix_units, own_units;
+  int32_t pos, end, prefix_units;
   int32_t turn = 0;     // split segments so far: they begin on the streams in turn
   int32_t chunk = 0;
-  int64_t before = 0;   // own units before the chunk
+  int32_t before = 0;   // own units before the chunk
   bool loaded = false;
   int32_t mine;         // own tokens of the lane's sequence
-  int64_t upto;
+  int32_t upto;
 
-  __device__ static int64_t units(const AttendArgs& a) {
-    return static_cast<int64_t>(a.kv_heads) * a.prefix_blocks * a.prefix_tiles;
+  // Units of a group with n key tiles.
+  __device__ static int32_t group_units(int32_t n) { return n > 0 ? n + kSegCost : 0; }
+  __device__ static int32_t units(const AttendArgs& a) {
+    return a.kv_heads * a.prefix_blocks * group_units(a.prefix_tiles);
   }
-  __device__ static int64_t share_of(int64_t all, int64_t grid) { return (all + grid - 1) / grid; }
+  __device__ static int32_t share_of(int32_t all, int32_t grid) {
+    return static_cast<int32_t>((static_cast<uint32_t>(all) + grid - 1) / grid);
+  }
 
   __device__ explicit PagedSchedule(const AttendArgs& a) {
     const int lane = threadIdx.x & 31;
     prefix_units = units(a);
-    own_units = 0;
+    int32_t own_units = 0;
     // CTA 0 also writes down where each sequence's units start.
     const bool first = blockIdx.x == 0;
+#pragma unroll 1
     for (int64_t b0 = 0; b0 < a.tokens; b0 += 32) {
       const int64_t b = b0 + lane;
-      int64_t n = 0;
-      if (b < a.tokens) n = static_cast<int64_t>(tiles_of(own_tokens(a, b))) * a.kv_heads;
-      int64_t inc = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += y;
-      }
+      int32_t n = 0;
+      if (b < a.tokens) n = group_units(tiles_of(own_tokens(a, b))) * a.kv_heads;
+      const int32_t inc = static_cast<int32_t>(warp_sum_upto(n));
       if (first && b < a.tokens) a.starts[b] = own_units + inc - n;
       own_units += __shfl_sync(~0u, inc, 31);
     }
     if (first && lane == 0) a.starts[a.tokens] = own_units;
-    const int64_t all = prefix_units + own_units, share = share_of(all, gridDim.x);
-    pos = min(share * blockIdx.x, all);
-    end = min(pos + share, all);
+    const int32_t all = prefix_units + own_units, share = share_of(all, gridDim.x);
+    const int64_t from = static_cast<int64_t>(share) * blockIdx.x;
+    pos = static_cast<int32_t>(min(from, static_cast<int64_t>(all)));
+    end = static_cast<int32_t>(min(from + share, static_cast<int64_t>(all)));
   }
 
+  // The tiles of a group of `tiles` whose units at, at + 1, ... are next in
+  // this CTA's share: from t0, n of them (0: only the group's own cost).
+  __device__ int32_t take(int32_t at, int32_t tiles, int32_t& t0) {
+    const int32_t n = min(group_units(tiles) - at, end - pos);
+    pos += n;
+    t0 = max(at - kSegCost, 0);
+    return max(at + n - kSegCost, 0) - t0;
+  }
   __device__ void split(Seg& g, int32_t n) {
     g.first = turn++ & 1;
     g.n[g.first] = (n + 1) / 2;
@@ -318,83 +343,73 @@ struct PagedSchedule {
 
   // Whether a page of the segment's tiles is missing: looked up here, ahead
   // of the streams, which then need no table.
-  __device__ static void find_gaps(const AttendArgs& a, Seg& g) {
-    const int64_t k0 = static_cast<int64_t>(g.t0) * kTile;
-    int64_t k1 = k0 + static_cast<int64_t>(max(g.split ? g.n[0] + g.n[1] : g.n[0], g.n[1])) * kTile;
-    k1 = min(k1, g.seq < 0 ? a.prefix_len : static_cast<int64_t>(g.kv_len));
-    const int64_t p1 = (k1 + a.page_size - 1) >> a.page_log2;
+  __device__ static void find_gaps(const AttendArgs& a, Seg& g, int32_t n) {
+    const int32_t end = g.seq < 0 ? static_cast<int32_t>(a.prefix_len) : g.kv_len;
+    const int32_t k1 = end - g.t0 * kTile > n * kTile ? (g.t0 + n) * kTile : end;
+    const int32_t p1 = (k1 + a.page_size - 1) >> a.page_log2;
     bool none = false;
-#pragma unroll 4
-    for (int64_t p = (k0 >> a.page_log2) + (threadIdx.x & 31); p < p1; p += 32)
-      none |= page_of(a, g.seq, p << a.page_log2) >= a.num_pages;
+#pragma unroll 1
+    for (int32_t p = ((g.t0 * kTile) >> a.page_log2) + (threadIdx.x & 31); p < p1; p += 32)
+      none |= page_of(a, g.seq, static_cast<int64_t>(p) << a.page_log2) >= a.num_pages;
     g.gaps = __any_sync(~0u, none);
   }
 
   __device__ bool next(const AttendArgs& a, Seg& g) {
-    if (pos >= end) return false;
-    g.k0 = g.q_end = g.kv_len = 0;
-    if (pos < prefix_units) {
-      const int64_t pg = pos / a.prefix_tiles;
-      const int32_t t = static_cast<int32_t>(pos % a.prefix_tiles);
-      const int32_t rb = static_cast<int32_t>(pg % a.prefix_blocks);
-      const int32_t n = static_cast<int32_t>(
-          min(static_cast<int64_t>(a.prefix_tiles - t), end - pos));
-      pos += n;
-      g.kh = static_cast<int32_t>(pg / a.prefix_blocks);
-      g.split = a.prefix_split;
-      g.t0 = t;
-      g.seq = -1;
-      g.slot = pg + blockIdx.x;
-      const int32_t rows = static_cast<int32_t>(a.tokens);
-      g.tok[0] = rb * (a.prefix_split ? 1 : 2) * a.tile_tokens;
-      g.ntok[0] = min(a.tile_tokens, rows - g.tok[0]);
-      g.tok[1] = g.tok[0] + g.ntok[0];
-      g.ntok[1] = g.split ? 0 : min(a.tile_tokens, rows - g.tok[1]);
-      if (g.split) {
-        split(g, n);
-      } else {
-        g.first = 0;
-        g.n[0] = n;
-        g.n[1] = g.ntok[1] > 0 ? n : 0;
-      }
-      find_gaps(a, g);
-      return true;
-    }
     const int lane = threadIdx.x & 31;
-    const int64_t at = pos - prefix_units;
-    for (;; chunk += 32, loaded = false) {
-      if (chunk >= a.tokens) return false;  // the lengths changed under the call
-      if (!loaded) {
-        const int64_t b = static_cast<int64_t>(chunk) + lane;
-        mine = b < a.tokens ? own_tokens(a, b) : 0;
-        upto = static_cast<int64_t>(tiles_of(mine)) * a.kv_heads;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(~0u, upto, o);
-          if (lane >= o) upto += y;
+    int32_t n = 0;
+#pragma unroll 1
+    while (n == 0) {
+      if (pos >= end) return false;
+      if (pos < prefix_units) {
+        const int32_t pg = pos / group_units(a.prefix_tiles);
+        n = take(pos - pg * group_units(a.prefix_tiles), a.prefix_tiles, g.t0);
+        g.kh = pg / a.prefix_blocks;
+        g.seq = -1;
+        g.kv_len = 0;
+        g.slot = pg + static_cast<int32_t>(blockIdx.x);
+        g.split = a.prefix_split;
+        g.tok[0] = (pg - g.kh * a.prefix_blocks) * (g.split ? 1 : 2) * a.tile_tokens;
+      } else {
+        const int32_t at = pos - prefix_units;
+#pragma unroll 1
+        for (;; chunk += 32, loaded = false) {
+          if (chunk >= a.tokens) return false;  // the lengths changed under the call
+          if (!loaded) {
+            const int64_t b = static_cast<int64_t>(chunk) + lane;
+            mine = b < a.tokens ? own_tokens(a, b) : 0;
+            upto = static_cast<int32_t>(
+                warp_sum_upto(group_units(tiles_of(mine)) * a.kv_heads));
+            loaded = true;
+          }
+          const int32_t all = __shfl_sync(~0u, upto, 31);
+          if (at - before < all) break;
+          before += all;
         }
-        loaded = true;
+        const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
+        g.kv_len = __shfl_sync(~0u, mine, src);
+        const int32_t tiles = tiles_of(g.kv_len), per = group_units(tiles);
+        const int32_t rel = at - before - (__shfl_sync(~0u, upto, src) - per * a.kv_heads);
+        g.kh = rel / per;
+        n = take(rel - g.kh * per, tiles, g.t0);
+        g.seq = chunk + src;
+        g.slot = g.seq * a.kv_heads + g.kh + static_cast<int32_t>(blockIdx.x);
+        g.split = 1;
+        g.tok[0] = g.seq;
       }
-      const int64_t all = __shfl_sync(~0u, upto, 31);
-      if (at - before < all) break;
-      before += all;
     }
-    const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
-    g.kv_len = __shfl_sync(~0u, mine, src);
-    const int32_t tiles = tiles_of(g.kv_len);
-    const int64_t rel = at - before - (__shfl_sync(~0u, upto, src) -
-                                       static_cast<int64_t>(tiles) * a.kv_heads);
-    g.kh = static_cast<int32_t>(rel / tiles);
-    g.t0 = static_cast<int32_t>(rel % tiles);
-    const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(tiles - g.t0), end - pos));
-    pos += n;
-    g.seq = chunk + src;
-    g.split = 1;
-    split(g, n);
-    g.tok[0] = g.tok[1] = g.seq;
-    g.ntok[0] = 1;
-    g.ntok[1] = 0;
-    g.slot = static_cast<int64_t>(g.seq) * a.kv_heads + g.kh + blockIdx.x;
-    find_gaps(a, g);
+    const int32_t rows = static_cast<int32_t>(a.tokens);
+    g.k0 = g.q_end = 0;
+    g.ntok[0] = g.seq < 0 ? min(a.tile_tokens, rows - g.tok[0]) : 1;
+    g.tok[1] = g.tok[0] + g.ntok[0];
+    g.ntok[1] = g.split ? 0 : min(a.tile_tokens, rows - g.tok[1]);
+    if (g.split) {
+      split(g, n);
+    } else {
+      g.first = 0;
+      g.n[0] = n;
+      g.n[1] = g.ntok[1] > 0 ? n : 0;
+    }
+    find_gaps(a, g, n);
     return true;
   }
 };
@@ -431,11 +446,14 @@ __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s
   const int lane = threadIdx.x & 31;
   const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s ^ g.first : 0);
   bool hidden = false;
+#pragma unroll 1
   for (int32_t i = 0; i < g.n[s]; ++i) {
     const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
+#pragma unroll 1
     for (int64_t j = max(k0, static_cast<int64_t>(lim)); j < k0 + kTile; ++j) {
       const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
       if (!v) continue;
+#pragma unroll 1
       for (int d = lane; d < a.dim; d += 32) hidden |= !finite(to_f(v[d]));
     }
     if (__any_sync(~0u, hidden)) break;
@@ -444,9 +462,11 @@ __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s
   const T* q = static_cast<const T*>(a.q) + tok * a.q_st + head * a.q_sh;
   float m = neg_inf(), l = 0.f;
   for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+#pragma unroll 1
   for (int32_t i = 0; i < g.n[s]; ++i) {
     const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
     const int64_t k1 = min(k0 + kTile, static_cast<int64_t>(lim));
+#pragma unroll 1
     for (int64_t j0 = k0; j0 < k1; j0 += 32) {
       float x = neg_inf();
       const T* k = j0 + lane < k1
@@ -454,18 +474,22 @@ __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s
                        : nullptr;
       if (k) {
         x = 0.f;
+#pragma unroll 1
         for (int d = 0; d < a.dim; ++d) x = fmaf(to_f(q[d]), to_f(k[d]), x);
         x *= a.c;
       }
       float mx = x;
+#pragma unroll 1
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
       const float m_new = fmaxf(m, mx), base = m_new == neg_inf() ? 0.f : m_new;
       const float keep = ex2(m - base), p = ex2(x - base);
       float sum = p;
+#pragma unroll 1
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
       l = l * keep + sum;
       m = m_new;
       for (int e = 0; e < 4; ++e) acc[e] *= keep;
+#pragma unroll 1
       for (int64_t j = j0; j < j0 + 32 && j < k1; ++j) {
         const float pj = __shfl_sync(~0u, p, static_cast<int>(j - j0));
         const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
@@ -513,12 +537,14 @@ struct Ring {
 // Segment `k` of the list, for one warp (or for one thread alone).
 template <bool WARP>
 __device__ __forceinline__ bool take_seg(Ctrl* c, uint32_t k, Seg& g, unsigned site) {
-  uint64_t* bar = &c->seg_full[k & 1];
-  if (!(WARP ? wait_warp(bar, (k >> 1) & 1, c, site) : wait(bar, (k >> 1) & 1, c, site)))
+  const int i = k % kSegs;
+  const uint32_t parity = (k / kSegs) & 1;
+  if (!(WARP ? wait_warp(&c->seg_full[i], parity, c, site)
+             : wait(&c->seg_full[i], parity, c, site)))
     return false;
-  g = c->seg[k & 1];
+  g = c->seg[i];
   if (WARP) __syncwarp();
-  if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&c->seg_empty[k & 1]);
+  if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&c->seg_empty[i]);
   return true;
 }
 
@@ -526,14 +552,16 @@ template <int DP, bool PAGED>
 __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
   Ctrl* c = cta.ctrl();
   typename ScheduleOf<PAGED>::type list(a);
+#pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     Seg g;
+    const int i = k % kSegs;
     const bool more = list.next(a, g);
     if (!more) g.n[0] = -1;
-    if (k >= 2 && !wait_warp(&c->seg_empty[k & 1], ((k >> 1) - 1) & 1, c, 16)) return;
+    if (k >= kSegs && !wait_warp(&c->seg_empty[i], (k / kSegs - 1) & 1, c, 16)) return;
     if ((threadIdx.x & 31) == 0) {
-      c->seg[k & 1] = g;
-      mbar_arrive(&c->seg_full[k & 1]);
+      c->seg[i] = g;
+      mbar_arrive(&c->seg_full[i]);
     }
     __syncwarp();
     if (!more) return;
@@ -542,6 +570,7 @@ __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
 
 // The loading warp: per segment the row tiles, then K and V in the order in
 // which the products take them: K leads V by one tile (shared) or two (split).
+// The pages of a load are looked up one load ahead.
 template <int DP, bool PAGED>
 __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorMap* qm1,
                      const CUtensorMap* km, const CUtensorMap* vm, Cta<DP> cta) {
@@ -549,24 +578,35 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
   Ctrl* c = cta.ctrl();
   const int lane = threadIdx.x & 31;
   Ring<DP> ring;
-  uint32_t qs[2] = {0, 0};  // uses of the two row-tile buffers
+  uint32_t used = 0, phase = 0;  // row-tile buffers: in use before, parity of the next wait
   uint32_t turn = 0;
   // boxes of a K or V tile, one lane each: page within the tile, half
-  const int boxes = PAGED && a.page_size < kTile ? kTile / a.page_size : 1;
+  const int boxes = (PAGED && a.page_size < kTile ? kTile >> a.page_log2 : 1) * L::kHalves;
   const int pi = lane / L::kHalves, h = lane % L::kHalves;
   const uint32_t to = h * L::kHalf + (PAGED ? pi * a.page_size * 128 : 0);
-  for (uint32_t k = 0;; ++k) {
-    Seg g;
-    if (!take_seg<true>(c, k, g, 17)) return;
-    if (g.n[0] < 0) break;
+  const auto page = [&](const Seg& g, int32_t t) -> int32_t {
+    if constexpr (PAGED) {
+      if (lane < boxes)
+        return page_of(a, g.seq, static_cast<int64_t>(t) * kTile + pi * a.page_size);
+    }
+    return 0;
+  };
+  Seg g;
+  if (!take_seg<true>(c, 0, g, 17)) return;
+  int32_t id = g.n[0] < 0 ? 0 : page(g, g.t0);
+#pragma unroll 1
+  for (uint32_t k = 1; g.n[0] >= 0; ++k) {
     const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
-    if (n == 0) continue;
     // Split segments take the two row-tile buffers in turn, so that the next
     // segment's rows load while this one's are in use; shared ones take both.
     const int q_first = g.split ? turn++ & 1 : 0, q_count = !g.split && g.ntok[1] > 0 ? 2 : 1;
-    for (int i = q_first; i < q_first + q_count; ++i) {
-      if (qs[i] > 0 && !wait_warp(&c->q_empty[i], (qs[i] - 1) & 1, c, 18)) return;
-      ++qs[i];
+#pragma unroll 1
+    for (int i = q_first; n > 0 && i < q_first + q_count; ++i) {
+      if ((used >> i) & 1) {
+        if (!wait_warp(&c->q_empty[i], (phase >> i) & 1, c, 18)) return;
+        phase ^= 1u << i;
+      }
+      used |= 1u << i;
       // a segment of one sequence needs that token's rows alone
       const bool one = PAGED && g.seq >= 0;
       if (lane == 0)
@@ -577,49 +617,56 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
         tma_load3(cta.q(i) + lane * L::kHalf, one ? qm1 : qm, lane * 64, g.kh * a.group,
                   g.tok[g.split ? 0 : i], &c->q_full[i]);
     }
-    const auto page = [&](int32_t t) -> int32_t {
-      if constexpr (PAGED) {
-        if (lane < boxes * L::kHalves && t < g.t0 + n)
-          return page_of(a, g.seq, static_cast<int64_t>(t) * kTile + pi * a.page_size);
-      }
-      return 0;
-    };
-    const auto put = [&](const CUtensorMap* map, int32_t t, int32_t id) -> bool {
+    // Load i: K for i < lead, then V_0, K_lead, V_1, K_lead+1, ..., and the
+    // last values.
+    const int32_t lead = min(n, g.split ? 2 : 1), pairs = 2 * (n - lead);
+    Seg next;
+    if (n == 0 && !take_seg<true>(c, k, next, 17)) return;
+#pragma unroll 1
+    for (int32_t i = 0; i < 2 * n; ++i) {
+      const auto tile = [&](int32_t i, bool& is_v) -> int32_t {
+        const int32_t u = i - lead;
+        if (u < 0) return is_v = false, i;
+        if (u >= pairs) return is_v = true, u - (n - lead);
+        is_v = (u & 1) == 0;
+        return is_v ? u / 2 : lead + u / 2;
+      };
+      bool is_v, next_v;
+      const int32_t t = g.t0 + tile(i, is_v);
+      // The next segment is taken early: its first pages are looked up under
+      // this one's last load.
+      if (i == 1 && !take_seg<true>(c, k, next, 17)) return;
+      int32_t id_next = 0;
+      if (i + 1 < 2 * n) id_next = page(g, g.t0 + tile(i + 1, next_v));
+      else if (next.n[0] >= 0) id_next = page(next, next.t0);
       const int st = ring.stage;
-      if (ring.round > 0 && !wait_warp(&c->kv_empty[st], (ring.round - 1) & 1, c, 19)) return false;
+      if (ring.round > 0 && !wait_warp(&c->kv_empty[st], (ring.round - 1) & 1, c, 19)) return;
       ring.next();
       if (lane == 0) mbar_arrive_expect_tx(&c->kv_full[st], L::kBytes);
       __syncwarp();
-      if (lane < boxes * L::kHalves) {
+      if (lane < boxes) {
         unsigned char* dst = cta.stage(st) + to;
+        const CUtensorMap* map = is_v ? vm : km;
         if constexpr (PAGED)
           tma_load4(dst, map, h * 64, g.kh, (t * kTile) & (a.page_size - 1), id, &c->kv_full[st]);
         else
           tma_load3(dst, map, h * 64, g.kh, g.k0 + t * kTile, &c->kv_full[st]);
       }
-      return true;
-    };
-    int32_t id0 = page(g.t0), id1 = page(g.t0 + 1);
-    const int lead = g.split ? 2 : 1;
-    if (!put(km, g.t0, id0)) return;
-    if (lead == 2 && n > 1 && !put(km, g.t0 + 1, id1)) return;
-    for (int32_t j = 0; j < n; ++j) {
-      const int32_t t = g.t0 + j;
-      const int32_t id2 = page(t + 2);
-      if (!put(vm, t, id0)) return;
-      if (j + lead < n && !put(km, t + lead, lead == 2 ? id2 : id1)) return;
-      id0 = id1;
-      id1 = id2;
+      id = id_next;
     }
+    if (n == 0 && next.n[0] >= 0) id = page(next, next.t0);
+    g = next;
   }
   // The last arrivals of the products on these barriers come before the
   // shared memory is given back.
+#pragma unroll 1
   for (int i = 0; i < L::kStages; ++i) {
     const uint32_t uses = ring.round + (i < ring.stage ? 1 : 0);
     if (uses > 0 && !wait_warp(&c->kv_empty[i], (uses - 1) & 1, c, 19)) return;
   }
+#pragma unroll 1
   for (int i = 0; i < 2; ++i)
-    if (qs[i] > 0 && !wait_warp(&c->q_empty[i], (qs[i] - 1) & 1, c, 18)) return;
+    if (((used >> i) & 1) && !wait_warp(&c->q_empty[i], (phase >> i) & 1, c, 18)) return;
 }
 
 // The thread that issues the products. In program order: for each key tile
@@ -628,24 +675,23 @@ template <typename T, int DP>
 __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
   using L = Layout<DP>;
   Ctrl* c = cta.ctrl();
-  constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
   constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
-  const uint32_t q0 = smem_addr(cta.q(0)), st0 = smem_addr(cta.stage(0));
+  const uint64_t q0 = operand(smem_addr(cta.q(0)), 16, 1024);
+  const uint64_t k0 = operand(smem_addr(cta.stage(0)), 16, 1024);
+  const uint64_t v0 = operand(smem_addr(cta.stage(0)), L::kHalf, 1024);
   Ring<DP> ring;
-  uint32_t qn[2] = {0, 0};       // uses of the two row-tile buffers
+  // Bit s (or i): parities of the next waits, and whether O_s was used before.
+  uint32_t q_phase = 0, p_phase = 0, o_phase = 0, o_used = 0;
   uint32_t turn = 0;
-  uint32_t done[2] = {0, 0};     // tiles of each stream
-  uint32_t outs[2] = {0, 0};     // segments of each stream with products
 
   const auto full = [&]() { return wait(&c->kv_full[ring.stage], ring.round & 1, c, 20); };
-  const auto drop = [&]() {
-    mma_commit(&c->kv_empty[ring.stage]);
-    ring.next();
-  };
-  const auto scores = [&](int s, int qs) {
-    const uint64_t qa = operand(q0 + qs * L::kBytes, 16, 1024);
-    const uint64_t kb = operand(st0 + ring.stage * L::kBytes, 16, 1024);
+  // Q K^T of stream s with the K tile in the ring's current stage
+  const auto scores = [&](int s, int q) {
+    tc_fence_after();
+    const uint64_t qa = q0 + ((q * L::kBytes) >> 4);
+    const uint64_t kb = k0 + ((ring.stage * L::kBytes) >> 4);
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const uint64_t off = ((i / 4) * L::kHalf + (i % 4) * 32) >> 4;
@@ -656,97 +702,80 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
   // P V of stream s with the V tile in the ring's current stage
   const auto values = [&](int s, bool first) -> bool {
     if (first) {
-      if (outs[s] > 0 && !wait(&c->o_free[s], (outs[s] - 1) & 1, c, 22)) return false;
-      ++outs[s];
+      if ((o_used >> s) & 1) {
+        if (!wait(&c->o_free[s], (o_phase >> s) & 1, c, 22)) return false;
+        o_phase ^= 1u << s;
+      }
+      o_used |= 1u << s;
     }
-    const uint64_t vb = operand(st0 + ring.stage * L::kBytes, L::kHalf, 1024);
-#pragma unroll
+    const uint64_t vb = v0 + ((ring.stage * L::kBytes) >> 4);
+    const uint32_t o = tmem + 2 * kTile + s * kTile, w = tmem + s * kTile;
+#pragma unroll 1
     for (int p = 0; p < kParts; ++p) {
-      if (!wait(&c->p_full[s][p], done[s] & 1, c, 21)) return false;
+      if (!wait(&c->p_full[s][p], (p_phase >> s) & 1, c, 21)) return false;
       tc_fence_after();
       constexpr int kSteps = kTile / 16 / kParts;
 #pragma unroll
-      for (int e = 0; e < kSteps; ++e) {
-        const int i = p * kSteps + e;
-        mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + i * 8, vb + ((i * 2048) >> 4),
-               kShapeO, !first || i > 0);
-      }
+      for (int e = 0; e < kSteps; ++e)
+        mma_ts(o, w + (p * kSteps + e) * 8, vb + (((p * kSteps + e) * 2048) >> 4), kShapeO,
+               !first || p > 0 || e > 0);
     }
-    ++done[s];
+    p_phase ^= 1u << s;
     mma_commit(&c->o_done[s]);
     return true;
   };
 
+#pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     Seg g;
     if (!take_seg<false>(c, k, g, 23) || g.n[0] < 0) return;
     const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
+    const int q_first = g.split ? turn++ & 1 : 0, q_count = !g.split && g.ntok[1] > 0 ? 2 : 1;
     if (n == 0) continue;
-    if (g.split) {
-      const int b = turn++ & 1;
-      if (!wait(&c->q_full[b], qn[b] & 1, c, 24)) return;
-      ++qn[b];
-      for (int32_t j = 0; j < min(n, 2); ++j) {
+#pragma unroll 1
+    for (int i = q_first; i < q_first + q_count; ++i) {
+      if (!wait(&c->q_full[i], (q_phase >> i) & 1, c, 24)) return;
+      q_phase ^= 1u << i;
+    }
+    const auto drop_rows = [&]() {
+#pragma unroll 1
+      for (int i = q_first; i < q_first + q_count; ++i) mma_commit(&c->q_empty[i]);
+    };
+    // Step j: with V_j, and with K_{j + lead} behind it. Steps before 0 have
+    // no values yet.
+    const int32_t lead = g.split ? 2 : 1;
+#pragma unroll 1
+    for (int32_t j = -lead; j < n; ++j) {
+      // shared: both streams take every tile; split: they take turns
+      const int s0 = g.split ? (j & 1) ^ g.first : 0, s1 = g.split ? s0 + 1 : 2;
+      const bool more = j + lead < n;
+      Ring<DP> v = ring, kn = ring;
+      if (j >= 0) {
         if (!full()) return;
-        tc_fence_after();
-        scores((j & 1) ^ g.first, b);
-        drop();
-      }
-      if (n <= 2) mma_commit(&c->q_empty[b]);
-      for (int32_t j = 0; j < n; ++j) {
-        const int s = (j & 1) ^ g.first;
-        if (!full()) return;
-        if (!values(s, j < 2)) return;
-        drop();
-        if (j + 2 < n) {
-          if (!full()) return;
-          tc_fence_after();
-          scores(s, b);
-          drop();
-          if (j + 3 == n) mma_commit(&c->q_empty[b]);
-        }
-      }
-    } else {
-      const int tiles = g.ntok[1] > 0 ? 2 : 1;
-      for (int i = 0; i < tiles; ++i) {
-        if (!wait(&c->q_full[i], qn[i] & 1, c, 24)) return;
-        ++qn[i];
-      }
-      const auto drop_rows = [&]() {
-        for (int i = 0; i < tiles; ++i) mma_commit(&c->q_empty[i]);
-      };
-      if (!full()) return;
-      tc_fence_after();
-      for (int s = 0; s < 2; ++s)
-        if (g.n[s] > 0) scores(s, s);
-      drop();
-      if (n == 1) drop_rows();
-      for (int32_t j = 0; j < n; ++j) {
-        // V_j in the current stage, K_{j+1} in the next one
-        if (!full()) return;
-        const Ring<DP> v = ring;
-        Ring<DP> kn = ring;
         kn.next();
-        bool have = false;
-        for (int s = 0; s < 2; ++s) {
-          if (j < g.n[s]) {
-            if (!values(s, j == 0)) return;
+      }
+      bool have = false;
+#pragma unroll 1
+      for (int s = s0; s < s1; ++s) {
+        if (j >= 0) {
+          ring = v;
+          if (g.split || j < g.n[s]) {
+            if (!values(s, j < lead)) return;
           }
-          if (s == 1) mma_commit(&c->kv_empty[v.stage]);
-          if (j + 1 < g.n[s]) {
-            ring = kn;
-            if (!have && !full()) return;
-            have = true;
-            tc_fence_after();
-            scores(s, s);
-            ring = v;
-          }
+          if (s + 1 == s1) mma_commit(&c->kv_empty[v.stage]);
         }
-        ring = kn;
-        if (j + 1 < n) {
-          drop();
-          if (j + 2 == n) drop_rows();
+        if (g.split ? more : j + 1 < g.n[s]) {
+          ring = kn;
+          if (!have && !full()) return;
+          have = true;
+          scores(s, g.split ? q_first : s);
         }
+      }
+      ring = kn;
+      if (more) {
+        mma_commit(&c->kv_empty[ring.stage]);
+        ring.next();
+        if (j + lead + 1 == n) drop_rows();
       }
     }
   }
@@ -763,6 +792,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
   const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kTile;
   const float grow = kGrow / a.c;
   uint32_t done = 0;
+#pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     Seg g;
     if (!take_seg<true>(c, k, g, 25) || g.n[0] < 0) return;
@@ -783,15 +813,14 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     }
     const bool busy = __any_sync(~0u, valid);  // else the warp only keeps step
     float base = neg_inf(), l = 0.f;  // the row's base, in units of <q, k>
+#pragma unroll 1
     for (int32_t i = 0; i < n; ++i) {
       const int32_t t = g.split ? g.t0 + (s ^ g.first) + 2 * i : g.t0 + i;
-      uint32_t bad = 0;  // pages of the tile that are not there
+      uint32_t bad = 0;  // groups of 16 keys whose page is not there
       if (PAGED && g.gaps) {
-        const int pages = a.page_size < kTile ? kTile >> a.page_log2 : 1;
         bool none = false;
-        if (lane < pages)
-          none = page_of(a, g.seq, static_cast<int64_t>(t) * kTile + lane * a.page_size) >=
-                 a.num_pages;
+        if (lane < kTile / 16)
+          none = page_of(a, g.seq, static_cast<int64_t>(t) * kTile + lane * 16) >= a.num_pages;
         bad = __ballot_sync(~0u, none);
       }
       if (!wait_warp(&c->s_full[s], done & 1, c, 26)) return;
@@ -806,16 +835,19 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       for (int b = 0; b < 4; ++b)
         tmem_load32(ts + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
       tmem_wait_load();
-      const int64_t rel = static_cast<int64_t>(lim) - static_cast<int64_t>(t) * kTile;
+      const int32_t rel = lim - t * kTile;
       if (rel < kTile || bad != 0) {
-        const int r = rel < 0 ? 0 : (rel > kTile ? kTile : static_cast<int>(rel));
-        if (bad == 0) {
+        // bit j of word b: key 32 b + j of the tile is seen
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) x[j] = j < r ? x[j] : neg_inf();
-        } else {
+        for (int b = 0; b < 4; ++b) {
+          const int r = rel - 32 * b;
+          uint32_t see = r >= 32 ? ~0u : r <= 0 ? 0u : (1u << r) - 1;
+          if (PAGED) {
+            if ((bad >> (2 * b)) & 1) see &= 0xffff0000u;
+            if ((bad >> (2 * b + 1)) & 1) see &= 0x0000ffffu;
+          }
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            x[j] = j < r && !((bad >> (j >> a.page_log2)) & 1) ? x[j] : neg_inf();
+          for (int j = 0; j < 32; ++j) x[32 * b + j] = (see >> j) & 1 ? x[32 * b + j] : neg_inf();
         }
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -939,6 +971,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     const int32_t seen_tiles = n > 0 ? (g.split ? g.t0 + (s ^ g.first) + 2 * (n - 1) : g.t0 + n - 1) + 1 : 0;
     uint32_t todo = __ballot_sync(
         ~0u, valid && odd && lim < static_cast<int64_t>(seen_tiles) * kTile);
+#pragma unroll 1
     while (todo != 0) {
       const int src = __ffs(todo) - 1;
       todo &= todo - 1;
@@ -989,8 +1022,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       for (int p = 0; p < kParts; ++p) mbar_init(&c->p_full[s][p], kTile);
       mbar_init(&c->o_done[s], 1);
       mbar_init(&c->o_free[s], kTile);
-      mbar_init(&c->seg_full[s], 1);
-      mbar_init(&c->seg_empty[s], 10);  // the loading and multiplying roles, eight warps
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&c->seg_full[i], 1);
+      mbar_init(&c->seg_empty[i], 10);  // the loading and multiplying roles, eight warps
     }
     c->dead = 0;
     mbar_init_fence();
@@ -1054,7 +1089,7 @@ struct JoinArgs {
   int64_t o_sb, o_sh;
   float* lse;
   int64_t l_sb, l_sh;
-  int64_t grid;  // CTAs that shared the work
+  int32_t grid;  // CTAs that shared the work
 };
 constexpr int kJoinWarps = 4;
 
@@ -1065,27 +1100,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   if (r >= a.tokens * a.heads) return;
   const int64_t b = r / a.heads;
-  const int32_t h = static_cast<int32_t>(r % a.heads), kh = h / a.group, e = h % a.group;
-  const int64_t pre = PagedSchedule::units(a), own = a.starts[a.tokens];
-  const int64_t share = PagedSchedule::share_of(pre + own, j.grid);
+  const int32_t h = static_cast<int32_t>(r - b * a.heads), kh = h / a.group, e = h - kh * a.group;
+  const int32_t pre = PagedSchedule::units(a), from = a.starts[b], upto = a.starts[b + 1];
+  const int32_t share = PagedSchedule::share_of(pre + a.starts[a.tokens], j.grid);
   // Partial i < np: prefix; np <= i < np + no: own. In both the segments of
   // one group have consecutive slots, each with one or two partials.
   int64_t p0 = 0, o0 = 0;
   int32_t np = 0, no = 0;
-  const int32_t per = a.prefix_split ? 2 : 1;
   if (a.prefix_tiles > 0) {
-    const int32_t block = (a.prefix_split ? 1 : 2) * a.tile_tokens;
-    const int64_t rb = b / block, in = b % block, pg = kh * a.prefix_blocks + rb;
-    const int64_t u = pg * a.prefix_tiles, c0 = u / share,
-                  c1 = (u + a.prefix_tiles - 1) / share;
-    np = static_cast<int32_t>(c1 - c0 + 1) * per;
-    p0 = (pg + c0) * 256 + (in / a.tile_tokens) * kTile + (in % a.tile_tokens) * a.group + e;
+    const int32_t block = (a.prefix_split ? 1 : 2) * a.tile_tokens, bi = static_cast<int32_t>(b);
+    const int32_t rb = bi / block, in = bi - rb * block, pg = kh * a.prefix_blocks + rb;
+    const int32_t u = pg * (a.prefix_tiles + kSegCost) + kSegCost;
+    const int32_t c0 = u / share, c1 = (u + a.prefix_tiles - 1) / share;
+    const int32_t s = in >= a.tile_tokens;
+    np = (c1 - c0 + 1) << a.prefix_split;
+    p0 = static_cast<int64_t>(pg + c0) * 256 + s * kTile + (in - s * a.tile_tokens) * a.group + e;
   }
-  const int64_t mine = a.starts[b + 1] - a.starts[b];
-  if (mine > 0) {
-    const int64_t tiles = mine / a.kv_heads, u = pre + a.starts[b] + kh * tiles;
-    const int64_t c0 = u / share, c1 = (u + tiles - 1) / share;
-    no = static_cast<int32_t>(c1 - c0 + 1) * 2;
+  if (upto > from) {
+    const int32_t per = (upto - from) / a.kv_heads, u = pre + from + kh * per + kSegCost;
+    const int32_t c0 = u / share, c1 = (u + per - kSegCost - 1) / share;
+    no = (c1 - c0 + 1) * 2;
     o0 = (b * a.kv_heads + kh + c0) * 2 * a.group + e;
   }
   const auto at = [&](int32_t i) -> int64_t {  // row of partial i in its buffer
@@ -1099,10 +1133,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   // Lane i keeps the log-sum-exp of partial i; more than 32 are read again.
   const float held = lse_of(lane);
   float m = held;
+#pragma unroll 1
   for (int32_t i = lane + 32; i < all; i += 32) m = fmaxf(m, lse_of(i));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
   const float base = m == neg_inf() ? 0.f : m;
   float sum = ex2(held - base);
+#pragma unroll 1
   for (int32_t i = lane + 32; i < all; i += 32) sum += ex2(lse_of(i) - base);
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const bool any = sum != 0.f;  // NaN counts
@@ -1113,6 +1149,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
   // Every partial holds an output (zeros where it saw nothing), so that the
   // loads wait for no log-sum-exp.
+#pragma unroll 1
   for (int32_t i0 = 0; i0 < all; i0 += 32) {
     const float w = any ? ex2((i0 == 0 ? held : lse_of(i0 + lane)) - lse) : 0.f;
     const int32_t n = min(all - i0, 32);

@@ -140,6 +140,7 @@ dsa_status launch_join(const AttendArgs& a, const JoinArgs& j, cudaStream_t stre
 struct PagedPlan {
   int32_t tile_tokens, prefix_tiles, prefix_blocks, prefix_split;
   int grid;
+  bool fits;  // units, slots and rows within 32 bits
   size_t starts, prefix_o, prefix_lse, own_o, own_lse, bytes;
 };
 
@@ -159,7 +160,9 @@ PagedPlan plan_paged(int64_t batch, int32_t heads, int32_t kv_heads, int32_t hea
   p.prefix_blocks = static_cast<int32_t>((batch + block - 1) / block);
   const int64_t groups = static_cast<int64_t>(kv_heads) * p.prefix_blocks;
   const int64_t own_tiles = (max_pages * page_size - prefix_len + kTile - 1) / kTile;
-  const int64_t most = groups * p.prefix_tiles + batch * kv_heads * own_tiles;
+  const int64_t most = groups * (p.prefix_tiles + kSegCost) +
+                       batch * kv_heads * (own_tiles + kSegCost);
+  p.fits = most <= INT32_MAX - 1024;
   const int64_t sms = sm_count();
   p.grid = static_cast<int>(most < 1 ? 1 : (most < sms ? most : sms));
   const size_t pslots = p.prefix_tiles > 0 ? groups + p.grid : 0;
@@ -170,7 +173,7 @@ PagedPlan plan_paged(int64_t batch, int32_t heads, int32_t kv_heads, int32_t hea
     at += up256(n);
     return was;
   };
-  p.starts = take((batch + 1) * 8);
+  p.starts = take((batch + 1) * 4);
   p.prefix_o = take(pslots * 256 * dp * 4);
   p.prefix_lse = take(pslots * 256 * 4);
   p.own_o = take(oslots * 2 * group * dp * 4);
@@ -268,6 +271,7 @@ extern "C" dsa_status dsa_prompt_attention(
   // No more blocks than this, whatever the offsets hold.
   const int64_t blocks = (total_q / (2 * a.tile_tokens) + seqs) * kv_heads;
   const int64_t sms = dsa::sm_count();
+  if (blocks + 2 * sms > UINT32_MAX) return DSA_EUNSUPPORTED;
   return dsa::launch<false>(m, a, dtype, static_cast<int>(blocks < sms ? blocks : sms),
                             static_cast<cudaStream_t>(stream));
 }
@@ -305,6 +309,7 @@ extern "C" dsa_status dsa_shared_prefix_attention(
     return DSA_EUNSUPPORTED;
   const dsa::PagedPlan p =
       dsa::plan_paged(batch, heads, kv_heads, head_dim, prefix_len, max_pages, page_size);
+  if (!p.fits) return DSA_EUNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return DSA_EINVAL;
@@ -340,7 +345,7 @@ extern "C" dsa_status dsa_shared_prefix_attention(
   a.prefix_tiles = num_pages > 0 ? p.prefix_tiles : 0;
   a.prefix_blocks = p.prefix_blocks;
   a.prefix_split = p.prefix_split;
-  a.starts = reinterpret_cast<int64_t*>(ws + p.starts);
+  a.starts = reinterpret_cast<int32_t*>(ws + p.starts);
   a.prefix_o = reinterpret_cast<float*>(ws + p.prefix_o);
   a.prefix_lse = reinterpret_cast<float*>(ws + p.prefix_lse);
   a.own_o = reinterpret_cast<float*>(ws + p.own_o);
