@@ -118,7 +118,9 @@ struct AttendArgs {
   int64_t prefix_len;
   int32_t prefix_tiles, prefix_blocks, prefix_split;
   int32_t* starts;                 // [tokens + 1]: own units before each sequence
-  float *prefix_o, *prefix_lse;    // [slot][256][DP], [slot][256]
+  // [slot][2][DP / 4][128][4] (neighbouring rows write neighbouring 16 bytes),
+  // [slot][256]
+  float *prefix_o, *prefix_lse;
   float *own_o, *own_lse;          // [slot][2 G][DP], [slot][2 G]
 };
 
@@ -280,16 +282,17 @@ __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
 // Pages: the work is a line of units (fewer than 2^31), cut into equal shares,
 // one per CTA: first the prefix (key/value head, block of the batch), then
 // every sequence's own tokens (sequence, key/value head). Each such group is
-// as long as its key tiles, of which one costs about the same in either part
-// (256 rows of products against a tile read from HBM), and kSegCost for
-// itself. A share is a list of segments, a group's tiles each; segment
-// (group g, CTA x) has slot g + x, which grows along the line: no two
-// segments share one.
-constexpr int32_t kSegCost = 2;
+// as long as it is dear: kSegCost for itself and a cost for each of its key
+// tiles, which falls to the share that holds the tile's first unit. A share is
+// a list of segments, a group's tiles each; segment (group g, CTA x) has slot
+// g + x, which grows along the line: no two segments share one.
+constexpr int32_t kSegCost = 8;
+constexpr int32_t kTileCost = 4;        // one row tile
+constexpr int32_t kTwoTileCost = 5;     // two row tiles, bound by products
 
 struct PagedSchedule {
   int32_t pos, end, prefix_units;
-  int32_t turn = 0;     // split segments so far: they begin on the streams in turn
+  int32_t turn = 0;     // tiles of split segments so far: the streams take turns
   int32_t chunk = 0;
   int32_t before = 0;   // own units before the chunk
   bool loaded = false;
@@ -297,14 +300,27 @@ struct PagedSchedule {
   int32_t upto;
 
   // Units of a group with n key tiles.
-  __device__ static int32_t group_units(int32_t n) { return n > 0 ? n + kSegCost : 0; }
+  __device__ static int32_t group_units(int32_t n, int32_t cost) {
+    return n > 0 ? n * cost + kSegCost : 0;
+  }
+  __device__ static int32_t prefix_cost(const AttendArgs& a) {
+    return a.prefix_split || a.prefix_tiles == 0 ? kTileCost : kTwoTileCost;
+  }
+  // Never less than a tile: between a group's first and last segment each
+  // share then begins some tile, so that no slot between theirs is empty.
+  __device__ static int32_t share_of(const AttendArgs& a, int32_t all, int32_t grid) {
+    return max(static_cast<int32_t>((static_cast<uint32_t>(all) + grid - 1) / grid),
+               prefix_cost(a));
+  }
+  __device__ static int32_t prefix_group(const AttendArgs& a) {
+    return group_units(a.prefix_tiles, prefix_cost(a));
+  }
+  __device__ static int32_t own_group(int32_t tokens) {
+    return group_units(tiles_of(tokens), kTileCost);
+  }
   __device__ static int32_t units(const AttendArgs& a) {
-    return a.kv_heads * a.prefix_blocks * group_units(a.prefix_tiles);
+    return a.kv_heads * a.prefix_blocks * prefix_group(a);
   }
-  __device__ static int32_t share_of(int32_t all, int32_t grid) {
-    return static_cast<int32_t>((static_cast<uint32_t>(all) + grid - 1) / grid);
-  }
-
   __device__ explicit PagedSchedule(const AttendArgs& a) {
     const int lane = threadIdx.x & 31;
     prefix_units = units(a);
@@ -315,28 +331,29 @@ struct PagedSchedule {
     for (int64_t b0 = 0; b0 < a.tokens; b0 += 32) {
       const int64_t b = b0 + lane;
       int32_t n = 0;
-      if (b < a.tokens) n = group_units(tiles_of(own_tokens(a, b))) * a.kv_heads;
+      if (b < a.tokens) n = own_group(own_tokens(a, b)) * a.kv_heads;
       const int32_t inc = static_cast<int32_t>(warp_sum_upto(n));
       if (first && b < a.tokens) a.starts[b] = own_units + inc - n;
       own_units += __shfl_sync(~0u, inc, 31);
     }
     if (first && lane == 0) a.starts[a.tokens] = own_units;
-    const int32_t all = prefix_units + own_units, share = share_of(all, gridDim.x);
+    const int32_t all = prefix_units + own_units, share = share_of(a, all, gridDim.x);
     const int64_t from = static_cast<int64_t>(share) * blockIdx.x;
     pos = static_cast<int32_t>(min(from, static_cast<int64_t>(all)));
     end = static_cast<int32_t>(min(from + share, static_cast<int64_t>(all)));
   }
 
-  // The tiles of a group of `tiles` whose units at, at + 1, ... are next in
-  // this CTA's share: from t0, n of them (0: only the group's own cost).
-  __device__ int32_t take(int32_t at, int32_t tiles, int32_t& t0) {
-    const int32_t n = min(group_units(tiles) - at, end - pos);
-    pos += n;
-    t0 = max(at - kSegCost, 0);
-    return max(at + n - kSegCost, 0) - t0;
+  // The tiles of a group of `units` whose units at, at + 1, ... are next in
+  // this CTA's share: from t0, n of them (0: only a part of a cost).
+  __device__ int32_t take(int32_t at, int32_t units, int32_t cost, int32_t& t0) {
+    const int32_t m = min(units - at, end - pos);
+    pos += m;
+    t0 = max(at - kSegCost + cost - 1, 0) / cost;
+    return max(at + m - kSegCost + cost - 1, 0) / cost - t0;
   }
   __device__ void split(Seg& g, int32_t n) {
-    g.first = turn++ & 1;
+    g.first = turn & 1;
+    turn += n;
     g.n[g.first] = (n + 1) / 2;
     g.n[1 - g.first] = n / 2;
   }
@@ -361,8 +378,8 @@ struct PagedSchedule {
     while (n == 0) {
       if (pos >= end) return false;
       if (pos < prefix_units) {
-        const int32_t pg = pos / group_units(a.prefix_tiles);
-        n = take(pos - pg * group_units(a.prefix_tiles), a.prefix_tiles, g.t0);
+        const int32_t per = prefix_group(a), pg = pos / per;
+        n = take(pos - pg * per, per, prefix_cost(a), g.t0);
         g.kh = pg / a.prefix_blocks;
         g.seq = -1;
         g.kv_len = 0;
@@ -378,7 +395,7 @@ struct PagedSchedule {
             const int64_t b = static_cast<int64_t>(chunk) + lane;
             mine = b < a.tokens ? own_tokens(a, b) : 0;
             upto = static_cast<int32_t>(
-                warp_sum_upto(group_units(tiles_of(mine)) * a.kv_heads));
+                warp_sum_upto(own_group(mine) * a.kv_heads));
             loaded = true;
           }
           const int32_t all = __shfl_sync(~0u, upto, 31);
@@ -387,10 +404,10 @@ struct PagedSchedule {
         }
         const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
         g.kv_len = __shfl_sync(~0u, mine, src);
-        const int32_t tiles = tiles_of(g.kv_len), per = group_units(tiles);
+        const int32_t per = own_group(g.kv_len);
         const int32_t rel = at - before - (__shfl_sync(~0u, upto, src) - per * a.kv_heads);
         g.kh = rel / per;
-        n = take(rel - g.kh * per, tiles, g.t0);
+        n = take(rel - g.kh * per, per, kTileCost, g.t0);
         g.seq = chunk + src;
         g.slot = g.seq * a.kv_heads + g.kh + static_cast<int32_t>(blockIdx.x);
         g.split = 1;
@@ -534,18 +551,56 @@ struct Ring {
   }
 };
 
-// Segment `k` of the list, for one warp (or for one thread alone).
+// Segment `k` of the list, for one warp (or for one thread alone); `last` lets
+// go of its entry.
 template <bool WARP>
-__device__ __forceinline__ bool take_seg(Ctrl* c, uint32_t k, Seg& g, unsigned site) {
+__device__ __forceinline__ bool take_seg(Ctrl* c, uint32_t k, Seg& g, bool last, unsigned site) {
   const int i = k % kSegs;
   const uint32_t parity = (k / kSegs) & 1;
   if (!(WARP ? wait_warp(&c->seg_full[i], parity, c, site)
              : wait(&c->seg_full[i], parity, c, site)))
     return false;
   g = c->seg[i];
-  if (WARP) __syncwarp();
-  if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&c->seg_empty[i]);
+  if (last) {
+    if (WARP) __syncwarp();
+    if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&c->seg_empty[i]);
+  }
   return true;
+}
+
+// A place in the list of key tiles of all segments; n = 0 in a segment without
+// any.
+template <bool WARP>
+struct Place {
+  Seg g;
+  uint32_t k = 0;         // segments taken
+  int32_t j = -1, n = 0;  // tile of n in the segment
+  bool more = true;       // false behind the last segment
+
+  __device__ __forceinline__ bool next(Ctrl* c, bool last, unsigned site) {
+    if (++j < n) return true;
+    if (!take_seg<WARP>(c, k, g, last, site)) return false;
+    ++k;
+    j = 0;
+    more = g.n[0] >= 0;
+    n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
+    return true;
+  }
+};
+
+// The order of the products, and of the loads for them. A tile's scores
+// (Q K^T, which need K) lead its values (P V, which need V) by one tile where
+// both streams take each tile (shared), by two where they take turns (split),
+// across segments of one kind. `ahead`: tiles that have scores but no values.
+// One step is the values of place p, or the scores of place q, or both;
+// neither where both stand at a segment without tiles. (q never looks past
+// such a segment: it would wait for entries that p has yet to let go of.)
+template <bool WARP>
+__device__ __forceinline__ void order(const Place<WARP>& p, const Place<WARP>& q, int ahead,
+                                      bool& values, bool& scores) {
+  const int lead = (ahead > 0 ? p.g.split : q.g.split) ? 2 : 1;
+  scores = q.more && q.n > 0 && (ahead == 0 || p.g.split == q.g.split);
+  values = ahead > 0 && (ahead >= lead || !scores);
 }
 
 template <int DP, bool PAGED>
@@ -568,9 +623,8 @@ __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
   }
 }
 
-// The loading warp: per segment the row tiles, then K and V in the order in
-// which the products take them: K leads V by one tile (shared) or two (split).
-// The pages of a load are looked up one load ahead.
+// The loading warp: row tiles, K and V in the order in which the products take
+// them. The pages of a load are looked up a step ahead.
 template <int DP, bool PAGED>
 __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorMap* qm1,
                      const CUtensorMap* km, const CUtensorMap* vm, Cta<DP> cta) {
@@ -584,61 +638,48 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
   const int boxes = (PAGED && a.page_size < kTile ? kTile >> a.page_log2 : 1) * L::kHalves;
   const int pi = lane / L::kHalves, h = lane % L::kHalves;
   const uint32_t to = h * L::kHalf + (PAGED ? pi * a.page_size * 128 : 0);
-  const auto page = [&](const Seg& g, int32_t t) -> int32_t {
+  const auto page = [&](const Place<true>& p) -> int32_t {
     if constexpr (PAGED) {
-      if (lane < boxes)
-        return page_of(a, g.seq, static_cast<int64_t>(t) * kTile + pi * a.page_size);
+      if (p.more && lane < boxes)
+        return page_of(a, p.g.seq,
+                       static_cast<int64_t>(p.g.t0 + p.j) * kTile + pi * a.page_size);
     }
     return 0;
   };
-  Seg g;
-  if (!take_seg<true>(c, 0, g, 17)) return;
-  int32_t id = g.n[0] < 0 ? 0 : page(g, g.t0);
+  Place<true> p, q;  // of the values and of the scores
+  if (!q.next(c, false, 17) || !p.next(c, true, 17)) return;
+  int ahead = 0;
+  int32_t p_id = page(p), q_id = p_id;
 #pragma unroll 1
-  for (uint32_t k = 1; g.n[0] >= 0; ++k) {
-    const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
+  while (p.more) {
+    bool values, scores;
+    order(p, q, ahead, values, scores);
     // Split segments take the two row-tile buffers in turn, so that the next
     // segment's rows load while this one's are in use; shared ones take both.
-    const int q_first = g.split ? turn++ & 1 : 0, q_count = !g.split && g.ntok[1] > 0 ? 2 : 1;
+    const int q_first = q.g.split ? turn & 1 : 0;
+    const int q_count = !scores || q.j > 0 ? 0 : !q.g.split && q.g.ntok[1] > 0 ? 2 : 1;
+    if (q_count > 0 && q.g.split) ++turn;
 #pragma unroll 1
-    for (int i = q_first; n > 0 && i < q_first + q_count; ++i) {
-      if ((used >> i) & 1) {
-        if (!wait_warp(&c->q_empty[i], (phase >> i) & 1, c, 18)) return;
-        phase ^= 1u << i;
+    for (int i = values ? 0 : 1; i < (scores ? 2 : 1); ++i) {  // V, then K
+      if (i == 1) {
+#pragma unroll 1
+        for (int r = q_first; r < q_first + q_count; ++r) {
+          if ((used >> r) & 1) {
+            if (!wait_warp(&c->q_empty[r], (phase >> r) & 1, c, 18)) return;
+            phase ^= 1u << r;
+          }
+          used |= 1u << r;
+          // a segment of one sequence needs that token's rows alone
+          const bool one = PAGED && q.g.seq >= 0;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&c->q_full[r],
+                                  L::kHalves * (one ? 1 : a.tile_tokens) * a.group * 128);
+          __syncwarp();
+          if (lane < L::kHalves)
+            tma_load3(cta.q(r) + lane * L::kHalf, one ? qm1 : qm, lane * 64, q.g.kh * a.group,
+                      q.g.tok[q.g.split ? 0 : r], &c->q_full[r]);
+        }
       }
-      used |= 1u << i;
-      // a segment of one sequence needs that token's rows alone
-      const bool one = PAGED && g.seq >= 0;
-      if (lane == 0)
-        mbar_arrive_expect_tx(&c->q_full[i],
-                              L::kHalves * (one ? 1 : a.tile_tokens) * a.group * 128);
-      __syncwarp();
-      if (lane < L::kHalves)
-        tma_load3(cta.q(i) + lane * L::kHalf, one ? qm1 : qm, lane * 64, g.kh * a.group,
-                  g.tok[g.split ? 0 : i], &c->q_full[i]);
-    }
-    // Load i: K for i < lead, then V_0, K_lead, V_1, K_lead+1, ..., and the
-    // last values.
-    const int32_t lead = min(n, g.split ? 2 : 1), pairs = 2 * (n - lead);
-    Seg next;
-    if (n == 0 && !take_seg<true>(c, k, next, 17)) return;
-#pragma unroll 1
-    for (int32_t i = 0; i < 2 * n; ++i) {
-      const auto tile = [&](int32_t i, bool& is_v) -> int32_t {
-        const int32_t u = i - lead;
-        if (u < 0) return is_v = false, i;
-        if (u >= pairs) return is_v = true, u - (n - lead);
-        is_v = (u & 1) == 0;
-        return is_v ? u / 2 : lead + u / 2;
-      };
-      bool is_v, next_v;
-      const int32_t t = g.t0 + tile(i, is_v);
-      // The next segment is taken early: its first pages are looked up under
-      // this one's last load.
-      if (i == 1 && !take_seg<true>(c, k, next, 17)) return;
-      int32_t id_next = 0;
-      if (i + 1 < 2 * n) id_next = page(g, g.t0 + tile(i + 1, next_v));
-      else if (next.n[0] >= 0) id_next = page(next, next.t0);
       const int st = ring.stage;
       if (ring.round > 0 && !wait_warp(&c->kv_empty[st], (ring.round - 1) & 1, c, 19)) return;
       ring.next();
@@ -646,16 +687,26 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
       __syncwarp();
       if (lane < boxes) {
         unsigned char* dst = cta.stage(st) + to;
-        const CUtensorMap* map = is_v ? vm : km;
+        const CUtensorMap* map = i == 0 ? vm : km;
+        const int32_t t = i == 0 ? p.g.t0 + p.j : q.g.t0 + q.j, kh = i == 0 ? p.g.kh : q.g.kh;
         if constexpr (PAGED)
-          tma_load4(dst, map, h * 64, g.kh, (t * kTile) & (a.page_size - 1), id, &c->kv_full[st]);
+          tma_load4(dst, map, h * 64, kh, (t * kTile) & (a.page_size - 1), i == 0 ? p_id : q_id,
+                    &c->kv_full[st]);
         else
-          tma_load3(dst, map, h * 64, g.kh, g.k0 + t * kTile, &c->kv_full[st]);
+          tma_load3(dst, map, h * 64, kh, (i == 0 ? p.g.k0 : q.g.k0) + t * kTile,
+                    &c->kv_full[st]);
       }
-      id = id_next;
     }
-    if (n == 0 && next.n[0] >= 0) id = page(next, next.t0);
-    g = next;
+    if (scores || !values) {  // q first: p lets go of the entries it takes
+      if (!q.next(c, false, 17)) return;
+      q_id = page(q);
+      ahead += scores;
+    }
+    if (values || !scores) {
+      if (!p.next(c, true, 17)) return;
+      p_id = page(p);
+      ahead -= values;
+    }
   }
   // The last arrivals of the products on these barriers come before the
   // shared memory is given back.
@@ -669,8 +720,8 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     if (((used >> i) & 1) && !wait_warp(&c->q_empty[i], (phase >> i) & 1, c, 18)) return;
 }
 
-// The thread that issues the products. In program order: for each key tile
-// the products P V of a stream, then the next Q K^T into the same columns.
+// The thread that issues the products. In program order: the values of a
+// stream's tile, then the scores of its next one into the same columns.
 template <typename T, int DP>
 __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
   using L = Layout<DP>;
@@ -686,12 +737,10 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
   uint32_t q_phase = 0, p_phase = 0, o_phase = 0, o_used = 0;
   uint32_t turn = 0;
 
-  const auto full = [&]() { return wait(&c->kv_full[ring.stage], ring.round & 1, c, 20); };
-  // Q K^T of stream s with the K tile in the ring's current stage
-  const auto scores = [&](int s, int q) {
-    tc_fence_after();
+  // Q K^T of stream s
+  const auto scores_of = [&](int s, int q, int stage) {
     const uint64_t qa = q0 + ((q * L::kBytes) >> 4);
-    const uint64_t kb = k0 + ((ring.stage * L::kBytes) >> 4);
+    const uint64_t kb = k0 + ((stage * L::kBytes) >> 4);
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const uint64_t off = ((i / 4) * L::kHalf + (i % 4) * 32) >> 4;
@@ -699,8 +748,8 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
     }
     mma_commit(&c->s_full[s]);
   };
-  // P V of stream s with the V tile in the ring's current stage
-  const auto values = [&](int s, bool first) -> bool {
+  // P V of stream s
+  const auto values_of = [&](int s, bool first, int stage) -> bool {
     if (first) {
       if ((o_used >> s) & 1) {
         if (!wait(&c->o_free[s], (o_phase >> s) & 1, c, 22)) return false;
@@ -708,7 +757,7 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
       }
       o_used |= 1u << s;
     }
-    const uint64_t vb = v0 + ((ring.stage * L::kBytes) >> 4);
+    const uint64_t vb = v0 + ((stage * L::kBytes) >> 4);
     const uint32_t o = tmem + 2 * kTile + s * kTile, w = tmem + s * kTile;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
@@ -725,61 +774,62 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
     return true;
   };
 
+  Place<false> p, q;  // of the values and of the scores
+  if (!q.next(c, false, 23) || !p.next(c, true, 23)) return;
+  int ahead = 0;
+  int rows = 0;  // first row-tile buffer of q's segment
 #pragma unroll 1
-  for (uint32_t k = 0;; ++k) {
-    Seg g;
-    if (!take_seg<false>(c, k, g, 23) || g.n[0] < 0) return;
-    const int32_t n = g.split ? g.n[0] + g.n[1] : max(g.n[0], g.n[1]);
-    const int q_first = g.split ? turn++ & 1 : 0, q_count = !g.split && g.ntok[1] > 0 ? 2 : 1;
-    if (n == 0) continue;
+  while (p.more) {
+    bool values, scores;
+    order(p, q, ahead, values, scores);
+    const int q_count = !q.g.split && q.g.ntok[1] > 0 ? 2 : 1;
+    if (scores && q.j == 0) {
+      rows = q.g.split ? turn++ & 1 : 0;
 #pragma unroll 1
-    for (int i = q_first; i < q_first + q_count; ++i) {
-      if (!wait(&c->q_full[i], (q_phase >> i) & 1, c, 24)) return;
-      q_phase ^= 1u << i;
+      for (int i = rows; i < rows + q_count; ++i) {
+        if (!wait(&c->q_full[i], (q_phase >> i) & 1, c, 24)) return;
+        q_phase ^= 1u << i;
+      }
     }
-    const auto drop_rows = [&]() {
-#pragma unroll 1
-      for (int i = q_first; i < q_first + q_count; ++i) mma_commit(&c->q_empty[i]);
-    };
-    // Step j: with V_j, and with K_{j + lead} behind it. Steps before 0 have
-    // no values yet.
-    const int32_t lead = g.split ? 2 : 1;
-#pragma unroll 1
-    for (int32_t j = -lead; j < n; ++j) {
-      // shared: both streams take every tile; split: they take turns
-      const int s0 = g.split ? (j & 1) ^ g.first : 0, s1 = g.split ? s0 + 1 : 2;
-      const bool more = j + lead < n;
-      Ring<DP> v = ring, kn = ring;
-      if (j >= 0) {
-        if (!full()) return;
-        kn.next();
-      }
-      bool have = false;
-      // unrolled: the issuing thread is on the way of every product (prompts
-      // lose 8% with one copy for both streams)
+    const Ring<DP> v = ring;
+    if (values) {
+      if (!wait(&c->kv_full[ring.stage], ring.round & 1, c, 20)) return;
+      ring.next();
+    }
+    bool have = false;
+    // streams of the two tiles: shared ones go to both, as far as these see
+    // the tile; split ones take turns. Unrolled: the issuing thread is on the
+    // way of every product (prompts lose 8% with one copy for both streams).
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s < s0 || s >= s1) continue;
-        if (j >= 0) {
-          ring = v;
-          if (g.split || j < g.n[s]) {
-            if (!values(s, j < lead)) return;
-          }
-          if (s + 1 == s1) mma_commit(&c->kv_empty[v.stage]);
+    for (int s = 0; s < 2; ++s) {
+      if (values) {
+        if (p.g.split ? ((p.j & 1) ^ p.g.first) == s : p.j < p.g.n[s]) {
+          if (!values_of(s, p.j < (p.g.split ? 2 : 1), v.stage)) return;
         }
-        if (g.split ? more : j + 1 < g.n[s]) {
-          ring = kn;
-          if (!have && !full()) return;
-          have = true;
-          scores(s, g.split ? q_first : s);
-        }
+        if (s == 1) mma_commit(&c->kv_empty[v.stage]);
       }
-      ring = kn;
-      if (more) {
-        mma_commit(&c->kv_empty[ring.stage]);
-        ring.next();
-        if (j + lead + 1 == n) drop_rows();
+      if (scores && (q.g.split ? ((q.j & 1) ^ q.g.first) == s : q.j < q.g.n[s])) {
+        if (!have && !wait(&c->kv_full[ring.stage], ring.round & 1, c, 20)) return;
+        have = true;
+        tc_fence_after();
+        scores_of(s, q.g.split ? rows : s, ring.stage);
       }
+    }
+    if (scores) {
+      mma_commit(&c->kv_empty[ring.stage]);
+      ring.next();
+      if (q.j + 1 == q.n) {
+#pragma unroll 1
+        for (int i = rows; i < rows + q_count; ++i) mma_commit(&c->q_empty[i]);
+      }
+    }
+    if (scores || !values) {
+      if (!q.next(c, false, 23)) return;
+      ahead += scores;
+    }
+    if (values || !scores) {
+      if (!p.next(c, true, 23)) return;
+      ahead -= values;
     }
   }
 }
@@ -798,7 +848,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     Seg g;
-    if (!take_seg<true>(c, k, g, 25) || g.n[0] < 0) return;
+    if (!take_seg<true>(c, k, g, true, 25) || g.n[0] < 0) return;
     const int qs = g.split ? 0 : s;
     const int32_t n = g.n[s];
     const bool valid = rt < g.ntok[qs];  // ntok <= tile_tokens
@@ -914,14 +964,15 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     const int32_t head = g.kh * a.group + head0;
     T* out = nullptr;
     float *part = nullptr, *lse_at = nullptr;
+    const int step = PAGED && g.seq < 0 ? 4 * kTile : 4;  // from four values to the next
     if (valid) {
       if constexpr (PAGED) {
         if (g.seq < 0) {
-          const int64_t r = g.slot * 256 + (s ^ g.first) * kTile + row;
-          part = a.prefix_o + r * DP;
-          lse_at = a.prefix_lse + r;
+          const int64_t r = g.slot * 256ll + (s ^ g.first) * kTile;
+          part = a.prefix_o + r * DP + row * 4;
+          lse_at = a.prefix_lse + r + row;
         } else {
-          const int64_t r = (g.slot * 2 + (s ^ g.first)) * a.group + row;
+          const int64_t r = (g.slot * 2ll + (s ^ g.first)) * a.group + row;
           part = a.own_o + r * DP;
           lse_at = a.own_lse + r;
         }
@@ -951,7 +1002,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
         if (part) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(part + b + j) =
+            *reinterpret_cast<float4*>(part + (b + j) / 4 * step) =
                 make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       } else {
@@ -992,7 +1043,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       for (int e = 0; e < 4; ++e) {
         const int d = lane + 32 * e;
         if (d < a.dim) {
-          if constexpr (PAGED) fpart[d] = acc[e];
+          if constexpr (PAGED) fpart[d / 4 * step + d % 4] = acc[e];
           else fout[d] = from_f<T>(acc[e]);
         }
       }
@@ -1105,33 +1156,39 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t b = r / a.heads;
   const int32_t h = static_cast<int32_t>(r - b * a.heads), kh = h / a.group, e = h - kh * a.group;
   const int32_t pre = PagedSchedule::units(a), from = a.starts[b], upto = a.starts[b + 1];
-  const int32_t share = PagedSchedule::share_of(pre + a.starts[a.tokens], j.grid);
+  const int32_t share = PagedSchedule::share_of(a, pre + a.starts[a.tokens], j.grid);
   // Partial i < np: prefix; np <= i < np + no: own. In both the segments of
   // one group have consecutive slots, each with one or two partials.
   int64_t p0 = 0, o0 = 0;
-  int32_t np = 0, no = 0;
+  int32_t np = 0, no = 0, prow = 0;
   if (a.prefix_tiles > 0) {
     const int32_t block = (a.prefix_split ? 1 : 2) * a.tile_tokens, bi = static_cast<int32_t>(b);
     const int32_t rb = bi / block, in = bi - rb * block, pg = kh * a.prefix_blocks + rb;
-    const int32_t u = pg * (a.prefix_tiles + kSegCost) + kSegCost;
-    const int32_t c0 = u / share, c1 = (u + a.prefix_tiles - 1) / share;
+    const int32_t u = pg * PagedSchedule::prefix_group(a) + kSegCost;
+    const int32_t c0 = u / share,
+                  c1 = (u + (a.prefix_tiles - 1) * PagedSchedule::prefix_cost(a)) / share;
     const int32_t s = in >= a.tile_tokens;
     np = (c1 - c0 + 1) << a.prefix_split;
-    p0 = static_cast<int64_t>(pg + c0) * 256 + s * kTile + (in - s * a.tile_tokens) * a.group + e;
+    p0 = static_cast<int64_t>(pg + c0) * 256 + s * kTile;
+    prow = (in - s * a.tile_tokens) * a.group + e;
   }
   if (upto > from) {
     const int32_t per = (upto - from) / a.kv_heads, u = pre + from + kh * per + kSegCost;
-    const int32_t c0 = u / share, c1 = (u + per - kSegCost - 1) / share;
+    const int32_t c0 = u / share, c1 = (u + per - kSegCost - kTileCost) / share;
     no = (c1 - c0 + 1) * 2;
     o0 = (b * a.kv_heads + kh + c0) * 2 * a.group + e;
   }
-  const auto at = [&](int32_t i) -> int64_t {  // row of partial i in its buffer
-    if (i < np) return p0 + (a.prefix_split ? static_cast<int64_t>(i) * kTile : i * 256ll);
+  // Prefix partials: tiles of 128 rows, [DP / 4][128][4] each; own ones: rows.
+  const auto tile_at = [&](int32_t i) -> int64_t {
+    return p0 + (a.prefix_split ? i * 128ll : i * 256ll);
+  };
+  const auto row_of = [&](int32_t i) -> int64_t {
     return o0 + static_cast<int64_t>(i - np) * a.group;
   };
   const int32_t all = np + no;
   const auto lse_of = [&](int32_t i) {
-    return i >= all ? neg_inf() : i < np ? a.prefix_lse[at(i)] : a.own_lse[at(i)];
+    return i >= all ? neg_inf()
+                    : i < np ? a.prefix_lse[tile_at(i) + prow] : a.own_lse[row_of(i)];
   };
   // Lane i keeps the log-sum-exp of partial i; more than 32 are read again.
   const float held = lse_of(lane);
@@ -1159,7 +1216,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll 8
     for (int32_t i = 0; i < n; ++i) {
       const float wi = __shfl_sync(~0u, w, i);
-      const float* o = (i0 + i < np ? a.prefix_o : a.own_o) + at(i0 + i) * DP + lane * kPer;
+      const int32_t d = lane * kPer;
+      const float* o = i0 + i < np
+                           ? a.prefix_o + tile_at(i0 + i) * DP + (d / 4 * kTile + prow) * 4 + d % 4
+                           : a.own_o + row_of(i0 + i) * DP + d;
       const Vec v = *reinterpret_cast<const Vec*>(o);
       acc[0] = fmaf(wi, v.x, acc[0]);
       acc[1] = fmaf(wi, v.y, acc[1]);

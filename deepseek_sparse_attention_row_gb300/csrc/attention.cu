@@ -160,9 +160,8 @@ PagedPlan plan_paged(int64_t batch, int32_t heads, int32_t kv_heads, int32_t hea
   p.prefix_blocks = static_cast<int32_t>((batch + block - 1) / block);
   const int64_t groups = static_cast<int64_t>(kv_heads) * p.prefix_blocks;
   const int64_t own_tiles = (max_pages * page_size - prefix_len + kTile - 1) / kTile;
-  const int64_t most = groups * (p.prefix_tiles + kSegCost) +
-                       batch * kv_heads * (own_tiles + kSegCost);
-  p.fits = most <= INT32_MAX - 1024;
+  const int64_t most = groups * p.prefix_tiles + batch * kv_heads * own_tiles;
+  p.fits = most <= INT32_MAX / (kTwoTileCost + kSegCost) - 1024;
   const int64_t sms = sm_count();
   p.grid = static_cast<int>(most < 1 ? 1 : (most < sms ? most : sms));
   const size_t pslots = p.prefix_tiles > 0 ? groups + p.grid : 0;

@@ -85,6 +85,16 @@ def test_prompt_wide_groups(env, heads, kv_heads, dim):
     check_prompt(env, q, k, v, [20, 3], [147, 3], True)
 
 
+def test_prompt_runs_of_sequences_without_keys(env):
+    """More of them in a row than a CTA plans ahead, between others."""
+    torch, _ = env
+    ql = [40] + [9] * 4000 + [130] + [1] * 30 + [20]
+    kl = [40] + [0] * 4000 + [130] + [0] * 30 + [25]
+    q, k, v = make(torch, 21, sum(ql), sum(kl), 2, 1, 64, torch.bfloat16)
+    check_prompt(env, q, k, v, ql, kl, True)
+    check_prompt(env, q, k, v, ql, kl, False)
+
+
 def test_prompt_longer_keys(env):
     """Many key tiles per row, so that the running maximum moves often."""
     torch, _ = env
@@ -273,6 +283,15 @@ def test_shared_sweep(env, case, dtype):
     batch, heads, kv_heads, dim, page, prefix, own = case
     t = make_paged(torch, dim + page, *case, getattr(torch, dtype))
     check_paged(env, *t, prefix)
+
+
+def test_shared_many_short_sequences(env):
+    """Several segments per CTA, most of one tile, every third one empty."""
+    torch, _ = env
+    own = [0 if i % 3 == 0 else 1 + (i * 53) % 260 for i in range(700)]
+    t = make_paged(torch, 24, 700, 4, 2, 64, 16, 32, own, torch.bfloat16)
+    check_paged(env, *t, 32)
+    check_paged(env, *t, 0)
 
 
 def test_shared_prefix_is_only_a_matter_of_speed(env):
