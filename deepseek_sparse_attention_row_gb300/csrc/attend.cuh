@@ -721,35 +721,43 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
 }
 
 // The thread that issues the products. In program order: the values of a
-// stream's tile, then the scores of its next one into the same columns.
-template <typename T, int DP>
-__device__ void multiply(Cta<DP> cta, uint32_t tmem) {
+// stream's tile, then the scores of its next one into the same columns. It is
+// on the way of every product, so that its loops are kept short: one for
+// segments of two row tiles, with both streams written out (one copy for both,
+// or the steps of order() here, cost prompts 8 to 13%), one for runs of split
+// segments.
+template <typename T, int DP, bool PAGED>
+__device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
   using L = Layout<DP>;
   Ctrl* c = cta.ctrl();
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
-  constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
+  // The products stop at the head dimension, in steps of 16.
+  const int steps = (a.dim + 15) / 16;
+  const uint32_t shape_o = mma_shape(kBf16, 16 * steps, true);
   const uint64_t q0 = operand(smem_addr(cta.q(0)), 16, 1024);
   const uint64_t k0 = operand(smem_addr(cta.stage(0)), 16, 1024);
   const uint64_t v0 = operand(smem_addr(cta.stage(0)), L::kHalf, 1024);
   Ring<DP> ring;
   // Bit s (or i): parities of the next waits, and whether O_s was used before.
   uint32_t q_phase = 0, p_phase = 0, o_phase = 0, o_used = 0;
-  uint32_t turn = 0;
 
+  const auto full = [&]() { return wait(&c->kv_full[ring.stage], ring.round & 1, c, 20); };
   // Q K^T of stream s
-  const auto scores_of = [&](int s, int q, int stage) {
+  const auto scores = [&](int s, int q, int stage) {
+    tc_fence_after();
     const uint64_t qa = q0 + ((q * L::kBytes) >> 4);
     const uint64_t kb = k0 + ((stage * L::kBytes) >> 4);
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const uint64_t off = ((i / 4) * L::kHalf + (i % 4) * 32) >> 4;
-      mma_ss(tmem + s * kTile, qa + off, kb + off, kShapeS, i > 0);
+      if (i < (DP == 128 ? 5 : 1) || i < steps)
+        mma_ss(tmem + s * kTile, qa + off, kb + off, kShapeS, i > 0);
     }
     mma_commit(&c->s_full[s]);
   };
   // P V of stream s
-  const auto values_of = [&](int s, bool first, int stage) -> bool {
+  const auto values = [&](int s, bool first, int stage) -> bool {
     if (first) {
       if ((o_used >> s) & 1) {
         if (!wait(&c->o_free[s], (o_phase >> s) & 1, c, 22)) return false;
@@ -766,7 +774,7 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
       constexpr int kSteps = kTile / 16 / kParts;
 #pragma unroll
       for (int e = 0; e < kSteps; ++e)
-        mma_ts(o, w + (p * kSteps + e) * 8, vb + (((p * kSteps + e) * 2048) >> 4), kShapeO,
+        mma_ts(o, w + (p * kSteps + e) * 8, vb + (((p * kSteps + e) * 2048) >> 4), shape_o,
                !first || p > 0 || e > 0);
     }
     p_phase ^= 1u << s;
@@ -774,62 +782,93 @@ __device__ void multiply(Cta<DP> cta, uint32_t tmem) {
     return true;
   };
 
-  Place<false> p, q;  // of the values and of the scores
-  if (!q.next(c, false, 23) || !p.next(c, true, 23)) return;
-  int ahead = 0;
-  int rows = 0;  // first row-tile buffer of q's segment
+  Place<false> p;
+  if (!p.next(c, true, 23)) return;
+  uint32_t turn = 0;
 #pragma unroll 1
   while (p.more) {
-    bool values, scores;
-    order(p, q, ahead, values, scores);
-    const int q_count = !q.g.split && q.g.ntok[1] > 0 ? 2 : 1;
-    if (scores && q.j == 0) {
-      rows = q.g.split ? turn++ & 1 : 0;
+    if (!PAGED || !p.g.split) {
+      const Seg& g = p.g;
+      const int32_t n = p.n;
+      const int tiles = g.ntok[1] > 0 ? 2 : 1;
+      if (n > 0) {
 #pragma unroll 1
-      for (int i = rows; i < rows + q_count; ++i) {
-        if (!wait(&c->q_full[i], (q_phase >> i) & 1, c, 24)) return;
-        q_phase ^= 1u << i;
-      }
-    }
-    const Ring<DP> v = ring;
-    if (values) {
-      if (!wait(&c->kv_full[ring.stage], ring.round & 1, c, 20)) return;
-      ring.next();
-    }
-    bool have = false;
-    // streams of the two tiles: shared ones go to both, as far as these see
-    // the tile; split ones take turns. Unrolled: the issuing thread is on the
-    // way of every product (prompts lose 8% with one copy for both streams).
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (values) {
-        if (p.g.split ? ((p.j & 1) ^ p.g.first) == s : p.j < p.g.n[s]) {
-          if (!values_of(s, p.j < (p.g.split ? 2 : 1), v.stage)) return;
+        for (int i = 0; i < tiles; ++i) {
+          if (!wait(&c->q_full[i], (q_phase >> i) & 1, c, 24)) return;
+          q_phase ^= 1u << i;
         }
-        if (s == 1) mma_commit(&c->kv_empty[v.stage]);
+        if (!full()) return;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (g.n[s] > 0) scores(s, s, ring.stage);
+        mma_commit(&c->kv_empty[ring.stage]);
+        ring.next();
       }
-      if (scores && (q.g.split ? ((q.j & 1) ^ q.g.first) == s : q.j < q.g.n[s])) {
-        if (!have && !wait(&c->kv_full[ring.stage], ring.round & 1, c, 20)) return;
-        have = true;
-        tc_fence_after();
-        scores_of(s, q.g.split ? rows : s, ring.stage);
-      }
-    }
-    if (scores) {
-      mma_commit(&c->kv_empty[ring.stage]);
-      ring.next();
-      if (q.j + 1 == q.n) {
 #pragma unroll 1
-        for (int i = rows; i < rows + q_count; ++i) mma_commit(&c->q_empty[i]);
+      for (int32_t j = 0; j < n; ++j) {
+        // V_j in the current stage, K_{j+1} in the next one
+        if (j + 1 == n) {
+#pragma unroll 1
+          for (int i = 0; i < tiles; ++i) mma_commit(&c->q_empty[i]);
+        }
+        if (!full()) return;
+        const int v = ring.stage;
+        ring.next();
+        bool have = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (j < g.n[s]) {
+            if (!values(s, j == 0, v)) return;
+          }
+          if (s == 1) mma_commit(&c->kv_empty[v]);
+          if (j + 1 < g.n[s]) {
+            if (!have && !full()) return;
+            have = true;
+            scores(s, s, ring.stage);
+          }
+        }
+        if (j + 1 < n) {
+          mma_commit(&c->kv_empty[ring.stage]);
+          ring.next();
+        }
       }
-    }
-    if (scores || !values) {
-      if (!q.next(c, false, 23)) return;
-      ahead += scores;
-    }
-    if (values || !scores) {
+      p.j = n;
       if (!p.next(c, true, 23)) return;
-      ahead -= values;
+      continue;
+    }
+    // A run of split segments: scores at place q, two tiles before the values
+    // at p, the streams taking turns.
+    Place<false> q = p;
+    int ahead = 0, rows = 0;
+#pragma unroll 1
+    for (;;) {
+      const bool more = q.more && q.g.split, late = ahead == 2 || !more;
+      if (late) {
+        if (ahead == 0) break;
+        if (!full()) return;
+        const int v = ring.stage;
+        ring.next();
+        if (!values((p.j & 1) ^ p.g.first, p.j < 2, v)) return;
+        mma_commit(&c->kv_empty[v]);
+      }
+      if (more) {
+        if (q.j == 0) {
+          rows = turn++ & 1;
+          if (!wait(&c->q_full[rows], (q_phase >> rows) & 1, c, 24)) return;
+          q_phase ^= 1u << rows;
+        }
+        if (!full()) return;
+        scores((q.j & 1) ^ q.g.first, rows, ring.stage);
+        mma_commit(&c->kv_empty[ring.stage]);
+        ring.next();
+        if (q.j + 1 == q.n) mma_commit(&c->q_empty[rows]);
+        if (!q.next(c, false, 23)) return;
+        ++ahead;
+      }
+      if (late) {
+        if (!p.next(c, true, 23)) return;
+        --ahead;
+      }
     }
   }
 }
@@ -1110,7 +1149,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   } else {
     reg_shrink<72>();
     if (warp == 8) {
-      if (elect_one()) multiply<T, DP>(cta, tmem);
+      if (elect_one()) multiply<T, DP, PAGED>(a, cta, tmem);
     } else if (warp == 9) {
       load<DP, PAGED>(a, &qm, &q1, &km, &vm, cta);
     } else if (warp == 10) {
