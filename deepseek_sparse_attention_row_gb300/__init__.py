@@ -40,6 +40,7 @@ the device first.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -557,62 +558,73 @@ DTYPE_F16 = 2
 class _Launch:
     """One call's device and stream: the tensors' device made current, and
     (for a given ``stream``) that stream, so that what the call allocates
-    belongs to the stream that it runs on."""
+    belongs to the stream that it runs on. ``_launch`` makes none for the
+    usual call, on the current stream of the current device."""
 
-    def __init__(self, device, stream):
+    def __init__(self, index, stream):
         torch = _torch()
-        self._guards = []
-        if device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
+        self._guards = [torch.cuda.device(index)]
         if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
             self._guards.append(torch.cuda.stream(stream))
-        self._stream = stream
-        self._device = device
 
     def __enter__(self):
         for g in self._guards:
             g.__enter__()
-        s = self._stream
-        if s is None:
-            s = _torch().cuda.current_stream(self._device)
-        return s.cuda_stream or None
 
     def __exit__(self, *exc):
         for g in reversed(self._guards):
             g.__exit__(*exc)
 
 
-def _on_gpu(t, dtype, name, dim, device=None):
-    """Device address of a CUDA tensor of the given type, rank and device."""
+_here = contextlib.nullcontext()
+
+
+def _launch(index: int, stream):
+    torch = _torch()
+    if stream is None and index == torch._C._cuda_getDevice():
+        return _here
+    return _Launch(index, stream)
+
+
+def _current_handle(index: int):
+    """The current stream of a device, as the C calls take it."""
+    return _torch()._C._cuda_getCurrentRawStream(index) or None
+
+
+def _on_gpu(t, dtype, name, dim, index=None):
+    """Address, shape and strides of a CUDA tensor of the given type and rank
+    on device ``index``."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr() or None
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {tuple(shape)}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return t.data_ptr() or None, shape, t.stride()
 
 
-def _rows_of(t, name):
+def _row_strides(shape, strides, name):
     """Strides of all dimensions but the last, which has unit stride. A
     dimension of one element is never stepped over: any stride will do."""
-    last = t.shape[-1]
-    if last > 1 and t.stride(-1) != 1:
+    last = shape[-1]
+    if strides[-1] != 1 and last > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return [st if n > 1 else last for n, st in zip(t.shape[:-1], t.stride()[:-1])]
+    if 1 in shape[:-1]:
+        return tuple(st if n != 1 else last for n, st in zip(shape[:-1], strides[:-1]))
+    return strides[:-1]
 
 
-def _vector(t, name, device):
+def _vector(t, name, index):
     """Address and length of a contiguous int32 vector."""
-    torch = _torch()
-    ptr = _on_gpu(t, torch.int32, name, 1, device)
-    if t.shape[0] > 1 and t.stride(0) != 1:
+    ptr, (n,), (st,) = _on_gpu(t, _torch().int32, name, 1, index)
+    if st != 1 and n > 1:
         raise ValueError(f"{name} must be contiguous")
-    return ptr, t.shape[0]
+    return ptr, n
 
 
 def _attention_dtype(t, name):
@@ -624,20 +636,24 @@ def _attention_dtype(t, name):
     raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
 
 
-def _attention_outputs(q, out, lse_out):
+def _attention_outputs(q, shape, index, out, lse_out):
     """Output tensors (allocated when None) and their addresses and strides."""
     torch = _torch()
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse_out is None:
-        lse_out = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    elif lse_out.shape != q.shape[:2]:
-        raise ValueError(f"lse_out must be {tuple(q.shape[:2])}, got {tuple(lse_out.shape)}")
-    args = (_on_gpu(out, q.dtype, "out", 3, q.device), *_rows_of(out, "out"),
-            _on_gpu(lse_out, torch.float32, "lse_out", 2, q.device), *lse_out.stride())
-    return out, lse_out, args
+        lse_out = q.new_empty(shape[:2], dtype=torch.float32)
+    op, oshape, ost = _on_gpu(out, q.dtype, "out", 3, index)
+    lp, lshape, lst = _on_gpu(lse_out, torch.float32, "lse_out", 2, index)
+    if oshape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(oshape)}")
+    if lshape != shape[:2]:
+        raise ValueError(f"lse_out must be {tuple(shape[:2])}, got {tuple(lshape)}")
+    return out, lse_out, (op, *_row_strides(oshape, ost, "out"), lp, *lst)
+
+
+def _scale(scale, dim):
+    return (dim ** -0.5 if dim else 1.0) if scale is None else float(scale)
 
 
 def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None, out=None,
@@ -654,24 +670,23 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
     no sequence are left as they were. Forward only: the outputs carry no
     autograd graph."""
     code = _attention_dtype(q, "q")
-    dev = q.device
-    qp = _on_gpu(q, q.dtype, "q", 3)
-    kp, vp = _on_gpu(k, q.dtype, "k", 3, dev), _on_gpu(v, q.dtype, "v", 3, dev)
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} "
-                         "do not match")
+    dt, dev = q.dtype, q.get_device()
+    qp, qs, qst = _on_gpu(q, dt, "q", 3)
+    kp, ks, kst = _on_gpu(k, dt, "k", 3, dev)
+    vp, vs, vst = _on_gpu(v, dt, "v", 3, dev)
+    if ks != vs or ks[2] != qs[2]:
+        raise ValueError(f"q {tuple(qs)}, k {tuple(ks)} and v {tuple(vs)} do not match")
     (cq, nq), (ck, nk) = _vector(cu_q, "cu_q", dev), _vector(cu_k, "cu_k", dev)
     if nq != nk or nq < 1:
         raise ValueError(f"cu_q and cu_k must have one length of at least 1, got {nq} and {nk}")
-    D = q.shape[2]
-    scale = D ** -0.5 if scale is None and D else scale or 0.0
-    with _Launch(dev, stream) as handle:
-        out, lse_out, outs = _attention_outputs(q, out, lse_out)
+    with _launch(dev, stream):
+        out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         st = library().dsa_prompt_attention(
-            qp, kp, vp, code, q.shape[0], k.shape[0], q.shape[1], k.shape[1], D,
-            *_rows_of(q, "q"), *_rows_of(k, "k"), *_rows_of(v, "v"), cq, ck, nq - 1,
-            int(bool(causal)), scale, *outs, handle)
-    _check("dsa_prompt_attention", st)
+            qp, kp, vp, code, qs[0], ks[0], qs[1], ks[1], qs[2], *_row_strides(qs, qst, "q"),
+            *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cq, ck, nq - 1,
+            1 if causal else 0, _scale(scale, qs[2]), *outs, _current_handle(dev))
+    if st:
+        _check("dsa_prompt_attention", st)
     return out, lse_out
 
 
@@ -694,22 +709,20 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
     uses (allocated when None)."""
     torch = _torch()
     code = _attention_dtype(q, "q")
-    dev = q.device
-    qp = _on_gpu(q, q.dtype, "q", 3)
-    kp = _on_gpu(k_pages, q.dtype, "k_pages", 4, dev)
-    vp = _on_gpu(v_pages, q.dtype, "v_pages", 4, dev)
-    tp = _on_gpu(tables, torch.int32, "tables", 2, dev)
+    dt, dev = q.dtype, q.get_device()
+    qp, (B, H, D), qst = _on_gpu(q, dt, "q", 3)
+    kp, ks, kst = _on_gpu(k_pages, dt, "k_pages", 4, dev)
+    vp, vs, vst = _on_gpu(v_pages, dt, "v_pages", 4, dev)
+    tp, (Bt, P), tst = _on_gpu(tables, torch.int32, "tables", 2, dev)
     lp, n = _vector(lens, "lens", dev)
-    B, H, D = q.shape
-    N, page, Hkv, _ = k_pages.shape
-    if k_pages.shape != v_pages.shape or k_pages.shape[3] != D:
-        raise ValueError(f"q {tuple(q.shape)}, k_pages {tuple(k_pages.shape)} and v_pages "
-                         f"{tuple(v_pages.shape)} do not match")
-    if n != B or tables.shape[0] != B:
+    N, page, Hkv, Dk = ks
+    if ks != vs or Dk != D:
+        raise ValueError(f"q {tuple(q.shape)}, k_pages {tuple(ks)} and v_pages {tuple(vs)} do "
+                         "not match")
+    if n != B or Bt != B:
         raise ValueError(f"tables {tuple(tables.shape)} and lens {tuple(lens.shape)} do not "
                          f"match q {tuple(q.shape)}")
-    P = tables.shape[1]
-    if P > 1 and tables.stride(1) != 1:
+    if P > 1 and tst[1] != 1:
         raise ValueError("tables must have unit stride in its last dimension")
     prefix_len = int(prefix_len)
     pp = None
@@ -721,81 +734,84 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
             if page > 0 and n < prefix_len // page:
                 raise ValueError(f"prefix_pages holds {n} pages, prefix_len {prefix_len} needs "
                                  f"{prefix_len // page}")
-    scale = D ** -0.5 if scale is None and D else scale or 0.0
-    with _Launch(dev, stream) as handle:
-        out, lse_out, outs = _attention_outputs(q, out, lse_out)
-        need = shared_prefix_workspace_bytes(B, H, Hkv, D, prefix_len, P, page)
-        ws, ws_bytes = _scratch(workspace, need, dev)
+    with _launch(dev, stream):
+        out, lse_out, outs = _attention_outputs(q, q.shape, dev, out, lse_out)
+        held, ws, ws_bytes = _scratch(
+            workspace, shared_prefix_workspace_bytes(B, H, Hkv, D, prefix_len, P, page), q)
         st = library().dsa_shared_prefix_attention(
-            qp, kp, vp, code, B, H, Hkv, D, N, page, *_rows_of(q, "q"),
-            *_rows_of(k_pages, "k_pages"), *_rows_of(v_pages, "v_pages"), pp, prefix_len, tp, P,
-            tables.stride(0) if B > 1 else P, lp, scale, *outs,
-            ws.data_ptr() if ws_bytes else None, ws_bytes, handle)
-    _check("dsa_shared_prefix_attention", st)
+            qp, kp, vp, code, B, H, Hkv, D, N, page, *_row_strides((B, H, D), qst, "q"),
+            *_row_strides(ks, kst, "k_pages"), *_row_strides(vs, vst, "v_pages"), pp, prefix_len,
+            tp, P, tst[0] if B > 1 else P, lp, _scale(scale, D), *outs, ws, ws_bytes,
+            _current_handle(dev))
+    if st:
+        _check("dsa_shared_prefix_attention", st)
     return out, lse_out
 
 
 def shared_prefix_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int,
                                   prefix_len: int, max_pages: int, page_size: int) -> int:
     """Bytes of workspace of a ``dsa_shared_prefix_attention`` call."""
-    return int(library().dsa_shared_prefix_workspace_bytes(batch, heads, kv_heads, head_dim,
-                                                           prefix_len, max_pages, page_size))
+    return library().dsa_shared_prefix_workspace_bytes(batch, heads, kv_heads, head_dim,
+                                                       prefix_len, max_pages, page_size)
 
 
-def _scratch(workspace, need: int, device):
-    """A call's workspace and its bytes: the caller's tensor, or a new one.
-    A new one comes from the allocator of the current stream (of the graph,
-    in a capture), which hands its memory on only behind this call."""
-    torch = _torch()
+def _scratch(workspace, need: int, like):
+    """A call's workspace, held until the call is enqueued, with its address
+    and bytes: the caller's tensor, or a new one on ``like``'s device. A new
+    one comes from the allocator of the current stream (of the graph, in a
+    capture), which hands its memory on only behind this call."""
     if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+        if not need:
+            return None, None, 0
+        workspace = like.new_empty(need, dtype=_torch().uint8)
+        return workspace, workspace.data_ptr(), need
+    if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    n = workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr() if n else None, n
 
 
 FORK_OK, FORK_NO_PAGE, FORK_REFUSED = 0, 1, 2
 
 
-def _cache_state(refs, tables, lens, device=None):
+def _cache_state(refs, tables, lens):
     """Arguments that describe refs, tables and lens, and their device."""
-    torch = _torch()
-    tp = _on_gpu(tables, torch.int32, "tables", 2, device)
-    dev = tables.device
+    tp, (S, P), (ld, one) = _on_gpu(tables, _torch().int32, "tables", 2)
+    dev = tables.get_device()
     rp, pages = _vector(refs, "refs", dev)
-    S, P = tables.shape
-    if P > 1 and tables.stride(1) != 1:
+    if P > 1 and one != 1:
         raise ValueError("tables must have unit stride in its last dimension")
-    if S > 1 and tables.stride(0) < P:
+    if S > 1 and ld < P:
         raise ValueError("rows of tables must not overlap")
     lp = None
     if lens is not None:
         lp, n = _vector(lens, "lens", dev)
         if n != S:
             raise ValueError(f"lens holds {n} lengths, tables {S} rows")
-    return rp, pages, tp, S, P, tables.stride(0) if S > 1 else P, lp, dev
+    return rp, pages, tp, S, P, ld if S > 1 else P, lp, dev
 
 
-def _cache_planes(cache, pages):
+def _cache_planes(cache, pages, index=None):
     """Arguments that describe the page contents [planes, N, page, ...]."""
     if not cache.is_cuda:
         raise ValueError("cache must be a CUDA tensor")
-    if cache.dim() < 3 or cache.shape[1] != pages:
-        raise ValueError(f"cache must be [planes, {pages}, page, ...], got {tuple(cache.shape)}")
-    e = cache.element_size()
-    token = e
-    for n, st in zip(reversed(cache.shape[3:]), reversed(cache.stride()[3:])):
-        if n > 1 and st * e != token:
+    shape, strides, e = cache.shape, cache.stride(), cache.element_size()
+    if index is not None and cache.get_device() != index:
+        raise ValueError(f"cache is on {cache.device}, expected cuda:{index}")
+    if len(shape) < 3 or shape[1] != pages:
+        raise ValueError(f"cache must be [planes, {pages}, page, ...], got {tuple(shape)}")
+    inner = 1
+    for d in range(len(shape) - 1, 1, -1):
+        if shape[d] > 1 and strides[d] != inner:
             raise ValueError("the pages of cache must be contiguous")
-        token *= n
-    if cache.shape[2] > 1 and cache.stride(2) * e != token:
-        raise ValueError("the pages of cache must be contiguous")
-    page = cache.shape[2] * token
-    strides = [st * e if n > 1 else page for n, st in zip(cache.shape[:2], cache.stride()[:2])]
-    if any(n > 1 and st < page for n, st in zip(cache.shape[:2], strides)):
+        if d > 2:
+            inner *= shape[d]
+    token, page = inner * e, inner * e * shape[2]
+    plane_st = strides[0] * e if shape[0] > 1 else page
+    page_st = strides[1] * e if pages > 1 else page
+    if plane_st < page or page_st < page:
         raise ValueError("the pages of cache must not overlap")
-    return (cache.data_ptr() or None, cache.shape[0], strides[0], pages, strides[1],
-            cache.shape[2], token)
+    return cache.data_ptr() or None, shape[0], plane_st, pages, page_st, shape[2], token
 
 
 def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None, workspace=None,
@@ -810,22 +826,21 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
     when None; the host waits for nothing."""
     torch = _torch()
     rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
-    planes = _cache_planes(cache, pages)
-    if cache.device != dev:
-        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    planes = _cache_planes(cache, pages, dev)
     (pp, n), (cp, nc) = _vector(parents, "parents", dev), _vector(children, "children", dev)
     if n != nc:
         raise ValueError(f"{n} parents, {nc} children")
-    with _Launch(dev, stream) as handle:
+    with _launch(dev, stream):
         if status is None:
-            status = torch.empty(n, dtype=torch.int32, device=dev)
+            status = refs.new_empty(n)
         sp, ns = _vector(status, "status", dev)
         if ns != n:
             raise ValueError(f"status holds {ns} entries, expected {n}")
-        ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(n, pages) if n else 0, dev)
-        st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp,
-                                      ws.data_ptr() if ws_bytes else None, ws_bytes, handle)
-    _check("dsa_cache_fork", st)
+        held, ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(n, pages) if n else 0, refs)
+        st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp, ws, ws_bytes,
+                                      _current_handle(dev))
+    if st:
+        _check("dsa_cache_fork", st)
     return status
 
 
@@ -834,9 +849,10 @@ def dsa_cache_free(refs, tables, lens, seqs, *, stream=None):
     refs go down by one, their rows become -1 and their lengths 0."""
     rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
     sp, n = _vector(seqs, "seqs", dev)
-    with _Launch(dev, stream) as handle:
-        st = library().dsa_cache_free(rp, pages, tp, S, P, ld, lp, sp, n, handle)
-    _check("dsa_cache_free", st)
+    with _launch(dev, stream):
+        st = library().dsa_cache_free(rp, pages, tp, S, P, ld, lp, sp, n, _current_handle(dev))
+    if st:
+        _check("dsa_cache_free", st)
 
 
 def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=None, stream=None):
@@ -844,30 +860,28 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
     refs and table entries). Returns ``remap`` int32 [N], the new number of
     each used page (-1 for free ones), and ``live`` int32 [1], how many are in
     use; allocated when None."""
-    torch = _torch()
     rp, pages, tp, S, P, ld, _, dev = _cache_state(refs, tables, None)
-    planes = _cache_planes(cache, pages)
-    if cache.device != dev:
-        raise ValueError(f"cache is on {cache.device}, expected {dev}")
-    with _Launch(dev, stream) as handle:
+    planes = _cache_planes(cache, pages, dev)
+    with _launch(dev, stream):
         if remap is None:
-            remap = torch.empty(pages, dtype=torch.int32, device=dev)
+            remap = refs.new_empty(pages)
         if live is None:
-            live = torch.empty(1, dtype=torch.int32, device=dev)
+            live = refs.new_empty(1)
         (mp, n), (vp, one) = _vector(remap, "remap", dev), _vector(live, "live", dev)
         if n != pages or one != 1:
             raise ValueError(f"remap must have {pages} entries and live one")
-        ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(0, pages), dev)
-        st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp,
-                                         ws.data_ptr() if ws_bytes else None, ws_bytes, handle)
-    _check("dsa_cache_compact", st)
+        held, ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(0, pages), refs)
+        st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp, ws, ws_bytes,
+                                         _current_handle(dev))
+    if st:
+        _check("dsa_cache_compact", st)
     return remap, live
 
 
 def cache_workspace_bytes(pairs: int, num_pages: int) -> int:
     """Bytes of workspace of ``dsa_cache_fork`` (of ``pairs`` pairs) or, with
     0 pairs, of ``dsa_cache_compact``."""
-    return int(library().dsa_cache_workspace_bytes(pairs, num_pages))
+    return library().dsa_cache_workspace_bytes(pairs, num_pages)
 
 
 def _to_device(host, dev_buf, stream):

@@ -233,8 +233,12 @@ def test_binding_takes_cuda_tensors_only(dsa):
 
 def test_binding_strides(dsa):
     x = torch.zeros(5, 4, 64)
-    assert dsa._rows_of(x, "q") == [256, 64]
-    assert dsa._rows_of(x[:, ::2], "q") == [256, 128]
-    assert dsa._rows_of(torch.as_strided(x, (1, 4, 64), (3, 64, 1)), "q") == [64, 64]
+
+    def rows(t):
+        return dsa._row_strides(t.shape, t.stride(), "q")
+
+    assert rows(x) == (256, 64)
+    assert rows(x[:, ::2]) == (256, 128)
+    assert rows(torch.as_strided(x, (1, 4, 64), (3, 64, 1))) == (64, 64)
     with pytest.raises(ValueError, match="unit stride"):
-        dsa._rows_of(x.transpose(1, 2), "q")
+        rows(x.transpose(1, 2))
