@@ -639,17 +639,24 @@ def _attention_dtype(t, name):
 def _attention_outputs(q, shape, index, out, lse_out):
     """Output tensors (allocated when None) and their addresses and strides."""
     torch = _torch()
+    T, H, D = shape
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o = out.data_ptr(), H * D, D
+    else:
+        op, oshape, ost = _on_gpu(out, q.dtype, "out", 3, index)
+        if oshape != shape:
+            raise ValueError(f"out must be {tuple(shape)}, got {tuple(oshape)}")
+        o = op, *_row_strides(oshape, ost, "out")
     if lse_out is None:
-        lse_out = q.new_empty(shape[:2], dtype=torch.float32)
-    op, oshape, ost = _on_gpu(out, q.dtype, "out", 3, index)
-    lp, lshape, lst = _on_gpu(lse_out, torch.float32, "lse_out", 2, index)
-    if oshape != shape:
-        raise ValueError(f"out must be {tuple(shape)}, got {tuple(oshape)}")
-    if lshape != shape[:2]:
-        raise ValueError(f"lse_out must be {tuple(shape[:2])}, got {tuple(lshape)}")
-    return out, lse_out, (op, *_row_strides(oshape, ost, "out"), lp, *lst)
+        lse_out = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        l = lse_out.data_ptr(), H, 1
+    else:
+        lp, lshape, lst = _on_gpu(lse_out, torch.float32, "lse_out", 2, index)
+        if lshape != shape[:2]:
+            raise ValueError(f"lse_out must be {tuple(shape[:2])}, got {tuple(lshape)}")
+        l = lp, *lst
+    return out, lse_out, (*o, *l)
 
 
 def _scale(scale, dim):
@@ -763,7 +770,8 @@ def _scratch(workspace, need: int, like):
     if workspace is None:
         if not need:
             return None, None, 0
-        workspace = like.new_empty(need, dtype=_torch().uint8)
+        torch = _torch()
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
@@ -832,7 +840,7 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
         raise ValueError(f"{n} parents, {nc} children")
     with _launch(dev, stream):
         if status is None:
-            status = refs.new_empty(n)
+            status = torch.empty(n, dtype=torch.int32, device=refs.device)
         sp, ns = _vector(status, "status", dev)
         if ns != n:
             raise ValueError(f"status holds {ns} entries, expected {n}")
@@ -860,13 +868,14 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
     refs and table entries). Returns ``remap`` int32 [N], the new number of
     each used page (-1 for free ones), and ``live`` int32 [1], how many are in
     use; allocated when None."""
+    torch = _torch()
     rp, pages, tp, S, P, ld, _, dev = _cache_state(refs, tables, None)
     planes = _cache_planes(cache, pages, dev)
     with _launch(dev, stream):
         if remap is None:
-            remap = refs.new_empty(pages)
+            remap = torch.empty(pages, dtype=torch.int32, device=refs.device)
         if live is None:
-            live = refs.new_empty(1)
+            live = torch.empty(1, dtype=torch.int32, device=refs.device)
         (mp, n), (vp, one) = _vector(remap, "remap", dev), _vector(live, "live", dev)
         if n != pages or one != 1:
             raise ValueError(f"remap must have {pages} entries and live one")
