@@ -41,6 +41,7 @@
 
 #include <type_traits>
 
+#include "follow.cuh"
 #include "umma.cuh"
 
 namespace dsa {
@@ -1189,6 +1190,7 @@ constexpr int kJoinWarps = 4;
 template <typename T, int DP>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_kernel(const __grid_constant__ AttendArgs a, const JoinArgs j) {
+  follow();
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   if (r >= a.tokens * a.heads) return;

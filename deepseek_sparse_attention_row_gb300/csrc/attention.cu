@@ -129,10 +129,11 @@ dsa_status launch_join(const AttendArgs& a, const JoinArgs& j, cudaStream_t stre
   const int64_t rows = a.tokens * a.heads;
   const int64_t ctas = (rows + kJoinWarps - 1) / kJoinWarps;
   if (ctas > INT32_MAX) return DSA_EUNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(ctas);
-  if (a.dim > 64) join_kernel<T, 128><<<grid, kJoinWarps * 32, 0, stream>>>(a, j);
-  else join_kernel<T, 64><<<grid, kJoinWarps * 32, 0, stream>>>(a, j);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
+  const dim3 grid(static_cast<unsigned>(ctas));
+  const bool ok = a.dim > 64
+                      ? launch_after(join_kernel<T, 128>, grid, kJoinWarps * 32, stream, a, j)
+                      : launch_after(join_kernel<T, 64>, grid, kJoinWarps * 32, stream, a, j);
+  return ok ? DSA_OK : DSA_ECUDA;
 }
 
 // How a paged call's work is cut, and where its partial outputs lie in the
