@@ -66,6 +66,7 @@ __all__ = [
     "FORK_REFUSED",
     "select_candidate_blocks_host",
     "select_candidate_blocks_sharded_host",
+    "prompt_workspace_bytes",
     "shared_prefix_workspace_bytes",
     "cache_workspace_bytes",
     "max_select_blocks",
@@ -105,6 +106,7 @@ EXPORTED_SYMBOLS = (
     "dsa_mask_candidate_logits_sharded_starts_bf16",
     "dsa_select_set_launch_override",
     "dsa_pipeline_error",
+    "dsa_prompt_workspace_bytes",
     "dsa_prompt_attention",
     "dsa_shared_prefix_workspace_bytes",
     "dsa_shared_prefix_attention",
@@ -178,7 +180,9 @@ def library():
     f32 = ctypes.c_float
     lib.dsa_prompt_attention.argtypes = [p, p, p, i32, i64, i64, i32, i32, i32, i64, i64, i64,
                                          i64, i64, i64, p, p, i32, i32, f32, p, i64, i64, p, i64,
-                                         i64, p]
+                                         i64, p, sz, p]
+    lib.dsa_prompt_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i32]
+    lib.dsa_prompt_workspace_bytes.restype = sz
     lib.dsa_shared_prefix_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i64, i32]
     lib.dsa_shared_prefix_workspace_bytes.restype = sz
     lib.dsa_shared_prefix_attention.argtypes = [p, p, p, i32, i64, i32, i32, i32, i64, i32, i64,
@@ -664,7 +668,7 @@ def _scale(scale, dim):
 
 
 def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None, out=None,
-                         lse_out=None, stream=None):
+                         lse_out=None, workspace=None, stream=None):
     """Attention over packed prompts with grouped heads.
 
     ``q`` [Tq, H, D], ``k`` and ``v`` [Tk, Hkv, D] bfloat16 or float16, D a
@@ -674,8 +678,10 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
     earlier one a key less. ``scale`` defaults to 1/sqrt(D). Writes ``out``
     [Tq, H, D] and the base-2 log-sum-exp ``lse_out`` [Tq, H] fp32 (allocated
     when None) and returns both; rows that see no key get 0 and -inf, rows of
-    no sequence are left as they were. Forward only: the outputs carry no
-    autograd graph."""
+    no sequence are left as they were. ``workspace``: a CUDA uint8 tensor of
+    ``prompt_workspace_bytes(...)`` bytes that no overlapping call uses
+    (allocated when None). Forward only: the outputs carry no autograd
+    graph."""
     code = _attention_dtype(q, "q")
     dt, dev = q.dtype, q.get_device()
     qp, qs, qst = _on_gpu(q, dt, "q", 3)
@@ -688,13 +694,21 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
         raise ValueError(f"cu_q and cu_k must have one length of at least 1, got {nq} and {nk}")
     with _launch(dev, stream):
         out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
+        held, ws, ws_bytes = _scratch(
+            workspace, prompt_workspace_bytes(qs[0], ks[0], qs[1], ks[1], qs[2], nq - 1), q)
         st = library().dsa_prompt_attention(
             qp, kp, vp, code, qs[0], ks[0], qs[1], ks[1], qs[2], *_row_strides(qs, qst, "q"),
             *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cq, ck, nq - 1,
-            1 if causal else 0, _scale(scale, qs[2]), *outs, _current_handle(dev))
+            1 if causal else 0, _scale(scale, qs[2]), *outs, ws, ws_bytes, _current_handle(dev))
     if st:
         _check("dsa_prompt_attention", st)
     return out, lse_out
+
+
+def prompt_workspace_bytes(total_q: int, total_k: int, heads: int, kv_heads: int, head_dim: int,
+                           seqs: int) -> int:
+    """Bytes of workspace of a ``dsa_prompt_attention`` call."""
+    return library().dsa_prompt_workspace_bytes(total_q, total_k, heads, kv_heads, head_dim, seqs)
 
 
 def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: int = 0, *,

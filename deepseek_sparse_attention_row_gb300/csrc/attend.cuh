@@ -94,7 +94,7 @@ struct Seg {
   // pages: the sequence whose own tokens these are (kv_len of them), or -1
   // for the prefix; whether a page of the segment is missing
   int32_t seq, gaps;
-  int32_t slot;     // of the partial outputs
+  int32_t slot;     // of the partial outputs (-1: written out at once)
 };
 
 struct AttendArgs {
@@ -111,6 +111,8 @@ struct AttendArgs {
   int64_t o_st, o_sh;
   float* lse;
   int64_t l_st, l_sh;
+  int32_t cut;                     // whether blocks may be cut, with room for it:
+  struct CutBlock* cuts;           // [CTAs], and the parts in prefix_o, prefix_lse
   // pages
   int64_t k_sn, v_sn;
   int64_t num_pages, max_pages, ld_tables;
@@ -209,66 +211,202 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int
 
 // ---- schedules ------------------------------------------------------------
 
-// Prompts: blocks of 2 * tile_tokens tokens for every key/value head, those
-// of the same tokens next to each other, a sequence's last (causal: longest)
-// ones first. They are dealt in rounds of one block per CTA, every other
-// round in reverse, so that the CTAs' sums of falling costs come out alike.
-struct PromptSchedule {
-  uint32_t round = 0;
-  int32_t chunk = 0;     // first of the 32 sequences that the lanes hold
-  uint32_t before = 0;   // blocks before them
-  bool loaded = false;
-  int32_t q0, q1, k0, k1;
-  uint32_t upto;         // blocks up to the lane's sequence, it included
+// Prompts: the work is a line of units, cut into equal shares, one per CTA:
+// (sequence, key/value head, block of 2 * tile_tokens tokens). A block is as
+// long as the keys that its last token sees, and kBlockCost for itself; a key
+// tile falls to the share that holds its first unit, so that CTAs finish
+// together whatever the lengths are. A share is a list of segments, a block's
+// tiles each. Blocks that lie in one share are written out at once; of a block
+// that is cut, each share holds a partial output, in slot 2 x of CTA x where
+// the block begins in an earlier share, 2 x + 1 where it goes on in the next,
+// and join_blocks_kernel joins them.
+// Without cuts (a.cut = 0: few keys, where the join would cost more than it
+// evens out) every block is one unit.
+constexpr int32_t kBlockCost = 4 * kTile;
+constexpr int32_t kMinShare = 4 * kTile;
 
-  __device__ explicit PromptSchedule(const AttendArgs&) {}
+// A cut block: what the joining kernel needs of it, with the CTA that begins it.
+struct CutBlock {
+  int32_t tok, ntok[2], kh;
+  int32_t more;  // CTAs behind this one that hold parts; 0: no block is cut here
+};
+
+struct PromptSchedule {
+  int64_t pos, end, share;
+  int64_t start;         // unit at which the current block begins
+  int32_t chunk = 0;     // first of the 32 sequences that the lanes hold
+  int32_t l_q0, l_q1, l_k0, l_k1;
+  int32_t lane_of = -1;  // lane of the current sequence
+  int32_t q0, q1, k0, kv, blocks, kh, b;
+  bool cut_here = false;
+
+  __device__ void hold(const AttendArgs& a) {
+    const int32_t i = chunk + (threadIdx.x & 31);
+    l_q0 = l_q1 = l_k0 = l_k1 = 0;
+    if (i < a.seqs) {
+      l_q0 = clamp_to(a.cu_q[i], a.tokens);
+      l_q1 = max(l_q0, clamp_to(a.cu_q[i + 1], a.tokens));
+      l_k0 = clamp_to(a.cu_k[i], a.total_k);
+      l_k1 = max(l_k0, clamp_to(a.cu_k[i + 1], a.total_k));
+    }
+  }
+  __device__ static int32_t blocks_of(const AttendArgs& a, int32_t tokens) {
+    const uint32_t block = 2 * a.tile_tokens;
+    return static_cast<int32_t>((static_cast<uint32_t>(tokens) + block - 1) / block);
+  }
+  // Keys that token e - 1 of n sees of kv, and units of the block that ends there.
+  __device__ static int32_t keys_of(const AttendArgs& a, int32_t n, int32_t kv, int32_t e) {
+    return a.causal ? max(kv - (n - e), 0) : kv;
+  }
+  __device__ static int32_t cost_of(const AttendArgs& a, int32_t keys) {
+    return a.cut ? kBlockCost + keys : 1;
+  }
+  // Units of the first m blocks of n tokens on kv keys (m below the number of
+  // blocks: all of them whole).
+  __device__ static int64_t units_of(const AttendArgs& a, int32_t n, int32_t kv, int32_t m) {
+    if (!a.cut) return m;
+    const int64_t own = static_cast<int64_t>(m) * kBlockCost;
+    if (!a.causal) return own + static_cast<int64_t>(m) * kv;
+    // block i sees kv - n + (i + 1) * block keys, none below i = none
+    const int32_t block = 2 * a.tile_tokens;
+    const int32_t none = kv >= n ? 0 : min((n - kv) / block, m);
+    const int64_t some = m - none;
+    return own + some * (static_cast<int64_t>(kv) - n) + block * (some * (none + 1 + m) / 2);
+  }
+  __device__ static int64_t all_of(const AttendArgs& a, int32_t n, int32_t kv) {
+    const int32_t m = blocks_of(a, n);
+    return m == 0 ? 0 : units_of(a, n, kv, m - 1) + cost_of(a, kv);
+  }
+  // Makes lane `src`'s sequence the current one.
+  __device__ void enter(const AttendArgs& a, int src) {
+    lane_of = src;
+    q0 = __shfl_sync(~0u, l_q0, src);
+    q1 = __shfl_sync(~0u, l_q1, src);
+    k0 = __shfl_sync(~0u, l_k0, src);
+    kv = __shfl_sync(~0u, l_k1, src) - k0;
+    blocks = blocks_of(a, q1 - q0);
+    kh = b = 0;
+  }
+
+  __device__ explicit PromptSchedule(const AttendArgs& a) {
+    int64_t all = 0;
+#pragma unroll 1
+    for (chunk = 0; chunk < a.seqs; chunk += 32) {
+      hold(a);
+      int64_t n = all_of(a, l_q1 - l_q0, l_k1 - l_k0);
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(~0u, n, o);
+      all += n * a.kv_heads;
+    }
+    share = (all + gridDim.x - 1) / gridDim.x;
+    if (a.cut) share = max(share, static_cast<int64_t>(kMinShare));
+    pos = min(share * blockIdx.x, all);
+    end = min(pos + share, all);
+    start = 0;
+    if (pos >= end) return;
+    // the sequence, the head and the block that hold unit pos
+#pragma unroll 1
+    for (chunk = 0;; chunk += 32) {
+      if (a.seqs > 32) hold(a);
+      const int64_t n = all_of(a, l_q1 - l_q0, l_k1 - l_k0) * a.kv_heads;
+      int64_t upto = n;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, upto, o);
+        if ((threadIdx.x & 31) >= o) upto += y;
+      }
+      const uint32_t found = __ballot_sync(~0u, upto > pos - start);
+      if (found != 0) {
+        const int src = __ffs(found) - 1;
+        start += __shfl_sync(~0u, upto - n, src);
+        enter(a, src);
+        break;
+      }
+      start += __shfl_sync(~0u, upto, 31);
+    }
+    const int64_t per = all_of(a, q1 - q0, kv);
+    kh = static_cast<int32_t>((pos - start) / per);
+    start += kh * per;
+    int32_t lo = 0, hi = blocks;  // units_of(lo) <= pos - start < those of hi blocks
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) >> 1;
+      if (units_of(a, q1 - q0, kv, mid) <= pos - start) lo = mid; else hi = mid;
+    }
+    b = lo;
+    start += units_of(a, q1 - q0, kv, b);
+  }
 
   __device__ bool next(const AttendArgs& a, Seg& g) {
-    const int lane = threadIdx.x & 31;
     const int32_t block = 2 * a.tile_tokens;
-    const uint32_t id =
-        round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    ++round;
-    const uint32_t at = id / a.kv_heads;
-    g.kh = static_cast<int32_t>(id - at * a.kv_heads);
 #pragma unroll 1
-    for (; chunk < a.seqs; chunk += 32, loaded = false) {
-      if (!loaded) {
-        const int32_t i = chunk + lane;
-        q0 = q1 = k0 = k1 = 0;
-        if (i < a.seqs) {
-          q0 = clamp_to(a.cu_q[i], a.tokens);
-          q1 = max(q0, clamp_to(a.cu_q[i + 1], a.tokens));
-          k0 = clamp_to(a.cu_k[i], a.total_k);
-          k1 = max(k0, clamp_to(a.cu_k[i + 1], a.total_k));
-        }
-        upto = warp_sum_upto((static_cast<uint32_t>(q1 - q0) + block - 1) / block);
-        loaded = true;
+    for (;;) {
+      if (pos >= end) {
+        if (!cut_here && (threadIdx.x & 31) == 0 && a.cut) a.cuts[blockIdx.x].more = 0;
+        cut_here = true;
+        return false;
       }
-      const uint32_t all = __shfl_sync(~0u, upto, 31);
-      if (at - before < all) {
-        const int src = __ffs(__ballot_sync(~0u, upto > at - before)) - 1;
-        const int32_t s0 = __shfl_sync(~0u, q0, src), s1 = __shfl_sync(~0u, q1, src);
-        g.k0 = __shfl_sync(~0u, k0, src);
-        g.kv_len = __shfl_sync(~0u, k1, src) - g.k0;
-        g.q_end = s1;
-        g.tok[0] = s0 + static_cast<int32_t>(__shfl_sync(~0u, upto, src) - 1 - (at - before)) *
-                            block;
-        g.ntok[0] = min(a.tile_tokens, s1 - g.tok[0]);
-        g.tok[1] = g.tok[0] + g.ntok[0];
-        g.ntok[1] = min(a.tile_tokens, s1 - g.tok[1]);
-        g.split = g.first = g.t0 = g.seq = g.gaps = g.slot = 0;
-        for (int s = 0; s < 2; ++s) {
-          // keys that the tile's last token sees
-          const int32_t lim =
-              a.causal ? g.kv_len - (s1 - g.tok[s] - g.ntok[s]) : g.kv_len;
-          g.n[s] = g.ntok[s] > 0 ? tiles_of(lim) : 0;
+      const int32_t e = min((b + 1) * static_cast<int64_t>(block), static_cast<int64_t>(q1 - q0));
+      const int32_t keys = keys_of(a, q1 - q0, kv, e), cost = cost_of(a, keys);
+      const int32_t from = static_cast<int32_t>(pos - start);
+      const int32_t to = static_cast<int32_t>(min(static_cast<int64_t>(cost), end - start));
+      const int64_t at = start;
+      const int32_t tiles = tiles_of(keys), my_kh = kh, my_k0 = k0, my_kv = kv, my_q1 = q1;
+      const int32_t tok = q0 + b * block;
+      const int32_t t0 = a.cut ? tiles_of(from - kBlockCost) : 0;
+      const int32_t t1 = a.cut ? tiles_of(to - kBlockCost) : tiles;
+      pos = start + to;
+      if (to == cost) {
+        start = pos;
+        if (++b == blocks) {
+          b = 0;
+          if (++kh == a.kv_heads && pos < end) {
+            // the next sequence that has any tokens
+            uint32_t found =
+                __ballot_sync(~0u, l_q1 > l_q0) & (lane_of == 31 ? 0u : ~0u << (lane_of + 1));
+#pragma unroll 1
+            while (found == 0 && chunk < a.seqs) {
+              chunk += 32;
+              hold(a);
+              found = __ballot_sync(~0u, l_q1 > l_q0);
+            }
+            if (found == 0) end = pos;  // the offsets changed under the call
+            else enter(a, __ffs(found) - 1);
+          }
         }
-        return true;
       }
-      before += all;
+      // a block without keys goes to the share where it begins
+      if (t1 <= t0 && !(tiles == 0 && from == 0)) continue;
+      g.kh = my_kh;
+      g.k0 = my_k0;
+      g.kv_len = my_kv;
+      g.q_end = my_q1;
+      g.tok[0] = tok;
+      g.ntok[0] = min(a.tile_tokens, my_q1 - tok);
+      g.tok[1] = tok + g.ntok[0];
+      g.ntok[1] = min(a.tile_tokens, my_q1 - g.tok[1]);
+      g.split = g.first = g.seq = g.gaps = 0;
+      g.t0 = t0;
+      for (int s = 0; s < 2; ++s) {
+        // tiles up to the last key that the row tile's last token sees
+        const int32_t lim = a.causal ? my_kv - (my_q1 - g.tok[s] - g.ntok[s]) : my_kv;
+        g.n[s] = g.ntok[s] > 0 ? max(min(tiles_of(lim), t1) - t0, 0) : 0;
+      }
+      g.slot = -1;
+      if (t1 - t0 < tiles) {
+        g.slot = 2 * static_cast<int32_t>(blockIdx.x) + (t0 == 0);
+        if (t0 == 0) {
+          cut_here = true;
+          if ((threadIdx.x & 31) == 0) {
+            const int64_t last =
+                (at + kBlockCost + static_cast<int64_t>(tiles - 1) * kTile) / share;
+            a.cuts[blockIdx.x] = CutBlock{tok, {g.ntok[0], g.ntok[1]}, my_kh,
+                                          static_cast<int32_t>(last - blockIdx.x)};
+          }
+        }
+      }
+      return true;
     }
-    return false;
   }
 };
 
@@ -1004,23 +1142,28 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     const int32_t head = g.kh * a.group + head0;
     T* out = nullptr;
     float *part = nullptr, *lse_at = nullptr;
-    const int step = PAGED && g.seq < 0 ? 4 * kTile : 4;  // from four values to the next
+    // from four values of a partial output to the next
+    const int step = !PAGED || g.seq < 0 ? 4 * kTile : 4;
     if (valid) {
-      if constexpr (PAGED) {
-        if (g.seq < 0) {
-          const int64_t r = g.slot * 256ll + (s ^ g.first) * kTile;
-          part = a.prefix_o + r * DP + row * 4;
-          lse_at = a.prefix_lse + r + row;
-        } else {
-          const int64_t r = (g.slot * 2ll + (s ^ g.first)) * a.group + row;
-          part = a.own_o + r * DP;
-          lse_at = a.own_lse + r;
-        }
+      if (PAGED && g.seq >= 0) {
+        const int64_t r = (g.slot * 2ll + (s ^ g.first)) * a.group + row;
+        part = a.own_o + r * DP;
+        lse_at = a.own_lse + r;
+      } else if (PAGED || g.slot >= 0) {
+        const int64_t r = g.slot * 256ll + (s ^ g.first) * kTile;
+        part = a.prefix_o + r * DP + row * 4;
+        lse_at = a.prefix_lse + r + row;
       } else {
         out = static_cast<T*>(a.out) + tok * a.o_st + head * a.o_sh;
         if (a.lse) lse_at = a.lse + tok * a.l_st + head * a.l_sh;
       }
     }
+    T* quad[4];  // the rows of this thread and its three neighbours
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      quad[j] = PAGED ? nullptr
+                      : reinterpret_cast<T*>(__shfl_sync(
+                            ~0u, reinterpret_cast<unsigned long long>(out), (lane & ~3) + j));
     bool odd = false;  // a value that is not finite
     if (n > 0) {
       if (!wait_warp(&c->o_done[s], (done - 1) & 1, c, 28)) return;
@@ -1038,22 +1181,37 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
         o[j] = l == 0.f ? 0.f : o[j] * inv;
         odd |= b + j < a.dim && !finite(o[j]);
       }
-      if constexpr (PAGED) {
-        if (part) {
+      if (part) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(part + (b + j) / 4 * step) =
-                make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-        }
-      } else {
-        if (out) {
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<float4*>(part + (b + j) / 4 * step) =
+              make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+      } else if (!PAGED && g.slot < 0) {
+        // Rows lie apart: four neighbouring threads change their 16-byte
+        // pieces about, so that each row gets 64 bytes at a time (a quarter
+        // of the lines per store).
+        uint32_t u[4][4];
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (b + j < a.dim)
-              *reinterpret_cast<uint4*>(out + b + j) =
-                  make_uint4(pack2(o[j], o[j + 1], T()), pack2(o[j + 2], o[j + 3], T()),
-                             pack2(o[j + 4], o[j + 5], T()), pack2(o[j + 6], o[j + 7], T()));
+        for (int j = 0; j < 32; j += 2) u[j / 8][j % 8 / 2] = pack2(o[j], o[j + 1], T());
+#pragma unroll
+        for (int m = 1; m <= 2; m *= 2) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j & m) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t mine = lane & m ? u[j][e] : u[j | m][e];
+              const uint32_t other = __shfl_xor_sync(~0u, mine, m);
+              if (lane & m) u[j][e] = other;
+              else u[j | m][e] = other;
+            }
+          }
         }
+        const int32_t d = b + 8 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (quad[j] && d < a.dim)
+            *reinterpret_cast<uint4*>(quad[j] + d) = make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
       }
     }
     if (n > 0) {
@@ -1083,7 +1241,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       for (int e = 0; e < 4; ++e) {
         const int d = lane + 32 * e;
         if (d < a.dim) {
-          if constexpr (PAGED) fpart[d / 4 * step + d % 4] = acc[e];
+          if (PAGED || fpart) fpart[d / 4 * step + d % 4] = acc[e];
           else fout[d] = from_f<T>(acc[e]);
         }
       }
@@ -1275,6 +1433,61 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     for (int d = 0; d < kPer; ++d) out[d] = from_f<T>(acc[d]);
   }
   if (j.lse && lane == 0) j.lse[b * j.l_sb + h * j.l_sh] = lse;
+}
+
+// The partial outputs of the blocks that are cut: CTA x joins the block that
+// begins in share x and goes on, one row per thread.
+constexpr int kJoinRows = 2 * kTile;
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kJoinRows)
+    join_blocks_kernel(const __grid_constant__ AttendArgs a) {
+  follow();
+  const CutBlock cut = a.cuts[blockIdx.x];
+  if (cut.more == 0) return;
+  const int s = threadIdx.x >> 7, row = threadIdx.x & 127, rt = row / a.group;
+  if (rt >= cut.ntok[s]) return;
+  const int64_t x = blockIdx.x;
+  // part i's row tile
+  const auto tile_at = [&](int32_t i) -> int64_t {
+    return (2 * (x + i) + (i == 0)) * 256 + s * kTile;
+  };
+  float m = neg_inf();
+#pragma unroll 1
+  for (int32_t i = 0; i <= cut.more; ++i) m = fmaxf(m, a.prefix_lse[tile_at(i) + row]);
+  const float base = m == neg_inf() ? 0.f : m;
+  float sum = 0.f;
+  float acc[DP];
+#pragma unroll
+  for (int d = 0; d < DP; ++d) acc[d] = 0.f;
+#pragma unroll 1
+  for (int32_t i = 0; i <= cut.more; ++i) {
+    const int64_t r = tile_at(i);
+    const float w = ex2(a.prefix_lse[r + row] - base);
+    sum += w;
+    const float4* o = reinterpret_cast<const float4*>(a.prefix_o + r * DP) + row;
+#pragma unroll
+    for (int d = 0; d < DP; d += 4) {
+      const float4 v = o[d / 4 * kTile];
+      acc[d] = fmaf(w, v.x, acc[d]);
+      acc[d + 1] = fmaf(w, v.y, acc[d + 1]);
+      acc[d + 2] = fmaf(w, v.z, acc[d + 2]);
+      acc[d + 3] = fmaf(w, v.w, acc[d + 3]);
+    }
+  }
+  const bool any = sum != 0.f;  // NaN counts
+  const float inv = any ? 1.f / sum : 0.f;
+  const int64_t tok = cut.tok + s * cut.ntok[0] + rt, head = cut.kh * a.group + row % a.group;
+  T* out = static_cast<T*>(a.out) + tok * a.o_st + head * a.o_sh;
+#pragma unroll
+  for (int d = 0; d < DP; d += 8)
+    if (d < a.dim)
+      *reinterpret_cast<uint4*>(out + d) =
+          make_uint4(pack2(acc[d] * inv, acc[d + 1] * inv, T()),
+                     pack2(acc[d + 2] * inv, acc[d + 3] * inv, T()),
+                     pack2(acc[d + 4] * inv, acc[d + 5] * inv, T()),
+                     pack2(acc[d + 6] * inv, acc[d + 7] * inv, T()));
+  if (a.lse) a.lse[tok * a.l_st + head * a.l_sh] = any ? base + log2f(sum) : neg_inf();
 }
 
 }  // namespace

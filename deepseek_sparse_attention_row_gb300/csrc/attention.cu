@@ -136,6 +136,48 @@ dsa_status launch_join(const AttendArgs& a, const JoinArgs& j, cudaStream_t stre
   return ok ? DSA_OK : DSA_ECUDA;
 }
 
+template <typename T>
+bool launch_join_blocks(const AttendArgs& a, unsigned grid, cudaStream_t stream) {
+  return a.dim > 64
+             ? launch_after(join_blocks_kernel<T, 128>, dim3(grid), kJoinRows, stream, a)
+             : launch_after(join_blocks_kernel<T, 64>, dim3(grid), kJoinRows, stream, a);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// How a prompt call's work is dealt, and where its partial outputs lie in the
+// workspace (each part 256-byte aligned).
+struct PromptPlan {
+  int32_t tile_tokens;
+  int cut, grid;
+  bool fits;  // blocks within 32 bits
+  size_t cuts, part_o, part_lse, bytes;
+};
+
+// Below this many keys in the batch blocks are not cut.
+constexpr int64_t kCutKeys = 2048;
+
+PromptPlan plan_prompt(int64_t total_q, int64_t total_k, int32_t heads, int32_t kv_heads,
+                       int32_t head_dim, int32_t seqs) {
+  PromptPlan p{};
+  p.tile_tokens = kTile / (heads / kv_heads);
+  // No more blocks than this, whatever the offsets hold.
+  const int64_t blocks = (total_q / (2 * p.tile_tokens) + seqs) * kv_heads;
+  const int64_t sms = sm_count();
+  p.fits = blocks <= INT32_MAX;
+  p.cut = total_k > kCutKeys;
+  // A block is cut at most into its key tiles.
+  const int64_t most = p.cut ? sms : blocks;
+  p.grid = static_cast<int>(most < sms ? most : sms);
+  if (!p.cut) return p;
+  const size_t slots = 2 * static_cast<size_t>(p.grid), dp = head_dim > 64 ? 128 : 64;
+  p.cuts = 0;
+  p.part_o = up256(p.grid * sizeof(CutBlock));
+  p.part_lse = p.part_o + up256(slots * 256 * dp * 4);
+  p.bytes = p.part_lse + up256(slots * 256 * 4);
+  return p;
+}
+
 // How a paged call's work is cut, and where its partial outputs lie in the
 // workspace (each part 256-byte aligned).
 struct PagedPlan {
@@ -144,8 +186,6 @@ struct PagedPlan {
   bool fits;  // units, slots and rows within 32 bits
   size_t starts, prefix_o, prefix_lse, own_o, own_lse, bytes;
 };
-
-size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 PagedPlan plan_paged(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,
                      int64_t prefix_len, int64_t max_pages, int32_t page_size) {
@@ -218,18 +258,30 @@ extern "C" dsa_status dsa_prompt_attention(
     int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t q_st, int64_t q_sh, int64_t k_st,
     int64_t k_sh, int64_t v_st, int64_t v_sh, const int32_t* cu_q, const int32_t* cu_k,
     int32_t seqs, int32_t causal, float scale, void* out, int64_t o_st, int64_t o_sh, float* lse,
-    int64_t l_st, int64_t l_sh, void* stream) {
+    int64_t l_st, int64_t l_sh, void* workspace, size_t workspace_bytes, void* stream) {
   if (total_k < 0 || seqs < 0) return DSA_EINVAL;
   const dsa_status st = dsa::check_common(dtype, total_q, heads, kv_heads, head_dim, scale);
   if (st != DSA_OK) return st;
-  if (total_k > INT32_MAX) return DSA_EUNSUPPORTED;
+  if (total_k > INT32_MAX - 4096) return DSA_EUNSUPPORTED;
   if (total_q == 0 || heads == 0 || seqs == 0) return DSA_OK;
   if (!q || !out || !cu_q || !cu_k || (total_k > 0 && (!k || !v))) return DSA_EINVAL;
   if (!dsa::aligned16(q) || !dsa::aligned16(k) || !dsa::aligned16(v) || !dsa::aligned16(out) ||
       !dsa::by8(q_st, q_sh) || !dsa::by8(k_st, k_sh) || !dsa::by8(v_st, v_sh) ||
       !dsa::by8(o_st, o_sh))
     return DSA_EUNSUPPORTED;
+  const dsa::PromptPlan p = dsa::plan_prompt(total_q, total_k, heads, kv_heads, head_dim, seqs);
+  if (!p.fits) return DSA_EUNSUPPORTED;
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes ||
+                      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return DSA_EINVAL;
   dsa::AttendArgs a{};
+  a.cut = p.cut;
+  if (p.cut) {
+    char* ws = static_cast<char*>(workspace);
+    a.cuts = reinterpret_cast<dsa::CutBlock*>(ws + p.cuts);
+    a.prefix_o = reinterpret_cast<float*>(ws + p.part_o);
+    a.prefix_lse = reinterpret_cast<float*>(ws + p.part_lse);
+  }
   a.q = q;
   a.k = k;
   a.v = v;
@@ -239,7 +291,7 @@ extern "C" dsa_status dsa_prompt_attention(
   a.kv_heads = kv_heads;
   a.group = heads / kv_heads;
   a.dim = head_dim;
-  a.tile_tokens = dsa::kTile / a.group;
+  a.tile_tokens = p.tile_tokens;
   a.c = scale * dsa::kLog2e;
   a.tokens = total_q;
   a.total_k = total_k;
@@ -268,12 +320,21 @@ extern "C" dsa_status dsa_prompt_attention(
        !dsa::encode<3>(&m.v, dtype, v, {head_dim, kv_heads, total_k}, {v_sh, v_st},
                        {64, 1, dsa::kTile})))
     return DSA_EUNSUPPORTED;
-  // No more blocks than this, whatever the offsets hold.
-  const int64_t blocks = (total_q / (2 * a.tile_tokens) + seqs) * kv_heads;
-  const int64_t sms = dsa::sm_count();
-  if (blocks + 2 * sms > UINT32_MAX) return DSA_EUNSUPPORTED;
-  return dsa::launch<false>(m, a, dtype, static_cast<int>(blocks < sms ? blocks : sms),
-                            static_cast<cudaStream_t>(stream));
+  cudaStream_t strm = static_cast<cudaStream_t>(stream);
+  const dsa_status done = dsa::launch<false>(m, a, dtype, p.grid, strm);
+  if (done != DSA_OK || !p.cut) return done;
+  const bool ok = dtype == DSA_DTYPE_BF16
+                      ? dsa::launch_join_blocks<__nv_bfloat16>(a, p.grid, strm)
+                      : dsa::launch_join_blocks<__half>(a, p.grid, strm);
+  return ok ? DSA_OK : DSA_ECUDA;
+}
+
+extern "C" size_t dsa_prompt_workspace_bytes(int64_t total_q, int64_t total_k, int32_t heads,
+                                             int32_t kv_heads, int32_t head_dim, int32_t seqs) {
+  if (dsa::check_common(DSA_DTYPE_BF16, total_q, heads, kv_heads, head_dim, 1.f) != DSA_OK ||
+      total_k < 0 || total_k > INT32_MAX || seqs < 0 || total_q == 0 || heads == 0 || seqs == 0)
+    return 0;
+  return dsa::plan_prompt(total_q, total_k, heads, kv_heads, head_dim, seqs).bytes;
 }
 
 extern "C" size_t dsa_shared_prefix_workspace_bytes(int64_t batch, int32_t heads,

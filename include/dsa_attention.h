@@ -44,6 +44,17 @@ extern "C" {
 #endif
 
 /*
+ * Bytes of device workspace of a dsa_prompt_attention call with these sizes
+ * on the current device (0 where it needs none, and for sizes that it refuses
+ * or has nothing to do for). The contents need no initialisation and mean
+ * nothing after the call; two calls that may run at the same time must not
+ * share a workspace.
+ */
+size_t dsa_prompt_workspace_bytes(int64_t total_q, int64_t total_k,
+                                  int32_t heads, int32_t kv_heads,
+                                  int32_t head_dim, int32_t seqs);
+
+/*
  * dsa_prompt_attention -- attention of whole prompts, packed.
  *
  *   q      [total_q, heads, head_dim] of `dtype` (DSA_DTYPE_BF16 or
@@ -58,6 +69,8 @@ extern "C" {
  *   scale  > 0, finite: the factor of <q, k>.
  *   out    [total_q, heads, head_dim] of `dtype`.
  *   lse    [total_q, heads] fp32 at lse + t*l_st + h*l_sh, or NULL.
+ *   workspace     dsa_prompt_workspace_bytes(...) bytes, 256-byte aligned
+ *          (NULL when that is 0).
  *
  * Offsets are clamped to [0, total]; a sequence whose end is below its start
  * is empty. Rows that belong to no sequence (behind the last one, as in a
@@ -67,7 +80,8 @@ extern "C" {
  * total_q == 0, heads == 0 or seqs == 0: DSA_OK, nothing written. DSA_EINVAL
  * for an unknown dtype, negative sizes, kv_heads < 1 or no divisor of heads,
  * head_dim < 1, a scale that is not positive and finite, or a NULL q, cu_q,
- * cu_k or out (or k or v with total_k > 0). DSA_EUNSUPPORTED for
+ * cu_k or out (or k or v with total_k > 0), or a workspace that is too small.
+ * DSA_EUNSUPPORTED for
  * DSA_DTYPE_F32, head_dim over 128 or no multiple of 8, heads / kv_heads >
  * 128, layouts other than above, and sizes from 2^31.
  */
@@ -80,7 +94,8 @@ dsa_status dsa_prompt_attention(const void *q, const void *k, const void *v,
                                 const int32_t *cu_k, int32_t seqs,
                                 int32_t causal, float scale, void *out,
                                 int64_t o_st, int64_t o_sh, float *lse,
-                                int64_t l_st, int64_t l_sh, void *stream);
+                                int64_t l_st, int64_t l_sh, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 /*
  * Bytes of device workspace of a dsa_shared_prefix_attention call with these

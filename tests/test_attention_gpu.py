@@ -446,9 +446,48 @@ def test_own_workspace(env):
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert (buf[need:] == 255).all()
-    if need:
-        with pytest.raises(dsa.DsaError):
-            dsa.dsa_shared_prefix_attention(*p, 320, workspace=buf[:need - 1])
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_shared_prefix_attention(*p, 320, workspace=buf[:need - 1])
+    q, k, v = make(torch, 32, 300, 5000, 4, 2, 64, torch.bfloat16)
+    want = check_prompt(env, q, k, v, [300], [5000], True)
+    need = dsa.prompt_workspace_bytes(300, 5000, 4, 2, 64, 1)
+    buf = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    cu = ints(torch, [0, 300]), ints(torch, [0, 5000])
+    got = dsa.dsa_prompt_attention(q, k, v, *cu, workspace=buf[:need])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (buf[need:] == 255).all()
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_prompt_attention(q, k, v, *cu, workspace=buf[:need - 1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("ql,kl", [
+    ([1, 1], [9000, 3]),                     # one block across many CTAs
+    ([700, 0, 33, 300], [2500, 10, 0, 900]),
+    ([2100, 5], [1500, 3000]),               # rows without keys, then few with many
+    ([9] * 300, [40] * 300),
+], ids=str)
+def test_prompt_blocks_cut_between_ctas(env, ql, kl, causal):
+    """More keys than the kernel leaves whole: blocks are cut between CTAs and
+    their parts joined, at odd places."""
+    torch, dsa = env
+    for heads, kv_heads, dim in ((6, 2, 64), (4, 4, 128), (5, 1, 72)):
+        q, k, v = make(torch, sum(ql) + dim, sum(ql), sum(kl), heads, kv_heads, dim,
+                       torch.bfloat16)
+        assert dsa.prompt_workspace_bytes(sum(ql), sum(kl), heads, kv_heads, dim, len(ql)) > 0
+        check_prompt(env, q, k, v, ql, kl, causal)
+
+
+def test_prompt_cut_blocks_with_values_that_are_not_finite(env):
+    """Hidden infinities and NaN beside a cut, and seen ones behind it."""
+    torch, _ = env
+    ql, kl = [300, 40], [5000, 700]
+    q, k, v = make(torch, 31, 340, 5700, 4, 2, 64, torch.bfloat16)
+    v[4999, 0], k[4999, 1] = math.nan, math.inf     # the last query's own key
+    v[4800, 1, 7] = math.inf
+    v[5000 + 650, 0, 2] = -math.inf
+    check_prompt(env, q, k, v, ql, kl, True)
 
 
 def test_nothing_to_do(env):

@@ -28,7 +28,7 @@ def prompt(lib, **kw):
     a = dict(q=FAKE, k=FAKE, v=FAKE, dtype=BF16, total_q=10, total_k=10, heads=4, kv_heads=2,
              head_dim=64, q_st=256, q_sh=64, k_st=128, k_sh=64, v_st=128, v_sh=64, cu_q=FAKE,
              cu_k=FAKE, seqs=1, causal=1, scale=0.125, out=FAKE, o_st=256, o_sh=64, lse=None,
-             l_st=4, l_sh=1, stream=None)
+             l_st=4, l_sh=1, workspace=FAKE, workspace_bytes=1 << 30, stream=None)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.dsa_prompt_attention(*a.values())
@@ -76,6 +76,9 @@ COMMON = [
     (dict(v=ODD), DSA_EUNSUPPORTED),
     (dict(total_q=0, q=None, out=None), DSA_OK),
     (dict(seqs=0, q=None, out=None, cu_q=None), DSA_OK),
+    (dict(total_k=100000, workspace=None), DSA_EINVAL),
+    (dict(total_k=100000, workspace=ODD), DSA_EINVAL),
+    (dict(total_k=100000, workspace_bytes=4096), DSA_EINVAL),
 ], ids=str)
 def test_prompt_refusals(dsa, kw, want):
     assert prompt(dsa.library(), **kw) == want
@@ -213,6 +216,10 @@ def test_workspace_sizes(dsa):
     assert dsa.shared_prefix_workspace_bytes(0, 8, 2, 64, 0, 5, 16) == 0
     assert dsa.shared_prefix_workspace_bytes(-1, 8, 2, 64, 0, 5, 16) == 0
     assert dsa.shared_prefix_workspace_bytes(4, 8, 3, 64, 0, 5, 16) == 0
+    assert dsa.prompt_workspace_bytes(0, 100000, 8, 2, 64, 1) == 0
+    assert dsa.prompt_workspace_bytes(100, 100, 8, 2, 64, 1) == 0
+    assert dsa.prompt_workspace_bytes(100, -1, 8, 2, 64, 1) == 0
+    assert dsa.prompt_workspace_bytes(100, 100000, 8, 2, 64, 1) > 256 * 64 * 4
 
 
 def test_binding_takes_cuda_tensors_only(dsa):
