@@ -762,8 +762,11 @@ __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
   }
 }
 
-// The loading warp: row tiles, K and V in the order in which the products take
-// them. The pages of a load are looked up a step ahead.
+// The loading warp: row tiles, K and V, in the order in which the products
+// take them. Lane i looks up the tile's i-th page, a step ahead and compared
+// only when the load is due, so that nothing waits for the table. One elected
+// lane issues every copy: copies that several lanes issue at once are taken
+// one by one, at about 150 cycles each (16 per tile of 16-token pages).
 template <int DP, bool PAGED>
 __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorMap* qm1,
                      const CUtensorMap* km, const CUtensorMap* vm, Cta<DP> cta) {
@@ -773,77 +776,93 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
   Ring<DP> ring;
   uint32_t used = 0, phase = 0;  // row-tile buffers: in use before, parity of the next wait
   uint32_t turn = 0;
-  // boxes of a K or V tile, one lane each: page within the tile, half
-  const int boxes = (PAGED && a.page_size < kTile ? kTile >> a.page_log2 : 1) * L::kHalves;
-  const int pi = lane / L::kHalves, h = lane % L::kHalves;
-  const uint32_t to = h * L::kHalf + (PAGED ? pi * a.page_size * 128 : 0);
-  const auto page = [&](const Place<true>& p) -> int32_t {
+  const int pages = PAGED && a.page_size < kTile ? kTile >> a.page_log2 : 1;
+  const uint32_t page_bytes = kTile * 128 / pages;
+  const uint32_t none = static_cast<uint32_t>(a.num_pages);
+  const auto look_up = [&](const Place<true>& p) -> uint32_t {
+    if (!PAGED || !p.more) return none;
+    // the list's table, from its first page on, and how many pages it has
+    const int32_t pre = static_cast<int32_t>(a.prefix_len >> a.page_log2);
+    const bool own = p.g.seq >= 0;
+    const int32_t* table = own ? a.tables + p.g.seq * a.ld_tables + pre : a.prefix_pages;
+    const int32_t count = own ? static_cast<int32_t>(a.max_pages) - pre : pre;
+    const int32_t at = (((p.g.t0 + p.j) * kTile) >> a.page_log2) + lane;
+    return lane < pages && at < count ? static_cast<uint32_t>(__ldg(table + at)) : none;
+  };
+  // A K or V tile into the ring's next stage.
+  const auto put = [&](const CUtensorMap* map, const Place<true>& p, uint32_t ids) -> bool {
+    uint64_t* bar = &c->kv_full[ring.stage];
+    if (ring.round > 0 && !wait_warp(&c->kv_empty[ring.stage], (ring.round - 1) & 1, c, 19))
+      return false;
+    unsigned char* dst = cta.stage(ring.stage);
+    ring.next();
+    if (elect_one()) mbar_arrive_expect_tx(bar, L::kBytes);
+    const int32_t t = (p.g.t0 + p.j) * kTile;
     if constexpr (PAGED) {
-      if (p.more && lane < boxes)
-        return page_of(a, p.g.seq,
-                       static_cast<int64_t>(p.g.t0 + p.j) * kTile + pi * a.page_size);
+#pragma unroll 1
+      for (int i = 0; i < pages; ++i) {
+        // a page that is not there: behind the last one, where zeros are read
+        const uint32_t id = min(__shfl_sync(~0u, ids, i), none);
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load4(dst + h * L::kHalf + i * page_bytes, map, h * 64, p.g.kh,
+                      t & (a.page_size - 1), static_cast<int>(id), bar);
+        }
+      }
+    } else if (elect_one()) {
+#pragma unroll
+      for (int h = 0; h < L::kHalves; ++h)
+        tma_load3(dst + h * L::kHalf, map, h * 64, p.g.kh, p.g.k0 + t, bar);
     }
-    return 0;
+    __syncwarp();
+    return true;
   };
   Place<true> p, q;  // of the values and of the scores
   if (!q.next(c, false, 17) || !p.next(c, true, 17)) return;
   int ahead = 0;
-  int32_t p_id = page(p), q_id = p_id;
+  uint32_t p_ids = look_up(p), q_ids = p_ids;
 #pragma unroll 1
   while (p.more) {
     bool values, scores;
     order(p, q, ahead, values, scores);
-    // Split segments take the two row-tile buffers in turn, so that the next
-    // segment's rows load while this one's are in use; shared ones take both.
-    const int q_first = q.g.split ? turn & 1 : 0;
-    const int q_count = !scores || q.j > 0 ? 0 : !q.g.split && q.g.ntok[1] > 0 ? 2 : 1;
-    if (q_count > 0 && q.g.split) ++turn;
+    if (values && !put(vm, p, p_ids)) return;
+    if (scores) {
+      if (q.j == 0) {
+        // Split segments take the two row-tile buffers in turn, so that the
+        // next segment's rows load while this one's are in use; shared ones
+        // take both. A segment of one sequence needs that token's rows alone.
+        const int first = q.g.split ? turn++ & 1 : 0;
+        const int count = !q.g.split && q.g.ntok[1] > 0 ? 2 : 1;
+        const bool one = PAGED && q.g.seq >= 0;
 #pragma unroll 1
-    for (int i = values ? 0 : 1; i < (scores ? 2 : 1); ++i) {  // V, then K
-      if (i == 1) {
-#pragma unroll 1
-        for (int r = q_first; r < q_first + q_count; ++r) {
+        for (int r = first; r < first + count; ++r) {
           if ((used >> r) & 1) {
             if (!wait_warp(&c->q_empty[r], (phase >> r) & 1, c, 18)) return;
             phase ^= 1u << r;
           }
           used |= 1u << r;
-          // a segment of one sequence needs that token's rows alone
-          const bool one = PAGED && q.g.seq >= 0;
-          if (lane == 0)
+          if (elect_one()) {
             mbar_arrive_expect_tx(&c->q_full[r],
                                   L::kHalves * (one ? 1 : a.tile_tokens) * a.group * 128);
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+              tma_load3(cta.q(r) + h * L::kHalf, one ? qm1 : qm, h * 64, q.g.kh * a.group,
+                        q.g.tok[q.g.split ? 0 : r], &c->q_full[r]);
+          }
           __syncwarp();
-          if (lane < L::kHalves)
-            tma_load3(cta.q(r) + lane * L::kHalf, one ? qm1 : qm, lane * 64, q.g.kh * a.group,
-                      q.g.tok[q.g.split ? 0 : r], &c->q_full[r]);
         }
       }
-      const int st = ring.stage;
-      if (ring.round > 0 && !wait_warp(&c->kv_empty[st], (ring.round - 1) & 1, c, 19)) return;
-      ring.next();
-      if (lane == 0) mbar_arrive_expect_tx(&c->kv_full[st], L::kBytes);
-      __syncwarp();
-      if (lane < boxes) {
-        unsigned char* dst = cta.stage(st) + to;
-        const CUtensorMap* map = i == 0 ? vm : km;
-        const int32_t t = i == 0 ? p.g.t0 + p.j : q.g.t0 + q.j, kh = i == 0 ? p.g.kh : q.g.kh;
-        if constexpr (PAGED)
-          tma_load4(dst, map, h * 64, kh, (t * kTile) & (a.page_size - 1), i == 0 ? p_id : q_id,
-                    &c->kv_full[st]);
-        else
-          tma_load3(dst, map, h * 64, kh, (i == 0 ? p.g.k0 : q.g.k0) + t * kTile,
-                    &c->kv_full[st]);
-      }
+      if (!put(km, q, q_ids)) return;
     }
     if (scores || !values) {  // q first: p lets go of the entries it takes
       if (!q.next(c, false, 17)) return;
-      q_id = page(q);
+      q_ids = look_up(q);
       ahead += scores;
     }
     if (values || !scores) {
       if (!p.next(c, true, 17)) return;
-      p_id = page(p);
+      p_ids = look_up(p);
       ahead -= values;
     }
   }
