@@ -42,6 +42,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -695,7 +696,8 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
     with _launch(dev, stream):
         out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
-            workspace, prompt_workspace_bytes(qs[0], ks[0], qs[1], ks[1], qs[2], nq - 1), q)
+            workspace, _need("dsa_prompt_workspace_bytes", dev, qs[0], ks[0], qs[1], ks[1], qs[2],
+                             nq - 1), q)
         st = library().dsa_prompt_attention(
             qp, kp, vp, code, qs[0], ks[0], qs[1], ks[1], qs[2], *_row_strides(qs, qst, "q"),
             *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cq, ck, nq - 1,
@@ -758,7 +760,8 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
     with _launch(dev, stream):
         out, lse_out, outs = _attention_outputs(q, q.shape, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
-            workspace, shared_prefix_workspace_bytes(B, H, Hkv, D, prefix_len, P, page), q)
+            workspace, _need("dsa_shared_prefix_workspace_bytes", dev, B, H, Hkv, D, prefix_len, P,
+                             page), q)
         st = library().dsa_shared_prefix_attention(
             qp, kp, vp, code, B, H, Hkv, D, N, page, *_row_strides((B, H, D), qst, "q"),
             *_row_strides(ks, kst, "k_pages"), *_row_strides(vs, vst, "v_pages"), pp, prefix_len,
@@ -774,6 +777,12 @@ def shared_prefix_workspace_bytes(batch: int, heads: int, kv_heads: int, head_di
     """Bytes of workspace of a ``dsa_shared_prefix_attention`` call."""
     return library().dsa_shared_prefix_workspace_bytes(batch, heads, kv_heads, head_dim,
                                                        prefix_len, max_pages, page_size)
+
+
+@functools.lru_cache(maxsize=4096)
+def _need(name: str, index: int, *sizes) -> int:
+    """A workspace's bytes on device ``index`` (the current one)."""
+    return getattr(library(), name)(*sizes)
 
 
 def _scratch(workspace, need: int, like):
@@ -858,7 +867,8 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
         sp, ns = _vector(status, "status", dev)
         if ns != n:
             raise ValueError(f"status holds {ns} entries, expected {n}")
-        held, ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(n, pages) if n else 0, refs)
+        held, ws, ws_bytes = _scratch(
+            workspace, _need("dsa_cache_workspace_bytes", dev, n, pages) if n else 0, refs)
         st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp, ws, ws_bytes,
                                       _current_handle(dev))
     if st:
@@ -893,7 +903,8 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
         (mp, n), (vp, one) = _vector(remap, "remap", dev), _vector(live, "live", dev)
         if n != pages or one != 1:
             raise ValueError(f"remap must have {pages} entries and live one")
-        held, ws, ws_bytes = _scratch(workspace, cache_workspace_bytes(0, pages), refs)
+        held, ws, ws_bytes = _scratch(
+            workspace, _need("dsa_cache_workspace_bytes", dev, 0, pages), refs)
         st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp, ws, ws_bytes,
                                          _current_handle(dev))
     if st:

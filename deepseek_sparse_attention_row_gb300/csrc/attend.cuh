@@ -425,9 +425,9 @@ __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
 // tiles, which falls to the share that holds the tile's first unit. A share is
 // a list of segments, a group's tiles each; segment (group g, CTA x) has slot
 // g + x, which grows along the line: no two segments share one.
-constexpr int32_t kSegCost = 8;
+constexpr int32_t kSegCost = 12;
 constexpr int32_t kTileCost = 4;        // one row tile
-constexpr int32_t kTwoTileCost = 5;     // two row tiles, bound by products
+constexpr int32_t kTwoTileCost = 7;     // two row tiles, bound by products
 
 struct PagedSchedule {
   int32_t pos, end, prefix_units;
@@ -1397,16 +1397,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     o0 = (b * a.kv_heads + kh + c0) * 2 * a.group + e;
   }
   // Prefix partials: tiles of 128 rows, [DP / 4][128][4] each; own ones: rows.
-  const auto tile_at = [&](int32_t i) -> int64_t {
-    return p0 + (a.prefix_split ? i * 128ll : i * 256ll);
-  };
-  const auto row_of = [&](int32_t i) -> int64_t {
-    return o0 + static_cast<int64_t>(i - np) * a.group;
-  };
-  const int32_t all = np + no;
+  // Partial i's row is a step behind partial i - 1's.
+  constexpr int kPer = DP / 32;  // values of a lane
+  const int32_t all = np + no, d = lane * kPer;
+  const int64_t p_step = a.prefix_split ? kTile : 2 * kTile;
+  const float* p_lse = a.prefix_lse + p0 + prow;
+  const float* o_lse = a.own_lse + o0;
+  const float* p_out = a.prefix_o + p0 * DP + (d / 4 * kTile + prow) * 4 + d % 4;
+  const float* o_out = a.own_o + o0 * DP + d;
   const auto lse_of = [&](int32_t i) {
-    return i >= all ? neg_inf()
-                    : i < np ? a.prefix_lse[tile_at(i) + prow] : a.own_lse[row_of(i)];
+    return i >= all ? neg_inf() : i < np ? p_lse[i * p_step] : o_lse[(i - np) * a.group];
   };
   // Lane i keeps the log-sum-exp of partial i; more than 32 are read again.
   const float held = lse_of(lane);
@@ -1421,7 +1421,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const bool any = sum != 0.f;  // NaN counts
   const float lse = any ? base + log2f(sum) : neg_inf();
-  constexpr int kPer = DP / 32;  // values of a lane
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   float acc[kPer];
   for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
@@ -1431,13 +1430,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int32_t i0 = 0; i0 < all; i0 += 32) {
     const float w = any ? ex2((i0 == 0 ? held : lse_of(i0 + lane)) - lse) : 0.f;
     const int32_t n = min(all - i0, 32);
-#pragma unroll 8
+#pragma unroll 4
     for (int32_t i = 0; i < n; ++i) {
       const float wi = __shfl_sync(~0u, w, i);
-      const int32_t d = lane * kPer;
-      const float* o = i0 + i < np
-                           ? a.prefix_o + tile_at(i0 + i) * DP + (d / 4 * kTile + prow) * 4 + d % 4
-                           : a.own_o + row_of(i0 + i) * DP + d;
+      const int32_t k = i0 + i;
+      const float* o = k < np ? p_out + k * p_step * DP
+                              : o_out + static_cast<int64_t>(k - np) * a.group * DP;
       const Vec v = *reinterpret_cast<const Vec*>(o);
       acc[0] = fmaf(wi, v.x, acc[0]);
       acc[1] = fmaf(wi, v.y, acc[1]);
@@ -1454,9 +1452,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (j.lse && lane == 0) j.lse[b * j.l_sb + h * j.l_sh] = lse;
 }
 
-// The partial outputs of the blocks that are cut: CTA x joins the block that
-// begins in share x and goes on, one row per thread.
+// The partial outputs of the blocks that are cut: CTAs (x, y) join the block
+// that begins in share x and goes on, one row per thread, 32 columns each
+// (with all columns in one thread the launch took 15.5 us for a packed prefill
+// chunk, so FIXME).
 constexpr int kJoinRows = 2 * kTile;
+constexpr int kJoinCols = 32;
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kJoinRows)
@@ -1476,17 +1477,19 @@ __global__ void __launch_bounds__(kJoinRows)
   for (int32_t i = 0; i <= cut.more; ++i) m = fmaxf(m, a.prefix_lse[tile_at(i) + row]);
   const float base = m == neg_inf() ? 0.f : m;
   float sum = 0.f;
-  float acc[DP];
+  float acc[kJoinCols];
 #pragma unroll
-  for (int d = 0; d < DP; ++d) acc[d] = 0.f;
+  for (int d = 0; d < kJoinCols; ++d) acc[d] = 0.f;
+  const int d0 = blockIdx.y * kJoinCols;
 #pragma unroll 1
   for (int32_t i = 0; i <= cut.more; ++i) {
     const int64_t r = tile_at(i);
     const float w = ex2(a.prefix_lse[r + row] - base);
     sum += w;
-    const float4* o = reinterpret_cast<const float4*>(a.prefix_o + r * DP) + row;
+    const float4* o =
+        reinterpret_cast<const float4*>(a.prefix_o + r * DP) + d0 / 4 * kTile + row;
 #pragma unroll
-    for (int d = 0; d < DP; d += 4) {
+    for (int d = 0; d < kJoinCols; d += 4) {
       const float4 v = o[d / 4 * kTile];
       acc[d] = fmaf(w, v.x, acc[d]);
       acc[d + 1] = fmaf(w, v.y, acc[d + 1]);
@@ -1497,16 +1500,17 @@ __global__ void __launch_bounds__(kJoinRows)
   const bool any = sum != 0.f;  // NaN counts
   const float inv = any ? 1.f / sum : 0.f;
   const int64_t tok = cut.tok + s * cut.ntok[0] + rt, head = cut.kh * a.group + row % a.group;
-  T* out = static_cast<T*>(a.out) + tok * a.o_st + head * a.o_sh;
+  T* out = static_cast<T*>(a.out) + tok * a.o_st + head * a.o_sh + d0;
 #pragma unroll
-  for (int d = 0; d < DP; d += 8)
-    if (d < a.dim)
+  for (int d = 0; d < kJoinCols; d += 8)
+    if (d0 + d < a.dim)
       *reinterpret_cast<uint4*>(out + d) =
           make_uint4(pack2(acc[d] * inv, acc[d + 1] * inv, T()),
                      pack2(acc[d + 2] * inv, acc[d + 3] * inv, T()),
                      pack2(acc[d + 4] * inv, acc[d + 5] * inv, T()),
                      pack2(acc[d + 6] * inv, acc[d + 7] * inv, T()));
-  if (a.lse) a.lse[tok * a.l_st + head * a.l_sh] = any ? base + log2f(sum) : neg_inf();
+  if (a.lse && d0 == 0)
+    a.lse[tok * a.l_st + head * a.l_sh] = any ? base + log2f(sum) : neg_inf();
 }
 
 }  // namespace

@@ -138,9 +138,9 @@ dsa_status launch_join(const AttendArgs& a, const JoinArgs& j, cudaStream_t stre
 
 template <typename T>
 bool launch_join_blocks(const AttendArgs& a, unsigned grid, cudaStream_t stream) {
-  return a.dim > 64
-             ? launch_after(join_blocks_kernel<T, 128>, dim3(grid), kJoinRows, stream, a)
-             : launch_after(join_blocks_kernel<T, 64>, dim3(grid), kJoinRows, stream, a);
+  const dim3 ctas(grid, (a.dim + kJoinCols - 1) / kJoinCols);
+  return a.dim > 64 ? launch_after(join_blocks_kernel<T, 128>, ctas, kJoinRows, stream, a)
+                    : launch_after(join_blocks_kernel<T, 64>, ctas, kJoinRows, stream, a);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
