@@ -893,9 +893,9 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
   // The products stop at the head dimension, in steps of 16.
   const int steps = (a.dim + 15) / 16;
   const uint32_t shape_o = mma_shape(kBf16, 16 * steps, true);
-  const uint64_t q0 = operand(smem_addr(cta.q(0)), 16, 1024);
-  const uint64_t k0 = operand(smem_addr(cta.stage(0)), 16, 1024);
-  const uint64_t v0 = operand(smem_addr(cta.stage(0)), L::kHalf, 1024);
+  const uint32_t q0 = operand(smem_addr(cta.q(0)), 16);
+  const uint32_t k0 = operand(smem_addr(cta.stage(0)), 16);
+  const uint32_t v0 = operand(smem_addr(cta.stage(0)), L::kHalf);
   Ring<DP> ring;
   // Bit s (or i): parities of the next waits, and whether O_s was used before.
   uint32_t q_phase = 0, p_phase = 0, o_phase = 0, o_used = 0;
@@ -904,11 +904,10 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
   // Q K^T of stream s
   const auto scores = [&](int s, int q, int stage) {
     tc_fence_after();
-    const uint64_t qa = q0 + ((q * L::kBytes) >> 4);
-    const uint64_t kb = k0 + ((stage * L::kBytes) >> 4);
+    const uint32_t qa = q0 + q * (L::kBytes >> 4), kb = k0 + stage * (L::kBytes >> 4);
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
-      const uint64_t off = ((i / 4) * L::kHalf + (i % 4) * 32) >> 4;
+      const uint32_t off = ((i / 4) * L::kHalf + (i % 4) * 32) >> 4;
       if (i < (DP == 128 ? 5 : 1) || i < steps)
         mma_ss(tmem + s * kTile, qa + off, kb + off, kShapeS, i > 0);
     }
@@ -923,7 +922,7 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
       }
       o_used |= 1u << s;
     }
-    const uint64_t vb = v0 + ((stage * L::kBytes) >> 4);
+    const uint32_t vb = v0 + stage * (L::kBytes >> 4);
     const uint32_t o = tmem + 2 * kTile + s * kTile, w = tmem + s * kTile;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
@@ -1031,7 +1030,9 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
   }
 }
 
-// Four warps of stream s, one row per thread.
+// Four warps of stream s, one row per thread. What the output needs of the
+// segment is read again behind the tiles: between them 128 scores fill the
+// registers.
 template <typename T, int DP, bool PAGED>
 __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
   Ctrl* c = cta.ctrl();
@@ -1044,16 +1045,19 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
   uint32_t done = 0;
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
-    Seg g;
-    if (!take_seg<true>(c, k, g, true, 25) || g.n[0] < 0) return;
+    if (!wait_warp(&c->seg_full[k % kSegs], (k / kSegs) & 1, c, 25)) return;
+    const Seg& g = c->seg[k % kSegs];
+    if (g.n[0] < 0) return;
     const int qs = g.split ? 0 : s;
     const int32_t n = g.n[s];
     const bool valid = rt < g.ntok[qs];  // ntok <= tile_tokens
-    const int32_t tok = g.tok[qs] + rt;
+    const int32_t tile0 = g.split ? g.t0 + (s ^ g.first) : g.t0, tile_step = g.split ? 2 : 1;
+    const bool gaps = PAGED && g.gaps;
     // keys that the row sees, of the segment's list; rows of no token are
     // not masked at all (nothing is written for them)
     int32_t lim = 0x7fffffff;
     if (valid) {
+      const int32_t tok = g.tok[qs] + rt;
       if constexpr (PAGED) {
         lim = g.seq < 0 ? min(seen_tokens(a, tok), static_cast<int32_t>(a.prefix_len))
                         : g.kv_len;
@@ -1065,9 +1069,9 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     float base = neg_inf(), l = 0.f;  // the row's base, in units of <q, k>
 #pragma unroll 1
     for (int32_t i = 0; i < n; ++i) {
-      const int32_t t = g.split ? g.t0 + (s ^ g.first) + 2 * i : g.t0 + i;
+      const int32_t t = tile0 + i * tile_step;
       uint32_t bad = 0;  // groups of 16 keys whose page is not there
-      if (PAGED && g.gaps) {
+      if (gaps) {
         bool none = false;
         if (lane < kTile / 16)
           none = page_of(a, g.seq, static_cast<int64_t>(t) * kTile + lane * 16) >= a.num_pages;
@@ -1082,8 +1086,8 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       }
       float x[kTile];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        tmem_load32(ts + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
+      for (int b = 0; b < kTile / 16; ++b)
+        tmem_load16(ts + 16 * b, *reinterpret_cast<uint32_t(*)[16]>(x + 16 * b));
       tmem_wait_load();
       const int32_t rel = lim - t * kTile;
       if (rel < kTile || bad != 0) {
@@ -1158,7 +1162,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     // The output. l is 0 only where no key was seen.
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float lse = l == 0.f ? neg_inf() : base * a.c + log2f(l);
-    const int32_t head = g.kh * a.group + head0;
+    const int32_t head = g.kh * a.group + head0, tok = g.tok[qs] + rt;
     T* out = nullptr;
     float *part = nullptr, *lse_at = nullptr;
     // from four values of a partial output to the next
@@ -1239,7 +1243,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     }
     if (lse_at) *lse_at = lse;
 
-    const int32_t seen_tiles = n > 0 ? (g.split ? g.t0 + (s ^ g.first) + 2 * (n - 1) : g.t0 + n - 1) + 1 : 0;
+    const int32_t seen_tiles = n > 0 ? tile0 + (n - 1) * tile_step + 1 : 0;
     uint32_t todo = __ballot_sync(
         ~0u, valid && odd && lim < static_cast<int64_t>(seen_tiles) * kTile);
 #pragma unroll 1
@@ -1267,6 +1271,8 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       if (flse_at && lane == 0) *flse_at = flse;
       __syncwarp();
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->seg_empty[k % kSegs]);
   }
 }
 

@@ -56,6 +56,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -86,15 +96,15 @@ __device__ __forceinline__ void tmem_wait_store() {
 
 // ---- matrix products -----------------------------------------------------
 
-// Shared-memory operand with 128-byte swizzle. `lbo` and `sbo` in bytes.
-// K-major ([rows][64 elements]): sbo = 1024, the step between groups of 8
-// rows; lbo is not used. MN-major ([k][64 elements]): sbo = the step between
-// groups of 8 k, lbo = the step to the next 64 elements.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
-         (static_cast<uint64_t>(lbo >> 4) << 16) | (static_cast<uint64_t>(sbo >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Shared-memory operand with 128-byte swizzle: the low word of its descriptor,
+// which holds the address and `lbo`, in bytes (the high word is the same for
+// all: steps of 1024 bytes between groups of 8 rows or of 8 k). K-major
+// ([rows][64 elements]): lbo is not used. MN-major ([k][64 elements]): lbo =
+// the step to the next 64 elements. Adding bytes / 16 moves the address.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
 }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction descriptor of kind::f16: fp32 accumulators, both operands bf16
 // or both fp16, M = 128.
@@ -103,21 +113,23 @@ __host__ __device__ constexpr uint32_t mma_shape(bool bf16, uint32_t n, bool b_m
          ((b_mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape,
                                        bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
       : "memory");
 }
 // A from tensor memory (two 16-bit elements of a row in each column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape,
                                        bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
       : "memory");
 }
 // Arrives on `bar` when all products issued so far by this thread are done.
