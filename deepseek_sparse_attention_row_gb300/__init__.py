@@ -40,7 +40,6 @@ the device first.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -561,10 +560,9 @@ DTYPE_F16 = 2
 
 
 class _Launch:
-    """One call's device and stream: the tensors' device made current, and
-    (for a given ``stream``) that stream, so that what the call allocates
-    belongs to the stream that it runs on. ``_launch`` makes none for the
-    usual call, on the current stream of the current device."""
+    """The device of a call's tensors made current and, for a given
+    ``stream``, that stream, so that what the call allocates belongs to the
+    stream that it runs on."""
 
     def __init__(self, index, stream):
         torch = _torch()
@@ -583,32 +581,29 @@ class _Launch:
             g.__exit__(*exc)
 
 
-_here = contextlib.nullcontext()
-
-
-def _launch(index: int, stream):
-    torch = _torch()
-    if stream is None and index == torch._C._cuda_getDevice():
-        return _here
-    return _Launch(index, stream)
-
-
-def _current_handle(index: int):
-    """The current stream of a device, as the C calls take it."""
-    return _torch()._C._cuda_getCurrentRawStream(index) or None
+def _call(index: int, stream, enqueue, *args):
+    """``enqueue(*args, stream handle)`` with device ``index`` and ``stream``
+    current; nothing is switched for the usual call, on the current stream of
+    the current device."""
+    c = _torch()._C
+    if stream is None and index == c._cuda_getDevice():
+        return enqueue(*args, c._cuda_getCurrentRawStream(index) or None)
+    with _Launch(index, stream):
+        return enqueue(*args, c._cuda_getCurrentRawStream(index) or None)
 
 
 def _on_gpu(t, dtype, name, dim, index=None):
     """Address, shape and strides of a CUDA tensor of the given type and rank
     on device ``index``."""
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape = t.shape
     if len(shape) != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {tuple(shape)}")
-    if index is not None and t.get_device() != index:
+    if at != index and index is not None:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     return t.data_ptr() or None, shape, t.stride()
 
@@ -619,34 +614,39 @@ def _row_strides(shape, strides, name):
     last = shape[-1]
     if strides[-1] != 1 and last > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    if 1 in shape[:-1]:
+    if 1 in shape:
         return tuple(st if n != 1 else last for n, st in zip(shape[:-1], strides[:-1]))
     return strides[:-1]
 
 
 def _vector(t, name, index):
     """Address and length of a contiguous int32 vector."""
-    ptr, (n,), (st,) = _on_gpu(t, _torch().int32, name, 1, index)
-    if st != 1 and n > 1:
+    at = t.get_device()
+    if at != index or t.dtype is not _torch().int32 or t.dim() != 1:
+        _on_gpu(t, _torch().int32, name, 1, index)
+    n = t.shape[0]
+    if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
-    return ptr, n
+    return t.data_ptr() or None, n
 
 
 def _attention_dtype(t, name):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return DTYPE_BF16
-    if t.dtype == torch.float16:
+    if dt is torch.float16:
         return DTYPE_F16
-    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float16, got {dt}")
 
 
 def _attention_outputs(q, shape, index, out, lse_out):
     """Output tensors (allocated when None) and their addresses and strides."""
     torch = _torch()
     T, H, D = shape
+    device = q.device
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=device)
         o = out.data_ptr(), H * D, D
     else:
         op, oshape, ost = _on_gpu(out, q.dtype, "out", 3, index)
@@ -654,7 +654,7 @@ def _attention_outputs(q, shape, index, out, lse_out):
             raise ValueError(f"out must be {tuple(shape)}, got {tuple(oshape)}")
         o = op, *_row_strides(oshape, ost, "out")
     if lse_out is None:
-        lse_out = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse_out = torch.empty((T, H), dtype=torch.float32, device=device)
         l = lse_out.data_ptr(), H, 1
     else:
         lp, lshape, lst = _on_gpu(lse_out, torch.float32, "lse_out", 2, index)
@@ -693,18 +693,22 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
     (cq, nq), (ck, nk) = _vector(cu_q, "cu_q", dev), _vector(cu_k, "cu_k", dev)
     if nq != nk or nq < 1:
         raise ValueError(f"cu_q and cu_k must have one length of at least 1, got {nq} and {nk}")
-    with _launch(dev, stream):
+    T, H, D = qs
+    Tk, Hkv, _ = ks
+    args = (qp, kp, vp, code, T, Tk, H, Hkv, D, *_row_strides(qs, qst, "q"),
+            *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cq, ck, nq - 1,
+            1 if causal else 0, _scale(scale, D))
+
+    def enqueue(out, lse_out, handle):
         out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
-            workspace, _need("dsa_prompt_workspace_bytes", dev, qs[0], ks[0], qs[1], ks[1], qs[2],
-                             nq - 1), q)
-        st = library().dsa_prompt_attention(
-            qp, kp, vp, code, qs[0], ks[0], qs[1], ks[1], qs[2], *_row_strides(qs, qst, "q"),
-            *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cq, ck, nq - 1,
-            1 if causal else 0, _scale(scale, qs[2]), *outs, ws, ws_bytes, _current_handle(dev))
-    if st:
-        _check("dsa_prompt_attention", st)
-    return out, lse_out
+            workspace, _need("dsa_prompt_workspace_bytes", dev, T, Tk, H, Hkv, D, nq - 1), q)
+        st = library().dsa_prompt_attention(*args, *outs, ws, ws_bytes, handle)
+        if st:
+            _check("dsa_prompt_attention", st)
+        return out, lse_out
+
+    return _call(dev, stream, enqueue, out, lse_out)
 
 
 def prompt_workspace_bytes(total_q: int, total_k: int, heads: int, kv_heads: int, head_dim: int,
@@ -733,7 +737,8 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
     torch = _torch()
     code = _attention_dtype(q, "q")
     dt, dev = q.dtype, q.get_device()
-    qp, (B, H, D), qst = _on_gpu(q, dt, "q", 3)
+    qp, qs, qst = _on_gpu(q, dt, "q", 3)
+    B, H, D = qs
     kp, ks, kst = _on_gpu(k_pages, dt, "k_pages", 4, dev)
     vp, vs, vst = _on_gpu(v_pages, dt, "v_pages", 4, dev)
     tp, (Bt, P), tst = _on_gpu(tables, torch.int32, "tables", 2, dev)
@@ -757,19 +762,21 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
             if page > 0 and n < prefix_len // page:
                 raise ValueError(f"prefix_pages holds {n} pages, prefix_len {prefix_len} needs "
                                  f"{prefix_len // page}")
-    with _launch(dev, stream):
-        out, lse_out, outs = _attention_outputs(q, q.shape, dev, out, lse_out)
+    args = (qp, kp, vp, code, B, H, Hkv, D, N, page, *_row_strides(qs, qst, "q"),
+            *_row_strides(ks, kst, "k_pages"), *_row_strides(vs, vst, "v_pages"), pp, prefix_len,
+            tp, P, tst[0] if B > 1 else P, lp, _scale(scale, D))
+
+    def enqueue(out, lse_out, handle):
+        out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
             workspace, _need("dsa_shared_prefix_workspace_bytes", dev, B, H, Hkv, D, prefix_len, P,
                              page), q)
-        st = library().dsa_shared_prefix_attention(
-            qp, kp, vp, code, B, H, Hkv, D, N, page, *_row_strides((B, H, D), qst, "q"),
-            *_row_strides(ks, kst, "k_pages"), *_row_strides(vs, vst, "v_pages"), pp, prefix_len,
-            tp, P, tst[0] if B > 1 else P, lp, _scale(scale, D), *outs, ws, ws_bytes,
-            _current_handle(dev))
-    if st:
-        _check("dsa_shared_prefix_attention", st)
-    return out, lse_out
+        st = library().dsa_shared_prefix_attention(*args, *outs, ws, ws_bytes, handle)
+        if st:
+            _check("dsa_shared_prefix_attention", st)
+        return out, lse_out
+
+    return _call(dev, stream, enqueue, out, lse_out)
 
 
 def shared_prefix_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int,
@@ -822,13 +829,14 @@ def _cache_state(refs, tables, lens):
     return rp, pages, tp, S, P, ld if S > 1 else P, lp, dev
 
 
-def _cache_planes(cache, pages, index=None):
+def _cache_planes(cache, pages, index):
     """Arguments that describe the page contents [planes, N, page, ...]."""
-    if not cache.is_cuda:
+    at = cache.get_device()
+    if at < 0:
         raise ValueError("cache must be a CUDA tensor")
-    shape, strides, e = cache.shape, cache.stride(), cache.element_size()
-    if index is not None and cache.get_device() != index:
+    if at != index:
         raise ValueError(f"cache is on {cache.device}, expected cuda:{index}")
+    shape, strides, e = cache.shape, cache.stride(), cache.element_size()
     if len(shape) < 3 or shape[1] != pages:
         raise ValueError(f"cache must be [planes, {pages}, page, ...], got {tuple(shape)}")
     inner = 1
@@ -861,7 +869,8 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
     (pp, n), (cp, nc) = _vector(parents, "parents", dev), _vector(children, "children", dev)
     if n != nc:
         raise ValueError(f"{n} parents, {nc} children")
-    with _launch(dev, stream):
+
+    def enqueue(status, handle):
         if status is None:
             status = torch.empty(n, dtype=torch.int32, device=refs.device)
         sp, ns = _vector(status, "status", dev)
@@ -870,10 +879,12 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
         held, ws, ws_bytes = _scratch(
             workspace, _need("dsa_cache_workspace_bytes", dev, n, pages) if n else 0, refs)
         st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp, ws, ws_bytes,
-                                      _current_handle(dev))
-    if st:
-        _check("dsa_cache_fork", st)
-    return status
+                                       handle)
+        if st:
+            _check("dsa_cache_fork", st)
+        return status
+
+    return _call(dev, stream, enqueue, status)
 
 
 def dsa_cache_free(refs, tables, lens, seqs, *, stream=None):
@@ -881,8 +892,7 @@ def dsa_cache_free(refs, tables, lens, seqs, *, stream=None):
     refs go down by one, their rows become -1 and their lengths 0."""
     rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
     sp, n = _vector(seqs, "seqs", dev)
-    with _launch(dev, stream):
-        st = library().dsa_cache_free(rp, pages, tp, S, P, ld, lp, sp, n, _current_handle(dev))
+    st = _call(dev, stream, library().dsa_cache_free, rp, pages, tp, S, P, ld, lp, sp, n)
     if st:
         _check("dsa_cache_free", st)
 
@@ -895,7 +905,8 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
     torch = _torch()
     rp, pages, tp, S, P, ld, _, dev = _cache_state(refs, tables, None)
     planes = _cache_planes(cache, pages, dev)
-    with _launch(dev, stream):
+
+    def enqueue(remap, live, handle):
         if remap is None:
             remap = torch.empty(pages, dtype=torch.int32, device=refs.device)
         if live is None:
@@ -905,11 +916,12 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
             raise ValueError(f"remap must have {pages} entries and live one")
         held, ws, ws_bytes = _scratch(
             workspace, _need("dsa_cache_workspace_bytes", dev, 0, pages), refs)
-        st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp, ws, ws_bytes,
-                                         _current_handle(dev))
-    if st:
-        _check("dsa_cache_compact", st)
-    return remap, live
+        st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp, ws, ws_bytes, handle)
+        if st:
+            _check("dsa_cache_compact", st)
+        return remap, live
+
+    return _call(dev, stream, enqueue, remap, live)
 
 
 def cache_workspace_bytes(pairs: int, num_pages: int) -> int:

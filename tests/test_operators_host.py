@@ -235,7 +235,7 @@ def test_binding_takes_cuda_tensors_only(dsa):
     with pytest.raises(ValueError, match="tables must be a CUDA tensor"):
         dsa.dsa_cache_free(i, t, torch.zeros(3, dtype=torch.int32), i)
     with pytest.raises(ValueError, match="cache must be a CUDA tensor"):
-        dsa._cache_planes(torch.zeros(2, 3, 4, 8), 3)
+        dsa._cache_planes(torch.zeros(2, 3, 4, 8), 3, 0)
 
 
 def test_binding_strides(dsa):
