@@ -30,6 +30,12 @@
 // Every wait is bounded (kWaitTurns); one that gives up records its site in
 // g_pipe_error, and all roles leave.
 //
+// Values that a row does not see have weight 0, which an infinite or NaN value
+// turns into NaN. What lies behind a sequence's end in its last tile (often
+// memory never written) is cleared by a warp of its own before the products;
+// what causal rows do not see of their own sequence is finite in any sane
+// call, and is checked for in the output (fix_row).
+//
 // Code size matters: the roles of an SM run different code at the same time,
 // and a call with short segments runs each piece only a few times. Loops that
 // need no registers as arrays are therefore not unrolled, and each wait and
@@ -92,9 +98,17 @@ struct Seg {
   // prompt: keys [k0, k0 + kv_len); the token before q_end sees all of them
   int32_t k0, kv_len, q_end;
   // pages: the sequence whose own tokens these are (kv_len of them), or -1
-  // for the prefix; whether a page of the segment is missing
+  // for the prefix (kv_len 0); whether a page of the segment is missing
   int32_t seq, gaps;
   int32_t slot;     // of the partial outputs (-1: written out at once)
+
+  // The key tile from which on values lie behind the sequence's last key: the
+  // next sequence's, or what a page holds that is not full.
+  __device__ int32_t tail() const { return kv_len > 0 ? kv_len / kTile : 0x7fffffff; }
+};
+// A V tile with such values, for the warp that clears them.
+struct Tail {
+  int32_t stage, parity, rows;  // the first `rows` values stay
 };
 
 struct AttendArgs {
@@ -138,12 +152,15 @@ struct Layout {
 };
 
 constexpr int kMaxStages = 10;
+constexpr int kTails = 16;  // more than V tiles in the ring
 struct Ctrl {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2][kParts], o_done[2], o_free[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t tail_full[kTails], tail_done[kTails];
   Seg seg[kSegs];
+  Tail tail[kTails];
   uint32_t tmem;
   int dead;
 };
@@ -463,18 +480,23 @@ struct PagedSchedule {
   __device__ explicit PagedSchedule(const AttendArgs& a) {
     const int lane = threadIdx.x & 31;
     prefix_units = units(a);
-    int32_t own_units = 0;
     // CTA 0 also writes down where each sequence's units start.
     const bool first = blockIdx.x == 0;
+    int32_t own_units = 0, mine_next = lane < a.tokens ? own_tokens(a, lane) : 0;
 #pragma unroll 1
     for (int64_t b0 = 0; b0 < a.tokens; b0 += 32) {
       const int64_t b = b0 + lane;
-      int32_t n = 0;
-      if (b < a.tokens) n = own_group(own_tokens(a, b)) * a.kv_heads;
-      const int32_t inc = static_cast<int32_t>(warp_sum_upto(n));
-      if (first && b < a.tokens) a.starts[b] = own_units + inc - n;
-      own_units += __shfl_sync(~0u, inc, 31);
+      const int32_t n = own_group(mine_next) * a.kv_heads;
+      mine_next = b + 32 < a.tokens ? own_tokens(a, b + 32) : 0;
+      if (first) {
+        const int32_t inc = static_cast<int32_t>(warp_sum_upto(n));
+        if (b < a.tokens) a.starts[b] = own_units + inc - n;
+        own_units += __shfl_sync(~0u, inc, 31);
+      } else {
+        own_units += n;  // the lane's share of the sum
+      }
     }
+    if (!first) own_units = __shfl_sync(~0u, warp_sum_upto(own_units), 31);
     if (first && lane == 0) a.starts[a.tokens] = own_units;
     const int32_t all = prefix_units + own_units, share = share_of(a, all, gridDim.x);
     const int64_t from = static_cast<int64_t>(share) * blockIdx.x;
@@ -601,12 +623,14 @@ __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s
                                      int32_t tok, int32_t head, float (&acc)[4], float& lse) {
   const int lane = threadIdx.x & 31;
   const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s ^ g.first : 0);
+  // nothing is hidden behind the sequence's end: that was cleared
+  const int64_t end = g.kv_len > 0 ? g.kv_len : INT64_MAX;
   bool hidden = false;
 #pragma unroll 1
   for (int32_t i = 0; i < g.n[s]; ++i) {
     const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
 #pragma unroll 1
-    for (int64_t j = max(k0, static_cast<int64_t>(lim)); j < k0 + kTile; ++j) {
+    for (int64_t j = max(k0, static_cast<int64_t>(lim)); j < min(k0 + kTile, end); ++j) {
       const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
       if (!v) continue;
 #pragma unroll 1
@@ -821,12 +845,25 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
   Place<true> p, q;  // of the values and of the scores
   if (!q.next(c, false, 17) || !p.next(c, true, 17)) return;
   int ahead = 0;
+  uint32_t tails = 0;
   uint32_t p_ids = look_up(p), q_ids = p_ids;
 #pragma unroll 1
   while (p.more) {
     bool values, scores;
     order(p, q, ahead, values, scores);
-    if (values && !put(vm, p, p_ids)) return;
+    if (values) {
+      const Ring<DP> at = ring;
+      if (!put(vm, p, p_ids)) return;
+      if (p.g.t0 + p.j >= p.g.tail()) {
+        const uint32_t i = tails++ % kTails;
+        if (lane == 0) {
+          c->tail[i] = Tail{at.stage, static_cast<int32_t>(at.round & 1),
+                            p.g.kv_len - (p.g.t0 + p.j) * kTile};
+          mbar_arrive(&c->tail_full[i]);
+        }
+        __syncwarp();
+      }
+    }
     if (scores) {
       if (q.j == 0) {
         // Split segments take the two row-tile buffers in turn, so that the
@@ -866,6 +903,11 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
       ahead -= values;
     }
   }
+  if (lane == 0) {
+    c->tail[tails % kTails].stage = -1;  // no more
+    mbar_arrive(&c->tail_full[tails % kTails]);
+  }
+  __syncwarp();
   // The last arrivals of the products on these barriers come before the
   // shared memory is given back.
 #pragma unroll 1
@@ -876,6 +918,35 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
 #pragma unroll 1
   for (int i = 0; i < 2; ++i)
     if (((used >> i) & 1) && !wait_warp(&c->q_empty[i], (phase >> i) & 1, c, 18)) return;
+}
+
+// The warp that clears V tiles behind their sequences' ends.
+template <int DP>
+__device__ void clear_tails(Cta<DP> cta) {
+  using L = Layout<DP>;
+  Ctrl* c = cta.ctrl();
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (uint32_t k = 0;; ++k) {
+    const int i = k % kTails;
+    if (!wait_warp(&c->tail_full[i], (k / kTails) & 1, c, 29)) return;
+    const Tail t = c->tail[i];
+    if (t.stage < 0) return;
+    if (!wait_warp(&c->kv_full[t.stage], t.parity, c, 30)) return;
+    // 16-byte pieces of the rows behind the end; swizzling keeps a row's
+    // pieces within the row
+    const int first = t.rows * 8;
+#pragma unroll 1
+    for (int j = first + lane; j < kTile * 8; j += 32) {
+#pragma unroll
+      for (int h = 0; h < L::kHalves; ++h)
+        *reinterpret_cast<uint4*>(cta.stage(t.stage) + h * L::kHalf + j * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->tail_done[i]);
+  }
 }
 
 // The thread that issues the products. In program order: the values of a
@@ -913,6 +984,11 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
     }
     mma_commit(&c->s_full[s]);
   };
+  uint32_t tails = 0;
+  const auto clean = [&]() {
+    const uint32_t k = tails++;
+    return wait(&c->tail_done[k % kTails], (k / kTails) & 1, c, 31);
+  };
   // P V of stream s
   const auto values = [&](int s, bool first, int stage) -> bool {
     if (first) {
@@ -948,6 +1024,7 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
       const Seg& g = p.g;
       const int32_t n = p.n;
       const int tiles = g.ntok[1] > 0 ? 2 : 1;
+      const int32_t tail = g.tail() - g.t0;
       if (n > 0) {
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
@@ -969,6 +1046,7 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
           for (int i = 0; i < tiles; ++i) mma_commit(&c->q_empty[i]);
         }
         if (!full()) return;
+        if (j >= tail && !clean()) return;
         const int v = ring.stage;
         ring.next();
         bool have = false;
@@ -1003,6 +1081,7 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
       if (late) {
         if (ahead == 0) break;
         if (!full()) return;
+        if (p.g.t0 + p.j >= p.g.tail() && !clean()) return;
         const int v = ring.stage;
         ring.next();
         if (!values((p.j & 1) ^ p.g.first, p.j < 2, v)) return;
@@ -1304,6 +1383,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(&c->seg_full[i], 1);
       mbar_init(&c->seg_empty[i], 10);  // the loading and multiplying roles, eight warps
     }
+    for (int i = 0; i < kTails; ++i) {
+      mbar_init(&c->tail_full[i], 1);
+      mbar_init(&c->tail_done[i], 1);
+    }
     c->dead = 0;
     mbar_init_fence();
   }
@@ -1338,6 +1421,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       load<DP, PAGED>(a, &qm, &q1, &km, &vm, cta);
     } else if (warp == 10) {
       schedule<DP, PAGED>(a, cta);
+    } else {
+      clear_tails<DP>(cta);
     }
   }
   __syncwarp();
@@ -1479,7 +1564,7 @@ __global__ void __launch_bounds__(kJoinRows)
     return (2 * (x + i) + (i == 0)) * 256 + s * kTile;
   };
   float m = neg_inf();
-#pragma unroll 1
+#pragma unroll 4
   for (int32_t i = 0; i <= cut.more; ++i) m = fmaxf(m, a.prefix_lse[tile_at(i) + row]);
   const float base = m == neg_inf() ? 0.f : m;
   float sum = 0.f;
@@ -1487,7 +1572,7 @@ __global__ void __launch_bounds__(kJoinRows)
 #pragma unroll
   for (int d = 0; d < kJoinCols; ++d) acc[d] = 0.f;
   const int d0 = blockIdx.y * kJoinCols;
-#pragma unroll 1
+#pragma unroll 2
   for (int32_t i = 0; i <= cut.more; ++i) {
     const int64_t r = tile_at(i);
     const float w = ex2(a.prefix_lse[r + row] - base);
