@@ -108,7 +108,7 @@ struct Seg {
 };
 // A V tile with such values, for the warp that clears them.
 struct Tail {
-  int32_t stage, parity, rows;  // the first `rows` values stay
+  int32_t stage, parity, from, to;  // the rows to clear
 };
 
 struct AttendArgs {
@@ -805,11 +805,11 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
   const uint32_t none = static_cast<uint32_t>(a.num_pages);
   const auto look_up = [&](const Place<true>& p) -> uint32_t {
     if (!PAGED || !p.more) return none;
-    // the list's table, from its first page on, and how many pages it has
+    // the list's table, from its first page on, and how many pages are seen
     const int32_t pre = static_cast<int32_t>(a.prefix_len >> a.page_log2);
     const bool own = p.g.seq >= 0;
     const int32_t* table = own ? a.tables + p.g.seq * a.ld_tables + pre : a.prefix_pages;
-    const int32_t count = own ? static_cast<int32_t>(a.max_pages) - pre : pre;
+    const int32_t count = own ? (p.g.kv_len + a.page_size - 1) >> a.page_log2 : pre;
     const int32_t at = (((p.g.t0 + p.j) * kTile) >> a.page_log2) + lane;
     return lane < pages && at < count ? static_cast<uint32_t>(__ldg(table + at)) : none;
   };
@@ -857,8 +857,10 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
       if (p.g.t0 + p.j >= p.g.tail()) {
         const uint32_t i = tails++ % kTails;
         if (lane == 0) {
-          c->tail[i] = Tail{at.stage, static_cast<int32_t>(at.round & 1),
-                            p.g.kv_len - (p.g.t0 + p.j) * kTile};
+          // whole pages behind the end are not loaded (zeros are)
+          const int32_t from = p.g.kv_len - (p.g.t0 + p.j) * kTile;
+          const int32_t to = PAGED ? min((from + a.page_size - 1) & -a.page_size, kTile) : kTile;
+          c->tail[i] = Tail{at.stage, static_cast<int32_t>(at.round & 1), from, to};
           mbar_arrive(&c->tail_full[i]);
         }
         __syncwarp();
@@ -935,9 +937,8 @@ __device__ void clear_tails(Cta<DP> cta) {
     if (!wait_warp(&c->kv_full[t.stage], t.parity, c, 30)) return;
     // 16-byte pieces of the rows behind the end; swizzling keeps a row's
     // pieces within the row
-    const int first = t.rows * 8;
-#pragma unroll 1
-    for (int j = first + lane; j < kTile * 8; j += 32) {
+#pragma unroll 2
+    for (int j = t.from * 8 + lane; j < t.to * 8; j += 32) {
 #pragma unroll
       for (int h = 0; h < L::kHalves; ++h)
         *reinterpret_cast<uint4*>(cta.stage(t.stage) + h * L::kHalf + j * 16) =
