@@ -139,6 +139,59 @@ def test_prompt_one_token_views(env):
     check_prompt(env, odd, k, v, [1], [9], True)
 
 
+def test_broadcast_heads(env):
+    """One key/value head expanded to several (a stride of 0)."""
+    torch, dsa = env
+    q, k, v = make(torch, 33, 90, 150, 4, 1, 64, torch.bfloat16)
+    ke, ve = k.expand(-1, 2, -1), v.expand(-1, 2, -1)
+    want, want_lse = check_prompt(env, q, k.repeat(1, 2, 1), v.repeat(1, 2, 1), [90], [150], True)
+    out, lse = dsa.dsa_prompt_attention(q, ke, ve, ints(torch, [0, 90]), ints(torch, [0, 150]))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import test_attention_gpu as t
+import deepseek_sparse_attention_row_gb300 as dsa
+q, k, v = t.make(torch, 40, 100, 3000, 8, 2, 128, torch.bfloat16)
+cu_q, cu_k = t.ints(torch, [0, 100]), t.ints(torch, [0, 3000])
+p = t.make_paged(torch, 41, 5, 8, 2, 64, 16, 32, [3, 0, 40, 17, 90], torch.bfloat16)
+c = torch.zeros(2, 9, 16, 8, dtype=torch.bfloat16, device="cuda")
+refs = t.ints(torch, [1] + [0] * 8)
+tables, lens = t.ints(torch, [[0, -1], [-1, -1]]), t.ints(torch, [5, 0])
+who, kid = t.ints(torch, [0]), t.ints(torch, [1])
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = dsa.dsa_prompt_attention(q, k, v, cu_q, cu_k)
+    b = dsa.dsa_shared_prefix_attention(*p, 32)
+    dsa.dsa_cache_free(refs, tables, lens, kid)
+    st = dsa.dsa_cache_fork(c, refs, tables, lens, who, kid)
+    m = dsa.dsa_cache_compact(c, refs, tables)
+g.replay()
+torch.cuda.synchronize()
+t.check_prompt((torch, dsa), q, k, v, [100], [3000], True)
+t.check_paged((torch, dsa), *p, 32)
+assert torch.equal(a[0], dsa.dsa_prompt_attention(q, k, v, cu_q, cu_k)[0])
+assert torch.equal(b[0], dsa.dsa_shared_prefix_attention(*p, 32)[0])
+assert st.tolist() == [0] and tables.tolist() == [[0, -1], [1, -1]] and m[1].tolist() == [2]
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured(env):
+    import os
+    import subprocess
+    import sys
+
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout + res.stderr
+
+
 def test_prompt_rows_of_no_sequence(env):
     """Rows before the first and behind the last sequence stay as they were,
     and what lies there is not read into any result."""
@@ -464,10 +517,11 @@ def test_own_workspace(env):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("ql,kl", [
     ([1, 1], [9000, 3]),                     # one block across many CTAs
+    ([2], [40000]),
     ([700, 0, 33, 300], [2500, 10, 0, 900]),
     ([2100, 5], [1500, 3000]),               # rows without keys, then few with many
     ([9] * 300, [40] * 300),
-], ids=str)
+], ids=["one block", "long and alone", "mixed", "few queries", "many"])
 def test_prompt_blocks_cut_between_ctas(env, ql, kl, causal):
     """More keys than the kernel leaves whole: blocks are cut between CTAs and
     their parts joined, at odd places."""
