@@ -238,7 +238,8 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int
 // the block begins in an earlier share, 2 x + 1 where it goes on in the next,
 // and join_blocks_kernel joins them.
 // Without cuts (a.cut = 0: few keys, where the join would cost more than it
-// evens out) every block is one unit.
+// evens out) every block is one unit. kBlockCost = 2, 4, 6, 8 tiles: packed
+// prefill chunk 411, 367, 369, 375 us, one long prompt 776, 647, 687, 699.
 constexpr int32_t kBlockCost = 4 * kTile;
 constexpr int32_t kMinShare = 4 * kTile;
 
@@ -441,10 +442,13 @@ __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
 // as long as it is dear: kSegCost for itself and a cost for each of its key
 // tiles, which falls to the share that holds the tile's first unit. A share is
 // a list of segments, a group's tiles each; segment (group g, CTA x) has slot
-// g + x, which grows along the line: no two segments share one.
+// g + x, which grows along the line: no two segments share one. The costs are
+// fitted: (group, one row tile, two) = (12, 4, 6) gave 53.6 us for 64 chat
+// sequences behind 8192 shared tokens and 114 for 128 behind 32768; (8, 4, 5)
+// 57 and 115, (12, 4, 7) 54.6 and 124, (20, 4, 7) 53.7 and 117.
 constexpr int32_t kSegCost = 12;
 constexpr int32_t kTileCost = 4;        // one row tile
-constexpr int32_t kTwoTileCost = 7;     // two row tiles, bound by products
+constexpr int32_t kTwoTileCost = 6;     // two row tiles, bound by products
 
 struct PagedSchedule {
   int32_t pos, end, prefix_units;
@@ -1546,8 +1550,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 // The partial outputs of the blocks that are cut: CTAs (x, y) join the block
 // that begins in share x and goes on, one row per thread, 32 columns each
-// (with all columns in one thread the launch took 15.5 us for a packed prefill
-// chunk, so FIXME).
+// (14 us for 152 cut blocks of 256 rows, two parts each: 40 MB of fp32 parts;
+// 15.5 us with all 128 columns in one thread).
 constexpr int kJoinRows = 2 * kTile;
 constexpr int kJoinCols = 32;
 
