@@ -43,6 +43,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from typing import Optional
 
 __all__ = [
@@ -681,7 +682,7 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
     when None) and returns both; rows that see no key get 0 and -inf, rows of
     no sequence are left as they were. ``workspace``: a CUDA uint8 tensor of
     ``prompt_workspace_bytes(...)`` bytes that no overlapping call uses
-    (allocated when None). Forward only: the outputs carry no autograd
+    (None: one kept for this thread and stream). Forward only: the outputs carry no autograd
     graph."""
     code = _attention_dtype(q, "q")
     dt, dev = q.dtype, q.get_device()
@@ -702,7 +703,8 @@ def dsa_prompt_attention(q, k, v, cu_q, cu_k, *, causal: bool = True, scale=None
     def enqueue(out, lse_out, handle):
         out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
-            workspace, _need("dsa_prompt_workspace_bytes", dev, T, Tk, H, Hkv, D, nq - 1), q)
+            workspace, _need("dsa_prompt_workspace_bytes", dev, T, Tk, H, Hkv, D, nq - 1), q,
+            handle)
         st = library().dsa_prompt_attention(*args, *outs, ws, ws_bytes, handle)
         if st:
             _check("dsa_prompt_attention", st)
@@ -733,7 +735,7 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
     returns both; a sequence that sees no token gets 0 and -inf.
     ``workspace``: a CUDA uint8 tensor of
     ``shared_prefix_workspace_bytes(...)`` bytes that no overlapping call
-    uses (allocated when None)."""
+    uses (None: one kept for this thread and stream)."""
     torch = _torch()
     code = _attention_dtype(q, "q")
     dt, dev = q.dtype, q.get_device()
@@ -770,7 +772,7 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
         out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
             workspace, _need("dsa_shared_prefix_workspace_bytes", dev, B, H, Hkv, D, prefix_len, P,
-                             page), q)
+                             page), q, handle)
         st = library().dsa_shared_prefix_attention(*args, *outs, ws, ws_bytes, handle)
         if st:
             _check("dsa_shared_prefix_attention", st)
@@ -792,17 +794,32 @@ def _need(name: str, index: int, *sizes) -> int:
     return getattr(library(), name)(*sizes)
 
 
-def _scratch(workspace, need: int, like):
+_KEEP_BYTES = 64 << 20
+_scratch_cache = {}
+
+
+def _scratch(workspace, need: int, like, handle):
     """A call's workspace, held until the call is enqueued, with its address
-    and bytes: the caller's tensor, or a new one on ``like``'s device. A new
-    one comes from the allocator of the current stream (of the graph, in a
-    capture), which hands its memory on only behind this call."""
+    and bytes: the caller's tensor, or one of its own on ``like``'s device.
+
+    Its own one is kept for the next call of this thread on this stream, whose
+    calls follow each other; larger ones than 64 MiB, and those of a capture
+    (whose graph may run beside other calls), come from the allocator of the
+    current stream or graph, which hands their memory on only behind this
+    call."""
     if workspace is None:
         if not need:
             return None, None, 0
         torch = _torch()
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        return workspace, workspace.data_ptr(), need
+        if need > _KEEP_BYTES or torch._C._cuda_isCurrentStreamCapturing():
+            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+            return workspace, workspace.data_ptr(), need
+        key = threading.get_ident(), like.get_device(), handle
+        kept = _scratch_cache.get(key)
+        if kept is None or kept[2] < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+            kept = _scratch_cache[key] = workspace, workspace.data_ptr(), need
+        return kept
     if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     n = workspace.numel() * workspace.element_size()
@@ -877,7 +894,7 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
         if ns != n:
             raise ValueError(f"status holds {ns} entries, expected {n}")
         held, ws, ws_bytes = _scratch(
-            workspace, _need("dsa_cache_workspace_bytes", dev, n, pages) if n else 0, refs)
+            workspace, _need("dsa_cache_workspace_bytes", dev, n, pages) if n else 0, refs, handle)
         st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp, ws, ws_bytes,
                                        handle)
         if st:
@@ -915,7 +932,7 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
         if n != pages or one != 1:
             raise ValueError(f"remap must have {pages} entries and live one")
         held, ws, ws_bytes = _scratch(
-            workspace, _need("dsa_cache_workspace_bytes", dev, 0, pages), refs)
+            workspace, _need("dsa_cache_workspace_bytes", dev, 0, pages), refs, handle)
         st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp, ws, ws_bytes, handle)
         if st:
             _check("dsa_cache_compact", st)

@@ -514,6 +514,45 @@ def test_own_workspace(env):
         dsa.dsa_prompt_attention(q, k, v, *cu, workspace=buf[:need - 1])
 
 
+def test_calls_at_the_same_time(env):
+    """Threads that call on one stream and on streams of their own, and a
+    replayed graph beside them: no call disturbs another."""
+    import threading
+
+    torch, dsa = env
+    q, k, v = make(torch, 34, 300, 6000, 8, 2, 64, torch.bfloat16)
+    cu = ints(torch, [0, 300]), ints(torch, [0, 6000])
+    p = make_paged(torch, 35, 20, 8, 2, 64, 16, 160, [7 * i for i in range(20)], torch.bfloat16)
+    want = (*check_prompt(env, q, k, v, [300], [6000], True), *check_paged(env, *p, 160))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        graphed = (*dsa.dsa_prompt_attention(q, k, v, *cu),
+                   *dsa.dsa_shared_prefix_attention(*p, 160))
+    main, bad = torch.cuda.current_stream(), []
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            got = [(*dsa.dsa_prompt_attention(q, k, v, *cu),
+                    *dsa.dsa_shared_prefix_attention(*p, 160)) for _ in range(15)]
+        stream.synchronize()
+        bad.extend(1 for r in got if not all(torch.equal(x, y) for x, y in zip(r, want)))
+
+    streams = [main, main, torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(s,)) for s in streams]
+    for t in threads:
+        t.start()
+    beside = torch.cuda.Stream()
+    with torch.cuda.stream(beside):
+        for _ in range(15):
+            g.replay()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+    assert all(torch.equal(x, y) for x, y in zip(graphed, want))
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("ql,kl", [
     ([1, 1], [9000, 3]),                     # one block across many CTAs
