@@ -1371,28 +1371,29 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   cta.base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);  // swizzle atoms are 1 KiB
   Ctrl* c = cta.ctrl();
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
+  if (warp == 0) {  // each lane the barriers of its number
+    const int i = threadIdx.x;
+    if (i < L::kStages) {
       mbar_init(&c->kv_full[i], 1);
       mbar_init(&c->kv_empty[i], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&c->q_full[s], 1);
-      mbar_init(&c->q_empty[s], 1);
-      mbar_init(&c->s_full[s], 1);
-      for (int p = 0; p < kParts; ++p) mbar_init(&c->p_full[s][p], kTile);
-      mbar_init(&c->o_done[s], 1);
-      mbar_init(&c->o_free[s], kTile);
+    if (i < 2) {
+      mbar_init(&c->q_full[i], 1);
+      mbar_init(&c->q_empty[i], 1);
+      mbar_init(&c->s_full[i], 1);
+      for (int p = 0; p < kParts; ++p) mbar_init(&c->p_full[i][p], kTile);
+      mbar_init(&c->o_done[i], 1);
+      mbar_init(&c->o_free[i], kTile);
     }
-    for (int i = 0; i < kSegs; ++i) {
+    if (i < kSegs) {
       mbar_init(&c->seg_full[i], 1);
       mbar_init(&c->seg_empty[i], 10);  // the loading and multiplying roles, eight warps
     }
-    for (int i = 0; i < kTails; ++i) {
+    if (i < kTails) {
       mbar_init(&c->tail_full[i], 1);
       mbar_init(&c->tail_done[i], 1);
     }
-    c->dead = 0;
+    if (i == 0) c->dead = 0;
     mbar_init_fence();
   }
   if (warp == 8) {

@@ -83,7 +83,8 @@ size_t dsa_prompt_workspace_bytes(int64_t total_q, int64_t total_k,
  * cu_k or out (or k or v with total_k > 0), or a workspace that is too small.
  * DSA_EUNSUPPORTED for
  * DSA_DTYPE_F32, head_dim over 128 or no multiple of 8, heads / kv_heads >
- * 128, layouts other than above, and sizes from 2^31.
+ * 128, layouts other than above, and sizes from 2^31 (total_k from 2^31 -
+ * 4096).
  */
 dsa_status dsa_prompt_attention(const void *q, const void *k, const void *v,
                                 int32_t dtype, int64_t total_q, int64_t total_k,
@@ -137,8 +138,9 @@ size_t dsa_shared_prefix_workspace_bytes(int64_t batch, int32_t heads,
  * batch == 0 or heads == 0: DSA_OK, nothing written. DSA_EINVAL and
  * DSA_EUNSUPPORTED as for dsa_prompt_attention, and DSA_EINVAL for a
  * prefix_len that is negative, no multiple of page_size or over max_pages *
- * page_size, a NULL required pointer or a workspace that is too small;
- * DSA_EUNSUPPORTED for another page_size.
+ * page_size, a NULL required pointer or a workspace that is too small or not
+ * aligned; DSA_EUNSUPPORTED for another page_size, and where batch * kv_heads
+ * times the 128-token tiles that a row of `tables` has room for passes 10^8.
  */
 dsa_status dsa_shared_prefix_attention(
     const void *q, const void *k_pages, const void *v_pages, int32_t dtype,
