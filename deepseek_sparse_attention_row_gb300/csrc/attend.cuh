@@ -3,11 +3,13 @@
 //
 // Mathematics. For a row q over the keys that it sees (c = scale * log2 e):
 // x_j = c <q, k_j>, m = max x_j, l = sum 2^(x_j - m), O = sum 2^(x_j - m) v_j.
-// Keys go by in tiles of 128. Per tile the row keeps a base b <= m + 8 / c
-// (in units of <q, k>) and adds 2^(c (s_j - b)) to l and to O; only when a new
+// Keys go by in tiles of 128. The row keeps a base b, m - 8 / c <= b <= m (in
+// units of <q, k>), and adds 2^(c (s_j - b)) to l and to O; only when a new
 // maximum passes the base by more than 2^8 in weight are l and O multiplied
 // down and the base moved. Weights then stay below 2^8, and the largest is at
 // least 1, so that neither fp32 sums nor 16-bit weights lose anything by it.
+// Weights are rounded to the operands' type for the product with V: the tensor
+// cores take one type for both operands. l sums them unrounded.
 //
 // Rows. The G query heads of one key/value head share every key, so a matrix
 // tile of 128 rows holds 128 / G tokens of G heads each.
@@ -24,8 +26,15 @@
 // results are two partial outputs).
 //
 // A persistent CTA walks a list of segments (row tiles x a range of key
-// tiles) that the scheduling warp writes to a two-entry ring, so that loads
-// of the next segment run under the current one's end.
+// tiles) that the scheduling warp writes to a ring of eight, so that loads and
+// products of the next segment run under the current one's end.
+//
+// What bounds it. Prompts: the tensor cores, active in 77% of the cycles (one
+// full attention of 8192 tokens, 16 heads of 128: 315 us, 1745 TFLOP/s, 0.91
+// of a plain product's burst rate; 16389 causal tokens: 640 us, 1715); the rest
+// is the chain scores - softmax - weights of a stream, about 1100 cycles of
+// softmax a tile, and the ends of segments. Decode on pages: HBM (64 sequences
+// of up to 4096 tokens: 96 us for 527 MB with the join; the loads alone 93).
 //
 // Every wait is bounded (kWaitTurns); one that gives up records its site in
 // g_pipe_error, and all roles leave.
@@ -1451,7 +1460,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
 // One warp per (sequence, head): the partial outputs of its prefix segments
 // and of its own ones, weighted by 2^(lse_i - F) with F the log-sum-exp of
-// their log-sum-exps.
+// their log-sum-exps. Bound by its chain of loads (starts, log-sum-exps,
+// outputs): 9 us for 2048 rows, launched under the kernel before it.
 struct JoinArgs {
   void* out;
   int64_t o_sb, o_sh;
