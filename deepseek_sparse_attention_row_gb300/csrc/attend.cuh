@@ -1134,7 +1134,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
   const int32_t rt = row / a.group, head0 = row % a.group;  // token of the tile, head of the group
   const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
   const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kTile;
-  const float grow = kGrow / a.c;
+  const float grow = fminf(kGrow / a.c, 3e38f);  // finite, so that -inf + grow stays -inf
   uint32_t done = 0;
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {

@@ -111,6 +111,17 @@ def test_prompt_scale(env, scale):
     check_prompt(env, q, k, v, [150], [150], True, scale)
 
 
+@pytest.mark.parametrize("scale", [2e-38, 1e-30])
+def test_scales_that_make_all_keys_equal(env, scale):
+    """8 / (scale log2 e) overflows for the first: the base has to move all the
+    same, and the sums are those of equal weights."""
+    torch, _ = env
+    q, k, v = make(torch, 36, 40, 300, 4, 2, 64, torch.bfloat16)
+    check_prompt(env, q, k, v, [40], [300], True, scale)
+    p = make_paged(torch, 37, 3, 4, 2, 64, 16, 32, [20, 0, 150], torch.bfloat16)
+    check_paged(env, *p, 32, scale=scale)
+
+
 def test_prompt_strided(env):
     """Views: a fused [T, H + 2 Hkv, D] projection, head-major tensors, padded
     heads; outputs into views, the bytes around them untouched."""
