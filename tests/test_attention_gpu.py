@@ -234,6 +234,24 @@ def test_prompt_offsets_are_clamped(env):
     ref.check(lse, want[1], want[3], "lse")
 
 
+@pytest.mark.parametrize("total_k", [120, 9000])
+def test_prompt_offsets_that_decrease(env, total_k):
+    """Rows are unspecified then, and nothing else is: the call ends, writes
+    only rows of out and lse, and leaves the next call alone."""
+    torch, dsa = env
+    q, k, v = make(torch, 38, 90, total_k, 4, 2, 64, torch.bfloat16)
+    out = torch.full((94, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((94, 4), 4.0, device="cuda")
+    for a, b in (([60, 10, 90, 0, 80], [0, total_k, 50, 100, 7]),
+                 ([2 ** 31 - 1, -2 ** 31, 45, 44, 90], [total_k, 0, total_k, 0, total_k])):
+        dsa.dsa_prompt_attention(q, k, v, ints(torch, a), ints(torch, b), out=out[2:92],
+                                 lse_out=lse[2:92])
+        torch.cuda.synchronize()
+        for t, x in ((out, 3.0), (lse, 4.0)):
+            assert (t[:2] == x).all() and (t[92:] == x).all()
+    check_prompt(env, q, k, v, [50, 40], [60, total_k - 60], True)
+
+
 @pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 def test_prompt_masked_places_hold_anything(env, what, dtype):
