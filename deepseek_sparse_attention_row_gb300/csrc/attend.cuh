@@ -257,6 +257,17 @@ struct CutBlock {
   int32_t tok, ntok[2], kh;
   int32_t more;  // CTAs behind this one that hold parts; 0: no block is cut here
 };
+// Whether CTA x of `ctas` left a block to join, with all of its parts in the
+// workspace and its rows in the output. Every share keeps to that while the
+// offsets stay as they are; a caller who changes them under the call gets
+// wrong rows, but no access out of range.
+__host__ __device__ inline bool joinable(const CutBlock& b, const AttendArgs& a, int64_t x,
+                                         int64_t ctas) {
+  return b.more > 0 && b.more < ctas - x && b.tok >= 0 && b.ntok[0] >= 0 &&
+         b.ntok[0] <= a.tile_tokens && b.ntok[1] >= 0 && b.ntok[1] <= a.tile_tokens &&
+         static_cast<int64_t>(b.tok) + b.ntok[0] + b.ntok[1] <= a.tokens && b.kh >= 0 &&
+         b.kh < a.kv_heads;
+}
 
 struct PromptSchedule {
   int64_t pos, end, share;
@@ -265,7 +276,6 @@ struct PromptSchedule {
   int32_t l_q0, l_q1, l_k0, l_k1;
   int32_t lane_of = -1;  // lane of the current sequence
   int32_t q0, q1, k0, kv, blocks, kh, b;
-  bool cut_here = false;
 
   __device__ void hold(const AttendArgs& a) {
     const int32_t i = chunk + (threadIdx.x & 31);
@@ -316,6 +326,9 @@ struct PromptSchedule {
   }
 
   __device__ explicit PromptSchedule(const AttendArgs& a) {
+    // No block is cut here until next() says so: before any wait, so that the
+    // join finds no stale entry where a wait gives up.
+    if (a.cut && (threadIdx.x & 31) == 0) a.cuts[blockIdx.x].more = 0;
     int64_t all = 0;
 #pragma unroll 1
     for (chunk = 0; chunk < a.seqs; chunk += 32) {
@@ -368,11 +381,7 @@ struct PromptSchedule {
     const int32_t block = 2 * a.tile_tokens;
 #pragma unroll 1
     for (;;) {
-      if (pos >= end) {
-        if (!cut_here && (threadIdx.x & 31) == 0 && a.cut) a.cuts[blockIdx.x].more = 0;
-        cut_here = true;
-        return false;
-      }
+      if (pos >= end) return false;
       const int32_t e = min((b + 1) * static_cast<int64_t>(block), static_cast<int64_t>(q1 - q0));
       const int32_t keys = keys_of(a, q1 - q0, kv, e), cost = cost_of(a, keys);
       const int32_t from = static_cast<int32_t>(pos - start);
@@ -422,14 +431,10 @@ struct PromptSchedule {
       g.slot = -1;
       if (t1 - t0 < tiles) {
         g.slot = 2 * static_cast<int32_t>(blockIdx.x) + (t0 == 0);
-        if (t0 == 0) {
-          cut_here = true;
-          if ((threadIdx.x & 31) == 0) {
-            const int64_t last =
-                (at + kBlockCost + static_cast<int64_t>(tiles - 1) * kTile) / share;
-            a.cuts[blockIdx.x] = CutBlock{tok, {g.ntok[0], g.ntok[1]}, my_kh,
-                                          static_cast<int32_t>(last - blockIdx.x)};
-          }
+        if (t0 == 0 && (threadIdx.x & 31) == 0) {
+          const int64_t last = (at + kBlockCost + static_cast<int64_t>(tiles - 1) * kTile) / share;
+          a.cuts[blockIdx.x] = CutBlock{tok, {g.ntok[0], g.ntok[1]}, my_kh,
+                                        static_cast<int32_t>(last - blockIdx.x)};
         }
       }
       return true;
@@ -1571,7 +1576,7 @@ __global__ void __launch_bounds__(kJoinRows)
     join_blocks_kernel(const __grid_constant__ AttendArgs a) {
   follow();
   const CutBlock cut = a.cuts[blockIdx.x];
-  if (cut.more == 0) return;
+  if (!joinable(cut, a, blockIdx.x, gridDim.x)) return;
   const int s = threadIdx.x >> 7, row = threadIdx.x & 127, rt = row / a.group;
   if (rt >= cut.ntok[s]) return;
   const int64_t x = blockIdx.x;
