@@ -67,11 +67,12 @@ constexpr int kAttendThreads = 384;  // no calls in the kernel: ptxas could not 
 constexpr int kParts = 2;            // parts of a weight tile handed to the products one by one
 constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's base
 constexpr int kSegs = 8;             // segments that the scheduling warp may be ahead
-// A wait gives up between its second and third turn of the global timer's high
-// word, after 8.6 to 12.9 seconds: a row's recomputation (fix_row) may hold up
-// its CTA's other roles for seconds when a huge context holds infinities in
-// masked places.
-constexpr uint32_t kWaitTurns = 3;
+// A wait gives up when its CTA has got on with nothing between the second and
+// third turn of the global timer's high word, for 8.6 to 12.9 seconds. What
+// counts are the loads (each round of the ring) and the rows that fix_row goes
+// through: a wait may be as long as the call, like that for the next value
+// behind a sequence's end, of which a call may have none.
+constexpr int32_t kWaitTurns = 3;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -171,6 +172,7 @@ struct Ctrl {
   Seg seg[kSegs];
   Tail tail[kTails];
   uint32_t tmem;
+  uint32_t beat;  // global_turns() when the CTA last got on
   int dead;
 };
 constexpr size_t attend_smem(uint32_t ctrl) { return 1024 + ctrl + sizeof(Ctrl); }
@@ -180,14 +182,17 @@ __device__ __forceinline__ uint32_t global_turns() {
   asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(t));
   return t;
 }
+__device__ __forceinline__ void get_on(Ctrl* c) {
+  *reinterpret_cast<volatile uint32_t*>(&c->beat) = global_turns();
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctrl* c, unsigned site) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint32_t t0 = global_turns();
 #pragma unroll 1
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&c->dead)) return false;
-    if (global_turns() - t0 >= kWaitTurns) {
+    const uint32_t beat = *reinterpret_cast<volatile uint32_t*>(&c->beat);
+    if (static_cast<int32_t>(global_turns() - beat) >= kWaitTurns) {
       atomicCAS(&g_pipe_error, 0u, site);
       *reinterpret_cast<volatile int*>(&c->dead) = 1;
       return false;
@@ -637,8 +642,8 @@ __device__ __forceinline__ const T* row_at(const AttendArgs& a, const Seg& g, co
 // again from its own keys alone. Returns false where no such value exists.
 // On return acc[i] is the normalised output of dimension lane + 32 i.
 template <typename T, bool PAGED>
-__device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s, int32_t lim,
-                                     int32_t tok, int32_t head, float (&acc)[4], float& lse) {
+__device__ __forceinline__ bool fix_row(const AttendArgs& a, Ctrl* c, const Seg& g, int s,
+                                     int32_t lim, int32_t tok, int32_t head, float (&acc)[4], float& lse) {
   const int lane = threadIdx.x & 31;
   const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s ^ g.first : 0);
   // nothing is hidden behind the sequence's end: that was cleared
@@ -647,6 +652,7 @@ __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s
 #pragma unroll 1
   for (int32_t i = 0; i < g.n[s]; ++i) {
     const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
+    get_on(c);
 #pragma unroll 1
     for (int64_t j = max(k0, static_cast<int64_t>(lim)); j < min(k0 + kTile, end); ++j) {
       const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
@@ -664,6 +670,7 @@ __device__ __forceinline__ bool fix_row(const AttendArgs& a, const Seg& g, int s
   for (int32_t i = 0; i < g.n[s]; ++i) {
     const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
     const int64_t k1 = min(k0 + kTile, static_cast<int64_t>(lim));
+    get_on(c);
 #pragma unroll 1
     for (int64_t j0 = k0; j0 < k1; j0 += 32) {
       float x = neg_inf();
@@ -838,6 +845,7 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
       return false;
     unsigned char* dst = cta.stage(ring.stage);
     ring.next();
+    if (ring.stage == 0) get_on(c);
     if (elect_one()) mbar_arrive_expect_tx(bar, L::kBytes);
     const int32_t t = (p.g.t0 + p.j) * kTile;
     if constexpr (PAGED) {
@@ -1357,7 +1365,7 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       float* flse_at = reinterpret_cast<float*>(
           __shfl_sync(~0u, reinterpret_cast<unsigned long long>(lse_at), src));
       float acc[4], flse;
-      if (!fix_row<T, PAGED>(a, g, s, flim, ftok, fhead, acc, flse)) continue;
+      if (!fix_row<T, PAGED>(a, c, g, s, flim, ftok, fhead, acc, flse)) continue;
       __syncwarp();  // behind the row's first stores, which another lane made
       for (int e = 0; e < 4; ++e) {
         const int d = lane + 32 * e;
@@ -1407,7 +1415,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(&c->tail_full[i], 1);
       mbar_init(&c->tail_done[i], 1);
     }
-    if (i == 0) c->dead = 0;
+    if (i == 0) {
+      c->dead = 0;
+      get_on(c);
+    }
     mbar_init_fence();
   }
   if (warp == 8) {

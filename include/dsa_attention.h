@@ -155,8 +155,8 @@ dsa_status dsa_shared_prefix_attention(
 
 /*
  * dsa_attention_error -- whether a wait inside an attention kernel has given
- * up (after ten seconds) since the process started or the last clear; such a
- * call's outputs are not valid. Returns the wait's nonzero site code, 0 for
+ * up (after some ten seconds without any progress) since the process started
+ * or the last clear; such a call's outputs are not valid. Returns the wait's nonzero site code, 0 for
  * none, or -1 if the flag could not be read. clear != 0 resets it after
  * reading. Synchronises with the current device.
  */

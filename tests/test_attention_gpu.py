@@ -651,3 +651,44 @@ def test_prompt_long(env):
             want = ref.prompt(q[a + t:a + t + 1], k[c:c + n], v[c:c + n], [0, 1], [0, n], False)
             ref.check(out[a + t:a + t + 1], want[0], want[2], f"out {i} {t}")
             ref.check(lse[a + t:a + t + 1], want[1], want[3], f"lse {i} {t}")
+
+
+def test_prompt_that_takes_longer_than_a_wait_may_stand_still(env):
+    """About 16 seconds on the device, with no value behind the sequence's end
+    (whole key tiles): the warp that clears those waits all along."""
+    torch, dsa = env
+    tokens, heads, dim, keys = 65536, 128, 8, 1 << 17
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+    q = rand(tokens, heads, dim)
+    cu_q = ints(torch, [0, tokens])
+
+    def run(n):
+        k, v = rand(n, 1, dim), rand(n, 1, dim)
+        first, last = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        first.record()
+        out, lse = dsa.dsa_prompt_attention(q, k, v, cu_q, ints(torch, [0, n]), causal=False)
+        last.record()
+        torch.cuda.synchronize()
+        return k, v, out, lse, first.elapsed_time(last) / 1e3
+
+    run(keys)
+    keys *= int(16 / run(keys)[-1]) + 1
+    k, v, out, lse, seconds = run(keys)
+    assert dsa.attention_error() == 0, f"a wait gave up in a call of {seconds:.1f} s"
+    # Some rows in 64 bits. Weights rounded to bf16 (half a step: 2^-9 each
+    # way of the fraction line's upper part) move an output by at most
+    # 2^-9 sum w |v|, about 0.8 of that here; fp32 sums of key tiles, each
+    # rounded twice 2^-24 at most of a sum that stays within five deviations,
+    # 5 sqrt(keys) of values around 0, add 2^-12. l is a sum over keys / 128
+    # tiles, 2^-24 of it lost at each: below 2^-8 of l for 2^23 keys, and
+    # 1 / ln 2 of that in the base-2 logarithm.
+    for t in (0, tokens // 2 + 1, tokens - 1):
+        for h in (0, 77, heads - 1):
+            x = k[:, 0].double() @ q[t, h].double() / math.sqrt(dim)
+            want = torch.softmax(x, 0) @ v[:, 0].double()
+            assert (out[t, h].double() - want).abs().max() < 2.0 ** -8, (t, h)
+            assert abs(lse[t, h].double() - torch.logsumexp(x, 0) / math.log(2.0)) < 2.0 ** -7
