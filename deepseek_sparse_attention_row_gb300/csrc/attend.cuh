@@ -218,7 +218,10 @@ __device__ __forceinline__ uint32_t warp_sum_upto(uint32_t x) {
   }
   return x;
 }
-__device__ __forceinline__ int32_t tiles_of(int32_t n) { return n <= 0 ? 0 : (n + kTile - 1) / kTile; }
+// Key tiles of n keys (in 32 bits without a sign: n may be 2^31 - 1).
+__host__ __device__ inline int32_t tiles_of(int32_t n) {
+  return n <= 0 ? 0 : static_cast<int32_t>((static_cast<uint32_t>(n) + kTile - 1) / kTile);
+}
 
 // ---- keys on pages ----------------------------------------------------------
 

@@ -58,8 +58,23 @@ static int joins_stay_in_range() {
          joinable(good, a, 4, 8);
 }
 
+// Up to the longest table of pages of 16 tokens and the longest sequence.
+static int tiles_hold_the_longest_lengths() {
+  const int64_t most = INT32_MAX;
+  for (const int64_t n : {int64_t{-5}, int64_t{0}, int64_t{1}, int64_t{128}, int64_t{129},
+                          most - 4096, most - 127, most - 63, most - 15, most - 1, most}) {
+    const int64_t want = n <= 0 ? 0 : (n + kTile - 1) / kTile;
+    if (tiles_of(static_cast<int32_t>(n)) != want) {
+      std::printf("%lld keys: %d tiles\n", static_cast<long long>(n),
+                  tiles_of(static_cast<int32_t>(n)));
+      return 1;
+    }
+  }
+  return 0;
+}
+
 int main() {
-  if (joins_stay_in_range()) return 1;
+  if (joins_stay_in_range() || tiles_hold_the_longest_lengths()) return 1;
   std::puts("ok");
   return 0;
 }

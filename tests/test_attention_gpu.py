@@ -692,3 +692,21 @@ def test_prompt_that_takes_longer_than_a_wait_may_stand_still(env):
             want = torch.softmax(x, 0) @ v[:, 0].double()
             assert (out[t, h].double() - want).abs().max() < 2.0 ** -8, (t, h)
             assert abs(lse[t, h].double() - torch.logsumexp(x, 0) / math.log(2.0)) < 2.0 ** -7
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_shared_tables_of_the_longest_length(env, page):
+    """A row of pages for all lengths below 2^31, of which the first and the
+    last are there: the sequence's last key tile ends at 2^31."""
+    torch, dsa = env
+    width = (2 ** 31 - 1) // page
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(1, 4, 64, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(2, page, 2, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    tables = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    tables[0, 0], tables[0, -1] = 1, 0
+    for lens in (width * page, 2 ** 31 - 1):
+        out, lse = dsa.dsa_shared_prefix_attention(q, k, v, tables, ints(torch, [lens]))
+        want = ref.paged(q, k, v, ints(torch, [[1, 0]]), ints(torch, [2 * page]), None, 0)
+        ref.check(out, want[0], want[2], "out")
+        ref.check(lse, want[1], want[3], "lse")
