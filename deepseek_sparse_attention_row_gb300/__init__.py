@@ -236,7 +236,7 @@ def pipeline_error(clear: bool = False) -> int:
 
 def attention_error(clear: bool = False) -> int:
     """The attention kernels' give-up flag (0: none of their waits ever gave
-    up); see dsa_attention_error."""
+    up), read behind all work of the current device; see dsa_attention_error."""
     return int(library().dsa_attention_error(1 if clear else 0))
 
 

@@ -439,6 +439,8 @@ extern "C" dsa_status dsa_shared_prefix_attention(
 
 extern "C" int dsa_attention_error(int clear) {
   unsigned int code = 0;
+  // the copies below wait for the default stream alone
+  if (cudaDeviceSynchronize() != cudaSuccess) return -1;
   if (cudaMemcpyFromSymbol(&code, dsa::g_pipe_error, sizeof(code)) != cudaSuccess) return -1;
   if (clear && code != 0) {
     const unsigned int zero = 0;

@@ -158,7 +158,8 @@ dsa_status dsa_shared_prefix_attention(
  * up (after some ten seconds without any progress) since the process started
  * or the last clear; such a call's outputs are not valid. Returns the wait's nonzero site code, 0 for
  * none, or -1 if the flag could not be read. clear != 0 resets it after
- * reading. Synchronises with the current device.
+ * reading. Waits for all of the current device's streams first; not for use
+ * while one of them is captured.
  */
 int dsa_attention_error(int clear);
 

@@ -710,3 +710,17 @@ def test_shared_tables_of_the_longest_length(env, page):
         want = ref.paged(q, k, v, ints(torch, [[1, 0]]), ints(torch, [2 * page]), None, 0)
         ref.check(out, want[0], want[2], "out")
         ref.check(lse, want[1], want[3], "lse")
+
+
+def test_the_error_flag_is_read_behind_all_streams(env):
+    """A call on a stream that the default stream does not wait for."""
+    torch, dsa = env
+    side = torch.cuda.Stream()
+    q, k, v = make(torch, 41, 4096, 262144, 8, 1, 128, torch.bfloat16)
+    cu_q, cu_k = ints(torch, [0, 4096]), ints(torch, [0, 262144])
+    torch.cuda.synchronize()
+    for _ in range(20):  # some 3 ms each
+        dsa.dsa_prompt_attention(q, k, v, cu_q, cu_k, causal=False, stream=side)
+    assert not side.query(), "the calls ended before the flag was read: nothing is shown"
+    assert dsa.attention_error() == 0
+    assert side.query(), "the flag was read before the calls ended"
