@@ -69,8 +69,8 @@ constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's ba
 constexpr int kSegs = 8;             // segments that the scheduling warp may be ahead
 // A wait gives up when its CTA has got on with nothing between the second and
 // third turn of the global timer's high word, for 8.6 to 12.9 seconds. What
-// counts are the loads (each round of the ring) and the rows that fix_row goes
-// through: a wait may be as long as the call, like that for the next value
+// counts are the loads (every 16 rounds of the ring) and the keys that fix_row
+// goes through: a wait may be as long as the call, like that for the next value
 // behind a sequence's end, of which a call may have none.
 constexpr int32_t kWaitTurns = 3;
 
@@ -107,8 +107,9 @@ struct Seg {
   int32_t ntok[2];  // its tokens
   // prompt: keys [k0, k0 + kv_len); the token before q_end sees all of them
   int32_t k0, kv_len, q_end;
-  // pages: the sequence whose own tokens these are (kv_len of them), or -1
-  // for the prefix (kv_len 0); whether a page of the segment is missing
+  // pages: the sequence whose own tokens these are (kv_len of them), or ~r for
+  // the prefix (kv_len 0), whose pages stand r rows of tables behind
+  // prefix_pages; whether a page of the segment is missing
   int32_t seq, gaps;
   int32_t slot;     // of the partial outputs (-1: written out at once)
 
@@ -234,7 +235,7 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int
   int32_t id;
   if (seq < 0) {
     if (p >= pre) return none;
-    id = __ldg(a.prefix_pages + p);
+    id = __ldg(a.prefix_pages + ~seq * a.ld_tables + p);
   } else {
     p += pre;
     if (p >= a.max_pages) return none;
@@ -454,8 +455,11 @@ struct PromptSchedule {
 __device__ __forceinline__ int32_t seen_tokens(const AttendArgs& a, int64_t b) {
   return clamp_to(a.lens[b], a.max_pages << a.page_log2);
 }
+__device__ __forceinline__ int32_t own_of(const AttendArgs& a, int32_t len) {
+  return max(clamp_to(len, a.max_pages << a.page_log2) - static_cast<int32_t>(a.prefix_len), 0);
+}
 __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
-  return max(seen_tokens(a, b) - static_cast<int32_t>(a.prefix_len), 0);
+  return own_of(a, a.lens[b]);
 }
 
 // Pages: the work is a line of units (fewer than 2^31), cut into equal shares,
@@ -474,6 +478,7 @@ constexpr int32_t kTwoTileCost = 6;     // two row tiles, bound by products
 
 struct PagedSchedule {
   int32_t pos, end, prefix_units;
+  int32_t prefix_row = 0;
   int32_t turn = 0;     // tiles of split segments so far: the streams take turns
   int32_t chunk = 0;
   int32_t before = 0;   // own units before the chunk
@@ -506,14 +511,25 @@ struct PagedSchedule {
   __device__ explicit PagedSchedule(const AttendArgs& a) {
     const int lane = threadIdx.x & 31;
     prefix_units = units(a);
+    // By default the prefix is the first row's that holds pages: empty slots
+    // of a cache (length 0, first entry negative) may stand before it.
+    bool look = a.prefix_pages == a.tables && a.prefix_tiles > 0;
     // CTA 0 also writes down where each sequence's units start.
     const bool first = blockIdx.x == 0;
-    int32_t own_units = 0, mine_next = lane < a.tokens ? own_tokens(a, lane) : 0;
+    int32_t own_units = 0, next_len = lane < a.tokens ? a.lens[lane] : 0;
 #pragma unroll 1
     for (int64_t b0 = 0; b0 < a.tokens; b0 += 32) {
       const int64_t b = b0 + lane;
-      const int32_t n = own_group(mine_next) * a.kv_heads;
-      mine_next = b + 32 < a.tokens ? own_tokens(a, b + 32) : 0;
+      const int32_t len = next_len, n = own_group(own_of(a, len)) * a.kv_heads;
+      next_len = b + 32 < a.tokens ? a.lens[b + 32] : 0;
+      if (look) {
+        const uint32_t found = __ballot_sync(
+            ~0u, len > 0 || (b < a.tokens && a.tables[b * a.ld_tables] >= 0));
+        if (found != 0) {
+          prefix_row = static_cast<int32_t>(b0) + __ffs(found) - 1;
+          look = false;
+        }
+      }
       if (first) {
         const int32_t inc = static_cast<int32_t>(warp_sum_upto(n));
         if (b < a.tokens) a.starts[b] = own_units + inc - n;
@@ -568,7 +584,7 @@ struct PagedSchedule {
         const int32_t per = prefix_group(a), pg = pos / per;
         n = take(pos - pg * per, per, prefix_cost(a), g.t0);
         g.kh = pg / a.prefix_blocks;
-        g.seq = -1;
+        g.seq = ~prefix_row;
         g.kv_len = 0;
         g.slot = pg + static_cast<int32_t>(blockIdx.x);
         g.split = a.prefix_split;
@@ -836,7 +852,8 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     // the list's table, from its first page on, and how many pages are seen
     const int32_t pre = static_cast<int32_t>(a.prefix_len >> a.page_log2);
     const bool own = p.g.seq >= 0;
-    const int32_t* table = own ? a.tables + p.g.seq * a.ld_tables + pre : a.prefix_pages;
+    const int32_t* table = own ? a.tables + p.g.seq * a.ld_tables + pre
+                               : a.prefix_pages + ~p.g.seq * a.ld_tables;
     const int32_t count = own ? (p.g.kv_len + a.page_size - 1) >> a.page_log2 : pre;
     const int32_t at = (((p.g.t0 + p.j) * kTile) >> a.page_log2) + lane;
     return lane < pages && at < count ? static_cast<uint32_t>(__ldg(table + at)) : none;
@@ -848,7 +865,7 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
       return false;
     unsigned char* dst = cta.stage(ring.stage);
     ring.next();
-    if (ring.stage == 0) get_on(c);
+    if (ring.stage == 0 && ring.round % 16 == 0) get_on(c);
     if (elect_one()) mbar_arrive_expect_tx(bar, L::kBytes);
     const int32_t t = (p.g.t0 + p.j) * kTile;
     if constexpr (PAGED) {
@@ -1418,14 +1435,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(&c->tail_full[i], 1);
       mbar_init(&c->tail_done[i], 1);
     }
-    if (i == 0) {
-      c->dead = 0;
-      get_on(c);
-    }
+    if (i == 0) c->dead = 0;
     mbar_init_fence();
   }
   if (warp == 8) {
     tmem_alloc(&c->tmem);
+  } else if (warp == 10) {
+    get_on(c);
   } else if (warp == 9 && (threadIdx.x & 31) == 0) {
     tma_prefetch(PAGED ? &q1 : &qm);
     tma_prefetch(&km);

@@ -125,8 +125,10 @@ size_t dsa_shared_prefix_workspace_bytes(int64_t batch, int32_t heads,
  *            prefix_len the page is prefix_pages[t / page_size] for every
  *            sequence and the tables' first prefix_len / page_size columns
  *            are not read (a sequence with fewer tokens sees what it has).
- *   prefix_pages  [prefix_len / page_size] device int32 (may be a row of
- *            `tables`); NULL when prefix_len == 0.
+ *   prefix_pages  [prefix_len / page_size] device int32; NULL when
+ *            prefix_len == 0. May be a row of `tables`; `tables` itself stands
+ *            for the first row whose slot is not empty (its length is over 0
+ *            or its first entry not negative; row 0 if all are empty).
  *   out      [batch, heads, head_dim] of `dtype`.
  *   lse      [batch, heads] fp32 at lse + b*l_sb + h*l_sh, or NULL.
  *   workspace     dsa_shared_prefix_workspace_bytes(...) bytes, 256-byte

@@ -724,3 +724,37 @@ def test_the_error_flag_is_read_behind_all_streams(env):
     assert not side.query(), "the calls ended before the flag was read: nothing is shown"
     assert dsa.attention_error() == 0
     assert side.query(), "the flag was read before the calls ended"
+
+
+@pytest.mark.parametrize("empty", [[0], [0, 1, 2], list(range(40)), list(range(45))])
+def test_shared_default_prefix_passes_over_empty_slots(env, empty):
+    """Slots that dsa_cache_free emptied, in front of the live ones."""
+    torch, dsa = env
+    q, k, v, tables, lens = make_paged(torch, 43, 45, 8, 2, 64, 16, 96, [20 + i for i in range(45)],
+                                       torch.bfloat16)
+    pages = tables[-1, :6].clone()
+    refs = torch.full((k.shape[0],), 50, dtype=torch.int32, device="cuda")
+    dsa.dsa_cache_free(refs, tables, lens, ints(torch, empty))
+    out, lse = dsa.dsa_shared_prefix_attention(q, k, v, tables, lens, 96)
+    want = ref.paged(q, k, v, tables, lens, pages, 96)
+    ref.check(out, want[0], want[2], "out")
+    ref.check(lse, want[1], want[3], "lse")
+    # a row that is named is taken as it is
+    last = dsa.dsa_shared_prefix_attention(q, k, v, tables, lens, 96, prefix_pages=pages)
+    assert torch.equal(out, last[0]) and torch.equal(lse, last[1])
+
+
+def test_shared_default_prefix_of_a_slot_without_tokens(env):
+    """A row with pages counts although its sequence sees none of them yet; an
+    empty slot whose entries behind the first are stale does not."""
+    torch, dsa = env
+    q, k, v, tables, lens = make_paged(torch, 44, 3, 4, 2, 64, 16, 64, [9, 30, 17], torch.float16)
+    lens[0] = 0
+    tables[1, :4] = 99999  # not there
+    check_paged(env, q, k, v, tables, lens, 64)
+    tables[0, 0] = -1
+    tables[1, :4] = tables[2, :4]
+    out, lse = dsa.dsa_shared_prefix_attention(q, k, v, tables, lens, 64)
+    want = ref.paged(q, k, v, tables, lens, tables[1, :4], 64)
+    ref.check(out, want[0], want[2], "out")
+    ref.check(lse, want[1], want[3], "lse")
