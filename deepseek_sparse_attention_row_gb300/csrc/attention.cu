@@ -234,7 +234,7 @@ dsa_status check_common(int32_t dtype, int64_t tokens, int32_t heads, int32_t kv
     return DSA_EINVAL;
   if (tokens < 0 || heads < 0 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1)
     return DSA_EINVAL;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DSA_EINVAL;
+  if (!(scale > 0.f) || !std::isfinite(scale * kLog2e)) return DSA_EINVAL;
   if (dtype == DSA_DTYPE_F32 || head_dim > kMaxHeadDim || head_dim % 8 != 0 ||
       heads / kv_heads > kMaxGroup || tokens > INT32_MAX)
     return DSA_EUNSUPPORTED;

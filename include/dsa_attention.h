@@ -66,7 +66,8 @@ size_t dsa_prompt_workspace_bytes(int64_t total_q, int64_t total_k,
  *   causal 0: every query of a sequence sees all of its keys; nonzero: query
  *          t of n sees the keys j <= t + (keys - n), so that the last query
  *          sees all of them (the keys before the first query are cached ones).
- *   scale  > 0, finite: the factor of <q, k>.
+ *   scale  > 0: the factor of <q, k>; scale * log2(e) is finite in fp32
+ *          (scale up to 2.35e38).
  *   out    [total_q, heads, head_dim] of `dtype`.
  *   lse    [total_q, heads] fp32 at lse + t*l_st + h*l_sh, or NULL.
  *   workspace     dsa_prompt_workspace_bytes(...) bytes, 256-byte aligned
@@ -79,8 +80,8 @@ size_t dsa_prompt_workspace_bytes(int64_t total_q, int64_t total_k,
  *
  * total_q == 0, heads == 0 or seqs == 0: DSA_OK, nothing written. DSA_EINVAL
  * for an unknown dtype, negative sizes, kv_heads < 1 or no divisor of heads,
- * head_dim < 1, a scale that is not positive and finite, or a NULL q, cu_q,
- * cu_k or out (or k or v with total_k > 0), or a workspace that is too small.
+ * head_dim < 1, a scale that is not as above, or a NULL q, cu_q, cu_k or
+ * out (or k or v with total_k > 0), or a workspace that is too small.
  * DSA_EUNSUPPORTED for
  * DSA_DTYPE_F32, head_dim over 128 or no multiple of 8, heads / kv_heads >
  * 128, layouts other than above, and sizes from 2^31 (total_k from 2^31 -

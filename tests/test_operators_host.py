@@ -249,3 +249,11 @@ def test_binding_strides(dsa):
     assert rows(torch.as_strided(x, (1, 4, 64), (3, 64, 1))) == (64, 64)
     with pytest.raises(ValueError, match="unit stride"):
         rows(x.transpose(1, 2))
+
+
+@pytest.mark.parametrize("scale,want", [(2.4e38, DSA_EINVAL), (3.4e38, DSA_EINVAL),
+                                        (2.3e38, DSA_OK), (1e-38, DSA_OK)])
+def test_scales_whose_product_with_log2_e_overflows(dsa, scale, want):
+    """Accepted ones fall through to the next check (no heads: nothing to do)."""
+    assert prompt(dsa.library(), scale=scale, heads=0) == want
+    assert shared(dsa.library(), scale=scale, heads=0) == want
