@@ -22,7 +22,8 @@ Functions carry the C ABI's names:
   C ABI in ``include/dsa_dcp_attn.h``) and the sum over shards after it.
 * ``dsa_prompt_attention`` / ``dsa_shared_prefix_attention`` -- attention over
   packed prompts, and of single tokens on a paged cache whose first pages a
-  batch shares; both give the base-2 LSE that the merge takes
+  batch shares; both give the base-2 LSE that the merge takes, with bf16
+  outputs as they are and fp16 ones widened to fp32
   (``include/dsa_attention.h``).
 * ``dsa_cache_fork`` / ``dsa_cache_free`` / ``dsa_cache_compact`` -- the pages
   of such a cache (``include/dsa_cache.h``).

@@ -15,9 +15,10 @@
  * NaN that they do not see are summed in another order, within the same
  * rounding); a NaN in a key that it sees makes the row NaN.
  *
- * (out, lse) is a partial output as dsa_merge_attn_out and
- * dsa_correct_attn_out of dsa_dcp_attn.h take it: runs over disjoint sets of
- * keys merge into the run over their union.
+ * (out, lse) is a partial output for dsa_merge_attn_out and
+ * dsa_correct_attn_out of dsa_dcp_attn.h: runs over disjoint sets of keys
+ * merge into the run over their union. Those two take bf16 and fp32: an fp16
+ * out is widened to fp32 for them (which loses nothing).
  *
  * Arithmetic: products of bf16 or fp16 operands summed in fp32; maxima,
  * exponentials and sums in fp32; the weights 2^(x_j - m) are rounded to the

@@ -758,3 +758,29 @@ def test_shared_default_prefix_of_a_slot_without_tokens(env):
     want = ref.paged(q, k, v, tables, lens, tables[1, :4], 64)
     ref.check(out, want[0], want[2], "out")
     ref.check(lse, want[1], want[3], "lse")
+
+
+def test_fp16_parts_merge_in_fp32(env):
+    """The merge takes no fp16; widened parts lose nothing on the way."""
+    torch, dsa = env
+    T, H, D = 150, 4, 96
+    q, k, v = make(torch, 45, T, 350, H, 2, D, torch.float16)
+    one = ints(torch, [0, T])
+    parts = [dsa.dsa_prompt_attention(q, k[:200], v[:200], one, ints(torch, [0, 200]),
+                                      causal=False),
+             dsa.dsa_prompt_attention(q, k[200:], v[200:], one, ints(torch, [0, 150]),
+                                      causal=True)]
+    outs, lses = (torch.stack([p[i] for p in parts]) for i in range(2))
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        dsa.dsa_merge_attn_out(outs, lses)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        dsa.dsa_correct_attn_out(outs[0], lses, 0)
+    merged, lse = dsa.dsa_merge_attn_out(outs.float(), lses)
+    torch.cuda.synchronize()
+    want = ref.prompt(q, k, v, [0, T], [0, 350], True)
+    # each part carries a rounding of its own, the merged sum none but fp32's
+    h = ref.half_step(torch.float16)
+    size = sum(p[0].double().cpu().abs() * torch.exp2(p[1].double().cpu() - want[1])[..., None]
+               for p in parts)
+    ref.check(merged.transpose(0, 1), want[0], 2 * want[2] + 2 * h * size + 2.0 ** -24, "out")
+    ref.check(lse, want[1], 3 * want[3] + 8 * ref.U, "lse")

@@ -257,3 +257,12 @@ def test_scales_whose_product_with_log2_e_overflows(dsa, scale, want):
     """Accepted ones fall through to the next check (no heads: nothing to do)."""
     assert prompt(dsa.library(), scale=scale, heads=0) == want
     assert shared(dsa.library(), scale=scale, heads=0) == want
+
+
+def test_the_merge_takes_no_fp16(dsa):
+    """As dsa_attention.h says of the outputs that go to it."""
+    lib = dsa.library()
+    assert lib.dsa_merge_attn_out(FAKE, F16, 2, 3, 4, 64, 768, 256, 64, 1, FAKE, 12, 4, 1, FAKE,
+                                  192, 64, 1, None, 4, 1, None) == DSA_EINVAL
+    assert lib.dsa_correct_attn_out(FAKE, F16, 3, 4, 64, 256, 64, 1, FAKE, 2, 12, 4, 1, 0, FAKE,
+                                    192, 64, 1, None, 4, 1, None) == DSA_EINVAL
