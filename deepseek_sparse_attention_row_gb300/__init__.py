@@ -71,6 +71,7 @@ __all__ = [
     "prompt_workspace_bytes",
     "shared_prefix_workspace_bytes",
     "cache_workspace_bytes",
+    "release_workspaces",
     "max_select_blocks",
     "mapped_host_pointer",
     "set_launch_override",
@@ -94,6 +95,7 @@ EXPORTED_SYMBOLS = (
     "dsa_mask_candidate_logits_sharded",
     "dsa_select_candidate_blocks_sharded_static",
     "dsa_mapped_host_pointer",
+    "dsa_stream_id",
     "dsa_attn_max_shards",
     "dsa_correct_attn_out",
     "dsa_merge_attn_out",
@@ -169,6 +171,8 @@ def library():
                                                       i32, i64, p]
     lib.dsa_mapped_host_pointer.argtypes = [p, ctypes.POINTER(ctypes.c_void_p)]
     lib.dsa_mapped_host_pointer.restype = ctypes.c_int
+    lib.dsa_stream_id.argtypes = [p]
+    lib.dsa_stream_id.restype = ctypes.c_uint64
     lib.dsa_attn_max_shards.argtypes = []
     lib.dsa_attn_max_shards.restype = i32
     lib.dsa_correct_attn_out.argtypes = [p, i32, i64, i64, i64, i64, i64, i64, p, i32, i64, i64,
@@ -797,18 +801,21 @@ def _need(name: str, index: int, *sizes) -> int:
 
 
 _KEEP_BYTES = 64 << 20
-_scratch_cache = {}
+_KEEP_ALL_BYTES = 256 << 20
+_scratch_cache = {}  # in the order of their allocation
+_scratch_lock = threading.Lock()
 
 
 def _scratch(workspace, need: int, like, handle):
     """A call's workspace, held until the call is enqueued, with its address
     and bytes: the caller's tensor, or one of its own on ``like``'s device.
 
-    Its own one is kept for the next call of this thread on this stream, whose
-    calls follow each other; larger ones than 64 MiB, and those of a capture
-    (whose graph may run beside other calls), come from the allocator of the
-    current stream or graph, which hands their memory on only behind this
-    call."""
+    Its own one is kept for the next call of this thread on this stream (the
+    stream itself, not its handle, which another one may get), whose calls
+    follow each other; larger ones than 64 MiB, and those of a capture (whose
+    graph may run beside other calls), come from the allocator of the current
+    stream or graph, which hands their memory on only behind this call. So
+    does what is let go: the oldest ones over 256 MiB in all."""
     if workspace is None:
         if not need:
             return None, None, 0
@@ -816,16 +823,32 @@ def _scratch(workspace, need: int, like, handle):
         if need > _KEEP_BYTES or torch._C._cuda_isCurrentStreamCapturing():
             workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
             return workspace, workspace.data_ptr(), need
-        key = threading.get_ident(), like.get_device(), handle
+        # the default stream (no handle) is never destroyed
+        stream = handle if handle is None else library().dsa_stream_id(handle)
+        key = threading.get_ident(), like.get_device(), stream
         kept = _scratch_cache.get(key)
         if kept is None or kept[2] < need:
             workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-            kept = _scratch_cache[key] = workspace, workspace.data_ptr(), need
+            kept = workspace, workspace.data_ptr(), need
+            with _scratch_lock:
+                _scratch_cache.pop(key, None)
+                _scratch_cache[key] = kept
+                over = sum(k[2] for k in _scratch_cache.values()) - _KEEP_ALL_BYTES
+                while over > 0:
+                    over -= _scratch_cache.pop(next(iter(_scratch_cache)))[2]
         return kept
     if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     n = workspace.numel() * workspace.element_size()
     return workspace, workspace.data_ptr() if n else None, n
+
+
+def release_workspaces() -> None:
+    """Let go of the workspaces that attention and cache calls keep (up to 256
+    MiB in all); their memory goes back to PyTorch's allocator. Calls under
+    way are not disturbed."""
+    with _scratch_lock:
+        _scratch_cache.clear()
 
 
 FORK_OK, FORK_NO_PAGE, FORK_REFUSED = 0, 1, 2

@@ -1283,6 +1283,15 @@ extern "C" dsa_status dsa_mapped_host_pointer(const void* host, void** device) {
   return DSA_OK;
 }
 
+extern "C" uint64_t dsa_stream_id(void* stream) {
+  unsigned long long id = 0;
+  if (cudaStreamGetId(static_cast<cudaStream_t>(stream), &id) != cudaSuccess) {
+    cudaGetLastError();  // not sticky: clear it
+    return UINT64_MAX;
+  }
+  return id;
+}
+
 extern "C" dsa_status dsa_select_candidate_blocks_sharded_static(
     const float* logits, int32_t shards, int64_t rows, int64_t local_width, int64_t ld_logits,
     int64_t shard_stride, const int32_t* global_row_ke, int32_t global_block_size,

@@ -488,6 +488,14 @@ dsa_status dsa_select_candidate_blocks_sharded_static(
  */
 dsa_status dsa_mapped_host_pointer(const void *host, void **device);
 
+/*
+ * dsa_stream_id -- a number that `stream` shares with no other stream of the
+ * process, destroyed ones included (a handle may come again): what a caller
+ * that keeps something for a stream, such as a workspace, keeps it under.
+ * UINT64_MAX if the stream is none.
+ */
+uint64_t dsa_stream_id(void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -784,3 +784,65 @@ def test_fp16_parts_merge_in_fp32(env):
                for p in parts)
     ref.check(merged.transpose(0, 1), want[0], 2 * want[2] + 2 * h * size + 2.0 ** -24, "out")
     ref.check(lse, want[1], 3 * want[3] + 8 * ref.U, "lse")
+
+
+def test_kept_workspaces_are_bounded_and_released(env):
+    """Streams and threads without end keep no more than the bound."""
+    import threading
+
+    torch, dsa = env
+    q, k, v = make(torch, 46, 300, 6000, 8, 2, 128, torch.bfloat16)
+    cu = ints(torch, [0, 300]), ints(torch, [0, 6000])
+    need = dsa.prompt_workspace_bytes(300, 6000, 8, 2, 128, 1)
+    assert dsa._KEEP_ALL_BYTES < 12 * need and need <= dsa._KEEP_BYTES
+    want = check_prompt(env, q, k, v, [300], [6000], True)
+    dsa.release_workspaces()
+    got = []
+
+    def work(stream):
+        got.append(dsa.dsa_prompt_attention(q, k, v, *cu, stream=stream))
+        kept = sum(x[2] for x in list(dsa._scratch_cache.values()))
+        got[-1] += (kept,)
+
+    torch.cuda.synchronize()
+    for s in [torch.cuda.Stream() for _ in range(12)]:
+        work(s)
+    for _ in range(12):
+        t = threading.Thread(target=work, args=(torch.cuda.current_stream(),))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert len(got) == 24
+    for out, lse, kept in got:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert need <= kept <= dsa._KEEP_ALL_BYTES
+    before = torch.cuda.memory_allocated()
+    dsa.release_workspaces()
+    assert not dsa._scratch_cache and torch.cuda.memory_allocated() <= before - need
+
+
+def test_a_stream_with_another_ones_handle_gets_a_workspace_of_its_own(env):
+    """Streams that are not PyTorch's: one is destroyed, the next may get its
+    handle."""
+    import ctypes
+
+    torch, dsa = env
+    rt = ctypes.CDLL("libcudart.so." + torch.version.cuda.split(".")[0])
+    p = make_paged(torch, 47, 4, 4, 2, 64, 16, 32, [5, 60, 0, 9], torch.bfloat16)
+    want = check_paged(env, *p, 32)
+    dsa.release_workspaces()
+    ids, handles = set(), set()
+    for _ in range(5):
+        handle = ctypes.c_void_p()
+        assert rt.cudaStreamCreateWithFlags(ctypes.byref(handle), 1) == 0
+        stream = torch.cuda.ExternalStream(handle.value)
+        ids.add(dsa.library().dsa_stream_id(handle.value))
+        handles.add(handle.value)
+        for _ in range(2):
+            got = dsa.dsa_shared_prefix_attention(*p, 32, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert rt.cudaStreamDestroy(handle) == 0
+    assert len(ids) == 5 and 2 ** 64 - 1 not in ids
+    assert len(dsa._scratch_cache) == 5, f"{len(handles)} handles"
+    dsa.release_workspaces()
