@@ -42,8 +42,17 @@
 // Values that a row does not see have weight 0, which an infinite or NaN value
 // turns into NaN. What lies behind a sequence's end in its last tile (often
 // memory never written) is cleared by a warp of its own before the products;
-// what causal rows do not see of their own sequence is finite in any sane
-// call, and is checked for in the output (fix_row).
+// what a row does not see of its own sequence (causal rows) or of the prefix
+// (lengths that end in it) is finite in any sane call. Where an output is not
+// finite and its row does not see all of its tiles, the CTA goes through its
+// list again: the clearing warp makes the tiles finite that some row does not
+// see whole, and at the end the scheduling warp adds to each row what it sees
+// of the values that were not (add_seen). Such a CTA takes about twice as long
+// (262144 tokens, one hidden infinity: 20 ms, 10 without; rows computed again
+// one by one took 6.8 s). A prefix that rows end in, with a NaN behind them, is
+// read by one warp: 128 sequences on 32768 tokens 13 ms, 0.16 without. In the
+// softmax warps this costs one store: with more code there, 128 sequences
+// behind a shared document took 122 us instead of 105.
 //
 // Code size matters: the roles of an SM run different code at the same time,
 // and a call with short segments runs each piece only a few times. Loops that
@@ -69,9 +78,10 @@ constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's ba
 constexpr int kSegs = 8;             // segments that the scheduling warp may be ahead
 // A wait gives up when its CTA has got on with nothing between the second and
 // third turn of the global timer's high word, for 8.6 to 12.9 seconds. What
-// counts are the loads (every 16 rounds of the ring) and the keys that fix_row
-// goes through: a wait may be as long as the call, like that for the next value
-// behind a sequence's end, of which a call may have none.
+// counts are the loads (every 16 rounds of the ring) and the key tiles that are
+// looked through for values that are not finite: a wait may be as long as the
+// call, like that for the next value behind a sequence's end, of which a call
+// may have none.
 constexpr int32_t kWaitTurns = 3;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -112,14 +122,20 @@ struct Seg {
   // prefix_pages; whether a page of the segment is missing
   int32_t seq, gaps;
   int32_t slot;     // of the partial outputs (-1: written out at once)
-
-  // The key tile from which on values lie behind the sequence's last key: the
-  // next sequence's, or what a page holds that is not full.
-  __device__ int32_t tail() const { return kv_len > 0 ? kv_len / kTile : 0x7fffffff; }
+  // Passes 1 and 2: the key tile from which on some row does not see all, whose
+  // values are made finite. kNone in pass 0.
+  int32_t sane;
+  // The key tile from which on values go through the clearing warp: sane, or
+  // where values lie behind the sequence's last key (the next sequence's, or
+  // what a page holds that is not full).
+  int32_t tail;
 };
-// A V tile with such values, for the warp that clears them.
+constexpr int32_t kNone = 0x7fffffff;
+// A V tile for the clearing warp.
 struct Tail {
-  int32_t stage, parity, from, to;  // the rows to clear
+  int32_t stage, parity;
+  int32_t sane;      // whether the rows below `from` are made finite
+  int32_t from, to;  // the rows to clear
 };
 
 struct AttendArgs {
@@ -175,6 +191,8 @@ struct Ctrl {
   uint32_t tmem;
   uint32_t beat;  // global_turns() when the CTA last got on
   int dead;
+  int doubt;  // an output may hold what its row does not see
+  int pass;   // 0; 1: once more, with finite values; 2: what is seen is added
 };
 constexpr size_t attend_smem(uint32_t ctrl) { return 1024 + ctrl + sizeof(Ctrl); }
 
@@ -386,6 +404,11 @@ struct PromptSchedule {
     start += units_of(a, q1 - q0, kv, b);
   }
 
+  // The key tile from which on some row of the segment does not see all keys.
+  __device__ static int32_t first_masked(const AttendArgs& a, const Seg& g) {
+    return a.causal ? max(g.kv_len - (g.q_end - 1 - g.tok[0]), 0) / kTile : kNone;
+  }
+
   __device__ bool next(const AttendArgs& a, Seg& g) {
     const int32_t block = 2 * a.tile_tokens;
 #pragma unroll 1
@@ -561,6 +584,19 @@ struct PagedSchedule {
     g.n[1 - g.first] = n / 2;
   }
 
+  // As above, of the prefix; rows that see nothing of it do not count.
+  __device__ static int32_t first_masked(const AttendArgs& a, const Seg& g) {
+    if (g.seq >= 0) return kNone;
+    int32_t least = kNone;
+#pragma unroll 1
+    for (int32_t b = g.tok[0] + (threadIdx.x & 31); b < g.tok[1] + g.ntok[1]; b += 32) {
+      const int32_t n = seen_tokens(a, b);
+      if (n > 0 && n < a.prefix_len) least = min(least, n);
+    }
+    least = __reduce_min_sync(~0u, least);
+    return least == kNone ? kNone : least / kTile;
+  }
+
   // Whether a page of the segment's tiles is missing: looked up here, ahead
   // of the streams, which then need no table.
   __device__ static void find_gaps(const AttendArgs& a, Seg& g, int32_t n) {
@@ -655,85 +691,68 @@ __device__ __forceinline__ const T* row_at(const AttendArgs& a, const Seg& g, co
 
 // ---- rows with infinities or NaN in places that they do not see ------------
 
-// A masked weight is 0, but 0 times an infinite or NaN value is NaN: where a
-// row's output is not finite and a key tile that it visited holds a value
-// that is not finite behind the row's last key, the warp computes the row
-// again from its own keys alone. Returns false where no such value exists.
-// On return acc[i] is the normalised output of dimension lane + 32 i.
-template <typename T, bool PAGED>
-__device__ __forceinline__ bool fix_row(const AttendArgs& a, Ctrl* c, const Seg& g, int s,
-                                     int32_t lim, int32_t tok, int32_t head, float (&acc)[4], float& lse) {
-  const int lane = threadIdx.x & 31;
+// A masked weight is 0, but 0 times an infinite or NaN value is NaN.
+
+// Pass 2: to 32 rows of a segment (rows 32 w ... of stream s) the values that
+// were made finite in the products and that the row sees. Rows are taken in
+// the order of their ends, so that each key is read once. Weights are over 0,
+// so that the sum of such values is what they make of an output, infinite or
+// NaN.
+template <typename T, int DP, bool PAGED>
+__device__ __forceinline__ void add_seen(const AttendArgs& a, Ctrl* c, const Seg& g, int s, int w) {
+  const int lane = threadIdx.x & 31, row = 32 * w + lane, rt = row / a.group;
+  const int qs = g.split ? 0 : s;
+  const bool valid = rt < g.ntok[qs];
+  const int32_t tok = g.tok[qs] + rt, head = g.kh * a.group + row % a.group;
+  int32_t lim = 0;
+  T* out = nullptr;
+  float* part = nullptr;
+  if (valid) {
+    if constexpr (PAGED) lim = min(seen_tokens(a, tok), static_cast<int32_t>(a.prefix_len));
+    else lim = g.kv_len - (g.q_end - 1 - tok);
+    if (PAGED || g.slot >= 0)
+      part = a.prefix_o + (g.slot * 256ll + (s ^ g.first) * kTile) * DP + row * 4;
+    else
+      out = static_cast<T*>(a.out) + tok * a.o_st + head * a.o_sh;
+  }
   const int32_t step = g.split ? 2 : 1, first = g.t0 + (g.split ? s ^ g.first : 0);
-  // nothing is hidden behind the sequence's end: that was cleared
-  const int64_t end = g.kv_len > 0 ? g.kv_len : INT64_MAX;
-  bool hidden = false;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};  // of dimension lane + 32 e
+  uint32_t rows = __ballot_sync(~0u, lim > 0);
+  int32_t i = max(g.sane - first + step - 1, 0) / step, at = 0;  // tile, key of it
 #pragma unroll 1
-  for (int32_t i = 0; i < g.n[s]; ++i) {
-    const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
-    get_on(c);
+  while (rows != 0) {
+    const int32_t mine = (rows >> lane) & 1 ? lim : kNone;
+    const int32_t least = __reduce_min_sync(~0u, mine);
+    const int src = __ffs(__ballot_sync(~0u, mine == least) & rows) - 1;
+    rows &= ~(1u << src);
 #pragma unroll 1
-    for (int64_t j = max(k0, static_cast<int64_t>(lim)); j < min(k0 + kTile, end); ++j) {
+    while (i < g.n[s]) {
+      const int64_t j = static_cast<int64_t>(first + i * step) * kTile + at;
+      if (j >= least) break;
       const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
-      if (!v) continue;
-#pragma unroll 1
-      for (int d = lane; d < a.dim; d += 32) hidden |= !finite(to_f(v[d]));
-    }
-    if (__any_sync(~0u, hidden)) break;
-  }
-  if (!__any_sync(~0u, hidden)) return false;
-  const T* q = static_cast<const T*>(a.q) + tok * a.q_st + head * a.q_sh;
-  float m = neg_inf(), l = 0.f;
-  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
-#pragma unroll 1
-  for (int32_t i = 0; i < g.n[s]; ++i) {
-    const int64_t k0 = static_cast<int64_t>(first + i * step) * kTile;
-    const int64_t k1 = min(k0 + kTile, static_cast<int64_t>(lim));
-    get_on(c);
-#pragma unroll 1
-    for (int64_t j0 = k0; j0 < k1; j0 += 32) {
-      float x = neg_inf();
-      const T* k = j0 + lane < k1
-                       ? row_at<T, PAGED>(a, g, a.k, a.k_sn, a.k_st, a.k_sh, j0 + lane)
-                       : nullptr;
-      if (k) {
-        x = 0.f;
-#pragma unroll 1
-        for (int d = 0; d < a.dim; ++d) x = fmaf(to_f(q[d]), to_f(k[d]), x);
-        x *= a.c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = v && lane + 32 * e < a.dim ? to_f(v[lane + 32 * e]) : 0.f;
+        if (!finite(x)) sum[e] += x;
       }
-      float mx = x;
-#pragma unroll 1
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-      const float m_new = fmaxf(m, mx), base = m_new == neg_inf() ? 0.f : m_new;
-      const float keep = ex2(m - base), p = ex2(x - base);
-      float sum = p;
-#pragma unroll 1
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      l = l * keep + sum;
-      m = m_new;
-      for (int e = 0; e < 4; ++e) acc[e] *= keep;
-#pragma unroll 1
-      for (int64_t j = j0; j < j0 + 32 && j < k1; ++j) {
-        const float pj = __shfl_sync(~0u, p, static_cast<int>(j - j0));
-        const T* v = row_at<T, PAGED>(a, g, a.v, a.v_sn, a.v_st, a.v_sh, j);
-        if (!v) continue;
-        for (int e = 0; e < 4; ++e)
-          if (lane + 32 * e < a.dim) acc[e] = fmaf(pj, to_f(v[lane + 32 * e]), acc[e]);
-      }
-      // nothing brings a NaN back: stop once all of the row is one
-      bool gone = true;
-      for (int e = 0; e < 4; ++e) gone &= lane + 32 * e >= a.dim || acc[e] != acc[e];
-      if (l != l || __all_sync(~0u, gone)) {
-        i = g.n[s];
-        break;
+      if (++at == kTile) {
+        at = 0;
+        ++i;
+        get_on(c);
       }
     }
+    T* o = reinterpret_cast<T*>(
+        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), src));
+    float* p = reinterpret_cast<float*>(
+        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(part), src));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = lane + 32 * e;
+      if (d >= a.dim || sum[e] == 0.f) continue;
+      if (PAGED || p) p[d / 4 * (4 * kTile) + d % 4] += sum[e];
+      else o[d] = from_f<T>(to_f(o[d]) + sum[e]);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int e = 0; e < 4; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
-  lse = l == 0.f ? neg_inf() : m + log2f(l);
-  return true;
 }
 
 // ---- roles ------------------------------------------------------------------
@@ -810,16 +829,26 @@ __device__ __forceinline__ void order(const Place<WARP>& p, const Place<WARP>& q
   values = ahead > 0 && (ahead >= lead || !scores);
 }
 
-template <int DP, bool PAGED>
+template <typename T, int DP, bool PAGED>
 __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
   Ctrl* c = cta.ctrl();
+  const int pass = c->pass;
   typename ScheduleOf<PAGED>::type list(a);
+  uint32_t k = 0;
 #pragma unroll 1
-  for (uint32_t k = 0;; ++k) {
+  for (;;) {
     Seg g;
-    const int i = k % kSegs;
     const bool more = list.next(a, g);
     if (!more) g.n[0] = -1;
+    g.sane = pass > 0 && more ? list.first_masked(a, g) : kNone;
+    g.tail = min(g.sane, g.kv_len > 0 ? g.kv_len / kTile : kNone);
+    if (pass == 2 && more) {
+#pragma unroll 1
+      for (int w = 0; w < 8 && g.sane != kNone; ++w)
+        add_seen<T, DP, PAGED>(a, c, g, w >> 2, w & 3);
+      continue;
+    }
+    const int i = k % kSegs;
     if (k >= kSegs && !wait_warp(&c->seg_empty[i], (k / kSegs - 1) & 1, c, 16)) return;
     if ((threadIdx.x & 31) == 0) {
       c->seg[i] = g;
@@ -827,6 +856,7 @@ __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
     }
     __syncwarp();
     if (!more) return;
+    ++k;
   }
 }
 
@@ -900,13 +930,14 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     if (values) {
       const Ring<DP> at = ring;
       if (!put(vm, p, p_ids)) return;
-      if (p.g.t0 + p.j >= p.g.tail()) {
+      if (p.g.t0 + p.j >= p.g.tail) {
         const uint32_t i = tails++ % kTails;
         if (lane == 0) {
           // whole pages behind the end are not loaded (zeros are)
-          const int32_t from = p.g.kv_len - (p.g.t0 + p.j) * kTile;
+          const int32_t t = p.g.t0 + p.j;
+          const int32_t from = p.g.kv_len > 0 ? min(p.g.kv_len - t * kTile, kTile) : kTile;
           const int32_t to = PAGED ? min((from + a.page_size - 1) & -a.page_size, kTile) : kTile;
-          c->tail[i] = Tail{at.stage, static_cast<int32_t>(at.round & 1), from, to};
+          c->tail[i] = Tail{at.stage, static_cast<int32_t>(at.round & 1), t >= p.g.sane, from, to};
           mbar_arrive(&c->tail_full[i]);
         }
         __syncwarp();
@@ -968,8 +999,15 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     if (((used >> i) & 1) && !wait_warp(&c->q_empty[i], (phase >> i) & 1, c, 18)) return;
 }
 
+// Two values, 0 in place of those that are not finite (exponents of ones).
+template <typename T>
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+  constexpr uint32_t kOnes = std::is_same<T, __nv_bfloat16>::value ? 0x7f807f80u : 0x7c007c00u;
+  return x & ~__vcmpeq2(x & kOnes, kOnes);
+}
+
 // The warp that clears V tiles behind their sequences' ends.
-template <int DP>
+template <typename T, int DP>
 __device__ void clear_tails(Cta<DP> cta) {
   using L = Layout<DP>;
   Ctrl* c = cta.ctrl();
@@ -981,6 +1019,15 @@ __device__ void clear_tails(Cta<DP> cta) {
     const Tail t = c->tail[i];
     if (t.stage < 0) return;
     if (!wait_warp(&c->kv_full[t.stage], t.parity, c, 30)) return;
+    if (t.sane) {
+#pragma unroll 1
+      for (int j = lane; j < t.from * 8 * L::kHalves; j += 32) {
+        uint4* at = reinterpret_cast<uint4*>(cta.stage(t.stage) +
+                                             (j >= t.from * 8 ? L::kHalf - t.from * 128 : 0)) + j;
+        const uint4 x = *at;
+        *at = make_uint4(finite2<T>(x.x), finite2<T>(x.y), finite2<T>(x.z), finite2<T>(x.w));
+      }
+    }
     // 16-byte pieces of the rows behind the end; swizzling keeps a row's
     // pieces within the row
 #pragma unroll 2
@@ -1071,7 +1118,7 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
       const Seg& g = p.g;
       const int32_t n = p.n;
       const int tiles = g.ntok[1] > 0 ? 2 : 1;
-      const int32_t tail = g.tail() - g.t0;
+      const int32_t tail = g.tail - g.t0;
       if (n > 0) {
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
@@ -1128,7 +1175,7 @@ __device__ void multiply(const AttendArgs& a, Cta<DP> cta, uint32_t tmem) {
       if (late) {
         if (ahead == 0) break;
         if (!full()) return;
-        if (p.g.t0 + p.j >= p.g.tail() && !clean()) return;
+        if (p.g.t0 + p.j >= p.g.tail && !clean()) return;
         const int v = ring.stage;
         ring.next();
         if (!values((p.j & 1) ^ p.g.first, p.j < 2, v)) return;
@@ -1313,7 +1360,9 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
       quad[j] = PAGED ? nullptr
                       : reinterpret_cast<T*>(__shfl_sync(
                             ~0u, reinterpret_cast<unsigned long long>(out), (lane & ~3) + j));
-    bool odd = false;  // a value that is not finite
+    // NaN once a value is not finite: 0 times each, summed in pairs (a test of
+    // each took 10 us of 115 for 128 sequences behind a shared document)
+    float2 odd = make_float2(0.f, 0.f);
     if (n > 0) {
       if (!wait_warp(&c->o_done[s], (done - 1) & 1, c, 28)) return;
       tc_fence_after();
@@ -1326,9 +1375,15 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
         tmem_wait_load();
       }
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        o[j] = l == 0.f ? 0.f : o[j] * inv;
-        odd |= b + j < a.dim && !finite(o[j]);
+      for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
+      // columns behind the last step of 16 of the products hold anything
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = h; j < h + 16; j += 2)
+          z = fma2(make_float2(o[j], o[j + 1]), make_float2(0.f, 0.f), z);
+        if (b + h < a.dim) odd = add2(odd, z);
       }
       if (part) {
 #pragma unroll
@@ -1369,37 +1424,69 @@ __device__ void soften(const AttendArgs& a, Cta<DP> cta, uint32_t tmem, int s) {
     }
     if (lse_at) *lse_at = lse;
 
-    const int32_t seen_tiles = n > 0 ? tile0 + (n - 1) * tile_step + 1 : 0;
-    uint32_t todo = __ballot_sync(
-        ~0u, valid && odd && lim < static_cast<int64_t>(seen_tiles) * kTile);
-#pragma unroll 1
-    while (todo != 0) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int32_t flim = __shfl_sync(~0u, lim, src), ftok = __shfl_sync(~0u, tok, src),
-                    fhead = __shfl_sync(~0u, head, src);
-      T* fout = reinterpret_cast<T*>(
-          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), src));
-      float* fpart = reinterpret_cast<float*>(
-          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(part), src));
-      float* flse_at = reinterpret_cast<float*>(
-          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(lse_at), src));
-      float acc[4], flse;
-      if (!fix_row<T, PAGED>(a, c, g, s, flim, ftok, fhead, acc, flse)) continue;
-      __syncwarp();  // behind the row's first stores, which another lane made
-      for (int e = 0; e < 4; ++e) {
-        const int d = lane + 32 * e;
-        if (d < a.dim) {
-          if (PAGED || fpart) fpart[d / 4 * step + d % 4] = acc[e];
-          else fout[d] = from_f<T>(acc[e]);
-        }
-      }
-      if (flse_at && lane == 0) *flse_at = flse;
-      __syncwarp();
-    }
+    // whether the tiles hold keys that the row does not see (what lies behind
+    // the sequence's end was cleared)
+    const int32_t tiles = n > 0 ? tile0 + (n - 1) * tile_step + 1 : 0;
+    if (valid && !finite(odd.x + odd.y) && lim < static_cast<int64_t>(tiles) * kTile &&
+        lim < (PAGED && g.seq < 0 ? a.prefix_len : g.kv_len))
+      c->doubt = 1;
     __syncwarp();
     if (lane == 0) mbar_arrive(&c->seg_empty[k % kSegs]);
   }
+}
+
+// By one warp, each lane the barriers of its number; with `old` ones to give up.
+template <int DP>
+__device__ __forceinline__ void init_barriers(Ctrl* c, bool old = false) {
+  const int i = threadIdx.x & 31;
+  const auto init = [&](uint64_t* bar, uint32_t count) {
+    if (old) mbar_inval(bar);
+    mbar_init(bar, count);
+  };
+  if (i < Layout<DP>::kStages) {
+    init(&c->kv_full[i], 1);
+    init(&c->kv_empty[i], 1);
+  }
+  if (i < 2) {
+    init(&c->q_full[i], 1);
+    init(&c->q_empty[i], 1);
+    init(&c->s_full[i], 1);
+    for (int p = 0; p < kParts; ++p) init(&c->p_full[i][p], kTile);
+    init(&c->o_done[i], 1);
+    init(&c->o_free[i], kTile);
+  }
+  if (i < kSegs) {
+    init(&c->seg_full[i], 1);
+    init(&c->seg_empty[i], 10);  // the loading and multiplying roles, eight warps
+  }
+  if (i < kTails) {
+    init(&c->tail_full[i], 1);
+    init(&c->tail_done[i], 1);
+  }
+}
+
+// The end of every role in a pass: whether there is another one. All copies and
+// products have landed by then (load() and soften() waited for them), so that
+// the barriers can start anew.
+template <int DP>
+__device__ __forceinline__ bool again(Ctrl* c) {
+  const auto together = [] {
+    asm volatile("bar.sync 1, %0;" ::"n"(kAttendThreads) : "memory");
+  };
+  __syncwarp();
+  tc_fence_before();
+  together();
+  if (c->doubt == 0 || c->pass == 2 || c->dead) return false;
+  together();
+  if (threadIdx.x >= kAttendThreads - 32) {
+    init_barriers<DP>(c, true);
+    if ((threadIdx.x & 31) == 0) ++c->pass;
+    get_on(c);
+    mbar_init_fence();
+  }
+  together();
+  tc_fence_after();
+  return true;
 }
 
 template <typename T, int DP, bool PAGED>
@@ -1413,29 +1500,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   cta.base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);  // swizzle atoms are 1 KiB
   Ctrl* c = cta.ctrl();
   const int warp = threadIdx.x >> 5;
-  if (warp == 0) {  // each lane the barriers of its number
-    const int i = threadIdx.x;
-    if (i < L::kStages) {
-      mbar_init(&c->kv_full[i], 1);
-      mbar_init(&c->kv_empty[i], 1);
-    }
-    if (i < 2) {
-      mbar_init(&c->q_full[i], 1);
-      mbar_init(&c->q_empty[i], 1);
-      mbar_init(&c->s_full[i], 1);
-      for (int p = 0; p < kParts; ++p) mbar_init(&c->p_full[i][p], kTile);
-      mbar_init(&c->o_done[i], 1);
-      mbar_init(&c->o_free[i], kTile);
-    }
-    if (i < kSegs) {
-      mbar_init(&c->seg_full[i], 1);
-      mbar_init(&c->seg_empty[i], 10);  // the loading and multiplying roles, eight warps
-    }
-    if (i < kTails) {
-      mbar_init(&c->tail_full[i], 1);
-      mbar_init(&c->tail_done[i], 1);
-    }
-    if (i == 0) c->dead = 0;
+  if (warp == 0) {
+    init_barriers<DP>(c);
+    if (threadIdx.x == 0) c->dead = c->doubt = c->pass = 0;
     mbar_init_fence();
   }
   if (warp == 8) {
@@ -1462,22 +1529,24 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   // 168 registers a thread at the launch: 256 x 216 + 128 x 72 = 384 x 168.
   if (warp < 8) {
     reg_grow<216>();
-    soften<T, DP, PAGED>(a, cta, tmem, warp >> 2);
+#pragma unroll 1
+    do soften<T, DP, PAGED>(a, cta, tmem, warp >> 2);
+    while (again<DP>(c));
   } else {
     reg_shrink<72>();
-    if (warp == 8) {
-      if (elect_one()) multiply<T, DP, PAGED>(a, cta, tmem);
-    } else if (warp == 9) {
-      load<DP, PAGED>(a, &qm, &q1, &km, &vm, cta);
-    } else if (warp == 10) {
-      schedule<DP, PAGED>(a, cta);
-    } else {
-      clear_tails<DP>(cta);
-    }
+#pragma unroll 1
+    do {
+      if (warp == 8) {
+        if (elect_one()) multiply<T, DP, PAGED>(a, cta, tmem);
+      } else if (warp == 9) {
+        load<DP, PAGED>(a, &qm, &q1, &km, &vm, cta);
+      } else if (warp == 10) {
+        schedule<T, DP, PAGED>(a, cta);
+      } else {
+        clear_tails<T, DP>(cta);
+      }
+    } while (again<DP>(c));
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
   if (c->dead) {
     // A wait gave up: loads and products may still be under way. Give them
     // time to land before the memory is handed on.

@@ -168,6 +168,11 @@ __device__ __forceinline__ void async_proxy_fence() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Before a barrier's place is initialised again.
+__device__ __forceinline__ void mbar_inval(uint64_t* bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void reg_grow() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

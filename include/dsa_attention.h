@@ -11,9 +11,10 @@
  *   l   = sum_j 2^(x_j - m);
  *   out = (sum_j 2^(x_j - m) v_j) / l;  lse = m + log2(l)   (base 2).
  * A row that sees no key has out = 0 and lse = -inf. Keys that a row does not
- * see have no influence on it, whatever they hold (rows beside infinities or
- * NaN that they do not see are summed in another order, within the same
- * rounding); a NaN in a key that it sees makes the row NaN.
+ * see have no influence on it, whatever they hold, not on a bit; a NaN in a key
+ * that it sees makes the row NaN, one in a value that dimension of it.
+ * (Infinities or NaN among the values that some row of a block does not see
+ * cost about the time of the block once more.)
  *
  * (out, lse) is a partial output for dsa_merge_attn_out and
  * dsa_correct_attn_out of dsa_dcp_attn.h: runs over disjoint sets of keys

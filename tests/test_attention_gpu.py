@@ -846,3 +846,75 @@ def test_a_stream_with_another_ones_handle_gets_a_workspace_of_its_own(env):
     assert len(ids) == 5 and 2 ** 64 - 1 not in ids
     assert len(dsa._scratch_cache) == 5, f"{len(handles)} handles"
     dsa.release_workspaces()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 4, 64), (8, 1, 128), (6, 2, 40), (2, 2, 104)])
+@pytest.mark.parametrize("ql,kl", [([130, 70, 200], [190, 70, 290]), ([300, 40], [5000, 700]),
+                                   ([128], [128]), ([700], [700])])
+def test_prompt_values_that_are_not_seen_leave_no_trace(env, ql, kl, heads, kv_heads, dim, dtype):
+    """Rows in front of infinities and NaN: the same bits as with any other
+    values there. Rows behind them: what their definition says."""
+    torch, _ = env
+    tq, tk = sum(ql), sum(kl)
+    q, k, v = make(torch, 48, tq, tk, heads, kv_heads, dim, getattr(torch, dtype))
+    clean = check_prompt(env, q, k, v, ql, kl, True)
+    first = kl[0] - ql[0] + ql[0] // 2       # seen by the first sequence's second half
+    v[first, 0, 3] = math.inf
+    v[first + 9, 0, 3] = -math.inf
+    v[first + 5, kv_heads - 1, dim - 1] = math.nan
+    v[first + 20, :, 17] = math.inf
+    v[tk - 1] = math.nan                     # seen by the last query alone
+    k[first + 31, 0] = math.nan              # its rows are NaN from there on
+    out, lse = check_prompt(env, q, k, v, ql, kl, True)
+    for t in (slice(0, ql[0] // 2), slice(ql[0], tq - 1)):
+        assert torch.equal(out[t], clean[0][t]) and torch.equal(lse[t], clean[1][t])
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,dim,page", [
+    (3, 4, 2, 64, 16), (9, 8, 2, 128, 64), (150, 4, 1, 64, 16), (40, 16, 2, 80, 256)])
+def test_shared_prefix_values_that_are_not_seen_leave_no_trace(env, batch, heads, kv_heads, dim,
+                                                               page):
+    """The same for sequences that end inside the prefix."""
+    torch, _ = env
+    prefix = 768
+    t = make_paged(torch, 49, batch, heads, kv_heads, dim, page, prefix,
+                   [(i * 31) % 90 for i in range(batch)], torch.bfloat16)
+    q, k, v, tables, lens = t
+    short = [(i * 97) % 700 for i in range(batch)]
+    for i in range(0, batch, 2):
+        lens[i] = short[i]
+    clean = check_paged(env, *t, prefix)
+
+    def at(pos):
+        return tables[0, pos // page].item(), pos % page
+
+    v[at(420)][0, 3] = math.inf
+    v[at(421)][kv_heads - 1, 5] = math.nan
+    v[at(767)][:] = math.nan
+    v[at(300)][0, 7], v[at(650)][0, 7] = math.inf, -math.inf
+    out, lse = check_paged(env, *t, prefix)
+    front = (lens <= 300)
+    assert front.any() and torch.equal(out[front], clean[0][front])
+    assert torch.equal(lse, clean[1])
+
+
+def test_a_hidden_infinity_does_not_hold_up_a_long_prompt(env):
+    """One infinite value at the end of 262144 tokens; 11 ms without it."""
+    torch, dsa = env
+    n = 262144
+    g = torch.Generator(device="cuda").manual_seed(50)
+    q, k, v = (torch.randn(n, 1, 128, generator=g, device="cuda").bfloat16() for _ in range(3))
+    cu = ints(torch, [0, n])
+    want = dsa.dsa_prompt_attention(q, k, v, cu, cu)
+    v[-1, 0, 77] = math.inf
+    for _ in range(2):
+        first, last = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        first.record()
+        got = dsa.dsa_prompt_attention(q, k, v, cu, cu)
+        last.record()
+        torch.cuda.synchronize()
+    assert dsa.attention_error() == 0
+    assert torch.equal(got[0][:-1], want[0][:-1]) and torch.equal(got[1], want[1])
+    assert got[0][-1].isinf().nonzero().tolist() == [[0, 77]]
+    assert first.elapsed_time(last) < 500, "ms"
