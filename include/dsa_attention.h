@@ -10,11 +10,12 @@
  *   x_j = scale * log2(e) * <q, k_j>;   m = max_j x_j;
  *   l   = sum_j 2^(x_j - m);
  *   out = (sum_j 2^(x_j - m) v_j) / l;  lse = m + log2(l)   (base 2).
- * A row that sees no key has out = 0 and lse = -inf. Keys that a row does not
+ * A row that sees no key has out = 0 and lse = -inf, and so has one all of
+ * whose scores are -inf (of infinities in q or k). Keys that a row does not
  * see have no influence on it, whatever they hold, not on a bit; a NaN in a key
  * that it sees makes the row NaN, one in a value that dimension of it.
- * (Infinities or NaN among the values that some row of a block does not see
- * cost about the time of the block once more.)
+ * (An output that is not finite, of a row that does not see all of its block's
+ * keys, costs about the block's time once more.)
  *
  * (out, lse) is a partial output for dsa_merge_attn_out and
  * dsa_correct_attn_out of dsa_dcp_attn.h: runs over disjoint sets of keys
