@@ -46,13 +46,13 @@
 // (lengths that end in it) is finite in any sane call. Where an output is not
 // finite and its row does not see all of its tiles, the CTA goes through its
 // list again: the clearing warp makes the tiles finite that some row does not
-// see whole, and at the end the scheduling warp adds to each row what it sees
-// of the values that were not (add_seen). Such a CTA takes about twice as long
+// see whole, and at the end each row gets what it sees of the values that were
+// not (add_seen). Such a CTA takes about twice as long
 // (262144 tokens, one hidden infinity: 20 ms, 10 without; rows computed again
 // one by one took 6.8 s). A prefix that rows end in, with a NaN behind them, is
-// read by one warp: 128 sequences on 32768 tokens 13 ms, 0.16 without. In the
-// softmax warps this costs one store: with more code there, 128 sequences
-// behind a shared document took 122 us instead of 105.
+// read by four warps of each CTA: 128 sequences on 32768 tokens 4.8 ms, 0.15
+// without. In the softmax warps this costs one store: with more code there, 128
+// sequences behind a shared document took 122 us instead of 105.
 //
 // Code size matters: the roles of an SM run different code at the same time,
 // and a call with short segments runs each piece only a few times. Loops that
@@ -78,10 +78,9 @@ constexpr float kGrow = 8.0f;        // log2 of the growth that moves a row's ba
 constexpr int kSegs = 8;             // segments that the scheduling warp may be ahead
 // A wait gives up when its CTA has got on with nothing between the second and
 // third turn of the global timer's high word, for 8.6 to 12.9 seconds. What
-// counts are the loads (every 16 rounds of the ring) and the key tiles that are
-// looked through for values that are not finite: a wait may be as long as the
-// call, like that for the next value behind a sequence's end, of which a call
-// may have none.
+// counts are the loads (every 64 steps): a wait may be as long as the call, like
+// that for the next value behind a sequence's end, of which a call may have
+// none.
 constexpr int32_t kWaitTurns = 3;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -122,8 +121,8 @@ struct Seg {
   // prefix_pages; whether a page of the segment is missing
   int32_t seq, gaps;
   int32_t slot;     // of the partial outputs (-1: written out at once)
-  // Passes 1 and 2: the key tile from which on some row does not see all, whose
-  // values are made finite. kNone in pass 0.
+  // Pass 1: the key tile from which on some row does not see all, whose values
+  // are made finite. kNone in pass 0.
   int32_t sane;
   // The key tile from which on values go through the clearing warp: sane, or
   // where values lie behind the sequence's last key (the next sequence's, or
@@ -192,7 +191,7 @@ struct Ctrl {
   uint32_t beat;  // global_turns() when the CTA last got on
   int dead;
   int doubt;  // an output may hold what its row does not see
-  int pass;   // 0; 1: once more, with finite values; 2: what is seen is added
+  int pass;   // 0; 1: once more, with finite values
 };
 constexpr size_t attend_smem(uint32_t ctrl) { return 1024 + ctrl + sizeof(Ctrl); }
 
@@ -693,13 +692,13 @@ __device__ __forceinline__ const T* row_at(const AttendArgs& a, const Seg& g, co
 
 // A masked weight is 0, but 0 times an infinite or NaN value is NaN.
 
-// Pass 2: to 32 rows of a segment (rows 32 w ... of stream s) the values that
-// were made finite in the products and that the row sees. Rows are taken in
+// To 32 rows of a segment (rows 32 w ... of stream s) the values that were made
+// finite in the products and that the row sees. Rows are taken in
 // the order of their ends, so that each key is read once. Weights are over 0,
 // so that the sum of such values is what they make of an output, infinite or
 // NaN.
 template <typename T, int DP, bool PAGED>
-__device__ __forceinline__ void add_seen(const AttendArgs& a, Ctrl* c, const Seg& g, int s, int w) {
+__device__ __forceinline__ void add_seen(const AttendArgs& a, const Seg& g, int s, int w) {
   const int lane = threadIdx.x & 31, row = 32 * w + lane, rt = row / a.group;
   const int qs = g.split ? 0 : s;
   const bool valid = rt < g.ntok[qs];
@@ -738,7 +737,6 @@ __device__ __forceinline__ void add_seen(const AttendArgs& a, Ctrl* c, const Seg
       if (++at == kTile) {
         at = 0;
         ++i;
-        get_on(c);
       }
     }
     T* o = reinterpret_cast<T*>(
@@ -752,6 +750,19 @@ __device__ __forceinline__ void add_seen(const AttendArgs& a, Ctrl* c, const Seg
       if (PAGED || p) p[d / 4 * (4 * kTile) + d % 4] += sum[e];
       else o[d] = from_f<T>(to_f(o[d]) + sum[e]);
     }
+  }
+}
+
+// Behind pass 1: that for all segments of the CTA, by four warps (number w).
+template <typename T, int DP, bool PAGED>
+__device__ __forceinline__ void add_all_seen(const AttendArgs& a, int w) {
+  typename ScheduleOf<PAGED>::type list(a);
+  Seg g;
+#pragma unroll 1
+  while (list.next(a, g)) {
+    g.sane = list.first_masked(a, g);
+#pragma unroll 1
+    for (int i = w; i < 8 && g.sane != kNone; i += 4) add_seen<T, DP, PAGED>(a, g, i >> 2, i & 3);
   }
 }
 
@@ -829,26 +840,19 @@ __device__ __forceinline__ void order(const Place<WARP>& p, const Place<WARP>& q
   values = ahead > 0 && (ahead >= lead || !scores);
 }
 
-template <typename T, int DP, bool PAGED>
+template <int DP, bool PAGED>
 __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
   Ctrl* c = cta.ctrl();
-  const int pass = c->pass;
   typename ScheduleOf<PAGED>::type list(a);
-  uint32_t k = 0;
+  const bool again = c->pass > 0;
 #pragma unroll 1
-  for (;;) {
+  for (uint32_t k = 0;; ++k) {
     Seg g;
+    const int i = k % kSegs;
     const bool more = list.next(a, g);
     if (!more) g.n[0] = -1;
-    g.sane = pass > 0 && more ? list.first_masked(a, g) : kNone;
+    g.sane = again && more ? list.first_masked(a, g) : kNone;
     g.tail = min(g.sane, g.kv_len > 0 ? g.kv_len / kTile : kNone);
-    if (pass == 2 && more) {
-#pragma unroll 1
-      for (int w = 0; w < 8 && g.sane != kNone; ++w)
-        add_seen<T, DP, PAGED>(a, c, g, w >> 2, w & 3);
-      continue;
-    }
-    const int i = k % kSegs;
     if (k >= kSegs && !wait_warp(&c->seg_empty[i], (k / kSegs - 1) & 1, c, 16)) return;
     if ((threadIdx.x & 31) == 0) {
       c->seg[i] = g;
@@ -856,7 +860,6 @@ __device__ void schedule(const AttendArgs& a, Cta<DP> cta) {
     }
     __syncwarp();
     if (!more) return;
-    ++k;
   }
 }
 
@@ -882,8 +885,8 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
     // the list's table, from its first page on, and how many pages are seen
     const int32_t pre = static_cast<int32_t>(a.prefix_len >> a.page_log2);
     const bool own = p.g.seq >= 0;
-    const int32_t* table = own ? a.tables + p.g.seq * a.ld_tables + pre
-                               : a.prefix_pages + ~p.g.seq * a.ld_tables;
+    const int32_t* table = (own ? a.tables + pre : a.prefix_pages) +
+                           (own ? p.g.seq : ~p.g.seq) * a.ld_tables;
     const int32_t count = own ? (p.g.kv_len + a.page_size - 1) >> a.page_log2 : pre;
     const int32_t at = (((p.g.t0 + p.j) * kTile) >> a.page_log2) + lane;
     return lane < pages && at < count ? static_cast<uint32_t>(__ldg(table + at)) : none;
@@ -895,7 +898,6 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
       return false;
     unsigned char* dst = cta.stage(ring.stage);
     ring.next();
-    if (ring.stage == 0 && ring.round % 16 == 0) get_on(c);
     if (elect_one()) mbar_arrive_expect_tx(bar, L::kBytes);
     const int32_t t = (p.g.t0 + p.j) * kTile;
     if constexpr (PAGED) {
@@ -922,9 +924,10 @@ __device__ void load(const AttendArgs& a, const CUtensorMap* qm, const CUtensorM
   if (!q.next(c, false, 17) || !p.next(c, true, 17)) return;
   int ahead = 0;
   uint32_t tails = 0;
-  uint32_t p_ids = look_up(p), q_ids = p_ids;
+  uint32_t p_ids = look_up(p), q_ids = p_ids, steps = 0;
 #pragma unroll 1
   while (p.more) {
+    if (++steps % 64 == 0) get_on(c);
     bool values, scores;
     order(p, q, ahead, values, scores);
     if (values) {
@@ -1476,11 +1479,11 @@ __device__ __forceinline__ bool again(Ctrl* c) {
   __syncwarp();
   tc_fence_before();
   together();
-  if (c->doubt == 0 || c->pass == 2 || c->dead) return false;
+  if (c->doubt == 0 || c->pass > 0 || c->dead) return false;
   together();
   if (threadIdx.x >= kAttendThreads - 32) {
     init_barriers<DP>(c, true);
-    if ((threadIdx.x & 31) == 0) ++c->pass;
+    c->pass = 1;
     get_on(c);
     mbar_init_fence();
   }
@@ -1541,11 +1544,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       } else if (warp == 9) {
         load<DP, PAGED>(a, &qm, &q1, &km, &vm, cta);
       } else if (warp == 10) {
-        schedule<T, DP, PAGED>(a, cta);
+        schedule<DP, PAGED>(a, cta);
       } else {
         clear_tails<T, DP>(cta);
       }
     } while (again<DP>(c));
+    if (c->pass > 0 && !c->dead) add_all_seen<T, DP, PAGED>(a, warp - 8);
   }
   if (c->dead) {
     // A wait gave up: loads and products may still be under way. Give them
