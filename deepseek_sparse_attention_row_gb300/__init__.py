@@ -741,7 +741,8 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
     returns both; a sequence that sees no token gets 0 and -inf.
     ``workspace``: a CUDA uint8 tensor of
     ``shared_prefix_workspace_bytes(...)`` bytes that no overlapping call
-    uses (None: one kept for this thread and stream)."""
+    uses (None: one kept for this thread and stream). Forward only, as
+    ``dsa_prompt_attention``."""
     torch = _torch()
     code = _attention_dtype(q, "q")
     dt, dev = q.dtype, q.get_device()

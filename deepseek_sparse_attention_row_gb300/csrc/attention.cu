@@ -126,10 +126,7 @@ dsa_status launch(const Maps& m, const AttendArgs& a, int32_t dtype, int grid,
 
 template <typename T>
 dsa_status launch_join(const AttendArgs& a, const JoinArgs& j, cudaStream_t stream) {
-  const int64_t rows = a.tokens * a.heads;
-  const int64_t ctas = (rows + kJoinWarps - 1) / kJoinWarps;
-  if (ctas > INT32_MAX) return DSA_EUNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(ctas));
+  const dim3 grid(static_cast<unsigned>((a.tokens * a.heads + kJoinWarps - 1) / kJoinWarps));
   const bool ok = a.dim > 64
                       ? launch_after(join_kernel<T, 128>, grid, kJoinWarps * 32, stream, a, j)
                       : launch_after(join_kernel<T, 64>, grid, kJoinWarps * 32, stream, a, j);
@@ -188,7 +185,7 @@ PromptPlan plan_prompt(int64_t total_q, int64_t total_k, int32_t heads, int32_t 
 struct PagedPlan {
   int32_t tile_tokens, prefix_tiles, prefix_blocks, prefix_split;
   int grid;
-  bool fits;  // units, slots and rows within 32 bits
+  bool fits;  // units, slots and CTAs of the join within 32 bits
   size_t starts, prefix_o, prefix_lse, own_o, own_lse, bytes;
 };
 
@@ -207,7 +204,8 @@ PagedPlan plan_paged(int64_t batch, int32_t heads, int32_t kv_heads, int32_t hea
   const int64_t groups = static_cast<int64_t>(kv_heads) * p.prefix_blocks;
   const int64_t own_tiles = (max_pages * page_size - prefix_len + kTile - 1) / kTile;
   const int64_t most = groups * p.prefix_tiles + batch * kv_heads * own_tiles;
-  p.fits = most <= INT32_MAX / (kTwoTileCost + kSegCost) - 1024;
+  p.fits = most <= INT32_MAX / (kTwoTileCost + kSegCost) - 1024 &&
+           batch * heads <= static_cast<int64_t>(kJoinWarps) * INT32_MAX;
   const int64_t sms = sm_count();
   p.grid = static_cast<int>(most < 1 ? 1 : (most < sms ? most : sms));
   const size_t pslots = p.prefix_tiles > 0 ? groups + p.grid : 0;

@@ -145,8 +145,9 @@ size_t dsa_shared_prefix_workspace_bytes(int64_t batch, int32_t heads,
  * DSA_EUNSUPPORTED as for dsa_prompt_attention, and DSA_EINVAL for a
  * prefix_len that is negative, no multiple of page_size or over max_pages *
  * page_size, a NULL required pointer or a workspace that is too small or not
- * aligned; DSA_EUNSUPPORTED for another page_size, and where batch * kv_heads
- * times the 128-token tiles that a row of `tables` has room for passes 10^8.
+ * aligned, and for ld_tables below max_pages; DSA_EUNSUPPORTED for another
+ * page_size, and where batch * kv_heads times the 128-token tiles that a row of
+ * `tables` has room for passes 10^8, or batch * heads 8 * 10^9.
  */
 dsa_status dsa_shared_prefix_attention(
     const void *q, const void *k_pages, const void *v_pages, int32_t dtype,

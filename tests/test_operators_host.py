@@ -266,3 +266,11 @@ def test_the_merge_takes_no_fp16(dsa):
                                   192, 64, 1, None, 4, 1, None) == DSA_EINVAL
     assert lib.dsa_correct_attn_out(FAKE, F16, 3, 4, 64, 256, 64, 1, FAKE, 2, 12, 4, 1, 0, FAKE,
                                     192, 64, 1, None, 4, 1, None) == DSA_EINVAL
+
+
+@pytest.mark.parametrize("batch,want", [(2 ** 31 - 1, DSA_EUNSUPPORTED), (2 ** 26, DSA_EINVAL)])
+def test_batches_whose_join_has_too_many_ctas(dsa, batch, want):
+    """Refused before a launch; the one below the limit gets as far as its
+    missing workspace. (No pages: the rows alone count.)"""
+    assert shared(dsa.library(), batch=batch, heads=128, kv_heads=1, prefix_len=0,
+                  prefix_pages=None, max_pages=0, num_pages=0, workspace=None) == want
