@@ -268,7 +268,7 @@ def test_the_merge_takes_no_fp16(dsa):
                                     192, 64, 1, None, 4, 1, None) == DSA_EINVAL
 
 
-@pytest.mark.parametrize("batch,want", [(2 ** 31 - 1, DSA_EUNSUPPORTED), (2 ** 26, DSA_EINVAL)])
+@pytest.mark.parametrize("batch,want", [(2 ** 31 - 1, DSA_EUNSUPPORTED), (2 ** 26 - 1, DSA_EINVAL)])
 def test_batches_whose_join_has_too_many_ctas(dsa, batch, want):
     """Refused before a launch; the one below the limit gets as far as its
     missing workspace. (No pages: the rows alone count.)"""
