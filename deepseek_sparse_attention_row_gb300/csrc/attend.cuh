@@ -29,12 +29,12 @@
 // tiles) that the scheduling warp writes to a ring of eight, so that loads and
 // products of the next segment run under the current one's end.
 //
-// What bounds it. Prompts: the tensor cores, active in 77% of the cycles (one
-// full attention of 8192 tokens, 16 heads of 128: 315 us, 1745 TFLOP/s, 0.91
-// of a plain product's burst rate; 16389 causal tokens: 640 us, 1715); the rest
+// What bounds it. Prompts: the tensor cores, active in 78% of the cycles (one
+// full attention of 8192 tokens, 16 heads of 128: 316 us, 1740 TFLOP/s, 0.91
+// of a plain product's burst rate; 16389 causal tokens: 645 us, 1705); the rest
 // is the chain scores - softmax - weights of a stream, about 1100 cycles of
 // softmax a tile, and the ends of segments. Decode on pages: HBM (64 sequences
-// of up to 4096 tokens: 96 us for 527 MB with the join; the loads alone 93).
+// of up to 4096 tokens: 95 us for 527 MB with the join; the loads alone 93).
 //
 // Every wait is bounded (kWaitTurns); one that gives up records its site in
 // g_pipe_error, and all roles leave.
@@ -47,12 +47,12 @@
 // finite and its row does not see all of its tiles, the CTA goes through its
 // list again: the clearing warp makes the tiles finite that some row does not
 // see whole, and at the end each row gets what it sees of the values that were
-// not (add_seen). Such a CTA takes about twice as long
-// (262144 tokens, one hidden infinity: 20 ms, 10 without; rows computed again
-// one by one took 6.8 s). A prefix that rows end in, with a NaN behind them, is
-// read by four warps of each CTA: 128 sequences on 32768 tokens 4.8 ms, 0.15
-// without. In the softmax warps this costs one store: with more code there, 128
-// sequences behind a shared document took 122 us instead of 105.
+// not (add_seen). Such a CTA takes about twice as long (262144 tokens, one
+// hidden infinity: 20 ms, 10 without; rows computed again one by one took 6.8
+// s). A prefix that rows end in, with a NaN behind them, is read by four warps
+// of each CTA: 128 sequences on 32768 tokens 4.8 ms, 0.15 without. In the
+// softmax warps this costs one store: with more code there, 128 sequences
+// behind a shared document took 122 us instead of 105.
 //
 // Code size matters: the roles of an SM run different code at the same time,
 // and a call with short segments runs each piece only a few times. Loops that
@@ -274,7 +274,7 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, int32_t seq, int
 // and join_blocks_kernel joins them.
 // Without cuts (a.cut = 0: few keys, where the join would cost more than it
 // evens out) every block is one unit. kBlockCost = 2, 4, 6, 8 tiles: packed
-// prefill chunk 411, 367, 369, 375 us, one long prompt 776, 647, 687, 699.
+// prefill chunk 351, 339, 349, 350 us, one long prompt 665, 645, 662, 664.
 constexpr int32_t kBlockCost = 4 * kTile;
 constexpr int32_t kMinShare = 4 * kTile;
 
@@ -491,9 +491,10 @@ __device__ __forceinline__ int32_t own_tokens(const AttendArgs& a, int64_t b) {
 // tiles, which falls to the share that holds the tile's first unit. A share is
 // a list of segments, a group's tiles each; segment (group g, CTA x) has slot
 // g + x, which grows along the line: no two segments share one. The costs are
-// fitted: (group, one row tile, two) = (12, 4, 6) gave 53.6 us for 64 chat
-// sequences behind 8192 shared tokens and 114 for 128 behind 32768; (8, 4, 5)
-// 57 and 115, (12, 4, 7) 54.6 and 124, (20, 4, 7) 53.7 and 117.
+// fitted to two batches, and where the cuts fall moves the best point with any
+// change of the kernel: (group, one row tile, two) = (12, 4, 6) takes 53.8 us
+// for 64 chat sequences behind 8192 shared tokens and 105 for 128 behind 32768;
+// (8, 4, 5) 53.0 and 104, (12, 4, 7) 56.0 and 117, (20, 4, 7) 51.1 and 108.
 constexpr int32_t kSegCost = 12;
 constexpr int32_t kTileCost = 4;        // one row tile
 constexpr int32_t kTwoTileCost = 6;     // two row tiles, bound by products

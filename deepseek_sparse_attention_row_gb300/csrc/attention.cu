@@ -153,10 +153,14 @@ struct PromptPlan {
 
 // Blocks are cut where the batch has more than kCutKeys keys and kCutMean on
 // average for a sequence, or more than kCutBatch. Cut / whole, us (32 query
-// heads, 8 key/value heads, causal, head dimension 128): 1024 keys 25.2 / 20.1;
-// 2048 keys 42.0 / 53.5; one query on 1500 keys 16.9 / 21.8; 8 x 512 keys 41.5
-// / 41.0 (8 heads 22.4 / 15.2); 4 x 800 41.9 / 42.3; 4 x 1024 53.1 / 62.2; 80 x
-// 100 54.0 / 52.4; 2500, 10 and 900 keys with 8 heads 23.7 / 34.2.
+// heads, 8 key/value heads, causal, head dimension 128): 1024 keys 25.0 / 20.0;
+// 2048 keys 42.7 / 53.1; one query on 1500 keys 17.2 / 22.3; 8 x 512 keys 41.6
+// / 41.3 (8 query heads on 2: 21.4 / 15.0); 4 x 800 41.8 / 40.9; 4 x 1024 54.0 /
+// 60.6; 80 x 100 51.7 / 49.0; 2500, 10 and 900 keys 62.9 / 88.8 (8 query heads
+// on 2: 29.4 / 34.8). The lengths themselves are on the device: a mean says
+// nothing of a batch in which one sequence has most of the keys and the others
+// few, and there whole blocks lose (full attention, 128 heads on 8, queries
+// 1060, 3357, 175, 2 on keys 2, 173, 2632, 12: 127 / 469).
 constexpr int64_t kCutKeys = 1400, kCutMean = 800, kCutBatch = 8192;
 
 PromptPlan plan_prompt(int64_t total_q, int64_t total_k, int32_t heads, int32_t kv_heads,
