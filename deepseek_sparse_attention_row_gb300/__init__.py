@@ -735,7 +735,8 @@ def dsa_shared_prefix_attention(q, k_pages, v_pages, tables, lens, prefix_len: i
     (int32 [B, P]); the sequence sees its first ``lens``[b] tokens (int32
     [B]). The prefix is read once, through ``prefix_pages`` (int32, by default
     the first row of ``tables`` that is not an empty slot's, of length 0 and
-    with a negative first entry); 0 gives plain paged decode attention. Pages
+    with a negative first entry; ``tables[0]`` stands for that too); 0 gives
+    plain paged decode attention. Pages
     numbered outside [0, N) are not seen. Writes ``out`` [B, H, D] and the
     base-2 log-sum-exp ``lse_out`` [B, H] fp32 (allocated when None) and
     returns both; a sequence that sees no token gets 0 and -inf.

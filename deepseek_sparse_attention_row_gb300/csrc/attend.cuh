@@ -694,10 +694,9 @@ __device__ __forceinline__ const T* row_at(const AttendArgs& a, const Seg& g, co
 // A masked weight is 0, but 0 times an infinite or NaN value is NaN.
 
 // To 32 rows of a segment (rows 32 w ... of stream s) the values that were made
-// finite in the products and that the row sees. Rows are taken in
-// the order of their ends, so that each key is read once. Weights are over 0,
-// so that the sum of such values is what they make of an output, infinite or
-// NaN.
+// finite in the products and that the row sees. Rows are taken in the order of
+// their ends, so that each key is read once. Weights are over 0, so that the
+// sum of such values is what they make of an output, infinite or NaN.
 template <typename T, int DP, bool PAGED>
 __device__ __forceinline__ void add_seen(const AttendArgs& a, const Seg& g, int s, int w) {
   const int lane = threadIdx.x & 31, row = 32 * w + lane, rt = row / a.group;
@@ -1010,7 +1009,8 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x & ~__vcmpeq2(x & kOnes, kOnes);
 }
 
-// The warp that clears V tiles behind their sequences' ends.
+// The warp that clears V tiles behind their sequences' ends and, in pass 1,
+// makes the rows before that finite where some row does not see them.
 template <typename T, int DP>
 __device__ void clear_tails(Cta<DP> cta) {
   using L = Layout<DP>;
