@@ -1,8 +1,8 @@
 """GB300 (sm_103a) DSA candidate-block selection.
 
 A thin binding over ``libdsa_cb.so`` (C ABI declared in ``include/dsa_cb.h``,
-``include/dsa_dcp_attn.h``, ``include/dsa_attention.h`` and
-``include/dsa_cache.h``):
+``include/dsa_dcp_attn.h``, ``include/dsa_attention.h``,
+``include/dsa_cache.h``, ``include/dsa_rotary.h`` and ``include/dsa_quant.h``):
 argument marshalling only. Every step of the computation runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback, and every call
 raises if the library is missing or a call fails.
@@ -27,13 +27,20 @@ Functions carry the C ABI's names:
   (``include/dsa_attention.h``).
 * ``dsa_cache_fork`` / ``dsa_cache_free`` / ``dsa_cache_compact`` -- the pages
   of such a cache (``include/dsa_cache.h``).
+* ``dsa_rotary`` -- queries and keys turned by their positions, or gradients
+  turned back (``include/dsa_rotary.h``); ``rotary_frequencies`` and
+  ``rotary_turns`` lay its angles out.
+* ``dsa_quant_cache_write`` / ``dsa_quant_cache_read`` /
+  ``dsa_quant_attention`` -- pages of 8-bit codes with a scale for each block
+  of tokens and head: written, read back as packed rows, and attended to by
+  single tokens (``include/dsa_quant.h``).
 
 Tensors are PyTorch CUDA tensors (PyTorch supplies device memory and the
 current stream) or pinned host tensors, which the kernels read and write in
 place through ``dsa_mapped_host_pointer`` (across NVLink-C2C on Grace
 systems). Logits may be float32 or bfloat16 (the ``*_bf16`` C entry points);
-scores follow the logits' dtype. The attention and cache operators take CUDA
-tensors only. ``select_candidate_blocks[_sharded]_host``
+scores follow the logits' dtype. The attention, cache and rotary operators
+take CUDA tensors only. ``select_candidate_blocks[_sharded]_host``
 take host tensors and wait for the ids: pinned inputs are read in place
 (only the in-window logits cross the link), other host tensors are copied to
 the device first.
@@ -43,6 +50,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import threading
 from typing import Optional
@@ -63,6 +71,12 @@ __all__ = [
     "dsa_cache_fork",
     "dsa_cache_free",
     "dsa_cache_compact",
+    "dsa_rotary",
+    "rotary_frequencies",
+    "rotary_turns",
+    "dsa_quant_cache_write",
+    "dsa_quant_cache_read",
+    "dsa_quant_attention",
     "FORK_OK",
     "FORK_NO_PAGE",
     "FORK_REFUSED",
@@ -71,6 +85,7 @@ __all__ = [
     "prompt_workspace_bytes",
     "shared_prefix_workspace_bytes",
     "cache_workspace_bytes",
+    "quant_attention_workspace_bytes",
     "release_workspaces",
     "max_select_blocks",
     "mapped_host_pointer",
@@ -119,6 +134,11 @@ EXPORTED_SYMBOLS = (
     "dsa_cache_fork",
     "dsa_cache_free",
     "dsa_cache_compact",
+    "dsa_rotary",
+    "dsa_quant_cache_write",
+    "dsa_quant_cache_read",
+    "dsa_quant_attention_workspace_bytes",
+    "dsa_quant_attention",
 )
 
 # Knobs of dsa_select_set_launch_override (include/dsa_cb.h).
@@ -203,8 +223,21 @@ def library():
     lib.dsa_cache_free.argtypes = [p, i64, p, i64, i64, i64, p, p, i64, p]
     lib.dsa_cache_compact.argtypes = [p, i64, i64, i64, i64, i32, i64, p, p, i64, i64, i64, p, p,
                                       p, sz, p]
+    lib.dsa_rotary.argtypes = [p, p, i32, i64, i64, i64, i64, p, p, i32, i64, i64, i64, i64, i32,
+                               i64, i32, p, p, i32, i32, f32, i32, p]
+    rows, strides = [i64] * 4, [i64] * 8
+    lib.dsa_quant_cache_write.argtypes = [p, p, i32, i64, i32, i32, *rows, p, i32, p, p, i64, i32,
+                                          i32, *strides[:6], p, p, i64, i64, p, i64, i64, p, p]
+    lib.dsa_quant_cache_read.argtypes = [p, p, p, p, i64, i32, i32, i32, i32, *strides, p, i64,
+                                         i64, p, i32, i64, i32, p, i64, i64, p, i64, i64, p]
+    lib.dsa_quant_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i32]
+    lib.dsa_quant_attention_workspace_bytes.restype = sz
+    lib.dsa_quant_attention.argtypes = [p, i32, i64, i32, i32, i32, i64, i64, p, p, p, p, i64, i32,
+                                        i32, *strides, p, i64, i64, p, f32, p, i64, i64, p, i64,
+                                        i64, p, sz, p]
     for f in (lib.dsa_prompt_attention, lib.dsa_shared_prefix_attention, lib.dsa_cache_fork,
-              lib.dsa_cache_free, lib.dsa_cache_compact):
+              lib.dsa_cache_free, lib.dsa_cache_compact, lib.dsa_rotary, lib.dsa_quant_cache_write,
+              lib.dsa_quant_cache_read, lib.dsa_quant_attention):
         f.restype = ctypes.c_int
     for name in ("dsa_block_scores", "dsa_select_candidate_blocks",
                  "dsa_select_candidate_blocks_sharded", "dsa_mask_candidate_logits",
@@ -972,6 +1005,304 @@ def cache_workspace_bytes(pairs: int, num_pages: int) -> int:
     """Bytes of workspace of ``dsa_cache_fork`` (of ``pairs`` pairs) or, with
     0 pairs, of ``dsa_cache_compact``."""
     return library().dsa_cache_workspace_bytes(pairs, num_pages)
+
+
+_ROTARY_DTYPES = {}
+
+
+def _rotary_dtype(t, name):
+    if not _ROTARY_DTYPES:
+        torch = _torch()
+        _ROTARY_DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
+                               torch.float16: DTYPE_F16})
+    code = _ROTARY_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, stretch: float = 1.0,
+                       method: str = "linear", trained: int = 8192, slow: float = 1.0,
+                       fast: float = 32.0):
+    """Radians per token of the ``rotary_dim`` / 2 pairs, base^(-2i/rotary_dim),
+    as a float64 CPU tensor, for a context ``stretch`` times as long as the
+    trained one:
+
+    * ``"linear"``: every frequency divided by ``stretch``.
+    * ``"base"``: the base raised to base * stretch^(R / (R - 2)), which keeps
+      the fastest pair and divides the slowest by ``stretch``.
+    * ``"parts"``: pairs that turn ``fast`` times or more within ``trained``
+      tokens are kept, those that turn ``slow`` times or less are divided by
+      ``stretch``, those between are mixed linearly in their turns."""
+    torch = _torch()
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
+    if not base > 0 or not stretch > 0:
+        raise ValueError(f"base and stretch must be positive, got {base} and {stretch}")
+    if method not in ("linear", "base", "parts"):
+        raise ValueError(f'method must be "linear", "base" or "parts", got {method!r}')
+    if method == "base":
+        if rotary_dim < 4 and stretch != 1.0:
+            raise ValueError("a single pair has no base to raise")
+        base = base * stretch ** (rotary_dim / max(rotary_dim - 2, 1))
+    f = float(base) ** (-torch.arange(rotary_dim // 2, dtype=torch.float64) * 2 / rotary_dim)
+    if method == "linear":
+        return f / stretch
+    if method == "base":
+        return f
+    if not fast > slow or not trained > 0:
+        raise ValueError(f"expected fast > slow and trained > 0, got {fast}, {slow}, {trained}")
+    keep = ((f * trained / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+    return f * (keep + (1 - keep) / stretch)
+
+
+def rotary_turns(frequencies, device="cuda"):
+    """The ``turns`` of ``dsa_rotary`` for these radians per token (a sequence
+    or tensor, taken in fp64): turns per token in fixed point, 2^64 to a turn,
+    as an int64 tensor on ``device``. Laid out once for a model."""
+    torch = _torch()
+    if isinstance(frequencies, torch.Tensor):
+        if frequencies.dim() != 1:
+            raise ValueError(f"frequencies must be a vector, got {tuple(frequencies.shape)}")
+        frequencies = frequencies.double().tolist()
+    values = [float(f) / (2 * math.pi) for f in frequencies]
+    if not all(math.isfinite(x) for x in values):
+        raise ValueError("frequencies must be finite")
+    # a float times 2^64 is a float, and its integer exact
+    fixed = [(round(x * 2.0 ** 64) + 2 ** 63) % 2 ** 64 - 2 ** 63 for x in values]
+    return torch.tensor(fixed, dtype=torch.int64, device=device)
+
+
+def _rotary_rows(x, out, name, code, index, tokens, dim):
+    """Addresses, heads and strides of an input and its output, if given."""
+    xp, shape, st = _on_gpu(x, x.dtype, name, 3, index)
+    if tokens is not None and (shape[0] != tokens or shape[2] != dim):
+        raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {tuple(shape)}")
+    st = _row_strides(shape, st, name)
+    if out is None:
+        return xp, shape, st, None, None
+    op, oshape, ost = _on_gpu(out, x.dtype, name + "_out", 3, index)
+    if oshape != shape:
+        raise ValueError(f"{name}_out must be {tuple(shape)}, got {tuple(oshape)}")
+    ost = _row_strides(oshape, ost, name + "_out")
+    if op == xp and ost != st:
+        raise ValueError(f"{name}_out must be {name} itself or lie apart from it")
+    return xp, shape, st, op, ost
+
+
+def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: float = 1.0,
+               transpose: bool = False, q_out=None, k_out=None, stream=None):
+    """Queries and keys turned by their positions, in one launch.
+
+    ``q`` [T, H, D] and ``k`` [T, Hkv, D] (or None) bfloat16, float16 or
+    float32; ``positions`` int32 [T]; ``turns`` int64 [R / 2] from
+    ``rotary_turns``: the first R elements of each head are turned in pairs (i,
+    i + R/2), or (2i, 2i + 1) if ``interleaved``, and multiplied by ``factor``;
+    the others are copied. ``transpose`` applies the transposed map: given the
+    gradients of the outputs it gives those of the inputs (and, with factor 1,
+    turns heads back). Writes ``q_out`` and ``k_out`` (allocated when None; they
+    may be ``q`` and ``k`` themselves) and returns both. The outputs carry no
+    autograd graph."""
+    torch = _torch()
+    code = _rotary_dtype(q, "q")
+    dev = q.get_device()
+    qp, qs, qst, qop, qost = _rotary_rows(q, q_out, "q", code, None, None, None)
+    T, H, D = qs
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        kp = kop = None
+        ks, kst, kost = (T, 0, D), (0, 0), (0, 0)
+    else:
+        if k.dtype is not q.dtype:
+            raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+        kp, ks, kst, kop, kost = _rotary_rows(k, k_out, "k", code, dev, T, D)
+    pp, n = _vector(positions, "positions", dev)
+    if n != T:
+        raise ValueError(f"positions holds {n} entries, expected {T}")
+    tp, (pairs,), (step,) = _on_gpu(turns, torch.int64, "turns", 1, dev)
+    if pairs > 1 and step != 1:
+        raise ValueError("turns must be contiguous")
+    if 2 * pairs > D:
+        raise ValueError(f"{pairs} pairs do not fit in heads of {D}")
+    mode = (pairs, 1 if interleaved else 0, float(factor), 1 if transpose else 0)
+
+    def enqueue(handle):
+        qo, ko, qa, ka, qb, kb = q_out, k_out, qop, kop, qost, kost
+        if qo is None:
+            qo = torch.empty(qs, dtype=q.dtype, device=q.device)
+            qa, qb = qo.data_ptr() or None, (H * D, D)
+        if ko is None and k is not None:
+            ko = torch.empty(ks, dtype=q.dtype, device=q.device)
+            ka, kb = ko.data_ptr() or None, (ks[1] * D, D)
+        st = library().dsa_rotary(qp, qa, H, *qst, *qb, kp, ka, ks[1], *kst, *kb, code, T, D, pp,
+                                  tp, *mode, handle)
+        if st:
+            _check("dsa_rotary", st)
+        return qo, ko
+
+    return _call(dev, stream, enqueue)
+
+
+def _quant_pool(k_pages, v_pages, k_scales, v_scales, tables, index):
+    """Addresses, sizes and strides of the pages, scales and tables of an 8-bit
+    cache on device ``index``."""
+    torch = _torch()
+    kp, shape, kst = _on_gpu(k_pages, torch.float8_e4m3fn, "k_pages", 4, index)
+    vp, vshape, vst = _on_gpu(v_pages, torch.float8_e4m3fn, "v_pages", 4, index)
+    if vshape != shape:
+        raise ValueError(f"k_pages {tuple(shape)} and v_pages {tuple(vshape)} do not match")
+    N, page, Hkv, D = shape
+    scales = []
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        sp, (n, per, heads), st = _on_gpu(t, torch.float32, name, 3, index)
+        if n != N or heads != Hkv or per < 1 or page % per:
+            raise ValueError(f"{name} must be [{N}, page / block, {Hkv}], got {tuple(t.shape)}")
+        if (heads > 1 and st[2] != 1) or (per > 1 and st[1] != heads):
+            raise ValueError(f"the pages of {name} must be contiguous")
+        scales.append((sp, per, st[0] if n > 1 else per * heads))
+    (ksp, per, ksn), (vsp, vper, vsn) = scales
+    if vper != per:
+        raise ValueError(f"k_scales {tuple(k_scales.shape)} and v_scales {tuple(v_scales.shape)} "
+                         "do not match")
+    tp, (S, P), tst = _on_gpu(tables, torch.int32, "tables", 2, index)
+    if P > 1 and tst[1] != 1:
+        raise ValueError("tables must have unit stride in its last dimension")
+    return ((kp, vp), (ksp, vsp), (N, page, page // per), (Hkv, D),
+            (*_row_strides(shape, kst, "k_pages"), *_row_strides(shape, vst, "v_pages")),
+            (ksn, vsn), (tp, P, tst[0] if S > 1 else P), S)
+
+
+def dsa_quant_cache_write(k, v, cu, k_pages, v_pages, k_scales, v_scales, tables, lens, *,
+                          stream=None):
+    """Append tokens to sequences on pages of 8-bit codes, in place.
+
+    ``k`` and ``v`` [T, Hkv, D] bfloat16 or float16, D a multiple of 16 up to
+    128; row cu[s] + i (``cu`` int32 [S + 1]) becomes token lens[s] + i of
+    sequence s, on page ``tables``[s, token // page] (int32 [S, P]). ``lens``
+    int32 [S], the tokens held before, is left as it is. ``k_pages`` and
+    ``v_pages`` [N, page, Hkv, D] float8_e4m3fn; ``k_scales`` and ``v_scales``
+    [N, page / block, Hkv] float32, the pages of each contiguous. A block's
+    scale is the least power of two that holds its largest value, old and new;
+    codes that are there already are rounded to a scale that grew. Tokens
+    without a page are dropped."""
+    code = _attention_dtype(k, "k")
+    dt, dev = k.dtype, k.get_device()
+    kp, ks, kst = _on_gpu(k, dt, "k", 3)
+    vp, vs, vst = _on_gpu(v, dt, "v", 3, dev)
+    pages, scales, sizes, heads, strides, steps, table, S = _quant_pool(k_pages, v_pages, k_scales,
+                                                                        v_scales, tables, dev)
+    if ks != vs or ks[1:] != heads:
+        raise ValueError(f"k {tuple(ks)}, v {tuple(vs)} and pages {tuple(k_pages.shape)} do not "
+                         "match")
+    (cp, nc), (lp, n) = _vector(cu, "cu", dev), _vector(lens, "lens", dev)
+    if nc != S + 1 or n != S:
+        raise ValueError(f"cu holds {nc} offsets and lens {n} lengths for {S} rows of tables")
+    st = _call(dev, stream, library().dsa_quant_cache_write, kp, vp, code, ks[0], *heads,
+               *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cp, S, *pages, *sizes,
+               *strides, *scales, *steps, *table, lp)
+    if st:
+        _check("dsa_quant_cache_write", st)
+
+
+def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, total=None,
+                         dtype=None, k_out=None, v_out=None, stream=None):
+    """The first tokens of each sequence as packed rows, the ``k`` and ``v`` of
+    ``dsa_prompt_attention``.
+
+    Pages, scales and ``tables`` [S, P] as for ``dsa_quant_cache_write``; token i
+    of sequence s becomes row cu[s] + i, for i < cu[s + 1] - cu[s] (``cu`` int32
+    [S + 1]). Writes ``k_out`` and ``v_out`` [T, Hkv, D] and returns them; when
+    None they are allocated with T = ``total`` rows (which has to be given) of
+    ``dtype`` (bfloat16 when None, or float16). Rows of no sequence are left
+    as they were, those of tokens without a page are 0."""
+    torch = _torch()
+    dev = k_pages.get_device()
+    pages, scales, sizes, heads, strides, steps, table, S = _quant_pool(
+        k_pages, v_pages, k_scales, v_scales, tables, None if dev < 0 else dev)
+    cp, nc = _vector(cu, "cu", dev)
+    if nc != S + 1:
+        raise ValueError(f"cu holds {nc} offsets for {S} rows of tables")
+    given = [t for t in (k_out, v_out) if t is not None]
+    if given:
+        if total is not None and total != given[0].shape[0]:
+            raise ValueError(f"total is {total}, the output has {given[0].shape[0]} rows")
+        if dtype is not None and dtype is not given[0].dtype:
+            raise TypeError(f"dtype is {dtype}, the output {given[0].dtype}")
+        total, dtype = given[0].shape[0], given[0].dtype
+    elif total is None:
+        raise ValueError("total, the number of rows, is needed where no output is given")
+    total, dtype = int(total), torch.bfloat16 if dtype is None else dtype
+    if total < 0:
+        raise ValueError(f"total must not be negative, got {total}")
+    shape = (total, *heads)
+
+    def enqueue(k_out, v_out, handle):
+        outs, args = [], []
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=k_pages.device)
+            code = _attention_dtype(t, name)
+            op, oshape, ost = _on_gpu(t, dtype, name, 3, dev)
+            if oshape != shape:
+                raise ValueError(f"{name} must be {shape}, got {tuple(oshape)}")
+            outs.append(t)
+            args += [op, *_row_strides(oshape, ost, name)]
+        st = library().dsa_quant_cache_read(*pages, *scales, *sizes, *heads, *strides, *steps,
+                                            *table, cp, S, total, code, *args, handle)
+        if st:
+            _check("dsa_quant_cache_read", st)
+        return outs[0], outs[1]
+
+    return _call(dev, stream, enqueue, k_out, v_out)
+
+
+def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *, scale=None,
+                        out=None, lse_out=None, workspace=None, stream=None):
+    """Attention of one query token per sequence on pages of 8-bit codes.
+
+    ``q`` [B, H, D] bfloat16 or float16; pages, scales and ``tables`` [B, P] as
+    for ``dsa_quant_cache_write``; sequence b sees its first ``lens``[b] tokens
+    (int32 [B]), but for those on pages numbered outside [0, N). ``scale``
+    defaults to 1/sqrt(D). Writes ``out`` [B, H, D] and the base-2 log-sum-exp
+    ``lse_out`` [B, H] fp32 (allocated when None) and returns both; a sequence
+    that sees no token gets 0 and -inf. ``workspace``: a CUDA uint8 tensor of
+    ``quant_attention_workspace_bytes(...)`` bytes that no overlapping call
+    uses (None: one kept for this thread and stream). Forward only, as
+    ``dsa_prompt_attention``."""
+    code = _attention_dtype(q, "q")
+    dev = q.get_device()
+    qp, qs, qst = _on_gpu(q, q.dtype, "q", 3)
+    pages, scales, sizes, heads, strides, steps, table, S = _quant_pool(k_pages, v_pages, k_scales,
+                                                                        v_scales, tables, dev)
+    B, H, D = qs
+    lp, n = _vector(lens, "lens", dev)
+    if D != heads[1]:
+        raise ValueError(f"q {tuple(qs)} and pages {tuple(k_pages.shape)} do not match")
+    if n != B or S != B:
+        raise ValueError(f"tables {tuple(tables.shape)} and lens {tuple(lens.shape)} do not "
+                         f"match q {tuple(qs)}")
+    args = (qp, code, B, H, *heads, *_row_strides(qs, qst, "q"), *pages, *scales, *sizes, *strides,
+            *steps, *table, lp, _scale(scale, D))
+
+    def enqueue(out, lse_out, handle):
+        out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
+        held, ws, ws_bytes = _scratch(
+            workspace, _need("dsa_quant_attention_workspace_bytes", dev, B, H, heads[0], D,
+                             table[1], sizes[1]), q, handle)
+        st = library().dsa_quant_attention(*args, *outs, ws, ws_bytes, handle)
+        if st:
+            _check("dsa_quant_attention", st)
+        return out, lse_out
+
+    return _call(dev, stream, enqueue, out, lse_out)
+
+
+def quant_attention_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int,
+                                    max_pages: int, page_size: int) -> int:
+    """Bytes of workspace of a ``dsa_quant_attention`` call."""
+    return library().dsa_quant_attention_workspace_bytes(batch, heads, kv_heads, head_dim,
+                                                         max_pages, page_size)
 
 
 def _to_device(host, dev_buf, stream):
