@@ -1,0 +1,918 @@
+// quant_attend.cuh -- the kernels of dsa_quant_attention (include/dsa_quant.h):
+// single tokens over pages of e4m3 codes.
+//
+// The heads that share a key/value head are the columns (8 or 16) of both
+// products, and keys and dimensions their rows, so that no row of a tensor
+// instruction is padding:
+//   S^T [keys x heads] = K [keys x dim] Q^T,   O^T [dim x heads] += V^T P^T.
+// A warp works alone: it goes through a line of 4 KiB tiles of keys (32 of up to
+// 128 dimensions, 64 of up to 64) with its codes on their way by cp.async into
+// shared memory that only the lane that asked for them reads, so that no
+// barrier stands between a load and its use. Codes become fp16 in registers,
+// which is exact; so are queries after a power of two that brings the largest
+// of a row to 2^14.
+//
+// Each (sequence, key/value head) is a row of tiles; the rows lie on one line
+// that is cut into equal shares, one for each warp of the GPU. Rows that lie
+// within a warp's share are finished by it; pieces are joined by their
+// log-sum-exps, first within the CTA at its end, then, for rows that pass from
+// CTA to CTA, by a second launch.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cfloat>
+
+#include "follow.cuh"
+#include "quant.cuh"
+
+namespace dsa {
+
+constexpr int kQuantWarps = 8;
+constexpr int kQuantThreads = 32 * kQuantWarps;
+constexpr int kQuantTileBytes = 4096;
+
+struct QuantAttnArgs {
+  QuantPool pool;
+  const void* q;
+  int64_t q_sb, q_sh;
+  int64_t batch;
+  int32_t group, splits, split_heads;  // a group's heads, its parts, and heads of a part
+  int32_t rows;                        // kv_heads * splits
+  const int32_t* lens;
+  float c;  // scale * log2 e
+  void* out;
+  int64_t o_sb, o_sh;
+  float* lse;
+  int64_t l_sb, l_sh;
+  int32_t bf16;
+  int32_t whole;    // a CTA for each row
+  int32_t* starts;  // [batch + 1] tiles in front of each sequence
+  float* part_o;    // [2 grid][heads][DP]
+  float* part_lse;  // [2 grid][heads]
+};
+
+template <int DP, int NT>
+struct QuantLayout {
+  static constexpr int kTile = kQuantTileBytes / DP;  // keys
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kScales = kTile * 8;  // bytes of a tile's two scales
+  static constexpr int kRing = 4 * kQuantTileBytes + 2 * kScales;
+  static constexpr int kPiece = kHeads * DP * 4;
+  static constexpr int kWarp = kRing + kPiece;
+  static constexpr int kSmem = kQuantWarps * kWarp;
+  static_assert(kPiece <= kRing, "a tail piece lies over the ring");
+};
+
+// ---- instructions ----------------------------------------------------------
+
+__device__ __forceinline__ uint32_t shared_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 or 8 bytes, zeros where `yes` is false (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool yes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(yes ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool yes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+               "r"(yes ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool yes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(yes ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float shared4(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+// [16 x 16] by [16 x 8] of fp16, added in fp32.
+__device__ __forceinline__ void product(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit elements, two of a row in each lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float power_of_two(float x) {  // 2^x, within 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---- the line of tiles -----------------------------------------------------
+
+// Unit at which share i of n begins.
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t i, int64_t n) {
+  return total * i / n;
+}
+
+__device__ __forceinline__ int32_t quant_length(const QuantAttnArgs& a, int64_t b) {
+  const int64_t most = a.pool.max_pages << a.pool.page_log2, n = a.lens[b];
+  return static_cast<int32_t>(n < 0 ? 0 : (n < most ? n : most));
+}
+
+// A place on the line.
+struct Spot {
+  int64_t b;
+  int32_t row, tile, tiles, tokens;
+};
+
+template <int TILE>
+__device__ __forceinline__ void enter(const QuantAttnArgs& a, Spot& s) {
+  s.tokens = quant_length(a, s.b);
+  s.tiles = (s.tokens + TILE - 1) / TILE;
+}
+// To the next tile; never called behind the last one of the line.
+template <int TILE>
+__device__ __forceinline__ void advance(const QuantAttnArgs& a, Spot& s) {
+  if (++s.tile < s.tiles) return;
+  s.tile = 0;
+  if (++s.row < a.rows) return;
+  s.row = 0;
+  do {
+    ++s.b;
+    enter<TILE>(a, s);
+  } while (s.tiles == 0 && s.b + 1 < a.batch);
+}
+
+// ---- output ----------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t pack_pair(const QuantAttnArgs& a, float lo, float hi) {
+  if (a.bf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return half_pair(lo, hi);
+}
+
+// The first query head of a row, and how many it has.
+__device__ __forceinline__ int32_t row_heads(const QuantAttnArgs& a, int32_t row, int32_t& first) {
+  const int32_t kv = row / a.splits, part = row - kv * a.splits;
+  first = kv * a.group + part * a.split_heads;
+  return min(a.split_heads, a.group - part * a.split_heads);
+}
+
+__device__ __forceinline__ uint16_t* out_row(const QuantAttnArgs& a, int64_t b, int32_t head) {
+  return static_cast<uint16_t*>(a.out) + b * a.o_sb + head * a.o_sh;
+}
+
+// Pieces of a row that a warp leaves for the CTA's end.
+struct PieceInfo {
+  int64_t b[2];
+  int32_t row[2];
+  int32_t has[2];  // head piece (the row began before), tail piece (it goes on behind)
+  int32_t ends;    // the head piece ends its row
+  int32_t empty;   // no share
+};
+
+// ---- the kernel ------------------------------------------------------------
+
+template <int DP, int NT>
+struct QuantWarp {
+  using L = QuantLayout<DP, NT>;
+  static constexpr int kTile = L::kTile;
+  static constexpr int kGroups = kTile / 16;  // of 16 keys
+  static constexpr int kChunks = DP / 64;     // 16-byte chunks of a key in a lane
+  static constexpr int kSteps = DP / 16;      // of 16 dimensions
+  static constexpr int kMasks = kTile / 32;
+
+  const QuantAttnArgs& a;
+  const int lane, g, t;
+  const uint32_t ring;  // this warp's shared memory
+
+  // loads: the tile that is due next, and the pages of its groups (lane i: group i)
+  Spot due;
+  int32_t due_page;
+  int64_t due_left;  // tiles from it to the share's end
+  uint32_t due_ok[kMasks];
+
+  uint32_t qf[NT][kSteps][2];
+  float q_power[NT][2];  // of the columns' heads
+  float o[NT][DP / 16][4];
+  float l[NT][2], m[NT][2], big[NT][2];  // sums; bases of the sums and of the weights
+
+  __device__ __forceinline__ QuantWarp(const QuantAttnArgs& args, uint32_t smem)
+      : a(args), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3), ring(smem) {}
+
+  __device__ __forceinline__ uint32_t k_slot(int stage) const {
+    return ring + stage * kQuantTileBytes;
+  }
+  __device__ __forceinline__ uint32_t v_slot(int stage) const {
+    return ring + (2 + stage) * kQuantTileBytes;
+  }
+  __device__ __forceinline__ uint32_t s_slot(int stage) const {
+    return ring + 4 * kQuantTileBytes + stage * L::kScales;
+  }
+
+  __device__ __forceinline__ void look_up() {
+    due_page = -1;
+    const int32_t at = due.tile * kTile + 16 * lane;
+    if (due_left > 0 && lane < kGroups && at < due.tokens) due_page = quant_page(a.pool, due.b, at);
+  }
+
+  // Keys and both scales of the due tile; then its mask is in due_ok.
+  __device__ __forceinline__ void load_keys(int stage) {
+    if (due_left <= 0) {
+      copies_commit();
+      return;
+    }
+    const int32_t head = due.row / a.splits, t0 = due.tile * kTile;
+    const int32_t inside = (1 << a.pool.page_log2) - 1;
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+      const int32_t page = __shfl_sync(~0u, due_page, x);
+      const uint8_t* base = a.pool.codes[0] + page * a.pool.sn[0] + head * a.pool.sh[0] + t * 16;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int32_t tok = t0 + 16 * x + 8 * y + g;
+        const bool ok = page >= 0 && tok < due.tokens;
+        const uint8_t* key = base + (tok & inside) * a.pool.st[0];
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          const bool in = ok && 64 * j + 16 * t < a.pool.dim;
+          copy16(k_slot(stage) + ((x * 2 + y) * kChunks + j) * 512 + lane * 16,
+                 in ? key + 64 * j : a.pool.codes[0], in);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kMasks; ++x) {
+      const int32_t page = __shfl_sync(~0u, due_page, 2 * x + (lane >> 4));
+      const int32_t tok = t0 + 32 * x + lane;
+      const bool ok = page >= 0 && tok < due.tokens;
+      due_ok[x] = __ballot_sync(~0u, ok);
+      const int64_t in = static_cast<int64_t>((tok & inside) >> a.pool.block_log2) *
+                             a.pool.kv_heads + head;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+        copy4(s_slot(stage) + (x * 64 + kv * 32 + lane) * 4,
+              ok ? a.pool.scales[kv] + page * a.pool.ssn[kv] + in : a.pool.scales[kv], ok);
+    }
+    copies_commit();
+  }
+
+  // Its values; then the next tile is due.
+  __device__ __forceinline__ void load_values(int stage) {
+    constexpr int kBytes = DP / 8;
+    if (due_left <= 0) {
+      copies_commit();
+      return;
+    }
+    const int32_t head = due.row / a.splits, t0 = due.tile * kTile;
+    const int32_t inside = (1 << a.pool.page_log2) - 1;
+    const bool some = g * kBytes < a.pool.dim;
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+      const int32_t page = __shfl_sync(~0u, due_page, x);
+      const uint8_t* base =
+          a.pool.codes[1] + page * a.pool.sn[1] + head * a.pool.sh[1] + g * kBytes;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int32_t tok = t0 + 16 * x + 2 * t + (y & 1) + 8 * (y >> 1);
+        const bool in = some && page >= 0 && tok < due.tokens;
+        const uint8_t* value = in ? base + (tok & inside) * a.pool.st[1] : a.pool.codes[1];
+        const uint32_t to = v_slot(stage) + (x * 4 + y) * 32 * kBytes + lane * kBytes;
+        if constexpr (kBytes == 16)
+          copy16(to, value, in);
+        else
+          copy8(to, value, in);
+      }
+    }
+    copies_commit();
+    if (--due_left > 0) advance<kTile>(a, due);
+    look_up();
+  }
+
+  // The queries of a row as the products' right-hand side: column g is a head,
+  // and this lane has the dimensions that it has of a key. Each head is
+  // multiplied by a power of two that brings its largest element to 2^14, which
+  // fp16 then holds exactly to 2^-38 of it.
+  __device__ __forceinline__ void begin(int64_t b, int32_t row) {
+    int32_t first;
+    const int32_t heads = row_heads(a, row, first);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + g;
+      float x[kChunks][16];
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        const int d = 64 * j + 16 * t;
+        uint4 u[2] = {};
+        if (h < heads && d < a.pool.dim) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(a.q) + b * a.q_sb + (first + h) * a.q_sh + d);
+          u[0] = src[0];
+          u[1] = src[1];
+        }
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float2 f;
+          if (a.bf16)
+            f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+          else
+            f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          x[j][2 * i] = f.x;
+          x[j][2 * i + 1] = f.y;
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      // the power's exponent: what brings `top` to [2^14, 2^15), from 2^-126 on
+      // (bf16's smallest number is 2^-133: 2^-7 then)
+      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
+      e = max(e, -126);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[n][4 * j + r][i] =
+                half_pair(x[j][4 * r + 2 * i] * down, x[j][4 * r + 2 * i + 1] * down);
+      q_power[n][0] = __shfl_sync(~0u, up, 8 * t);
+      q_power[n][1] = __shfl_sync(~0u, up, 8 * t + 4);
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        l[n][j] = 0.f;
+        m[n][j] = big[n][j] = -FLT_MAX;
+      }
+    }
+  }
+
+  // One tile. Weights with their values' scales, 2^(x + log2 sv), are kept
+  // relative to a base of their own, as 2^7 at most 2^8 times over: the largest
+  // is then from 2^7 to 2^15 of fp16's range, and what is lost lies 2^-32 below
+  // it. The sums of 2^x have another base. Both move rarely.
+  __device__ __forceinline__ void tile(int stage, const uint32_t (&ok)[kMasks]) {
+    float s[kGroups][NT][4];
+    copies_wait<3>();
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[x][n][j] = 0.f;
+      uint32_t k[2][kChunks][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          const uint4 u =
+              shared16(k_slot(stage) + ((x * 2 + y) * kChunks + j) * 512 + lane * 16);
+          k[y][j][0] = u.x;
+          k[y][j][1] = u.y;
+          k[y][j][2] = u.z;
+          k[y][j][3] = u.w;
+        }
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t a0 = decode2(k[0][j][r]), a2 = decode2(k[0][j][r] >> 16);
+          const uint32_t a1 = decode2(k[1][j][r]), a3 = decode2(k[1][j][r] >> 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            product(s[x][n], a0, a1, a2, a3, qf[n][4 * j + r][0], qf[n][4 * j + r][1]);
+        }
+    }
+    float sk[kMasks], lv[kMasks];
+#pragma unroll
+    for (int x = 0; x < kMasks; ++x) {
+      sk[x] = a.c * shared4(s_slot(stage) + (x * 64 + lane) * 4);
+      lv[x] = log2f(shared4(s_slot(stage) + (x * 64 + 32 + lane) * 4));
+    }
+    load_keys(stage);
+    // scores, and with the values' scales
+    float w[kGroups][NT][4];
+    float top[NT][2], wide[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) top[n][h] = wide[n][h] = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int from = (16 * x + 8 * y + g) & 31;
+        const float fk = __shfl_sync(~0u, sk[x / 2], from);
+        const float fv = __shfl_sync(~0u, lv[x / 2], from);
+        const bool seen = (ok[x / 2] >> from) & 1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float z = seen ? s[x][n][2 * y + h] * (q_power[n][h] * fk) : -INFINITY;
+            s[x][n][2 * y + h] = z;
+            w[x][n][2 * y + h] = z + fv;
+            top[n][h] = fmaxf(top[n][h], z);
+            wide[n][h] = fmaxf(wide[n][h], z + fv);
+          }
+      }
+    bool move = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        move |= top[n][h] > m[n][h] + 64.f || wide[n][h] > big[n][h] + 8.f;
+    if (__any_sync(~0u, move)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float u = top[n][h], v = wide[n][h];
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) {
+            u = fmaxf(u, __shfl_xor_sync(~0u, u, i));
+            v = fmaxf(v, __shfl_xor_sync(~0u, v, i));
+          }
+          u = fmaxf(u, m[n][h]);
+          v = fmaxf(v, big[n][h]);
+          l[n][h] *= power_of_two(m[n][h] - u);
+          const float f = power_of_two(big[n][h] - v);
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) {
+            o[n][i][h] *= f;
+            o[n][i][2 + h] *= f;
+          }
+          m[n][h] = u;
+          big[n][h] = v;
+        }
+    }
+    uint32_t p[kGroups][NT][2];
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float e[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            l[n][h] += power_of_two(s[x][n][2 * y + h] - m[n][h]);
+            e[h] = power_of_two(w[x][n][2 * y + h] - (big[n][h] - 7.f));
+          }
+          p[x][n][y] = transposed(half_pair(e[0], e[1]));
+        }
+      }
+    copies_wait<3>();
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+      constexpr int kWords = DP / 32;  // of a lane's part of a value
+      uint32_t v[4][kWords];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t at = v_slot(stage) + (x * 4 + y) * 4 * DP + lane * (DP / 8);
+        if constexpr (DP == 128) {
+          const uint4 u = shared16(at);
+          v[y][0] = u.x;
+          v[y][1] = u.y;
+          v[y][2] = u.z;
+          v[y][3] = u.w;
+        } else {
+          const uint2 u = shared8(at);
+          v[y][0] = u.x;
+          v[y][1] = u.y;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kWords; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // codes of neighbouring keys side by side, of two dimensions
+          const uint32_t u = __byte_perm(v[0][r], v[1][r], i ? 0x7362 : 0x5140);
+          const uint32_t z = __byte_perm(v[2][r], v[3][r], i ? 0x7362 : 0x5140);
+          const uint32_t a0 = decode2(u), a1 = decode2(u >> 16);
+          const uint32_t a2 = decode2(z), a3 = decode2(z >> 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            product(o[n][2 * r + i], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
+        }
+    }
+    load_values(stage);
+  }
+
+  // The outputs of what this warp has of a row, and its log-sum-exps, in
+  // place: o and m.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float sum = l[n][h];
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(~0u, sum, i);
+        const bool none = sum == 0.f;
+        const float f = none ? 0.f : exp2f(big[n][h] - 7.f - m[n][h]) / sum;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          o[n][i][h] = none ? 0.f : o[n][i][h] * f;
+          o[n][i][2 + h] = none ? 0.f : o[n][i][2 + h] * f;
+        }
+        m[n][h] = none ? -INFINITY : m[n][h] + log2f(sum);
+      }
+  }
+
+  __device__ __forceinline__ void store(int64_t b, int32_t row) {
+    constexpr int kDims = DP / 8;  // of a lane
+    int32_t first;
+    const int32_t heads = row_heads(a, row, first);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int32_t at = 8 * n + 2 * t + h;
+        if (at >= heads) continue;
+        if (g * kDims < a.pool.dim) {
+          uint4* to = reinterpret_cast<uint4*>(out_row(a, b, first + at) + g * kDims);
+#pragma unroll
+          for (int i = 0; i < DP / 64; ++i) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              u[j] = pack_pair(a, o[n][4 * i + j][h], o[n][4 * i + j][2 + h]);
+            to[i] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+        if (g == 0 && a.lse) a.lse[b * a.l_sb + (first + at) * a.l_sh] = m[n][h];
+      }
+  }
+
+  // To a piece [heads][DP] and its log-sum-exps in shared memory.
+  __device__ __forceinline__ void keep(float* piece, float* lse) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int32_t at = 8 * n + 2 * t + h;
+        float2* to = reinterpret_cast<float2*>(piece + at * DP + g * (DP / 8));
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) to[i] = make_float2(o[n][i][h], o[n][i][2 + h]);
+        if (g == 0) lse[at] = m[n][h];
+      }
+  }
+};
+
+// Where share `unit` lies; all lanes of a warp together. sums[i]: tiles in front
+// of chunk i (of `chunk` sequences each) for i up to kQuantThreads.
+template <int TILE>
+__device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int64_t unit,
+                                          const int64_t* sums, int64_t chunk) {
+  const int lane = threadIdx.x & 31;
+  int below = 0;
+  for (int i = lane; i < kQuantThreads; i += 32) below += sums[i] * a.rows <= unit;
+  below = __reduce_add_sync(~0u, below) - 1;  // the last chunk that begins at or before it
+  int64_t before = sums[below];
+  for (int64_t b0 = below * chunk;; b0 += 32) {
+    Spot s;
+    s.b = b0 + lane;
+    s.tiles = 0;
+    if (s.b < a.batch) enter<TILE>(a, s);
+    int64_t upto = s.tiles;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, upto, i);
+      if (lane >= i) upto += y;
+    }
+    const uint32_t past = __ballot_sync(~0u, (before + upto) * a.rows > unit);
+    if (past) {
+      const int who = __ffs(past) - 1;
+      const int64_t rest = unit - (before + upto - s.tiles) * a.rows;
+      s.b = b0 + who;
+      s.tiles = __shfl_sync(~0u, s.tiles, who);
+      const int64_t in = __shfl_sync(~0u, rest, who);
+      s.tokens = quant_length(a, s.b);
+      s.row = static_cast<int32_t>(in / s.tiles);
+      s.tile = static_cast<int32_t>(in - static_cast<int64_t>(s.row) * s.tiles);
+      return s;
+    }
+    before += __shfl_sync(~0u, upto, 31);
+  }
+}
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const QuantAttnArgs a) {
+  using L = QuantLayout<DP, NT>;
+  using Warp = QuantWarp<DP, NT>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ PieceInfo info[kQuantWarps];
+  __shared__ float piece_lse[kQuantWarps][2][L::kHeads];
+  __shared__ int64_t sums[kQuantThreads + 1];
+  __shared__ int64_t part[kQuantWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  // This warp's share: `count` units from `spot` on.
+  Spot spot{};
+  int64_t count, cta_begins, cta_ends;
+  if (a.whole) {
+    spot.b = blockIdx.x / a.rows;
+    spot.row = static_cast<int32_t>(blockIdx.x - spot.b * a.rows);
+    enter<L::kTile>(a, spot);
+    if (spot.tiles == 0) {
+      int32_t first;
+      const int32_t heads = row_heads(a, spot.row, first);
+      for (int i = threadIdx.x; i < heads * a.pool.dim; i += kQuantThreads)
+        out_row(a, spot.b, first + i / a.pool.dim)[i % a.pool.dim] = 0;
+      if (a.lse && threadIdx.x < heads)
+        a.lse[spot.b * a.l_sb + (first + static_cast<int>(threadIdx.x)) * a.l_sh] = -INFINITY;
+      return;
+    }
+    cta_begins = 0;
+    cta_ends = spot.tiles;
+    const int64_t s0 = share_start(spot.tiles, warp, kQuantWarps);
+    count = share_start(spot.tiles, warp + 1, kQuantWarps) - s0;
+    spot.tile = static_cast<int32_t>(s0);
+  } else {
+    const int64_t chunk = (a.batch + kQuantThreads - 1) / kQuantThreads;
+    const int64_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, a.batch);
+    int64_t mine = 0;
+    for (int64_t b = b0; b < b1; ++b) mine += (quant_length(a, b) + L::kTile - 1) / L::kTile;
+    int64_t upto = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, upto, i);
+      if (lane >= i) upto += y;
+    }
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kQuantWarps; ++i) {
+      if (i < warp) before += part[i];
+      total += part[i];
+    }
+    sums[threadIdx.x] = before;
+    if (blockIdx.x == 0) {
+      int64_t at = before;
+      for (int64_t b = b0; b < b1; ++b) {
+        a.starts[b] = static_cast<int32_t>(at);
+        at += (quant_length(a, b) + L::kTile - 1) / L::kTile;
+      }
+      if (threadIdx.x == 0) a.starts[a.batch] = static_cast<int32_t>(total);
+    }
+    __syncthreads();
+    total *= a.rows;
+    const int64_t shares = static_cast<int64_t>(gridDim.x) * kQuantWarps;
+    const int64_t share = static_cast<int64_t>(blockIdx.x) * kQuantWarps + warp;
+    cta_begins = share_start(total, share - warp, shares);
+    cta_ends = share_start(total, share - warp + kQuantWarps, shares);
+    const int64_t u0 = share_start(total, share, shares);
+    count = share_start(total, share + 1, shares) - u0;
+    if (count > 0) spot = find_spot<L::kTile>(a, u0, sums, chunk);
+  }
+
+  Warp w(a, shared_addr(smem) + warp * L::kWarp);
+  float* head_piece = reinterpret_cast<float*>(smem + warp * L::kWarp + L::kRing);
+  float* tail_piece = reinterpret_cast<float*>(smem + warp * L::kWarp);
+  if (lane == 0) {
+    info[warp].has[0] = info[warp].has[1] = info[warp].ends = 0;
+    info[warp].empty = count == 0;
+  }
+  __syncwarp();
+  if (count > 0) {
+    uint32_t ok[2][Warp::kMasks];
+    w.due = spot;
+    w.due_left = count;
+    w.look_up();
+#pragma unroll
+    for (int stage = 0; stage < 2; ++stage) {
+      w.load_keys(stage);
+#pragma unroll
+      for (int i = 0; i < Warp::kMasks; ++i) ok[stage][i] = w.due_ok[i];
+      w.load_values(stage);
+    }
+    bool began = spot.tile == 0;  // the row begins in this share
+    w.begin(spot.b, spot.row);
+    int stage = 0;
+    for (int64_t i = 0; i < count; ++i) {
+      w.tile(stage, ok[0]);
+#pragma unroll
+      for (int j = 0; j < Warp::kMasks; ++j) {
+        ok[0][j] = ok[1][j];
+        ok[1][j] = w.due_ok[j];
+      }
+      stage ^= 1;
+      const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
+      if (ends || last) {
+        w.finish();
+        if (began && ends) {
+          w.store(spot.b, spot.row);
+        } else {
+          const int tail = began ? 1 : 0;
+          __syncwarp();  // the ring has been read
+          w.keep(tail ? tail_piece : head_piece, piece_lse[warp][tail]);
+          if (lane == 0) {
+            info[warp].b[tail] = spot.b;
+            info[warp].row[tail] = spot.row;
+            info[warp].has[tail] = 1;
+            if (!tail) info[warp].ends = ends;
+          }
+        }
+        if (!last) {
+          advance<L::kTile>(a, spot);
+          w.begin(spot.b, spot.row);
+          began = true;
+        }
+      } else {
+        ++spot.tile;
+      }
+    }
+    copies_wait<0>();
+  }
+  __syncthreads();
+
+  // Chains of pieces of one row: a tail piece and the head pieces behind it, or
+  // those at the CTA's begin, whose row began in another CTA.
+  for (int from = -1; from < kQuantWarps; ++from) {
+    int at = from;
+    if (from < 0) {
+      at = 0;
+      while (at < kQuantWarps && info[at].empty) ++at;
+      if (at == kQuantWarps) break;
+      if (!info[at].has[0]) continue;
+    } else if (!info[from].has[1]) {
+      continue;
+    }
+    const int kind = from < 0 ? 0 : 1;
+    const int64_t b = info[at].b[kind];
+    const int32_t row = info[at].row[kind];
+    // the warps whose head pieces follow, and whether the row ends with them
+    bool ends = kind == 0 && info[at].ends;
+    int to = at + 1;
+    while (!ends && to < kQuantWarps) {
+      if (!info[to].empty) ends = info[to].ends != 0;
+      ++to;
+    }
+    const auto piece = [&](int i) {
+      return reinterpret_cast<const float*>(smem + i * L::kWarp + (i == from ? 0 : L::kRing));
+    };
+    int32_t first;
+    const int32_t heads = row_heads(a, row, first);
+    const bool done = kind == 1 && ends;
+    const int64_t slot = 2ll * blockIdx.x + kind;
+    for (int e = threadIdx.x; e < heads * (DP / 2); e += kQuantThreads) {
+      const int h = e / (DP / 2), d = e % (DP / 2) * 2;
+      float top = -INFINITY;
+      for (int i = at; i < to; ++i)
+        if (!info[i].empty) top = fmaxf(top, piece_lse[i][i == from][h]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float2 x = make_float2(0.f, 0.f);
+      for (int i = at; i < to; ++i) {
+        if (info[i].empty) continue;
+        const float f = power_of_two(piece_lse[i][i == from][h] - base);
+        const float2 y = *reinterpret_cast<const float2*>(piece(i) + h * DP + d);
+        sum += f;
+        x.x += f * y.x;
+        x.y += f * y.y;
+      }
+      const float f = sum == 0.f ? 0.f : 1.f / sum, z = base + log2f(sum);
+      x.x = sum == 0.f ? 0.f : x.x * f;
+      x.y = sum == 0.f ? 0.f : x.y * f;
+      if (done) {
+        if (d < a.pool.dim)
+          *reinterpret_cast<uint32_t*>(out_row(a, b, first + h) + d) = pack_pair(a, x.x, x.y);
+        if (d == 0 && a.lse) a.lse[b * a.l_sb + (first + h) * a.l_sh] = z;
+      } else {
+        *reinterpret_cast<float2*>(a.part_o + (slot * L::kHeads + h) * DP + d) = x;
+        if (d == 0) a.part_lse[slot * L::kHeads + h] = z;
+      }
+    }
+  }
+}
+
+constexpr int kQuantJoinWarps = 4;
+constexpr int kQuantJoinThreads = 32 * kQuantJoinWarps;
+
+// A CTA for each query head: joins what the CTAs of the first launch left of
+// rows that lie in several of them, and writes those without tiles.
+template <int DP, int NT>
+__global__ void __launch_bounds__(kQuantJoinThreads)
+    quant_join_kernel(const QuantAttnArgs a, int32_t ctas) {
+  constexpr int kHeads = 8 * NT, kDims = DP / 32;
+  __shared__ float shared_o[kQuantJoinWarps][DP];
+  __shared__ float shared_top[kQuantJoinWarps], shared_sum[kQuantJoinWarps];
+  follow();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t all = static_cast<int64_t>(a.pool.kv_heads) * a.group;
+  const int64_t b = blockIdx.x / all;
+  const int32_t head = static_cast<int32_t>(blockIdx.x - b * all);
+  const int32_t kv = head / a.group, in = head - kv * a.group;
+  const int32_t row = kv * a.splits + in / a.split_heads, h = in % a.split_heads;
+  const int64_t start = a.starts[b], tiles = a.starts[b + 1] - start;
+  const int64_t total = static_cast<int64_t>(a.starts[a.batch]) * a.rows;
+  const int64_t u0 = start * a.rows + row * tiles, u1 = u0 + tiles - 1;
+  // the CTA that holds a unit: share_start(total, c, ctas) <= u
+  const auto holder = [&](int64_t u) {
+    int64_t c = u * ctas / total;
+    while (share_start(total, c + 1, ctas) <= u) ++c;
+    while (share_start(total, c, ctas) > u) --c;
+    return c;
+  };
+  int64_t c0 = 0, c1 = -1;
+  if (tiles > 0) {
+    c0 = holder(u0);
+    c1 = holder(u1);
+    if (c0 == c1) return;
+  }
+  // slot 1 of the first CTA, slot 0 of the others
+  const auto slot = [&](int64_t c) { return (2 * c + (c == c0)) * kHeads + h; };
+  const auto has = [&](int64_t c) {
+    return share_start(total, c, ctas) < share_start(total, c + 1, ctas);
+  };
+  float top = -INFINITY;
+  for (int64_t c = c0 + threadIdx.x; c <= c1; c += kQuantJoinThreads)
+    if (has(c)) top = fmaxf(top, a.part_lse[slot(c)]);
+#pragma unroll
+  for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+  if (lane == 0) shared_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuantJoinWarps; ++i) top = fmaxf(top, shared_top[i]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, x[kDims] = {};
+#pragma unroll 4
+  for (int64_t c = c0 + warp; c <= c1; c += kQuantJoinWarps) {
+    if (!has(c)) continue;
+    const float f = power_of_two(a.part_lse[slot(c)] - base);
+    const float* y = a.part_o + slot(c) * DP + lane * kDims;
+    sum += f;
+    if constexpr (kDims == 4) {
+      const float4 z = *reinterpret_cast<const float4*>(y);
+      x[0] += f * z.x;
+      x[1] += f * z.y;
+      x[2] += f * z.z;
+      x[3] += f * z.w;
+    } else {
+      const float2 z = *reinterpret_cast<const float2*>(y);
+      x[0] += f * z.x;
+      x[1] += f * z.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kDims; ++i) shared_o[warp][lane * kDims + i] = x[i];
+  if (lane == 0) shared_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kQuantJoinWarps; ++i) sum += shared_sum[i];
+  const int d = 2 * threadIdx.x;
+  if (d < a.pool.dim) {
+    float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kQuantJoinWarps; ++i) {
+      z.x += shared_o[i][d];
+      z.y += shared_o[i][d + 1];
+    }
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint32_t*>(out_row(a, b, head) + d) =
+        sum == 0.f ? 0u : pack_pair(a, z.x * f, z.y * f);
+  }
+  if (threadIdx.x == 0 && a.lse) a.lse[b * a.l_sb + head * a.l_sh] = base + log2f(sum);
+}
+
+}  // namespace dsa

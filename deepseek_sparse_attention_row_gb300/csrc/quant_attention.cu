@@ -2,90 +2,101 @@
 // dsa_quant_attention of include/dsa_quant.h.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
-#include "quant.cuh"
+#include "quant_attend.cuh"
 
 namespace dsa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct AttnArgs {
-  QuantPool pool;
-  const void* q;
-  int64_t q_sb, q_sh;
-  int32_t heads, group;
-  const int32_t* lens;
-  float c;  // scale * log2 e
-  void* out;
-  int64_t o_sb, o_sh;
-  float* lse;
-  int64_t l_sb, l_sh;
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? dev : -1;
+}
+
+// Streaming multiprocessors of the current device, cached per device.
+int sm_count() {
+  static std::atomic<int> cached[64];
+  const int dev = current_device();
+  if (dev < 0) return 152;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      return 152;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// How a call's work is cut, and where its partial outputs lie in the workspace
+// (each part 256-byte aligned).
+struct QuantPlan {
+  int32_t dp, columns, splits, split_heads;
+  bool whole;
+  int64_t grid;
+  bool fits;
+  size_t starts, part_o, part_lse, bytes;
 };
 
-constexpr int kWarps = 4;
+constexpr int64_t kMaxUnits = 1000000000;
+// Tiles of a row that a CTA of its own still takes.
+constexpr int64_t kWholeTiles = 2 * kQuantWarps;
 
-// A CTA for each sequence and head; its warps take every fourth token.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const AttnArgs a) {
-  __shared__ float part[kWarps][130];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.x / a.heads;
-  const int h = blockIdx.x % a.heads, head = h / a.group, d = lane * 4;
-  const bool mine = d < a.pool.dim;
-  float q[4] = {}, o[4] = {};
-  if (mine) {
-    const T* row = static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh + d;
-    for (int i = 0; i < 4; ++i) q[i] = static_cast<float>(row[i]);
+QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                         int64_t max_pages, int32_t page_size) {
+  QuantPlan p{};
+  const int32_t group = heads / kv_heads;
+  p.dp = head_dim > 64 ? 128 : 64;
+  p.splits = (group + 15) / 16;
+  p.split_heads = (group + p.splits - 1) / p.splits;
+  p.columns = p.split_heads > 8 ? 2 : 1;
+  const int64_t tile = kQuantTileBytes / p.dp;
+  const int64_t tiles = (max_pages * page_size + tile - 1) / tile;
+  const int64_t rows = batch * kv_heads * p.splits, units = rows * tiles;
+  p.fits = batch * kv_heads * ((max_pages * page_size + 31) / 32) <= kMaxUnits;
+  const int64_t sms = sm_count();
+  p.whole = rows <= sms && tiles <= kWholeTiles;
+  if (p.whole) {
+    p.grid = rows;
+    return p;
   }
-  int64_t n = a.lens[b];
-  const int64_t most = a.pool.max_pages << a.pool.page_log2;
-  n = n < 0 ? 0 : (n < most ? n : most);
-  float m = -INFINITY, l = 0.f;
-  for (int32_t t = warp; t < n; t += kWarps) {
-    const int32_t page = quant_page(a.pool, b, t);
-    if (page < 0) continue;
-    uint32_t kc = 0, vc = 0;
-    if (mine) {
-      kc = *reinterpret_cast<const uint32_t*>(quant_code(a.pool, 0, page, t, head) + d);
-      vc = *reinterpret_cast<const uint32_t*>(quant_code(a.pool, 1, page, t, head) + d);
-    }
-    const float2 k0 = decode2f(kc & 0xffff), k1 = decode2f(kc >> 16);
-    float x = q[0] * k0.x + q[1] * k0.y + q[2] * k1.x + q[3] * k1.y;
-    for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(~0u, x, i);
-    x *= a.c * *quant_scale(a.pool, 0, page, t, head);
-    const float top = x > m ? x : m, base = top == -INFINITY ? 0.f : top;
-    const float keep = exp2f(m - base), p = exp2f(x - base);
-    const float pv = p * *quant_scale(a.pool, 1, page, t, head);
-    const float2 v0 = decode2f(vc & 0xffff), v1 = decode2f(vc >> 16);
-    l = l * keep + p;
-    o[0] = o[0] * keep + pv * v0.x;
-    o[1] = o[1] * keep + pv * v0.y;
-    o[2] = o[2] * keep + pv * v1.x;
-    o[3] = o[3] * keep + pv * v1.y;
-    m = top;
+  const int64_t most = (units + kQuantWarps - 1) / kQuantWarps;
+  p.grid = most < 1 ? 1 : (most < sms ? most : sms);
+  const size_t slots = 2 * static_cast<size_t>(p.grid) * 8 * p.columns;
+  p.starts = 0;
+  p.part_o = up256((batch + 1) * 4);
+  p.part_lse = p.part_o + up256(slots * p.dp * 4);
+  p.bytes = p.part_lse + up256(slots * 4);
+  return p;
+}
+
+template <int DP, int NT>
+dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t stream) {
+  constexpr int kSmem = QuantLayout<DP, NT>::kSmem;
+  static_assert(kSmem + 8192 <= 232448, "shared memory of one SM");
+  static std::atomic<bool> ready[64];  // per device
+  const int dev = current_device();
+  if (dev < 0) return DSA_ECUDA;
+  auto* kernel = quant_attend_kernel<DP, NT>;
+  if (!ready[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+        cudaSuccess)
+      return DSA_ECUDA;
+    ready[dev].store(true, std::memory_order_relaxed);
   }
-  for (int i = 0; i < 4; ++i)
-    if (mine) part[warp][d + i] = o[i];
-  if (lane == 0) {
-    part[warp][128] = m;
-    part[warp][129] = l;
-  }
-  __syncthreads();
-  float top = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][128]);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, out = 0.f;
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = exp2f(part[w][128] - base);
-    sum += f * part[w][129];
-    if (threadIdx.x < a.pool.dim) out += f * part[w][threadIdx.x];
-  }
-  if (threadIdx.x < a.pool.dim)
-    static_cast<T*>(a.out)[b * a.o_sb + h * a.o_sh + threadIdx.x] =
-        static_cast<T>(sum == 0.f ? 0.f : out / sum);
-  if (threadIdx.x == 0 && a.lse) a.lse[b * a.l_sb + h * a.l_sh] = base + log2f(sum);
+  kernel<<<static_cast<unsigned>(p.grid), kQuantThreads, kSmem, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
+  if (p.whole) return DSA_OK;
+  const int64_t ctas = a.batch * a.pool.kv_heads * a.group;
+  return launch_after(quant_join_kernel<DP, NT>, dim3(static_cast<unsigned>(ctas)),
+                      kQuantJoinThreads, stream, a, static_cast<int32_t>(p.grid))
+             ? DSA_OK
+             : DSA_ECUDA;
 }
 
 constexpr int64_t kMaxRows = 1000000000;
@@ -103,7 +114,14 @@ dsa_status check_sizes(int64_t batch, int32_t heads, int32_t kv_heads) {
 extern "C" size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t heads,
                                                       int32_t kv_heads, int32_t head_dim,
                                                       int64_t max_pages, int32_t page_size) {
-  return 0;
+  if (dsa::check_sizes(batch, heads, kv_heads) != DSA_OK || batch == 0 || heads == 0 ||
+      head_dim < 1 || head_dim > 128 || head_dim % 16 != 0 || max_pages < 0 ||
+      max_pages > INT32_MAX || page_size < 16 || (page_size & (page_size - 1)) != 0 ||
+      max_pages * page_size > INT32_MAX)
+    return 0;
+  const dsa::QuantPlan p =
+      dsa::plan_attention(batch, heads, kv_heads, head_dim, max_pages, page_size);
+  return p.fits ? p.bytes : 0;
 }
 
 extern "C" dsa_status dsa_quant_attention(
@@ -117,7 +135,7 @@ extern "C" dsa_status dsa_quant_attention(
   if (dtype != DSA_DTYPE_F32 && dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_F16)
     return DSA_EINVAL;
   if (!(scale > 0.f) || !std::isfinite(scale * dsa::kLog2e)) return DSA_EINVAL;
-  dsa::AttnArgs a{};
+  dsa::QuantAttnArgs a{};
   dsa_status st = dsa::quant_pool(a.pool, k_codes, v_codes, k_scales, v_scales, num_pages,
                                   page_size, block, kv_heads, head_dim,
                                   {kc_sn, kc_st, kc_sh, vc_sn, vc_st, vc_sh}, ks_sn, vs_sn, tables,
@@ -131,12 +149,21 @@ extern "C" dsa_status dsa_quant_attention(
   if (!dsa::quant_aligned16(q) || !dsa::quant_aligned16(out)) return DSA_EUNSUPPORTED;
   for (int64_t s : {q_sb, q_sh, o_sb, o_sh})
     if (s < 0 || s % 8 != 0) return DSA_EUNSUPPORTED;
-  if (num_pages == 0) a.pool.max_pages = 0;
+  const dsa::QuantPlan p =
+      dsa::plan_attention(batch, heads, kv_heads, head_dim, max_pages, page_size);
+  if (!p.fits) return DSA_EUNSUPPORTED;
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes ||
+                      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return DSA_EINVAL;
+  if (num_pages == 0) a.pool.max_pages = 0;  // nothing is seen
   a.q = q;
   a.q_sb = q_sb;
   a.q_sh = q_sh;
-  a.heads = heads;
+  a.batch = batch;
   a.group = heads / kv_heads;
+  a.splits = p.splits;
+  a.split_heads = p.split_heads;
+  a.rows = kv_heads * p.splits;
   a.lens = lens;
   a.c = scale * dsa::kLog2e;
   a.out = out;
@@ -145,11 +172,14 @@ extern "C" dsa_status dsa_quant_attention(
   a.lse = lse;
   a.l_sb = l_sb;
   a.l_sh = l_sh;
-  const unsigned grid = static_cast<unsigned>(batch * heads);
+  a.bf16 = dtype == DSA_DTYPE_BF16;
+  a.whole = p.whole;
+  char* ws = static_cast<char*>(workspace);
+  a.starts = reinterpret_cast<int32_t*>(ws + p.starts);
+  a.part_o = reinterpret_cast<float*>(ws + p.part_o);
+  a.part_lse = reinterpret_cast<float*>(ws + p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == DSA_DTYPE_BF16)
-    dsa::attention_kernel<__nv_bfloat16><<<grid, dsa::kWarps * 32, 0, s>>>(a);
-  else
-    dsa::attention_kernel<__half><<<grid, dsa::kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
+  if (p.dp == 128)
+    return p.columns == 1 ? dsa::launch<128, 1>(a, p, s) : dsa::launch<128, 2>(a, p, s);
+  return p.columns == 1 ? dsa::launch<64, 1>(a, p, s) : dsa::launch<64, 2>(a, p, s);
 }
