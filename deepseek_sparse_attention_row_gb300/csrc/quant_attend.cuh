@@ -6,11 +6,11 @@
 // instruction is padding:
 //   S^T [keys x heads] = K [keys x dim] Q^T,   O^T [dim x heads] += V^T P^T.
 // A warp works alone: it goes through a line of 4 KiB tiles of keys (32 of up to
-// 128 dimensions, 64 of up to 64) with its codes on their way by cp.async into
-// shared memory that only the lane that asked for them reads, so that no
+// 128 dimensions, 64 of up to 64), and as many of values, that cp.async brings
+// into a ring of three of its own in shared memory, whole rows at a time; no
 // barrier stands between a load and its use. Codes become fp16 in registers,
-// which is exact; so are queries after a power of two that brings the largest
-// of a row to 2^14.
+// which is exact; so are queries after a power of two that brings the largest of
+// a row to 2^14.
 //
 // Each (sequence, key/value head) is a row of tiles; the rows lie on one line
 // that is cut into equal shares, one for each warp of the GPU. Rows that lie
@@ -25,11 +25,10 @@
 
 #include "follow.cuh"
 #include "quant.cuh"
+#include "umma.cuh"
 
 namespace dsa {
 
-constexpr int kQuantWarps = 8;
-constexpr int kQuantThreads = 32 * kQuantWarps;
 constexpr int kQuantTileBytes = 4096;
 
 struct QuantAttnArgs {
@@ -56,33 +55,21 @@ template <int DP, int NT>
 struct QuantLayout {
   static constexpr int kTile = kQuantTileBytes / DP;  // keys
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kScales = kTile * 8;  // bytes of a tile's two scales
-  static constexpr int kRing = 4 * kQuantTileBytes + 2 * kScales;
-  static constexpr int kPiece = kHeads * DP * 4;
-  static constexpr int kWarp = kRing + kPiece;
-  static constexpr int kSmem = kQuantWarps * kWarp;
-  static_assert(kPiece <= kRing, "a tail piece lies over the ring");
+  // As many as the registers let be: 16 columns take 230 of a thread.
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRing = 3 * kQuantTileBytes;
+  static constexpr int kPiece = kHeads * DP;  // floats
+  static constexpr int kWarp = kRing + kPiece * 4;
+  static constexpr int kSmem = kWarps * kWarp;
+  static_assert(kPiece * 4 <= kRing, "a tail piece lies over the ring");
 };
 
 // ---- instructions ----------------------------------------------------------
 
-__device__ __forceinline__ uint32_t shared_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 or 8 bytes, zeros where `yes` is false (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool yes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(yes ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool yes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-               "r"(yes ? 8 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool yes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(yes ? 4 : 0)
+// 16 bytes, zeros where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
@@ -92,23 +79,21 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 shared16(uint32_t a) {
-  uint4 v;
+__device__ __forceinline__ void shared_words(uint32_t (&x)[4], uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(at)
                : "memory");
-  return v;
 }
-__device__ __forceinline__ uint2 shared8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void shared_words(uint32_t (&x)[2], uint32_t at) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ float shared4(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+// Four codes as two pairs of fp16.
+__device__ __forceinline__ void decode4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 // [16 x 16] by [16 x 8] of fp16, added in fp32.
 __device__ __forceinline__ void product(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -125,14 +110,12 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float power_of_two(float x) {  // 2^x, within 2^-22
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  return fma2(a, b, make_float2(-0.f, -0.f));
 }
 
 // ---- the line of tiles -----------------------------------------------------
@@ -209,35 +192,66 @@ struct QuantWarp {
   static constexpr int kTile = L::kTile;
   static constexpr int kGroups = kTile / 16;  // of 16 keys
   static constexpr int kChunks = DP / 64;     // 16-byte chunks of a key in a lane
+  static constexpr int kWords = DP / 32;      // 4-byte words of a value in a lane
   static constexpr int kSteps = DP / 16;      // of 16 dimensions
   static constexpr int kMasks = kTile / 32;
+  static constexpr int kRowLanes = DP / 16;          // lanes that load a row
+  static constexpr int kRows = 32 / kRowLanes;       // rows of one copy
+  static constexpr int kCopies = 16 / kRows;         // of 16 keys
+
+  // A tile whose loads are due or under way.
+  struct Tile {
+    int32_t page;       // of its groups (lane i: group i); -1: none
+    int32_t inside;     // its first token's place on its page
+    int32_t head;
+    uint32_t seen[kMasks];
+    float sk[kMasks], sv[kMasks];  // scales, of key 32 x + lane
+  };
 
   const QuantAttnArgs& a;
   const int lane, g, t;
-  const uint32_t ring;  // this warp's shared memory
+  const uint32_t ring;        // this warp's shared memory
+  uint32_t fill, read;        // slots of the next tile to load and to use
 
-  // loads: the tile that is due next, and the pages of its groups (lane i: group i)
-  Spot due;
-  int32_t due_page;
+  const int copy_row;   // what this lane copies: rows from this one on,
+  const int copy_byte;  // and 16 bytes of each
+
+  Spot due;          // the tile whose keys are loaded next
+  int32_t due_page;  // and the pages of its groups
   int64_t due_left;  // tiles from it to the share's end
-  uint32_t due_ok[kMasks];
+  Tile now, next;
 
   uint32_t qf[NT][kSteps][2];
-  float q_power[NT][2];  // of the columns' heads
+  float2 q_power[NT];  // of the columns' heads
   float o[NT][DP / 16][4];
-  float l[NT][2], m[NT][2], big[NT][2];  // sums; bases of the sums and of the weights
+  float2 l[NT], m[NT], big[NT];  // sums; bases of the sums and of the weights
+
+  // Rows of 128 bytes (two of 64) are swizzled by 16-byte chunks: the eight
+  // lanes that read together (two keys of four chunks, or four pairs of a row's
+  // chunks two rows apart) find theirs on different banks.
+  static __device__ __forceinline__ uint32_t key_at(int row, int chunk) {
+    if constexpr (DP == 128) return row * 128 + ((chunk ^ ((row & 1) << 2)) << 4);
+    return row * 64 + (chunk << 4);
+  }
+  static __device__ __forceinline__ uint32_t value_at(int row, int chunk) {
+    if constexpr (DP == 128) return row * 128 + ((chunk ^ (row & 6)) << 4);
+    return (row >> 1) * 128 + (((((row & 1) << 2) | chunk) ^ (row & 6)) << 4);
+  }
 
   __device__ __forceinline__ QuantWarp(const QuantAttnArgs& args, uint32_t smem)
-      : a(args), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3), ring(smem) {}
+      : a(args),
+        lane(threadIdx.x & 31),
+        g(lane >> 2),
+        t(lane & 3),
+        ring(smem),
+        fill(smem),
+        read(smem),
+        copy_row(lane / kRowLanes),
+        copy_byte(lane % kRowLanes * 16) {}
 
-  __device__ __forceinline__ uint32_t k_slot(int stage) const {
-    return ring + stage * kQuantTileBytes;
-  }
-  __device__ __forceinline__ uint32_t v_slot(int stage) const {
-    return ring + (2 + stage) * kQuantTileBytes;
-  }
-  __device__ __forceinline__ uint32_t s_slot(int stage) const {
-    return ring + 4 * kQuantTileBytes + stage * L::kScales;
+  __device__ __forceinline__ void step(uint32_t& slot) {
+    slot += kQuantTileBytes;
+    if (slot == ring + 3 * kQuantTileBytes) slot = ring;
   }
 
   __device__ __forceinline__ void look_up() {
@@ -246,77 +260,67 @@ struct QuantWarp {
     if (due_left > 0 && lane < kGroups && at < due.tokens) due_page = quant_page(a.pool, due.b, at);
   }
 
-  // Keys and both scales of the due tile; then its mask is in due_ok.
-  __device__ __forceinline__ void load_keys(int stage) {
-    if (due_left <= 0) {
-      copies_commit();
-      return;
-    }
-    const int32_t head = due.row / a.splits, t0 = due.tile * kTile;
-    const int32_t inside = (1 << a.pool.page_log2) - 1;
+  // Rows of keys (kv 0) or values of `x` into the next slot.
+  __device__ __forceinline__ void load(int kv, const Tile& x) {
+    const uint8_t* row = a.pool.codes[kv] + x.head * a.pool.sh[kv] +
+                         copy_row * a.pool.st[kv] + copy_byte;
+    const int32_t mask = (1 << a.pool.page_log2) - 1;
+    const uint32_t bytes = copy_byte < a.pool.dim ? 16 : 0;
+    bool full = true;
 #pragma unroll
-    for (int x = 0; x < kGroups; ++x) {
-      const int32_t page = __shfl_sync(~0u, due_page, x);
-      const uint8_t* base = a.pool.codes[0] + page * a.pool.sn[0] + head * a.pool.sh[0] + t * 16;
+    for (int i = 0; i < kMasks; ++i) full &= x.seen[i] == ~0u;
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int32_t tok = t0 + 16 * x + 8 * y + g;
-        const bool ok = page >= 0 && tok < due.tokens;
-        const uint8_t* key = base + (tok & inside) * a.pool.st[0];
+    for (int i = 0; i < kGroups; ++i) {
+      const int32_t page = __shfl_sync(~0u, x.page, i);
+      const uint8_t* p =
+          row + page * a.pool.sn[kv] + ((x.inside + 16 * i) & mask) * a.pool.st[kv];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-          const bool in = ok && 64 * j + 16 * t < a.pool.dim;
-          copy16(k_slot(stage) + ((x * 2 + y) * kChunks + j) * 512 + lane * 16,
-                 in ? key + 64 * j : a.pool.codes[0], in);
-        }
+      for (int j = 0; j < kCopies; ++j) {
+        const int at = 16 * i + j * kRows;
+        uint32_t n = bytes;
+        if (!full && !(x.seen[i / 2] >> ((at + copy_row) & 31) & 1)) n = 0;
+        const uint32_t to =
+            fill + (kv ? value_at(at + copy_row, copy_byte >> 4) : key_at(at + copy_row, copy_byte >> 4));
+        copy16(to, n ? p : a.pool.codes[kv], n);
+        p += kRows * a.pool.st[kv];
       }
     }
+    step(fill);
+  }
+
+  // Keys and scales of the due tile, which becomes `next`; the one behind it is
+  // due then.
+  __device__ __forceinline__ void load_keys() {
+    if (due_left > 0) {
+      const int32_t t0 = due.tile * kTile, mask = (1 << a.pool.page_log2) - 1;
+      next.page = due_page;
+      next.inside = t0 & mask;
+      next.head = due.row / a.splits;
 #pragma unroll
-    for (int x = 0; x < kMasks; ++x) {
-      const int32_t page = __shfl_sync(~0u, due_page, 2 * x + (lane >> 4));
-      const int32_t tok = t0 + 32 * x + lane;
-      const bool ok = page >= 0 && tok < due.tokens;
-      due_ok[x] = __ballot_sync(~0u, ok);
-      const int64_t in = static_cast<int64_t>((tok & inside) >> a.pool.block_log2) *
-                             a.pool.kv_heads + head;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
-        copy4(s_slot(stage) + (x * 64 + kv * 32 + lane) * 4,
-              ok ? a.pool.scales[kv] + page * a.pool.ssn[kv] + in : a.pool.scales[kv], ok);
+      for (int x = 0; x < kMasks; ++x) {
+        const int32_t page = __shfl_sync(~0u, due_page, 2 * x + (lane >> 4));
+        const int32_t tok = t0 + 32 * x + lane;
+        const bool ok = page >= 0 && tok < due.tokens;
+        next.seen[x] = __ballot_sync(~0u, ok);
+        next.sk[x] = next.sv[x] = 0.f;
+        if (ok) {
+          const int64_t in = static_cast<int64_t>((tok & mask) >> a.pool.block_log2) *
+                                 a.pool.kv_heads + next.head;
+          next.sk[x] = a.pool.scales[0][page * a.pool.ssn[0] + in];
+          next.sv[x] = a.pool.scales[1][page * a.pool.ssn[1] + in];
+        }
+      }
+      load(0, next);
+      if (--due_left > 0) advance<kTile>(a, due);
+      look_up();
+    } else {
+      next.page = -2;  // no tile
     }
     copies_commit();
   }
-
-  // Its values; then the next tile is due.
-  __device__ __forceinline__ void load_values(int stage) {
-    constexpr int kBytes = DP / 8;
-    if (due_left <= 0) {
-      copies_commit();
-      return;
-    }
-    const int32_t head = due.row / a.splits, t0 = due.tile * kTile;
-    const int32_t inside = (1 << a.pool.page_log2) - 1;
-    const bool some = g * kBytes < a.pool.dim;
-#pragma unroll
-    for (int x = 0; x < kGroups; ++x) {
-      const int32_t page = __shfl_sync(~0u, due_page, x);
-      const uint8_t* base =
-          a.pool.codes[1] + page * a.pool.sn[1] + head * a.pool.sh[1] + g * kBytes;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int32_t tok = t0 + 16 * x + 2 * t + (y & 1) + 8 * (y >> 1);
-        const bool in = some && page >= 0 && tok < due.tokens;
-        const uint8_t* value = in ? base + (tok & inside) * a.pool.st[1] : a.pool.codes[1];
-        const uint32_t to = v_slot(stage) + (x * 4 + y) * 32 * kBytes + lane * kBytes;
-        if constexpr (kBytes == 16)
-          copy16(to, value, in);
-        else
-          copy8(to, value, in);
-      }
-    }
+  __device__ __forceinline__ void load_values() {
+    if (next.page != -2) load(1, next);
     copies_commit();
-    if (--due_left > 0) advance<kTile>(a, due);
-    look_up();
   }
 
   // The queries of a row as the products' right-hand side: column g is a head,
@@ -370,17 +374,14 @@ struct QuantWarp {
           for (int i = 0; i < 2; ++i)
             qf[n][4 * j + r][i] =
                 half_pair(x[j][4 * r + 2 * i] * down, x[j][4 * r + 2 * i + 1] * down);
-      q_power[n][0] = __shfl_sync(~0u, up, 8 * t);
-      q_power[n][1] = __shfl_sync(~0u, up, 8 * t + 4);
+      q_power[n].x = __shfl_sync(~0u, up, 8 * t);
+      q_power[n].y = __shfl_sync(~0u, up, 8 * t + 4);
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        l[n][j] = 0.f;
-        m[n][j] = big[n][j] = -FLT_MAX;
-      }
+      l[n] = make_float2(0.f, 0.f);
+      m[n] = big[n] = make_float2(-FLT_MAX, -FLT_MAX);
     }
   }
 
@@ -388,152 +389,144 @@ struct QuantWarp {
   // relative to a base of their own, as 2^7 at most 2^8 times over: the largest
   // is then from 2^7 to 2^15 of fp16's range, and what is lost lies 2^-32 below
   // it. The sums of 2^x have another base. Both move rarely.
-  __device__ __forceinline__ void tile(int stage, const uint32_t (&ok)[kMasks]) {
+  __device__ __forceinline__ void tile() {
+    copies_wait<2>();
+    __syncwarp();
     float s[kGroups][NT][4];
-    copies_wait<3>();
 #pragma unroll
-    for (int x = 0; x < kGroups; ++x) {
+    for (int x = 0; x < kGroups; ++x)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[x][n][j] = 0.f;
-      uint32_t k[2][kChunks][4];
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+    for (int j = 0; j < kChunks; ++j) {
+      uint32_t k[kGroups][2][4];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-          const uint4 u =
-              shared16(k_slot(stage) + ((x * 2 + y) * kChunks + j) * 512 + lane * 16);
-          k[y][j][0] = u.x;
-          k[y][j][1] = u.y;
-          k[y][j][2] = u.z;
-          k[y][j][3] = u.w;
-        }
+      for (int x = 0; x < kGroups; ++x)
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j)
+        for (int y = 0; y < 2; ++y)
+          shared_words(k[x][y], read + key_at(16 * x + 8 * y + g, 4 * j + t));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t a0 = decode2(k[0][j][r]), a2 = decode2(k[0][j][r] >> 16);
-          const uint32_t a1 = decode2(k[1][j][r]), a3 = decode2(k[1][j][r] >> 16);
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int x = 0; x < kGroups; ++x) {
+          uint32_t a0, a1, a2, a3;
+          decode4(k[x][0][r], a0, a2);
+          decode4(k[x][1][r], a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             product(s[x][n], a0, a1, a2, a3, qf[n][4 * j + r][0], qf[n][4 * j + r][1]);
         }
     }
-    float sk[kMasks], lv[kMasks];
+    step(read);
+    __syncwarp();  // the slot has been read
+    load_values();
+    float ck[kMasks], lv[kMasks];
+    bool full = true;
 #pragma unroll
     for (int x = 0; x < kMasks; ++x) {
-      sk[x] = a.c * shared4(s_slot(stage) + (x * 64 + lane) * 4);
-      lv[x] = log2f(shared4(s_slot(stage) + (x * 64 + 32 + lane) * 4));
+      ck[x] = a.c * now.sk[x];
+      lv[x] = log2f(now.sv[x]);
+      full &= now.seen[x] == ~0u;
     }
-    load_keys(stage);
     // scores, and with the values' scales
-    float w[kGroups][NT][4];
-    float top[NT][2], wide[NT][2];
+    float2 w[kGroups][2][NT];
+    float2 top[NT], wide[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) top[n][h] = wide[n][h] = -INFINITY;
+    for (int n = 0; n < NT; ++n) top[n] = wide[n] = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
     for (int x = 0; x < kGroups; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int from = (16 * x + 8 * y + g) & 31;
-        const float fk = __shfl_sync(~0u, sk[x / 2], from);
+        const float fk = __shfl_sync(~0u, ck[x / 2], from);
         const float fv = __shfl_sync(~0u, lv[x / 2], from);
-        const bool seen = (ok[x / 2] >> from) & 1;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float z = seen ? s[x][n][2 * y + h] * (q_power[n][h] * fk) : -INFINITY;
-            s[x][n][2 * y + h] = z;
-            w[x][n][2 * y + h] = z + fv;
-            top[n][h] = fmaxf(top[n][h], z);
-            wide[n][h] = fmaxf(wide[n][h], z + fv);
-          }
+        for (int n = 0; n < NT; ++n) {
+          float2 z = mul2(make_float2(s[x][n][2 * y], s[x][n][2 * y + 1]),
+                          mul2(q_power[n], make_float2(fk, fk)));
+          if (!full && !(now.seen[x / 2] >> from & 1)) z = make_float2(-INFINITY, -INFINITY);
+          s[x][n][2 * y] = z.x;
+          s[x][n][2 * y + 1] = z.y;
+          const float2 v = add2(z, make_float2(fv, fv));
+          w[x][y][n] = v;
+          top[n] = make_float2(fmaxf(top[n].x, z.x), fmaxf(top[n].y, z.y));
+          wide[n] = make_float2(fmaxf(wide[n].x, v.x), fmaxf(wide[n].y, v.y));
+        }
       }
     bool move = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        move |= top[n][h] > m[n][h] + 64.f || wide[n][h] > big[n][h] + 8.f;
+      move |= top[n].x > m[n].x + 64.f || top[n].y > m[n].y + 64.f ||
+              wide[n].x > big[n].x + 8.f || wide[n].y > big[n].y + 8.f;
     if (__any_sync(~0u, move)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        const float2 m0 = m[n], big0 = big[n];
+        m[n] = make_float2(column_max(top[n].x, m0.x), column_max(top[n].y, m0.y));
+        big[n] = make_float2(column_max(wide[n].x, big0.x), column_max(wide[n].y, big0.y));
+        l[n].x *= ex2(m0.x - m[n].x);
+        l[n].y *= ex2(m0.y - m[n].y);
+        const float fx = ex2(big0.x - big[n].x), fy = ex2(big0.y - big[n].y);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float u = top[n][h], v = wide[n][h];
-#pragma unroll
-          for (int i = 4; i < 32; i <<= 1) {
-            u = fmaxf(u, __shfl_xor_sync(~0u, u, i));
-            v = fmaxf(v, __shfl_xor_sync(~0u, v, i));
-          }
-          u = fmaxf(u, m[n][h]);
-          v = fmaxf(v, big[n][h]);
-          l[n][h] *= power_of_two(m[n][h] - u);
-          const float f = power_of_two(big[n][h] - v);
-#pragma unroll
-          for (int i = 0; i < DP / 16; ++i) {
-            o[n][i][h] *= f;
-            o[n][i][2 + h] *= f;
-          }
-          m[n][h] = u;
-          big[n][h] = v;
+        for (int i = 0; i < DP / 16; ++i) {
+          o[n][i][0] *= fx;
+          o[n][i][1] *= fy;
+          o[n][i][2] *= fx;
+          o[n][i][3] *= fy;
         }
+      }
     }
     uint32_t p[kGroups][NT][2];
 #pragma unroll
-    for (int x = 0; x < kGroups; ++x)
+    for (int n = 0; n < NT; ++n) {
+      const float2 m0 = make_float2(-m[n].x, -m[n].y);
+      const float2 b0 = make_float2(7.f - big[n].x, 7.f - big[n].y);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int x = 0; x < kGroups; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float e[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            l[n][h] += power_of_two(s[x][n][2 * y + h] - m[n][h]);
-            e[h] = power_of_two(w[x][n][2 * y + h] - (big[n][h] - 7.f));
-          }
-          p[x][n][y] = transposed(half_pair(e[0], e[1]));
+          const float2 z = add2(make_float2(s[x][n][2 * y], s[x][n][2 * y + 1]), m0);
+          const float2 v = add2(w[x][y][n], b0);
+          l[n] = add2(l[n], make_float2(ex2(z.x), ex2(z.y)));
+          p[x][n][y] = transposed(half_pair(ex2(v.x), ex2(v.y)));
         }
-      }
-    copies_wait<3>();
+    }
+    copies_wait<2>();
+    __syncwarp();
 #pragma unroll
     for (int x = 0; x < kGroups; ++x) {
-      constexpr int kWords = DP / 32;  // of a lane's part of a value
       uint32_t v[4][kWords];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const uint32_t at = v_slot(stage) + (x * 4 + y) * 4 * DP + lane * (DP / 8);
-        if constexpr (DP == 128) {
-          const uint4 u = shared16(at);
-          v[y][0] = u.x;
-          v[y][1] = u.y;
-          v[y][2] = u.z;
-          v[y][3] = u.w;
-        } else {
-          const uint2 u = shared8(at);
-          v[y][0] = u.x;
-          v[y][1] = u.y;
-        }
-      }
+      for (int y = 0; y < 4; ++y)
+        shared_words(v[y], read + value_at(16 * x + 2 * t + (y & 1) + 8 * (y >> 1),
+                                           DP == 128 ? g : g >> 1) +
+                               (DP == 128 ? 0 : (g & 1) * 8));
 #pragma unroll
       for (int r = 0; r < kWords; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           // codes of neighbouring keys side by side, of two dimensions
-          const uint32_t u = __byte_perm(v[0][r], v[1][r], i ? 0x7362 : 0x5140);
-          const uint32_t z = __byte_perm(v[2][r], v[3][r], i ? 0x7362 : 0x5140);
-          const uint32_t a0 = decode2(u), a1 = decode2(u >> 16);
-          const uint32_t a2 = decode2(z), a3 = decode2(z >> 16);
+          uint32_t a0, a1, a2, a3;
+          decode4(__byte_perm(v[0][r], v[1][r], i ? 0x7362 : 0x5140), a0, a1);
+          decode4(__byte_perm(v[2][r], v[3][r], i ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             product(o[n][2 * r + i], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
         }
     }
-    load_values(stage);
+    step(read);
+    __syncwarp();
+    now = next;
+    load_keys();
+  }
+
+  // The largest of a column, and of `x`.
+  __device__ __forceinline__ float column_max(float v, float x) {
+#pragma unroll
+    for (int i = 4; i < 32; i <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, i));
+    return fmaxf(v, x);
   }
 
   // The outputs of what this warp has of a row, and its log-sum-exps, in
@@ -543,17 +536,19 @@ struct QuantWarp {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float sum = l[n][h];
+        float sum = h ? l[n].y : l[n].x;
+        float& base = h ? m[n].y : m[n].x;
+        const float weights = h ? big[n].y : big[n].x;
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(~0u, sum, i);
         const bool none = sum == 0.f;
-        const float f = none ? 0.f : exp2f(big[n][h] - 7.f - m[n][h]) / sum;
+        const float f = none ? 0.f : exp2f(weights - 7.f - base) / sum;
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
           o[n][i][h] = none ? 0.f : o[n][i][h] * f;
           o[n][i][2 + h] = none ? 0.f : o[n][i][2 + h] * f;
         }
-        m[n][h] = none ? -INFINITY : m[n][h] + log2f(sum);
+        base = none ? -INFINITY : base + log2f(sum);
       }
   }
 
@@ -578,7 +573,7 @@ struct QuantWarp {
             to[i] = make_uint4(u[0], u[1], u[2], u[3]);
           }
         }
-        if (g == 0 && a.lse) a.lse[b * a.l_sb + (first + at) * a.l_sh] = m[n][h];
+        if (g == 0 && a.lse) a.lse[b * a.l_sb + (first + at) * a.l_sh] = h ? m[n].y : m[n].x;
       }
   }
 
@@ -592,19 +587,19 @@ struct QuantWarp {
         float2* to = reinterpret_cast<float2*>(piece + at * DP + g * (DP / 8));
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) to[i] = make_float2(o[n][i][h], o[n][i][2 + h]);
-        if (g == 0) lse[at] = m[n][h];
+        if (g == 0) lse[at] = h ? m[n].y : m[n].x;
       }
   }
 };
 
 // Where share `unit` lies; all lanes of a warp together. sums[i]: tiles in front
-// of chunk i (of `chunk` sequences each) for i up to kQuantThreads.
-template <int TILE>
+// of chunk i (of `chunk` sequences each).
+template <int TILE, int THREADS>
 __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int64_t unit,
                                           const int64_t* sums, int64_t chunk) {
   const int lane = threadIdx.x & 31;
   int below = 0;
-  for (int i = lane; i < kQuantThreads; i += 32) below += sums[i] * a.rows <= unit;
+  for (int i = lane; i < THREADS; i += 32) below += sums[i] * a.rows <= unit;
   below = __reduce_add_sync(~0u, below) - 1;  // the last chunk that begins at or before it
   int64_t before = sums[below];
   for (int64_t b0 = below * chunk;; b0 += 32) {
@@ -635,13 +630,15 @@ __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int64_t unit,
 }
 
 template <int DP, int NT>
-__global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const QuantAttnArgs a) {
+__global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
+    quant_attend_kernel(const QuantAttnArgs a) {
   using L = QuantLayout<DP, NT>;
   using Warp = QuantWarp<DP, NT>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kQuantWarps = L::kWarps, kQuantThreads = L::kThreads;
+  extern __shared__ __align__(16) uint8_t smem[];  // for each warp a ring and a head piece
   __shared__ PieceInfo info[kQuantWarps];
   __shared__ float piece_lse[kQuantWarps][2][L::kHeads];
-  __shared__ int64_t sums[kQuantThreads + 1];
+  __shared__ int64_t sums[kQuantThreads];
   __shared__ int64_t part[kQuantWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
@@ -702,40 +699,31 @@ __global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const Qu
     cta_ends = share_start(total, share - warp + kQuantWarps, shares);
     const int64_t u0 = share_start(total, share, shares);
     count = share_start(total, share + 1, shares) - u0;
-    if (count > 0) spot = find_spot<L::kTile>(a, u0, sums, chunk);
+    if (count > 0) spot = find_spot<L::kTile, kQuantThreads>(a, u0, sums, chunk);
   }
 
-  Warp w(a, shared_addr(smem) + warp * L::kWarp);
-  float* head_piece = reinterpret_cast<float*>(smem + warp * L::kWarp + L::kRing);
-  float* tail_piece = reinterpret_cast<float*>(smem + warp * L::kWarp);
+  Warp w(a, smem_addr(smem) + warp * L::kWarp);
+  // a head piece lies behind its warp's ring, a tail piece over it
+  const auto piece = [&](int i, bool tail) {
+    return reinterpret_cast<float*>(smem + i * L::kWarp + (tail ? 0 : L::kRing));
+  };
   if (lane == 0) {
     info[warp].has[0] = info[warp].has[1] = info[warp].ends = 0;
     info[warp].empty = count == 0;
   }
   __syncwarp();
   if (count > 0) {
-    uint32_t ok[2][Warp::kMasks];
     w.due = spot;
     w.due_left = count;
     w.look_up();
-#pragma unroll
-    for (int stage = 0; stage < 2; ++stage) {
-      w.load_keys(stage);
-#pragma unroll
-      for (int i = 0; i < Warp::kMasks; ++i) ok[stage][i] = w.due_ok[i];
-      w.load_values(stage);
-    }
+    w.load_keys();
+    w.load_values();
+    w.now = w.next;
+    w.load_keys();
     bool began = spot.tile == 0;  // the row begins in this share
     w.begin(spot.b, spot.row);
-    int stage = 0;
     for (int64_t i = 0; i < count; ++i) {
-      w.tile(stage, ok[0]);
-#pragma unroll
-      for (int j = 0; j < Warp::kMasks; ++j) {
-        ok[0][j] = ok[1][j];
-        ok[1][j] = w.due_ok[j];
-      }
-      stage ^= 1;
+      w.tile();
       const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
       if (ends || last) {
         w.finish();
@@ -744,7 +732,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const Qu
         } else {
           const int tail = began ? 1 : 0;
           __syncwarp();  // the ring has been read
-          w.keep(tail ? tail_piece : head_piece, piece_lse[warp][tail]);
+          w.keep(piece(warp, tail), piece_lse[warp][tail]);
           if (lane == 0) {
             info[warp].b[tail] = spot.b;
             info[warp].row[tail] = spot.row;
@@ -761,7 +749,6 @@ __global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const Qu
         ++spot.tile;
       }
     }
-    copies_wait<0>();
   }
   __syncthreads();
 
@@ -787,9 +774,6 @@ __global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const Qu
       if (!info[to].empty) ends = info[to].ends != 0;
       ++to;
     }
-    const auto piece = [&](int i) {
-      return reinterpret_cast<const float*>(smem + i * L::kWarp + (i == from ? 0 : L::kRing));
-    };
     int32_t first;
     const int32_t heads = row_heads(a, row, first);
     const bool done = kind == 1 && ends;
@@ -804,8 +788,8 @@ __global__ void __launch_bounds__(kQuantThreads, 1) quant_attend_kernel(const Qu
       float2 x = make_float2(0.f, 0.f);
       for (int i = at; i < to; ++i) {
         if (info[i].empty) continue;
-        const float f = power_of_two(piece_lse[i][i == from][h] - base);
-        const float2 y = *reinterpret_cast<const float2*>(piece(i) + h * DP + d);
+        const float f = ex2(piece_lse[i][i == from][h] - base);
+        const float2 y = *reinterpret_cast<const float2*>(piece(i, i == from) + h * DP + d);
         sum += f;
         x.x += f * y.x;
         x.y += f * y.y;
@@ -878,7 +862,7 @@ __global__ void __launch_bounds__(kQuantJoinThreads)
 #pragma unroll 4
   for (int64_t c = c0 + warp; c <= c1; c += kQuantJoinWarps) {
     if (!has(c)) continue;
-    const float f = power_of_two(a.part_lse[slot(c)] - base);
+    const float f = ex2(a.part_lse[slot(c)] - base);
     const float* y = a.part_o + slot(c) * DP + lane * kDims;
     sum += f;
     if constexpr (kDims == 4) {

@@ -45,7 +45,7 @@ struct QuantPlan {
 
 constexpr int64_t kMaxUnits = 1000000000;
 // Tiles of a row that a CTA of its own still takes.
-constexpr int64_t kWholeTiles = 2 * kQuantWarps;
+constexpr int64_t kWholeTiles = 16;
 
 QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,
                          int64_t max_pages, int32_t page_size) {
@@ -65,7 +65,7 @@ QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t
     p.grid = rows;
     return p;
   }
-  const int64_t most = (units + kQuantWarps - 1) / kQuantWarps;
+  const int64_t warps = p.columns == 1 ? 12 : 8, most = (units + warps - 1) / warps;
   p.grid = most < 1 ? 1 : (most < sms ? most : sms);
   const size_t slots = 2 * static_cast<size_t>(p.grid) * 8 * p.columns;
   p.starts = 0;
@@ -89,7 +89,7 @@ dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t strea
       return DSA_ECUDA;
     ready[dev].store(true, std::memory_order_relaxed);
   }
-  kernel<<<static_cast<unsigned>(p.grid), kQuantThreads, kSmem, stream>>>(a);
+  kernel<<<static_cast<unsigned>(p.grid), QuantLayout<DP, NT>::kThreads, kSmem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
   if (p.whole) return DSA_OK;
   const int64_t ctas = a.batch * a.pool.kv_heads * a.group;
