@@ -12,6 +12,11 @@ __device__ __forceinline__ void follow() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// In the kernel that it follows: from here on (in all CTAs) it may be launched.
+__device__ __forceinline__ void launch_followers() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <typename... P, typename... A>
 bool launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream,
                   A... args) {

@@ -13,10 +13,10 @@
 // a row to 2^14.
 //
 // Each (sequence, key/value head) is a row of tiles; the rows lie on one line
-// that is cut into equal shares, one for each warp of the GPU. Rows that lie
-// within a warp's share are finished by it; pieces are joined by their
-// log-sum-exps, first within the CTA at its end, then, for rows that pass from
-// CTA to CTA, by a second launch.
+// that is cut into equal shares of CTAs, one on each SM, and those into equal ones
+// of warps. Rows that lie within a warp's share are finished by it; pieces are
+// joined by their log-sum-exps, first within the CTA at its end, then, for rows
+// that pass from CTA to CTA, by a second launch.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -47,6 +47,8 @@ struct QuantAttnArgs {
   int32_t bf16;
   int32_t whole;    // a CTA for each row
   int32_t* starts;  // [batch + 1] tiles in front of each sequence
+  int32_t ctas;
+  int32_t* begins;  // [ctas + 1] first unit of each CTA's share
   float* part_o;    // [2 grid][heads][DP]
   float* part_lse;  // [2 grid][heads]
 };
@@ -55,7 +57,7 @@ template <int DP, int NT>
 struct QuantLayout {
   static constexpr int kTile = kQuantTileBytes / DP;  // keys
   static constexpr int kHeads = 8 * NT;
-  // As many as the registers let be: 16 columns take 230 of a thread.
+  // As many as the registers let be: 16 columns take 250 of a thread.
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = 3 * kQuantTileBytes;
@@ -120,9 +122,14 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // ---- the line of tiles -----------------------------------------------------
 
-// Unit at which share i of n begins.
-__device__ __forceinline__ int64_t share_start(int64_t total, int64_t i, int64_t n) {
-  return total * i / n;
+// Unit at which share i of n begins (units number less than 2^31).
+__device__ __forceinline__ int32_t share_start(int32_t total, uint32_t i, uint32_t n) {
+  return static_cast<int32_t>(static_cast<uint64_t>(total) * i / n);
+}
+
+// The last of n shares that begins at or before `unit`.
+__device__ __forceinline__ int32_t share_of(int32_t total, int32_t unit, uint32_t n) {
+  return static_cast<int32_t>((static_cast<uint64_t>(unit + 1) * n - 1) / total);
 }
 
 __device__ __forceinline__ int32_t quant_length(const QuantAttnArgs& a, int64_t b) {
@@ -175,14 +182,14 @@ __device__ __forceinline__ uint16_t* out_row(const QuantAttnArgs& a, int64_t b, 
   return static_cast<uint16_t*>(a.out) + b * a.o_sb + head * a.o_sh;
 }
 
-// Pieces of a row that a warp leaves for the CTA's end.
+// Pieces of rows that a warp leaves for the CTA's end: a head piece (its row
+// began before the share) and a tail piece (its row goes on behind it).
 struct PieceInfo {
   int64_t b[2];
   int32_t row[2];
-  int32_t has[2];  // head piece (the row began before), tail piece (it goes on behind)
-  int32_t ends;    // the head piece ends its row
-  int32_t empty;   // no share
+  int32_t flags;
 };
+constexpr int kHasHead = 1, kHasTail = 2, kHeadEnds = 4, kEmpty = 8;
 
 // ---- the kernel ------------------------------------------------------------
 
@@ -218,7 +225,7 @@ struct QuantWarp {
 
   Spot due;          // the tile whose keys are loaded next
   int32_t due_page;  // and the pages of its groups
-  int64_t due_left;  // tiles from it to the share's end
+  int32_t due_left;  // tiles from it to the share's end
   Tile now, next;
 
   uint32_t qf[NT][kSteps][2];
@@ -311,7 +318,10 @@ struct QuantWarp {
         }
       }
       load(0, next);
-      if (--due_left > 0) advance<kTile>(a, due);
+      if (--due_left > 0) {
+        advance<kTile>(a, due);
+        if (due.tile == 0) fetch_queries();
+      }
       look_up();
     } else {
       next.page = -2;  // no tile
@@ -321,6 +331,20 @@ struct QuantWarp {
   __device__ __forceinline__ void load_values() {
     if (next.page != -2) load(1, next);
     copies_commit();
+  }
+
+  // Brings the queries of the due tile's row nearer, which begins in two tiles.
+  __device__ __forceinline__ void fetch_queries() {
+    int32_t first;
+    const int32_t heads = row_heads(a, due.row, first);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + g;
+      if (h < heads && 32 * t < a.pool.dim)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint16_t*>(a.q) +
+                                                      due.b * a.q_sb + (first + h) * a.q_sh +
+                                                      32 * t));
+    }
   }
 
   // The queries of a row as the products' right-hand side: column g is a head,
@@ -592,37 +616,38 @@ struct QuantWarp {
   }
 };
 
-// Where share `unit` lies; all lanes of a warp together. sums[i]: tiles in front
-// of chunk i (of `chunk` sequences each).
+// Where `unit` lies; all lanes of a warp together. sums[i]: tiles in front of
+// chunk i (of `chunk` sequences each).
 template <int TILE, int THREADS>
-__device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int64_t unit,
-                                          const int64_t* sums, int64_t chunk) {
+__device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
+                                          const int32_t* sums, int64_t chunk) {
   const int lane = threadIdx.x & 31;
   int below = 0;
-  for (int i = lane; i < THREADS; i += 32) below += sums[i] * a.rows <= unit;
+#pragma unroll
+  for (int i = 0; i < THREADS; i += 32) below += sums[i + lane] * a.rows <= unit;
   below = __reduce_add_sync(~0u, below) - 1;  // the last chunk that begins at or before it
-  int64_t before = sums[below];
+  int32_t before = sums[below];
   for (int64_t b0 = below * chunk;; b0 += 32) {
     Spot s;
     s.b = b0 + lane;
-    s.tiles = 0;
+    s.tiles = s.tokens = 0;
     if (s.b < a.batch) enter<TILE>(a, s);
-    int64_t upto = s.tiles;
+    int32_t upto = s.tiles;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, upto, i);
+      const int32_t y = __shfl_up_sync(~0u, upto, i);
       if (lane >= i) upto += y;
     }
     const uint32_t past = __ballot_sync(~0u, (before + upto) * a.rows > unit);
     if (past) {
       const int who = __ffs(past) - 1;
-      const int64_t rest = unit - (before + upto - s.tiles) * a.rows;
+      const uint32_t in = __shfl_sync(~0u, unit - (before + upto - s.tiles) * a.rows, who);
       s.b = b0 + who;
       s.tiles = __shfl_sync(~0u, s.tiles, who);
-      const int64_t in = __shfl_sync(~0u, rest, who);
-      s.tokens = quant_length(a, s.b);
-      s.row = static_cast<int32_t>(in / s.tiles);
-      s.tile = static_cast<int32_t>(in - static_cast<int64_t>(s.row) * s.tiles);
+      s.tokens = __shfl_sync(~0u, s.tokens, who);
+      const uint32_t row = in / static_cast<uint32_t>(s.tiles);
+      s.row = static_cast<int32_t>(row);
+      s.tile = static_cast<int32_t>(in - row * s.tiles);
       return s;
     }
     before += __shfl_sync(~0u, upto, 31);
@@ -634,17 +659,18 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     quant_attend_kernel(const QuantAttnArgs a) {
   using L = QuantLayout<DP, NT>;
   using Warp = QuantWarp<DP, NT>;
-  constexpr int kQuantWarps = L::kWarps, kQuantThreads = L::kThreads;
+  constexpr int W = L::kWarps;
   extern __shared__ __align__(16) uint8_t smem[];  // for each warp a ring and a head piece
-  __shared__ PieceInfo info[kQuantWarps];
-  __shared__ float piece_lse[kQuantWarps][2][L::kHeads];
-  __shared__ int64_t sums[kQuantThreads];
-  __shared__ int64_t part[kQuantWarps];
+  __shared__ PieceInfo info[W];
+  __shared__ float piece_lse[W][2][L::kHeads];  // then the pieces' weights
+  __shared__ float chain_lse[W + 1][L::kHeads];
+  __shared__ int32_t sums[L::kThreads];
+  __shared__ int32_t part[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   // This warp's share: `count` units from `spot` on.
   Spot spot{};
-  int64_t count, cta_begins, cta_ends;
+  int32_t count;
   if (a.whole) {
     spot.b = blockIdx.x / a.rows;
     spot.row = static_cast<int32_t>(blockIdx.x - spot.b * a.rows);
@@ -652,54 +678,54 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     if (spot.tiles == 0) {
       int32_t first;
       const int32_t heads = row_heads(a, spot.row, first);
-      for (int i = threadIdx.x; i < heads * a.pool.dim; i += kQuantThreads)
+      for (int i = threadIdx.x; i < heads * a.pool.dim; i += L::kThreads)
         out_row(a, spot.b, first + i / a.pool.dim)[i % a.pool.dim] = 0;
       if (a.lse && threadIdx.x < heads)
         a.lse[spot.b * a.l_sb + (first + static_cast<int>(threadIdx.x)) * a.l_sh] = -INFINITY;
       return;
     }
-    cta_begins = 0;
-    cta_ends = spot.tiles;
-    const int64_t s0 = share_start(spot.tiles, warp, kQuantWarps);
-    count = share_start(spot.tiles, warp + 1, kQuantWarps) - s0;
-    spot.tile = static_cast<int32_t>(s0);
+    spot.tile = share_start(spot.tiles, warp, W);
+    count = share_start(spot.tiles, warp + 1, W) - spot.tile;
   } else {
-    const int64_t chunk = (a.batch + kQuantThreads - 1) / kQuantThreads;
+    launch_followers();
+    const int64_t chunk = (a.batch + L::kThreads - 1) / L::kThreads;
     const int64_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, a.batch);
-    int64_t mine = 0;
+    int32_t mine = 0;
     for (int64_t b = b0; b < b1; ++b) mine += (quant_length(a, b) + L::kTile - 1) / L::kTile;
-    int64_t upto = mine;
+    int32_t upto = mine;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, upto, i);
+      const int32_t y = __shfl_up_sync(~0u, upto, i);
       if (lane >= i) upto += y;
     }
     if (lane == 31) part[warp] = upto;
     __syncthreads();
-    int64_t before = upto - mine, total = 0;
+    int32_t before = upto - mine, total = 0;
 #pragma unroll
-    for (int i = 0; i < kQuantWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
       if (i < warp) before += part[i];
       total += part[i];
     }
     sums[threadIdx.x] = before;
+    __syncthreads();
+    const int32_t units = total * a.rows;
+    const int32_t u0 = share_start(units, blockIdx.x, a.ctas);
+    const int32_t ours = share_start(units, blockIdx.x + 1, a.ctas) - u0;
+    const int32_t first = share_start(ours, warp, W);
+    count = share_start(ours, warp + 1, W) - first;
+    if (count > 0) spot = find_spot<L::kTile, L::kThreads>(a, u0 + first, sums, chunk);
+    if (threadIdx.x == 0) {
+      a.begins[blockIdx.x] = u0;
+      if (blockIdx.x + 1 == a.ctas) a.begins[a.ctas] = units;
+    }
     if (blockIdx.x == 0) {
-      int64_t at = before;
+      int32_t at = before;
       for (int64_t b = b0; b < b1; ++b) {
-        a.starts[b] = static_cast<int32_t>(at);
+        a.starts[b] = at;
         at += (quant_length(a, b) + L::kTile - 1) / L::kTile;
       }
-      if (threadIdx.x == 0) a.starts[a.batch] = static_cast<int32_t>(total);
+      if (threadIdx.x == 0) a.starts[a.batch] = total;
     }
-    __syncthreads();
-    total *= a.rows;
-    const int64_t shares = static_cast<int64_t>(gridDim.x) * kQuantWarps;
-    const int64_t share = static_cast<int64_t>(blockIdx.x) * kQuantWarps + warp;
-    cta_begins = share_start(total, share - warp, shares);
-    cta_ends = share_start(total, share - warp + kQuantWarps, shares);
-    const int64_t u0 = share_start(total, share, shares);
-    count = share_start(total, share + 1, shares) - u0;
-    if (count > 0) spot = find_spot<L::kTile, kQuantThreads>(a, u0, sums, chunk);
   }
 
   Warp w(a, smem_addr(smem) + warp * L::kWarp);
@@ -707,11 +733,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   const auto piece = [&](int i, bool tail) {
     return reinterpret_cast<float*>(smem + i * L::kWarp + (tail ? 0 : L::kRing));
   };
-  if (lane == 0) {
-    info[warp].has[0] = info[warp].has[1] = info[warp].ends = 0;
-    info[warp].empty = count == 0;
-  }
-  __syncwarp();
+  int flags = count > 0 ? 0 : kEmpty;
   if (count > 0) {
     w.due = spot;
     w.due_left = count;
@@ -722,7 +744,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     w.load_keys();
     bool began = spot.tile == 0;  // the row begins in this share
     w.begin(spot.b, spot.row);
-    for (int64_t i = 0; i < count; ++i) {
+    for (int32_t i = 0; i < count; ++i) {
       w.tile();
       const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
       if (ends || last) {
@@ -736,9 +758,8 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
           if (lane == 0) {
             info[warp].b[tail] = spot.b;
             info[warp].row[tail] = spot.row;
-            info[warp].has[tail] = 1;
-            if (!tail) info[warp].ends = ends;
           }
+          flags |= tail ? kHasTail : kHasHead | (ends ? kHeadEnds : 0);
         }
         if (!last) {
           advance<L::kTile>(a, spot);
@@ -750,106 +771,117 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
       }
     }
   }
+  if (lane == 0) info[warp].flags = flags;
   __syncthreads();
 
-  // Chains of pieces of one row: a tail piece and the head pieces behind it, or
-  // those at the CTA's begin, whose row began in another CTA.
-  for (int from = -1; from < kQuantWarps; ++from) {
-    int at = from;
-    if (from < 0) {
-      at = 0;
-      while (at < kQuantWarps && info[at].empty) ++at;
-      if (at == kQuantWarps) break;
-      if (!info[at].has[0]) continue;
-    } else if (!info[from].has[1]) {
-      continue;
-    }
-    const int kind = from < 0 ? 0 : 1;
-    const int64_t b = info[at].b[kind];
-    const int32_t row = info[at].row[kind];
-    // the warps whose head pieces follow, and whether the row ends with them
-    bool ends = kind == 0 && info[at].ends;
-    int to = at + 1;
-    while (!ends && to < kQuantWarps) {
-      if (!info[to].empty) ends = info[to].ends != 0;
-      ++to;
-    }
-    int32_t first;
-    const int32_t heads = row_heads(a, row, first);
-    const bool done = kind == 1 && ends;
-    const int64_t slot = 2ll * blockIdx.x + kind;
-    for (int e = threadIdx.x; e < heads * (DP / 2); e += kQuantThreads) {
-      const int h = e / (DP / 2), d = e % (DP / 2) * 2;
-      float top = -INFINITY;
-      for (int i = at; i < to; ++i)
-        if (!info[i].empty) top = fmaxf(top, piece_lse[i][i == from][h]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      float2 x = make_float2(0.f, 0.f);
-      for (int i = at; i < to; ++i) {
-        if (info[i].empty) continue;
-        const float f = ex2(piece_lse[i][i == from][h] - base);
-        const float2 y = *reinterpret_cast<const float2*>(piece(i, i == from) + h * DP + d);
-        sum += f;
-        x.x += f * y.x;
-        x.y += f * y.y;
+  // Chains of pieces of one row. Chain 0: the head pieces at the CTA's begin, of
+  // a row that began in another CTA; chain i + 1: warp i's tail piece and the
+  // head pieces behind it.
+  const int kinds = lane < W ? info[lane].flags : kEmpty;
+  const uint32_t empty = __ballot_sync(~0u, kinds & kEmpty);
+  const uint32_t head_ends = __ballot_sync(~0u, kinds & kHeadEnds);
+  const uint32_t heads_at = __ballot_sync(~0u, kinds & kHasHead);
+  const uint32_t tails = __ballot_sync(~0u, kinds & kHasTail);
+  const int front = __ffs(~empty) - 1;  // 0 to W
+  const uint32_t chains = (tails << 1) | (heads_at >> front & 1);
+  // warps [from, to) have pieces of chain c, but for empty ones
+  const auto from_of = [&](int c) { return c == 0 ? front : c - 1; };
+  const auto to_of = [&](int c, bool& ends) {
+    const uint32_t past = c == 0 ? head_ends & (~0u << front) : head_ends & (~0u << c);
+    ends = past != 0;
+    return past ? __ffs(past) : W;
+  };
+  for (int i = threadIdx.x; i < (W + 1) * L::kHeads; i += L::kThreads) {
+    const int c = i / L::kHeads, h = i % L::kHeads;
+    if (!(chains >> c & 1)) continue;
+    bool ends;
+    const int from = from_of(c), to = to_of(c, ends);
+    float top = -INFINITY;
+    for (int j = from; j < to; ++j)
+      if (!(empty >> j & 1)) top = fmaxf(top, piece_lse[j][j == c - 1][h]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int j = from; j < to; ++j)
+      if (!(empty >> j & 1)) sum += ex2(piece_lse[j][j == c - 1][h] - base);
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    for (int j = from; j < to; ++j)
+      if (!(empty >> j & 1)) {
+        float& x = piece_lse[j][j == c - 1][h];
+        x = ex2(x - base) * f;
       }
-      const float f = sum == 0.f ? 0.f : 1.f / sum, z = base + log2f(sum);
-      x.x = sum == 0.f ? 0.f : x.x * f;
-      x.y = sum == 0.f ? 0.f : x.y * f;
-      if (done) {
-        if (d < a.pool.dim)
-          *reinterpret_cast<uint32_t*>(out_row(a, b, first + h) + d) = pack_pair(a, x.x, x.y);
-        if (d == 0 && a.lse) a.lse[b * a.l_sb + (first + h) * a.l_sh] = z;
+    chain_lse[c][h] = base + log2f(sum);
+  }
+  __syncthreads();
+  constexpr int kDims = DP / 32;
+  int turn = 0;
+  for (uint32_t left = chains; left; left &= left - 1) {
+    const int c = __ffs(left) - 1;
+    bool ends;
+    const int from = from_of(c), to = to_of(c, ends), kind = c == 0 ? 0 : 1;
+    const int64_t b = info[from].b[kind];
+    int32_t first;
+    const int32_t heads = row_heads(a, info[from].row[kind], first);
+    for (int h = 0; h < heads; ++h) {
+      if (turn++ % W != warp) continue;
+      float x[kDims] = {};
+      for (int j = from; j < to; ++j) {
+        if (empty >> j & 1) continue;
+        const float f = piece_lse[j][j == c - 1][h];
+        const float* y = piece(j, j == c - 1) + h * DP + lane * kDims;
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) x[i] += f * y[i];
+      }
+      if (c > 0 && ends) {
+        uint16_t* to_row = out_row(a, b, first + h) + lane * kDims;
+        if (lane * kDims < a.pool.dim) {
+#pragma unroll
+          for (int i = 0; i < kDims; i += 2)
+            *reinterpret_cast<uint32_t*>(to_row + i) = pack_pair(a, x[i], x[i + 1]);
+        }
+        if (lane == 0 && a.lse) a.lse[b * a.l_sb + (first + h) * a.l_sh] = chain_lse[c][h];
       } else {
-        *reinterpret_cast<float2*>(a.part_o + (slot * L::kHeads + h) * DP + d) = x;
-        if (d == 0) a.part_lse[slot * L::kHeads + h] = z;
+        const int64_t slot = (2ll * blockIdx.x + kind) * L::kHeads + h;
+        float* to_part = a.part_o + slot * DP + lane * kDims;
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) to_part[i] = x[i];
+        if (lane == 0) a.part_lse[slot] = chain_lse[c][h];
       }
     }
   }
 }
 
-constexpr int kQuantJoinWarps = 4;
+constexpr int kQuantJoinWarps = 8;
 constexpr int kQuantJoinThreads = 32 * kQuantJoinWarps;
 
 // A CTA for each query head: joins what the CTAs of the first launch left of
 // rows that lie in several of them, and writes those without tiles.
 template <int DP, int NT>
-__global__ void __launch_bounds__(kQuantJoinThreads)
-    quant_join_kernel(const QuantAttnArgs a, int32_t ctas) {
+__global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const QuantAttnArgs a) {
   constexpr int kHeads = 8 * NT, kDims = DP / 32;
   __shared__ float shared_o[kQuantJoinWarps][DP];
   __shared__ float shared_top[kQuantJoinWarps], shared_sum[kQuantJoinWarps];
-  follow();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t all = static_cast<int64_t>(a.pool.kv_heads) * a.group;
+  const int32_t all = a.pool.kv_heads * a.group;
   const int64_t b = blockIdx.x / all;
   const int32_t head = static_cast<int32_t>(blockIdx.x - b * all);
   const int32_t kv = head / a.group, in = head - kv * a.group;
   const int32_t row = kv * a.splits + in / a.split_heads, h = in % a.split_heads;
-  const int64_t start = a.starts[b], tiles = a.starts[b + 1] - start;
-  const int64_t total = static_cast<int64_t>(a.starts[a.batch]) * a.rows;
-  const int64_t u0 = start * a.rows + row * tiles, u1 = u0 + tiles - 1;
-  // the CTA that holds a unit: share_start(total, c, ctas) <= u
-  const auto holder = [&](int64_t u) {
-    int64_t c = u * ctas / total;
-    while (share_start(total, c + 1, ctas) <= u) ++c;
-    while (share_start(total, c, ctas) > u) --c;
-    return c;
-  };
-  int64_t c0 = 0, c1 = -1;
+  follow();
+  const int32_t start = a.starts[b], tiles = a.starts[b + 1] - start;
+  const int32_t units = a.starts[a.batch] * a.rows;
+  // the first and the last CTA that have some of the row
+  int32_t c0 = 0, c1 = -1;
   if (tiles > 0) {
-    c0 = holder(u0);
-    c1 = holder(u1);
+    const int32_t u0 = start * a.rows + row * tiles;
+    c0 = share_of(units, u0, a.ctas);
+    c1 = share_of(units, u0 + tiles - 1, a.ctas);
     if (c0 == c1) return;
   }
-  // slot 1 of the first CTA, slot 0 of the others
-  const auto slot = [&](int64_t c) { return (2 * c + (c == c0)) * kHeads + h; };
-  const auto has = [&](int64_t c) {
-    return share_start(total, c, ctas) < share_start(total, c + 1, ctas);
-  };
+  // slot 1 of the first CTA, slot 0 of the others; some have no share
+  const auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0)) * kHeads + h; };
+  const auto has = [&](int c) { return a.begins[c] < a.begins[c + 1]; };
   float top = -INFINITY;
-  for (int64_t c = c0 + threadIdx.x; c <= c1; c += kQuantJoinThreads)
+  for (int c = c0 + threadIdx.x; c <= c1; c += kQuantJoinThreads)
     if (has(c)) top = fmaxf(top, a.part_lse[slot(c)]);
 #pragma unroll
   for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
@@ -860,21 +892,23 @@ __global__ void __launch_bounds__(kQuantJoinThreads)
   const float base = top == -INFINITY ? 0.f : top;
   float sum = 0.f, x[kDims] = {};
 #pragma unroll 4
-  for (int64_t c = c0 + warp; c <= c1; c += kQuantJoinWarps) {
-    if (!has(c)) continue;
-    const float f = ex2(a.part_lse[slot(c)] - base);
+  for (int c = c0 + warp; c <= c1; c += kQuantJoinWarps) {
+    // what an empty share's slot holds is not used, whatever it is
+    const bool some = has(c);
+    const float lse = a.part_lse[slot(c)];
+    const float f = some ? ex2(lse - base) : 0.f;
     const float* y = a.part_o + slot(c) * DP + lane * kDims;
     sum += f;
     if constexpr (kDims == 4) {
       const float4 z = *reinterpret_cast<const float4*>(y);
-      x[0] += f * z.x;
-      x[1] += f * z.y;
-      x[2] += f * z.z;
-      x[3] += f * z.w;
+      x[0] += some ? f * z.x : 0.f;
+      x[1] += some ? f * z.y : 0.f;
+      x[2] += some ? f * z.z : 0.f;
+      x[3] += some ? f * z.w : 0.f;
     } else {
       const float2 z = *reinterpret_cast<const float2*>(y);
-      x[0] += f * z.x;
-      x[1] += f * z.y;
+      x[0] += some ? f * z.x : 0.f;
+      x[1] += some ? f * z.y : 0.f;
     }
   }
 #pragma unroll

@@ -40,10 +40,11 @@ struct QuantPlan {
   bool whole;
   int64_t grid;
   bool fits;
-  size_t starts, part_o, part_lse, bytes;
+  size_t starts, begins, part_o, part_lse, bytes;
 };
 
-constexpr int64_t kMaxUnits = 1000000000;
+// Units of a call stay within 31 bits with the most parts of a group, 8.
+constexpr int64_t kMaxUnits = 250000000;
 // Tiles of a row that a CTA of its own still takes.
 constexpr int64_t kWholeTiles = 16;
 
@@ -69,7 +70,8 @@ QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t
   p.grid = most < 1 ? 1 : (most < sms ? most : sms);
   const size_t slots = 2 * static_cast<size_t>(p.grid) * 8 * p.columns;
   p.starts = 0;
-  p.part_o = up256((batch + 1) * 4);
+  p.begins = up256((batch + 1) * 4);
+  p.part_o = p.begins + up256((p.grid + 1) * 4);
   p.part_lse = p.part_o + up256(slots * p.dp * 4);
   p.bytes = p.part_lse + up256(slots * 4);
   return p;
@@ -94,7 +96,7 @@ dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t strea
   if (p.whole) return DSA_OK;
   const int64_t ctas = a.batch * a.pool.kv_heads * a.group;
   return launch_after(quant_join_kernel<DP, NT>, dim3(static_cast<unsigned>(ctas)),
-                      kQuantJoinThreads, stream, a, static_cast<int32_t>(p.grid))
+                      kQuantJoinThreads, stream, a)
              ? DSA_OK
              : DSA_ECUDA;
 }
@@ -174,8 +176,10 @@ extern "C" dsa_status dsa_quant_attention(
   a.l_sh = l_sh;
   a.bf16 = dtype == DSA_DTYPE_BF16;
   a.whole = p.whole;
+  a.ctas = static_cast<int32_t>(p.grid);
   char* ws = static_cast<char*>(workspace);
   a.starts = reinterpret_cast<int32_t*>(ws + p.starts);
+  a.begins = reinterpret_cast<int32_t*>(ws + p.begins);
   a.part_o = reinterpret_cast<float*>(ws + p.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

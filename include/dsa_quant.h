@@ -151,8 +151,8 @@ size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t heads,
  * is too small or not aligned, and as for dsa_quant_cache_write.
  * DSA_EUNSUPPORTED as there, for heads / kv_heads > 128, q and out not 16-byte
  * aligned or with strides that are no multiples of 8, and where batch *
- * kv_heads times the 32-token tiles that a row of `tables` has room for passes
- * 10^9, or batch * heads 10^9.
+ * kv_heads times the 32-token tiles that a row of `tables` has room for passes 2.5 *
+ * 10^8, or batch * heads 10^9.
  */
 dsa_status dsa_quant_attention(
     const void *q, int32_t dtype, int64_t batch, int32_t heads,
