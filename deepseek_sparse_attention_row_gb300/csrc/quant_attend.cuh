@@ -65,14 +65,18 @@ struct QuantLayout {
   static constexpr int kWarp = kRing + kPiece * 4;
   static constexpr int kSmem = kWarps * kWarp;
   static_assert(kPiece * 4 <= kRing, "a tail piece lies over the ring");
+  static_assert(kWarp % 128 == 0, "rows of 128 bytes");
 };
 
 // ---- instructions ----------------------------------------------------------
 
-// 16 bytes, zeros where `bytes` is 0 (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+// 16 bytes, zeros where `yes` is false (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool yes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %2, 0;\n\t"
+      "cp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst),
+      "l"(src), "r"(static_cast<uint32_t>(yes))
+      : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -272,7 +276,7 @@ struct QuantWarp {
     const uint8_t* row = a.pool.codes[kv] + x.head * a.pool.sh[kv] +
                          copy_row * a.pool.st[kv] + copy_byte;
     const int32_t mask = (1 << a.pool.page_log2) - 1;
-    const uint32_t bytes = copy_byte < a.pool.dim ? 16 : 0;
+    const bool some = copy_byte < a.pool.dim;
     bool full = true;
 #pragma unroll
     for (int i = 0; i < kMasks; ++i) full &= x.seen[i] == ~0u;
@@ -284,11 +288,10 @@ struct QuantWarp {
 #pragma unroll
       for (int j = 0; j < kCopies; ++j) {
         const int at = 16 * i + j * kRows;
-        uint32_t n = bytes;
-        if (!full && !(x.seen[i / 2] >> ((at + copy_row) & 31) & 1)) n = 0;
+        const bool yes = some && (full || (x.seen[i / 2] >> ((at + copy_row) & 31) & 1));
         const uint32_t to =
             fill + (kv ? value_at(at + copy_row, copy_byte >> 4) : key_at(at + copy_row, copy_byte >> 4));
-        copy16(to, n ? p : a.pool.codes[kv], n);
+        copy16(to, yes ? p : a.pool.codes[kv], yes);
         p += kRows * a.pool.st[kv];
       }
     }
@@ -660,7 +663,9 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   using L = QuantLayout<DP, NT>;
   using Warp = QuantWarp<DP, NT>;
   constexpr int W = L::kWarps;
-  extern __shared__ __align__(16) uint8_t smem[];  // for each warp a ring and a head piece
+  // For each warp a ring and a head piece. Rows of 128 bytes have to begin at
+  // multiples of 128 (with others, copies took twice the sectors).
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PieceInfo info[W];
   __shared__ float piece_lse[W][2][L::kHeads];  // then the pieces' weights
   __shared__ float chain_lse[W + 1][L::kHeads];
