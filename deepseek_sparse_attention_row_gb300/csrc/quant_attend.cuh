@@ -126,15 +126,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // ---- the line of tiles -----------------------------------------------------
 
-// Unit at which share i of n begins (units number less than 2^31).
-__device__ __forceinline__ int32_t share_start(int32_t total, uint32_t i, uint32_t n) {
-  return static_cast<int32_t>(static_cast<uint64_t>(total) * i / n);
-}
-
-// The last of n shares that begins at or before `unit`.
-__device__ __forceinline__ int32_t share_of(int32_t total, int32_t unit, uint32_t n) {
-  return static_cast<int32_t>((static_cast<uint64_t>(unit + 1) * n - 1) / total);
-}
+// The line cut into n (up to 1024) equal shares: share i begins at floor(total *
+// i / n), in 32 bits.
+struct Shares {
+  uint32_t n, whole, rest;
+  __device__ __forceinline__ Shares(int32_t total, uint32_t parts)
+      : n(parts), whole(total / parts), rest(total - whole * parts) {}
+  __device__ __forceinline__ int32_t begin(uint32_t i) const {
+    return static_cast<int32_t>(whole * i + rest * i / n);
+  }
+  // The last one that begins at or before `unit` of a line of `total` units.
+  __device__ __forceinline__ int32_t of(int32_t total, int32_t unit) const {
+    const float guess = static_cast<float>(unit) * static_cast<float>(n) / static_cast<float>(total);
+    uint32_t i = min(static_cast<uint32_t>(guess), n - 1);
+    while (i > 0 && begin(i) > unit) --i;
+    while (i + 1 < n && begin(i + 1) <= unit) ++i;
+    return static_cast<int32_t>(i);
+  }
+};
 
 __device__ __forceinline__ int32_t quant_length(const QuantAttnArgs& a, int64_t b) {
   const int64_t most = a.pool.max_pages << a.pool.page_log2, n = a.lens[b];
@@ -689,8 +698,9 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
         a.lse[spot.b * a.l_sb + (first + static_cast<int>(threadIdx.x)) * a.l_sh] = -INFINITY;
       return;
     }
-    spot.tile = share_start(spot.tiles, warp, W);
-    count = share_start(spot.tiles, warp + 1, W) - spot.tile;
+    const Shares warps(spot.tiles, W);
+    spot.tile = warps.begin(warp);
+    count = warps.begin(warp + 1) - spot.tile;
   } else {
     launch_followers();
     const int64_t chunk = (a.batch + L::kThreads - 1) / L::kThreads;
@@ -714,10 +724,11 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     sums[threadIdx.x] = before;
     __syncthreads();
     const int32_t units = total * a.rows;
-    const int32_t u0 = share_start(units, blockIdx.x, a.ctas);
-    const int32_t ours = share_start(units, blockIdx.x + 1, a.ctas) - u0;
-    const int32_t first = share_start(ours, warp, W);
-    count = share_start(ours, warp + 1, W) - first;
+    const Shares ctas(units, a.ctas);
+    const int32_t u0 = ctas.begin(blockIdx.x);
+    const Shares warps(ctas.begin(blockIdx.x + 1) - u0, W);
+    const int32_t first = warps.begin(warp);
+    count = warps.begin(warp + 1) - first;
     if (count > 0) spot = find_spot<L::kTile, L::kThreads>(a, u0 + first, sums, chunk);
     if (threadIdx.x == 0) {
       a.begins[blockIdx.x] = u0;
@@ -801,19 +812,23 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     if (!(chains >> c & 1)) continue;
     bool ends;
     const int from = from_of(c), to = to_of(c, ends);
-    float top = -INFINITY;
-    for (int j = from; j < to; ++j)
-      if (!(empty >> j & 1)) top = fmaxf(top, piece_lse[j][j == c - 1][h]);
+    const uint32_t pieces = ((1u << to) - (1u << from)) & ~empty;
+    float z[W], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      z[j] = pieces >> j & 1 ? piece_lse[j][j == c - 1][h] : -INFINITY;
+      top = fmaxf(top, z[j]);
+    }
     const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int j = from; j < to; ++j)
-      if (!(empty >> j & 1)) sum += ex2(piece_lse[j][j == c - 1][h] - base);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      z[j] = ex2(z[j] - base);
+      sum += z[j];
+    }
     const float f = sum == 0.f ? 0.f : 1.f / sum;
-    for (int j = from; j < to; ++j)
-      if (!(empty >> j & 1)) {
-        float& x = piece_lse[j][j == c - 1][h];
-        x = ex2(x - base) * f;
-      }
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (pieces >> j & 1) piece_lse[j][j == c - 1][h] = z[j] * f;
     chain_lse[c][h] = base + log2f(sum);
   }
   __syncthreads();
@@ -823,14 +838,16 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     const int c = __ffs(left) - 1;
     bool ends;
     const int from = from_of(c), to = to_of(c, ends), kind = c == 0 ? 0 : 1;
+    const uint32_t pieces = ((1u << to) - (1u << from)) & ~empty;
     const int64_t b = info[from].b[kind];
     int32_t first;
     const int32_t heads = row_heads(a, info[from].row[kind], first);
     for (int h = 0; h < heads; ++h) {
       if (turn++ % W != warp) continue;
       float x[kDims] = {};
-      for (int j = from; j < to; ++j) {
-        if (empty >> j & 1) continue;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if (!(pieces >> j & 1)) continue;
         const float f = piece_lse[j][j == c - 1][h];
         const float* y = piece(j, j == c - 1) + h * DP + lane * kDims;
 #pragma unroll
@@ -858,84 +875,101 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
 constexpr int kQuantJoinWarps = 8;
 constexpr int kQuantJoinThreads = 32 * kQuantJoinWarps;
 
-// A CTA for each query head: joins what the CTAs of the first launch left of
-// rows that lie in several of them, and writes those without tiles.
-template <int DP, int NT>
+// Joins what the CTAs of the first launch left of rows that lie in several of
+// them, and writes those without tiles: TEAM warps for each query head. Loads of
+// pieces do not wait for one another.
+template <int DP, int NT, int TEAM>
 __global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const QuantAttnArgs a) {
-  constexpr int kHeads = 8 * NT, kDims = DP / 32;
-  __shared__ float shared_o[kQuantJoinWarps][DP];
-  __shared__ float shared_top[kQuantJoinWarps], shared_sum[kQuantJoinWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kHeads = 8 * NT, kDims = DP / 32, kAtOnce = 4;
+  __shared__ float shared_o[TEAM][DP];
+  __shared__ float shared_top[TEAM], shared_sum[TEAM];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mate = warp % TEAM;
+  const int64_t item =
+      static_cast<int64_t>(blockIdx.x) * (kQuantJoinWarps / TEAM) + warp / TEAM;
   const int32_t all = a.pool.kv_heads * a.group;
-  const int64_t b = blockIdx.x / all;
-  const int32_t head = static_cast<int32_t>(blockIdx.x - b * all);
+  const int64_t b = item / all;
+  const int32_t head = static_cast<int32_t>(item - b * all);
   const int32_t kv = head / a.group, in = head - kv * a.group;
   const int32_t row = kv * a.splits + in / a.split_heads, h = in % a.split_heads;
   follow();
+  if (b >= a.batch) return;  // (only where a team is a warp)
   const int32_t start = a.starts[b], tiles = a.starts[b + 1] - start;
   const int32_t units = a.starts[a.batch] * a.rows;
   // the first and the last CTA that have some of the row
   int32_t c0 = 0, c1 = -1;
   if (tiles > 0) {
+    const Shares shares(units, a.ctas);
     const int32_t u0 = start * a.rows + row * tiles;
-    c0 = share_of(units, u0, a.ctas);
-    c1 = share_of(units, u0 + tiles - 1, a.ctas);
+    c0 = shares.of(units, u0);
+    c1 = shares.of(units, u0 + tiles - 1);
     if (c0 == c1) return;
   }
-  // slot 1 of the first CTA, slot 0 of the others; some have no share
-  const auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0)) * kHeads + h; };
-  const auto has = [&](int c) { return a.begins[c] < a.begins[c + 1]; };
-  float top = -INFINITY;
-  for (int c = c0 + threadIdx.x; c <= c1; c += kQuantJoinThreads)
-    if (has(c)) top = fmaxf(top, a.part_lse[slot(c)]);
+  float top = -INFINITY, sum = 0.f, x[kDims] = {};
+  for (int32_t c = c0 + mate; c <= c1; c += TEAM * kAtOnce) {
+    float lse[kAtOnce], y[kAtOnce][kDims];
+    float most = top;
 #pragma unroll
-  for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
-  if (lane == 0) shared_top[warp] = top;
-  __syncthreads();
+    for (int i = 0; i < kAtOnce; ++i) {
+      lse[i] = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kQuantJoinWarps; ++i) top = fmaxf(top, shared_top[i]);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, x[kDims] = {};
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += kQuantJoinWarps) {
-    // what an empty share's slot holds is not used, whatever it is
-    const bool some = has(c);
-    const float lse = a.part_lse[slot(c)];
-    const float f = some ? ex2(lse - base) : 0.f;
-    const float* y = a.part_o + slot(c) * DP + lane * kDims;
-    sum += f;
-    if constexpr (kDims == 4) {
-      const float4 z = *reinterpret_cast<const float4*>(y);
-      x[0] += some ? f * z.x : 0.f;
-      x[1] += some ? f * z.y : 0.f;
-      x[2] += some ? f * z.z : 0.f;
-      x[3] += some ? f * z.w : 0.f;
-    } else {
-      const float2 z = *reinterpret_cast<const float2*>(y);
-      x[0] += some ? f * z.x : 0.f;
-      x[1] += some ? f * z.y : 0.f;
+      for (int j = 0; j < kDims; ++j) y[i][j] = 0.f;
+      const int32_t at = c + i * TEAM;
+      // some have no share, and have left nothing
+      if (at <= c1 && a.begins[at] < a.begins[at + 1]) {
+        // slot 1 of the first CTA, slot 0 of the others
+        const int64_t slot = static_cast<int64_t>(2 * at + (at == c0)) * kHeads + h;
+        lse[i] = a.part_lse[slot];
+        const float* from = a.part_o + slot * DP + lane * kDims;
+#pragma unroll
+        for (int j = 0; j < kDims; ++j) y[i][j] = from[j];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) most = fmaxf(most, lse[i]);
+    const float base = most == -INFINITY ? 0.f : most, keep = ex2(top - base);
+    sum *= keep;
+#pragma unroll
+    for (int j = 0; j < kDims; ++j) x[j] *= keep;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float f = ex2(lse[i] - base);
+      sum += f;
+#pragma unroll
+      for (int j = 0; j < kDims; ++j) x[j] += f * y[i][j];
+    }
+    top = most;
+  }
+  if constexpr (TEAM > 1) {
+#pragma unroll
+    for (int j = 0; j < kDims; ++j) shared_o[mate][lane * kDims + j] = x[j];
+    if (lane == 0) {
+      shared_top[mate] = top;
+      shared_sum[mate] = sum;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) top = fmaxf(top, shared_top[i]);
+    sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kDims; ++j) x[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) {
+      const float f = ex2(shared_top[i] - (top == -INFINITY ? 0.f : top));
+      sum += f * shared_sum[i];
+#pragma unroll
+      for (int j = 0; j < kDims; ++j) x[j] += f * shared_o[i][lane * kDims + j];
     }
   }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  if (lane * kDims < a.pool.dim) {
+    uint32_t* to = reinterpret_cast<uint32_t*>(out_row(a, b, head) + lane * kDims);
 #pragma unroll
-  for (int i = 0; i < kDims; ++i) shared_o[warp][lane * kDims + i] = x[i];
-  if (lane == 0) shared_sum[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kQuantJoinWarps; ++i) sum += shared_sum[i];
-  const int d = 2 * threadIdx.x;
-  if (d < a.pool.dim) {
-    float2 z = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kQuantJoinWarps; ++i) {
-      z.x += shared_o[i][d];
-      z.y += shared_o[i][d + 1];
-    }
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint32_t*>(out_row(a, b, head) + d) =
-        sum == 0.f ? 0u : pack_pair(a, z.x * f, z.y * f);
+    for (int j = 0; j < kDims; j += 2)
+      to[j / 2] = sum == 0.f ? 0u : pack_pair(a, x[j] * f, x[j + 1] * f);
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[b * a.l_sb + head * a.l_sh] = base + log2f(sum);
+  if (lane == 0 && a.lse)
+    a.lse[b * a.l_sb + head * a.l_sh] = (top == -INFINITY ? 0.f : top) + log2f(sum);
 }
 
 }  // namespace dsa

@@ -28,7 +28,7 @@ int sm_count() {
       return 152;
     cached[dev].store(n, std::memory_order_relaxed);
   }
-  return n;
+  return n < 1024 ? n : 1024;  // as many shares as the kernels take
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -94,11 +94,17 @@ dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t strea
   kernel<<<static_cast<unsigned>(p.grid), QuantLayout<DP, NT>::kThreads, kSmem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
   if (p.whole) return DSA_OK;
-  const int64_t ctas = a.batch * a.pool.kv_heads * a.group;
-  return launch_after(quant_join_kernel<DP, NT>, dim3(static_cast<unsigned>(ctas)),
-                      kQuantJoinThreads, stream, a)
-             ? DSA_OK
-             : DSA_ECUDA;
+  // Rows that outnumber the CTAs lie in two of them, as a rule, and a warp joins
+  // those; fewer lie in many.
+  const int64_t items = a.batch * a.pool.kv_heads * a.group;
+  const bool ok =
+      a.batch * a.rows >= p.grid
+          ? launch_after(quant_join_kernel<DP, NT, 1>,
+                         dim3(static_cast<unsigned>((items + kQuantJoinWarps - 1) / kQuantJoinWarps)),
+                         kQuantJoinThreads, stream, a)
+          : launch_after(quant_join_kernel<DP, NT, kQuantJoinWarps>,
+                         dim3(static_cast<unsigned>(items)), kQuantJoinThreads, stream, a);
+  return ok ? DSA_OK : DSA_ECUDA;
 }
 
 constexpr int64_t kMaxRows = 1000000000;
