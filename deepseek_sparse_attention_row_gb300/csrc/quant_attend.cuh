@@ -70,7 +70,10 @@ struct QuantLayout {
 
 // ---- instructions ----------------------------------------------------------
 
-// 16 bytes, zeros where `yes` is false (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same, but zeros where `yes` is false (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool yes) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %2, 0;\n\t"
@@ -219,26 +222,31 @@ struct QuantWarp {
   static constexpr int kRows = 32 / kRowLanes;       // rows of one copy
   static constexpr int kCopies = 16 / kRows;         // of 16 keys
 
-  // A tile whose loads are due or under way.
+  // A tile whose loads are under way or its turn.
   struct Tile {
-    int32_t page;       // of its groups (lane i: group i); -1: none
-    int32_t inside;     // its first token's place on its page
-    int32_t head;
+    bool some;            // there is one
+    bool full;            // all keys are seen
+    int32_t page[kGroups];  // of 16 keys; -1: none
+    int32_t inside;       // its first token's place on its page
+    const uint8_t* values;  // what this lane copies of the row's values, on page 0
     uint32_t seen[kMasks];
     float sk[kMasks], sv[kMasks];  // scales, of key 32 x + lane
   };
 
   const QuantAttnArgs& a;
   const int lane, g, t;
-  const uint32_t ring;        // this warp's shared memory
-  uint32_t fill, read;        // slots of the next tile to load and to use
+  const uint32_t ring;     // this warp's shared memory
+  uint32_t fill, read;     // slots of the next tile to load and to use
+  const bool copies;       // this lane copies 16 bytes of every kRows-th row
+  uint32_t copy_to[2];     // where to, in even and odd steps of kRows
+  uint32_t key_from[2];    // where this lane's chunks of keys are, on even and odd rows
+  uint32_t value_from[2];  // its parts of values
 
-  const int copy_row;   // what this lane copies: rows from this one on,
-  const int copy_byte;  // and 16 bytes of each
-
-  Spot due;          // the tile whose keys are loaded next
-  int32_t due_page;  // and the pages of its groups
-  int32_t due_left;  // tiles from it to the share's end
+  Spot due;       // the tile whose keys are loaded next
+  int32_t left;   // tiles from it to the share's end
+  int32_t page[kGroups];
+  const uint8_t *keys, *values;  // what this lane copies of the due row, on page 0
+  const float *k_scales, *v_scales;
   Tile now, next;
 
   uint32_t qf[NT][kSteps][2];
@@ -246,15 +254,12 @@ struct QuantWarp {
   float o[NT][DP / 16][4];
   float2 l[NT], m[NT], big[NT];  // sums; bases of the sums and of the weights
 
-  // Rows of 128 bytes (two of 64) are swizzled by 16-byte chunks: the eight
-  // lanes that read together (two keys of four chunks, or four pairs of a row's
-  // chunks two rows apart) find theirs on different banks.
-  static __device__ __forceinline__ uint32_t key_at(int row, int chunk) {
-    if constexpr (DP == 128) return row * 128 + ((chunk ^ ((row & 1) << 2)) << 4);
-    return row * 64 + (chunk << 4);
-  }
-  static __device__ __forceinline__ uint32_t value_at(int row, int chunk) {
-    if constexpr (DP == 128) return row * 128 + ((chunk ^ (row & 6)) << 4);
+  // Rows of 128 bytes, or pairs of rows of 64, are swizzled by 16-byte chunks: the
+  // eight lanes that read together (two keys of four chunks, or two chunks of
+  // values that lie two rows apart) find theirs on different banks.
+  static __device__ __forceinline__ uint32_t place(int row, int chunk) {
+    if constexpr (DP == 128)
+      return row * 128 + ((chunk ^ (row & 6) ^ ((row & 1) << 2)) << 4);
     return (row >> 1) * 128 + (((((row & 1) << 2) | chunk) ^ (row & 6)) << 4);
   }
 
@@ -266,42 +271,74 @@ struct QuantWarp {
         ring(smem),
         fill(smem),
         read(smem),
-        copy_row(lane / kRowLanes),
-        copy_byte(lane % kRowLanes * 16) {}
+        copies(lane % kRowLanes * 16 < args.pool.dim) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      copy_to[i] = place(lane / kRowLanes + i * kRows, lane % kRowLanes) - i * kRows * DP;
+      key_from[i] = place(g, DP == 128 ? 4 * i + t : t);
+      value_from[i] = place(2 * t + i, DP == 128 ? g : g >> 1) + (DP == 128 ? 0 : (g & 1) * 8);
+    }
+  }
 
   __device__ __forceinline__ void step(uint32_t& slot) {
     slot += kQuantTileBytes;
     if (slot == ring + 3 * kQuantTileBytes) slot = ring;
   }
 
+  // Pointers for the due row.
+  __device__ __forceinline__ void enter_row() {
+    const int32_t head = due.row / a.splits;
+    const int row = lane / kRowLanes, byte = lane % kRowLanes * 16;
+    keys = a.pool.codes[0] + head * a.pool.sh[0] + row * a.pool.st[0] + byte;
+    values = a.pool.codes[1] + head * a.pool.sh[1] + row * a.pool.st[1] + byte;
+    k_scales = a.pool.scales[0] + head;
+    v_scales = a.pool.scales[1] + head;
+  }
+  __device__ __forceinline__ bool one_page() const { return (1 << a.pool.page_log2) >= kTile; }
   __device__ __forceinline__ void look_up() {
-    due_page = -1;
-    const int32_t at = due.tile * kTile + 16 * lane;
-    if (due_left > 0 && lane < kGroups && at < due.tokens) due_page = quant_page(a.pool, due.b, at);
+    if (left <= 0) return;
+    const int32_t t0 = due.tile * kTile;
+    page[0] = quant_page(a.pool, due.b, t0);
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i)
+      page[i] = one_page() ? page[0]
+                           : t0 + 16 * i < due.tokens ? quant_page(a.pool, due.b, t0 + 16 * i) : -1;
   }
 
-  // Rows of keys (kv 0) or values of `x` into the next slot.
-  __device__ __forceinline__ void load(int kv, const Tile& x) {
-    const uint8_t* row = a.pool.codes[kv] + x.head * a.pool.sh[kv] +
-                         copy_row * a.pool.st[kv] + copy_byte;
+  // The rows of a tile into the next slot; `from`: what this lane copies, on page 0.
+  __device__ __forceinline__ void copy_rows(const Tile& x, const uint8_t* from, int kv) {
+    const int64_t sn = a.pool.sn[kv], st = a.pool.st[kv];
     const int32_t mask = (1 << a.pool.page_log2) - 1;
-    const bool some = copy_byte < a.pool.dim;
-    bool full = true;
+    const uint32_t to[2] = {fill + copy_to[0], fill + copy_to[1]};
+    const uint8_t* p = from + x.page[0] * sn + x.inside * st;
+    if (x.full) {
+      if (copies) {
 #pragma unroll
-    for (int i = 0; i < kMasks; ++i) full &= x.seen[i] == ~0u;
+        for (int i = 0; i < kGroups; ++i) {
+          if (i > 0 && !one_page())
+            p = from + x.page[i] * sn + ((x.inside + 16 * i) & mask) * st;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int32_t page = __shfl_sync(~0u, x.page, i);
-      const uint8_t* p =
-          row + page * a.pool.sn[kv] + ((x.inside + 16 * i) & mask) * a.pool.st[kv];
+          for (int j = 0; j < kCopies; ++j) {
+            copy16(to[j & 1] + (16 * i + j * kRows) * DP, p);
+            p += kRows * st;
+          }
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) {
-        const int at = 16 * i + j * kRows;
-        const bool yes = some && (full || (x.seen[i / 2] >> ((at + copy_row) & 31) & 1));
-        const uint32_t to =
-            fill + (kv ? value_at(at + copy_row, copy_byte >> 4) : key_at(at + copy_row, copy_byte >> 4));
-        copy16(to, yes ? p : a.pool.codes[kv], yes);
-        p += kRows * a.pool.st[kv];
+        for (int i = 0; i < kGroups * kCopies; ++i)
+          copy16(to[i & 1] + i * kRows * DP, a.pool.codes[kv], false);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        p = from + x.page[i] * sn + ((x.inside + 16 * i) & mask) * st;
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+          const int at = 16 * i + j * kRows + lane / kRowLanes;
+          const bool yes = copies && (x.seen[i / 2] >> (at & 31) & 1);
+          copy16(to[j & 1] + (16 * i + j * kRows) * DP, yes ? p : a.pool.codes[kv], yes);
+          p += kRows * st;
+        }
       }
     }
     step(fill);
@@ -310,38 +347,48 @@ struct QuantWarp {
   // Keys and scales of the due tile, which becomes `next`; the one behind it is
   // due then.
   __device__ __forceinline__ void load_keys() {
-    if (due_left > 0) {
+    next.some = left > 0;
+    if (next.some) {
       const int32_t t0 = due.tile * kTile, mask = (1 << a.pool.page_log2) - 1;
-      next.page = due_page;
       next.inside = t0 & mask;
-      next.head = due.row / a.splits;
+      next.values = values;
+      bool full = t0 + kTile <= due.tokens;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        next.page[i] = page[i];
+        full &= page[i] >= 0;
+      }
+      next.full = full;
 #pragma unroll
       for (int x = 0; x < kMasks; ++x) {
-        const int32_t page = __shfl_sync(~0u, due_page, 2 * x + (lane >> 4));
+        const int32_t mine = lane < 16 ? page[2 * x] : page[2 * x + 1];
         const int32_t tok = t0 + 32 * x + lane;
-        const bool ok = page >= 0 && tok < due.tokens;
-        next.seen[x] = __ballot_sync(~0u, ok);
+        const bool ok = mine >= 0 && tok < due.tokens;
+        next.seen[x] = full ? ~0u : __ballot_sync(~0u, ok);
+        const int64_t in =
+            static_cast<int64_t>((tok & mask) >> a.pool.block_log2) * a.pool.kv_heads;
         next.sk[x] = next.sv[x] = 0.f;
         if (ok) {
-          const int64_t in = static_cast<int64_t>((tok & mask) >> a.pool.block_log2) *
-                                 a.pool.kv_heads + next.head;
-          next.sk[x] = a.pool.scales[0][page * a.pool.ssn[0] + in];
-          next.sv[x] = a.pool.scales[1][page * a.pool.ssn[1] + in];
+          next.sk[x] = k_scales[mine * a.pool.ssn[0] + in];
+          next.sv[x] = v_scales[mine * a.pool.ssn[1] + in];
         }
       }
-      load(0, next);
-      if (--due_left > 0) {
+      copy_rows(next, keys, 0);
+      if (--left > 0) {
+        const int32_t row = due.row;
+        const int64_t b = due.b;
         advance<kTile>(a, due);
-        if (due.tile == 0) fetch_queries();
+        if (due.row != row || due.b != b) {
+          enter_row();
+          fetch_queries();
+        }
       }
       look_up();
-    } else {
-      next.page = -2;  // no tile
     }
     copies_commit();
   }
   __device__ __forceinline__ void load_values() {
-    if (next.page != -2) load(1, next);
+    if (next.some) copy_rows(next, next.values, 1);
     copies_commit();
   }
 
@@ -442,7 +489,7 @@ struct QuantWarp {
       for (int x = 0; x < kGroups; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          shared_words(k[x][y], read + key_at(16 * x + 8 * y + g, 4 * j + t));
+          shared_words(k[x][y], read + key_from[j] + (16 * x + 8 * y) * DP);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -459,12 +506,10 @@ struct QuantWarp {
     __syncwarp();  // the slot has been read
     load_values();
     float ck[kMasks], lv[kMasks];
-    bool full = true;
 #pragma unroll
     for (int x = 0; x < kMasks; ++x) {
       ck[x] = a.c * now.sk[x];
-      lv[x] = log2f(now.sv[x]);
-      full &= now.seen[x] == ~0u;
+      lv[x] = __log2f(now.sv[x]);
     }
     // scores, and with the values' scales
     float2 w[kGroups][2][NT];
@@ -482,7 +527,7 @@ struct QuantWarp {
         for (int n = 0; n < NT; ++n) {
           float2 z = mul2(make_float2(s[x][n][2 * y], s[x][n][2 * y + 1]),
                           mul2(q_power[n], make_float2(fk, fk)));
-          if (!full && !(now.seen[x / 2] >> from & 1)) z = make_float2(-INFINITY, -INFINITY);
+          if (!now.full && !(now.seen[x / 2] >> from & 1)) z = make_float2(-INFINITY, -INFINITY);
           s[x][n][2 * y] = z.x;
           s[x][n][2 * y + 1] = z.y;
           const float2 v = add2(z, make_float2(fv, fv));
@@ -536,9 +581,7 @@ struct QuantWarp {
       uint32_t v[4][kWords];
 #pragma unroll
       for (int y = 0; y < 4; ++y)
-        shared_words(v[y], read + value_at(16 * x + 2 * t + (y & 1) + 8 * (y >> 1),
-                                           DP == 128 ? g : g >> 1) +
-                               (DP == 128 ? 0 : (g & 1) * 8));
+        shared_words(v[y], read + value_from[y & 1] + (16 * x + 8 * (y >> 1)) * DP);
 #pragma unroll
       for (int r = 0; r < kWords; ++r)
 #pragma unroll
@@ -752,7 +795,8 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   int flags = count > 0 ? 0 : kEmpty;
   if (count > 0) {
     w.due = spot;
-    w.due_left = count;
+    w.left = count;
+    w.enter_row();
     w.look_up();
     w.load_keys();
     w.load_values();
