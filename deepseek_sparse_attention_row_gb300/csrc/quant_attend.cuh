@@ -12,11 +12,13 @@
 // which is exact; so are queries after a power of two that brings the largest of
 // a row to 2^14.
 //
-// Each (sequence, key/value head) is a row of tiles; the rows lie on one line
-// that is cut into equal shares of CTAs, one on each SM, and those into equal ones
-// of warps. Rows that lie within a warp's share are finished by it; pieces are
-// joined by their log-sum-exps, first within the CTA at its end, then, for rows
-// that pass from CTA to CTA, by a second launch.
+// The tiles of all sequences lie on one line. It is cut into equal shares, one for
+// each team of as many warps as there are key/value heads; the warps of a team go
+// through its share side by side, each with a head of its own, so that what the
+// heads of a token have in common of a line of memory is there once for all (with
+// heads of 80 bytes, a warp after the other, 264 MB were read where 174 would
+// do). Sequences that lie within a share are finished by its warps; of the others
+// each leaves a piece, and a second launch joins those by their log-sum-exps.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -45,12 +47,10 @@ struct QuantAttnArgs {
   float* lse;
   int64_t l_sb, l_sh;
   int32_t bf16;
-  int32_t whole;    // a CTA for each row
+  int32_t warps;    // of the first launch
   int32_t* starts;  // [batch + 1] tiles in front of each sequence
-  int32_t ctas;
-  int32_t* begins;  // [ctas + 1] first unit of each CTA's share
-  float* part_o;    // [2 grid][heads][DP]
-  float* part_lse;  // [2 grid][heads]
+  float* part_o;    // [2 warps][columns][DP]
+  float* part_lse;  // [2 warps][columns]
 };
 
 template <int DP, int NT>
@@ -62,10 +62,8 @@ struct QuantLayout {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = 3 * kQuantTileBytes;
   static constexpr int kPiece = kHeads * DP;  // floats
-  static constexpr int kWarp = kRing + kPiece * 4;
-  static constexpr int kSmem = kWarps * kWarp;
-  static_assert(kPiece * 4 <= kRing, "a tail piece lies over the ring");
-  static_assert(kWarp % 128 == 0, "rows of 128 bytes");
+  static constexpr int kSmem = kWarps * kRing;
+  static_assert(kPiece * 4 <= kRing, "a piece lies over its warp's ring");
 };
 
 // ---- instructions ----------------------------------------------------------
@@ -129,8 +127,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // ---- the line of tiles -----------------------------------------------------
 
-// The line cut into n (up to 1024) equal shares: share i begins at floor(total *
-// i / n), in 32 bits.
+// A line of `total` tiles cut into n shares, in 32 bits (n up to 65535): share i
+// begins at floor(total * i / n). None is empty if n is not above the total.
 struct Shares {
   uint32_t n, whole, rest;
   __device__ __forceinline__ Shares(int32_t total, uint32_t parts)
@@ -138,7 +136,7 @@ struct Shares {
   __device__ __forceinline__ int32_t begin(uint32_t i) const {
     return static_cast<int32_t>(whole * i + rest * i / n);
   }
-  // The last one that begins at or before `unit` of a line of `total` units.
+  // The last one that begins at or before `unit` of the line.
   __device__ __forceinline__ int32_t of(int32_t total, int32_t unit) const {
     const float guess = static_cast<float>(unit) * static_cast<float>(n) / static_cast<float>(total);
     uint32_t i = min(static_cast<uint32_t>(guess), n - 1);
@@ -148,6 +146,14 @@ struct Shares {
   }
 };
 
+// Teams among which a line is cut: of as many warps as there are rows, and with
+// kTeamTiles tiles each where there are that many.
+constexpr int kTeamTiles = 1;
+__device__ __forceinline__ uint32_t quant_teams(const QuantAttnArgs& a, int32_t total) {
+  const int32_t most = max(a.warps / a.rows, 1), useful = max(total / kTeamTiles, 1);
+  return static_cast<uint32_t>(min(most, useful));
+}
+
 __device__ __forceinline__ int32_t quant_length(const QuantAttnArgs& a, int64_t b) {
   const int64_t most = a.pool.max_pages << a.pool.page_log2, n = a.lens[b];
   return static_cast<int32_t>(n < 0 ? 0 : (n < most ? n : most));
@@ -156,7 +162,7 @@ __device__ __forceinline__ int32_t quant_length(const QuantAttnArgs& a, int64_t 
 // A place on the line.
 struct Spot {
   int64_t b;
-  int32_t row, tile, tiles, tokens;
+  int32_t tile, tiles, tokens;
 };
 
 template <int TILE>
@@ -169,8 +175,6 @@ template <int TILE>
 __device__ __forceinline__ void advance(const QuantAttnArgs& a, Spot& s) {
   if (++s.tile < s.tiles) return;
   s.tile = 0;
-  if (++s.row < a.rows) return;
-  s.row = 0;
   do {
     ++s.b;
     enter<TILE>(a, s);
@@ -198,16 +202,24 @@ __device__ __forceinline__ uint16_t* out_row(const QuantAttnArgs& a, int64_t b, 
   return static_cast<uint16_t*>(a.out) + b * a.o_sb + head * a.o_sh;
 }
 
-// Pieces of rows that a warp leaves for the CTA's end: a head piece (its row
-// began before the share) and a tail piece (its row goes on behind it).
-struct PieceInfo {
-  int64_t b[2];
-  int32_t row[2];
-  int32_t flags;
-};
-constexpr int kHasHead = 1, kHasTail = 2, kHeadEnds = 4, kEmpty = 8;
+// A warp's joined output of a head, kDims elements in each lane, `sum` times too
+// large, and its log-sum-exp relative to `top`.
+template <int kDims>
+__device__ __forceinline__ void write_joined(const QuantAttnArgs& a, int64_t b, int32_t head,
+                                             const float (&x)[kDims], float sum, float top) {
+  const int lane = threadIdx.x & 31;
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  if (lane * kDims < a.pool.dim) {
+    uint32_t* to = reinterpret_cast<uint32_t*>(out_row(a, b, head) + lane * kDims);
+#pragma unroll
+    for (int j = 0; j < kDims; j += 2)
+      to[j / 2] = sum == 0.f ? 0u : pack_pair(a, x[j] * f, x[j + 1] * f);
+  }
+  if (lane == 0 && a.lse)
+    a.lse[b * a.l_sb + head * a.l_sh] = (top == -INFINITY ? 0.f : top) + log2f(sum);
+}
 
-// ---- the kernel ------------------------------------------------------------
+// ---- the kernels -----------------------------------------------------------
 
 template <int DP, int NT>
 struct QuantWarp {
@@ -228,7 +240,6 @@ struct QuantWarp {
     bool full;            // all keys are seen
     int32_t page[kGroups];  // of 16 keys; -1: none
     int32_t inside;       // its first token's place on its page
-    const uint8_t* values;  // what this lane copies of the row's values, on page 0
     uint32_t seen[kMasks];
     float sk[kMasks], sv[kMasks];  // scales, of key 32 x + lane
   };
@@ -245,7 +256,8 @@ struct QuantWarp {
   Spot due;       // the tile whose keys are loaded next
   int32_t left;   // tiles from it to the share's end
   int32_t page[kGroups];
-  const uint8_t *keys, *values;  // what this lane copies of the due row, on page 0
+  int32_t row;    // this warp's
+  const uint8_t *keys, *values;  // what this lane copies of it, on page 0
   const float *k_scales, *v_scales;
   Tile now, next;
 
@@ -285,12 +297,12 @@ struct QuantWarp {
     if (slot == ring + 3 * kQuantTileBytes) slot = ring;
   }
 
-  // Pointers for the due row.
-  __device__ __forceinline__ void enter_row() {
-    const int32_t head = due.row / a.splits;
-    const int row = lane / kRowLanes, byte = lane % kRowLanes * 16;
-    keys = a.pool.codes[0] + head * a.pool.sh[0] + row * a.pool.st[0] + byte;
-    values = a.pool.codes[1] + head * a.pool.sh[1] + row * a.pool.st[1] + byte;
+  __device__ __forceinline__ void take_row(int32_t r) {
+    row = r;
+    const int32_t head = r / a.splits;
+    const int from = lane / kRowLanes, byte = lane % kRowLanes * 16;
+    keys = a.pool.codes[0] + head * a.pool.sh[0] + from * a.pool.st[0] + byte;
+    values = a.pool.codes[1] + head * a.pool.sh[1] + from * a.pool.st[1] + byte;
     k_scales = a.pool.scales[0] + head;
     v_scales = a.pool.scales[1] + head;
   }
@@ -351,7 +363,6 @@ struct QuantWarp {
     if (next.some) {
       const int32_t t0 = due.tile * kTile, mask = (1 << a.pool.page_log2) - 1;
       next.inside = t0 & mask;
-      next.values = values;
       bool full = t0 + kTile <= due.tokens;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
@@ -375,27 +386,22 @@ struct QuantWarp {
       }
       copy_rows(next, keys, 0);
       if (--left > 0) {
-        const int32_t row = due.row;
-        const int64_t b = due.b;
         advance<kTile>(a, due);
-        if (due.row != row || due.b != b) {
-          enter_row();
-          fetch_queries();
-        }
+        if (due.tile == 0) fetch_queries();
       }
       look_up();
     }
     copies_commit();
   }
   __device__ __forceinline__ void load_values() {
-    if (next.some) copy_rows(next, next.values, 1);
+    if (next.some) copy_rows(next, values, 1);
     copies_commit();
   }
 
-  // Brings the queries of the due tile's row nearer, which begins in two tiles.
+  // Brings the queries of the due sequence nearer, which begins in two tiles.
   __device__ __forceinline__ void fetch_queries() {
     int32_t first;
-    const int32_t heads = row_heads(a, due.row, first);
+    const int32_t heads = row_heads(a, row, first);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = 8 * n + g;
@@ -406,11 +412,11 @@ struct QuantWarp {
     }
   }
 
-  // The queries of a row as the products' right-hand side: column g is a head,
+  // The queries of a sequence as the products' right-hand side: column g is a head,
   // and this lane has the dimensions that it has of a key. Each head is
   // multiplied by a power of two that brings its largest element to 2^14, which
   // fp16 then holds exactly to 2^-38 of it.
-  __device__ __forceinline__ void begin(int64_t b, int32_t row) {
+  __device__ __forceinline__ void begin(int64_t b) {
     int32_t first;
     const int32_t heads = row_heads(a, row, first);
 #pragma unroll
@@ -608,7 +614,7 @@ struct QuantWarp {
     return fmaxf(v, x);
   }
 
-  // The outputs of what this warp has of a row, and its log-sum-exps, in
+  // The outputs of what this warp has of a sequence, and its log-sum-exps, in
   // place: o and m.
   __device__ __forceinline__ void finish() {
 #pragma unroll
@@ -631,7 +637,7 @@ struct QuantWarp {
       }
   }
 
-  __device__ __forceinline__ void store(int64_t b, int32_t row) {
+  __device__ __forceinline__ void store(int64_t b) {
     constexpr int kDims = DP / 8;  // of a lane
     int32_t first;
     const int32_t heads = row_heads(a, row, first);
@@ -656,30 +662,68 @@ struct QuantWarp {
       }
   }
 
-  // To a piece [heads][DP] and its log-sum-exps in shared memory.
+  // To a piece [columns][DP] and its log-sum-exps.
   __device__ __forceinline__ void keep(float* piece, float* lse) {
+    int32_t first;
+    const int32_t heads = row_heads(a, row, first);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int32_t at = 8 * n + 2 * t + h;
-        float2* to = reinterpret_cast<float2*>(piece + at * DP + g * (DP / 8));
+        if (at >= heads) continue;
+        float4* to = reinterpret_cast<float4*>(piece + at * DP + g * (DP / 8));
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) to[i] = make_float2(o[n][i][h], o[n][i][2 + h]);
+        for (int i = 0; i < DP / 32; ++i)
+          to[i] = make_float4(o[n][2 * i][h], o[n][2 * i][2 + h], o[n][2 * i + 1][h],
+                              o[n][2 * i + 1][2 + h]);
         if (g == 0) lse[at] = h ? m[n].y : m[n].x;
       }
   }
+
+  // `count` tiles of the line, from `spot` on. What it has of a sequence in part
+  // goes to `piece(b, whether the sequence begins here)` instead of the output.
+  template <typename F>
+  __device__ __forceinline__ void run(Spot spot, int32_t count, F piece) {
+    due = spot;
+    left = count;
+    look_up();
+    load_keys();
+    load_values();
+    now = next;
+    load_keys();
+    bool began = spot.tile == 0;
+    begin(spot.b);
+    for (int32_t i = 0; i < count; ++i) {
+      tile();
+      const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
+      if (!ends && !last) {
+        ++spot.tile;
+        continue;
+      }
+      finish();
+      if (began && ends)
+        store(spot.b);
+      else
+        piece(began);
+      if (!last) {
+        advance<kTile>(a, spot);
+        begin(spot.b);
+        began = true;
+      }
+    }
+  }
 };
 
-// Where `unit` lies; all lanes of a warp together. sums[i]: tiles in front of
-// chunk i (of `chunk` sequences each).
+// Where `unit` of the line lies; all lanes of a warp together. sums[i]: tiles in
+// front of chunk i (of `chunk` sequences each).
 template <int TILE, int THREADS>
 __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
                                           const int32_t* sums, int64_t chunk) {
   const int lane = threadIdx.x & 31;
   int below = 0;
 #pragma unroll
-  for (int i = 0; i < THREADS; i += 32) below += sums[i + lane] * a.rows <= unit;
+  for (int i = 0; i < THREADS; i += 32) below += sums[i + lane] <= unit;
   below = __reduce_add_sync(~0u, below) - 1;  // the last chunk that begins at or before it
   int32_t before = sums[below];
   for (int64_t b0 = below * chunk;; b0 += 32) {
@@ -693,16 +737,13 @@ __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
       const int32_t y = __shfl_up_sync(~0u, upto, i);
       if (lane >= i) upto += y;
     }
-    const uint32_t past = __ballot_sync(~0u, (before + upto) * a.rows > unit);
+    const uint32_t past = __ballot_sync(~0u, before + upto > unit);
     if (past) {
       const int who = __ffs(past) - 1;
-      const uint32_t in = __shfl_sync(~0u, unit - (before + upto - s.tiles) * a.rows, who);
+      s.tile = __shfl_sync(~0u, unit - (before + upto - s.tiles), who);
       s.b = b0 + who;
       s.tiles = __shfl_sync(~0u, s.tiles, who);
       s.tokens = __shfl_sync(~0u, s.tokens, who);
-      const uint32_t row = in / static_cast<uint32_t>(s.tiles);
-      s.row = static_cast<int32_t>(row);
-      s.tile = static_cast<int32_t>(in - row * s.tiles);
       return s;
     }
     before += __shfl_sync(~0u, upto, 31);
@@ -713,215 +754,112 @@ template <int DP, int NT>
 __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     quant_attend_kernel(const QuantAttnArgs a) {
   using L = QuantLayout<DP, NT>;
-  using Warp = QuantWarp<DP, NT>;
   constexpr int W = L::kWarps;
-  // For each warp a ring and a head piece. Rows of 128 bytes have to begin at
-  // multiples of 128 (with others, copies took twice the sectors).
+  // A ring for each warp. Rows of 128 bytes have to begin at multiples of 128 (with
+  // others, copies took twice the sectors).
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ PieceInfo info[W];
-  __shared__ float piece_lse[W][2][L::kHeads];  // then the pieces' weights
-  __shared__ float chain_lse[W + 1][L::kHeads];
   __shared__ int32_t sums[L::kThreads];
   __shared__ int32_t part[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  launch_followers();
+  const int64_t chunk = (a.batch + L::kThreads - 1) / L::kThreads;
+  const int64_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, a.batch);
+  int32_t mine = 0;
+  for (int64_t b = b0; b < b1; ++b) mine += (quant_length(a, b) + L::kTile - 1) / L::kTile;
+  int32_t upto = mine;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int32_t y = __shfl_up_sync(~0u, upto, i);
+    if (lane >= i) upto += y;
+  }
+  if (lane == 31) part[warp] = upto;
+  __syncthreads();
+  int32_t before = upto - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (i < warp) before += part[i];
+    total += part[i];
+  }
+  sums[threadIdx.x] = before;
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    int32_t at = before;
+    for (int64_t b = b0; b < b1; ++b) {
+      a.starts[b] = at;
+      at += (quant_length(a, b) + L::kTile - 1) / L::kTile;
+    }
+    if (threadIdx.x == 0) a.starts[a.batch] = total;
+  }
+  if (total == 0) return;
+  // Neighbouring warps of a team are on different SMs, so that short lines use
+  // many. With more rows than warps each goes through several.
+  const int32_t self = warp * gridDim.x + blockIdx.x;
+  const Shares shares(total, quant_teams(a, total));
+  const uint32_t team = self / a.rows;
+  if (team >= shares.n) return;
+  const int32_t first = shares.begin(team), count = shares.begin(team + 1) - first;
+  const Spot spot = find_spot<L::kTile, L::kThreads>(a, first, sums, chunk);
+  QuantWarp<DP, NT> w(a, smem_addr(smem) + warp * L::kRing);
+  for (int32_t row = self - team * a.rows; row < a.rows; row += a.warps) {
+    w.take_row(row);
+    w.run(spot, count, [&](bool began) {
+      const int64_t slot = 2ll * self + began;
+      w.keep(a.part_o + slot * L::kPiece, a.part_lse + slot * L::kHeads);
+    });
+  }
+}
 
-  // This warp's share: `count` units from `spot` on.
+// A CTA for each row of few tiles, whose warps share them: nothing is left to be
+// joined by a second launch.
+template <int DP, int NT>
+__global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
+    quant_attend_row_kernel(const QuantAttnArgs a) {
+  using L = QuantLayout<DP, NT>;
+  constexpr int W = L::kWarps, kDims = DP / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float piece_lse[W][L::kHeads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Spot spot{};
-  int32_t count;
-  if (a.whole) {
-    spot.b = blockIdx.x / a.rows;
-    spot.row = static_cast<int32_t>(blockIdx.x - spot.b * a.rows);
-    enter<L::kTile>(a, spot);
-    if (spot.tiles == 0) {
-      int32_t first;
-      const int32_t heads = row_heads(a, spot.row, first);
-      for (int i = threadIdx.x; i < heads * a.pool.dim; i += L::kThreads)
-        out_row(a, spot.b, first + i / a.pool.dim)[i % a.pool.dim] = 0;
-      if (a.lse && threadIdx.x < heads)
-        a.lse[spot.b * a.l_sb + (first + static_cast<int>(threadIdx.x)) * a.l_sh] = -INFINITY;
-      return;
-    }
-    const Shares warps(spot.tiles, W);
-    spot.tile = warps.begin(warp);
-    count = warps.begin(warp + 1) - spot.tile;
-  } else {
-    launch_followers();
-    const int64_t chunk = (a.batch + L::kThreads - 1) / L::kThreads;
-    const int64_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, a.batch);
-    int32_t mine = 0;
-    for (int64_t b = b0; b < b1; ++b) mine += (quant_length(a, b) + L::kTile - 1) / L::kTile;
-    int32_t upto = mine;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-      const int32_t y = __shfl_up_sync(~0u, upto, i);
-      if (lane >= i) upto += y;
-    }
-    if (lane == 31) part[warp] = upto;
-    __syncthreads();
-    int32_t before = upto - mine, total = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if (i < warp) before += part[i];
-      total += part[i];
-    }
-    sums[threadIdx.x] = before;
-    __syncthreads();
-    const int32_t units = total * a.rows;
-    const Shares ctas(units, a.ctas);
-    const int32_t u0 = ctas.begin(blockIdx.x);
-    const Shares warps(ctas.begin(blockIdx.x + 1) - u0, W);
-    const int32_t first = warps.begin(warp);
-    count = warps.begin(warp + 1) - first;
-    if (count > 0) spot = find_spot<L::kTile, L::kThreads>(a, u0 + first, sums, chunk);
-    if (threadIdx.x == 0) {
-      a.begins[blockIdx.x] = u0;
-      if (blockIdx.x + 1 == a.ctas) a.begins[a.ctas] = units;
-    }
-    if (blockIdx.x == 0) {
-      int32_t at = before;
-      for (int64_t b = b0; b < b1; ++b) {
-        a.starts[b] = at;
-        at += (quant_length(a, b) + L::kTile - 1) / L::kTile;
-      }
-      if (threadIdx.x == 0) a.starts[a.batch] = total;
-    }
+  spot.b = blockIdx.x / a.rows;
+  const int32_t row = static_cast<int32_t>(blockIdx.x - spot.b * a.rows);
+  enter<L::kTile>(a, spot);
+  int32_t first;
+  const int32_t heads = row_heads(a, row, first);
+  const uint32_t used = min(spot.tiles, W);
+  if (warp < used) {
+    const Shares shares(spot.tiles, used);
+    spot.tile = shares.begin(warp);
+    QuantWarp<DP, NT> w(a, smem_addr(smem) + warp * L::kRing);
+    w.take_row(row);
+    w.run(spot, shares.begin(warp + 1) - spot.tile, [&](bool) {
+      __syncwarp();  // the ring has been read
+      w.keep(reinterpret_cast<float*>(smem + warp * L::kRing), piece_lse[warp]);
+    });
+    if (used == 1) return;  // has stored them
   }
-
-  Warp w(a, smem_addr(smem) + warp * L::kWarp);
-  // a head piece lies behind its warp's ring, a tail piece over it
-  const auto piece = [&](int i, bool tail) {
-    return reinterpret_cast<float*>(smem + i * L::kWarp + (tail ? 0 : L::kRing));
-  };
-  int flags = count > 0 ? 0 : kEmpty;
-  if (count > 0) {
-    w.due = spot;
-    w.left = count;
-    w.enter_row();
-    w.look_up();
-    w.load_keys();
-    w.load_values();
-    w.now = w.next;
-    w.load_keys();
-    bool began = spot.tile == 0;  // the row begins in this share
-    w.begin(spot.b, spot.row);
-    for (int32_t i = 0; i < count; ++i) {
-      w.tile();
-      const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
-      if (ends || last) {
-        w.finish();
-        if (began && ends) {
-          w.store(spot.b, spot.row);
-        } else {
-          const int tail = began ? 1 : 0;
-          __syncwarp();  // the ring has been read
-          w.keep(piece(warp, tail), piece_lse[warp][tail]);
-          if (lane == 0) {
-            info[warp].b[tail] = spot.b;
-            info[warp].row[tail] = spot.row;
-          }
-          flags |= tail ? kHasTail : kHasHead | (ends ? kHeadEnds : 0);
-        }
-        if (!last) {
-          advance<L::kTile>(a, spot);
-          w.begin(spot.b, spot.row);
-          began = true;
-        }
-      } else {
-        ++spot.tile;
-      }
-    }
-  }
-  if (lane == 0) info[warp].flags = flags;
+  if (used == 1) return;
   __syncthreads();
-
-  // Chains of pieces of one row. Chain 0: the head pieces at the CTA's begin, of
-  // a row that began in another CTA; chain i + 1: warp i's tail piece and the
-  // head pieces behind it.
-  const int kinds = lane < W ? info[lane].flags : kEmpty;
-  const uint32_t empty = __ballot_sync(~0u, kinds & kEmpty);
-  const uint32_t head_ends = __ballot_sync(~0u, kinds & kHeadEnds);
-  const uint32_t heads_at = __ballot_sync(~0u, kinds & kHasHead);
-  const uint32_t tails = __ballot_sync(~0u, kinds & kHasTail);
-  const int front = __ffs(~empty) - 1;  // 0 to W
-  const uint32_t chains = (tails << 1) | (heads_at >> front & 1);
-  // warps [from, to) have pieces of chain c, but for empty ones
-  const auto from_of = [&](int c) { return c == 0 ? front : c - 1; };
-  const auto to_of = [&](int c, bool& ends) {
-    const uint32_t past = c == 0 ? head_ends & (~0u << front) : head_ends & (~0u << c);
-    ends = past != 0;
-    return past ? __ffs(past) : W;
-  };
-  for (int i = threadIdx.x; i < (W + 1) * L::kHeads; i += L::kThreads) {
-    const int c = i / L::kHeads, h = i % L::kHeads;
-    if (!(chains >> c & 1)) continue;
-    bool ends;
-    const int from = from_of(c), to = to_of(c, ends);
-    const uint32_t pieces = ((1u << to) - (1u << from)) & ~empty;
-    float z[W], top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      z[j] = pieces >> j & 1 ? piece_lse[j][j == c - 1][h] : -INFINITY;
-      top = fmaxf(top, z[j]);
-    }
+  for (int h = warp; h < heads; h += W) {
+    float top = -INFINITY, sum = 0.f, x[kDims] = {};
+    for (int i = 0; i < used; ++i) top = fmaxf(top, piece_lse[i][h]);
     const float base = top == -INFINITY ? 0.f : top;
+    for (int i = 0; i < used; ++i) {
+      const float f = ex2(piece_lse[i][h] - base);
+      const float* y = reinterpret_cast<const float*>(smem + i * L::kRing) + h * DP + lane * kDims;
+      sum += f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      z[j] = ex2(z[j] - base);
-      sum += z[j];
+      for (int j = 0; j < kDims; ++j) x[j] += f * y[j];
     }
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      if (pieces >> j & 1) piece_lse[j][j == c - 1][h] = z[j] * f;
-    chain_lse[c][h] = base + log2f(sum);
-  }
-  __syncthreads();
-  constexpr int kDims = DP / 32;
-  int turn = 0;
-  for (uint32_t left = chains; left; left &= left - 1) {
-    const int c = __ffs(left) - 1;
-    bool ends;
-    const int from = from_of(c), to = to_of(c, ends), kind = c == 0 ? 0 : 1;
-    const uint32_t pieces = ((1u << to) - (1u << from)) & ~empty;
-    const int64_t b = info[from].b[kind];
-    int32_t first;
-    const int32_t heads = row_heads(a, info[from].row[kind], first);
-    for (int h = 0; h < heads; ++h) {
-      if (turn++ % W != warp) continue;
-      float x[kDims] = {};
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        if (!(pieces >> j & 1)) continue;
-        const float f = piece_lse[j][j == c - 1][h];
-        const float* y = piece(j, j == c - 1) + h * DP + lane * kDims;
-#pragma unroll
-        for (int i = 0; i < kDims; ++i) x[i] += f * y[i];
-      }
-      if (c > 0 && ends) {
-        uint16_t* to_row = out_row(a, b, first + h) + lane * kDims;
-        if (lane * kDims < a.pool.dim) {
-#pragma unroll
-          for (int i = 0; i < kDims; i += 2)
-            *reinterpret_cast<uint32_t*>(to_row + i) = pack_pair(a, x[i], x[i + 1]);
-        }
-        if (lane == 0 && a.lse) a.lse[b * a.l_sb + (first + h) * a.l_sh] = chain_lse[c][h];
-      } else {
-        const int64_t slot = (2ll * blockIdx.x + kind) * L::kHeads + h;
-        float* to_part = a.part_o + slot * DP + lane * kDims;
-#pragma unroll
-        for (int i = 0; i < kDims; ++i) to_part[i] = x[i];
-        if (lane == 0) a.part_lse[slot] = chain_lse[c][h];
-      }
-    }
+    write_joined<kDims>(a, spot.b, first + h, x, sum, top);
   }
 }
 
 constexpr int kQuantJoinWarps = 8;
 constexpr int kQuantJoinThreads = 32 * kQuantJoinWarps;
 
-// Joins what the CTAs of the first launch left of rows that lie in several of
-// them, and writes those without tiles: TEAM warps for each query head. Loads of
-// pieces do not wait for one another.
+// Joins what the first launch left of sequences that lie in several shares, and
+// writes those without tiles: TEAM warps for each query head. Loads of pieces do
+// not wait for one another.
 template <int DP, int NT, int TEAM>
 __global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const QuantAttnArgs a) {
   constexpr int kHeads = 8 * NT, kDims = DP / 32, kAtOnce = 4;
@@ -937,19 +875,17 @@ __global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const Qua
   const int32_t row = kv * a.splits + in / a.split_heads, h = in % a.split_heads;
   follow();
   if (b >= a.batch) return;  // (only where a team is a warp)
-  const int32_t start = a.starts[b], tiles = a.starts[b + 1] - start;
-  const int32_t units = a.starts[a.batch] * a.rows;
-  // the first and the last CTA that have some of the row
-  int32_t c0 = 0, c1 = -1;
+  const int32_t start = a.starts[b], tiles = a.starts[b + 1] - start, total = a.starts[a.batch];
+  // the first and the last share that have some of the sequence
+  int32_t s0 = 0, s1 = -1;
   if (tiles > 0) {
-    const Shares shares(units, a.ctas);
-    const int32_t u0 = start * a.rows + row * tiles;
-    c0 = shares.of(units, u0);
-    c1 = shares.of(units, u0 + tiles - 1);
-    if (c0 == c1) return;
+    const Shares shares(total, quant_teams(a, total));
+    s0 = shares.of(total, start);
+    s1 = shares.of(total, start + tiles - 1);
+    if (s0 == s1) return;
   }
   float top = -INFINITY, sum = 0.f, x[kDims] = {};
-  for (int32_t c = c0 + mate; c <= c1; c += TEAM * kAtOnce) {
+  for (int32_t s = s0 + mate; s <= s1; s += TEAM * kAtOnce) {
     float lse[kAtOnce], y[kAtOnce][kDims];
     float most = top;
 #pragma unroll
@@ -957,11 +893,10 @@ __global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const Qua
       lse[i] = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kDims; ++j) y[i][j] = 0.f;
-      const int32_t at = c + i * TEAM;
-      // some have no share, and have left nothing
-      if (at <= c1 && a.begins[at] < a.begins[at + 1]) {
-        // slot 1 of the first CTA, slot 0 of the others
-        const int64_t slot = static_cast<int64_t>(2 * at + (at == c0)) * kHeads + h;
+      const int32_t at = s + i * TEAM;
+      if (at <= s1) {
+        // the first one's piece is where the sequence begins
+        const int64_t slot = (2ll * (at * a.rows + row) + (at == s0)) * kHeads + h;
         lse[i] = a.part_lse[slot];
         const float* from = a.part_o + slot * DP + lane * kDims;
 #pragma unroll
@@ -1005,15 +940,7 @@ __global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const Qua
       for (int j = 0; j < kDims; ++j) x[j] += f * shared_o[i][lane * kDims + j];
     }
   }
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
-  if (lane * kDims < a.pool.dim) {
-    uint32_t* to = reinterpret_cast<uint32_t*>(out_row(a, b, head) + lane * kDims);
-#pragma unroll
-    for (int j = 0; j < kDims; j += 2)
-      to[j / 2] = sum == 0.f ? 0u : pack_pair(a, x[j] * f, x[j + 1] * f);
-  }
-  if (lane == 0 && a.lse)
-    a.lse[b * a.l_sb + head * a.l_sh] = (top == -INFINITY ? 0.f : top) + log2f(sum);
+  write_joined<kDims>(a, b, head, x, sum, top);
 }
 
 }  // namespace dsa

@@ -40,7 +40,7 @@ struct QuantPlan {
   bool whole;
   int64_t grid;
   bool fits;
-  size_t starts, begins, part_o, part_lse, bytes;
+  size_t starts, part_o, part_lse, bytes;
 };
 
 // Units of a call stay within 31 bits with the most parts of a group, 8.
@@ -68,12 +68,11 @@ QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t
   }
   const int64_t warps = p.columns == 1 ? 12 : 8, most = (units + warps - 1) / warps;
   p.grid = most < 1 ? 1 : (most < sms ? most : sms);
-  const size_t slots = 2 * static_cast<size_t>(p.grid) * 8 * p.columns;
+  const size_t columns = 2 * static_cast<size_t>(p.grid) * warps * 8 * p.columns;
   p.starts = 0;
-  p.begins = up256((batch + 1) * 4);
-  p.part_o = p.begins + up256((p.grid + 1) * 4);
-  p.part_lse = p.part_o + up256(slots * p.dp * 4);
-  p.bytes = p.part_lse + up256(slots * 4);
+  p.part_o = up256((batch + 1) * 4);
+  p.part_lse = p.part_o + up256(columns * p.dp * 4);
+  p.bytes = p.part_lse + up256(columns * 4);
   return p;
 }
 
@@ -81,24 +80,24 @@ template <int DP, int NT>
 dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t stream) {
   constexpr int kSmem = QuantLayout<DP, NT>::kSmem;
   static_assert(kSmem + 8192 <= 232448, "shared memory of one SM");
-  static std::atomic<bool> ready[64];  // per device
+  static std::atomic<bool> ready[2][64];  // per device
   const int dev = current_device();
   if (dev < 0) return DSA_ECUDA;
-  auto* kernel = quant_attend_kernel<DP, NT>;
-  if (!ready[dev].load(std::memory_order_relaxed)) {
+  auto* kernel = p.whole ? quant_attend_row_kernel<DP, NT> : quant_attend_kernel<DP, NT>;
+  if (!ready[p.whole][dev].load(std::memory_order_relaxed)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
         cudaSuccess)
       return DSA_ECUDA;
-    ready[dev].store(true, std::memory_order_relaxed);
+    ready[p.whole][dev].store(true, std::memory_order_relaxed);
   }
   kernel<<<static_cast<unsigned>(p.grid), QuantLayout<DP, NT>::kThreads, kSmem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
   if (p.whole) return DSA_OK;
-  // Rows that outnumber the CTAs lie in two of them, as a rule, and a warp joins
-  // those; fewer lie in many.
+  // Where rows are cut into five pieces at most, on average, a warp joins them; a
+  // team where there are more.
   const int64_t items = a.batch * a.pool.kv_heads * a.group;
   const bool ok =
-      a.batch * a.rows >= p.grid
+      4 * a.batch * a.rows >= a.warps
           ? launch_after(quant_join_kernel<DP, NT, 1>,
                          dim3(static_cast<unsigned>((items + kQuantJoinWarps - 1) / kQuantJoinWarps)),
                          kQuantJoinThreads, stream, a)
@@ -181,11 +180,9 @@ extern "C" dsa_status dsa_quant_attention(
   a.l_sb = l_sb;
   a.l_sh = l_sh;
   a.bf16 = dtype == DSA_DTYPE_BF16;
-  a.whole = p.whole;
-  a.ctas = static_cast<int32_t>(p.grid);
+  a.warps = static_cast<int32_t>(p.grid) * (p.columns == 1 ? 12 : 8);
   char* ws = static_cast<char*>(workspace);
   a.starts = reinterpret_cast<int32_t*>(ws + p.starts);
-  a.begins = reinterpret_cast<int32_t*>(ws + p.begins);
   a.part_o = reinterpret_cast<float*>(ws + p.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
