@@ -48,7 +48,7 @@ struct QuantAttnArgs {
   int64_t l_sb, l_sh;
   int32_t bf16;
   int32_t warps;    // of the first launch
-  int32_t* starts;  // [batch + 1] tiles in front of each sequence
+  int2* spans;      // [batch] the first and the last share of each sequence
   float* part_o;    // [2 warps][columns][DP]
   float* part_lse;  // [2 warps][columns]
 };
@@ -782,21 +782,21 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   }
   sums[threadIdx.x] = before;
   __syncthreads();
-  if (blockIdx.x == 0) {
-    int32_t at = before;
-    for (int64_t b = b0; b < b1; ++b) {
-      a.starts[b] = at;
-      at += (quant_length(a, b) + L::kTile - 1) / L::kTile;
-    }
-    if (threadIdx.x == 0) a.starts[a.batch] = total;
-  }
-  if (total == 0) return;
   // Neighbouring warps of a team are on different SMs, so that short lines use
   // many. With more rows than warps each goes through several.
   const int32_t self = warp * gridDim.x + blockIdx.x;
   const Shares shares(total, quant_teams(a, total));
+  if (threadIdx.x % gridDim.x == blockIdx.x) {  // this CTA's part of the spans
+    int32_t at = before;
+    for (int64_t b = b0; b < b1; ++b) {
+      const int32_t tiles = (quant_length(a, b) + L::kTile - 1) / L::kTile;
+      a.spans[b] = tiles > 0 ? make_int2(shares.of(total, at), shares.of(total, at + tiles - 1))
+                             : make_int2(0, -1);
+      at += tiles;
+    }
+  }
   const uint32_t team = self / a.rows;
-  if (team >= shares.n) return;
+  if (total == 0 || team >= shares.n) return;
   const int32_t first = shares.begin(team), count = shares.begin(team + 1) - first;
   const Spot spot = find_spot<L::kTile, L::kThreads>(a, first, sums, chunk);
   QuantWarp<DP, NT> w(a, smem_addr(smem) + warp * L::kRing);
@@ -854,20 +854,20 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   }
 }
 
-constexpr int kQuantJoinWarps = 8;
-constexpr int kQuantJoinThreads = 32 * kQuantJoinWarps;
-
 // Joins what the first launch left of sequences that lie in several shares, and
 // writes those without tiles: TEAM warps for each query head. Loads of pieces do
 // not wait for one another.
+template <int TEAM>
+struct JoinShape {
+  static constexpr int kWarps = TEAM < 8 ? 8 : TEAM, kThreads = 32 * kWarps;
+};
 template <int DP, int NT, int TEAM>
-__global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const QuantAttnArgs a) {
-  constexpr int kHeads = 8 * NT, kDims = DP / 32, kAtOnce = 4;
+__global__ void __launch_bounds__(JoinShape<TEAM>::kThreads) quant_join_kernel(const QuantAttnArgs a) {
+  constexpr int kHeads = 8 * NT, kDims = DP / 32, kAtOnce = 8, kWarps = JoinShape<TEAM>::kWarps;
   __shared__ float shared_o[TEAM][DP];
   __shared__ float shared_top[TEAM], shared_sum[TEAM];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mate = warp % TEAM;
-  const int64_t item =
-      static_cast<int64_t>(blockIdx.x) * (kQuantJoinWarps / TEAM) + warp / TEAM;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kWarps / TEAM) + warp / TEAM;
   const int32_t all = a.pool.kv_heads * a.group;
   const int64_t b = item / all;
   const int32_t head = static_cast<int32_t>(item - b * all);
@@ -875,15 +875,9 @@ __global__ void __launch_bounds__(kQuantJoinThreads) quant_join_kernel(const Qua
   const int32_t row = kv * a.splits + in / a.split_heads, h = in % a.split_heads;
   follow();
   if (b >= a.batch) return;  // (only where a team is a warp)
-  const int32_t start = a.starts[b], tiles = a.starts[b + 1] - start, total = a.starts[a.batch];
-  // the first and the last share that have some of the sequence
-  int32_t s0 = 0, s1 = -1;
-  if (tiles > 0) {
-    const Shares shares(total, quant_teams(a, total));
-    s0 = shares.of(total, start);
-    s1 = shares.of(total, start + tiles - 1);
-    if (s0 == s1) return;
-  }
+  const int2 span = a.spans[b];
+  const int32_t s0 = span.x, s1 = span.y;
+  if (s0 == s1) return;
   float top = -INFINITY, sum = 0.f, x[kDims] = {};
   for (int32_t s = s0 + mate; s <= s1; s += TEAM * kAtOnce) {
     float lse[kAtOnce], y[kAtOnce][kDims];

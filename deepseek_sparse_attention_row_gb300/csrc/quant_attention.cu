@@ -40,7 +40,7 @@ struct QuantPlan {
   bool whole;
   int64_t grid;
   bool fits;
-  size_t starts, part_o, part_lse, bytes;
+  size_t spans, part_o, part_lse, bytes;
 };
 
 // Units of a call stay within 31 bits with the most parts of a group, 8.
@@ -69,11 +69,19 @@ QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t
   const int64_t warps = p.columns == 1 ? 12 : 8, most = (units + warps - 1) / warps;
   p.grid = most < 1 ? 1 : (most < sms ? most : sms);
   const size_t columns = 2 * static_cast<size_t>(p.grid) * warps * 8 * p.columns;
-  p.starts = 0;
-  p.part_o = up256((batch + 1) * 4);
+  p.spans = 0;
+  p.part_o = up256(batch * sizeof(int2));
   p.part_lse = p.part_o + up256(columns * p.dp * 4);
   p.bytes = p.part_lse + up256(columns * 4);
   return p;
+}
+
+template <int DP, int NT, int TEAM>
+bool launch_join(const QuantAttnArgs& a, cudaStream_t stream) {
+  const int64_t items = a.batch * a.pool.kv_heads * a.group, each = JoinShape<TEAM>::kWarps / TEAM;
+  return launch_after(quant_join_kernel<DP, NT, TEAM>,
+                      dim3(static_cast<unsigned>((items + each - 1) / each)),
+                      JoinShape<TEAM>::kThreads, stream, a);
 }
 
 template <int DP, int NT>
@@ -93,16 +101,12 @@ dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t strea
   kernel<<<static_cast<unsigned>(p.grid), QuantLayout<DP, NT>::kThreads, kSmem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
   if (p.whole) return DSA_OK;
-  // Where rows are cut into five pieces at most, on average, a warp joins them; a
-  // team where there are more.
-  const int64_t items = a.batch * a.pool.kv_heads * a.group;
-  const bool ok =
-      4 * a.batch * a.rows >= a.warps
-          ? launch_after(quant_join_kernel<DP, NT, 1>,
-                         dim3(static_cast<unsigned>((items + kQuantJoinWarps - 1) / kQuantJoinWarps)),
-                         kQuantJoinThreads, stream, a)
-          : launch_after(quant_join_kernel<DP, NT, kQuantJoinWarps>,
-                         dim3(static_cast<unsigned>(items)), kQuantJoinThreads, stream, a);
+  // A warp has eight pieces of a row under way at once, so that it joins rows of
+  // about as many; where there are more, 8 or 32 warps do.
+  const int64_t rows = a.batch * a.rows;
+  const bool ok = 8 * rows >= a.warps    ? launch_join<DP, NT, 1>(a, stream)
+                  : 64 * rows >= a.warps ? launch_join<DP, NT, 8>(a, stream)
+                                         : launch_join<DP, NT, 32>(a, stream);
   return ok ? DSA_OK : DSA_ECUDA;
 }
 
@@ -182,7 +186,7 @@ extern "C" dsa_status dsa_quant_attention(
   a.bf16 = dtype == DSA_DTYPE_BF16;
   a.warps = static_cast<int32_t>(p.grid) * (p.columns == 1 ? 12 : 8);
   char* ws = static_cast<char*>(workspace);
-  a.starts = reinterpret_cast<int32_t*>(ws + p.starts);
+  a.spans = reinterpret_cast<int2*>(ws + p.spans);
   a.part_o = reinterpret_cast<float*>(ws + p.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
