@@ -24,16 +24,19 @@ __device__ __forceinline__ int64_t clamped(int32_t x, int64_t most) {
   return x < 0 ? 0 : (x < most ? x : most);
 }
 
-// The last of n + 1 nondecreasing marks that is not above `x`, if mark 0 is not.
+// The last of the first n of nondecreasing marks that is not above `x` (0 if all
+// are), by a warp: each step reads 32 of them at once.
 template <typename F>
 __device__ __forceinline__ int32_t last_upto(int32_t n, int64_t x, F mark) {
-  int32_t lo = 0, hi = n;  // mark(lo) <= x, hi: beyond
-  while (hi - lo > 1) {
-    const int32_t mid = lo + (hi - lo) / 2;
-    if (mark(mid) <= x)
-      lo = mid;
-    else
-      hi = mid;
+  const int lane = threadIdx.x & 31;
+  int32_t lo = 0;  // what is sought is in [lo, lo + n)
+  while (n > 1) {
+    const int32_t step = (n + 31) / 32, at = lane * step;
+    const uint32_t upto = __ballot_sync(~0u, at < n && mark(lo + at) <= x);
+    // marks may decrease against the rules: the first ones that hold count
+    const int32_t held = max(__ffs(~upto) - 2, upto == ~0u ? 31 : 0);
+    lo += held * step;
+    n = min(step, n - held * step);
   }
   return lo;
 }
@@ -89,63 +92,96 @@ __device__ __forceinline__ Block find_block(const WriteArgs& a, int64_t item) {
   return b;
 }
 
-constexpr int kWriteWarps = 4;
+constexpr int kWriteWarps = 8;
+constexpr int kAtOnce = 8;  // 16-byte loads of a lane
 
-// A warp for each block, head and one of keys and values.
+// A team of `team` warps (a power of two, up to 16) for each block, head and one of
+// keys and values; the teams of a CTA share the block. Where a block's new tokens
+// are no more than a team has registers for, they are read once.
 template <typename T>
-__global__ void __launch_bounds__(kWriteWarps * 32) write_kernel(const WriteArgs a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(512) write_kernel(const WriteArgs a, int team) {
+  __shared__ uint32_t tops[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const Block b = find_block(a, blockIdx.x);
   if (b.page < 0) return;
   const int parts = a.pool.dim / 8, rows = 32 / parts;  // 8 elements of a lane
-  const int row = lane / parts, part = lane % parts;
-  for (int w = warp + kWriteWarps * blockIdx.y; w < 2 * a.pool.kv_heads;
-       w += kWriteWarps * gridDim.y) {
-    const int kv = w & 1, head = w >> 1;
-    const char* x = static_cast<const char*>(a.x[kv]) + head * a.xh[kv] * sizeof(T) + part * 16;
-    const auto load = [&](int32_t t) {
-      return *reinterpret_cast<const uint4*>(
-          x + (b.row + t - b.from) * a.xt[kv] * static_cast<int64_t>(sizeof(T)));
+  const int row = lane / parts, part = lane - row * parts;
+  const int mate = warp & (team - 1), each = warps / team;  // teams of a CTA
+  const int step = team * rows;                             // rows of a team at a time
+  const int from = row < rows ? mate * rows + row : 1 << 20;  // idle lanes: behind every row
+  const int count = b.to - b.from;
+  for (int w0 = blockIdx.y * each; w0 < 2 * a.pool.kv_heads; w0 += gridDim.y * each) {
+    const int w = w0 + warp / team;
+    const bool mine = w < 2 * a.pool.kv_heads;
+    const int kv = w & 1, head = mine ? w >> 1 : 0;
+    const char* x = static_cast<const char*>(a.x[kv]) +
+                    (b.row * a.xt[kv] + head * a.xh[kv]) * static_cast<int64_t>(sizeof(T)) +
+                    part * 16;
+    const int64_t x_step = a.xt[kv] * static_cast<int64_t>(sizeof(T));
+    uint4 u[kAtOnce];
+    const auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int at = i0 + from + i * step;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (mine && at < count) u[i] = *reinterpret_cast<const uint4*>(x + at * x_step);
+      }
     };
     float top = 0.f;
-    for (int32_t t = b.from + row; t < b.to && row < rows; t += rows) {
-      const uint4 u = load(t);
-      for (uint32_t two : {u.x, u.y, u.z, u.w}) {
-        const float2 f = pair<T>(two);
-        top = fmaxf(top, fmaxf(finite_size(f.x), finite_size(f.y)));
-      }
-    }
-    top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-    uint32_t e = need_exponent(top);
-    float* scale = quant_scale(a.pool, kv, b.page, b.start, head);
-    if (b.from > b.start) {
-      const float was = *scale;
-      e = max(e, held_exponent(was));
-      __syncwarp();
-      if (power(e) != was) {
-        for (int32_t t = b.start + row; t < b.from && row < rows; t += rows) {
-          uint2* at = reinterpret_cast<uint2*>(quant_code(a.pool, kv, b.page, t, head) + part * 8);
-          const uint2 u = *at;
-          const auto again = [&](uint32_t four) {
-            const float i = inverse_power(e);
-            const float2 lo = decode2f(four & 0xffffu), hi = decode2f(four >> 16);
-            return encode2(lo.x * was * i, lo.y * was * i) |
-                   (encode2(hi.x * was * i, hi.y * was * i) << 16);
-          };
-          *at = make_uint2(again(u.x), again(u.y));
+    for (int i0 = 0; i0 < count; i0 += kAtOnce * step) {
+      load(i0);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        for (uint32_t two : {u[i].x, u[i].y, u[i].z, u[i].w}) {
+          const float2 f = pair<T>(two);
+          top = fmaxf(top, fmaxf(finite_size(f.x), finite_size(f.y)));
         }
+    }
+    uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
+    float* scale = quant_scale(a.pool, kv, b.page, b.start, head);
+    const float was = mine && b.from > b.start ? *scale : 0.f;
+    if (team > 1) {
+      if (lane == 0) tops[warp] = most;
+      __syncthreads();  // and the scale has been read
+      for (int i = 0; i < team; ++i) most = max(most, tops[(warp & ~(team - 1)) + i]);
+      __syncthreads();
+    } else {
+      __syncwarp();
+    }
+    if (!mine) continue;
+    uint32_t e = need_exponent(__uint_as_float(most));
+    if (b.from > b.start) e = max(e, held_exponent(was));
+    if (mate == 0 && lane == 0) *scale = power(e);
+    const float i1 = inverse_power(e);
+    uint8_t* codes = quant_code(a.pool, kv, b.page, b.start, head) + part * 8;
+    const int64_t c_step = a.pool.st[kv];
+    if (b.from > b.start && power(e) != was) {
+      for (int at = from; at < b.from - b.start; at += step) {
+        uint2* to = reinterpret_cast<uint2*>(codes + at * c_step);
+        const uint2 v = *to;
+        const auto again = [&](uint32_t four) {
+          const float2 lo = decode2f(four & 0xffffu), hi = decode2f(four >> 16);
+          return encode2(lo.x * was * i1, lo.y * was * i1) |
+                 (encode2(hi.x * was * i1, hi.y * was * i1) << 16);
+        };
+        *to = make_uint2(again(v.x), again(v.y));
       }
     }
-    if (lane == 0) *scale = power(e);
-    const float i = inverse_power(e);
-    for (int32_t t = b.from + row; t < b.to && row < rows; t += rows) {
-      const uint4 u = load(t);
-      const auto code = [&](uint32_t two) {
-        const float2 f = pair<T>(two);
-        return encode2(nan_for_infinite(f.x) * i, nan_for_infinite(f.y) * i);
-      };
-      *reinterpret_cast<uint2*>(quant_code(a.pool, kv, b.page, t, head) + part * 8) =
-          make_uint2(code(u.x) | (code(u.y) << 16), code(u.z) | (code(u.w) << 16));
+    codes += (b.from - b.start) * c_step;
+    for (int i0 = 0; i0 < count; i0 += kAtOnce * step) {
+      if (count > kAtOnce * step) load(i0);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int at = i0 + from + i * step;
+        const auto code = [&](uint32_t two) {
+          const float2 f = pair<T>(two);
+          return encode2(nan_for_infinite(f.x) * i1, nan_for_infinite(f.y) * i1);
+        };
+        if (at < count)
+          *reinterpret_cast<uint2*>(codes + at * c_step) =
+              make_uint2(code(u[i].x) | (code(u[i].y) << 16),
+                         code(u[i].z) | (code(u[i].w) << 16));
+      }
     }
   }
 }
@@ -172,37 +208,71 @@ __device__ __forceinline__ uint32_t pack<__half>(float2 f) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-constexpr int kReadThreads = 256;
+constexpr int kReadWarps = 4;
+constexpr int kReadRows = 8;  // of a warp
 
-// A CTA for each row; a thread for 16 codes.
-template <typename T>
-__global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
-  const int64_t r = blockIdx.x;
-  const int32_t s = last_upto(a.seqs, r, [&](int32_t i) { return clamped(a.cu[i], a.total); });
-  const int64_t r0 = clamped(a.cu[s], a.total), r1 = clamped(a.cu[s + 1], a.total);
-  if (r < r0 || r >= r1) return;
-  const int64_t t = r - r0;
-  const int32_t page = t < (a.pool.max_pages << a.pool.page_log2)
-                           ? quant_page(a.pool, s, static_cast<int32_t>(t))
-                           : -1;
-  const int parts = a.pool.dim / 16;
-  for (int u = threadIdx.x; u < 2 * a.pool.kv_heads * parts; u += kReadThreads) {
-    const int part = u % parts, kv = u / parts & 1, head = u / parts >> 1;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
-    if (page >= 0) {
-      c = *reinterpret_cast<const uint4*>(
-          quant_code(a.pool, kv, page, static_cast<int32_t>(t), head) + part * 16);
-      scale = *quant_scale(a.pool, kv, page, static_cast<int32_t>(t), head);
+// A warp for eight rows: lane i finds row i's page, and then 16 codes at a time are
+// dealt to the lanes over all of them. WIDE: 32 bytes of an output at once.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 =
+      (static_cast<int64_t>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5)) * kReadRows;
+  if (r0 >= a.total) return;
+  int32_t s = last_upto(a.seqs, r0, [&](int32_t i) { return clamped(a.cu[i], a.total); });
+  // -2: a row of no sequence, -1: no page
+  int32_t page = -2, tok = 0;
+  const int64_t r = r0 + lane;
+  if (lane < kReadRows && r < a.total) {
+    while (s + 1 < a.seqs && r >= clamped(a.cu[s + 1], a.total)) ++s;
+    const int64_t c0 = clamped(a.cu[s], a.total), c1 = clamped(a.cu[s + 1], a.total);
+    if (r >= c0 && r < c1) {
+      tok = static_cast<int32_t>(r - c0);
+      page = tok < (a.pool.max_pages << a.pool.page_log2) ? quant_page(a.pool, s, tok) : -1;
     }
-    uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(a.x[kv]) + r * a.xt[kv] +
-                                         head * a.xh[kv] + part * 16);
-    const auto two = [&](uint32_t codes) {
-      const float2 f = decode2f(codes);
-      return pack<T>(make_float2(f.x * scale, f.y * scale));
-    };
-    to[0] = make_uint4(two(c.x & 0xffff), two(c.x >> 16), two(c.y & 0xffff), two(c.y >> 16));
-    to[1] = make_uint4(two(c.z & 0xffff), two(c.z >> 16), two(c.w & 0xffff), two(c.w >> 16));
+  }
+  const uint32_t parts = a.pool.dim / 16, half = a.pool.kv_heads * parts, units = 2 * half;
+  const uint32_t all = units * kReadRows;
+  constexpr int kUnroll = 4;
+  for (uint32_t e0 = 0; e0 < all; e0 += 32 * kUnroll) {
+    uint4 c[kUnroll];
+    float scale[kUnroll];
+    T* to[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const uint32_t e = e0 + 32 * i + lane, row = min(e / units, kReadRows - 1u);
+      const int32_t p = __shfl_sync(~0u, page, row), t = __shfl_sync(~0u, tok, row);
+      const uint32_t u = e - row * units, kv = u >= half, rest = u - (kv ? half : 0);
+      const int32_t head = rest / parts, part = rest - head * parts;
+      c[i] = make_uint4(0, 0, 0, 0);
+      scale[i] = 0.f;
+      to[i] = nullptr;
+      if (e < all && p >= -1)
+        to[i] = static_cast<T*>(a.x[kv]) + (r0 + row) * a.xt[kv] + head * a.xh[kv] + part * 16;
+      if (e < all && p >= 0) {
+        c[i] = *reinterpret_cast<const uint4*>(quant_code(a.pool, kv, p, t, head) + part * 16);
+        scale[i] = *quant_scale(a.pool, kv, p, t, head);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      if (!to[i]) continue;
+      const auto two = [&](uint32_t codes) {
+        const float2 f = decode2f(codes);
+        return pack<T>(make_float2(f.x * scale[i], f.y * scale[i]));
+      };
+      const uint32_t x[8] = {two(c[i].x & 0xffff), two(c[i].x >> 16), two(c[i].y & 0xffff),
+                             two(c[i].y >> 16),    two(c[i].z & 0xffff), two(c[i].z >> 16),
+                             two(c[i].w & 0xffff), two(c[i].w >> 16)};
+      if constexpr (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to[i]), "r"(x[0]),
+                     "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+      } else {
+        reinterpret_cast<uint4*>(to[i])[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4*>(to[i])[1] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+    }
   }
 }
 
@@ -256,14 +326,19 @@ extern "C" dsa_status dsa_quant_cache_write(
   a.lens = lens;
   const int64_t items = total / block + 2ll * seqs;
   if (items > INT32_MAX) return DSA_EUNSUPPORTED;
-  const unsigned ys = static_cast<unsigned>((2ll * kv_heads + dsa::kWriteWarps - 1) /
-                                            dsa::kWriteWarps);
-  const dim3 grid(static_cast<unsigned>(items), ys < 65535 ? ys : 65535);
+  // A team's registers hold the new tokens that a block gets on average, if few
+  // come to a sequence.
+  const int64_t rows = 32 / (head_dim / 8) * dsa::kAtOnce, mean = (total + seqs - 1) / seqs;
+  int team = 1;
+  while (team < 16 && team * rows < (mean < block ? mean : block)) team *= 2;
+  const int warps = team > dsa::kWriteWarps ? team : dsa::kWriteWarps;
+  const int64_t ys = (2ll * kv_heads + warps / team - 1) / (warps / team);
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(ys < 65535 ? ys : 65535));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == DSA_DTYPE_BF16)
-    dsa::write_kernel<__nv_bfloat16><<<grid, dsa::kWriteWarps * 32, 0, s>>>(a);
+    dsa::write_kernel<__nv_bfloat16><<<grid, warps * 32, 0, s>>>(a, team);
   else
-    dsa::write_kernel<__half><<<grid, dsa::kWriteWarps * 32, 0, s>>>(a);
+    dsa::write_kernel<__half><<<grid, warps * 32, 0, s>>>(a, team);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
@@ -292,11 +367,15 @@ extern "C" dsa_status dsa_quant_cache_read(
   a.total = total;
   a.cu = cu;
   a.seqs = seqs;
-  const unsigned grid = static_cast<unsigned>(total);
+  constexpr int64_t kRows = dsa::kReadWarps * dsa::kReadRows;
+  const unsigned grid = static_cast<unsigned>((total + kRows - 1) / kRows);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == DSA_DTYPE_BF16)
-    dsa::read_kernel<__nv_bfloat16><<<grid, dsa::kReadThreads, 0, s>>>(a);
-  else
-    dsa::read_kernel<__half><<<grid, dsa::kReadThreads, 0, s>>>(a);
+  const bool wide = (k_st | k_sh | v_st | v_sh) % 16 == 0 &&
+                    ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
+  auto* kernel =
+      dtype == DSA_DTYPE_BF16
+          ? (wide ? dsa::read_kernel<__nv_bfloat16, true> : dsa::read_kernel<__nv_bfloat16, false>)
+          : (wide ? dsa::read_kernel<__half, true> : dsa::read_kernel<__half, false>);
+  kernel<<<grid, dsa::kReadWarps * 32, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }

@@ -24,12 +24,12 @@ struct RotaryArgs {
   void *q_out, *k_out;
   int64_t q_st, q_sh, qo_st, qo_sh, k_st, k_sh, ko_st, ko_sh;
   int32_t heads, all_heads;  // all_heads counts those of k too
-  int64_t tokens;
+  uint32_t tokens;
   const int32_t* positions;
   const int64_t* turns;
   int32_t pairs;
-  int32_t turned, chunks;  // chunks of a head: those of the pairs, and all
-  int32_t lanes;           // threads that share a token's chunk
+  int32_t turned;          // chunks of a head: those of the pairs,
+  uint32_t chunks, lanes;  // all, and threads that share a token's chunk
   float factor;
   int32_t transpose;
 };
@@ -69,6 +69,15 @@ __device__ __forceinline__ __half narrow<__half>(float x) {
   return __float2half_rn(x);
 }
 
+// This thread's token, chunk and first head.
+__device__ __forceinline__ bool place(const RotaryArgs& a, uint32_t& t, int& c, int& first) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x, j = i / a.chunks;
+  t = j / a.lanes;
+  c = static_cast<int>(i - j * a.chunks);
+  first = static_cast<int>(j - t * a.lanes);
+  return t < a.tokens;
+}
+
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Vec {
   T x[V];
@@ -80,17 +89,16 @@ template <typename T, int V, bool HALVES>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   constexpr int P = HALVES ? V : V / 2;  // pairs of a chunk
   using Chunk = Vec<T, V>;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int c = static_cast<int>(i % a.chunks);
-  const int64_t j = i / a.chunks;
-  const int first = static_cast<int>(j % a.lanes);
-  const int64_t t = j / a.lanes;
-  if (t >= a.tokens) return;
+  uint32_t t;
+  int c, first;
+  if (!place(a, t, c, first)) return;
   const bool turned = c < a.turned;
   // where the chunk lies, and the other half of its pairs
   const int at = turned ? c * V : 2 * a.pairs + (c - a.turned) * V;
   const int other = HALVES && turned ? a.pairs : 0;
   float2 cs[P];
+#pragma unroll
+  for (int n = 0; n < P; ++n) cs[n] = make_float2(0.f, 0.f);
   if (turned) {
     const int32_t p = a.positions[t];
 #pragma unroll
@@ -100,47 +108,57 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
       cs[n].y *= a.factor;
     }
   }
-#pragma unroll 4
-  for (int h = first; h < a.all_heads; h += a.lanes) {
-    const bool q = h < a.heads;
-    const int g = q ? h : h - a.heads;
-    const T* x = static_cast<const T*>(q ? a.q : a.k) + t * (q ? a.q_st : a.k_st) +
-                 g * (q ? a.q_sh : a.k_sh) + at;
-    T* y = static_cast<T*>(q ? a.q_out : a.k_out) + t * (q ? a.qo_st : a.ko_st) +
-           g * (q ? a.qo_sh : a.ko_sh) + at;
-    Chunk u = *reinterpret_cast<const Chunk*>(x);
-    if (turned) {
-      if constexpr (HALVES) {
-        Chunk w = *reinterpret_cast<const Chunk*>(x + other);
+  const T* q = static_cast<const T*>(a.q) + t * a.q_st + at;
+  const T* k = static_cast<const T*>(a.k) + t * a.k_st + at;
+  T* qo = static_cast<T*>(a.q_out) + t * a.qo_st + at;
+  T* ko = static_cast<T*>(a.k_out) + t * a.ko_st + at;
+  // Outputs may be inputs, so that loads would wait for the stores before them:
+  // those of kAtOnce heads come first.
+  constexpr int kAtOnce = HALVES ? 4 : 8;
+  for (int h0 = first; h0 < a.all_heads; h0 += kAtOnce * a.lanes) {
+    Chunk u[kAtOnce], w[HALVES ? kAtOnce : 1];
 #pragma unroll
-        for (int n = 0; n < V; ++n) {
-          const float xa = widen(u.x[n]), xb = widen(w.x[n]);
-          u.x[n] = narrow<T>(fmaf(xa, cs[n].x, -(xb * cs[n].y)));
-          w.x[n] = narrow<T>(fmaf(xb, cs[n].x, xa * cs[n].y));
-        }
-        *reinterpret_cast<Chunk*>(y + other) = w;
-      } else {
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int h = h0 + i * a.lanes;
+      if (h >= a.all_heads) continue;
+      const T* x = h < a.heads ? q + h * a.q_sh : k + (h - a.heads) * a.k_sh;
+      u[i] = *reinterpret_cast<const Chunk*>(x);
+      if constexpr (HALVES) w[i] = *reinterpret_cast<const Chunk*>(x + other);
+    }
 #pragma unroll
-        for (int n = 0; n < P; ++n) {
-          const float xa = widen(u.x[2 * n]), xb = widen(u.x[2 * n + 1]);
-          u.x[2 * n] = narrow<T>(fmaf(xa, cs[n].x, -(xb * cs[n].y)));
-          u.x[2 * n + 1] = narrow<T>(fmaf(xb, cs[n].x, xa * cs[n].y));
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int h = h0 + i * a.lanes;
+      if (h >= a.all_heads) continue;
+      T* y = h < a.heads ? qo + h * a.qo_sh : ko + (h - a.heads) * a.ko_sh;
+      if (turned) {
+        if constexpr (HALVES) {
+#pragma unroll
+          for (int n = 0; n < V; ++n) {
+            const float xa = widen(u[i].x[n]), xb = widen(w[i].x[n]);
+            u[i].x[n] = narrow<T>(fmaf(xa, cs[n].x, -(xb * cs[n].y)));
+            w[i].x[n] = narrow<T>(fmaf(xb, cs[n].x, xa * cs[n].y));
+          }
+          *reinterpret_cast<Chunk*>(y + other) = w[i];
+        } else {
+#pragma unroll
+          for (int n = 0; n < P; ++n) {
+            const float xa = widen(u[i].x[2 * n]), xb = widen(u[i].x[2 * n + 1]);
+            u[i].x[2 * n] = narrow<T>(fmaf(xa, cs[n].x, -(xb * cs[n].y)));
+            u[i].x[2 * n + 1] = narrow<T>(fmaf(xb, cs[n].x, xa * cs[n].y));
+          }
         }
       }
+      *reinterpret_cast<Chunk*>(y) = u[i];
     }
-    *reinterpret_cast<Chunk*>(y) = u;
   }
 }
 
 // Neighbouring pairs at addresses that hold no pair whole, element by element.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const RotaryArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int c = static_cast<int>(i % a.chunks);
-  const int64_t j = i / a.chunks;
-  const int first = static_cast<int>(j % a.lanes);
-  const int64_t t = j / a.lanes;
-  if (t >= a.tokens) return;
+  uint32_t t;
+  int c, first;
+  if (!place(a, t, c, first)) return;
   const bool turned = c < a.turned;
   const int at = turned ? 2 * c : a.pairs + c;  // behind the pairs: 2 pairs + (c - pairs)
   float2 cs = make_float2(0.f, 0.f);
@@ -174,18 +192,29 @@ dsa_status launch(RotaryArgs a, int32_t head_dim, bool halves, cudaStream_t stre
   const bool pairs = !halves && V == 1;
   a.turned = halves ? a.pairs / V : pairs ? a.pairs : 2 * a.pairs / V;
   a.chunks = a.turned + (head_dim - 2 * a.pairs) / V;
-  const int64_t units = a.tokens * a.chunks, want = (kFull + units - 1) / units;
-  a.lanes = static_cast<int32_t>(want < a.all_heads ? want : a.all_heads);
-  const int64_t ctas = (units * a.lanes + kThreads - 1) / kThreads;
-  if (ctas > INT32_MAX) return DSA_EUNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(ctas);
-  if (halves)
-    rotary_kernel<T, V, true><<<grid, kThreads, 0, stream>>>(a);
-  else if constexpr (V == 1)
-    rotary_pairs_kernel<T><<<grid, kThreads, 0, stream>>>(a);
-  else
-    rotary_kernel<T, V, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
+  const int64_t tokens = a.tokens, units = tokens * a.chunks, want = (kFull + units - 1) / units;
+  a.lanes = static_cast<uint32_t>(want < a.all_heads ? want : a.all_heads);
+  // Threads of a launch are counted in 32 bits.
+  const int64_t most = (INT32_MAX - kThreads) / (static_cast<int64_t>(a.chunks) * a.lanes);
+  for (int64_t done = 0; done < tokens; done += most) {
+    const int64_t now = tokens - done < most ? tokens - done : most;
+    a.tokens = static_cast<uint32_t>(now);
+    const unsigned grid =
+        static_cast<unsigned>((now * a.chunks * a.lanes + kThreads - 1) / kThreads);
+    if (halves)
+      rotary_kernel<T, V, true><<<grid, kThreads, 0, stream>>>(a);
+    else if constexpr (V == 1)
+      rotary_pairs_kernel<T><<<grid, kThreads, 0, stream>>>(a);
+    else
+      rotary_kernel<T, V, false><<<grid, kThreads, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
+    a.q = static_cast<const T*>(a.q) + most * a.q_st;
+    a.k = static_cast<const T*>(a.k) + most * a.k_st;
+    a.q_out = static_cast<T*>(a.q_out) + most * a.qo_st;
+    a.k_out = static_cast<T*>(a.k_out) + most * a.ko_st;
+    a.positions += most;
+  }
+  return DSA_OK;
 }
 
 // The widest chunk of which `bits` (addresses and steps in bytes, or'ed) and
@@ -252,7 +281,7 @@ extern "C" dsa_status dsa_rotary(const void* q, void* q_out, int32_t heads, int6
   a.ko_sh = ko_sh;
   a.heads = heads;
   a.all_heads = static_cast<int32_t>(all);
-  a.tokens = tokens;
+  a.tokens = static_cast<uint32_t>(tokens);
   a.positions = positions;
   a.turns = turns;
   a.pairs = pairs;
