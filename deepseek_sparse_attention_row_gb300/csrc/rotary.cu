@@ -1,10 +1,12 @@
 // rotary.cu -- rotary positions of queries and keys: the C ABI of
 // include/dsa_rotary.h.
 //
-// A thread owns one chunk of pairs of one token and goes through heads with
-// it: the angle is the same for all heads, so that cosines and sines are
-// computed once and stay in registers. Chunks are as wide as alignment lets
-// them be, up to 16 bytes; neighbouring threads take neighbouring chunks.
+// A CTA takes a few tokens: it computes the cosines and sines of their positions
+// once, into shared memory, and then goes through the heads, a chunk of pairs to
+// a thread. Chunks are as wide as alignment lets them be, up to 16 bytes;
+// neighbouring threads take neighbouring chunks. The first loads are on their way
+// while the angles are computed. (With the angles in registers, computed again
+// by every thread, 8192 tokens of 40 heads of 128 took 48 us.)
 #include "../../include/dsa_rotary.h"
 
 #include <cuda_bf16.h>
@@ -24,15 +26,25 @@ struct RotaryArgs {
   void *q_out, *k_out;
   int64_t q_st, q_sh, qo_st, qo_sh, k_st, k_sh, ko_st, ko_sh;
   int32_t heads, all_heads;  // all_heads counts those of k too
-  uint32_t tokens;
+  int64_t tokens;
   const int32_t* positions;
   const int64_t* turns;
   int32_t pairs;
-  int32_t turned;          // chunks of a head: those of the pairs,
-  uint32_t chunks, lanes;  // all, and threads that share a token's chunk
+  int32_t turned, chunks;      // chunks of a head: those of the pairs, and all
+  int32_t step, other;         // from chunk to chunk, and to its second half (SPLIT)
+  int32_t each, part;          // tokens of a CTA, and heads
+  uint32_t by_chunks, by_part;  // ceil(2^32 / chunks) and / part, 0 for 1
   float factor;
   int32_t transpose;
 };
+
+// n / d for by = ceil(2^32 / d): exact while n * d is below 2^32.
+__device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t by) {
+  return by ? __umulhi(n, by) : n;
+}
+uint32_t reciprocal(uint32_t d) {
+  return d == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + d - 1) / d);
+}
 
 // cos and sin of the angle of position p. The fraction of a turn is exact;
 // what is left after the nearest quarter turn, at most an eighth, is rounded
@@ -69,152 +81,139 @@ __device__ __forceinline__ __half narrow<__half>(float x) {
   return __float2half_rn(x);
 }
 
-// This thread's token, chunk and first head.
-__device__ __forceinline__ bool place(const RotaryArgs& a, uint32_t& t, int& c, int& first) {
-  const uint32_t i = blockIdx.x * kThreads + threadIdx.x, j = i / a.chunks;
-  t = j / a.lanes;
-  c = static_cast<int>(i - j * a.chunks);
-  first = static_cast<int>(j - t * a.lanes);
-  return t < a.tokens;
-}
-
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Vec {
   T x[V];
 };
 
-// V elements of T at a time. HALVES: a chunk is V pairs (V elements from each
-// half); otherwise it is V / 2 neighbouring pairs.
-template <typename T, int V, bool HALVES>
+// V elements of T at a time. SPLIT: a chunk is V pairs, whose first and second
+// elements lie apart; otherwise it is V / 2 pairs of neighbours.
+template <typename T, int V, bool SPLIT>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
-  constexpr int P = HALVES ? V : V / 2;  // pairs of a chunk
+  constexpr int P = SPLIT ? V : V / 2;  // pairs of a chunk
+  constexpr int kAtOnce = SPLIT ? 2 : 4;
   using Chunk = Vec<T, V>;
-  uint32_t t;
-  int c, first;
-  if (!place(a, t, c, first)) return;
-  const bool turned = c < a.turned;
-  // where the chunk lies, and the other half of its pairs
-  const int at = turned ? c * V : 2 * a.pairs + (c - a.turned) * V;
-  const int other = HALVES && turned ? a.pairs : 0;
-  float2 cs[P];
-#pragma unroll
-  for (int n = 0; n < P; ++n) cs[n] = make_float2(0.f, 0.f);
-  if (turned) {
-    const int32_t p = a.positions[t];
-#pragma unroll
-    for (int n = 0; n < P; ++n) {
-      cs[n] = cos_sin(p, a.turns[c * P + n], a.transpose);
-      cs[n].x *= a.factor;
-      cs[n].y *= a.factor;
-    }
-  }
-  const T* q = static_cast<const T*>(a.q) + t * a.q_st + at;
-  const T* k = static_cast<const T*>(a.k) + t * a.k_st + at;
-  T* qo = static_cast<T*>(a.q_out) + t * a.qo_st + at;
-  T* ko = static_cast<T*>(a.k_out) + t * a.ko_st + at;
-  // Outputs may be inputs, so that loads would wait for the stores before them:
-  // those of kAtOnce heads come first.
-  constexpr int kAtOnce = HALVES ? 4 : 8;
-  for (int h0 = first; h0 < a.all_heads; h0 += kAtOnce * a.lanes) {
-    Chunk u[kAtOnce], w[HALVES ? kAtOnce : 1];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int h = h0 + i * a.lanes;
-      if (h >= a.all_heads) continue;
-      const T* x = h < a.heads ? q + h * a.q_sh : k + (h - a.heads) * a.k_sh;
-      u[i] = *reinterpret_cast<const Chunk*>(x);
-      if constexpr (HALVES) w[i] = *reinterpret_cast<const Chunk*>(x + other);
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int h = h0 + i * a.lanes;
-      if (h >= a.all_heads) continue;
-      T* y = h < a.heads ? qo + h * a.qo_sh : ko + (h - a.heads) * a.ko_sh;
-      if (turned) {
-        if constexpr (HALVES) {
-#pragma unroll
-          for (int n = 0; n < V; ++n) {
-            const float xa = widen(u[i].x[n]), xb = widen(w[i].x[n]);
-            u[i].x[n] = narrow<T>(fmaf(xa, cs[n].x, -(xb * cs[n].y)));
-            w[i].x[n] = narrow<T>(fmaf(xb, cs[n].x, xa * cs[n].y));
-          }
-          *reinterpret_cast<Chunk*>(y + other) = w[i];
-        } else {
-#pragma unroll
-          for (int n = 0; n < P; ++n) {
-            const float xa = widen(u[i].x[2 * n]), xb = widen(u[i].x[2 * n + 1]);
-            u[i].x[2 * n] = narrow<T>(fmaf(xa, cs[n].x, -(xb * cs[n].y)));
-            u[i].x[2 * n + 1] = narrow<T>(fmaf(xb, cs[n].x, xa * cs[n].y));
-          }
-        }
-      }
-      *reinterpret_cast<Chunk*>(y) = u[i];
-    }
-  }
-}
+  // [token][two pairs of a chunk][chunk]: neighbouring threads read neighbours
+  extern __shared__ __align__(16) float2 angles[];
+  const auto slot = [&](int token, int c, int n) {
+    return token * a.pairs + (P > 1 ? ((n >> 1) * a.turned + c) * 2 + (n & 1) : c);
+  };
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.each;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.each), a.tokens - t0));
+  const int first = blockIdx.y * a.part, part = min(a.part, a.all_heads - first);
+  const uint32_t units = tokens * a.part * a.chunks;
 
-// Neighbouring pairs at addresses that hold no pair whole, element by element.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const RotaryArgs a) {
-  uint32_t t;
-  int c, first;
-  if (!place(a, t, c, first)) return;
-  const bool turned = c < a.turned;
-  const int at = turned ? 2 * c : a.pairs + c;  // behind the pairs: 2 pairs + (c - pairs)
-  float2 cs = make_float2(0.f, 0.f);
-  if (turned) {
-    cs = cos_sin(a.positions[t], a.turns[c], a.transpose);
+  Chunk u[kAtOnce], w[SPLIT ? kAtOnce : 1];
+  // A unit's token, head and chunk; -1 for none.
+  struct Unit {
+    int token, head, c;
+  };
+  const auto unit = [&](uint32_t e) {
+    const uint32_t r = quotient(e, a.by_chunks);
+    Unit x;
+    x.c = static_cast<int>(e - r * a.chunks);
+    x.token = static_cast<int>(quotient(r, a.by_part));
+    x.head = static_cast<int>(r) - x.token * a.part;
+    if (e >= units || x.head >= part) x.token = -1;
+    x.head += first;
+    return x;
+  };
+  const auto offset = [&](const Unit& x) {
+    return x.c < a.turned ? x.c * a.step : 2 * a.pairs + (x.c - a.turned) * V;
+  };
+  const auto load = [&](uint32_t e0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const Unit x = unit(e0 + i * kThreads);
+      if (x.token < 0) continue;
+      const T* from = (x.head < a.heads
+                           ? static_cast<const T*>(a.q) + x.head * a.q_sh + (t0 + x.token) * a.q_st
+                           : static_cast<const T*>(a.k) + (x.head - a.heads) * a.k_sh +
+                                 (t0 + x.token) * a.k_st) +
+                      offset(x);
+      u[i] = *reinterpret_cast<const Chunk*>(from);
+      if constexpr (SPLIT)
+        if (x.c < a.turned) w[i] = *reinterpret_cast<const Chunk*>(from + a.other);
+    }
+  };
+  load(threadIdx.x);
+  for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
+    const int token = i / a.pairs, pair = i - token * a.pairs, c = pair / P;
+    float2 cs = cos_sin(a.positions[t0 + token], a.turns[pair], a.transpose);
     cs.x *= a.factor;
     cs.y *= a.factor;
+    angles[slot(token, c, pair - c * P)] = cs;
   }
-  for (int h = first; h < a.all_heads; h += a.lanes) {
-    const bool q = h < a.heads;
-    const int g = q ? h : h - a.heads;
-    const T* x = static_cast<const T*>(q ? a.q : a.k) + t * (q ? a.q_st : a.k_st) +
-                 g * (q ? a.q_sh : a.k_sh) + at;
-    T* y = static_cast<T*>(q ? a.q_out : a.k_out) + t * (q ? a.qo_st : a.ko_st) +
-           g * (q ? a.qo_sh : a.ko_sh) + at;
-    if (!turned) {
-      y[0] = x[0];
-      continue;
+  __syncthreads();
+  for (uint32_t e0 = threadIdx.x;;) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const Unit x = unit(e0 + i * kThreads);
+      if (x.token < 0) continue;
+      T* to = (x.head < a.heads
+                   ? static_cast<T*>(a.q_out) + x.head * a.qo_sh + (t0 + x.token) * a.qo_st
+                   : static_cast<T*>(a.k_out) + (x.head - a.heads) * a.ko_sh +
+                         (t0 + x.token) * a.ko_st) +
+              offset(x);
+      if (x.c < a.turned) {
+#pragma unroll
+        for (int n = 0; n < P; ++n) {
+          const float2 cs = angles[slot(x.token, x.c, n)];
+          T& p = SPLIT ? u[i].x[n] : u[i].x[2 * n];
+          T& r = SPLIT ? w[i].x[n] : u[i].x[2 * n + 1];
+          const float xa = widen(p), xb = widen(r);
+          p = narrow<T>(fmaf(xa, cs.x, -(xb * cs.y)));
+          r = narrow<T>(fmaf(xb, cs.x, xa * cs.y));
+        }
+        if constexpr (SPLIT) *reinterpret_cast<Chunk*>(to + a.other) = w[i];
+      }
+      *reinterpret_cast<Chunk*>(to) = u[i];
     }
-    const float xa = widen(x[0]), xb = widen(x[1]);
-    y[0] = narrow<T>(fmaf(xa, cs.x, -(xb * cs.y)));
-    y[1] = narrow<T>(fmaf(xb, cs.x, xa * cs.y));
+    e0 += kAtOnce * kThreads;
+    if (e0 - threadIdx.x >= units) return;
+    load(e0);
   }
 }
 
-// Threads that fill the GPU once.
-constexpr int64_t kFull = 152 * 2048;
+// Units of a CTA (a unit: a chunk of a head), and angles.
+constexpr int64_t kUnits = 1024, kAngles = 2048;
+constexpr int64_t kCtas = 152 * 4;
 
 template <typename T, int V>
 dsa_status launch(RotaryArgs a, int32_t head_dim, bool halves, cudaStream_t stream) {
-  const bool pairs = !halves && V == 1;
-  a.turned = halves ? a.pairs / V : pairs ? a.pairs : 2 * a.pairs / V;
+  // neighbours at addresses that hold no pair whole are taken one by one
+  const bool split = halves || V == 1;
+  a.turned = split ? a.pairs / V : 2 * a.pairs / V;
   a.chunks = a.turned + (head_dim - 2 * a.pairs) / V;
-  const int64_t tokens = a.tokens, units = tokens * a.chunks, want = (kFull + units - 1) / units;
-  a.lanes = static_cast<uint32_t>(want < a.all_heads ? want : a.all_heads);
-  // Threads of a launch are counted in 32 bits.
-  const int64_t most = (INT32_MAX - kThreads) / (static_cast<int64_t>(a.chunks) * a.lanes);
-  for (int64_t done = 0; done < tokens; done += most) {
-    const int64_t now = tokens - done < most ? tokens - done : most;
-    a.tokens = static_cast<uint32_t>(now);
-    const unsigned grid =
-        static_cast<unsigned>((now * a.chunks * a.lanes + kThreads - 1) / kThreads);
-    if (halves)
-      rotary_kernel<T, V, true><<<grid, kThreads, 0, stream>>>(a);
-    else if constexpr (V == 1)
-      rotary_pairs_kernel<T><<<grid, kThreads, 0, stream>>>(a);
-    else
-      rotary_kernel<T, V, false><<<grid, kThreads, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
-    a.q = static_cast<const T*>(a.q) + most * a.q_st;
-    a.k = static_cast<const T*>(a.k) + most * a.k_st;
-    a.q_out = static_cast<T*>(a.q_out) + most * a.qo_st;
-    a.k_out = static_cast<T*>(a.k_out) + most * a.ko_st;
-    a.positions += most;
+  a.step = halves ? V : V == 1 ? 2 : V;
+  a.other = halves ? a.pairs : 1;
+  // As many tokens to a CTA as fill it, while there are CTAs for all SMs; heads
+  // are divided where a few tokens have many.
+  const int64_t token = static_cast<int64_t>(a.all_heads) * a.chunks;
+  int64_t each = kUnits / token, parts = 1;
+  if (each > a.tokens / kCtas) each = a.tokens / kCtas;
+  if (a.pairs > 0 && each > kAngles / a.pairs) each = kAngles / a.pairs;
+  if (each < 1) {
+    each = 1;
+    parts = (token + kUnits - 1) / kUnits;
+    const int64_t few = (kCtas + a.tokens - 1) / a.tokens;  // CTAs that a token may have
+    if (parts < few) parts = few < (token + kThreads - 1) / kThreads
+                                 ? few
+                                 : (token + kThreads - 1) / kThreads;
+    if (parts > a.all_heads) parts = a.all_heads;
   }
-  return DSA_OK;
+  a.each = static_cast<int32_t>(each);
+  a.part = static_cast<int32_t>((a.all_heads + parts - 1) / parts);
+  a.by_chunks = reciprocal(a.chunks);
+  a.by_part = reciprocal(a.part);
+  const dim3 grid(static_cast<unsigned>((a.tokens + each - 1) / each),
+                  static_cast<unsigned>((a.all_heads + a.part - 1) / a.part));
+  const size_t smem = static_cast<size_t>(each) * a.pairs * sizeof(float2);
+  if (split)
+    rotary_kernel<T, V, true><<<grid, kThreads, smem, stream>>>(a);
+  else if constexpr (V > 1)
+    rotary_kernel<T, V, false><<<grid, kThreads, smem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
 // The widest chunk of which `bits` (addresses and steps in bytes, or'ed) and
@@ -251,7 +250,7 @@ extern "C" dsa_status dsa_rotary(const void* q, void* q_out, int32_t heads, int6
   const int64_t strides[] = {q_st, q_sh, qo_st, qo_sh, k_st, k_sh, ko_st, ko_sh};
   for (int i = heads > 0 ? 0 : 4; i < (kv_heads > 0 ? 8 : 4); ++i)
     if (strides[i] < 0) return DSA_EINVAL;
-  if (tokens > INT32_MAX || head_dim > 65536 || all * head_dim > INT32_MAX)
+  if (tokens > INT32_MAX || head_dim > 4096 || all > 65535)
     return DSA_EUNSUPPORTED;
   if (tokens == 0 || head_dim == 0 || all == 0) return DSA_OK;
   if ((heads > 0 && (!q || !q_out)) || (kv_heads > 0 && (!k || !k_out)) ||
@@ -281,7 +280,7 @@ extern "C" dsa_status dsa_rotary(const void* q, void* q_out, int32_t heads, int6
   a.ko_sh = ko_sh;
   a.heads = heads;
   a.all_heads = static_cast<int32_t>(all);
-  a.tokens = static_cast<uint32_t>(tokens);
+  a.tokens = tokens;
   a.positions = positions;
   a.turns = turns;
   a.pairs = pairs;

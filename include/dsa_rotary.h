@@ -56,8 +56,7 @@ extern "C" {
  * written. DSA_EINVAL for an unknown dtype, negative sizes or strides, pairs
  * beyond head_dim / 2, a factor that is not finite, a NULL required pointer
  * or an address that is no multiple of the element's size. DSA_EUNSUPPORTED
- * for sizes from 2^31, head_dim over 65536, or (heads + kv_heads) * head_dim
- * from 2^31.
+ * for tokens from 2^31, head_dim over 4096, or more than 65535 heads in all.
  */
 dsa_status dsa_rotary(const void *q, void *q_out, int32_t heads, int64_t q_st,
                       int64_t q_sh, int64_t qo_st, int64_t qo_sh, const void *k,

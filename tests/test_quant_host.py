@@ -52,7 +52,7 @@ def rotary(lib, **kw):
     (dict(k_out=None), DSA_EINVAL), (dict(positions=None), DSA_EINVAL),
     (dict(turns=None), DSA_EINVAL), (dict(q=ONE), DSA_EINVAL), (dict(k_out=ONE), DSA_EINVAL),
     (dict(q=ctypes.c_void_p(0x1002), dtype=F32), DSA_EINVAL),
-    (dict(tokens=2 ** 31), DSA_EUNSUPPORTED), (dict(head_dim=65537), DSA_EUNSUPPORTED),
+    (dict(tokens=2 ** 31), DSA_EUNSUPPORTED), (dict(head_dim=4097), DSA_EUNSUPPORTED),
     (dict(heads=2 ** 30, kv_heads=2 ** 30), DSA_EUNSUPPORTED),
     (dict(tokens=0, q=None, positions=None), DSA_OK), (dict(head_dim=0, pairs=0), DSA_OK),
     (dict(heads=0, kv_heads=0, q=None, q_st=-1), DSA_OK),
