@@ -2,11 +2,10 @@
 // include/dsa_rotary.h.
 //
 // A CTA takes a few tokens: it computes the cosines and sines of their positions
-// once, into shared memory, and then goes through the heads, a chunk of pairs to
-// a thread. Chunks are as wide as alignment lets them be, up to 16 bytes;
-// neighbouring threads take neighbouring chunks. The first loads are on their way
-// while the angles are computed. (With the angles in registers, computed again
-// by every thread, 8192 tokens of 40 heads of 128 took 48 us.)
+// once, into shared memory. Each thread owns a chunk of pairs of one head and goes
+// through the tokens with it, so that its addresses only step. Chunks are as wide
+// as alignment lets them be, up to 16 bytes; neighbouring threads take neighbouring
+// chunks. The first loads are on their way while the angles are computed.
 #include "../../include/dsa_rotary.h"
 
 #include <cuda_bf16.h>
@@ -19,8 +18,6 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
-
 struct RotaryArgs {
   const void *q, *k;
   void *q_out, *k_out;
@@ -30,21 +27,13 @@ struct RotaryArgs {
   const int32_t* positions;
   const int64_t* turns;
   int32_t pairs;
-  int32_t turned, chunks;      // chunks of a head: those of the pairs, and all
-  int32_t step, other;         // from chunk to chunk, and to its second half (SPLIT)
-  int32_t each, part;          // tokens of a CTA, and heads
-  uint32_t by_chunks, by_part;  // ceil(2^32 / chunks) and / part, 0 for 1
+  int32_t turned, chunks;  // chunks of a head: those of the pairs, and all
+  int32_t step, other;     // from chunk to chunk, and to its second half (SPLIT)
+  int32_t each;            // tokens of a CTA
+  int32_t part, width;     // heads of a CTA, and chunks of each
   float factor;
   int32_t transpose;
 };
-
-// n / d for by = ceil(2^32 / d): exact while n * d is below 2^32.
-__device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t by) {
-  return by ? __umulhi(n, by) : n;
-}
-uint32_t reciprocal(uint32_t d) {
-  return d == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + d - 1) / d);
-}
 
 // cos and sin of the angle of position p. The fraction of a turn is exact;
 // what is left after the nearest quarter turn, at most an eighth, is rounded
@@ -62,122 +51,131 @@ __device__ __forceinline__ float2 cos_sin(int32_t p, int64_t turn, bool transpos
   return r;
 }
 
+// Two neighbouring elements of T, and as floats.
 template <typename T>
-__device__ __forceinline__ float widen(T x) {
-  return static_cast<float>(x);
-}
+struct Two;
+template <>
+struct Two<float> {
+  using Raw = float2;
+  static __device__ __forceinline__ float2 widen(Raw x) { return x; }
+  static __device__ __forceinline__ Raw narrow(float2 x) { return x; }
+};
+template <>
+struct Two<__nv_bfloat16> {
+  using Raw = __nv_bfloat162;
+  static __device__ __forceinline__ float2 widen(Raw x) { return __bfloat1622float2(x); }
+  static __device__ __forceinline__ Raw narrow(float2 x) { return __float22bfloat162_rn(x); }
+};
+template <>
+struct Two<__half> {
+  using Raw = __half2;
+  static __device__ __forceinline__ float2 widen(Raw x) { return __half22float2(x); }
+  static __device__ __forceinline__ Raw narrow(float2 x) { return __float22half2_rn(x); }
+};
+
+// V elements of T, in memory as one load or store.
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Chunk {
+  typename Two<T>::Raw x[V / 2];
+};
 template <typename T>
-__device__ __forceinline__ T narrow(float x);
-template <>
-__device__ __forceinline__ float narrow<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half narrow<__half>(float x) {
-  return __float2half_rn(x);
+struct Chunk<T, 1> {
+  T x;
+};
+
+// (a, b) turned by (cos, sin).
+__device__ __forceinline__ float2 turned(float xa, float xb, float2 cs) {
+  return make_float2(fmaf(xa, cs.x, -(xb * cs.y)), fmaf(xb, cs.x, xa * cs.y));
 }
 
-template <typename T, int V>
-struct alignas(V * sizeof(T)) Vec {
-  T x[V];
-};
+constexpr int kMaxThreads = 512;
 
 // V elements of T at a time. SPLIT: a chunk is V pairs, whose first and second
 // elements lie apart; otherwise it is V / 2 pairs of neighbours.
 template <typename T, int V, bool SPLIT>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const RotaryArgs a) {
   constexpr int P = SPLIT ? V : V / 2;  // pairs of a chunk
-  constexpr int kAtOnce = SPLIT ? 2 : 4;
-  using Chunk = Vec<T, V>;
+  constexpr int kAtOnce = 2;  // tokens
+  using C = Chunk<T, V>;
   // [token][two pairs of a chunk][chunk]: neighbouring threads read neighbours
   extern __shared__ __align__(16) float2 angles[];
-  const auto slot = [&](int token, int c, int n) {
-    return token * a.pairs + (P > 1 ? ((n >> 1) * a.turned + c) * 2 + (n & 1) : c);
-  };
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.each;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(a.each), a.tokens - t0));
-  const int first = blockIdx.y * a.part, part = min(a.part, a.all_heads - first);
-  const uint32_t units = tokens * a.part * a.chunks;
-
-  Chunk u[kAtOnce], w[SPLIT ? kAtOnce : 1];
-  // A unit's token, head and chunk; -1 for none.
-  struct Unit {
-    int token, head, c;
-  };
-  const auto unit = [&](uint32_t e) {
-    const uint32_t r = quotient(e, a.by_chunks);
-    Unit x;
-    x.c = static_cast<int>(e - r * a.chunks);
-    x.token = static_cast<int>(quotient(r, a.by_part));
-    x.head = static_cast<int>(r) - x.token * a.part;
-    if (e >= units || x.head >= part) x.token = -1;
-    x.head += first;
-    return x;
-  };
-  const auto offset = [&](const Unit& x) {
-    return x.c < a.turned ? x.c * a.step : 2 * a.pairs + (x.c - a.turned) * V;
-  };
-  const auto load = [&](uint32_t e0) {
+  const int in = threadIdx.x / a.width, head = blockIdx.y * a.part + in;
+  const int c = blockIdx.z * a.width + threadIdx.x - in * a.width;
+  const bool mine = in < a.part && head < a.all_heads && c < a.chunks, turn = c < a.turned;
+  const int at = turn ? c * a.step : 2 * a.pairs + (c - a.turned) * V;
+  const bool q = head < a.heads;
+  const int64_t st = q ? a.q_st : a.k_st, ot = q ? a.qo_st : a.ko_st;
+  const T* from = q ? static_cast<const T*>(a.q) + head * a.q_sh
+                    : static_cast<const T*>(a.k) + (head - a.heads) * a.k_sh;
+  T* to = q ? static_cast<T*>(a.q_out) + head * a.qo_sh
+            : static_cast<T*>(a.k_out) + (head - a.heads) * a.ko_sh;
+  from += t0 * st + at;
+  to += t0 * ot + at;
+  C u[kAtOnce], w[SPLIT ? kAtOnce : 1];
+  const auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const Unit x = unit(e0 + i * kThreads);
-      if (x.token < 0) continue;
-      const T* from = (x.head < a.heads
-                           ? static_cast<const T*>(a.q) + x.head * a.q_sh + (t0 + x.token) * a.q_st
-                           : static_cast<const T*>(a.k) + (x.head - a.heads) * a.k_sh +
-                                 (t0 + x.token) * a.k_st) +
-                      offset(x);
-      u[i] = *reinterpret_cast<const Chunk*>(from);
+      if (!mine || t + i >= tokens) continue;
+      const T* x = from + (t + i) * st;
+      u[i] = *reinterpret_cast<const C*>(x);
       if constexpr (SPLIT)
-        if (x.c < a.turned) w[i] = *reinterpret_cast<const Chunk*>(from + a.other);
+        if (turn) w[i] = *reinterpret_cast<const C*>(x + a.other);
     }
   };
-  load(threadIdx.x);
-  for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
-    const int token = i / a.pairs, pair = i - token * a.pairs, c = pair / P;
+  load(0);
+  for (int i = threadIdx.x; i < tokens * a.pairs; i += blockDim.x) {
+    const int token = i / a.pairs, pair = i - token * a.pairs, chunk = pair / P, n = pair % P;
     float2 cs = cos_sin(a.positions[t0 + token], a.turns[pair], a.transpose);
     cs.x *= a.factor;
     cs.y *= a.factor;
-    angles[slot(token, c, pair - c * P)] = cs;
+    angles[token * a.pairs + (P > 1 ? ((n >> 1) * a.turned + chunk) * 2 + (n & 1) : chunk)] = cs;
   }
   __syncthreads();
-  for (uint32_t e0 = threadIdx.x;;) {
+  if (!mine) return;
+  for (int t = 0;;) {
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const Unit x = unit(e0 + i * kThreads);
-      if (x.token < 0) continue;
-      T* to = (x.head < a.heads
-                   ? static_cast<T*>(a.q_out) + x.head * a.qo_sh + (t0 + x.token) * a.qo_st
-                   : static_cast<T*>(a.k_out) + (x.head - a.heads) * a.ko_sh +
-                         (t0 + x.token) * a.ko_st) +
-              offset(x);
-      if (x.c < a.turned) {
+      if (t + i >= tokens) continue;
+      T* y = to + (t + i) * ot;
+      if (turn) {
+        const float2* cs = angles + (t + i) * a.pairs + (P > 1 ? c * 2 : c);
+        if constexpr (V == 1) {
+          const float2 z = turned(static_cast<float>(u[i].x), static_cast<float>(w[i].x), *cs);
+          u[i].x = static_cast<T>(z.x);
+          w[i].x = static_cast<T>(z.y);
+        } else if constexpr (SPLIT) {
 #pragma unroll
-        for (int n = 0; n < P; ++n) {
-          const float2 cs = angles[slot(x.token, x.c, n)];
-          T& p = SPLIT ? u[i].x[n] : u[i].x[2 * n];
-          T& r = SPLIT ? w[i].x[n] : u[i].x[2 * n + 1];
-          const float xa = widen(p), xb = widen(r);
-          p = narrow<T>(fmaf(xa, cs.x, -(xb * cs.y)));
-          r = narrow<T>(fmaf(xb, cs.x, xa * cs.y));
+          for (int n = 0; n < V / 2; ++n) {
+            const float4 f = *reinterpret_cast<const float4*>(cs + n * a.turned * 2);
+            const float2 xa = Two<T>::widen(u[i].x[n]), xb = Two<T>::widen(w[i].x[n]);
+            const float2 y0 = turned(xa.x, xb.x, make_float2(f.x, f.y));
+            const float2 y1 = turned(xa.y, xb.y, make_float2(f.z, f.w));
+            u[i].x[n] = Two<T>::narrow(make_float2(y0.x, y1.x));
+            w[i].x[n] = Two<T>::narrow(make_float2(y0.y, y1.y));
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < P; ++n) {
+            const float2 f = cs[P > 1 ? (n >> 1) * a.turned * 2 + (n & 1) : 0];
+            const float2 x = Two<T>::widen(u[i].x[n]);
+            u[i].x[n] = Two<T>::narrow(turned(x.x, x.y, f));
+          }
         }
-        if constexpr (SPLIT) *reinterpret_cast<Chunk*>(to + a.other) = w[i];
+        if constexpr (SPLIT) *reinterpret_cast<C*>(y + a.other) = w[i];
       }
-      *reinterpret_cast<Chunk*>(to) = u[i];
+      *reinterpret_cast<C*>(y) = u[i];
     }
-    e0 += kAtOnce * kThreads;
-    if (e0 - threadIdx.x >= units) return;
-    load(e0);
+    t += kAtOnce;
+    if (t >= tokens) return;
+    load(t);
   }
 }
 
-// Units of a CTA (a unit: a chunk of a head), and angles.
-constexpr int64_t kUnits = 1024, kAngles = 2048;
-constexpr int64_t kCtas = 152 * 4;
+// Tokens of a CTA, and angles; CTAs that are wanted before a CTA gets several
+// tokens.
+constexpr int64_t kTokens = 4, kAngles = 2048, kCtas = 152 * 4;
 
 template <typename T, int V>
 dsa_status launch(RotaryArgs a, int32_t head_dim, bool halves, cudaStream_t stream) {
@@ -187,32 +185,23 @@ dsa_status launch(RotaryArgs a, int32_t head_dim, bool halves, cudaStream_t stre
   a.chunks = a.turned + (head_dim - 2 * a.pairs) / V;
   a.step = halves ? V : V == 1 ? 2 : V;
   a.other = halves ? a.pairs : 1;
-  // As many tokens to a CTA as fill it, while there are CTAs for all SMs; heads
-  // are divided where a few tokens have many.
-  const int64_t token = static_cast<int64_t>(a.all_heads) * a.chunks;
-  int64_t each = kUnits / token, parts = 1;
-  if (each > a.tokens / kCtas) each = a.tokens / kCtas;
+  a.width = a.chunks < kMaxThreads ? a.chunks : kMaxThreads;
+  const int64_t most = kMaxThreads / a.width;
+  a.part = static_cast<int32_t>(a.all_heads < most ? a.all_heads : most);
+  const unsigned parts = (a.all_heads + a.part - 1) / a.part;
+  int64_t each = a.tokens * parts / kCtas;
+  if (each > kTokens) each = kTokens;
   if (a.pairs > 0 && each > kAngles / a.pairs) each = kAngles / a.pairs;
-  if (each < 1) {
-    each = 1;
-    parts = (token + kUnits - 1) / kUnits;
-    const int64_t few = (kCtas + a.tokens - 1) / a.tokens;  // CTAs that a token may have
-    if (parts < few) parts = few < (token + kThreads - 1) / kThreads
-                                 ? few
-                                 : (token + kThreads - 1) / kThreads;
-    if (parts > a.all_heads) parts = a.all_heads;
-  }
+  if (each < 1) each = 1;
   a.each = static_cast<int32_t>(each);
-  a.part = static_cast<int32_t>((a.all_heads + parts - 1) / parts);
-  a.by_chunks = reciprocal(a.chunks);
-  a.by_part = reciprocal(a.part);
-  const dim3 grid(static_cast<unsigned>((a.tokens + each - 1) / each),
-                  static_cast<unsigned>((a.all_heads + a.part - 1) / a.part));
+  const dim3 grid(static_cast<unsigned>((a.tokens + each - 1) / each), parts,
+                  (a.chunks + a.width - 1) / a.width);
+  const unsigned threads = (a.part * a.width + 31) / 32 * 32;
   const size_t smem = static_cast<size_t>(each) * a.pairs * sizeof(float2);
   if (split)
-    rotary_kernel<T, V, true><<<grid, kThreads, smem, stream>>>(a);
+    rotary_kernel<T, V, true><<<grid, threads, smem, stream>>>(a);
   else if constexpr (V > 1)
-    rotary_kernel<T, V, false><<<grid, kThreads, smem, stream>>>(a);
+    rotary_kernel<T, V, false><<<grid, threads, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
