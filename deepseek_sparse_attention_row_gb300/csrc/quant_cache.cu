@@ -52,19 +52,34 @@ __device__ __forceinline__ float2 pair<__half>(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&two));
 }
 
-__device__ __forceinline__ float finite_size(float x) {
-  const float a = fabsf(x);
-  return a < INFINITY ? a : 0.f;
-}
+// Sizes of 16-bit numbers are ordered as integers; from this one on they are not
+// finite. (Both halves alike.)
+template <typename T>
+constexpr uint32_t kInfinite = 0x7f80u;
+template <>
+constexpr uint32_t kInfinite<__half> = 0x7c00u;
+
 __device__ __forceinline__ float nan_for_infinite(float x) {
   return fabsf(x) < INFINITY ? x : NAN;
+}
+// The larger of the two halves of each word.
+__device__ __forceinline__ uint32_t largest2(uint32_t x, uint32_t sizes) {
+  return __vmaxu2(x, sizes & 0x7fff7fffu);
+}
+// The same, of finite numbers.
+template <typename T>
+__device__ __forceinline__ uint32_t largest_finite2(uint32_t x, uint32_t sizes) {
+  sizes &= 0x7fff7fffu;
+  if ((sizes & 0xffffu) >= kInfinite<T>) sizes &= 0xffff0000u;
+  if ((sizes >> 16) >= kInfinite<T>) sizes &= 0xffffu;
+  return __vmaxu2(x, sizes);
 }
 
 // A block of a sequence that gets new tokens. Sequence s of n tokens touches at
 // most n / block + 2 blocks, and floor(cu[s] / block) + 2 s counts that many
 // between one sequence and the next: item numbers are found from cu alone.
 struct Block {
-  int32_t seq, page;  // page -1: nothing to do
+  int32_t seq;        // -1: nothing to do
   int32_t start;      // its first token
   int32_t from, to;   // the new ones
   int64_t row;        // of the token `from`
@@ -73,7 +88,7 @@ struct Block {
 __device__ __forceinline__ Block find_block(const WriteArgs& a, int64_t item) {
   const int lg = a.pool.block_log2;
   Block b{};
-  b.page = -1;
+  b.seq = -1;
   const int32_t s = last_upto(a.seqs, item, [&](int32_t i) {
     return (clamped(a.cu[i], a.total) >> lg) + 2ll * i;
   });
@@ -88,7 +103,6 @@ __device__ __forceinline__ Block find_block(const WriteArgs& a, int64_t item) {
   b.from = static_cast<int32_t>(held > start ? held : start);
   b.to = static_cast<int32_t>(end < start + (1ll << lg) ? end : start + (1ll << lg));
   b.row = r0 + b.from - held;
-  b.page = quant_page(a.pool, s, b.start);
   return b;
 }
 
@@ -99,47 +113,65 @@ constexpr int kAtOnce = 8;  // 16-byte loads of a lane
 // keys and values; the teams of a CTA share the block. Where a block's new tokens
 // are no more than a team has registers for, they are read once.
 template <typename T>
-__global__ void __launch_bounds__(512) write_kernel(const WriteArgs a, int team) {
+__global__ void __launch_bounds__(512, 2) write_kernel(const WriteArgs a, int team) {
   __shared__ uint32_t tops[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const Block b = find_block(a, blockIdx.x);
-  if (b.page < 0) return;
-  const int parts = a.pool.dim / 8, rows = 32 / parts;  // 8 elements of a lane
+  if (b.seq < 0) return;
+  const int32_t page = quant_page(a.pool, b.seq, b.start);  // not waited for yet
+  const int parts = a.pool.dim / 8, rows = 32 / parts;      // 8 elements of a lane
   const int row = lane / parts, part = lane - row * parts;
   const int mate = warp & (team - 1), each = warps / team;  // teams of a CTA
   const int step = team * rows;                             // rows of a team at a time
   const int from = row < rows ? mate * rows + row : 1 << 20;  // idle lanes: behind every row
   const int count = b.to - b.from;
-  for (int w0 = blockIdx.y * each; w0 < 2 * a.pool.kv_heads; w0 += gridDim.y * each) {
-    const int w = w0 + warp / team;
-    const bool mine = w < 2 * a.pool.kv_heads;
-    const int kv = w & 1, head = mine ? w >> 1 : 0;
-    const char* x = static_cast<const char*>(a.x[kv]) +
-                    (b.row * a.xt[kv] + head * a.xh[kv]) * static_cast<int64_t>(sizeof(T)) +
-                    part * 16;
-    const int64_t x_step = a.xt[kv] * static_cast<int64_t>(sizeof(T));
-    uint4 u[kAtOnce];
-    const auto load = [&](int i0) {
+  // This team's work number w: keys or values of a head.
+  const auto source = [&](int w) {
+    const int kv = w & 1;
+    return static_cast<const char*>(a.x[kv]) +
+           (b.row * a.xt[kv] + (w >> 1) * a.xh[kv]) * static_cast<int64_t>(sizeof(T)) + part * 16;
+  };
+  const auto load = [&](uint4 (&u)[kAtOnce], int w, int i0) {
+    const char* x = source(w);
+    const int64_t x_step = a.xt[w & 1] * static_cast<int64_t>(sizeof(T));
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int at = i0 + from + i * step;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (mine && at < count) u[i] = *reinterpret_cast<const uint4*>(x + at * x_step);
-      }
-    };
-    float top = 0.f;
-    for (int i0 = 0; i0 < count; i0 += kAtOnce * step) {
-      load(i0);
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i)
-        for (uint32_t two : {u[i].x, u[i].y, u[i].z, u[i].w}) {
-          const float2 f = pair<T>(two);
-          top = fmaxf(top, fmaxf(finite_size(f.x), finite_size(f.y)));
-        }
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int at = i0 + from + i * step;
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (at < count) u[i] = *reinterpret_cast<const uint4*>(x + at * x_step);
     }
-    uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));
-    float* scale = quant_scale(a.pool, kv, b.page, b.start, head);
-    const float was = mine && b.from > b.start ? *scale : 0.f;
+  };
+  // The largest finite size of them and of `x` (two halves); `special`: this warp
+  // has some that are not finite.
+  const auto largest = [&](const uint4 (&u)[kAtOnce], uint32_t x, bool& special) {
+    uint32_t y = x;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      for (uint32_t two : {u[i].x, u[i].y, u[i].z, u[i].w}) y = largest2(y, two);
+    if (!__any_sync(~0u, max(y & 0xffffu, y >> 16) >= kInfinite<T>)) return y;
+    special = true;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      for (uint32_t two : {u[i].x, u[i].y, u[i].z, u[i].w}) x = largest_finite2<T>(x, two);
+    return x;
+  };
+  const int works = 2 * a.pool.kv_heads;
+  const bool once = count <= kAtOnce * step;
+  for (int w0 = blockIdx.y * each; w0 < works; w0 += gridDim.y * each) {
+    const int w = w0 + warp / team;
+    const bool mine = w < works;
+    const int kv = w & 1, head = mine ? w >> 1 : 0;
+    uint4 u[kAtOnce];
+    uint32_t sizes = 0;
+    bool special = false;
+    if (mine)
+      for (int i0 = 0; i0 < count; i0 += kAtOnce * step) {
+        load(u, w, i0);
+        sizes = largest(u, sizes, special);
+      }
+    uint32_t most = __reduce_max_sync(~0u, max(sizes & 0xffffu, sizes >> 16));
+    float* scale = quant_scale(a.pool, kv, page, b.start, head);
+    const float was = mine && page >= 0 && b.from > b.start ? *scale : 0.f;
     if (team > 1) {
       if (lane == 0) tops[warp] = most;
       __syncthreads();  // and the scale has been read
@@ -148,12 +180,12 @@ __global__ void __launch_bounds__(512) write_kernel(const WriteArgs a, int team)
     } else {
       __syncwarp();
     }
-    if (!mine) continue;
-    uint32_t e = need_exponent(__uint_as_float(most));
+    if (!mine || page < 0) continue;
+    uint32_t e = need_exponent(pair<T>(most).x);
     if (b.from > b.start) e = max(e, held_exponent(was));
     if (mate == 0 && lane == 0) *scale = power(e);
     const float i1 = inverse_power(e);
-    uint8_t* codes = quant_code(a.pool, kv, b.page, b.start, head) + part * 8;
+    uint8_t* codes = quant_code(a.pool, kv, page, b.start, head) + part * 8;
     const int64_t c_step = a.pool.st[kv];
     if (b.from > b.start && power(e) != was) {
       for (int at = from; at < b.from - b.start; at += step) {
@@ -169,13 +201,14 @@ __global__ void __launch_bounds__(512) write_kernel(const WriteArgs a, int team)
     }
     codes += (b.from - b.start) * c_step;
     for (int i0 = 0; i0 < count; i0 += kAtOnce * step) {
-      if (count > kAtOnce * step) load(i0);
+      if (!once) load(u, w, i0);
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int at = i0 + from + i * step;
         const auto code = [&](uint32_t two) {
-          const float2 f = pair<T>(two);
-          return encode2(nan_for_infinite(f.x) * i1, nan_for_infinite(f.y) * i1);
+          float2 f = pair<T>(two);
+          if (special) f = make_float2(nan_for_infinite(f.x), nan_for_infinite(f.y));
+          return encode2(f.x * i1, f.y * i1);
         };
         if (at < count)
           *reinterpret_cast<uint2*>(codes + at * c_step) =
@@ -209,9 +242,9 @@ __device__ __forceinline__ uint32_t pack<__half>(float2 f) {
 }
 
 constexpr int kReadWarps = 4;
-constexpr int kReadRows = 8;  // of a warp
+constexpr int kReadRows = 2;  // of a warp
 
-// A warp for eight rows: lane i finds row i's page, and then 16 codes at a time are
+// A warp for two rows: lane i finds row i's page, and then 16 codes at a time are
 // dealt to the lanes over all of them. WIDE: 32 bytes of an output at once.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a) {
