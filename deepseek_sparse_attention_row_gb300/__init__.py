@@ -134,6 +134,8 @@ EXPORTED_SYMBOLS = (
     "dsa_cache_fork",
     "dsa_cache_free",
     "dsa_cache_compact",
+    "dsa_cache_fork_scaled",
+    "dsa_cache_compact_scaled",
     "dsa_rotary",
     "dsa_quant_cache_write",
     "dsa_quant_cache_read",
@@ -223,6 +225,10 @@ def library():
     lib.dsa_cache_free.argtypes = [p, i64, p, i64, i64, i64, p, p, i64, p]
     lib.dsa_cache_compact.argtypes = [p, i64, i64, i64, i64, i32, i64, p, p, i64, i64, i64, p, p,
                                       p, sz, p]
+    for name in ("dsa_cache_fork", "dsa_cache_compact"):
+        plain, scaled = getattr(lib, name), getattr(lib, name + "_scaled")
+        scaled.argtypes = [*plain.argtypes[:7], p, i64, i64, i64, *plain.argtypes[7:]]
+        scaled.restype = ctypes.c_int
     lib.dsa_rotary.argtypes = [p, p, i32, i64, i64, i64, i64, p, p, i32, i64, i64, i64, i64, i32,
                                i64, i32, p, p, i32, i32, f32, i32, p]
     rows, strides = [i64] * 4, [i64] * 8
@@ -930,19 +936,42 @@ def _cache_planes(cache, pages, index):
     return cache.data_ptr() or None, shape[0], plane_st, pages, page_st, shape[2], token
 
 
-def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None, workspace=None,
-                   stream=None):
+def _page_scales(scales, planes, pages, index):
+    """Arguments that describe scales [planes, N, ...] beside the pages."""
+    at = scales.get_device()
+    if at < 0 or at != index:
+        raise ValueError(f"scales is on {scales.device}, expected cuda:{index}")
+    shape, strides, e = scales.shape, scales.stride(), scales.element_size()
+    if len(shape) < 2 or shape[0] != planes or shape[1] != pages:
+        raise ValueError(f"scales must be [{planes}, {pages}, ...], got {tuple(shape)}")
+    inner = 1
+    for d in range(len(shape) - 1, 1, -1):
+        if shape[d] > 1 and strides[d] != inner:
+            raise ValueError("the pages of scales must be contiguous")
+        inner *= shape[d]
+    page = inner * e
+    plane_st = strides[0] * e if planes > 1 else page
+    page_st = strides[1] * e if pages > 1 else page
+    if plane_st < page or page_st < page:
+        raise ValueError("the pages of scales must not overlap")
+    return scales.data_ptr() or None, plane_st, page_st, page
+
+
+def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, scales=None, status=None,
+                   workspace=None, stream=None):
     """Make slot children[i] a copy of slot parents[i] (int32 CUDA vectors).
 
     ``cache`` [planes, N, page, ...] of any type (pages contiguous, tokens of
     a multiple of 16 bytes), ``refs`` int32 [N], ``tables`` int32 [S, P],
     ``lens`` int32 [S]. Whole pages are shared; the used tokens of a partly
-    filled last page are copied to the lowest free page. Returns ``status``
-    int32 (FORK_OK, FORK_NO_PAGE or FORK_REFUSED for each pair), allocated
+    filled last page are copied to the lowest free page, and with them that
+    page's ``scales`` [planes, N, ...] (of any type, pages contiguous; those of
+    an 8-bit cache). Returns ``status`` int32 (FORK_OK, FORK_NO_PAGE or FORK_REFUSED for each pair), allocated
     when None; the host waits for nothing."""
     torch = _torch()
     rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
     planes = _cache_planes(cache, pages, dev)
+    beside = () if scales is None else _page_scales(scales, planes[1], pages, dev)
     (pp, n), (cp, nc) = _vector(parents, "parents", dev), _vector(children, "children", dev)
     if n != nc:
         raise ValueError(f"{n} parents, {nc} children")
@@ -955,8 +984,8 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, status=None,
             raise ValueError(f"status holds {ns} entries, expected {n}")
         held, ws, ws_bytes = _scratch(
             workspace, _need("dsa_cache_workspace_bytes", dev, n, pages) if n else 0, refs, handle)
-        st = library().dsa_cache_fork(*planes, rp, tp, S, P, ld, lp, pp, cp, n, sp, ws, ws_bytes,
-                                       handle)
+        fn = library().dsa_cache_fork if scales is None else library().dsa_cache_fork_scaled
+        st = fn(*planes, *beside, rp, tp, S, P, ld, lp, pp, cp, n, sp, ws, ws_bytes, handle)
         if st:
             _check("dsa_cache_fork", st)
         return status
@@ -974,14 +1003,16 @@ def dsa_cache_free(refs, tables, lens, seqs, *, stream=None):
         _check("dsa_cache_free", st)
 
 
-def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=None, stream=None):
+def dsa_cache_compact(cache, refs, tables, *, scales=None, remap=None, live=None, workspace=None,
+                      stream=None):
     """Move the pages in use to the lowest numbers (contents in all planes,
-    refs and table entries). Returns ``remap`` int32 [N], the new number of
-    each used page (-1 for free ones), and ``live`` int32 [1], how many are in
-    use; allocated when None."""
+    ``scales`` as for ``dsa_cache_fork``, refs and table entries). Returns
+    ``remap`` int32 [N], the new number of each used page (-1 for free ones),
+    and ``live`` int32 [1], how many are in use; allocated when None."""
     torch = _torch()
     rp, pages, tp, S, P, ld, _, dev = _cache_state(refs, tables, None)
     planes = _cache_planes(cache, pages, dev)
+    beside = () if scales is None else _page_scales(scales, planes[1], pages, dev)
 
     def enqueue(remap, live, handle):
         if remap is None:
@@ -993,7 +1024,8 @@ def dsa_cache_compact(cache, refs, tables, *, remap=None, live=None, workspace=N
             raise ValueError(f"remap must have {pages} entries and live one")
         held, ws, ws_bytes = _scratch(
             workspace, _need("dsa_cache_workspace_bytes", dev, 0, pages), refs, handle)
-        st = library().dsa_cache_compact(*planes, rp, tp, S, P, ld, mp, vp, ws, ws_bytes, handle)
+        fn = library().dsa_cache_compact if scales is None else library().dsa_cache_compact_scaled
+        st = fn(*planes, *beside, rp, tp, S, P, ld, mp, vp, ws, ws_bytes, handle)
         if st:
             _check("dsa_cache_compact", st)
         return remap, live

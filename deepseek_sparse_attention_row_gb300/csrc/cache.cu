@@ -40,6 +40,10 @@ struct CacheArgs {
   int32_t* tables;
   int64_t seqs, max_pages, ld_tables;
   int32_t* lens;
+  // scales that go with the pages, whole pages of words; 0 words for none
+  char* scales;
+  int64_t scale_plane, scale_page;  // strides in bytes
+  int32_t scale_words;
 };
 
 constexpr int kPlanPages = 4;  // pages of a thread in one round
@@ -171,6 +175,15 @@ __device__ __forceinline__ void copy_piece(char* to, const char* from, int64_t b
   }
 }
 
+// The scales of a page in one plane, by the whole CTA.
+__device__ __forceinline__ void copy_scales(const CacheArgs& a, int64_t plane, int32_t to,
+                                            int32_t from) {
+  char* base = a.scales + plane * a.scale_plane;
+  uint32_t* x = reinterpret_cast<uint32_t*>(base + to * a.scale_page);
+  const uint32_t* y = reinterpret_cast<const uint32_t*>(base + from * a.scale_page);
+  for (int32_t i = threadIdx.x; i < a.scale_words; i += kCopyThreads) x[i] = y[i];
+}
+
 // CTA (x, y): pair x, planes y, y + gridDim.y, ...; the CTAs of y = 0 also
 // write the child's row.
 __global__ void __launch_bounds__(kCopyThreads)
@@ -198,6 +211,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     char* plane = a.cache + pl * a.plane_stride;
     for (int64_t at = 0; at < bytes; at += kPiece)
       copy_piece(plane + f.to * a.page_stride, plane + f.from * a.page_stride, bytes, at);
+    if (a.scale_words > 0) copy_scales(a, pl, f.to, f.from);
   }
 }
 
@@ -280,6 +294,11 @@ __global__ void __launch_bounds__(kCopyThreads)
     copy_piece(plane + m.y * a.page_stride, plane + m.x * a.page_stride, bytes,
                (u - page * pieces) * kPiece);
   }
+  if (a.scale_words > 0)
+    for (int64_t u = blockIdx.x; u < *count * a.planes; u += gridDim.x) {
+      const int2 m = moves[u / a.planes];
+      copy_scales(a, u % a.planes, m.y, m.x);
+    }
   const int64_t entries = a.seqs * a.max_pages;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries;
        e += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
@@ -313,6 +332,23 @@ dsa_status check_cache(const CacheArgs& a) {
   return DSA_OK;
 }
 
+// Scales of `bytes` a page beside the pages of `a`; none for 0.
+dsa_status add_scales(CacheArgs& a, void* scales, int64_t plane_stride, int64_t page_stride,
+                      int64_t bytes) {
+  if (bytes < 0 || plane_stride < 0 || page_stride < 0) return DSA_EINVAL;
+  if (bytes > INT32_MAX) return DSA_EUNSUPPORTED;
+  if (bytes == 0) return DSA_OK;
+  if (!scales && a.planes > 0 && a.num_pages > 0) return DSA_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(scales) & 3u) != 0 ||
+      (plane_stride | page_stride | bytes) % 4 != 0)
+    return DSA_EUNSUPPORTED;
+  a.scales = static_cast<char*>(scales);
+  a.scale_plane = plane_stride;
+  a.scale_page = page_stride;
+  a.scale_words = static_cast<int32_t>(bytes / 4);
+  return DSA_OK;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Fork: want [pairs], plan [pairs]. Compaction: count (256 bytes), moves.
@@ -328,23 +364,21 @@ extern "C" size_t dsa_cache_workspace_bytes(int64_t pairs, int64_t num_pages) {
   return f > c ? f : c;
 }
 
-extern "C" dsa_status dsa_cache_fork(void* cache, int64_t planes, int64_t plane_stride,
-                                     int64_t num_pages, int64_t page_stride, int32_t page_size,
-                                     int64_t token_bytes, int32_t* refs, int32_t* tables,
-                                     int64_t seqs, int64_t max_pages, int64_t ld_tables,
-                                     int32_t* lens, const int32_t* parents,
-                                     const int32_t* children, int64_t pairs, int32_t* status,
-                                     void* workspace, size_t workspace_bytes, void* stream) {
-  const dsa::CacheArgs a{static_cast<char*>(cache), planes, plane_stride, num_pages, page_stride,
-                         page_size, token_bytes, refs, tables, seqs, max_pages, ld_tables, lens};
-  dsa_status st = dsa::check_tables(num_pages, refs, tables, seqs, max_pages, ld_tables);
+namespace {
+
+dsa_status fork(const dsa::CacheArgs& a, const int32_t* parents, const int32_t* children,
+                int64_t pairs, int32_t* status, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  dsa_status st = dsa::check_tables(a.num_pages, a.refs, a.tables, a.seqs, a.max_pages,
+                                    a.ld_tables);
   if (st != DSA_OK) return st;
   st = dsa::check_cache(a);
   if (st != DSA_OK) return st;
   if (pairs < 0) return DSA_EINVAL;
   if (pairs > dsa::kMaxPairs) return DSA_EUNSUPPORTED;
   if (pairs == 0) return DSA_OK;
-  if (max_pages < 1 || !parents || !children || !status || (seqs > 0 && !lens)) return DSA_EINVAL;
+  if (a.max_pages < 1 || !parents || !children || !status || (a.seqs > 0 && !a.lens))
+    return DSA_EINVAL;
   if (!workspace || workspace_bytes < dsa::fork_bytes(pairs) || !dsa::aligned16(workspace))
     return DSA_EINVAL;
   int32_t* want = static_cast<int32_t*>(workspace);
@@ -355,11 +389,43 @@ extern "C" dsa_status dsa_cache_fork(void* cache, int64_t planes, int64_t plane_
   dsa::fork_plan_kernel<<<1, dsa::kPlanThreads, 0, s>>>(a, parents, children, n, status, plan,
                                                         want);
   if (cudaGetLastError() != cudaSuccess) return DSA_ECUDA;
-  const unsigned ys = static_cast<unsigned>(planes < 1 ? 1 : (planes < 65535 ? planes : 65535));
+  const unsigned ys =
+      static_cast<unsigned>(a.planes < 1 ? 1 : (a.planes < 65535 ? a.planes : 65535));
   return dsa::launch_after(dsa::fork_copy_kernel, dim3(n, ys), dsa::kCopyThreads, s, a, parents,
                            children, static_cast<const dsa::ForkPair*>(plan))
              ? DSA_OK
              : DSA_ECUDA;
+}
+
+}  // namespace
+
+extern "C" dsa_status dsa_cache_fork(void* cache, int64_t planes, int64_t plane_stride,
+                                     int64_t num_pages, int64_t page_stride, int32_t page_size,
+                                     int64_t token_bytes, int32_t* refs, int32_t* tables,
+                                     int64_t seqs, int64_t max_pages, int64_t ld_tables,
+                                     int32_t* lens, const int32_t* parents,
+                                     const int32_t* children, int64_t pairs, int32_t* status,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  const dsa::CacheArgs a{static_cast<char*>(cache), planes, plane_stride, num_pages, page_stride,
+                         page_size, token_bytes, refs, tables, seqs, max_pages, ld_tables, lens,
+                         nullptr, 0, 0, 0};
+  return fork(a, parents, children, pairs, status, workspace, workspace_bytes, stream);
+}
+
+extern "C" dsa_status dsa_cache_fork_scaled(
+    void* cache, int64_t planes, int64_t plane_stride, int64_t num_pages, int64_t page_stride,
+    int32_t page_size, int64_t token_bytes, void* scales, int64_t scale_plane_stride,
+    int64_t scale_page_stride, int64_t scale_bytes, int32_t* refs, int32_t* tables, int64_t seqs,
+    int64_t max_pages, int64_t ld_tables, int32_t* lens, const int32_t* parents,
+    const int32_t* children, int64_t pairs, int32_t* status, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  dsa::CacheArgs a{static_cast<char*>(cache), planes, plane_stride, num_pages, page_stride,
+                   page_size, token_bytes, refs, tables, seqs, max_pages, ld_tables, lens,
+                   nullptr, 0, 0, 0};
+  const dsa_status st =
+      dsa::add_scales(a, scales, scale_plane_stride, scale_page_stride, scale_bytes);
+  if (st != DSA_OK) return st;
+  return fork(a, parents, children, pairs, status, workspace, workspace_bytes, stream);
 }
 
 extern "C" dsa_status dsa_cache_free(int32_t* refs, int64_t num_pages, int32_t* tables,
@@ -385,21 +451,17 @@ extern "C" dsa_status dsa_cache_free(int32_t* refs, int64_t num_pages, int32_t* 
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
-extern "C" dsa_status dsa_cache_compact(void* cache, int64_t planes, int64_t plane_stride,
-                                        int64_t num_pages, int64_t page_stride, int32_t page_size,
-                                        int64_t token_bytes, int32_t* refs, int32_t* tables,
-                                        int64_t seqs, int64_t max_pages, int64_t ld_tables,
-                                        int32_t* remap, int32_t* live, void* workspace,
-                                        size_t workspace_bytes, void* stream) {
-  const dsa::CacheArgs a{static_cast<char*>(cache), planes, plane_stride, num_pages, page_stride,
-                         page_size, token_bytes, refs, tables, seqs, max_pages, ld_tables,
-                         nullptr};
-  dsa_status st = dsa::check_tables(num_pages, refs, tables, seqs, max_pages, ld_tables);
+namespace {
+
+dsa_status compact(const dsa::CacheArgs& a, int32_t* remap, int32_t* live, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  dsa_status st = dsa::check_tables(a.num_pages, a.refs, a.tables, a.seqs, a.max_pages,
+                                    a.ld_tables);
   if (st != DSA_OK) return st;
   st = dsa::check_cache(a);
   if (st != DSA_OK) return st;
-  if (!live || (num_pages > 0 && !remap)) return DSA_EINVAL;
-  if (!workspace || workspace_bytes < dsa::compact_bytes(num_pages) ||
+  if (!live || (a.num_pages > 0 && !remap)) return DSA_EINVAL;
+  if (!workspace || workspace_bytes < dsa::compact_bytes(a.num_pages) ||
       !dsa::aligned16(workspace))
     return DSA_EINVAL;
   int32_t* count = static_cast<int32_t*>(workspace);
@@ -412,4 +474,33 @@ extern "C" dsa_status dsa_cache_compact(void* cache, int64_t planes, int64_t pla
                            static_cast<const int2*>(moves))
              ? DSA_OK
              : DSA_ECUDA;
+}
+
+}  // namespace
+
+extern "C" dsa_status dsa_cache_compact(void* cache, int64_t planes, int64_t plane_stride,
+                                        int64_t num_pages, int64_t page_stride, int32_t page_size,
+                                        int64_t token_bytes, int32_t* refs, int32_t* tables,
+                                        int64_t seqs, int64_t max_pages, int64_t ld_tables,
+                                        int32_t* remap, int32_t* live, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  const dsa::CacheArgs a{static_cast<char*>(cache), planes, plane_stride, num_pages, page_stride,
+                         page_size, token_bytes, refs, tables, seqs, max_pages, ld_tables,
+                         nullptr, nullptr, 0, 0, 0};
+  return compact(a, remap, live, workspace, workspace_bytes, stream);
+}
+
+extern "C" dsa_status dsa_cache_compact_scaled(
+    void* cache, int64_t planes, int64_t plane_stride, int64_t num_pages, int64_t page_stride,
+    int32_t page_size, int64_t token_bytes, void* scales, int64_t scale_plane_stride,
+    int64_t scale_page_stride, int64_t scale_bytes, int32_t* refs, int32_t* tables, int64_t seqs,
+    int64_t max_pages, int64_t ld_tables, int32_t* remap, int32_t* live, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  dsa::CacheArgs a{static_cast<char*>(cache), planes, plane_stride, num_pages, page_stride,
+                   page_size, token_bytes, refs, tables, seqs, max_pages, ld_tables, nullptr,
+                   nullptr, 0, 0, 0};
+  const dsa_status st =
+      dsa::add_scales(a, scales, scale_plane_stride, scale_page_stride, scale_bytes);
+  if (st != DSA_OK) return st;
+  return compact(a, remap, live, workspace, workspace_bytes, stream);
 }

@@ -82,6 +82,25 @@ dsa_status dsa_cache_fork(void *cache, int64_t planes, int64_t plane_stride,
                           size_t workspace_bytes, void *stream);
 
 /*
+ * dsa_cache_fork_scaled -- dsa_cache_fork for pages that have scales beside them
+ * (those of dsa_quant.h): `scale_bytes` of each page n in plane p at scales +
+ * p*scale_plane_stride + n*scale_page_stride, in bytes and multiples of 4.
+ * With a partial page that is copied go all of its scales.
+ *
+ * Errors as for dsa_cache_fork, and DSA_EINVAL for negative scale sizes or NULL
+ * scales with scale_bytes > 0, DSA_EUNSUPPORTED for other multiples and for
+ * scale_bytes from 2^31.
+ */
+dsa_status dsa_cache_fork_scaled(
+    void *cache, int64_t planes, int64_t plane_stride, int64_t num_pages,
+    int64_t page_stride, int32_t page_size, int64_t token_bytes, void *scales,
+    int64_t scale_plane_stride, int64_t scale_page_stride, int64_t scale_bytes,
+    int32_t *refs, int32_t *tables, int64_t seqs, int64_t max_pages,
+    int64_t ld_tables, int32_t *lens, const int32_t *parents,
+    const int32_t *children, int64_t pairs, int32_t *status, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/*
  * dsa_cache_free -- empties the slots named in seqs_list: the refs of the
  * pages of their rows go down by one (not below 0), their rows become -1 and
  * their lengths 0. Numbers outside [0, seqs) are passed over; a slot named
@@ -113,6 +132,19 @@ dsa_status dsa_cache_compact(void *cache, int64_t planes, int64_t plane_stride,
                              int64_t max_pages, int64_t ld_tables,
                              int32_t *remap, int32_t *live, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/*
+ * dsa_cache_compact_scaled -- dsa_cache_compact for pages that have scales
+ * beside them, which follow the pages. Scales and errors as for
+ * dsa_cache_fork_scaled.
+ */
+dsa_status dsa_cache_compact_scaled(
+    void *cache, int64_t planes, int64_t plane_stride, int64_t num_pages,
+    int64_t page_stride, int32_t page_size, int64_t token_bytes, void *scales,
+    int64_t scale_plane_stride, int64_t scale_page_stride, int64_t scale_bytes,
+    int32_t *refs, int32_t *tables, int64_t seqs, int64_t max_pages,
+    int64_t ld_tables, int32_t *remap, int32_t *live, void *workspace,
+    size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -668,6 +668,97 @@ def test_parts_merge(env):
     ref.check(lse, want[1], 3 * want[3] + 2.0 ** -20, "merged lse")
 
 
+@pytest.mark.parametrize("planes,per", [(2, 3), (6, 40), (1, 700)])
+def test_fork_and_compaction_carry_scales(env, planes, per):
+    """Byte for byte: a copied partial page brings all of its scales, moved pages
+    theirs, and nothing else changes. (Pages and tables are the plain calls'.)"""
+    torch, dsa = env
+    N, page, slots, width = 40, 4, 12, 6
+    rng = np.random.default_rng(per)
+    cache = rng.integers(-30000, 30000, (planes, N, page, 2, 8)).astype(np.int16)
+    wide = rng.standard_normal((planes, N, 2, per)).astype(np.float32)  # [:, :, 1]: another layer's
+    refs, lens = np.zeros(N, np.int32), np.zeros(slots, np.int32)
+    tables = np.full((slots, width), -1, np.int32)
+    ids = list(rng.permutation(N))
+    for s in range(6):
+        lens[s] = (5, 8, 0, 23, 1, 14)[s]
+        for j in range(-(-int(lens[s]) // page)):
+            tables[s, j] = ids.pop()
+            refs[tables[s, j]] = 1
+    state = [[torch.from_numpy(x.copy()).cuda() for x in (cache, refs, tables, lens)]
+             for _ in range(2)]
+    scales = torch.from_numpy(wide.copy()).cuda()
+    pairs = ints(torch, [0, 1, 2, 3, 3, 99]), ints(torch, [6, 7, 8, 9, 10, 11])
+    a = dsa.dsa_cache_fork(*state[0], *pairs)
+    b = dsa.dsa_cache_fork(*state[1], *pairs, scales=scales[:, :, 0])
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and a.tolist() == [0, 0, 0, 0, 0, 2]
+    for x, y in zip(*state):
+        assert torch.equal(x, y)
+    after = state[0][2].cpu().numpy()
+    for p, c in ((0, 6), (3, 9), (3, 10)):      # these end inside a page
+        j = lens[p] // page
+        assert after[c, j] != tables[p, j]
+        wide[:, after[c, j], 0] = wide[:, tables[p, j], 0]
+    np.testing.assert_array_equal(scales.cpu().numpy(), wide)
+    for st in state:
+        dsa.dsa_cache_free(*st[1:], ints(torch, [1, 5, 6]))
+    used = state[0][1].cpu().numpy() > 0
+    a = dsa.dsa_cache_compact(*state[0][:3])
+    b = dsa.dsa_cache_compact(*state[1][:3], scales=scales[:, :, 0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for x, y in zip(*state):
+        assert torch.equal(x, y)
+    moved = 0
+    for src, dst in enumerate(a[0].tolist()):
+        if used[src] and dst != src:
+            wide[:, dst, 0] = wide[:, src, 0]
+            moved += 1
+    assert moved > 0
+    np.testing.assert_array_equal(scales.cpu().numpy(), wide)
+
+
+def test_forked_samples_of_an_8_bit_cache(env):
+    """A sample forked from a prompt attends to the same bits; it grows, its block's
+    scale with it, the prompt stays as it was; compaction changes no bit."""
+    torch, dsa = env
+    Hkv, D, page, block, N = 2, 64, 32, 16, 20
+    pool = Pool(torch, 60, [75] + [0] * 3, Hkv, D, page, block, spare=N - 3)
+    N = pool.codes.shape[1]
+    pool.tables = np.concatenate([pool.tables, np.full((4, 1), -1, np.int32)], 1)
+    cache, scales, tables = pool.gpu()
+    refs = torch.zeros(N, dtype=torch.int32, device="cuda")
+    refs[tables[0, :3].long()] = 1
+    lens = ints(torch, [75, 0, 0, 0])
+    q = queries(torch, 61, 4, 8, D, torch.bfloat16)
+    q[1:] = q[0]
+    c = (cache[0], cache[1], scales[0], scales[1])
+    first = dsa.dsa_quant_attention(q, *c, tables, lens)
+    status = dsa.dsa_cache_fork(cache, refs, tables, lens, ints(torch, [0, 0]),
+                                ints(torch, [2, 3]), scales=scales)
+    assert status.tolist() == [0, 0]
+    got = dsa.dsa_quant_attention(q, *c, tables, lens)
+    for i in (0, 2, 3):
+        assert torch.equal(got[0][i], first[0][0]) and torch.equal(got[1][i], first[1][0])
+    k, v = rows(torch, 62, 1, Hkv, D, torch.bfloat16)
+    dsa.dsa_quant_cache_write(k * 100, v * 100, ints(torch, [0, 0, 0, 1, 1]), *c, tables, lens)
+    lens[2] += 1
+    grown = dsa.dsa_quant_attention(q, *c, tables, lens)
+    for i in (0, 3):
+        assert torch.equal(grown[0][i], first[0][0]) and torch.equal(grown[1][i], first[1][0])
+    assert not torch.equal(grown[0][2], first[0][0])
+    host = (cache.view(torch.uint8).cpu().numpy(), scales.cpu().numpy(), tables.cpu().numpy())
+    want = quant.attend(q, *host, lens.cpu().numpy())
+    ref.check(grown[0], want[0], want[2], "out")
+    dsa.dsa_cache_free(refs, tables, lens, ints(torch, [0]))
+    dsa.dsa_cache_compact(cache, refs, tables, scales=scales)
+    moved = dsa.dsa_quant_attention(q, *c, tables, lens)
+    torch.cuda.synchronize()
+    assert int(tables.max()) == 3               # two shared pages, two of their own
+    assert torch.equal(moved[0][2:], grown[0][2:]) and torch.equal(moved[1][2:], grown[1][2:])
+
+
 def test_serving_round(env):
     """Two prompts turned by their positions and written, chunk by chunk; the
     second chunk attends to the cache read back; then decode steps, each written

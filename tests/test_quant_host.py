@@ -149,6 +149,39 @@ def test_attention_refusals(dsa, kw, want):
     assert attend(dsa.library(), **kw) == want
 
 
+def scaled(**kw):
+    a = dict(cache=FAKE, planes=2, plane_stride=2560, num_pages=10, page_stride=256, page_size=4,
+             token_bytes=64, scales=FAKE, scale_plane=160, scale_page=16, scale_bytes=16,
+             refs=FAKE, tables=FAKE, seqs=5, max_pages=6, ld_tables=6)
+    a.update({n: v for n, v in kw.items() if n in a})
+    return a
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(scales=None), DSA_EINVAL), (dict(scale_bytes=-4), DSA_EINVAL),
+    (dict(scale_plane=-4), DSA_EINVAL), (dict(scale_page=-4), DSA_EINVAL),
+    (dict(scales=ONE), DSA_EUNSUPPORTED), (dict(scale_bytes=6), DSA_EUNSUPPORTED),
+    (dict(scale_page=18), DSA_EUNSUPPORTED), (dict(scale_plane=161), DSA_EUNSUPPORTED),
+    (dict(scale_bytes=2 ** 31), DSA_EUNSUPPORTED), (dict(cache=ODD), DSA_EUNSUPPORTED),
+    (dict(refs=None), DSA_EINVAL), (dict(tables=None), DSA_EINVAL),
+    (dict(ld_tables=5), DSA_EINVAL), (dict(workspace=None), DSA_EINVAL),
+    (dict(workspace_bytes=8), DSA_EINVAL),
+], ids=str)
+def test_scaled_cache_refusals(dsa, kw, want):
+    lib, ws = dsa.library(), dict(workspace=FAKE, workspace_bytes=1 << 20, stream=None)
+    ws.update({n: v for n, v in kw.items() if n in ws})
+    assert set(kw) <= set(scaled()) | set(ws)
+    assert lib.dsa_cache_fork_scaled(*scaled(**kw).values(), FAKE, FAKE, FAKE, 3, FAKE,
+                                     *ws.values()) == want
+    assert lib.dsa_cache_compact_scaled(*scaled(**kw).values(), FAKE, FAKE, *ws.values()) == want
+
+
+def test_scales_in_the_binding(dsa):
+    x = torch.zeros(2, 5, 3)
+    with pytest.raises(ValueError, match="expected cuda:0"):
+        dsa._page_scales(x, 2, 5, 0)
+
+
 def test_workspace_sizes(dsa):
     size = dsa.quant_attention_workspace_bytes
     assert size(0, 8, 2, 64, 100, 16) == 0 and size(3, 8, 3, 64, 100, 16) == 0
