@@ -52,6 +52,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -231,15 +232,11 @@ def library():
         scaled.restype = ctypes.c_int
     lib.dsa_rotary.argtypes = [p, p, i32, i64, i64, i64, i64, p, p, i32, i64, i64, i64, i64, i32,
                                i64, i32, p, p, i32, i32, f32, i32, p]
-    rows, strides = [i64] * 4, [i64] * 8
-    lib.dsa_quant_cache_write.argtypes = [p, p, i32, i64, i32, i32, *rows, p, i32, p, p, i64, i32,
-                                          i32, *strides[:6], p, p, i64, i64, p, i64, i64, p, p]
-    lib.dsa_quant_cache_read.argtypes = [p, p, p, p, i64, i32, i32, i32, i32, *strides, p, i64,
-                                         i64, p, i32, i64, i32, p, i64, i64, p, i64, i64, p]
+    lib.dsa_quant_cache_write.argtypes = [p, p, p, i32, i64, i64, i64, i64, i64, p, i32, p, p]
+    lib.dsa_quant_cache_read.argtypes = [p, p, i32, i64, i32, p, i64, i64, p, i64, i64, p]
     lib.dsa_quant_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i32]
     lib.dsa_quant_attention_workspace_bytes.restype = sz
-    lib.dsa_quant_attention.argtypes = [p, i32, i64, i32, i32, i32, i64, i64, p, p, p, p, i64, i32,
-                                        i32, *strides, p, i64, i64, p, f32, p, i64, i64, p, i64,
+    lib.dsa_quant_attention.argtypes = [p, p, i32, i64, i32, i64, i64, p, f32, p, i64, i64, p, i64,
                                         i64, p, sz, p]
     for f in (lib.dsa_prompt_attention, lib.dsa_shared_prefix_attention, lib.dsa_cache_fork,
               lib.dsa_cache_free, lib.dsa_cache_compact, lib.dsa_rotary, lib.dsa_quant_cache_write,
@@ -293,9 +290,15 @@ def max_select_blocks() -> int:
     return int(library().dsa_select_max_blocks())
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def workspace_bytes(rows: int, nblocks: int) -> int:
@@ -1176,33 +1179,61 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
     return _call(dev, stream, enqueue)
 
 
-def _quant_pool(k_pages, v_pages, k_scales, v_scales, tables, index):
-    """Addresses, sizes and strides of the pages, scales and tables of an 8-bit
-    cache on device ``index``."""
+# struct dsa_quant_pages
+_QUANT_PAGES = struct.Struct("4Q9qQ2q4i")
+
+
+def _quant_pages(k_pages, v_pages, k_scales, v_scales, tables, index):
+    """The pages, scales and tables of an 8-bit cache on device ``index`` as a
+    dsa_quant_pages, and their sizes: rows and columns of the tables, tokens of
+    a page, heads and head dimension."""
     torch = _torch()
-    kp, shape, kst = _on_gpu(k_pages, torch.float8_e4m3fn, "k_pages", 4, index)
-    vp, vshape, vst = _on_gpu(v_pages, torch.float8_e4m3fn, "v_pages", 4, index)
+    shape, sshape, tshape = k_pages.shape, k_scales.shape, tables.shape
+    kst, vst, ks, vs, tst = (k_pages.stride(), v_pages.stride(), k_scales.stride(),
+                             v_scales.stride(), tables.stride())
+    # the usual layout takes these few steps; any other all of the checks
+    if not (k_pages.dtype is torch.float8_e4m3fn and v_pages.dtype is torch.float8_e4m3fn
+            and k_scales.dtype is torch.float32 and v_scales.dtype is torch.float32
+            and tables.dtype is torch.int32 and len(shape) == 4 and len(sshape) == 3
+            and len(tshape) == 2 and v_pages.shape == shape and v_scales.shape == sshape
+            and sshape[0] == shape[0] and sshape[2] == shape[2] and sshape[1] > 0
+            and shape[1] % sshape[1] == 0 and kst[3] == vst[3] == ks[2] == vs[2] == tst[1] == 1
+            and ks[1] == vs[1] == shape[2] and 1 not in shape and tshape[0] > 1
+            and k_pages.get_device() == v_pages.get_device() == k_scales.get_device()
+            == v_scales.get_device() == tables.get_device() == index >= 0):
+        kst, vst, ks, vs, tst = _quant_checks(k_pages, v_pages, k_scales, v_scales, tables, index)
+    (N, page, Hkv, D), (S, P) = shape, tshape
+    return _QUANT_PAGES.pack(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                             v_scales.data_ptr(), N, kst[0], kst[1], kst[2], vst[0], vst[1],
+                             vst[2], ks[0], vs[0], tables.data_ptr(), P, tst[0], page,
+                             page // sshape[1], Hkv, D), S, P, page, Hkv, D
+
+
+def _quant_checks(k_pages, v_pages, k_scales, v_scales, tables, index):
+    """What is wrong with them is raised; their strides, where a dimension of one
+    element has one that will do."""
+    torch = _torch()
+    _, shape, kst = _on_gpu(k_pages, torch.float8_e4m3fn, "k_pages", 4, index)
+    _, vshape, vst = _on_gpu(v_pages, torch.float8_e4m3fn, "v_pages", 4, index)
     if vshape != shape:
         raise ValueError(f"k_pages {tuple(shape)} and v_pages {tuple(vshape)} do not match")
     N, page, Hkv, D = shape
     scales = []
     for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        sp, (n, per, heads), st = _on_gpu(t, torch.float32, name, 3, index)
+        _, (n, per, heads), st = _on_gpu(t, torch.float32, name, 3, index)
         if n != N or heads != Hkv or per < 1 or page % per:
             raise ValueError(f"{name} must be [{N}, page / block, {Hkv}], got {tuple(t.shape)}")
         if (heads > 1 and st[2] != 1) or (per > 1 and st[1] != heads):
             raise ValueError(f"the pages of {name} must be contiguous")
-        scales.append((sp, per, st[0] if n > 1 else per * heads))
-    (ksp, per, ksn), (vsp, vper, vsn) = scales
-    if vper != per:
+        scales.append((st[0] if n > 1 else per * heads,))
+    if k_scales.shape != v_scales.shape:
         raise ValueError(f"k_scales {tuple(k_scales.shape)} and v_scales {tuple(v_scales.shape)} "
                          "do not match")
-    tp, (S, P), tst = _on_gpu(tables, torch.int32, "tables", 2, index)
+    _, (S, P), tst = _on_gpu(tables, torch.int32, "tables", 2, index)
     if P > 1 and tst[1] != 1:
         raise ValueError("tables must have unit stride in its last dimension")
-    return ((kp, vp), (ksp, vsp), (N, page, page // per), (Hkv, D),
-            (*_row_strides(shape, kst, "k_pages"), *_row_strides(shape, vst, "v_pages")),
-            (ksn, vsn), (tp, P, tst[0] if S > 1 else P), S)
+    return (_row_strides(shape, kst, "k_pages"), _row_strides(shape, vst, "v_pages"), *scales,
+            (tst[0] if S > 1 else P,))
 
 
 def dsa_quant_cache_write(k, v, cu, k_pages, v_pages, k_scales, v_scales, tables, lens, *,
@@ -1222,17 +1253,15 @@ def dsa_quant_cache_write(k, v, cu, k_pages, v_pages, k_scales, v_scales, tables
     dt, dev = k.dtype, k.get_device()
     kp, ks, kst = _on_gpu(k, dt, "k", 3)
     vp, vs, vst = _on_gpu(v, dt, "v", 3, dev)
-    pages, scales, sizes, heads, strides, steps, table, S = _quant_pool(k_pages, v_pages, k_scales,
-                                                                        v_scales, tables, dev)
-    if ks != vs or ks[1:] != heads:
+    pages, S, _, _, Hkv, D = _quant_pages(k_pages, v_pages, k_scales, v_scales, tables, dev)
+    if ks != vs or ks[1] != Hkv or ks[2] != D:
         raise ValueError(f"k {tuple(ks)}, v {tuple(vs)} and pages {tuple(k_pages.shape)} do not "
                          "match")
     (cp, nc), (lp, n) = _vector(cu, "cu", dev), _vector(lens, "lens", dev)
     if nc != S + 1 or n != S:
         raise ValueError(f"cu holds {nc} offsets and lens {n} lengths for {S} rows of tables")
-    st = _call(dev, stream, library().dsa_quant_cache_write, kp, vp, code, ks[0], *heads,
-               *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cp, S, *pages, *sizes,
-               *strides, *scales, *steps, *table, lp)
+    st = _call(dev, stream, library().dsa_quant_cache_write, pages, kp, vp, code, ks[0],
+               *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cp, S, lp)
     if st:
         _check("dsa_quant_cache_write", st)
 
@@ -1250,43 +1279,51 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
     as they were, those of tokens without a page are 0."""
     torch = _torch()
     dev = k_pages.get_device()
-    pages, scales, sizes, heads, strides, steps, table, S = _quant_pool(
-        k_pages, v_pages, k_scales, v_scales, tables, None if dev < 0 else dev)
+    pages, S, _, _, Hkv, D = _quant_pages(k_pages, v_pages, k_scales, v_scales, tables,
+                                          None if dev < 0 else dev)
     cp, nc = _vector(cu, "cu", dev)
     if nc != S + 1:
         raise ValueError(f"cu holds {nc} offsets for {S} rows of tables")
-    given = [t for t in (k_out, v_out) if t is not None]
-    if given:
-        if total is not None and total != given[0].shape[0]:
-            raise ValueError(f"total is {total}, the output has {given[0].shape[0]} rows")
-        if dtype is not None and dtype is not given[0].dtype:
-            raise TypeError(f"dtype is {dtype}, the output {given[0].dtype}")
-        total, dtype = given[0].shape[0], given[0].dtype
-    elif total is None:
-        raise ValueError("total, the number of rows, is needed where no output is given")
-    total, dtype = int(total), torch.bfloat16 if dtype is None else dtype
-    if total < 0:
-        raise ValueError(f"total must not be negative, got {total}")
-    shape = (total, *heads)
+    given = k_out if k_out is not None else v_out
+    if given is not None:
+        if total is not None and total != given.shape[0]:
+            raise ValueError(f"total is {total}, the output has {given.shape[0]} rows")
+        if dtype is not None and dtype is not given.dtype:
+            raise TypeError(f"dtype is {dtype}, the output {given.dtype}")
+        total, dtype = given.shape[0], given.dtype
+        code = _attention_dtype(given, "k_out" if given is k_out else "v_out")
+    else:
+        if total is None:
+            raise ValueError("total, the number of rows, is needed where no output is given")
+        total = int(total)
+        if total < 0:
+            raise ValueError(f"total must not be negative, got {total}")
+        if dtype is None or dtype is torch.bfloat16:
+            dtype, code = torch.bfloat16, DTYPE_BF16
+        elif dtype is torch.float16:
+            code = DTYPE_F16
+        else:
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+    shape = (total, Hkv, D)
 
-    def enqueue(k_out, v_out, handle):
-        outs, args = [], []
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=k_pages.device)
-            code = _attention_dtype(t, name)
-            op, oshape, ost = _on_gpu(t, dtype, name, 3, dev)
-            if oshape != shape:
-                raise ValueError(f"{name} must be {shape}, got {tuple(oshape)}")
-            outs.append(t)
-            args += [op, *_row_strides(oshape, ost, name)]
-        st = library().dsa_quant_cache_read(*pages, *scales, *sizes, *heads, *strides, *steps,
-                                            *table, cp, S, total, code, *args, handle)
+    def output(t, name):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=k_pages.device)
+            return t, t.data_ptr() or None, Hkv * D, D
+        op, oshape, ost = _on_gpu(t, dtype, name, 3, dev)
+        if oshape != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(oshape)}")
+        return t, op, *_row_strides(oshape, ost, name)
+
+    def enqueue(handle):
+        k, *ka = output(k_out, "k_out")
+        v, *va = output(v_out, "v_out")
+        st = library().dsa_quant_cache_read(pages, cp, S, total, code, *ka, *va, handle)
         if st:
             _check("dsa_quant_cache_read", st)
-        return outs[0], outs[1]
+        return k, v
 
-    return _call(dev, stream, enqueue, k_out, v_out)
+    return _call(dev, stream, enqueue)
 
 
 def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *, scale=None,
@@ -1305,24 +1342,23 @@ def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *
     code = _attention_dtype(q, "q")
     dev = q.get_device()
     qp, qs, qst = _on_gpu(q, q.dtype, "q", 3)
-    pages, scales, sizes, heads, strides, steps, table, S = _quant_pool(k_pages, v_pages, k_scales,
-                                                                        v_scales, tables, dev)
+    pages, S, P, page, Hkv, Dk = _quant_pages(k_pages, v_pages, k_scales, v_scales, tables, dev)
     B, H, D = qs
     lp, n = _vector(lens, "lens", dev)
-    if D != heads[1]:
+    if D != Dk:
         raise ValueError(f"q {tuple(qs)} and pages {tuple(k_pages.shape)} do not match")
     if n != B or S != B:
         raise ValueError(f"tables {tuple(tables.shape)} and lens {tuple(lens.shape)} do not "
                          f"match q {tuple(qs)}")
-    args = (qp, code, B, H, *heads, *_row_strides(qs, qst, "q"), *pages, *scales, *sizes, *strides,
-            *steps, *table, lp, _scale(scale, D))
+    qst = _row_strides(qs, qst, "q")
 
     def enqueue(out, lse_out, handle):
         out, lse_out, outs = _attention_outputs(q, qs, dev, out, lse_out)
         held, ws, ws_bytes = _scratch(
-            workspace, _need("dsa_quant_attention_workspace_bytes", dev, B, H, heads[0], D,
-                             table[1], sizes[1]), q, handle)
-        st = library().dsa_quant_attention(*args, *outs, ws, ws_bytes, handle)
+            workspace, _need("dsa_quant_attention_workspace_bytes", dev, B, H, Hkv, D, P, page), q,
+            handle)
+        st = library().dsa_quant_attention(pages, qp, code, B, H, *qst, lp, _scale(scale, D), *outs,
+                                           ws, ws_bytes, handle)
         if st:
             _check("dsa_quant_attention", st)
         return out, lse_out

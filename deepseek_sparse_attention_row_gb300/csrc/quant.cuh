@@ -35,48 +35,47 @@ inline int32_t floor_log2(int64_t n) {
 }
 
 // Fills `p` from a call's arguments; the status of what is wrong with them.
-inline dsa_status quant_pool(QuantPool& p, const void* k_codes, const void* v_codes,
-                             const float* k_scales, const float* v_scales, int64_t num_pages,
-                             int32_t page_size, int32_t block, int32_t kv_heads, int32_t head_dim,
-                             const int64_t (&strides)[6], int64_t ks_sn, int64_t vs_sn,
-                             const int32_t* tables, int64_t max_pages, int64_t ld_tables,
-                             int64_t seqs) {
-  if (num_pages < 0 || page_size < 1 || block < 1 || kv_heads < 0 || head_dim < 1 ||
-      max_pages < 0 || ld_tables < max_pages || ks_sn < 0 || vs_sn < 0)
+inline dsa_status quant_pool(QuantPool& p, const dsa_quant_pages* pages, int64_t seqs) {
+  if (!pages) return DSA_EINVAL;
+  const dsa_quant_pages& x = *pages;
+  if (x.num_pages < 0 || x.page_size < 1 || x.block < 1 || x.kv_heads < 0 || x.head_dim < 1 ||
+      x.max_pages < 0 || x.ld_tables < x.max_pages || x.ks_sn < 0 || x.vs_sn < 0)
     return DSA_EINVAL;
-  if (page_size % block != 0) return DSA_EINVAL;
-  if (num_pages > INT32_MAX || max_pages > INT32_MAX || page_size < 16 ||
-      (page_size & (page_size - 1)) != 0 || (block & (block - 1)) != 0 ||
-      max_pages * page_size > INT32_MAX || head_dim > 128 || head_dim % 16 != 0 ||
-      kv_heads > kMaxKvHeads)
+  if (x.page_size % x.block != 0) return DSA_EINVAL;
+  if (x.num_pages > INT32_MAX || x.max_pages > INT32_MAX || x.page_size < 16 ||
+      (x.page_size & (x.page_size - 1)) != 0 || (x.block & (x.block - 1)) != 0 ||
+      x.max_pages * x.page_size > INT32_MAX || x.head_dim > 128 || x.head_dim % 16 != 0 ||
+      x.kv_heads > kMaxKvHeads)
     return DSA_EUNSUPPORTED;
-  if (num_pages > 0 && (!k_codes || !v_codes || !k_scales || !v_scales)) return DSA_EINVAL;
-  if (max_pages > 0 && seqs > 0 && !tables) return DSA_EINVAL;
-  if (!quant_aligned16(k_codes) || !quant_aligned16(v_codes)) return DSA_EUNSUPPORTED;
-  if (((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u) != 0)
+  if (x.num_pages > 0 && (!x.k_codes || !x.v_codes || !x.k_scales || !x.v_scales))
+    return DSA_EINVAL;
+  if (x.max_pages > 0 && seqs > 0 && !x.tables) return DSA_EINVAL;
+  if (!quant_aligned16(x.k_codes) || !quant_aligned16(x.v_codes)) return DSA_EUNSUPPORTED;
+  if (((reinterpret_cast<uintptr_t>(x.k_scales) | reinterpret_cast<uintptr_t>(x.v_scales)) & 3u) !=
+      0)
     return DSA_EUNSUPPORTED;
-  for (int64_t s : strides)
+  for (int64_t s : {x.kc_sn, x.kc_st, x.kc_sh, x.vc_sn, x.vc_st, x.vc_sh})
     if (s < 0 || s % 16 != 0) return DSA_EUNSUPPORTED;
-  // not written through by the calls that only read
-  p.codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
-  p.codes[1] = static_cast<uint8_t*>(const_cast<void*>(v_codes));
-  p.scales[0] = const_cast<float*>(k_scales);
-  p.scales[1] = const_cast<float*>(v_scales);
-  for (int i = 0; i < 2; ++i) {
-    p.sn[i] = strides[3 * i];
-    p.st[i] = strides[3 * i + 1];
-    p.sh[i] = strides[3 * i + 2];
-  }
-  p.ssn[0] = ks_sn;
-  p.ssn[1] = vs_sn;
-  p.num_pages = num_pages;
-  p.page_log2 = floor_log2(page_size);
-  p.block_log2 = floor_log2(block);
-  p.kv_heads = kv_heads;
-  p.dim = head_dim;
-  p.tables = tables;
-  p.max_pages = max_pages;
-  p.ld_tables = ld_tables;
+  p.codes[0] = static_cast<uint8_t*>(x.k_codes);
+  p.codes[1] = static_cast<uint8_t*>(x.v_codes);
+  p.scales[0] = x.k_scales;
+  p.scales[1] = x.v_scales;
+  p.sn[0] = x.kc_sn;
+  p.st[0] = x.kc_st;
+  p.sh[0] = x.kc_sh;
+  p.sn[1] = x.vc_sn;
+  p.st[1] = x.vc_st;
+  p.sh[1] = x.vc_sh;
+  p.ssn[0] = x.ks_sn;
+  p.ssn[1] = x.vs_sn;
+  p.num_pages = x.num_pages;
+  p.page_log2 = floor_log2(x.page_size);
+  p.block_log2 = floor_log2(x.block);
+  p.kv_heads = x.kv_heads;
+  p.dim = x.head_dim;
+  p.tables = x.tables;
+  p.max_pages = x.max_pages;
+  p.ld_tables = x.ld_tables;
   return DSA_OK;
 }
 

@@ -135,23 +135,19 @@ extern "C" size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t hea
   return p.fits ? p.bytes : 0;
 }
 
-extern "C" dsa_status dsa_quant_attention(
-    const void* q, int32_t dtype, int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,
-    int64_t q_sb, int64_t q_sh, const void* k_codes, const void* v_codes, const float* k_scales,
-    const float* v_scales, int64_t num_pages, int32_t page_size, int32_t block, int64_t kc_sn,
-    int64_t kc_st, int64_t kc_sh, int64_t vc_sn, int64_t vc_st, int64_t vc_sh, int64_t ks_sn,
-    int64_t vs_sn, const int32_t* tables, int64_t max_pages, int64_t ld_tables,
-    const int32_t* lens, float scale, void* out, int64_t o_sb, int64_t o_sh, float* lse,
-    int64_t l_sb, int64_t l_sh, void* workspace, size_t workspace_bytes, void* stream) {
+extern "C" dsa_status dsa_quant_attention(const dsa_quant_pages* pages, const void* q,
+                                          int32_t dtype, int64_t batch, int32_t heads,
+                                          int64_t q_sb, int64_t q_sh, const int32_t* lens,
+                                          float scale, void* out, int64_t o_sb, int64_t o_sh,
+                                          float* lse, int64_t l_sb, int64_t l_sh, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
   if (dtype != DSA_DTYPE_F32 && dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_F16)
     return DSA_EINVAL;
   if (!(scale > 0.f) || !std::isfinite(scale * dsa::kLog2e)) return DSA_EINVAL;
   dsa::QuantAttnArgs a{};
-  dsa_status st = dsa::quant_pool(a.pool, k_codes, v_codes, k_scales, v_scales, num_pages,
-                                  page_size, block, kv_heads, head_dim,
-                                  {kc_sn, kc_st, kc_sh, vc_sn, vc_st, vc_sh}, ks_sn, vs_sn, tables,
-                                  max_pages, ld_tables, batch);
+  dsa_status st = dsa::quant_pool(a.pool, pages, batch);
   if (st != DSA_OK) return st;
+  const int32_t kv_heads = a.pool.kv_heads;
   st = dsa::check_sizes(batch, heads, kv_heads);
   if (st != DSA_OK) return st;
   if (dtype == DSA_DTYPE_F32) return DSA_EUNSUPPORTED;
@@ -161,12 +157,12 @@ extern "C" dsa_status dsa_quant_attention(
   for (int64_t s : {q_sb, q_sh, o_sb, o_sh})
     if (s < 0 || s % 8 != 0) return DSA_EUNSUPPORTED;
   const dsa::QuantPlan p =
-      dsa::plan_attention(batch, heads, kv_heads, head_dim, max_pages, page_size);
+      dsa::plan_attention(batch, heads, kv_heads, a.pool.dim, a.pool.max_pages, pages->page_size);
   if (!p.fits) return DSA_EUNSUPPORTED;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes ||
                       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return DSA_EINVAL;
-  if (num_pages == 0) a.pool.max_pages = 0;  // nothing is seen
+  if (a.pool.num_pages == 0) a.pool.max_pages = 0;  // nothing is seen
   a.q = q;
   a.q_sb = q_sb;
   a.q_sh = q_sh;

@@ -328,25 +328,21 @@ dsa_status check_rows(const void* k, const void* v, int32_t dtype, int64_t total
 }  // namespace
 }  // namespace dsa
 
-extern "C" dsa_status dsa_quant_cache_write(
-    const void* k, const void* v, int32_t dtype, int64_t total, int32_t kv_heads, int32_t head_dim,
-    int64_t k_st, int64_t k_sh, int64_t v_st, int64_t v_sh, const int32_t* cu, int32_t seqs,
-    void* k_codes, void* v_codes, int64_t num_pages, int32_t page_size, int32_t block,
-    int64_t kc_sn, int64_t kc_st, int64_t kc_sh, int64_t vc_sn, int64_t vc_st, int64_t vc_sh,
-    float* k_scales, float* v_scales, int64_t ks_sn, int64_t vs_sn, const int32_t* tables,
-    int64_t max_pages, int64_t ld_tables, const int32_t* lens, void* stream) {
+extern "C" dsa_status dsa_quant_cache_write(const dsa_quant_pages* pages, const void* k,
+                                            const void* v, int32_t dtype, int64_t total,
+                                            int64_t k_st, int64_t k_sh, int64_t v_st,
+                                            int64_t v_sh, const int32_t* cu, int32_t seqs,
+                                            const int32_t* lens, void* stream) {
   dsa::WriteArgs a{};
-  dsa_status st = dsa::quant_pool(a.pool, k_codes, v_codes, k_scales, v_scales, num_pages,
-                                  page_size, block, kv_heads, head_dim,
-                                  {kc_sn, kc_st, kc_sh, vc_sn, vc_st, vc_sh}, ks_sn, vs_sn, tables,
-                                  max_pages, ld_tables, seqs);
+  dsa_status st = dsa::quant_pool(a.pool, pages, seqs);
   if (st != DSA_OK) return st;
-  st = dsa::check_rows(k, v, dtype, total, k_st, k_sh, v_st, v_sh, cu, seqs, kv_heads);
+  st = dsa::check_rows(k, v, dtype, total, k_st, k_sh, v_st, v_sh, cu, seqs, a.pool.kv_heads);
   if (st != DSA_OK) return st;
+  const int32_t kv_heads = a.pool.kv_heads, block = 1 << a.pool.block_log2;
   if (block > 256) return DSA_EUNSUPPORTED;
   if (total == 0 || seqs == 0 || kv_heads == 0) return DSA_OK;
   if (!lens) return DSA_EINVAL;
-  if (max_pages == 0 || num_pages == 0) return DSA_OK;
+  if (a.pool.max_pages == 0 || a.pool.num_pages == 0) return DSA_OK;
   a.x[0] = k;
   a.x[1] = v;
   a.xt[0] = k_st;
@@ -361,7 +357,7 @@ extern "C" dsa_status dsa_quant_cache_write(
   if (items > INT32_MAX) return DSA_EUNSUPPORTED;
   // A team's registers hold the new tokens that a block gets on average, if few
   // come to a sequence.
-  const int64_t rows = 32 / (head_dim / 8) * dsa::kAtOnce, mean = (total + seqs - 1) / seqs;
+  const int64_t rows = 32 / (a.pool.dim / 8) * dsa::kAtOnce, mean = (total + seqs - 1) / seqs;
   int team = 1;
   while (team < 16 && team * rows < (mean < block ? mean : block)) team *= 2;
   const int warps = team > dsa::kWriteWarps ? team : dsa::kWriteWarps;
@@ -375,22 +371,16 @@ extern "C" dsa_status dsa_quant_cache_write(
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ECUDA;
 }
 
-extern "C" dsa_status dsa_quant_cache_read(
-    const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
-    int64_t num_pages, int32_t page_size, int32_t block, int32_t kv_heads, int32_t head_dim,
-    int64_t kc_sn, int64_t kc_st, int64_t kc_sh, int64_t vc_sn, int64_t vc_st, int64_t vc_sh,
-    int64_t ks_sn, int64_t vs_sn, const int32_t* tables, int64_t max_pages, int64_t ld_tables,
-    const int32_t* cu, int32_t seqs, int64_t total, int32_t dtype, void* k, int64_t k_st,
-    int64_t k_sh, void* v, int64_t v_st, int64_t v_sh, void* stream) {
+extern "C" dsa_status dsa_quant_cache_read(const dsa_quant_pages* pages, const int32_t* cu,
+                                           int32_t seqs, int64_t total, int32_t dtype, void* k,
+                                           int64_t k_st, int64_t k_sh, void* v, int64_t v_st,
+                                           int64_t v_sh, void* stream) {
   dsa::ReadArgs a{};
-  dsa_status st = dsa::quant_pool(a.pool, k_codes, v_codes, k_scales, v_scales, num_pages,
-                                  page_size, block, kv_heads, head_dim,
-                                  {kc_sn, kc_st, kc_sh, vc_sn, vc_st, vc_sh}, ks_sn, vs_sn, tables,
-                                  max_pages, ld_tables, seqs);
+  dsa_status st = dsa::quant_pool(a.pool, pages, seqs);
   if (st != DSA_OK) return st;
-  st = dsa::check_rows(k, v, dtype, total, k_st, k_sh, v_st, v_sh, cu, seqs, kv_heads);
+  st = dsa::check_rows(k, v, dtype, total, k_st, k_sh, v_st, v_sh, cu, seqs, a.pool.kv_heads);
   if (st != DSA_OK) return st;
-  if (total == 0 || seqs == 0 || kv_heads == 0) return DSA_OK;
+  if (total == 0 || seqs == 0 || a.pool.kv_heads == 0) return DSA_OK;
   a.x[0] = k;
   a.x[1] = v;
   a.xt[0] = k_st;

@@ -35,6 +35,19 @@
 extern "C" {
 #endif
 
+/* The pages of one layer's keys and values, and the sequences on them, as above. */
+typedef struct {
+    void *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    int64_t num_pages;
+    int64_t kc_sn, kc_st, kc_sh; /* bytes */
+    int64_t vc_sn, vc_st, vc_sh;
+    int64_t ks_sn, vs_sn; /* floats */
+    const int32_t *tables;
+    int64_t max_pages, ld_tables;
+    int32_t page_size, block, kv_heads, head_dim;
+} dsa_quant_pages;
+
 /*
  * dsa_quant_cache_write -- appends tokens to sequences.
  *
@@ -64,21 +77,17 @@ extern "C" {
  *
  * total == 0, seqs == 0 or kv_heads == 0: DSA_OK, nothing written. DSA_EINVAL
  * for an unknown dtype, negative sizes, page_size, block or head_dim < 1, a
- * block that does not divide page_size, ld_tables below max_pages, or a NULL
- * required pointer. DSA_EUNSUPPORTED for DSA_DTYPE_F32, layouts and sizes
+ * block that does not divide page_size, ld_tables below max_pages, NULL pages or a
+ * NULL required pointer. DSA_EUNSUPPORTED for DSA_DTYPE_F32, layouts and sizes
  * other than above, k or v not 16-byte aligned or with strides that are no
  * multiples of 8 elements, a block over 256, and sizes from 2^31 (seqs from
  * 2^28).
  */
-dsa_status dsa_quant_cache_write(
-    const void *k, const void *v, int32_t dtype, int64_t total,
-    int32_t kv_heads, int32_t head_dim, int64_t k_st, int64_t k_sh,
-    int64_t v_st, int64_t v_sh, const int32_t *cu, int32_t seqs, void *k_codes,
-    void *v_codes, int64_t num_pages, int32_t page_size, int32_t block,
-    int64_t kc_sn, int64_t kc_st, int64_t kc_sh, int64_t vc_sn, int64_t vc_st,
-    int64_t vc_sh, float *k_scales, float *v_scales, int64_t ks_sn,
-    int64_t vs_sn, const int32_t *tables, int64_t max_pages, int64_t ld_tables,
-    const int32_t *lens, void *stream);
+dsa_status dsa_quant_cache_write(const dsa_quant_pages *pages, const void *k,
+                                 const void *v, int32_t dtype, int64_t total,
+                                 int64_t k_st, int64_t k_sh, int64_t v_st,
+                                 int64_t v_sh, const int32_t *cu, int32_t seqs,
+                                 const int32_t *lens, void *stream);
 
 /*
  * dsa_quant_cache_read -- the first tokens of each sequence as packed rows
@@ -93,15 +102,10 @@ dsa_status dsa_quant_cache_write(
  *           have no page, or lie behind max_pages * page_size, are 0.
  * Both may not overlap. Errors as for dsa_quant_cache_write.
  */
-dsa_status dsa_quant_cache_read(
-    const void *k_codes, const void *v_codes, const float *k_scales,
-    const float *v_scales, int64_t num_pages, int32_t page_size, int32_t block,
-    int32_t kv_heads, int32_t head_dim, int64_t kc_sn, int64_t kc_st,
-    int64_t kc_sh, int64_t vc_sn, int64_t vc_st, int64_t vc_sh, int64_t ks_sn,
-    int64_t vs_sn, const int32_t *tables, int64_t max_pages, int64_t ld_tables,
-    const int32_t *cu, int32_t seqs, int64_t total, int32_t dtype, void *k,
-    int64_t k_st, int64_t k_sh, void *v, int64_t v_st, int64_t v_sh,
-    void *stream);
+dsa_status dsa_quant_cache_read(const dsa_quant_pages *pages, const int32_t *cu,
+                                int32_t seqs, int64_t total, int32_t dtype,
+                                void *k, int64_t k_st, int64_t k_sh, void *v,
+                                int64_t v_st, int64_t v_sh, void *stream);
 
 /*
  * Bytes of device workspace of a dsa_quant_attention call with these sizes on
@@ -154,16 +158,13 @@ size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t heads,
  * kv_heads times the 32-token tiles that a row of `tables` has room for passes 2.5 *
  * 10^8, or batch * heads 10^9.
  */
-dsa_status dsa_quant_attention(
-    const void *q, int32_t dtype, int64_t batch, int32_t heads,
-    int32_t kv_heads, int32_t head_dim, int64_t q_sb, int64_t q_sh,
-    const void *k_codes, const void *v_codes, const float *k_scales,
-    const float *v_scales, int64_t num_pages, int32_t page_size, int32_t block,
-    int64_t kc_sn, int64_t kc_st, int64_t kc_sh, int64_t vc_sn, int64_t vc_st,
-    int64_t vc_sh, int64_t ks_sn, int64_t vs_sn, const int32_t *tables,
-    int64_t max_pages, int64_t ld_tables, const int32_t *lens, float scale,
-    void *out, int64_t o_sb, int64_t o_sh, float *lse, int64_t l_sb,
-    int64_t l_sh, void *workspace, size_t workspace_bytes, void *stream);
+dsa_status dsa_quant_attention(const dsa_quant_pages *pages, const void *q,
+                               int32_t dtype, int64_t batch, int32_t heads,
+                               int64_t q_sb, int64_t q_sh, const int32_t *lens,
+                               float scale, void *out, int64_t o_sb,
+                               int64_t o_sh, float *lse, int64_t l_sb,
+                               int64_t l_sh, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -61,37 +61,53 @@ def test_rotary_refusals(dsa, kw, want):
     assert rotary(dsa.library(), **kw) == want
 
 
-POOL = dict(k_codes=FAKE, v_codes=FAKE, k_scales=FAKE, v_scales=FAKE, num_pages=20, page_size=16,
-            block=8, kv_heads=2, head_dim=64)
-STRIDES = dict(kc_sn=2048, kc_st=128, kc_sh=64, vc_sn=2048, vc_st=128, vc_sh=64, ks_sn=4, vs_sn=4)
-TABLES = dict(tables=FAKE, max_pages=6, ld_tables=6)
+class Pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] + \
+        [(n, ctypes.c_int64) for n in ("num_pages", "kc_sn", "kc_st", "kc_sh", "vc_sn", "vc_st",
+                                       "vc_sh", "ks_sn", "vs_sn")] + \
+        [("tables", ctypes.c_void_p), ("max_pages", ctypes.c_int64),
+         ("ld_tables", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("page_size", "block", "kv_heads", "head_dim")]
+
+
+PAGES = dict(k_codes=FAKE, v_codes=FAKE, k_scales=FAKE, v_scales=FAKE, num_pages=20, kc_sn=2048,
+             kc_st=128, kc_sh=64, vc_sn=2048, vc_st=128, vc_sh=64, ks_sn=4, vs_sn=4, tables=FAKE,
+             max_pages=6, ld_tables=6, page_size=16, block=8, kv_heads=2, head_dim=64)
+
+
+def on_pages(fn, a, kw):
+    """fn with the keywords of PAGES in its first argument, or as that argument."""
+    pages = {**PAGES, **{n: v for n, v in kw.items() if n in PAGES}}
+    pages = ctypes.byref(Pages(*pages.values())) if kw.get("pages", 1) else None
+    return call(fn, dict(pages=pages, **a), {n: v for n, v in kw.items()
+                                             if n not in PAGES and n != "pages"})
 
 
 def write(lib, **kw):
-    p = dict(POOL)
-    return call(lib.dsa_quant_cache_write, dict(
-        k=FAKE, v=FAKE, dtype=BF16, total=10, kv_heads=p["kv_heads"], head_dim=p["head_dim"],
-        k_st=128, k_sh=64, v_st=128, v_sh=64, cu=FAKE, seqs=3, k_codes=FAKE, v_codes=FAKE,
-        num_pages=20, page_size=16, block=8,
-        **{n: STRIDES[n] for n in ("kc_sn", "kc_st", "kc_sh", "vc_sn", "vc_st", "vc_sh")},
-        k_scales=FAKE, v_scales=FAKE, ks_sn=4, vs_sn=4, **TABLES, lens=FAKE, stream=None), kw)
+    return on_pages(lib.dsa_quant_cache_write, dict(
+        k=FAKE, v=FAKE, dtype=BF16, total=10, k_st=128, k_sh=64, v_st=128, v_sh=64, cu=FAKE,
+        seqs=3, lens=FAKE, stream=None), kw)
 
 
 def read(lib, **kw):
-    return call(lib.dsa_quant_cache_read, dict(
-        **POOL, **STRIDES, **TABLES, cu=FAKE, seqs=3, total=10, dtype=BF16, k=FAKE, k_st=128,
-        k_sh=64, v=FAKE, v_st=128, v_sh=64, stream=None), kw)
+    return on_pages(lib.dsa_quant_cache_read, dict(
+        cu=FAKE, seqs=3, total=10, dtype=BF16, k=FAKE, k_st=128, k_sh=64, v=FAKE, v_st=128,
+        v_sh=64, stream=None), kw)
 
 
 def attend(lib, **kw):
-    p = {n: v for n, v in POOL.items() if n not in ("kv_heads", "head_dim")}
-    return call(lib.dsa_quant_attention, dict(
-        q=FAKE, dtype=BF16, batch=3, heads=8, kv_heads=2, head_dim=64, q_sb=512, q_sh=64, **p,
-        **STRIDES, **TABLES, lens=FAKE, scale=0.125, out=FAKE, o_sb=512, o_sh=64, lse=None,
-        l_sb=8, l_sh=1, workspace=FAKE, workspace_bytes=1 << 40, stream=None), kw)
+    return on_pages(lib.dsa_quant_attention, dict(
+        q=FAKE, dtype=BF16, batch=3, heads=8, q_sb=512, q_sh=64, lens=FAKE, scale=0.125, out=FAKE,
+        o_sb=512, o_sh=64, lse=None, l_sb=8, l_sh=1, workspace=FAKE, workspace_bytes=1 << 40,
+        stream=None), kw)
+
+
+def test_the_binding_packs_the_struct(dsa):
+    assert dsa._QUANT_PAGES.size == ctypes.sizeof(Pages) == 144
 
 
 COMMON = [
+    (dict(pages=0), DSA_EINVAL),
     (dict(num_pages=-1), DSA_EINVAL), (dict(page_size=0), DSA_EINVAL), (dict(block=0), DSA_EINVAL),
     (dict(block=32), DSA_EINVAL), (dict(head_dim=0), DSA_EINVAL), (dict(max_pages=-1), DSA_EINVAL),
     (dict(ld_tables=5), DSA_EINVAL), (dict(ks_sn=-1), DSA_EINVAL),
