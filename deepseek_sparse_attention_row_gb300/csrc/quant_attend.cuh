@@ -248,7 +248,9 @@ struct QuantWarp {
   const int lane, g, t;
   const uint32_t ring;     // this warp's shared memory
   uint32_t fill, read;     // slots of the next tile to load and to use
-  const bool copies;       // this lane copies 16 bytes of every kRows-th row
+  // This lane copies 16 bytes of every kRows-th row; what is its place where it
+  // does not (behind the head dimension) is 0 from the start.
+  const bool copies;
   uint32_t copy_to[2];     // where to, in even and odd steps of kRows
   uint32_t key_from[2];    // where this lane's chunks of keys are, on even and odd rows
   uint32_t value_from[2];  // its parts of values
@@ -290,6 +292,13 @@ struct QuantWarp {
       key_from[i] = place(g, DP == 128 ? 4 * i + t : t);
       value_from[i] = place(2 * t + i, DP == 128 ? g : g >> 1) + (DP == 128 ? 0 : (g & 1) * 8);
     }
+    if (!copies)
+#pragma unroll 1
+      for (uint32_t i = 0; i < 3 * kTile / kRows; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         ring + (i & 1 ? copy_to[1] : copy_to[0]) + i * kRows * DP),
+                     "r"(0)
+                     : "memory");
   }
 
   __device__ __forceinline__ void step(uint32_t& slot) {
@@ -322,9 +331,9 @@ struct QuantWarp {
     const int64_t sn = a.pool.sn[kv], st = a.pool.st[kv];
     const int32_t mask = (1 << a.pool.page_log2) - 1;
     const uint32_t to[2] = {fill + copy_to[0], fill + copy_to[1]};
-    const uint8_t* p = from + x.page[0] * sn + x.inside * st;
-    if (x.full) {
-      if (copies) {
+    if (copies) {
+      const uint8_t* p = from + x.page[0] * sn + x.inside * st;
+      if (x.full) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
           if (i > 0 && !one_page())
@@ -337,19 +346,15 @@ struct QuantWarp {
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < kGroups * kCopies; ++i)
-          copy16(to[i & 1] + i * kRows * DP, a.pool.codes[kv], false);
-      }
-    } else {
+        for (int i = 0; i < kGroups; ++i) {
+          p = from + x.page[i] * sn + ((x.inside + 16 * i) & mask) * st;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        p = from + x.page[i] * sn + ((x.inside + 16 * i) & mask) * st;
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j) {
-          const int at = 16 * i + j * kRows + lane / kRowLanes;
-          const bool yes = copies && (x.seen[i / 2] >> (at & 31) & 1);
-          copy16(to[j & 1] + (16 * i + j * kRows) * DP, yes ? p : a.pool.codes[kv], yes);
-          p += kRows * st;
+          for (int j = 0; j < kCopies; ++j) {
+            const int at = 16 * i + j * kRows + lane / kRowLanes;
+            const bool yes = x.seen[i / 2] >> (at & 31) & 1;
+            copy16(to[j & 1] + (16 * i + j * kRows) * DP, yes ? p : a.pool.codes[kv], yes);
+            p += kRows * st;
+          }
         }
       }
     }
@@ -478,10 +483,19 @@ struct QuantWarp {
   // relative to a base of their own, as 2^7 at most 2^8 times over: the largest
   // is then from 2^7 to 2^15 of fp16's range, and what is lost lies 2^-32 below
   // it. The sums of 2^x have another base. Both move rarely.
-  __device__ __forceinline__ void tile() {
+  __device__ __forceinline__ void tile(bool work) {
+    float s[kGroups][NT][4];
+    if (work) scores(s);
+    load_values();
+    if (work) outputs(s);
+    now = next;
+    load_keys();
+  }
+
+  // The products of queries and keys.
+  __device__ __forceinline__ void scores(float (&s)[kGroups][NT][4]) {
     copies_wait<2>();
     __syncwarp();
-    float s[kGroups][NT][4];
 #pragma unroll
     for (int x = 0; x < kGroups; ++x)
 #pragma unroll
@@ -510,7 +524,10 @@ struct QuantWarp {
     }
     step(read);
     __syncwarp();  // the slot has been read
-    load_values();
+  }
+
+  // Weights, sums and the products with values.
+  __device__ __forceinline__ void outputs(float (&s)[kGroups][NT][4]) {
     float ck[kMasks], lv[kMasks];
 #pragma unroll
     for (int x = 0; x < kMasks; ++x) {
@@ -603,8 +620,6 @@ struct QuantWarp {
     }
     step(read);
     __syncwarp();
-    now = next;
-    load_keys();
   }
 
   // The largest of a column, and of `x`.
@@ -688,14 +703,14 @@ struct QuantWarp {
     due = spot;
     left = count;
     look_up();
-    load_keys();
-    load_values();
-    now = next;
-    load_keys();
-    bool began = spot.tile == 0;
-    begin(spot.b);
-    for (int32_t i = 0; i < count; ++i) {
-      tile();
+    next.some = false;
+    bool began = spot.tile == 0, fresh = true;
+    // two rounds ahead of the first tile only load
+    for (int32_t i = -2; i < count; ++i) {
+      if (i >= 0 && fresh) begin(spot.b);
+      tile(i >= 0);
+      if (i < 0) continue;
+      fresh = false;
       const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
       if (!ends && !last) {
         ++spot.tile;
@@ -708,8 +723,7 @@ struct QuantWarp {
         piece(began);
       if (!last) {
         advance<kTile>(a, spot);
-        begin(spot.b);
-        began = true;
+        began = fresh = true;
       }
     }
   }

@@ -43,7 +43,12 @@ struct QuantPlan {
   size_t spans, part_o, part_lse, bytes;
 };
 
-// Units of a call stay within 31 bits with the most parts of a group, 8.
+// Warps of a CTA of the attention kernel.
+int32_t quant_warps(int columns) {
+  return columns == 1 ? QuantLayout<128, 1>::kWarps : QuantLayout<128, 2>::kWarps;
+}
+
+// Tiles of all heads; those of the sequences then stay within 31 bits.
 constexpr int64_t kMaxUnits = 250000000;
 // Tiles of a row that a CTA of its own still takes.
 constexpr int64_t kWholeTiles = 16;
@@ -66,7 +71,7 @@ QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t
     p.grid = rows;
     return p;
   }
-  const int64_t warps = p.columns == 1 ? 12 : 8, most = (units + warps - 1) / warps;
+  const int64_t warps = quant_warps(p.columns), most = (units + warps - 1) / warps;
   p.grid = most < 1 ? 1 : (most < sms ? most : sms);
   const size_t columns = 2 * static_cast<size_t>(p.grid) * warps * 8 * p.columns;
   p.spans = 0;
@@ -180,7 +185,7 @@ extern "C" dsa_status dsa_quant_attention(const dsa_quant_pages* pages, const vo
   a.l_sb = l_sb;
   a.l_sh = l_sh;
   a.bf16 = dtype == DSA_DTYPE_BF16;
-  a.warps = static_cast<int32_t>(p.grid) * (p.columns == 1 ? 12 : 8);
+  a.warps = static_cast<int32_t>(p.grid) * dsa::quant_warps(p.columns);
   char* ws = static_cast<char*>(workspace);
   a.spans = reinterpret_cast<int2*>(ws + p.spans);
   a.part_o = reinterpret_cast<float*>(ws + p.part_o);
