@@ -165,10 +165,15 @@ struct Spot {
   int32_t tile, tiles, tokens;
 };
 
+// (Lengths go up to 2^31 - 16: tokens behind a tile's start do not fit then.)
+template <int TILE>
+__device__ __forceinline__ int32_t tiles_of(int32_t tokens) {
+  return static_cast<int32_t>((static_cast<uint32_t>(tokens) + TILE - 1) / TILE);
+}
 template <int TILE>
 __device__ __forceinline__ void enter(const QuantAttnArgs& a, Spot& s) {
   s.tokens = quant_length(a, s.b);
-  s.tiles = (s.tokens + TILE - 1) / TILE;
+  s.tiles = tiles_of<TILE>(s.tokens);
 }
 // To the next tile; never called behind the last one of the line.
 template <int TILE>
@@ -318,12 +323,12 @@ struct QuantWarp {
   __device__ __forceinline__ bool one_page() const { return (1 << a.pool.page_log2) >= kTile; }
   __device__ __forceinline__ void look_up() {
     if (left <= 0) return;
-    const int32_t t0 = due.tile * kTile;
+    const int32_t t0 = due.tile * kTile, rest = due.tokens - t0;
     page[0] = quant_page(a.pool, due.b, t0);
 #pragma unroll
     for (int i = 1; i < kGroups; ++i)
       page[i] = one_page() ? page[0]
-                           : t0 + 16 * i < due.tokens ? quant_page(a.pool, due.b, t0 + 16 * i) : -1;
+                           : 16 * i < rest ? quant_page(a.pool, due.b, t0 + 16 * i) : -1;
   }
 
   // The rows of a tile into the next slot; `from`: what this lane copies, on page 0.
@@ -368,7 +373,8 @@ struct QuantWarp {
     if (next.some) {
       const int32_t t0 = due.tile * kTile, mask = (1 << a.pool.page_log2) - 1;
       next.inside = t0 & mask;
-      bool full = t0 + kTile <= due.tokens;
+      const int32_t rest = due.tokens - t0;
+      bool full = rest >= kTile;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
         next.page[i] = page[i];
@@ -378,11 +384,11 @@ struct QuantWarp {
 #pragma unroll
       for (int x = 0; x < kMasks; ++x) {
         const int32_t mine = lane < 16 ? page[2 * x] : page[2 * x + 1];
-        const int32_t tok = t0 + 32 * x + lane;
-        const bool ok = mine >= 0 && tok < due.tokens;
+        const bool ok = mine >= 0 && 32 * x + lane < rest;
         next.seen[x] = full ? ~0u : __ballot_sync(~0u, ok);
         const int64_t in =
-            static_cast<int64_t>((tok & mask) >> a.pool.block_log2) * a.pool.kv_heads;
+            static_cast<int64_t>(((next.inside + 32 * x + lane) & mask) >> a.pool.block_log2) *
+            a.pool.kv_heads;
         next.sk[x] = next.sv[x] = 0.f;
         if (ok) {
           next.sk[x] = k_scales[mine * a.pool.ssn[0] + in];
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   const int64_t chunk = (a.batch + L::kThreads - 1) / L::kThreads;
   const int64_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, a.batch);
   int32_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += (quant_length(a, b) + L::kTile - 1) / L::kTile;
+  for (int64_t b = b0; b < b1; ++b) mine += tiles_of<L::kTile>(quant_length(a, b));
   int32_t upto = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -803,7 +809,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   if (threadIdx.x % gridDim.x == blockIdx.x) {  // this CTA's part of the spans
     int32_t at = before;
     for (int64_t b = b0; b < b1; ++b) {
-      const int32_t tiles = (quant_length(a, b) + L::kTile - 1) / L::kTile;
+      const int32_t tiles = tiles_of<L::kTile>(quant_length(a, b));
       a.spans[b] = tiles > 0 ? make_int2(shares.of(total, at), shares.of(total, at + tiles - 1))
                              : make_int2(0, -1);
       at += tiles;

@@ -507,6 +507,87 @@ def test_attention_lengths_are_clamped(env):
     check_attend(env, pool, q, [65, -1])
 
 
+@pytest.mark.parametrize("page,dim", [(16, 64), (64, 128), (16, 128)])
+def test_attention_tables_of_the_longest_length(env, page, dim):
+    """A row of pages for all lengths below 2^31, of which the first and the last
+    are there: the last tile ends at 2^31, or a page before it."""
+    torch, dsa = env
+    pool = Pool(torch, 44, [2 * page], 2, dim, page, 16, spare=0)
+    cache, scales, _ = pool.gpu()
+    c = (cache[0], cache[1], scales[0], scales[1])
+    width = (2 ** 31 - 1) // page
+    tables = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    tables[0, 0], tables[0, -1] = int(pool.tables[0, 0]), int(pool.tables[0, 1])
+    q = queries(torch, 45, 1, 4, dim, torch.bfloat16)
+    want = quant.attend(q, pool.codes, pool.scales, pool.tables, [2 * page])
+    for n in (width * page, 2 ** 31 - 1):
+        out, lse = dsa.dsa_quant_attention(q, *c, tables, ints(torch, [n]))
+        ref.check(out, want[0], want[2], "out")
+        ref.check(lse, want[1], want[3], "lse")
+    # the last page's tokens, written and (its first row's) read back
+    k, v = rows(torch, 46, 3, 2, dim, torch.bfloat16)
+    held = width * page - 3
+    pool.scales[:, pool.tables[0, 1]] = 2.0 ** -9
+    scales.copy_(torch.from_numpy(pool.scales))
+    dsa.dsa_quant_cache_write(k, v, ints(torch, [0, 3]), *c, tables, ints(torch, [held]))
+    model = pool.scales.astype(np.float64)
+    quant.write(k.double().cpu().numpy(), v.double().cpu().numpy(), [0, 3], pool.codes, model,
+                pool.tables, [2 * page - 3])
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(scales.cpu().numpy(), model.astype(np.float32))
+    quant.same_codes(cache.view(torch.uint8).cpu().numpy(), pool.codes, "codes")
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch, quant_reference as quant, test_quant_gpu as t
+import deepseek_sparse_attention_row_gb300 as dsa
+
+for lens in ([60, 30], [3000, 30]):     # a launch, and two
+    pool = t.Pool(torch, 1, [n + 2 for n in lens], 2, 64, 16, 16)
+    cache, scales, tables = pool.gpu()
+    c = (cache[0], cache[1], scales[0], scales[1])
+    q, at = t.queries(torch, 2, 2, 4, 64, torch.bfloat16), t.ints(torch, lens)
+    k = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu, turns = t.ints(torch, [0, 2, 4]), dsa.rotary_turns([1.0] * 32)
+    pos = t.ints(torch, [0, 1, 2, 3])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        turned, _ = dsa.dsa_rotary(k, None, pos, turns)
+        back = dsa.dsa_quant_cache_read(*c, tables, cu, total=4)
+        out, lse = dsa.dsa_quant_attention(q, *c, tables, at)
+        dsa.dsa_quant_cache_write(turned, k, cu, *c, tables, at)
+    g.replay()
+    torch.cuda.synchronize()
+    want = quant.attend(q, pool.codes, pool.scales, pool.tables, lens)
+    assert ((out.double().cpu() - want[0]).abs() <= want[2]).all()
+    assert torch.equal(back[0].double().cpu()[:2],
+                       torch.from_numpy(quant.read(pool.codes, pool.scales, pool.tables, 0, 2)[0]))
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured(env):
+    import os
+    import subprocess
+    import sys
+
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout + res.stderr
+
+
+@pytest.mark.parametrize("kv_heads,group", [(40, 1), (7, 40), (2000, 1)])
+def test_attention_many_rows(env, kv_heads, group):
+    """Rows that do not divide the warps, parts of a group, and more rows than
+    warps."""
+    torch, _ = env
+    lens = [700, 33]
+    pool = Pool(torch, 47, lens, kv_heads, 16, 16, 16)
+    check_attend(env, pool, queries(torch, 48, 2, kv_heads * group, 16, torch.bfloat16), lens)
+
+
 def test_attention_strided(env):
     torch, dsa = env
     H, Hkv, D, page, block = 6, 3, 48, 32, 16
