@@ -1307,23 +1307,28 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
     shape = (total, Hkv, D)
 
     def output(t, name):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=k_pages.device)
-            return t, t.data_ptr() or None, Hkv * D, D
         op, oshape, ost = _on_gpu(t, dtype, name, 3, dev)
         if oshape != shape:
             raise ValueError(f"{name} must be {shape}, got {tuple(oshape)}")
-        return t, op, *_row_strides(oshape, ost, name)
+        return op, *_row_strides(oshape, ost, name)
 
-    def enqueue(handle):
-        k, *ka = output(k_out, "k_out")
-        v, *va = output(v_out, "v_out")
+    def enqueue(k, v, handle):
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=k_pages.device)
+            ka = k.data_ptr() or None, Hkv * D, D
+        else:
+            ka = output(k, "k_out")
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=k_pages.device)
+            va = v.data_ptr() or None, Hkv * D, D
+        else:
+            va = output(v, "v_out")
         st = library().dsa_quant_cache_read(pages, cp, S, total, code, *ka, *va, handle)
         if st:
             _check("dsa_quant_cache_read", st)
         return k, v
 
-    return _call(dev, stream, enqueue)
+    return _call(dev, stream, enqueue, k_out, v_out)
 
 
 def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *, scale=None,

@@ -19,6 +19,17 @@
 // heads of 80 bytes, a warp after the other, 264 MB were read where 174 would
 // do). Sequences that lie within a share are finished by its warps; of the others
 // each leaves a piece, and a second launch joins those by their log-sum-exps.
+//
+// Bound by HBM where contexts are long: 302,000 tokens of 8 heads of 128, 619 MB,
+// take 100 us (6.2 TB/s, 7.4 TB/s in the loop alone), 459,000 tokens of 4 heads 80
+// us (5.9 TB/s). About 8 us pass before the first tiles are done (lengths, page,
+// codes: a chain of loads, then all SMs' first ones at once) and 5 at the end (the
+// join). With heads of 80 the instructions of a tile bound it (51 us for 174 MB): a
+// scheduler has three warps, each of which issues every sixth cycle.
+// Codes through registers instead of the ring: 161 us for the first case (too few
+// bytes under way); 14 or 16 warps of 128 registers: 110 and 117 us; 8 warps with
+// tiles of 8 KiB: 102 us; pieces joined in the CTA and rows in turn instead of side
+// by side: 122 us.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -57,7 +68,8 @@ template <int DP, int NT>
 struct QuantLayout {
   static constexpr int kTile = kQuantTileBytes / DP;  // keys
   static constexpr int kHeads = 8 * NT;
-  // As many as the registers let be: 16 columns take 250 of a thread.
+  // As many as the registers let be: 16 columns take 250 of a thread (12 warps of
+  // them, spilled, took 79 us where 8 take 62: groups of 16, 64 sequences).
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = 3 * kQuantTileBytes;
@@ -146,12 +158,10 @@ struct Shares {
   }
 };
 
-// Teams among which a line is cut: of as many warps as there are rows, and with
-// kTeamTiles tiles each where there are that many.
-constexpr int kTeamTiles = 1;
+// Teams among which a line is cut: of as many warps as there are rows, and none
+// without a tile.
 __device__ __forceinline__ uint32_t quant_teams(const QuantAttnArgs& a, int32_t total) {
-  const int32_t most = max(a.warps / a.rows, 1), useful = max(total / kTeamTiles, 1);
-  return static_cast<uint32_t>(min(most, useful));
+  return static_cast<uint32_t>(min(max(a.warps / a.rows, 1), max(total, 1)));
 }
 
 __device__ __forceinline__ int32_t quant_length(const QuantAttnArgs& a, int64_t b) {

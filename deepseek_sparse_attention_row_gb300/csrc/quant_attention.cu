@@ -1,5 +1,6 @@
 // quant_attention.cu -- attention of single tokens over pages of e4m3 codes:
-// dsa_quant_attention of include/dsa_quant.h.
+// dsa_quant_attention of include/dsa_quant.h. The kernels are in quant_attend.cuh;
+// here are the checks of arguments, the workspace and the launches.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -50,7 +51,8 @@ int32_t quant_warps(int columns) {
 
 // Tiles of all heads; those of the sequences then stay within 31 bits.
 constexpr int64_t kMaxUnits = 250000000;
-// Tiles of a row that a CTA of its own still takes.
+// Tiles of a row that a CTA of its own still takes, if there is an SM for each row:
+// one launch instead of two (three sequences of 200 tokens, 2 heads of 64: 5.0 us).
 constexpr int64_t kWholeTiles = 16;
 
 QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,

@@ -1,6 +1,17 @@
 // quant_cache.cu -- writing keys and values into pages of e4m3 codes and
 // reading them back: dsa_quant_cache_write and dsa_quant_cache_read of
 // include/dsa_quant.h.
+//
+// Scales are powers of two: x / scale then is exact in fp32, so that a code is the
+// one next to x and does not depend on how it is computed, and a scale that grows
+// changes the held codes only where they fall below the smallest normal one.
+//
+// Both are bound by HBM and by how many loads are under way. Writing reads a
+// block's tokens once, into the registers of a team of warps that agree on their
+// largest size: 16389 tokens of 8 heads of 128, 100 MB, take 21.9 us (4.6 TB/s); 72
+// us when a warp went through the block twice, 30 with sizes taken as floats, 27
+// with registers for two CTAs of an SM instead of four. Reading 20541 tokens of 8
+// heads of 128, 126 MB, takes 22.8 us (5.5 TB/s); 25 us with eight rows to a warp.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -79,10 +90,10 @@ __device__ __forceinline__ uint32_t largest_finite2(uint32_t x, uint32_t sizes) 
 // most n / block + 2 blocks, and floor(cu[s] / block) + 2 s counts that many
 // between one sequence and the next: item numbers are found from cu alone.
 struct Block {
-  int32_t seq;        // -1: nothing to do
-  int32_t start;      // its first token
-  int32_t from, to;   // the new ones
-  int64_t row;        // of the token `from`
+  int32_t seq;       // -1: nothing to do
+  int32_t start;     // its first token
+  int32_t from, to;  // the new ones
+  int64_t row;       // of the token `from`
 };
 
 __device__ __forceinline__ Block find_block(const WriteArgs& a, int64_t item) {
@@ -112,6 +123,7 @@ constexpr int kAtOnce = 8;  // 16-byte loads of a lane
 // A team of `team` warps (a power of two, up to 16) for each block, head and one of
 // keys and values; the teams of a CTA share the block. Where a block's new tokens
 // are no more than a team has registers for, they are read once.
+// (64 registers, a few of them spilled, for twice the warps.)
 template <typename T>
 __global__ void __launch_bounds__(512, 2) write_kernel(const WriteArgs a, int team) {
   __shared__ uint32_t tops[16];
@@ -355,8 +367,8 @@ extern "C" dsa_status dsa_quant_cache_write(const dsa_quant_pages* pages, const 
   a.lens = lens;
   const int64_t items = total / block + 2ll * seqs;
   if (items > INT32_MAX) return DSA_EUNSUPPORTED;
-  // A team's registers hold the new tokens that a block gets on average, if few
-  // come to a sequence.
+  // A team's registers hold the new tokens that a block gets on average: one warp
+  // for single tokens, the whole block where more come to a sequence.
   const int64_t rows = 32 / (a.pool.dim / 8) * dsa::kAtOnce, mean = (total + seqs - 1) / seqs;
   int team = 1;
   while (team < 16 && team * rows < (mean < block ? mean : block)) team *= 2;

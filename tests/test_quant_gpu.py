@@ -305,6 +305,71 @@ def test_read_rows_of_no_sequence_and_without_a_page(env):
     assert (room[:10] == 7).all() and (room[50:] == 7).all()
 
 
+@pytest.mark.parametrize("which", ["k_out", "v_out"])
+def test_read_into_one_given_output(env, which):
+    torch, dsa = env
+    pool = Pool(torch, 24, [40, 3], 3, 16, 16, 16)
+    cache, scales, tables = pool.gpu()
+    c = (cache[0], cache[1], scales[0], scales[1])
+    cu = ints(torch, [0, 40, 43])
+    want = dsa.dsa_quant_cache_read(*c, tables, cu, total=43, dtype=torch.float16)
+    mine = torch.zeros(43, 3, 16, dtype=torch.float16, device="cuda")
+    got = dsa.dsa_quant_cache_read(*c, tables, cu, **{which: mine})
+    torch.cuda.synchronize()
+    assert got[which == "v_out"] is mine
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError, match="total is 42"):
+        dsa.dsa_quant_cache_read(*c, tables, cu, total=42, **{which: mine})
+    with pytest.raises(TypeError, match="bfloat16"):
+        dsa.dsa_quant_cache_read(*c, tables, cu, dtype=torch.bfloat16, **{which: mine})
+    with pytest.raises(TypeError, match="bfloat16 or float16"):
+        dsa.dsa_quant_cache_read(*c, tables, cu, **{which: mine.float()})
+    with pytest.raises(TypeError, match="bfloat16 or float16"):
+        dsa.dsa_quant_cache_read(*c, tables, cu, total=43, dtype=torch.float32)
+    with pytest.raises(ValueError, match="total"):
+        dsa.dsa_quant_cache_read(*c, tables, cu)
+
+
+def test_binding_refusals(env):
+    """Tensors that do not belong together."""
+    torch, dsa = env
+    pool = Pool(torch, 25, [40, 3], 2, 64, 16, 8)
+    cache, scales, tables = pool.gpu()
+    c = dict(k_pages=cache[0], v_pages=cache[1], k_scales=scales[0], v_scales=scales[1],
+             tables=tables)
+    q, lens = queries(torch, 26, 2, 4, 64, torch.bfloat16), ints(torch, [40, 3])
+    k = queries(torch, 27, 5, 2, 64, torch.bfloat16)
+    cu = ints(torch, [0, 2, 5])
+    bad = [  # changed, the error, what it says
+        (dict(k_pages=cache[0].view(torch.uint8)), TypeError, "float8"),
+        (dict(v_pages=cache[1][:-1]), ValueError, "do not match"),
+        (dict(k_pages=cache[0].permute(0, 1, 3, 2)), ValueError, "k_pages|do not match"),
+        (dict(k_scales=scales[0].half()), TypeError, "float32"),
+        (dict(k_scales=scales[0][:, :1].expand(-1, 3, -1)), ValueError, "k_scales must be"),
+        (dict(v_scales=scales[1][:, :1].contiguous()), ValueError, "do not match"),
+        (dict(v_scales=scales[1].transpose(1, 2).contiguous().transpose(1, 2)), ValueError,
+         "contiguous"),
+        (dict(tables=tables.long()), TypeError, "int32"),
+        (dict(tables=tables[0]), ValueError, "2 dimensions"),
+        (dict(tables=tables.cpu()), ValueError, "CUDA"),
+        (dict(tables=tables.repeat(1, 2)[:, ::2]), ValueError, "unit stride"),
+    ]
+    for kw, error, match in bad:
+        with pytest.raises(error, match=match):
+            dsa.dsa_quant_attention(q, lens=lens, **{**c, **kw})
+        with pytest.raises(error, match=match):
+            dsa.dsa_quant_cache_write(k, k, cu, lens=lens, **{**c, **kw})
+    for kw, match in ((dict(q=q[:1]), "do not match"), (dict(q=q[..., :32]), "do not match"),
+                      (dict(lens=lens[:1]), "do not match"), (dict(q=q[0]), "3 dimensions"),
+                      (dict(out=q[:, :2]), "out must be"), (dict(q=q[:, :3]), "invalid argument")):
+        with pytest.raises((ValueError, dsa.DsaError), match=match):
+            dsa.dsa_quant_attention(**{**dict(q=q, lens=lens), **c, **kw})
+    for kw, match in ((dict(v=k[:4]), "do not match"), (dict(k=k[:, :1], v=k[:, :1]), "match"),
+                      (dict(cu=cu[:2]), "cu holds"), (dict(lens=lens[:1]), "cu holds")):
+        with pytest.raises(ValueError, match=match):
+            dsa.dsa_quant_cache_write(**{**dict(k=k, v=k, cu=cu, lens=lens), **c, **kw})
+
+
 def test_read_strided(env):
     torch, dsa = env
     pool = Pool(torch, 22, [50, 21], 3, 48, 16, 4)
