@@ -12,19 +12,20 @@
 // which is exact; so are queries after a power of two that brings the largest of
 // a row to 2^14.
 //
-// The tiles of all sequences lie on one line. It is cut into equal shares, one for
-// each team of as many warps as there are key/value heads; the warps of a team go
-// through its share side by side, each with a head of its own, so that what the
-// heads of a token have in common of a line of memory is there once for all (with
-// heads of 80 bytes, a warp after the other, 264 MB were read where 174 would
-// do). Sequences that lie within a share are finished by its warps; of the others
-// each leaves a piece, and a second launch joins those by their log-sum-exps.
+// The tiles of all sequences lie on one line, in front of each sequence's a unit for
+// its start. It is cut into equal shares, one for each team of as many warps as there
+// are key/value heads; the warps of a team go through its share side by side, each
+// with a head of its own, so that what the heads of a token have in common of a line
+// of memory is there once for all (with heads of 80 bytes, a warp after the other,
+// 264 MB were read where 174 would do). Sequences that lie within a share are
+// finished by its warps; of the others each leaves a piece, and a second launch joins
+// those by their log-sum-exps.
 //
 // Bound by HBM where contexts are long: 302,000 tokens of 8 heads of 128, 619 MB,
 // take 100 us (6.2 TB/s, 7.4 TB/s in the loop alone), 459,000 tokens of 4 heads 80
 // us (5.9 TB/s). About 8 us pass before the first tiles are done (lengths, page,
 // codes: a chain of loads, then all SMs' first ones at once) and 5 at the end (the
-// join). With heads of 80 the instructions of a tile bound it (51 us for 174 MB): a
+// join). With heads of 80 the instructions of a tile bound it (50 us for 174 MB): a
 // scheduler has three warps, each of which issues every sixth cycle.
 // Codes through registers instead of the ring: 161 us for the first case (too few
 // bytes under way); 14 or 16 warps of 128 registers: 110 and 117 us; 8 warps with
@@ -43,6 +44,10 @@
 namespace dsa {
 
 constexpr int kQuantTileBytes = 4096;
+// What the start of a sequence takes of a share, in tiles. 128 sequences of 300 tokens,
+// 8 heads of 128: 18.6 us with 0, 17.2 with 1, 17.8 with 2; 300 of 700, 4 heads of 64:
+// 21.2, 20.2, 21.1; 33 of about 4100, 8 heads of 80: 50.7, 50.0, 50.1.
+constexpr int32_t kQuantStart = 1;
 
 struct QuantAttnArgs {
   QuantPool pool;
@@ -139,7 +144,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // ---- the line of tiles -----------------------------------------------------
 
-// A line of `total` tiles cut into n shares, in 32 bits (n up to 65535): share i
+// A line of `total` units cut into n shares, in 32 bits (n up to 65535): share i
 // begins at floor(total * i / n). None is empty if n is not above the total.
 struct Shares {
   uint32_t n, whole, rest;
@@ -159,7 +164,7 @@ struct Shares {
 };
 
 // Teams among which a line is cut: of as many warps as there are rows, and none
-// without a tile.
+// without a unit.
 __device__ __forceinline__ uint32_t quant_teams(const QuantAttnArgs& a, int32_t total) {
   return static_cast<uint32_t>(min(max(a.warps / a.rows, 1), max(total, 1)));
 }
@@ -184,6 +189,10 @@ template <int TILE>
 __device__ __forceinline__ void enter(const QuantAttnArgs& a, Spot& s) {
   s.tokens = quant_length(a, s.b);
   s.tiles = tiles_of<TILE>(s.tokens);
+}
+// Units of a sequence on the line: its start and its tiles.
+__device__ __forceinline__ int32_t units_of(int32_t tiles) {
+  return tiles > 0 ? tiles + kQuantStart : 0;
 }
 // To the next tile; never called behind the last one of the line.
 template <int TILE>
@@ -408,7 +417,10 @@ struct QuantWarp {
       copy_rows(next, keys, 0);
       if (--left > 0) {
         advance<kTile>(a, due);
-        if (due.tile == 0) fetch_queries();
+        if (due.tile == 0) {
+          fetch_queries();
+          left -= kQuantStart;
+        }
       }
       look_up();
     }
@@ -712,32 +724,34 @@ struct QuantWarp {
       }
   }
 
-  // `count` tiles of the line, from `spot` on. What it has of a sequence in part
+  // `units` of the line, from the tile of `spot` on. What it has of a sequence in part
   // goes to `piece(b, whether the sequence begins here)` instead of the output.
   template <typename F>
-  __device__ __forceinline__ void run(Spot spot, int32_t count, F piece) {
+  __device__ __forceinline__ void run(Spot spot, int32_t units, F piece) {
     due = spot;
-    left = count;
+    left = units;
     look_up();
     next.some = false;
     bool began = spot.tile == 0, fresh = true;
     // two rounds ahead of the first tile only load
-    for (int32_t i = -2; i < count; ++i) {
+    for (int32_t i = -2; units > 0; ++i) {
       if (i >= 0 && fresh) begin(spot.b);
       tile(i >= 0);
       if (i < 0) continue;
       fresh = false;
-      const bool ends = spot.tile + 1 == spot.tiles, last = i + 1 == count;
-      if (!ends && !last) {
+      --units;
+      const bool ends = spot.tile + 1 == spot.tiles;
+      if (!ends && units > 0) {
         ++spot.tile;
         continue;
       }
+      if (ends) units -= kQuantStart;
       finish();
       if (began && ends)
         store(spot.b);
       else
         piece(began);
-      if (!last) {
+      if (units > 0) {
         advance<kTile>(a, spot);
         began = fresh = true;
       }
@@ -745,8 +759,8 @@ struct QuantWarp {
   }
 };
 
-// Where `unit` of the line lies; all lanes of a warp together. sums[i]: tiles in
-// front of chunk i (of `chunk` sequences each).
+// Where `unit` of the line lies (in a sequence's start: a tile below 0); all lanes of
+// a warp together. sums[i]: units in front of chunk i (of `chunk` sequences each).
 template <int TILE, int THREADS>
 __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
                                           const int32_t* sums, int64_t chunk) {
@@ -761,7 +775,8 @@ __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
     s.b = b0 + lane;
     s.tiles = s.tokens = 0;
     if (s.b < a.batch) enter<TILE>(a, s);
-    int32_t upto = s.tiles;
+    const int32_t units = units_of(s.tiles);
+    int32_t upto = units;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
       const int32_t y = __shfl_up_sync(~0u, upto, i);
@@ -770,7 +785,7 @@ __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
     const uint32_t past = __ballot_sync(~0u, before + upto > unit);
     if (past) {
       const int who = __ffs(past) - 1;
-      s.tile = __shfl_sync(~0u, unit - (before + upto - s.tiles), who);
+      s.tile = __shfl_sync(~0u, unit - (before + upto - units), who) - kQuantStart;
       s.b = b0 + who;
       s.tiles = __shfl_sync(~0u, s.tiles, who);
       s.tokens = __shfl_sync(~0u, s.tokens, who);
@@ -795,7 +810,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   const int64_t chunk = (a.batch + L::kThreads - 1) / L::kThreads;
   const int64_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, a.batch);
   int32_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += tiles_of<L::kTile>(quant_length(a, b));
+  for (int64_t b = b0; b < b1; ++b) mine += units_of(tiles_of<L::kTile>(quant_length(a, b)));
   int32_t upto = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -820,19 +835,26 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     int32_t at = before;
     for (int64_t b = b0; b < b1; ++b) {
       const int32_t tiles = tiles_of<L::kTile>(quant_length(a, b));
-      a.spans[b] = tiles > 0 ? make_int2(shares.of(total, at), shares.of(total, at + tiles - 1))
+      const int32_t from = at + kQuantStart;
+      a.spans[b] = tiles > 0 ? make_int2(shares.of(total, from), shares.of(total, from + tiles - 1))
                              : make_int2(0, -1);
-      at += tiles;
+      at += units_of(tiles);
     }
   }
   const uint32_t team = self / a.rows;
   if (total == 0 || team >= shares.n) return;
-  const int32_t first = shares.begin(team), count = shares.begin(team + 1) - first;
-  const Spot spot = find_spot<L::kTile, L::kThreads>(a, first, sums, chunk);
+  const int32_t first = shares.begin(team);
+  int32_t units = shares.begin(team + 1) - first;
+  Spot spot = find_spot<L::kTile, L::kThreads>(a, first, sums, chunk);
+  if (spot.tile < 0) {  // it begins with a start
+    units += spot.tile;
+    spot.tile = 0;
+  }
+  if (units <= 0) return;
   QuantWarp<DP, NT> w(a, smem_addr(smem) + warp * L::kRing);
   for (int32_t row = self - team * a.rows; row < a.rows; row += a.warps) {
     w.take_row(row);
-    w.run(spot, count, [&](bool began) {
+    w.run(spot, units, [&](bool began) {
       const int64_t slot = 2ll * self + began;
       w.keep(a.part_o + slot * L::kPiece, a.part_lse + slot * L::kHeads);
     });

@@ -49,7 +49,7 @@ int32_t quant_warps(int columns) {
   return columns == 1 ? QuantLayout<128, 1>::kWarps : QuantLayout<128, 2>::kWarps;
 }
 
-// Tiles of all heads; those of the sequences then stay within 31 bits.
+// Tiles of all heads; those of the sequences and their starts then stay within 31 bits.
 constexpr int64_t kMaxUnits = 250000000;
 // Tiles of a row that a CTA of its own still takes, if there is an SM for each row:
 // one launch instead of two (three sequences of 200 tokens, 2 heads of 64: 5.0 us).

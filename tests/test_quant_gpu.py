@@ -653,6 +653,18 @@ def test_attention_many_rows(env, kv_heads, group):
     check_attend(env, pool, queries(torch, 48, 2, kv_heads * group, 16, torch.bfloat16), lens)
 
 
+@pytest.mark.parametrize("batch", [160, 901, 1823, 5000])
+@pytest.mark.parametrize("lens", [[1], [1, 0, 0, 33], [0, 0, 16, 0, 31, 700], [32, 64, 0]],
+                         ids=["ones", "some", "one longer", "whole tiles"])
+def test_attention_shares_about_a_tile_long(env, batch, lens):
+    """About as many short sequences as warps, which then have a tile, or parts of a
+    sequence, or nothing at all to do."""
+    torch, _ = env
+    lens = (lens * batch)[:batch]
+    pool = Pool(torch, 49, lens, 1, 16, 16, 16)
+    check_attend(env, pool, queries(torch, 50, batch, 1, 16, torch.bfloat16), lens)
+
+
 def test_attention_strided(env):
     torch, dsa = env
     H, Hkv, D, page, block = 6, 3, 48, 32, 16
