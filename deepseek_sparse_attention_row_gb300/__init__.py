@@ -969,8 +969,8 @@ def dsa_cache_fork(cache, refs, tables, lens, parents, children, *, scales=None,
     ``lens`` int32 [S]. Whole pages are shared; the used tokens of a partly
     filled last page are copied to the lowest free page, and with them that
     page's ``scales`` [planes, N, ...] (of any type, pages contiguous; those of
-    an 8-bit cache). Returns ``status`` int32 (FORK_OK, FORK_NO_PAGE or FORK_REFUSED for each pair), allocated
-    when None; the host waits for nothing."""
+    an 8-bit cache). Returns ``status`` int32 (FORK_OK, FORK_NO_PAGE or
+    FORK_REFUSED for each pair), allocated when None; the host waits for nothing."""
     torch = _torch()
     rp, pages, tp, S, P, ld, lp, dev = _cache_state(refs, tables, lens)
     planes = _cache_planes(cache, pages, dev)

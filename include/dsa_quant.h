@@ -69,8 +69,9 @@ typedef struct {
  *           (a negative or NaN one counts as 0, one over 2^126 as 2^126);
  *   code  = x / scale rounded to nearest even; NaN where x is not finite.
  * Where a block that held tokens gets another scale, their codes become
- * (code * old scale) / scale, rounded likewise (to 448 what passes it). Those are the tokens in front
- * of lens[s]; codes behind the new tokens are left as they were.
+ * (code * old scale) / scale, rounded likewise (to 448 what passes it). Those
+ * are the tokens in front of lens[s]; codes behind the new tokens are left as
+ * they were.
  *
  * No two sequences of a call may write to the same block (pages that hold new
  * tokens are not shared).
@@ -148,15 +149,17 @@ size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t heads,
  * Arithmetic: products of q and codes exact, summed in fp32; scores, maxima,
  * exponentials and sums in fp32; the weights 2^(x_j - m) * sv_j are rounded to
  * fp16 relative to the largest one (to 2^-11 of themselves, or 2^-32 of that)
- * for the product with the codes of V; out is rounded once from fp32.
+ * for the product with the codes of V; out is rounded once from fp32. Where
+ * scale * log2(e) * sk_j, or that times the largest |q| of a row, passes 2^127,
+ * the row may be NaN.
  *
  * batch == 0 or heads == 0: DSA_OK, nothing written. DSA_EINVAL for kv_heads
  * < 1 or no divisor of heads, a scale that is not as above, a workspace that
  * is too small or not aligned, and as for dsa_quant_cache_write.
  * DSA_EUNSUPPORTED as there, for heads / kv_heads > 128, q and out not 16-byte
  * aligned or with strides that are no multiples of 8, and where batch *
- * kv_heads times the 32-token tiles that a row of `tables` has room for passes 2.5 *
- * 10^8, or batch * heads 10^9.
+ * kv_heads times the 32-token tiles that a row of `tables` has room for passes
+ * 2.5 * 10^8, or batch * heads 10^9.
  */
 dsa_status dsa_quant_attention(const dsa_quant_pages *pages, const void *q,
                                int32_t dtype, int64_t batch, int32_t heads,
