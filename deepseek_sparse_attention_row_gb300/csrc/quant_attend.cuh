@@ -25,12 +25,14 @@
 // take 100 us (6.2 TB/s, 7.4 TB/s in the loop alone), 459,000 tokens of 4 heads 80
 // us (5.9 TB/s). About 8 us pass before the first tiles are done (lengths, page,
 // codes: a chain of loads, then all SMs' first ones at once) and 5 at the end (the
-// join). With heads of 80 the instructions of a tile bound it (50 us for 174 MB): a
-// scheduler has three warps, each of which issues every sixth cycle.
+// join). With heads of 80, 174 MB in 48 us, these are a third of the time; in the loop,
+// at 5.4 TB/s, a scheduler has three warps, each of which issues every sixth cycle
+// (16 warps: 47.4 us).
 // Codes through registers instead of the ring: 161 us for the first case (too few
 // bytes under way); 14 or 16 warps of 128 registers: 110 and 117 us; 8 warps with
 // tiles of 8 KiB: 102 us; pieces joined in the CTA and rows in turn instead of side
-// by side: 122 us.
+// by side: 122 us; rings of four slots, with loads a whole tile further ahead, 108 us;
+// heads of 80 in rows of 80 bytes, tiles of 64 keys, 54 us.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -111,6 +113,17 @@ __device__ __forceinline__ void shared_words(uint32_t (&x)[4], uint32_t at) {
 }
 __device__ __forceinline__ void shared_words(uint32_t (&x)[2], uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void shared_words(uint32_t (&x)[1], uint32_t at) {
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[0]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t shared_half_word(uint32_t at) {
+  uint32_t x;
+  asm volatile("{\n\t.reg .b16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+               : "=r"(x)
+               : "r"(at)
+               : "memory");
+  return x;
 }
 // Four codes as two pairs of fp16.
 __device__ __forceinline__ void decode4(uint32_t four, uint32_t& lo, uint32_t& hi) {
@@ -245,14 +258,18 @@ __device__ __forceinline__ void write_joined(const QuantAttnArgs& a, int64_t b, 
 
 // ---- the kernels -----------------------------------------------------------
 
-template <int DP, int NT>
+// KD: the dimensions that are multiplied. The first MD of them, 64 or 128, are dealt
+// to the lanes in whole chunks; 80 and 96 have a tail of one or two steps of 16.
+template <int DP, int NT, int KD>
 struct QuantWarp {
   using L = QuantLayout<DP, NT>;
+  static constexpr int kTail = KD == 80 ? 1 : KD == 96 ? 2 : 0, MD = KD - 16 * kTail;
+  static_assert(MD == 64 || MD == 128, "whole chunks");
   static constexpr int kTile = L::kTile;
   static constexpr int kGroups = kTile / 16;  // of 16 keys
-  static constexpr int kChunks = DP / 64;     // 16-byte chunks of a key in a lane
-  static constexpr int kWords = DP / 32;      // 4-byte words of a value in a lane
-  static constexpr int kSteps = DP / 16;      // of 16 dimensions
+  static constexpr int kChunks = MD / 64;     // 16-byte chunks of a key in a lane
+  static constexpr int kWords = MD / 32;      // 4-byte words of a value in a lane
+  static constexpr int kSteps = KD / 16;      // of 16 dimensions
   static constexpr int kMasks = kTile / 32;
   static constexpr int kRowLanes = DP / 16;          // lanes that load a row
   static constexpr int kRows = 32 / kRowLanes;       // rows of one copy
@@ -278,6 +295,7 @@ struct QuantWarp {
   uint32_t copy_to[2];     // where to, in even and odd steps of kRows
   uint32_t key_from[2];    // where this lane's chunks of keys are, on even and odd rows
   uint32_t value_from[2];  // its parts of values
+  uint32_t key_tail, value_tail[2];  // the same of the tail
 
   Spot due;       // the tile whose keys are loaded next
   int32_t left;   // tiles from it to the share's end
@@ -289,7 +307,7 @@ struct QuantWarp {
 
   uint32_t qf[NT][kSteps][2];
   float2 q_power[NT];  // of the columns' heads
-  float o[NT][DP / 16][4];
+  float o[NT][KD / 16][4];
   float2 l[NT], m[NT], big[NT];  // sums; bases of the sums and of the weights
 
   // Rows of 128 bytes, or pairs of rows of 64, are swizzled by 16-byte chunks: the
@@ -313,9 +331,12 @@ struct QuantWarp {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       copy_to[i] = place(lane / kRowLanes + i * kRows, lane % kRowLanes) - i * kRows * DP;
-      key_from[i] = place(g, DP == 128 ? 4 * i + t : t);
-      value_from[i] = place(2 * t + i, DP == 128 ? g : g >> 1) + (DP == 128 ? 0 : (g & 1) * 8);
+      key_from[i] = place(g, MD == 128 ? 4 * i + t : t);
+      value_from[i] = place(2 * t + i, MD == 128 ? g : g >> 1) + (MD == 128 ? 0 : (g & 1) * 8);
+      if constexpr (kTail > 0)
+        value_tail[i] = place(2 * t + i, 4 + 2 * kTail * g / 16) + 2 * kTail * g % 16;
     }
+    if constexpr (kTail > 0) key_tail = place(g, 4 + 4 * kTail * t / 16) + 4 * kTail * t % 16;
     if (!copies)
 #pragma unroll 1
       for (uint32_t i = 0; i < 3 * kTile / kRows; ++i)
@@ -449,37 +470,45 @@ struct QuantWarp {
   // and this lane has the dimensions that it has of a key. Each head is
   // multiplied by a power of two that brings its largest element to 2^14, which
   // fp16 then holds exactly to 2^-38 of it.
+  __device__ __forceinline__ float2 unpack_pair(uint32_t w) const {
+    if (a.bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
   __device__ __forceinline__ void begin(int64_t b) {
     int32_t first;
     const int32_t heads = row_heads(a, row, first);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = 8 * n + g;
-      float x[kChunks][16];
+      const uint16_t* from =
+          static_cast<const uint16_t*>(a.q) + b * a.q_sb + (first + h) * a.q_sh;
+      float2 x[2 * kSteps];
       float top = 0.f;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
         const int d = 64 * j + 16 * t;
         uint4 u[2] = {};
         if (h < heads && d < a.pool.dim) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(a.q) + b * a.q_sb + (first + h) * a.q_sh + d);
-          u[0] = src[0];
-          u[1] = src[1];
+          u[0] = reinterpret_cast<const uint4*>(from + d)[0];
+          u[1] = reinterpret_cast<const uint4*>(from + d)[1];
         }
         const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float2 f;
-          if (a.bf16)
-            f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-          else
-            f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-          x[j][2 * i] = f.x;
-          x[j][2 * i + 1] = f.y;
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        for (int i = 0; i < 8; ++i) x[8 * j + i] = unpack_pair(w[i]);
+      }
+      if constexpr (kTail > 0) {
+        uint2 u[kTail] = {};
+#pragma unroll
+        for (int i = 0; i < kTail; ++i) {
+          if (h < heads)
+            u[i] = *reinterpret_cast<const uint2*>(from + MD + 4 * (kTail * t + i));
+          x[8 * kChunks + 2 * i] = unpack_pair(u[i].x);
+          x[8 * kChunks + 2 * i + 1] = unpack_pair(u[i].y);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i)
+        top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
       // the power's exponent: what brings `top` to [2^14, 2^15), from 2^-126 on
@@ -489,17 +518,14 @@ struct QuantWarp {
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j)
+      for (int r = 0; r < kSteps; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qf[n][4 * j + r][i] =
-                half_pair(x[j][4 * r + 2 * i] * down, x[j][4 * r + 2 * i + 1] * down);
+        for (int i = 0; i < 2; ++i)
+          qf[n][r][i] = half_pair(x[2 * r + i].x * down, x[2 * r + i].y * down);
       q_power[n].x = __shfl_sync(~0u, up, 8 * t);
       q_power[n].y = __shfl_sync(~0u, up, 8 * t + 4);
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i)
+      for (int i = 0; i < KD / 16; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
       l[n] = make_float2(0.f, 0.f);
@@ -531,27 +557,31 @@ struct QuantWarp {
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[x][n][j] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      uint32_t k[kGroups][2][4];
-#pragma unroll
-      for (int x = 0; x < kGroups; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          shared_words(k[x][y], read + key_from[j] + (16 * x + 8 * y) * DP);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int x = 0; x < kGroups; ++x) {
-          uint32_t a0, a1, a2, a3;
-          decode4(k[x][0][r], a0, a2);
-          decode4(k[x][1][r], a1, a3);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            product(s[x][n], a0, a1, a2, a3, qf[n][4 * j + r][0], qf[n][4 * j + r][1]);
-        }
-    }
+    for (int j = 0; j < kChunks; ++j) score_steps<4>(s, key_from[j], 4 * j);
+    if constexpr (kTail > 0) score_steps<kTail>(s, key_tail, 4 * kChunks);
     step(read);
     __syncwarp();  // the slot has been read
+  }
+
+  // STEPS of them, from step `r0` on, whose codes are at `from` of a tile.
+  template <int STEPS>
+  __device__ __forceinline__ void score_steps(float (&s)[kGroups][NT][4], uint32_t from, int r0) {
+    uint32_t k[kGroups][2][STEPS];
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) shared_words(k[x][y], read + from + (16 * x + 8 * y) * DP);
+#pragma unroll
+    for (int r = 0; r < STEPS; ++r)
+#pragma unroll
+      for (int x = 0; x < kGroups; ++x) {
+        uint32_t a0, a1, a2, a3;
+        decode4(k[x][0][r], a0, a2);
+        decode4(k[x][1][r], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          product(s[x][n], a0, a1, a2, a3, qf[n][r0 + r][0], qf[n][r0 + r][1]);
+      }
   }
 
   // Weights, sums and the products with values.
@@ -602,7 +632,7 @@ struct QuantWarp {
         l[n].y *= ex2(m0.y - m[n].y);
         const float fx = ex2(big0.x - big[n].x), fy = ex2(big0.y - big[n].y);
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
+        for (int i = 0; i < KD / 16; ++i) {
           o[n][i][0] *= fx;
           o[n][i][1] *= fy;
           o[n][i][2] *= fx;
@@ -633,18 +663,34 @@ struct QuantWarp {
 #pragma unroll
       for (int y = 0; y < 4; ++y)
         shared_words(v[y], read + value_from[y & 1] + (16 * x + 8 * (y >> 1)) * DP);
+      const auto steps = [&](uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, int i, int to) {
+        // codes of neighbouring keys side by side, of two dimensions
+        uint32_t a0, a1, a2, a3;
+        decode4(__byte_perm(v0, v1, i ? 0x7362 : 0x5140), a0, a1);
+        decode4(__byte_perm(v2, v3, i ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) product(o[n][to], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
+      };
 #pragma unroll
       for (int r = 0; r < kWords; ++r)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // codes of neighbouring keys side by side, of two dimensions
-          uint32_t a0, a1, a2, a3;
-          decode4(__byte_perm(v[0][r], v[1][r], i ? 0x7362 : 0x5140), a0, a1);
-          decode4(__byte_perm(v[2][r], v[3][r], i ? 0x7362 : 0x5140), a2, a3);
+        for (int i = 0; i < 2; ++i) steps(v[0][r], v[1][r], v[2][r], v[3][r], i, 2 * r + i);
+      if constexpr (kTail > 0) {
+        uint32_t z[4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            product(o[n][2 * r + i], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t at = read + value_tail[y & 1] + (16 * x + 8 * (y >> 1)) * DP;
+          if constexpr (kTail == 1) {
+            z[y] = shared_half_word(at);
+          } else {
+            uint32_t word[1];
+            shared_words(word, at);
+            z[y] = word[0];
+          }
         }
+#pragma unroll
+        for (int i = 0; i < kTail; ++i) steps(z[0], z[1], z[2], z[3], i, 2 * kWords + i);
+      }
     }
     step(read);
     __syncwarp();
@@ -672,7 +718,7 @@ struct QuantWarp {
         const bool none = sum == 0.f;
         const float f = none ? 0.f : exp2f(weights - 7.f - base) / sum;
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
+        for (int i = 0; i < KD / 16; ++i) {
           o[n][i][h] = none ? 0.f : o[n][i][h] * f;
           o[n][i][2 + h] = none ? 0.f : o[n][i][2 + h] * f;
         }
@@ -681,7 +727,7 @@ struct QuantWarp {
   }
 
   __device__ __forceinline__ void store(int64_t b) {
-    constexpr int kDims = DP / 8;  // of a lane
+    constexpr int kDims = MD / 8;  // of a lane
     int32_t first;
     const int32_t heads = row_heads(a, row, first);
 #pragma unroll
@@ -693,7 +739,7 @@ struct QuantWarp {
         if (g * kDims < a.pool.dim) {
           uint4* to = reinterpret_cast<uint4*>(out_row(a, b, first + at) + g * kDims);
 #pragma unroll
-          for (int i = 0; i < DP / 64; ++i) {
+          for (int i = 0; i < MD / 64; ++i) {
             uint32_t u[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -701,11 +747,18 @@ struct QuantWarp {
             to[i] = make_uint4(u[0], u[1], u[2], u[3]);
           }
         }
+        if constexpr (kTail > 0) {
+          uint32_t* to =
+              reinterpret_cast<uint32_t*>(out_row(a, b, first + at) + MD + 2 * kTail * g);
+#pragma unroll
+          for (int i = 0; i < kTail; ++i)
+            to[i] = pack_pair(a, o[n][MD / 16 + i][h], o[n][MD / 16 + i][2 + h]);
+        }
         if (g == 0 && a.lse) a.lse[b * a.l_sb + (first + at) * a.l_sh] = h ? m[n].y : m[n].x;
       }
   }
 
-  // To a piece [columns][DP] and its log-sum-exps.
+  // To a piece [columns][DP], the first KD of each, and its log-sum-exps.
   __device__ __forceinline__ void keep(float* piece, float* lse) {
     int32_t first;
     const int32_t heads = row_heads(a, row, first);
@@ -715,11 +768,17 @@ struct QuantWarp {
       for (int h = 0; h < 2; ++h) {
         const int32_t at = 8 * n + 2 * t + h;
         if (at >= heads) continue;
-        float4* to = reinterpret_cast<float4*>(piece + at * DP + g * (DP / 8));
+        float4* to = reinterpret_cast<float4*>(piece + at * DP + g * (MD / 8));
 #pragma unroll
-        for (int i = 0; i < DP / 32; ++i)
+        for (int i = 0; i < MD / 32; ++i)
           to[i] = make_float4(o[n][2 * i][h], o[n][2 * i][2 + h], o[n][2 * i + 1][h],
                               o[n][2 * i + 1][2 + h]);
+        if constexpr (kTail > 0) {
+          float2* tail = reinterpret_cast<float2*>(piece + at * DP + MD + 2 * kTail * g);
+#pragma unroll
+          for (int i = 0; i < kTail; ++i)
+            tail[i] = make_float2(o[n][MD / 16 + i][h], o[n][MD / 16 + i][2 + h]);
+        }
         if (g == 0) lse[at] = h ? m[n].y : m[n].x;
       }
   }
@@ -795,7 +854,7 @@ __device__ __forceinline__ Spot find_spot(const QuantAttnArgs& a, int32_t unit,
   }
 }
 
-template <int DP, int NT>
+template <int DP, int NT, int KD>
 __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     quant_attend_kernel(const QuantAttnArgs a) {
   using L = QuantLayout<DP, NT>;
@@ -851,7 +910,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     spot.tile = 0;
   }
   if (units <= 0) return;
-  QuantWarp<DP, NT> w(a, smem_addr(smem) + warp * L::kRing);
+  QuantWarp<DP, NT, KD> w(a, smem_addr(smem) + warp * L::kRing);
   for (int32_t row = self - team * a.rows; row < a.rows; row += a.warps) {
     w.take_row(row);
     w.run(spot, units, [&](bool began) {
@@ -863,7 +922,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
 
 // A CTA for each row of few tiles, whose warps share them: nothing is left to be
 // joined by a second launch.
-template <int DP, int NT>
+template <int DP, int NT, int KD>
 __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
     quant_attend_row_kernel(const QuantAttnArgs a) {
   using L = QuantLayout<DP, NT>;
@@ -881,7 +940,7 @@ __global__ void __launch_bounds__(QuantLayout<DP, NT>::kThreads, 1)
   if (warp < used) {
     const Shares shares(spot.tiles, used);
     spot.tile = shares.begin(warp);
-    QuantWarp<DP, NT> w(a, smem_addr(smem) + warp * L::kRing);
+    QuantWarp<DP, NT, KD> w(a, smem_addr(smem) + warp * L::kRing);
     w.take_row(row);
     w.run(spot, shares.begin(warp + 1) - spot.tile, [&](bool) {
       __syncwarp();  // the ring has been read

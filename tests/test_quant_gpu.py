@@ -432,6 +432,15 @@ def test_attention_wide_groups(env, heads, kv_heads, dim):
     check_attend(env, pool, queries(torch, 1, 2, heads, dim, torch.bfloat16), lens)
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(3, 3), (15, 3), (27, 3), (16, 1), (40, 2)])
+@pytest.mark.parametrize("lens", [[1, 31, 32, 33], [3000, 0, 577]], ids=["short", "long"])
+@pytest.mark.parametrize("dim", [80, 96, 112])
+def test_attention_heads_between_64_and_128(env, dim, lens, heads, kv_heads):
+    torch, _ = env
+    pool = Pool(torch, 51, lens, kv_heads, dim, 32, 16)
+    check_attend(env, pool, queries(torch, 52, len(lens), heads, dim, torch.float16), lens)
+
+
 @pytest.mark.parametrize("lens", [[9000], [5000, 1, 0, 12345], [40] * 300, [3000] * 7])
 def test_attention_long_and_many(env, lens):
     torch, _ = env
