@@ -147,9 +147,9 @@ size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t heads,
  *           aligned (NULL when that is 0).
  *
  * Arithmetic: products of q and codes exact, summed in fp32; scores, maxima,
- * exponentials and sums in fp32; the weights 2^(x_j - m) * sv_j are rounded to
- * fp16 relative to the largest one (to 2^-11 of themselves, or 2^-32 of that)
- * for the product with the codes of V; out is rounded once from fp32. Where
+ * exponentials and sums in fp32; the weights 2^(x_j - m) * sv_j go into the
+ * product with the codes of V as two fp16 numbers (rounded to 2^-22 of
+ * themselves, or 2^-32 of the largest one); out is rounded once from fp32. Where
  * scale * log2(e) * sk_j, or that times the largest |q| of a row, passes 2^127,
  * the row may be NaN.
  *
