@@ -730,11 +730,13 @@ struct QuantWarp {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(~0u, sum, i);
         const bool none = sum == 0.f;
-        const float f = none ? 0.f : exp2f(weights - 7.f - base) / sum;
+        // 2^(weights - base) is near the values' scales, and subnormal with a sum of
+        // many tokens below it where these are near 2^-126: half of it at a time
+        const float half = exp2f(0.5f * (weights - 7.f - base)), f = half / sum;
 #pragma unroll
         for (int i = 0; i < KD / 16; ++i) {
-          o[n][i][h] = none ? 0.f : o[n][i][h] * f;
-          o[n][i][2 + h] = none ? 0.f : o[n][i][2 + h] * f;
+          o[n][i][h] = none ? 0.f : o[n][i][h] * f * half;
+          o[n][i][2 + h] = none ? 0.f : o[n][i][2 + h] * f * half;
         }
         base = none ? -INFINITY : base + log2f(sum);
       }

@@ -151,7 +151,8 @@ size_t dsa_quant_attention_workspace_bytes(int64_t batch, int32_t heads,
  * product with the codes of V as two fp16 numbers (rounded to 2^-22 of
  * themselves, or 2^-32 of the largest one); out is rounded once from fp32. Where
  * scale * log2(e) * sk_j, or that times the largest |q| of a row, passes 2^127,
- * the row may be NaN.
+ * the row may be NaN; where scale * log2(e) * sk_j lies below 2^-126 it is
+ * rounded to a multiple of 2^-149. Results are held to 2^-149 at the least.
  *
  * batch == 0 or heads == 0: DSA_OK, nothing written. DSA_EINVAL for kv_heads
  * < 1 or no divisor of heads, a scale that is not as above, a workspace that

@@ -1,4 +1,5 @@
-"""How exact attention on 8-bit pages is, where its error shows: values that cancel.
+"""How exact attention on 8-bit pages is, where its error shows: values that cancel, and
+scales at the lowest end of fp32.
 
 The bound is that of quant_reference.attend but for the weights, which are two fp16
 numbers, the nearest one and what is left of it: H = 2^-22 of a weight instead of 2^-11
@@ -90,3 +91,27 @@ def test_values_that_cancel(env, shape, dtype):
     k, v = (torch.from_numpy(quant.VALUES[codes[i, :n, 0]]) for i in (0, 1))
     for b in range(batch):
         check(torch, out[b], q[b].double(), k, v, 1.0, 0.25)
+
+
+@pytest.mark.parametrize("power", [-100, -119, -123, -126])
+@pytest.mark.parametrize("n,batch,kv_heads", [(9001, 300, 8), (901, 3, 1), (60, 2, 2)])
+def test_the_smallest_scales_of_values(env, n, batch, kv_heads, power):
+    """Even weights of many tokens under scales near 2^-126: what the sum is divided by may
+    not go through fp32's subnormal numbers. (The sequences share their pages.)"""
+    torch, dsa = env
+    dim, page = 64, 128
+    rng = np.random.default_rng(n)
+    pages = -(-n // page)
+    codes = rng.integers(0x38, 0x7f, (2, pages * page, 1, dim)).astype(np.uint8)  # 1 to 448
+    codes = np.repeat(codes, kv_heads, 2)
+    cache = torch.from_numpy(codes.reshape(2, pages, page, kv_heads, dim)).cuda().view(
+        torch.float8_e4m3fn)
+    s = torch.ones(2, pages, 1, kv_heads, device="cuda")
+    s[1] = 2.0 ** power
+    q = torch.zeros(batch, kv_heads, dim, dtype=torch.bfloat16)
+    tables = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(batch, 1)
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    out, _ = dsa.dsa_quant_attention(q.cuda(), cache[0], cache[1], s[0], s[1], tables, lens)
+    k, v = (torch.from_numpy(quant.VALUES[codes[i, :n, 0]]) for i in (0, 1))
+    got = out.reshape(batch * kv_heads, dim)
+    check(torch, got, torch.zeros(1, dim, dtype=torch.float64), k, v, 2.0 ** power, 0.125)
