@@ -1108,8 +1108,59 @@ def rotary_turns(frequencies, device="cuda"):
     return torch.tensor(fixed, dtype=torch.int64, device=device)
 
 
-def _rotary_rows(x, out, name, code, index, tokens, dim):
-    """Addresses, heads and strides of an input and its output, if given."""
+def _place(address, shape, strides, size):
+    """Where the rows of [T, H, D] elements of ``size`` bytes lie: the first byte, the
+    bytes of a row, T and H, and their strides in bytes; None where there are none (no
+    address)."""
+    T, H, D = shape
+    if not (address and T and H and D):
+        return None
+    return address, D * size, T, H, strides[0] * size, strides[1] * size
+
+
+def _rows_at(place, base):
+    """The first bytes of all rows, sorted, relative to ``base``."""
+    torch = _torch()
+    address, _, T, H, st, sh = place
+    rows = (torch.arange(T) * st)[:, None] + torch.arange(H) * sh
+    return rows.flatten().sort().values + (address - base)
+
+
+def _rows_overlap(place):
+    """Whether two of its rows have a byte in common."""
+    _, row, T, H, st, sh = place
+    if st >= (H - 1) * sh + row and (sh >= row or H == 1):
+        return False
+    if (sh >= (T - 1) * st + row or H == 1) and (st >= row or T == 1):
+        return False
+    if T == 1 and sh >= row:
+        return False
+    at = _rows_at(place, place[0])
+    return bool((at[1:] - at[:-1] < row).any())
+
+
+def _apart(a, b):
+    """Whether two places have no byte in common. Those of different tensors, and
+    parts of the rows of one, are found to be by arithmetic, others row by row."""
+    pa, ra, Ta, Ha, sta, sha = a
+    pb, rb, Tb, Hb, stb, shb = b
+    whole, other = (Ta - 1) * sta + (Ha - 1) * sha + ra, (Tb - 1) * stb + (Hb - 1) * shb + rb
+    if pb - pa >= whole or pa - pb >= other:
+        return True
+    if sta == stb and sta and Ta > 1 and Tb > 1:  # a token's heads in the gaps between others
+        if whole - (Ta - 1) * sta <= (pb - pa) % sta <= sta - other + (Tb - 1) * stb:
+            return True
+    step = math.gcd(*(st for n, st in ((Ta, sta), (Ha, sha), (Tb, stb), (Hb, shb)) if n > 1))
+    if step and ra <= (pb - pa) % step <= step - rb:  # rows in the gaps between others
+        return True
+    x, y = _rows_at(a, pa), _rows_at(b, pa)
+    i = _torch().searchsorted(x, y - ra, right=True)  # the first row of a that ends behind b's
+    return not bool(((i < len(x)) & (x[i.clamp(max=len(x) - 1)] < y + rb)).any())
+
+
+def _rotary_rows(x, out, name, index, tokens, dim):
+    """Address, shape and strides of an input, and address and strides of its output,
+    if given."""
     xp, shape, st = _on_gpu(x, x.dtype, name, 3, index)
     if tokens is not None and (shape[0] != tokens or shape[2] != dim):
         raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {tuple(shape)}")
@@ -1119,10 +1170,25 @@ def _rotary_rows(x, out, name, code, index, tokens, dim):
     op, oshape, ost = _on_gpu(out, x.dtype, name + "_out", 3, index)
     if oshape != shape:
         raise ValueError(f"{name}_out must be {tuple(shape)}, got {tuple(oshape)}")
-    ost = _row_strides(oshape, ost, name + "_out")
-    if op == xp and ost != st:
-        raise ValueError(f"{name}_out must be {name} itself or lie apart from it")
-    return xp, shape, st, op, ost
+    return xp, shape, st, op, _row_strides(oshape, ost, name + "_out")
+
+
+def _rotary_places(q, k, q_out, k_out):
+    """Refuses outputs whose rows overlap each other, another output or an input
+    that they are not themselves."""
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if out is None:
+            continue
+        if out != x and not _apart(out, x):
+            raise ValueError(f"{name}_out must be {name} itself or lie apart from it")
+        if _rows_overlap(out):
+            raise ValueError(f"the rows of {name}_out must not overlap")
+    if q_out and k and not _apart(q_out, k):
+        raise ValueError("q_out must lie apart from k")
+    if k_out and q and not (q_out == q and k_out == k) and not _apart(k_out, q):
+        raise ValueError("k_out must lie apart from q")
+    if q_out and k_out and q_out != q and k_out != k and not _apart(q_out, k_out):
+        raise ValueError("q_out and k_out must lie apart")
 
 
 def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: float = 1.0,
@@ -1136,12 +1202,12 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
     the others are copied. ``transpose`` applies the transposed map: given the
     gradients of the outputs it gives those of the inputs (and, with factor 1,
     turns heads back). Writes ``q_out`` and ``k_out`` (allocated when None; they
-    may be ``q`` and ``k`` themselves) and returns both. The outputs carry no
-    autograd graph."""
+    may be ``q`` and ``k`` themselves, and lie apart from all else) and returns
+    both. The outputs carry no autograd graph."""
     torch = _torch()
     code = _rotary_dtype(q, "q")
     dev = q.get_device()
-    qp, qs, qst, qop, qost = _rotary_rows(q, q_out, "q", code, None, None, None)
+    qp, qs, qst, qop, qost = _rotary_rows(q, q_out, "q", None, None, None)
     T, H, D = qs
     if k is None:
         if k_out is not None:
@@ -1151,7 +1217,7 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
     else:
         if k.dtype is not q.dtype:
             raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
-        kp, ks, kst, kop, kost = _rotary_rows(k, k_out, "k", code, dev, T, D)
+        kp, ks, kst, kop, kost = _rotary_rows(k, k_out, "k", dev, T, D)
     pp, n = _vector(positions, "positions", dev)
     if n != T:
         raise ValueError(f"positions holds {n} entries, expected {T}")
@@ -1160,6 +1226,10 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
         raise ValueError("turns must be contiguous")
     if 2 * pairs > D:
         raise ValueError(f"{pairs} pairs do not fit in heads of {D}")
+    if q_out is not None or k_out is not None:
+        e = q.element_size()
+        _rotary_places(_place(qp, qs, qst, e), _place(kp, ks, kst, e),
+                       _place(qop, qs, qost, e), _place(kop, ks, kost, e))
     mode = (pairs, 1 if interleaved else 0, float(factor), 1 if transpose else 0)
 
     def enqueue(handle):

@@ -1,0 +1,96 @@
+"""Outputs that the caller gives to the rotary and 8-bit cache operators: where they may
+lie."""
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import deepseek_sparse_attention_row_gb300 as dsa
+
+    assert torch.cuda.is_available(), "these tests need a CUDA device"
+    yield torch, dsa
+    torch.cuda.synchronize()
+
+
+T, H, HKV, D = 12, 4, 2, 32
+
+
+def turning(torch, dsa):
+    return (torch.arange(T, dtype=torch.int32, device="cuda"),
+            dsa.rotary_turns(dsa.rotary_frequencies(D)))
+
+
+def flat(torch, n, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(n, generator=g).cuda()
+
+
+def at(torch, x, offset, heads, token, head):
+    return torch.as_strided(x, (T, heads, D), (token, head, 1), offset)
+
+
+ROW = H * D
+OVERLAPS = [  # q, k, q_out, k_out as (offset, heads, token stride, head stride) of one buffer
+    ((0, H, ROW, D), None, (D, H, ROW, D), None),               # a head further
+    ((0, H, ROW, D), None, (ROW, H, ROW, D), None),             # a token further
+    ((ROW, H, ROW, D), None, (0, H, ROW, D), None),             # a token in front
+    ((0, H, ROW, D), None, (3, H, ROW, D), None),               # some elements further
+    ((0, H, ROW, D), None, (T * ROW - 1, H, ROW, D), None),     # one element in common
+    ((0, H, ROW, D), None, (0, H, D, T * D), None),             # heads in front of tokens
+    ((0, H, ROW, D), None, (40 * ROW, H, 16, D * T), None),     # rows of the output overlap
+    ((0, H, ROW, D), None, (40 * ROW, H, ROW, 0), None),
+    ((0, 2, ROW, D), (0, 2, ROW, D), (9000, 2, ROW, D), (0, 2, ROW, D)),   # q is read, too
+    ((0, 2, ROW, D), (2 * D, 2, ROW, D), (2 * D, 2, ROW, D), (9000, 2, ROW, D)),
+    ((0, 2, ROW, D), (2 * D, 2, ROW, D), (2 * D, 2, ROW, D), (0, 2, ROW, D)),  # exchanged
+    ((0, 2, ROW, D), (2 * D, 2, ROW, D), (4096, 2, ROW, D), (4096, 2, ROW, D)),
+    ((0, 2, ROW, D), (2 * D, 2, ROW, D), (4096, 2, ROW, D), (4096 + D, 2, ROW, D)),
+    ((0, 2, 3 * D, D), None, (2 * D, 2, 5 * D, D), None),       # steps of another length
+]
+
+
+@pytest.mark.parametrize("where", OVERLAPS, ids=str)
+def test_rotary_refuses_outputs_that_overlap(env, where):
+    torch, dsa = env
+    x = flat(torch, 20000)
+    was = x.clone()
+    q, k, qo, ko = (None if w is None else at(torch, x, *w) for w in where)
+    positions, turns = turning(torch, dsa)
+    with pytest.raises(ValueError, match="overlap|apart"):
+        dsa.dsa_rotary(q, k, positions, turns, q_out=qo, k_out=ko)
+    torch.cuda.synchronize()
+    assert torch.equal(x, was)
+
+
+APART = [
+    ((0, H, ROW, D), None, (T * ROW, H, ROW, D), None),                      # one behind the other
+    ((0, 2, ROW, D), (2 * D, 2, ROW, D), (0, 2, ROW, D), (2 * D, 2, ROW, D)),   # a fused row in place
+    ((0, 1, ROW, D), (2 * D, 1, ROW, D), (D, 1, ROW, D), (3 * D, 1, ROW, D)),   # gaps of a fused row
+    ((0, H, 2 * ROW, 2 * D), None, (D, H, 2 * ROW, 2 * D), None),              # halves of wider heads
+    ((D, H, 2 * ROW, 2 * D), None, (0, H, 2 * ROW, 2 * D), None),
+    ((0, 2, 2 * D, T * 2 * D), (D, 2, 2 * D, T * 2 * D),
+     (0, 2, 2 * D, T * 2 * D), (D, 2, 2 * D, T * 2 * D)),                      # heads first, in place
+    ((0, 2, 6 * D, D), None, (3 * D, 2, 6 * D, 2 * D), None),                  # other steps
+    ((0, 1, 4 * D, D), None, (2 * D, 2, 8 * D, 8 * D * T), None),
+]
+
+
+@pytest.mark.parametrize("where", APART, ids=str)
+def test_rotary_takes_interleaved_outputs(env, where):
+    torch, dsa = env
+    x = flat(torch, 20000, 1)
+    q, k, qo, ko = (None if w is None else at(torch, x, *w) for w in where)
+    if qo.shape != q.shape:
+        q = q.expand(qo.shape)
+    positions, turns = turning(torch, dsa)
+    want = dsa.dsa_rotary(q, k, positions, turns)
+    got = dsa.dsa_rotary(q, k, positions, turns, q_out=qo, k_out=ko)
+    for a, b in zip(got, want):
+        assert b is None or torch.equal(a, b)
