@@ -1343,10 +1343,10 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
 
     Pages, scales and ``tables`` [S, P] as for ``dsa_quant_cache_write``; token i
     of sequence s becomes row cu[s] + i, for i < cu[s + 1] - cu[s] (``cu`` int32
-    [S + 1]). Writes ``k_out`` and ``v_out`` [T, Hkv, D] and returns them; when
-    None they are allocated with T = ``total`` rows (which has to be given) of
-    ``dtype`` (bfloat16 when None, or float16). Rows of no sequence are left
-    as they were, those of tokens without a page are 0."""
+    [S + 1]). Writes ``k_out`` and ``v_out`` [T, Hkv, D], which lie apart, and
+    returns them; when None they are allocated with T = ``total`` rows (which has
+    to be given) of ``dtype`` (bfloat16 when None, or float16). Rows of no
+    sequence are left as they were, those of tokens without a page are 0."""
     torch = _torch()
     dev = k_pages.get_device()
     pages, S, _, _, Hkv, D = _quant_pages(k_pages, v_pages, k_scales, v_scales, tables,
@@ -1374,13 +1374,18 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
             code = DTYPE_F16
         else:
             raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
-    shape = (total, Hkv, D)
+    shape, places = (total, Hkv, D), []
 
     def output(t, name):
         op, oshape, ost = _on_gpu(t, dtype, name, 3, dev)
         if oshape != shape:
             raise ValueError(f"{name} must be {shape}, got {tuple(oshape)}")
-        return op, *_row_strides(oshape, ost, name)
+        ost = _row_strides(oshape, ost, name)
+        place = _place(op, oshape, ost, 2)
+        if place and _rows_overlap(place):
+            raise ValueError(f"the rows of {name} must not overlap")
+        places.append(place)
+        return op, *ost
 
     def enqueue(k, v, handle):
         if k is None:
@@ -1393,6 +1398,8 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
             va = v.data_ptr() or None, Hkv * D, D
         else:
             va = output(v, "v_out")
+        if len(places) == 2 and all(places) and not _apart(*places):
+            raise ValueError("k_out and v_out must lie apart")
         st = library().dsa_quant_cache_read(pages, cp, S, total, code, *ka, *va, handle)
         if st:
             _check("dsa_quant_cache_read", st)

@@ -94,3 +94,24 @@ def test_rotary_takes_interleaved_outputs(env, where):
     got = dsa.dsa_rotary(q, k, positions, turns, q_out=qo, k_out=ko)
     for a, b in zip(got, want):
         assert b is None or torch.equal(a, b)
+
+
+def cache(torch):
+    codes = torch.zeros(2, 5, 16, HKV, D, dtype=torch.uint8, device="cuda").view(
+        torch.float8_e4m3fn)
+    scales = torch.ones(2, 5, 1, HKV, device="cuda")
+    tables = torch.tensor([[0, 1], [3, 2]], dtype=torch.int32, device="cuda")
+    return codes, scales, tables, torch.tensor([20, 9], dtype=torch.int32, device="cuda")
+
+
+def test_read_refuses_outputs_that_overlap(env):
+    torch, dsa = env
+    codes, scales, tables, _ = cache(torch)
+    cu = torch.tensor([0, 7, 12], dtype=torch.int32, device="cuda")
+    x = torch.zeros(T, 2 * HKV, D, dtype=torch.bfloat16, device="cuda")
+    args = codes[0], codes[1], scales[0], scales[1], tables, cu
+    for k, v in ((x[:, :2], x[:, :2]), (x[:, :2], x[:, 1:3]),
+                 (x[:1, :2].expand(T, 2, D), x[:, 2:])):
+        with pytest.raises(ValueError, match="overlap|apart"):
+            dsa.dsa_quant_cache_read(*args, k_out=k, v_out=v)
+    dsa.dsa_quant_cache_read(*args, k_out=x[:, :2], v_out=x[:, 2:])
