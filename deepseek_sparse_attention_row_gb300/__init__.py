@@ -1108,6 +1108,12 @@ def rotary_turns(frequencies, device="cuda"):
     return torch.tensor(fixed, dtype=torch.int64, device=device)
 
 
+def _written(*tensors):
+    """Tells autograd that a kernel has written to those of a caller's tensors that are
+    given: a backward pass that kept one then finds that it has changed."""
+    _torch().autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _place(address, shape, strides, size):
     """Where the rows of [T, H, D] elements of ``size`` bytes lie: the first byte, the
     bytes of a row, T and H, and their strides in bytes; None where there are none (no
@@ -1246,7 +1252,10 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
             _check("dsa_rotary", st)
         return qo, ko
 
-    return _call(dev, stream, enqueue)
+    outs = _call(dev, stream, enqueue)
+    if q_out is not None or k_out is not None:
+        _written(q_out, k_out)
+    return outs
 
 
 # struct dsa_quant_pages
@@ -1334,6 +1343,7 @@ def dsa_quant_cache_write(k, v, cu, k_pages, v_pages, k_scales, v_scales, tables
                *_row_strides(ks, kst, "k"), *_row_strides(vs, vst, "v"), cp, S, lp)
     if st:
         _check("dsa_quant_cache_write", st)
+    _written(k_pages, v_pages, k_scales, v_scales)
 
 
 def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, total=None,
@@ -1405,7 +1415,10 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
             _check("dsa_quant_cache_read", st)
         return k, v
 
-    return _call(dev, stream, enqueue, k_out, v_out)
+    outs = _call(dev, stream, enqueue, k_out, v_out)
+    if given is not None:
+        _written(k_out, v_out)
+    return outs
 
 
 def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *, scale=None,
@@ -1445,7 +1458,10 @@ def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *
             _check("dsa_quant_attention", st)
         return out, lse_out
 
-    return _call(dev, stream, enqueue, out, lse_out)
+    outs = _call(dev, stream, enqueue, out, lse_out)
+    if out is not None or lse_out is not None:
+        _written(out, lse_out)
+    return outs
 
 
 def quant_attention_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int,

@@ -1,5 +1,5 @@
 """Outputs that the caller gives to the rotary and 8-bit cache operators: where they may
-lie."""
+lie, and what autograd learns of their being written."""
 
 import pytest
 
@@ -115,3 +115,43 @@ def test_read_refuses_outputs_that_overlap(env):
         with pytest.raises(ValueError, match="overlap|apart"):
             dsa.dsa_quant_cache_read(*args, k_out=k, v_out=v)
     dsa.dsa_quant_cache_read(*args, k_out=x[:, :2], v_out=x[:, 2:])
+
+
+def counted(tensors, call):
+    was = [t._version for t in tensors]
+    call()
+    assert all(t._version > v for t, v in zip(tensors, was))
+
+
+def test_writing_is_counted(env):
+    """Version counters move, so that a backward pass finds that what it kept is gone."""
+    torch, dsa = env
+    positions, turns = turning(torch, dsa)
+    q, k = (flat(torch, T * n * D, n).view(T, n, D) for n in (H, HKV))
+    counted((q, k), lambda: dsa.dsa_rotary(q, k, positions, turns, q_out=q, k_out=k))
+    counted((q,), lambda: dsa.dsa_rotary(q, k, positions, turns, q_out=q))
+    codes, scales, tables, lens = cache(torch)
+    pages = codes[0], codes[1], scales[0], scales[1], tables
+    x = torch.randn(3, HKV, D, device="cuda").bfloat16()
+    cu = torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda")
+    counted((codes, scales), lambda: dsa.dsa_quant_cache_write(x, x, cu, *pages, lens))
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    counted((y, z), lambda: dsa.dsa_quant_cache_read(*pages, cu, k_out=y, v_out=z))
+    q1 = torch.randn(2, H, D, device="cuda").bfloat16()
+    out, lse = torch.empty_like(q1), torch.empty(2, H, device="cuda")
+    counted((out, lse), lambda: dsa.dsa_quant_attention(q1, *pages, lens, out=out, lse_out=lse))
+    with torch.inference_mode():  # such tensors have no counter
+        y = torch.empty_like(x)
+        dsa.dsa_quant_cache_read(*pages, cu, k_out=y, v_out=z)
+    dsa.dsa_quant_cache_read(*pages, cu, k_out=y, v_out=z)
+
+
+def test_a_gradient_through_what_was_turned_in_place_is_refused(env):
+    torch, dsa = env
+    positions, turns = turning(torch, dsa)
+    w = torch.ones(T, H, D, device="cuda", requires_grad=True)
+    q = flat(torch, T * H * D).view(T, H, D)
+    loss = (q * w).sum()  # keeps q
+    dsa.dsa_rotary(q, None, positions, turns, q_out=q)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
