@@ -1108,6 +1108,14 @@ def rotary_turns(frequencies, device="cuda"):
     return torch.tensor(fixed, dtype=torch.int64, device=device)
 
 
+def _no_graph(**outputs):
+    """Refuses given outputs whose autograd graph would not know what is written to them."""
+    for name, t in outputs.items():
+        if t is not None and t.requires_grad and _torch().is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which would miss this call: "
+                             "detach it, or call under torch.no_grad()")
+
+
 def _written(*tensors):
     """Tells autograd that a kernel has written to those of a caller's tensors that are
     given: a backward pass that kept one then finds that it has changed."""
@@ -1209,7 +1217,8 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
     gradients of the outputs it gives those of the inputs (and, with factor 1,
     turns heads back). Writes ``q_out`` and ``k_out`` (allocated when None; they
     may be ``q`` and ``k`` themselves, and lie apart from all else) and returns
-    both. The outputs carry no autograd graph."""
+    both. The outputs carry no autograd graph; given ones that require a gradient
+    are refused where gradients are recorded."""
     torch = _torch()
     code = _rotary_dtype(q, "q")
     dev = q.get_device()
@@ -1233,6 +1242,7 @@ def dsa_rotary(q, k, positions, turns, *, interleaved: bool = False, factor: flo
     if 2 * pairs > D:
         raise ValueError(f"{pairs} pairs do not fit in heads of {D}")
     if q_out is not None or k_out is not None:
+        _no_graph(q_out=q_out, k_out=k_out)
         e = q.element_size()
         _rotary_places(_place(qp, qs, qst, e), _place(kp, ks, kst, e),
                        _place(qop, qs, qost, e), _place(kop, ks, kost, e))
@@ -1366,6 +1376,7 @@ def dsa_quant_cache_read(k_pages, v_pages, k_scales, v_scales, tables, cu, *, to
         raise ValueError(f"cu holds {nc} offsets for {S} rows of tables")
     given = k_out if k_out is not None else v_out
     if given is not None:
+        _no_graph(k_out=k_out, v_out=v_out)
         if total is not None and total != given.shape[0]:
             raise ValueError(f"total is {total}, the output has {given.shape[0]} rows")
         if dtype is not None and dtype is not given.dtype:
@@ -1445,6 +1456,8 @@ def dsa_quant_attention(q, k_pages, v_pages, k_scales, v_scales, tables, lens, *
     if n != B or S != B:
         raise ValueError(f"tables {tuple(tables.shape)} and lens {tuple(lens.shape)} do not "
                          f"match q {tuple(qs)}")
+    if out is not None or lse_out is not None:
+        _no_graph(out=out, lse_out=lse_out)
     qst = _row_strides(qs, qst, "q")
 
     def enqueue(out, lse_out, handle):

@@ -155,3 +155,33 @@ def test_a_gradient_through_what_was_turned_in_place_is_refused(env):
     dsa.dsa_rotary(q, None, positions, turns, q_out=q)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_outputs_that_require_a_gradient_are_refused(env):
+    """Their graphs would not know of the call: the gradient of what was turned in place
+    would come back without the turn."""
+    torch, dsa = env
+    positions, turns = turning(torch, dsa)
+    x = flat(torch, T * H * D).view(T, H, D).requires_grad_()
+    k = flat(torch, T * HKV * D).view(T, HKV, D)
+    q = x * 2
+    for kw in (dict(q_out=q), dict(q_out=torch.empty_like(q, requires_grad=True)),
+               dict(k_out=torch.empty_like(k, requires_grad=True))):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            dsa.dsa_rotary(q, k, positions, turns, **kw)
+    want = dsa.dsa_rotary(q, k, positions, turns)
+    with torch.no_grad():
+        got = dsa.dsa_rotary(q, k, positions, turns, q_out=q)
+    assert got[0] is q and torch.equal(q, want[0])
+    y = (x * 2).detach()
+    assert torch.equal(dsa.dsa_rotary(y, k, positions, turns, q_out=y)[0], want[0])
+    codes, scales, tables, lens = cache(torch)
+    pages = codes[0], codes[1], scales[0], scales[1], tables
+    cu = torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda")
+    z = torch.empty(3, HKV, D, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="v_out requires"):
+        dsa.dsa_quant_cache_read(*pages, cu, k_out=z.detach(), v_out=z)
+    q1 = torch.zeros(2, H, D, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="lse_out requires"):
+        dsa.dsa_quant_attention(q1, *pages, lens, lse_out=torch.empty(
+            2, H, device="cuda", requires_grad=True))
