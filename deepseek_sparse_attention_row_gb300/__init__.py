@@ -1136,7 +1136,8 @@ def _rows_at(place, base):
     """The first bytes of all rows, sorted, relative to ``base``."""
     torch = _torch()
     address, _, T, H, st, sh = place
-    rows = (torch.arange(T) * st)[:, None] + torch.arange(H) * sh
+    tokens, heads = (torch.arange(n, dtype=torch.int64, device="cpu") for n in (T, H))
+    rows = (tokens * st)[:, None] + heads * sh
     return rows.flatten().sort().values + (address - base)
 
 

@@ -74,3 +74,10 @@ def test_outputs_that_may_be(dsa, places):
 def test_outputs_that_may_not_be(dsa, places, match):
     with pytest.raises(ValueError, match=match):
         dsa._rotary_places(*places)
+
+
+def test_another_default_device(dsa):
+    """Rows are compared on the CPU wherever tensors are made by default."""
+    with torch.device("meta"):
+        assert dsa._rows_overlap((0, 8, 4, 2, 4, 64))
+        assert not dsa._apart((0, 8, 4, 2, 24, 8), (4, 8, 4, 2, 24, 8))
