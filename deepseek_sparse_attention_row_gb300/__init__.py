@@ -1080,7 +1080,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, stretch: float
         if rotary_dim < 4 and stretch != 1.0:
             raise ValueError("a single pair has no base to raise")
         base = base * stretch ** (rotary_dim / max(rotary_dim - 2, 1))
-    f = float(base) ** (-torch.arange(rotary_dim // 2, dtype=torch.float64) * 2 / rotary_dim)
+    pairs = torch.arange(rotary_dim // 2, dtype=torch.float64, device="cpu")
+    f = float(base) ** (-pairs * 2 / rotary_dim)
     if method == "linear":
         return f / stretch
     if method == "base":
