@@ -117,16 +117,16 @@ dsa_status launch(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t strea
   return ok ? DSA_OK : DSA_ECUDA;
 }
 
-// Heads of 80 and 96 multiply no more than they have, where that is faster than
-// going through products of 128: 33 sequences, 136,000 tokens of 8 heads of 80, take
-// 47.9 us instead of 50.0 (5 query heads each) and 56.3 instead of 63.5 (9); of 96, 57.0
-// instead of 62.1 (16), but 48.5 and 48.7 (4).
+// Heads of 80 and 96 multiply no more than they have, which is faster than going
+// through products of 128: 33 sequences, 136,000 tokens of 8 heads of 80, take 49.6 us
+// instead of 53.2 (5 query heads each) and 60.5 instead of 72.1 (9); of 96, 48.3
+// instead of 49.6 (4) and 61.7 instead of 70.0 (16). Heads of 112 go through products
+// of 128 (54.9 us; 4).
 template <int NT>
 dsa_status launch_heads(const QuantAttnArgs& a, const QuantPlan& p, cudaStream_t s) {
   if (p.dp == 64) return launch<64, NT, 64>(a, p, s);
   if (a.pool.dim == 80) return launch<128, NT, 80>(a, p, s);
-  if constexpr (NT == 2)
-    if (a.pool.dim == 96) return launch<128, NT, 96>(a, p, s);
+  if (a.pool.dim == 96) return launch<128, NT, 96>(a, p, s);
   return launch<128, NT, 128>(a, p, s);
 }
 
