@@ -10,7 +10,7 @@
 // into a ring of three of its own in shared memory, whole rows at a time; no
 // barrier stands between a load and its use. Codes become fp16 in registers,
 // which is exact; so are queries after a power of two that brings the largest of
-// a row to 2^14.
+// a row to 2^14. Weights are two fp16 numbers each, so that V^T P^T is two products.
 //
 // The tiles of all sequences lie on one line, in front of each sequence's a unit for
 // its start. It is cut into equal shares, one for each team of as many warps as there
@@ -22,17 +22,18 @@
 // those by their log-sum-exps.
 //
 // Bound by HBM where contexts are long: 302,000 tokens of 8 heads of 128, 619 MB,
-// take 100 us (6.2 TB/s, 7.4 TB/s in the loop alone), 459,000 tokens of 4 heads 80
+// take 100 us (6.2 TB/s, 7.3 TB/s in the loop alone), 459,000 tokens of 4 heads 80
 // us (5.9 TB/s). About 8 us pass before the first tiles are done (lengths, page,
 // codes: a chain of loads, then all SMs' first ones at once) and 5 at the end (the
-// join). With heads of 80, 174 MB in 48 us, these are a third of the time; in the loop,
-// at 5.4 TB/s, a scheduler has three warps, each of which issues every sixth cycle
-// (16 warps: 47.4 us).
-// Codes through registers instead of the ring: 161 us for the first case (too few
-// bytes under way); 14 or 16 warps of 128 registers: 110 and 117 us; 8 warps with
-// tiles of 8 KiB: 102 us; pieces joined in the CTA and rows in turn instead of side
-// by side: 122 us; rings of four slots, with loads a whole tile further ahead, 108 us;
-// heads of 80 in rows of 80 bytes, tiles of 64 keys, 54 us.
+// join). With heads of 80, 174 MB in 49.5 us, these are a quarter of the time; in the
+// loop, at 5.2 TB/s, a scheduler has three warps, each of which issues every sixth
+// cycle.
+// What was tried while weights were one fp16 number (100.0 us for the first case, 47.9
+// for heads of 80): codes through registers instead of the ring 161 us (too few bytes
+// under way); 14 or 16 warps of 128 registers 110 and 117 us (heads of 80, 16 warps:
+// 47.4); 8 warps with tiles of 8 KiB 102 us; pieces joined in the CTA and rows in turn
+// instead of side by side 122 us; rings of four slots, with loads a whole tile further
+// ahead, 108 us; heads of 80 in rows of 80 bytes, tiles of 64 keys, 54 us.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -46,9 +47,10 @@
 namespace dsa {
 
 constexpr int kQuantTileBytes = 4096;
-// What the start of a sequence takes of a share, in tiles. 128 sequences of 300 tokens,
-// 8 heads of 128: 18.6 us with 0, 17.2 with 1, 17.8 with 2; 300 of 700, 4 heads of 64:
-// 21.2, 20.2, 21.1; 33 of about 4100, 8 heads of 80: 50.7, 50.0, 50.1.
+// What the start of a sequence takes of a share, in tiles. 128 sequences of up to 300
+// tokens, 8 heads of 128: 18.7 us with 0, 17.4 with 1, 18.3 with 2; 300 of up to 700, 4
+// heads of 64: 21.7, 20.9, 22.1; 33 of up to 8000, 8 heads of 80: 50.2, 49.6, 49.9; 64
+// of up to 9216, 8 heads of 128: 101.0, 100.6, 101.0.
 constexpr int32_t kQuantStart = 1;
 
 struct QuantAttnArgs {
@@ -75,8 +77,9 @@ template <int DP, int NT>
 struct QuantLayout {
   static constexpr int kTile = kQuantTileBytes / DP;  // keys
   static constexpr int kHeads = 8 * NT;
-  // As many as the registers let be: 16 columns take 250 of a thread (12 warps of
-  // them, spilled, took 79 us where 8 take 62: groups of 16, 64 sequences).
+  // As many as the registers let be: 16 columns take 235 to 255 of a thread (12 warps
+  // of them, spilled, took 79 us where 8 took 62: groups of 16, 64 sequences, weights
+  // of one fp16 number).
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = 3 * kQuantTileBytes;

@@ -51,8 +51,16 @@ int32_t quant_warps(int columns) {
 
 // Tiles of all heads; those of the sequences and their starts then stay within 31 bits.
 constexpr int64_t kMaxUnits = 250000000;
-// Tiles of a row that a CTA of its own still takes, if there is an SM for each row:
-// one launch instead of two (three sequences of 200 tokens, 2 heads of 64: 5.0 us).
+// Tiles of a row that a CTA of its own still takes, if there is an SM for each row: one
+// launch instead of two. Lengths are on the device, so that the room of the table's
+// rows decides. 3 sequences with 2 heads of 64, 16 with 2 of 128 and 18 with 8 of 128,
+// us, in one launch and in two:
+//    4 tiles   5.0 10.9    5.3 9.7    5.4 10.2
+//   16         8.1 11.2    8.6 9.7    8.6 11.4
+//   32        10.9 11.5   10.4 9.9   12.4 15.4
+//   64        18.4 11.6   16.2 12.4  19.6 21.9
+// Short sequences in a wide table pay for that: three of about 200 tokens, 2 heads of
+// 64, take 4.9 us with room for 1024 tokens, 7.7 for 2048 and 8.3 for 8192.
 constexpr int64_t kWholeTiles = 16;
 
 QuantPlan plan_attention(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim,

@@ -6,12 +6,14 @@
 // one next to x and does not depend on how it is computed, and a scale that grows
 // changes the held codes only where they fall below the smallest normal one.
 //
-// Both are bound by HBM and by how many loads are under way. Writing reads a
-// block's tokens once, into the registers of a team of warps that agree on their
-// largest size: 16389 tokens of 8 heads of 128, 100 MB, take 21.9 us (4.6 TB/s); 72
-// us when a warp went through the block twice, 30 with sizes taken as floats, 27
-// with registers for two CTAs of an SM instead of four. Reading 20541 tokens of 8
-// heads of 128, 126 MB, takes 22.8 us (5.5 TB/s); 25 us with eight rows to a warp.
+// Reading is bound by HBM: 20541 tokens of 8 heads of 128, 126 MB, take 22.8 us (5.5
+// TB/s; 25 us with eight rows to a warp). Writing is bound by how many loads are under
+// way: it reads a block's tokens once, into the registers of a team of warps that agree
+// on their largest size, and a CTA has none under way while it agrees and stores. 16389
+// tokens of 8 heads of 128, 101 MB, take 22.2 us (4.5 TB/s); 72 us when a warp went
+// through the block twice, 30 with sizes taken as floats, 27 with registers for two
+// CTAs of an SM instead of four. Small blocks have a CTA each: 16000 tokens take 21.7 us
+// in blocks of 128, 21.2 of 16, 46 of 4 and 161 of 1.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -122,8 +124,10 @@ constexpr int kAtOnce = 8;  // 16-byte loads of a lane
 
 // A team of `team` warps (a power of two, up to 16) for each block, head and one of
 // keys and values; the teams of a CTA share the block. Where a block's new tokens
-// are no more than a team has registers for, they are read once.
-// (64 registers, a few of them spilled, for twice the warps.)
+// are no more than a team has registers for, they are read once. The team is laid out
+// for the mean of the sequences: a prompt of 2048 tokens, alone 4.6 us, takes 24.4 among
+// 255 single tokens (alone 7.5), as its blocks' warps go through them twice.
+// (64 registers, none spilled, for twice the warps.)
 template <typename T>
 __global__ void __launch_bounds__(512, 2) write_kernel(const WriteArgs a, int team) {
   __shared__ uint32_t tops[16];

@@ -7,7 +7,7 @@
 // as alignment lets them be, up to 16 bytes; neighbouring threads take neighbouring
 // chunks. The first loads are on their way while the angles are computed.
 //
-// Bound by HBM: 8192 tokens of 40 heads of 128, bf16, take 31.2 us (5.4 TB/s read
+// Bound by HBM: 8192 tokens of 40 heads of 128, bf16, take 31.3 us (5.4 TB/s read
 // and written; 48 us with the angles in registers, computed by every thread, 35 us
 // with chunks dealt to the threads by division); 4099 tokens of 16 heads of 96,
 // fp32, neighbours, 9.0 us (5.6 TB/s). Four tokens to a CTA and two under way in a
