@@ -40,7 +40,9 @@ current stream) or pinned host tensors, which the kernels read and write in
 place through ``dsa_mapped_host_pointer`` (across NVLink-C2C on Grace
 systems). Logits may be float32 or bfloat16 (the ``*_bf16`` C entry points);
 scores follow the logits' dtype. The attention, cache and rotary operators
-take CUDA tensors only. ``select_candidate_blocks[_sharded]_host``
+take CUDA tensors only; the rotary and 8-bit ones refuse given outputs that
+require a gradient where gradients are recorded, and move the version counters
+of what they write to. ``select_candidate_blocks[_sharded]_host``
 take host tensors and wait for the ids: pinned inputs are read in place
 (only the in-window logits cross the link), other host tensors are copied to
 the device first.
@@ -1148,8 +1150,6 @@ def _rows_overlap(place):
     if st >= (H - 1) * sh + row and (sh >= row or H == 1):
         return False
     if (sh >= (T - 1) * st + row or H == 1) and (st >= row or T == 1):
-        return False
-    if T == 1 and sh >= row:
         return False
     at = _rows_at(place, place[0])
     return bool((at[1:] - at[:-1] < row).any())
